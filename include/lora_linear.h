@@ -203,7 +203,15 @@ typedef enum {
     LORA_K_DOWN_BWD_GRAD_B = 7, /* s dY B and dB in one launch (both read dY) */
     LORA_K_SWIGLU_GRAD = 8,     /* SwiGLU pair: elementwise d_gate, d_up      */
     LORA_K_QUANT = 9,           /* fp8 variant: e4m3 quantisation of X or dY  */
-    LORA_K_GRAD_A_B = 10        /* dA and dB in one launch, after the dX GEMM */
+    LORA_K_GRAD_A_B = 10,       /* dA and dB in one launch, after the dX GEMM */
+    LORA_K_ROTARY = 11,         /* rotary positions of q and k               */
+    LORA_K_GRAD_NORM = 12,      /* global gradient norm                      */
+    LORA_K_GRAD_CLIP = 13,      /* gradients scaled by the clip factor       */
+    LORA_K_ATTN_PREP = 14,      /* attention: document ranges of the tiles   */
+    LORA_K_ATTN_FWD = 15,       /* attention: output and log-sum-exp         */
+    LORA_K_ATTN_DQ = 16,        /* attention: dq (and rowsum(do * o))        */
+    LORA_K_ATTN_DKV = 17,       /* attention: dk and dv                      */
+    LORA_K_ATTN_TOKEN = 18      /* attention: one new token over a cache     */
 } lora_kernel_kind_t;
 
 /*

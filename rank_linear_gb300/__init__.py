@@ -12,8 +12,16 @@ from .lora import (FP8Weight, Q4Weight, dequantize_w_q4, q4_backward, q4_forward
                    swiglu_backward,
                    swiglu_forward, swiglu_saved_bytes, swiglu_workspace_bytes, timing_events,
                    workspace_bytes)
+from .attention import (AttentionFunction, attention, attention_backward, attention_decode,
+                        attention_forward)
+from .clip import GradClip
+from .rotary import (RotaryFrequencies, RotaryFunction, rotary, rotary_backward, rotary_forward,
+                     rotary_frequencies)
 
-__all__ = ["FP8Weight", "Q4Weight", "dequantize_w_q4", "q4_backward", "q4_forward",
+__all__ = ["AttentionFunction", "attention", "attention_backward", "attention_decode",
+           "attention_forward", "GradClip", "RotaryFrequencies", "RotaryFunction", "rotary",
+           "rotary_backward", "rotary_forward", "rotary_frequencies",
+           "FP8Weight", "Q4Weight", "dequantize_w_q4", "q4_backward", "q4_forward",
            "quantize_w_q4", "LoRAFP8Function", "LoRAQ4Function", "lora_linear_fp8",
            "lora_linear_q4", "LoRALinearFunction", "LoRASwiGLUFunction", "backward", "device_status",
            "forward", "fp8_backward", "fp8_forward", "fp8_workspace_bytes", "quantize_rows_fp8", "quantize_w_fp8",

@@ -16,10 +16,38 @@ LORA_OK, LORA_ERR_INVALID_ARG, LORA_ERR_UNSUPPORTED, LORA_ERR_WORKSPACE, \
     LORA_ERR_CUDA, LORA_ERR_TIMEOUT = range(6)
 LORA_BF16, LORA_FP32 = 0, 1
 KERNEL_KINDS = ["prep", "down_fwd", "main_fwd", "down_bwd", "main_bwd", "grad_a", "grad_b",
-                "down_bwd_grad_b", "swiglu_grad", "quant", "grad_a_b"]
+                "down_bwd_grad_b", "swiglu_grad", "quant", "grad_a_b", "rotary", "grad_norm",
+                "grad_clip", "attn_prep", "attn_fwd", "attn_dq", "attn_dkv", "attn_token"]
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
 _int, _f32 = ctypes.c_int, ctypes.c_float
+
+_i32 = ctypes.c_int32
+
+
+class RotaryShape(ctypes.Structure):
+    """lora_rotary_t"""
+    _fields_ = [("batch", _i64), ("seq", _i64), ("q_heads", _i32), ("k_heads", _i32),
+                ("dim", _i32), ("rot", _i32), ("interleaved", _i32), ("inverse", _i32),
+                ("position_bits", _i32), ("magnitude", _f32), ("q_in", _i64 * 3),
+                ("k_in", _i64 * 3), ("q_out", _i64 * 3), ("k_out", _i64 * 3),
+                ("position", _i64 * 2)]
+
+
+class ClipTensor(ctypes.Structure):
+    """lora_clip_tensor_t"""
+    _fields_ = [("in_", _vp), ("out", _vp), ("count", _i64), ("dtype", _i32)]
+
+
+class AttentionShape(ctypes.Structure):
+    """lora_attention_t"""
+    _fields_ = [("batch", _i64), ("q_len", _i64), ("k_len", _i64), ("q_heads", _i32),
+                ("k_heads", _i32), ("dim", _i32), ("causal", _i32), ("scale", _f32),
+                ("softcap", _f32), ("q", _i64 * 3), ("k", _i64 * 3), ("v", _i64 * 3),
+                ("o", _i64 * 3), ("d_o", _i64 * 3), ("dq", _i64 * 3), ("dk", _i64 * 3),
+                ("dv", _i64 * 3), ("slopes", _vp), ("q_docs", _vp), ("k_docs", _vp),
+                ("q_docs_stride", _i64), ("k_docs_stride", _i64), ("prefix", _vp)]
+
 
 SIGNATURES = {
     "lora_linear_saved_bytes": ([_i64, _int, _int], _sz),
@@ -59,6 +87,18 @@ SIGNATURES = {
                          _vp, _vp, _vp, _sz, _vp], _int),
     "lora_swiglu_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _int, _i64, _i64,
                          _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "lora_rotary_turns": ([_vp, _int, _vp], _int),
+    "lora_rotary": ([_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp], _int),
+    "lora_clip_plan_bytes": ([_vp, _int], _sz),
+    "lora_clip_plan_build": ([_vp, _int, _vp, _sz], _int),
+    "lora_clip_norm": ([_vp, _sz, _int, _vp, _vp], _int),
+    "lora_clip": ([_vp, _sz, _f32, _int, _vp, _vp], _int),
+    "lora_attention_workspace_bytes": ([_vp, _int], _sz),
+    "lora_attention_fwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "lora_attention_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
+                           _int),
+    "lora_attention_token_workspace_bytes": ([_vp], _sz),
+    "lora_attention_token": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
 }
 
 _lib = None

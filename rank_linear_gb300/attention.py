@@ -1,0 +1,196 @@
+"""Attention between the q, k, v and o LoRA layers: scores capped by a tanh, a
+bias that falls with distance, document and prefix masks; forward, backward,
+and one new token over a cache (formulas in include/lora_attention.h; ch05
+"Acceleration principles: Triton kernels and fused LoRA", §5.10).
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from . import _lib
+from .lora import _stream_ptr
+from .rotary import _on
+
+
+def _strides(t, name):
+    if t.dtype != torch.bfloat16 or not t.is_cuda:
+        raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    s = t.stride()
+    if s[-1] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return s[:3]
+
+
+def _word(t, dtype, name, shape):
+    if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
+    if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    return t.data_ptr() or None
+
+
+def _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix):
+    if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape:
+        raise ValueError("q is [batch, q_len, q_heads, dim], k and v [batch, k_len, k_heads, dim]")
+    b, sq, hq, d = q.shape
+    sk, hk = k.shape[1], k.shape[2]
+    if k.shape[0] != b or k.shape[3] != d:
+        raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not fit")
+    sh = _lib.AttentionShape(batch=b, q_len=sq, k_len=sk, q_heads=hq, k_heads=hk, dim=d,
+                             causal=int(causal), scale=d ** -0.5 if scale is None else scale,
+                             softcap=softcap or 0.0)
+    sh.q, sh.k, sh.v = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
+    if slopes is not None:
+        sh.slopes = _word(slopes, torch.float32, "slopes", (hq,))
+    if documents is not None:
+        if isinstance(documents, (tuple, list)):
+            qd, kd = documents
+        else:
+            if sq > sk:
+                raise ValueError("one documents tensor needs q_len <= k_len")
+            kd = documents
+            qd = documents if sq == sk else documents[:, sk - sq:]
+        sh.q_docs, sh.q_docs_stride = _word(qd, torch.int32, "q documents", (b, sq)), qd.stride(0)
+        sh.k_docs, sh.k_docs_stride = _word(kd, torch.int32, "k documents", (b, sk)), kd.stride(0)
+        if sh.q_docs is None or sh.k_docs is None:  # an empty side: nothing to mask
+            sh.q_docs = sh.k_docs = None
+    if prefix is not None:
+        sh.prefix = _word(prefix, torch.int32, "prefix", (b,))
+    return sh
+
+
+def _scratch(nbytes, like, workspace):
+    if workspace is not None:
+        return workspace
+    return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr() or None
+
+
+def _size(t):
+    return 0 if t is None else t.numel() * t.element_size()
+
+
+def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=None,
+                      documents=None, prefix=None, out=None, lse=None, workspace=None,
+                      stream=None):
+    """(o, lse) of q [batch, q_len, q_heads, dim] over k, v [batch, k_len, k_heads, dim].
+
+    scale      of the scores; None: dim ** -0.5.
+    causal     the queries are the last q_len of the k_len positions.
+    softcap    > 0: scores become softcap * tanh(score / softcap).
+    slopes     float32 [q_heads]: score - slope * |distance|.
+    documents  int32 [batch, k_len], the queries' being its last q_len (or a
+               pair [batch, q_len], [batch, k_len]): a pair of tokens is
+               visible within one document; below zero: padding.
+    prefix     int32 [batch]: keys before it are visible to every query
+               (with causal).
+    """
+    sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix)
+    L = _lib.lib()
+    with _on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], dtype=torch.float32,
+                              device=q.device)
+        if out.shape != q.shape:
+            raise ValueError(f"out {tuple(out.shape)} is not {tuple(q.shape)}")
+        sh.o = _strides(out, "out")
+        workspace = _scratch(L.lora_attention_workspace_bytes(ctypes.byref(sh), 0), q, workspace)
+    _lib.check(L.lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                    _ptr(lse), _ptr(workspace), _size(workspace),
+                                    _stream_ptr(stream)), "lora_attention_fwd")
+    return out, lse
+
+
+def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, softcap=0.0,
+                       slopes=None, documents=None, prefix=None, dq=None, dk=None, dv=None,
+                       workspace=None, stream=None):
+    """(dq, dk, dv) from the gradient of attention_forward's output."""
+    sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix)
+    L = _lib.lib()
+    if out.shape != q.shape or dout.shape != q.shape:
+        raise ValueError("out and dout must have q's shape")
+    if lse.dtype != torch.float32 or not lse.is_contiguous() or \
+            tuple(lse.shape) != (q.shape[0], q.shape[2], q.shape[1]):
+        raise ValueError("lse must be the forward's: float32 [batch, q_heads, q_len]")
+    with _on(stream):
+        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+        if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
+            raise ValueError("dq, dk and dv must have the shapes of q, k and v")
+        sh.o, sh.d_o = _strides(out, "out"), _strides(dout, "dout")
+        sh.dq, sh.dk, sh.dv = _strides(dq, "dq"), _strides(dk, "dk"), _strides(dv, "dv")
+        workspace = _scratch(L.lora_attention_workspace_bytes(ctypes.byref(sh), 1), q, workspace)
+    _lib.check(L.lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
+                                    _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                                    _ptr(workspace), _size(workspace), _stream_ptr(stream)),
+               "lora_attention_bwd")
+    return dq, dk, dv
+
+
+def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, slopes=None,
+                     out=None, workspace=None, stream=None):
+    """One new token per sequence: q [batch, q_heads, dim] over the first
+    lengths[b] (int32 [batch], the token itself included) of k_cache, v_cache
+    [batch, positions, k_heads, dim].  Returns o like q; zero where the length is."""
+    if q.dim() != 3:
+        raise ValueError("q must be [batch, q_heads, dim]")
+    sh = _shape(q.unsqueeze(1), k_cache, v_cache, scale, False, softcap, slopes, None, None)
+    L = _lib.lib()
+    n = _word(lengths, torch.int32, "lengths", (q.shape[0],))
+    with _on(stream):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        if out.shape != q.shape:
+            raise ValueError(f"out {tuple(out.shape)} is not {tuple(q.shape)}")
+        sh.o = _strides(out.unsqueeze(1), "out")
+        workspace = _scratch(L.lora_attention_token_workspace_bytes(ctypes.byref(sh)), q,
+                             workspace)
+    _lib.check(L.lora_attention_token(ctypes.byref(sh), _ptr(q), _ptr(k_cache), _ptr(v_cache), n,
+                                      _ptr(out), _ptr(workspace), _size(workspace),
+                                      _stream_ptr(stream)), "lora_attention_token")
+    return out
+
+
+def _fit(t):
+    """t itself where its strides suit the kernels, else a contiguous copy."""
+    ok = (t.stride(-1) == 1 or t.shape[-1] == 1) and all(s % 8 == 0 for s in t.stride()[:3]) \
+        and t.data_ptr() % 16 == 0
+    return t if ok else t.contiguous()
+
+
+class AttentionFunction(torch.autograd.Function):
+    """Autograd function: saves q, k, v, the output and its log-sum-exp."""
+
+    @staticmethod
+    def forward(ctx, q, k, v, slopes, documents, prefix, scale, causal, softcap):
+        q, k, v = _fit(q), _fit(k), _fit(v)
+        ctx.opts = dict(scale=scale, causal=causal, softcap=softcap)
+        pair = isinstance(documents, (tuple, list))
+        docs = tuple(documents) if pair else (documents,)
+        out, lse = attention_forward(q, k, v, slopes=slopes, documents=documents, prefix=prefix,
+                                     **ctx.opts)
+        ctx.save_for_backward(q, k, v, out, lse, slopes, prefix, *docs)
+        ctx.pair = pair
+        return out
+
+    @staticmethod
+    def backward(ctx, dout):
+        q, k, v, out, lse, slopes, prefix, *docs = ctx.saved_tensors
+        dq, dk, dv = attention_backward(_fit(dout), q, k, v, out, lse, slopes=slopes,
+                                        documents=tuple(docs) if ctx.pair else docs[0],
+                                        prefix=prefix, **ctx.opts)
+        return dq, dk, dv, None, None, None, None, None, None
+
+
+def attention(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=None, documents=None,
+              prefix=None):
+    """attention_forward's output with gradients for q, k and v."""
+    return AttentionFunction.apply(q, k, v, slopes, documents, prefix, scale, causal, softcap)

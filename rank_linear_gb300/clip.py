@@ -1,0 +1,78 @@
+"""Global gradient norm and clipping over many tensors: what stands between
+the dA, dB of every LoRA layer and the optimiser (include/lora_clip.h)."""
+from __future__ import annotations
+
+import math
+
+import torch
+
+from . import _lib
+from .lora import _dtype_code, _stream_ptr
+
+
+class GradClip:
+    """The plan over a list of gradient tensors, laid out once on the device.
+
+    grads    contiguous CUDA tensors, bf16 and fp32 in any mix; the plan keeps
+             them alive and reads the values they hold at each call.
+    out      tensors of the same shapes and types for the clipped gradients;
+             None: in place.
+
+    Calls that overlap on the GPU (other streams) need a plan each.
+    """
+
+    def __init__(self, grads, out=None):
+        self.grads = list(grads)
+        self.out = self.grads if out is None else list(out)
+        if len(self.out) != len(self.grads):
+            raise ValueError(f"{len(self.out)} outputs for {len(self.grads)} gradients")
+        table = (_lib.ClipTensor * max(len(self.grads), 1))()
+        device = None
+        for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            if not g.is_cuda or not g.is_contiguous() or not o.is_contiguous():
+                raise ValueError(f"gradient {i}: contiguous CUDA tensors are needed")
+            if o.shape != g.shape or o.dtype != g.dtype or o.device != g.device:
+                raise ValueError(f"gradient {i}: its output has another shape, type or device")
+            if device is not None and g.device != device:
+                raise ValueError(f"gradient {i} is on another device")
+            device = g.device
+            table[i] = _lib.ClipTensor(g.data_ptr() or None, o.data_ptr() or None, g.numel(),
+                                       _dtype_code(g))
+        L = _lib.lib()
+        self.bytes = int(L.lora_clip_plan_bytes(table, len(self.grads)))
+        if self.bytes == 0:
+            _lib.check(_lib.LORA_ERR_INVALID_ARG, "lora_clip_plan_bytes")
+        image = torch.empty(self.bytes, dtype=torch.uint8)
+        _lib.check(L.lora_clip_plan_build(table, len(self.grads), image.data_ptr(), self.bytes),
+                   "lora_clip_plan_build")
+        self.plan = image.to(device if device is not None else torch.device("cuda"))
+
+    @staticmethod
+    def _largest(norm_type) -> int:
+        if norm_type == 2 or norm_type == math.inf:
+            return int(norm_type == math.inf)
+        raise ValueError(f"norm_type = {norm_type} is not 2 or inf")
+
+    def _norm_out(self, norm):
+        if norm is None:
+            return torch.empty((), dtype=torch.float32, device=self.plan.device)
+        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != self.plan.device:
+            raise ValueError("norm must be one float32 on the gradients' device")
+        return norm
+
+    def norm(self, *, norm_type: float = 2.0, norm=None, stream=None):
+        """The global norm (a device scalar); nothing is scaled."""
+        norm = self._norm_out(norm)
+        _lib.check(_lib.lib().lora_clip_norm(self.plan.data_ptr(), self.bytes,
+                                             self._largest(norm_type), norm.data_ptr(),
+                                             _stream_ptr(stream)), "lora_clip_norm")
+        return norm
+
+    def clip(self, max_norm: float, *, norm_type: float = 2.0, norm=None, stream=None):
+        """Scales every gradient by min(1, max_norm / (norm + 1e-6)); returns the
+        norm before it (a device scalar)."""
+        norm = self._norm_out(norm)
+        _lib.check(_lib.lib().lora_clip(self.plan.data_ptr(), self.bytes, float(max_norm),
+                                        self._largest(norm_type), norm.data_ptr(),
+                                        _stream_ptr(stream)), "lora_clip")
+        return norm

@@ -1,0 +1,31 @@
+// attn.h -- arguments and launchers of the attention kernels.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "internal.h"
+
+namespace lora {
+
+struct AttnArgs {
+  int B = 0, Sq = 0, Sk = 0, Hq = 0, Hk = 0, D = 0, group = 1, causal = 0;
+  float scale = 1.f, cap = 0.f;
+  int64_t sq[3] = {}, sk[3] = {}, sv[3] = {}, so[3] = {};
+  int64_t sdo[3] = {}, sdq[3] = {}, sdk[3] = {}, sdv[3] = {};
+  const void *q = nullptr, *k = nullptr, *v = nullptr, *d_o = nullptr;
+  void *o = nullptr, *dq = nullptr, *dk = nullptr, *dv = nullptr;
+  float *lse = nullptr, *delta = nullptr;
+  const float *slopes = nullptr;
+  const int *q_docs = nullptr, *k_docs = nullptr, *prefix = nullptr, *lengths = nullptr;
+  int64_t qds = 0, kds = 0;
+  unsigned *dev_status = nullptr;
+};
+
+cudaError_t launch_attn_fwd(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_dq(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_dkv(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_token(const AttnArgs &a, cudaStream_t s);
+
+}  // namespace lora

@@ -1,0 +1,219 @@
+// attn_api.cu -- the entry points of include/lora_attention.h: argument
+// checks, workspace layout and launches.
+#include <cmath>
+
+#include "attn.h"
+#include "host.h"
+#include "lora_attention.h"
+
+namespace lora {
+namespace {
+
+constexpr int64_t kMaxLen = int64_t(1) << 24;
+
+lora_status_t check_shape(const lora_attention_t *p) {
+  if (p == nullptr) return fail(LORA_ERR_INVALID_ARG, "shape is NULL");
+  if (p->batch < 0 || p->q_len < 0 || p->k_len < 0)
+    return fail(LORA_ERR_INVALID_ARG, "batch, q_len or k_len is negative");
+  if (p->q_heads < 1 || p->k_heads < 1 || p->q_heads % p->k_heads != 0)
+    return fail(LORA_ERR_INVALID_ARG, "%d query heads over %d key heads", p->q_heads, p->k_heads);
+  if (p->dim < 1) return fail(LORA_ERR_INVALID_ARG, "dim = %d", p->dim);
+  if ((p->causal | 1) != 1) return fail(LORA_ERR_INVALID_ARG, "causal = %d is not 0 or 1", p->causal);
+  if (!std::isfinite(p->scale)) return fail(LORA_ERR_INVALID_ARG, "scale is not finite");
+  if (!(p->softcap >= 0.f) || !std::isfinite(p->softcap))
+    return fail(LORA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
+  if ((p->q_docs == nullptr) != (p->k_docs == nullptr))
+    return fail(LORA_ERR_INVALID_ARG, "q_docs and k_docs are given together or not at all");
+  if (p->prefix != nullptr && !p->causal)
+    return fail(LORA_ERR_INVALID_ARG, "a prefix needs causal = 1");
+  for (const void *x : {static_cast<const void *>(p->slopes), static_cast<const void *>(p->q_docs),
+                        static_cast<const void *>(p->k_docs), static_cast<const void *>(p->prefix)})
+    if (reinterpret_cast<uintptr_t>(x) % 4 != 0)
+      return fail(LORA_ERR_INVALID_ARG, "slopes, documents or prefix is not 4-byte aligned");
+  if (p->dim % 8 != 0 || p->dim > 128)
+    return fail(LORA_ERR_UNSUPPORTED, "dim = %d: a multiple of 8 up to 128 is needed", p->dim);
+  if (p->q_len >= kMaxLen || p->k_len >= kMaxLen)
+    return fail(LORA_ERR_UNSUPPORTED, "q_len or k_len is 2^24 or more");
+  if (p->batch > 65535 || p->q_heads > 65535 ||
+      p->batch * p->q_heads * (p->q_len + p->k_len + 1) > (int64_t(1) << 33))
+    return fail(LORA_ERR_UNSUPPORTED, "too many heads or rows for one launch");
+  return LORA_OK;
+}
+
+// A tensor of the op: its pointer, and the strides of the dimensions that have
+// more than one entry (16-byte rows).
+lora_status_t check_tensor(const char *name, const void *p, const int64_t (&s)[3], int64_t batch,
+                           int64_t len, int64_t heads) {
+  const int64_t n[3] = {batch, len, heads};
+  LORA_TRY(check_ptr(p, name, batch * len == 0));
+  for (int i = 0; i < 3; ++i)
+    if (n[i] > 1 && (s[i] < 0 || s[i] % 8 != 0))
+      return fail(LORA_ERR_UNSUPPORTED,
+                  "%s: stride %lld is not a non-negative multiple of 8 elements", name,
+                  (long long)s[i]);
+  return LORA_OK;
+}
+
+AttnArgs make_args(const lora_attention_t *p, const DevInfo &di) {
+  AttnArgs a;
+  a.B = static_cast<int>(p->batch);
+  a.Sq = static_cast<int>(p->q_len);
+  a.Sk = static_cast<int>(p->k_len);
+  a.Hq = p->q_heads;
+  a.Hk = p->k_heads;
+  a.D = p->dim;
+  a.group = p->q_heads / p->k_heads;
+  a.causal = p->causal;
+  a.scale = p->scale;
+  a.cap = p->softcap;
+  for (int i = 0; i < 3; ++i) {
+    a.sq[i] = p->q[i];
+    a.sk[i] = p->k[i];
+    a.sv[i] = p->v[i];
+    a.so[i] = p->o[i];
+    a.sdo[i] = p->d_o[i];
+    a.sdq[i] = p->dq[i];
+    a.sdk[i] = p->dk[i];
+    a.sdv[i] = p->dv[i];
+  }
+  a.slopes = p->slopes;
+  a.q_docs = p->q_docs;
+  a.k_docs = p->k_docs;
+  a.qds = p->q_docs_stride;
+  a.kds = p->k_docs_stride;
+  a.prefix = p->prefix;
+  a.dev_status = di.status;
+  return a;
+}
+
+// Workspace: [delta].
+struct Plan {
+  size_t delta = 0, bytes = 0;
+};
+Plan make_plan(const lora_attention_t *p, bool backward) {
+  Plan w;
+  size_t off = 0;
+  if (backward) {
+    w.delta = off;
+    off += rup(size_t(p->batch) * p->q_heads * p->q_len * 4, 256);
+  }
+  w.bytes = off;
+  return w;
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t lora_attention_workspace_bytes(const lora_attention_t *shape, int backward) {
+  clear_error();
+  if (check_shape(shape) != LORA_OK) return 0;
+  return make_plan(shape, backward != 0).bytes;
+}
+
+lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, const void *k,
+                                 const void *v, void *o, float *lse, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  clear_error();
+  LORA_TRY(check_shape(shape));
+  const bool no_q = shape->batch == 0 || shape->q_len == 0;
+  const bool no_k = shape->batch == 0 || shape->k_len == 0;
+  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
+  if (reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+    return fail(LORA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
+  const Plan w = make_plan(shape, false);
+  LORA_TRY(check_ws(workspace, workspace_bytes, w.bytes));
+  if (no_q) return LORA_OK;
+  DevInfo di;
+  LORA_TRY(device_info(di));
+  AttnArgs a = make_args(shape, di);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lse = lse;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, st); });
+}
+
+lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o, const void *q,
+                                 const void *k, const void *v, const void *o, const float *lse,
+                                 void *dq, void *dk, void *dv, void *workspace,
+                                 size_t workspace_bytes, void *stream) {
+  clear_error();
+  LORA_TRY(check_shape(shape));
+  const bool no_q = shape->batch == 0 || shape->q_len == 0;
+  const bool no_k = shape->batch == 0 || shape->k_len == 0;
+  LORA_TRY(check_tensor("do", d_o, shape->d_o, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("dq", dq, shape->dq, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("dk", dk, shape->dk, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("dv", dv, shape->dv, shape->batch, shape->k_len, shape->k_heads));
+  if ((lse == nullptr && !no_q) || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
+    return fail(LORA_ERR_INVALID_ARG, "lse is NULL or not 4-byte aligned");
+  const Plan w = make_plan(shape, true);
+  LORA_TRY(check_ws(workspace, workspace_bytes, w.bytes));
+  if (no_q && no_k) return LORA_OK;
+  DevInfo di;
+  LORA_TRY(device_info(di));
+  AttnArgs a = make_args(shape, di);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.d_o = d_o;
+  a.o = const_cast<void *>(o);
+  a.lse = const_cast<float *>(lse);
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.delta = reinterpret_cast<float *>(at(workspace, w.delta));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!no_q) LORA_TRY(run(LORA_K_ATTN_DQ, st, "attention dq", [&] { return launch_attn_dq(a, st); }));
+  if (!no_k)
+    LORA_TRY(run(LORA_K_ATTN_DKV, st, "attention dk and dv", [&] { return launch_attn_dkv(a, st); }));
+  return LORA_OK;
+}
+
+size_t lora_attention_token_workspace_bytes(const lora_attention_t *shape) {
+  clear_error();
+  if (check_shape(shape) != LORA_OK) return 0;
+  return 0;
+}
+
+lora_status_t lora_attention_token(const lora_attention_t *shape, const void *q, const void *k,
+                                   const void *v, const int32_t *lengths, void *o,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
+  clear_error();
+  LORA_TRY(check_shape(shape));
+  if (shape->q_len != 1 || shape->causal || shape->q_docs != nullptr || shape->prefix != nullptr)
+    return fail(LORA_ERR_INVALID_ARG, "one token: q_len = 1 and no causal, documents or prefix");
+  const bool empty = shape->batch == 0;
+  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
+  if ((lengths == nullptr && !empty) || reinterpret_cast<uintptr_t>(lengths) % 4 != 0)
+    return fail(LORA_ERR_INVALID_ARG, "lengths is NULL or not 4-byte aligned");
+  if (empty) return LORA_OK;
+  DevInfo di;
+  LORA_TRY(device_info(di));
+  AttnArgs a = make_args(shape, di);
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.o = o;
+  a.lengths = lengths;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return run(LORA_K_ATTN_TOKEN, st, "attention of one token", [&] { return launch_attn_token(a, st); });
+}
+
+}  // extern "C"

@@ -1,0 +1,432 @@
+// clip.cu -- global gradient norm and clipping (include/lora_clip.h).
+//
+// Two passes, both bound by memory: one reads every gradient and leaves the
+// norm and the factor in the plan, the other scales.  The plan cuts the
+// tensors into chunks of 16 KB (4 KB where that would leave SMs without
+// work), one 32-byte record each, so that a block finds its work with one
+// load whatever the number of tensors; the record of a block's next chunk is
+// loaded before the present one is read.  The scaling pass visits the chunks
+// in reverse order: those read last are still in L2.
+#include <cuda_bf16.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "host.h"
+#include "lora_clip.h"
+#include "ptx.cuh"
+
+namespace lora {
+namespace {
+
+constexpr int kThreads = 256, kVecs = 4;  // 16-byte vectors of a thread per 16 KB chunk
+constexpr int kBlocksPerSm = 8, kMaxBlocks = 4096;
+
+struct Chunk {
+  const void *in;
+  void *out;
+  int count, dtype;
+  int64_t pad;
+};
+static_assert(sizeof(Chunk) == 32, "chunk record");
+
+struct PlanHead {
+  unsigned ticket;  // blocks of the norm pass done; 0 between calls
+  float factor;
+  int64_t pad;
+  double partial[kMaxBlocks];
+};
+static_assert(sizeof(PlanHead) % 32 == 0 || sizeof(PlanHead) % 16 == 0, "chunks stay aligned");
+
+__device__ __forceinline__ Chunk load_chunk(const Chunk *p) {
+  Chunk c;
+  const int4 a = __ldg(reinterpret_cast<const int4 *>(p));
+  const int4 b = __ldg(reinterpret_cast<const int4 *>(p) + 1);
+  reinterpret_cast<int4 *>(&c)[0] = a;
+  reinterpret_cast<int4 *>(&c)[1] = b;
+  return c;
+}
+
+// Elements before the first 16-byte boundary (at most n), and vectors after.
+template <int ES>
+__device__ __forceinline__ void split_run(const void *p, int n, int &head, int &vecs) {
+  head = min(n, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / ES);
+  vecs = (n - head) / (16 / ES);
+}
+
+__device__ __forceinline__ float2 bf2(unsigned u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// The elements of one 16-byte vector as floats.
+template <bool BF>
+__device__ __forceinline__ void unpack(const uint4 &v, float (&f)[BF ? 8 : 4]) {
+  const unsigned w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (BF) {
+      const float2 t = bf2(w[i]);
+      f[2 * i] = t.x;
+      f[2 * i + 1] = t.y;
+    } else {
+      f[i] = __uint_as_float(w[i]);
+    }
+  }
+}
+
+// fp32 sums of squares outside these bounds may have lost squares to
+// underflow or overflow (each square kept to 2^-24 above 2^-126).
+constexpr float kSafeLow = 1e-30f, kSafeHigh = 1e30f;
+
+template <bool BF, bool LARGEST>
+__device__ void add_chunk(const Chunk &c, double &acc) {
+  constexpr int N = BF ? 8 : 4, ES = 16 / N;
+  int head, vecs;
+  split_run<ES>(c.in, c.count, head, vecs);
+  const uint4 *body = reinterpret_cast<const uint4 *>(static_cast<const char *>(c.in) + head * ES);
+  const int tid = threadIdx.x;
+  uint4 v[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int i = tid + u * kThreads;
+    v[u] = i < vecs ? __ldg(body + i) : make_uint4(0, 0, 0, 0);
+  }
+  // the elements outside whole vectors: fewer than 2 N of them
+  const int rest = c.count - vecs * N;
+  float lone = 0.f;
+  if (tid < rest) {
+    const int i = tid < head ? tid : tid + vecs * N;
+    if constexpr (BF)
+      lone = __bfloat162float(static_cast<const __nv_bfloat16 *>(c.in)[i]);
+    else
+      lone = static_cast<const float *>(c.in)[i];
+  }
+  if constexpr (LARGEST) {
+    // fmaxf drops NaN: a NaN is carried over by the comparison
+    float m = static_cast<float>(acc);
+    auto top = [&](float x) {
+      x = fabsf(x);
+      if (!(x <= m)) m = (m != m) ? m : x;
+    };
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      float f[N];
+      unpack<BF>(v[u], f);
+#pragma unroll
+      for (int e = 0; e < N; ++e) top(f[e]);
+    }
+    top(lone);
+    acc = m;
+  } else {
+    float s0 = lone * lone, s1 = 0.f;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) {
+      float f[N];
+      unpack<BF>(v[u], f);
+#pragma unroll
+      for (int e = 0; e < N; e += 2) {
+        s0 = fmaf(f[e], f[e], s0);
+        s1 = fmaf(f[e + 1], f[e + 1], s1);
+      }
+    }
+    const float s = s0 + s1;
+    if (s >= kSafeLow && s <= kSafeHigh) {
+      acc += static_cast<double>(s);
+    } else {  // all zero, far off scale, or not finite: again in fp64
+      unsigned any = __float_as_uint(lone) << 1;
+#pragma unroll
+      for (int u = 0; u < kVecs; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
+      if (any != 0) {
+        double d = static_cast<double>(lone) * lone;
+#pragma unroll 1
+        for (int u = 0; u < kVecs; ++u) {
+          const int i = tid + u * kThreads;
+          if (i >= vecs) break;
+          float f[N];
+          unpack<BF>(__ldg(body + i), f);
+#pragma unroll
+          for (int e = 0; e < N; ++e) d += static_cast<double>(f[e]) * f[e];
+        }
+        acc += d;
+      }
+    }
+  }
+}
+
+template <bool LARGEST>
+__device__ __forceinline__ double join(double a, double b) {
+  if constexpr (LARGEST) return (a != a) ? a : (b <= a ? a : b);  // NaN wins
+  return a + b;
+}
+
+// The block's value in thread 0; the order depends on the block size only.
+template <bool LARGEST>
+__device__ double join_block(double v) {
+  __shared__ double part[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(~0u, v, o));
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
+  __syncthreads();
+  v = part[0];
+  if (threadIdx.x == 0)
+    for (int i = 1; i < kThreads / 32; ++i) v = join<LARGEST>(v, part[i]);
+  return v;
+}
+
+template <bool LARGEST>
+__global__ void __launch_bounds__(kThreads) k_grad_norm(PlanHead *head, const Chunk *chunks,
+                                                        int n, float max_norm, float *norm) {
+  __shared__ bool last;
+  griddep_wait();
+  griddep_launch_dependents();
+  double acc = 0.0;
+  int i = blockIdx.x;
+  if (i < n) {
+    Chunk c = load_chunk(chunks + i);
+    while (true) {
+      const int next = i + gridDim.x;
+      Chunk cn = c;
+      if (next < n) cn = load_chunk(chunks + next);
+      if (c.dtype == LORA_BF16)
+        add_chunk<true, LARGEST>(c, acc);
+      else
+        add_chunk<false, LARGEST>(c, acc);
+      if (next >= n) break;
+      c = cn;
+      i = next;
+    }
+  }
+  acc = join_block<LARGEST>(acc);
+  if (threadIdx.x == 0) {
+    head->partial[blockIdx.x] = acc;
+    __threadfence();
+    last = atomicAdd(&head->ticket, 1u) == gridDim.x - 1;
+  }
+  __syncthreads();
+  if (!last) return;
+  // the last block joins the partials in the order of the blocks' numbers
+  __threadfence();
+  double v = 0.0;
+  for (int b = threadIdx.x; b < gridDim.x; b += kThreads)
+    v = join<LARGEST>(v, __ldcg(&head->partial[b]));
+  __syncthreads();
+  v = join_block<LARGEST>(v);
+  if (threadIdx.x == 0) {
+    const double total = LARGEST ? v : sqrt(v);
+    const double by = static_cast<double>(max_norm) / (total + 1e-6);
+    norm[0] = static_cast<float>(total);
+    head->factor = by > 1.0 ? 1.f : static_cast<float>(by);  // NaN stays NaN
+    head->ticket = 0;
+  }
+}
+
+template <bool BF>
+__device__ __forceinline__ void scale_chunk(const Chunk &c, float f) {
+  constexpr int N = BF ? 8 : 4, ES = 16 / N;
+  using T = typename std::conditional<BF, __nv_bfloat16, float>::type;
+  const T *in = static_cast<const T *>(c.in);
+  T *out = static_cast<T *>(c.out);
+  auto one = [&](int i) {
+    if constexpr (BF)
+      out[i] = __float2bfloat16_rn(__bfloat162float(in[i]) * f);
+    else
+      out[i] = in[i] * f;
+  };
+  const int tid = threadIdx.x;
+  if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
+    for (int i = tid; i < c.count; i += kThreads) one(i);  // no common alignment
+    return;
+  }
+  int head, vecs;
+  split_run<ES>(c.in, c.count, head, vecs);
+  const uint4 *src = reinterpret_cast<const uint4 *>(in + head);
+  uint4 *dst = reinterpret_cast<uint4 *>(out + head);
+  uint4 v[kVecs];
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int i = tid + u * kThreads;
+    if (i < vecs) v[u] = src[i];
+  }
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int i = tid + u * kThreads;
+    if (i >= vecs) continue;
+    float x[N];
+    unpack<BF>(v[u], x);
+    uint4 o;
+    unsigned *w = reinterpret_cast<unsigned *>(&o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (BF) {
+        const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * e] * f, x[2 * e + 1] * f);
+        w[e] = *reinterpret_cast<const unsigned *>(&p);
+      } else {
+        w[e] = __float_as_uint(x[e] * f);
+      }
+    }
+    dst[i] = o;
+  }
+  if (tid < c.count - vecs * N) one(tid < head ? tid : tid + vecs * N);
+}
+
+__global__ void __launch_bounds__(kThreads) k_grad_clip(const PlanHead *head, const Chunk *chunks,
+                                                        int n) {
+  // the chunk records do not depend on the norm pass
+  int i = n - 1 - static_cast<int>(blockIdx.x);
+  Chunk c = load_chunk(chunks + max(i, 0));
+  griddep_wait();
+  griddep_launch_dependents();
+  const float f = __ldcg(&head->factor);
+  while (i >= 0) {
+    const int next = i - static_cast<int>(gridDim.x);
+    Chunk cn = c;
+    if (next >= 0) cn = load_chunk(chunks + next);
+    if (f != 1.f || c.in != c.out) {
+      if (c.dtype == LORA_BF16)
+        scale_chunk<true>(c, f);
+      else
+        scale_chunk<false>(c, f);
+    }
+    c = cn;
+    i = next;
+  }
+}
+
+// ---------------------------------------------------------------- host
+lora_status_t check_tensors(const lora_clip_tensor_t *t, int n, int64_t *bytes) {
+  if (n < 0 || n > (1 << 24)) return fail(LORA_ERR_INVALID_ARG, "n = %d tensors", n);
+  if (n > 0 && t == nullptr) return fail(LORA_ERR_INVALID_ARG, "tensors is NULL");
+  *bytes = 0;
+  for (int i = 0; i < n; ++i) {
+    if (t[i].dtype != LORA_BF16 && t[i].dtype != LORA_FP32)
+      return fail(LORA_ERR_INVALID_ARG, "tensor %d: dtype %d is not LORA_BF16 or LORA_FP32", i,
+                  int(t[i].dtype));
+    const int es = t[i].dtype == LORA_BF16 ? 2 : 4;
+    if (t[i].count < 0 || t[i].count > (int64_t(1) << 40))
+      return fail(LORA_ERR_INVALID_ARG, "tensor %d: %lld elements", i, (long long)t[i].count);
+    if (t[i].count == 0) continue;
+    if (t[i].in == nullptr || t[i].out == nullptr)
+      return fail(LORA_ERR_INVALID_ARG, "tensor %d: NULL", i);
+    if (reinterpret_cast<uintptr_t>(t[i].in) % es || reinterpret_cast<uintptr_t>(t[i].out) % es)
+      return fail(LORA_ERR_INVALID_ARG, "tensor %d is not aligned to its type", i);
+    *bytes += t[i].count * es;
+  }
+  if (*bytes > (int64_t(1) << 42))
+    return fail(LORA_ERR_UNSUPPORTED, "more than 2^42 bytes of gradients");
+  return LORA_OK;
+}
+
+// 4 KB chunks (one vector a thread) where 16 KB ones would not give a GB300's
+// 152 SMs four blocks each.
+int chunk_bytes(int64_t total) { return total < int64_t(152) * 4 * 16384 ? 4096 : 16384; }
+
+int64_t count_chunks(const lora_clip_tensor_t *t, int n, int cb) {
+  int64_t c = 0;
+  for (int i = 0; i < n; ++i) {
+    const int64_t per = cb / (t[i].dtype == LORA_BF16 ? 2 : 4);
+    c += (t[i].count + per - 1) / per;
+  }
+  return c;
+}
+
+lora_status_t check_plan(const void *plan, size_t bytes, int largest, const float *norm, int *n) {
+  if (plan == nullptr || norm == nullptr)
+    return fail(LORA_ERR_INVALID_ARG, "plan or norm is NULL");
+  if (reinterpret_cast<uintptr_t>(plan) % 16 || reinterpret_cast<uintptr_t>(norm) % 4)
+    return fail(LORA_ERR_INVALID_ARG, "plan (16 bytes) or norm (4 bytes) is not aligned");
+  if ((largest | 1) != 1) return fail(LORA_ERR_INVALID_ARG, "largest = %d is not 0 or 1", largest);
+  if (bytes < sizeof(PlanHead) || (bytes - sizeof(PlanHead)) % sizeof(Chunk) != 0 ||
+      (bytes - sizeof(PlanHead)) / sizeof(Chunk) > size_t(INT32_MAX) / 2)
+    return fail(LORA_ERR_INVALID_ARG, "%zu bytes is no plan's size", bytes);
+  *n = static_cast<int>((bytes - sizeof(PlanHead)) / sizeof(Chunk));
+  return LORA_OK;
+}
+
+lora_status_t norm_pass(const DevInfo &di, void *plan, int n, float max_norm, int largest,
+                        float *norm, cudaStream_t st) {
+  PlanHead *head = static_cast<PlanHead *>(plan);
+  const Chunk *chunks = reinterpret_cast<const Chunk *>(head + 1);
+  const int most = di.sms * kBlocksPerSm < kMaxBlocks ? di.sms * kBlocksPerSm : kMaxBlocks;
+  const int grid = n < 1 ? 1 : n < most ? n : most;
+  return run(LORA_K_GRAD_NORM, st, "gradient norm", [&] {
+    return largest ? launch_pdl(k_grad_norm<true>, dim3(grid), dim3(kThreads), 0, st, head, chunks,
+                                n, max_norm, norm)
+                   : launch_pdl(k_grad_norm<false>, dim3(grid), dim3(kThreads), 0, st, head,
+                                chunks, n, max_norm, norm);
+  });
+}
+
+}  // namespace
+}  // namespace lora
+
+using namespace lora;
+
+extern "C" {
+
+size_t lora_clip_plan_bytes(const lora_clip_tensor_t *tensors, int n) {
+  clear_error();
+  int64_t total = 0;
+  if (check_tensors(tensors, n, &total) != LORA_OK) return 0;
+  return sizeof(PlanHead) + size_t(count_chunks(tensors, n, chunk_bytes(total))) * sizeof(Chunk);
+}
+
+lora_status_t lora_clip_plan_build(const lora_clip_tensor_t *tensors, int n, void *image,
+                                   size_t image_bytes) {
+  clear_error();
+  int64_t total = 0;
+  LORA_TRY(check_tensors(tensors, n, &total));
+  const int cb = chunk_bytes(total);
+  const size_t need = sizeof(PlanHead) + size_t(count_chunks(tensors, n, cb)) * sizeof(Chunk);
+  if (image == nullptr || image_bytes != need)
+    return fail(LORA_ERR_WORKSPACE, "a plan image of %zu bytes is needed, got %zu%s", need,
+                image_bytes, image == nullptr ? " (NULL)" : "");
+  uint8_t *out = static_cast<uint8_t *>(image);
+  std::memset(out, 0, sizeof(PlanHead));
+  out += sizeof(PlanHead);
+  for (int i = 0; i < n; ++i) {
+    const int es = tensors[i].dtype == LORA_BF16 ? 2 : 4;
+    const int64_t per = cb / es;
+    for (int64_t at = 0; at < tensors[i].count; at += per) {
+      const int64_t left = tensors[i].count - at;
+      Chunk c = {};
+      c.in = static_cast<const char *>(tensors[i].in) + at * es;
+      c.out = static_cast<char *>(tensors[i].out) + at * es;
+      c.count = static_cast<int>(left < per ? left : per);
+      c.dtype = tensors[i].dtype;
+      std::memcpy(out, &c, sizeof(c));
+      out += sizeof(c);
+    }
+  }
+  return LORA_OK;
+}
+
+lora_status_t lora_clip_norm(void *plan, size_t plan_bytes, int largest, float *norm,
+                             void *stream) {
+  clear_error();
+  int n = 0;
+  LORA_TRY(check_plan(plan, plan_bytes, largest, norm, &n));
+  DevInfo di;
+  LORA_TRY(device_info(di));
+  return norm_pass(di, plan, n, 0.f, largest, norm, static_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_clip(void *plan, size_t plan_bytes, float max_norm, int largest, float *norm,
+                        void *stream) {
+  clear_error();
+  int n = 0;
+  LORA_TRY(check_plan(plan, plan_bytes, largest, norm, &n));
+  if (!(max_norm >= 0.f)) return fail(LORA_ERR_INVALID_ARG, "max_norm must be >= 0");
+  DevInfo di;
+  LORA_TRY(device_info(di));
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  LORA_TRY(norm_pass(di, plan, n, max_norm, largest, norm, st));
+  if (n == 0) return LORA_OK;
+  PlanHead *head = static_cast<PlanHead *>(plan);
+  const Chunk *chunks = reinterpret_cast<const Chunk *>(head + 1);
+  const int most = di.sms * kBlocksPerSm;
+  return run(LORA_K_GRAD_CLIP, st, "gradient clip", [&] {
+    return launch_pdl(k_grad_clip, dim3(n < most ? n : most), dim3(kThreads), 0, st, head, chunks, n);
+  });
+}
+
+}  // extern "C"

@@ -2,8 +2,6 @@
 // buffer planning, TMA tensor maps and the launch sequence of the forward
 // and backward passes.  No allocation, no synchronisation (except
 // lora_device_status, which reads the device status word).
-#include <cudaTypedefs.h>
-
 #include <atomic>
 #include <cmath>
 #include <cstdarg>
@@ -11,8 +9,7 @@
 #include <mutex>
 #include <string>
 
-#include "internal.h"
-#include "lora_linear.h"
+#include "host.h"
 #include "lora_fp8.h"
 #include "lora_q4.h"
 #include "lora_swiglu.h"
@@ -46,6 +43,10 @@ int take_one(std::atomic<int> &counter) {
   return pending > 0 ? 1 : 0;
 }
 
+}  // namespace
+
+void clear_error() { t_err.clear(); }
+
 lora_status_t fail(lora_status_t st, const char *fmt, ...) {
   char buf[512];
   va_list ap;
@@ -57,14 +58,11 @@ lora_status_t fail(lora_status_t st, const char *fmt, ...) {
 }
 
 // ---------------------------------------------------------------- device
-struct DevInfo {
-  bool init = false;
-  int sms = 0, major = 0, minor = 0;
-  unsigned *status = nullptr;
-};
+namespace {
 std::mutex g_mtx;
 constexpr int kMaxDevices = 64;
 DevInfo g_dev[kMaxDevices];
+}  // namespace
 
 lora_status_t device_info(DevInfo &out) {
   int dev = 0;
@@ -113,6 +111,7 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
+namespace {
 // 2-D bf16 map over a row-major [outer][inner] tensor with the given row
 // pitch; boxes of box_inner x box_outer elements, 128-byte swizzle,
 // out-of-bounds elements read as zero.
@@ -177,21 +176,25 @@ struct Q4W {
   const void *codes = nullptr, *scales = nullptr;
 };
 
+}  // namespace
+
 // ---------------------------------------------------------------- launches
-template <class F>
-lora_status_t run(lora_kernel_kind_t kind, cudaStream_t s, const char *what, F &&launch) {
-  int j = -1;
+lora_status_t timing_before(lora_kernel_kind_t kind, cudaStream_t s, const char *what, int *slot) {
+  *slot = -1;
   if (t_hook.events != nullptr && t_hook.used < t_hook.n) {
-    j = t_hook.used++;
+    const int j = t_hook.used++;
     const cudaError_t er = cudaEventRecord(static_cast<cudaEvent_t>(t_hook.events[2 * j]), s);
     if (er != cudaSuccess)
       return fail(LORA_ERR_CUDA, "timing event before %s: %s", what, cudaGetErrorString(er));
     if (t_hook.kinds) t_hook.kinds[j] = static_cast<int>(kind);
+    *slot = j;
   }
-  const cudaError_t e = launch();
-  if (e != cudaSuccess) return fail(LORA_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
-  if (j >= 0) {
-    const cudaError_t er = cudaEventRecord(static_cast<cudaEvent_t>(t_hook.events[2 * j + 1]), s);
+  return LORA_OK;
+}
+
+lora_status_t timing_after(int slot, cudaStream_t s, const char *what) {
+  if (slot >= 0) {
+    const cudaError_t er = cudaEventRecord(static_cast<cudaEvent_t>(t_hook.events[2 * slot + 1]), s);
     if (er != cudaSuccess)
       return fail(LORA_ERR_CUDA, "timing event after %s: %s", what, cudaGetErrorString(er));
   }
@@ -199,15 +202,8 @@ lora_status_t run(lora_kernel_kind_t kind, cudaStream_t s, const char *what, F &
   return LORA_OK;
 }
 
-#define LORA_TRY(expr)                     \
-  do {                                     \
-    const lora_status_t st_ = (expr);      \
-    if (st_ != LORA_OK) return st_;        \
-  } while (0)
-
+namespace {
 // ---------------------------------------------------------------- planning
-int64_t rup(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
 // Byte layout of the saved buffer and of the workspace for one shape.
 // The main GEMMs' tail-split region is optional: fwd_ws_min / bwd_ws_min
 // leave it out, fwd_ws / bwd_ws include it (when the shape splits at all).
@@ -303,7 +299,9 @@ lora_status_t check_shape(int r, int64_t M, int64_t d_in, int64_t d_out, lora_dt
   return LORA_OK;
 }
 
-lora_status_t check_ptr(const void *p, const char *name, bool may_be_null = false) {
+}  // namespace
+
+lora_status_t check_ptr(const void *p, const char *name, bool may_be_null) {
   if (p == nullptr) {
     if (may_be_null) return LORA_OK;
     return fail(LORA_ERR_INVALID_ARG, "%s is NULL", name);
@@ -323,7 +321,7 @@ lora_status_t check_ws(const void *ws, size_t have, size_t need) {
   return LORA_OK;
 }
 
-uint8_t *at(void *base, size_t off) { return static_cast<uint8_t *>(base) + off; }
+namespace {
 
 // ---------------------------------------------------------------- bf16 path
 // At least two 256 x 512 pair tiles of an M x N output for every CTA pair.

@@ -1,0 +1,203 @@
+"""Rotary positions of q and k (ch05 "Acceleration principles: Triton kernels
+and fused LoRA", §5.5): what stands between the q and k LoRA layers and the
+attention.  Both tensors are turned in one launch of the CUDA library; angles
+are exact at any position (see include/lora_rotary.h).
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+import math
+
+import torch
+
+from . import _lib
+from .lora import _dtype_code, _stream_ptr
+
+
+class RotaryFrequencies:
+    """Frequencies of a head's rotated pairs, on the device: what a program
+    keeps beside its weights.  `radians` are the frequencies per position,
+    `magnitude` the factor on the rotated elements."""
+
+    def __init__(self, radians, magnitude: float = 1.0, device=None):
+        self.radians = [float(w) for w in radians]
+        self.magnitude = float(magnitude)
+        n = len(self.radians)
+        words = (ctypes.c_uint64 * max(n, 1))()
+        _lib.check(_lib.lib().lora_rotary_turns((ctypes.c_double * max(n, 1))(*self.radians), n,
+                                                words), "lora_rotary_turns")
+        signed = [w - (1 << 64) if w >> 63 else w for w in words[:n]]
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+
+    @property
+    def rot(self) -> int:
+        return 2 * len(self.radians)
+
+
+def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling: dict | None = None,
+                       device=None) -> RotaryFrequencies:
+    """w_i = base^(-2i / rot), i < rot / 2, scaled for long contexts by `scaling`:
+
+    None
+        as they are.
+    {"kind": "linear", "factor": f}
+        every frequency divided by f (positions squeezed into the trained range).
+    {"kind": "base", "factor": f}
+        the base times f^(rot / (rot - 2)): the slowest pair is stretched f
+        times, the fastest not at all.
+    {"kind": "bands", "factor": f, "original": n, "low": a, "high": b}
+        by the turns t a pair makes over the n trained positions: kept for
+        t >= b, divided by f for t <= a, between them the blend
+        (t - a) / (b - a) of the two frequencies.
+    {"kind": "ramp", "factor": f, "original": n, "fast": a, "slow": b}
+        the same blend along a linear ramp over the pair's index, from the
+        pair that makes a turns over n positions (kept) to the one that makes
+        b; rotated elements are scaled by 0.1 ln f + 1, or by "magnitude".
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot = {rot} is not an even number >= 2")
+    if not (base > 0 and math.isfinite(base)):
+        raise ValueError(f"base = {base}")
+    s = dict(scaling or {})
+    kind = s.pop("kind", None)
+    need = {None: (), "linear": ("factor",), "base": ("factor",),
+            "bands": ("factor", "original", "low", "high"),
+            "ramp": ("factor", "original", "fast", "slow")}
+    if kind not in need:
+        raise ValueError(f"scaling kind {kind!r} is not one of {sorted(k for k in need if k)}")
+    magnitude = float(s.pop("magnitude", 0.1 * math.log(s.get("factor", 1.0)) + 1.0)) \
+        if kind == "ramp" else 1.0
+    if sorted(s) != sorted(need[kind]):
+        raise ValueError(f"scaling {kind!r} takes {need[kind]}, got {sorted(s)}")
+    for name, value in s.items():
+        if not (value > 0 and math.isfinite(value)):
+            raise ValueError(f"scaling {name} = {value} must be positive")
+    f = s.get("factor", 1.0)
+    if kind == "base" and rot > 2:
+        base = base * f ** (rot / (rot - 2))
+    w = [base ** (-2.0 * i / rot) for i in range(rot // 2)]
+    if kind == "linear":
+        w = [x / f for x in w]
+    elif kind == "bands":
+        if not s["high"] > s["low"]:
+            raise ValueError("scaling 'bands' needs high > low")
+
+        def band(x):
+            keep = (s["original"] * x / (2 * math.pi) - s["low"]) / (s["high"] - s["low"])
+            keep = min(1.0, max(0.0, keep))
+            return keep * x + (1.0 - keep) * x / f
+        w = [band(x) for x in w]
+    elif kind == "ramp":
+        def pair_of(turns):  # index of the pair that makes so many turns over `original`
+            return rot * math.log(s["original"] / (turns * 2 * math.pi)) / (2 * math.log(base))
+        lo = max(math.floor(pair_of(s["fast"])), 0)
+        hi = min(math.ceil(pair_of(s["slow"])), rot - 1)
+        go = [min(1.0, max(0.0, (i - lo) / max(hi - lo, 0.001))) for i in range(rot // 2)]
+        w = [(1.0 - g) * x + g * x / f for x, g in zip(w, go)]
+    return RotaryFrequencies(w, magnitude, device)
+
+
+def _strides(t, name):
+    """(batch, token, head) strides of [batch, seq, heads, dim] or [tokens, heads, dim]."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dim() == 4:
+        s = t.stride()
+    elif t.dim() == 3:
+        s = (0,) + t.stride()
+    else:
+        raise ValueError(f"{name} must be [batch, seq, heads, dim] or [tokens, heads, dim]")
+    if s[3] != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    return s[:3]
+
+
+def _empty_like(t):
+    return torch.empty(t.shape, dtype=t.dtype, device=t.device)
+
+
+def _on(stream):
+    """Buffers made for work on another stream come from that stream's pool."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _turn(q, k, positions, freqs, interleaved, inverse, q_out, k_out, stream):
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q and k are both None")
+    sh = _lib.RotaryShape()
+    lead = first.shape[:-2]
+    sh.batch, sh.seq = (1, lead[0]) if len(lead) == 1 else lead
+    sh.dim, sh.rot = first.shape[-1], freqs.rot
+    sh.interleaved, sh.inverse, sh.magnitude = int(interleaved), int(inverse), freqs.magnitude
+    with _on(stream):
+        if q is not None and q_out is None:
+            q_out = _empty_like(q)
+        if k is not None and k_out is None:
+            k_out = _empty_like(k)
+    for name, x, out in (("q", q, q_out), ("k", k, k_out)):
+        if x is None:
+            continue
+        if x.shape[:-2] != lead or x.shape[-1] != first.shape[-1] or out.shape != x.shape:
+            raise ValueError(f"{name} {tuple(x.shape)} and its output {tuple(out.shape)} do not fit")
+        if x.dtype != first.dtype or out.dtype != first.dtype:
+            raise TypeError("q, k and the outputs must share one dtype")
+        setattr(sh, name + "_heads", x.shape[-2])
+        setattr(sh, name + "_in", _strides(x, name))
+        setattr(sh, name + "_out", _strides(out, name + "_out"))
+    if positions.dtype not in (torch.int32, torch.int64) or not positions.is_cuda:
+        raise TypeError("positions must be an int32 or int64 CUDA tensor")
+    sh.position_bits = 64 if positions.dtype == torch.int64 else 32
+    if positions.shape == lead:
+        sh.position = positions.stride() if len(lead) == 2 else (0, positions.stride(0))
+    elif len(lead) == 2 and positions.shape == lead[1:]:
+        sh.position = (0, positions.stride(0))
+    else:
+        raise ValueError(f"positions {tuple(positions.shape)} do not fit tokens {tuple(lead)}")
+    if freqs.turns.device != first.device:
+        raise ValueError("the frequencies are on another device")
+    ptr = lambda t: None if t is None else t.data_ptr() or None
+    _lib.check(_lib.lib().lora_rotary(ctypes.byref(sh), ptr(q), ptr(k), ptr(positions),
+                                      ptr(freqs.turns), _dtype_code(first), ptr(q_out),
+                                      ptr(k_out), _stream_ptr(stream)), "lora_rotary")
+    return q_out, k_out
+
+
+def rotary_forward(q, k, positions, freqs: RotaryFrequencies, *, interleaved=False, q_out=None,
+                   k_out=None, stream=None):
+    """(q, k) turned by their tokens' positions; q or k may be None.
+
+    q and k are [batch, seq, heads, dim] or [tokens, heads, dim] with any
+    strides (views of a fused q|k|v output); positions [batch, seq], [seq] or
+    [tokens].  q_out / k_out may be q / k themselves (in place)."""
+    return _turn(q, k, positions, freqs, interleaved, False, q_out, k_out, stream)
+
+
+def rotary_backward(dq, dk, positions, freqs: RotaryFrequencies, *, interleaved=False,
+                    dq_out=None, dk_out=None, stream=None):
+    """Gradients of the inputs from those of rotary_forward's outputs."""
+    return _turn(dq, dk, positions, freqs, interleaved, True, dq_out, dk_out, stream)
+
+
+class RotaryFunction(torch.autograd.Function):
+    """Autograd function: saves the positions only."""
+
+    @staticmethod
+    def forward(ctx, q, k, positions, freqs, interleaved):
+        ctx.save_for_backward(positions)
+        ctx.freqs, ctx.interleaved = freqs, interleaved
+        return rotary_forward(q, k, positions, freqs, interleaved=interleaved)
+
+    @staticmethod
+    def backward(ctx, dq, dk):
+        positions, = ctx.saved_tensors
+        fit = lambda t: t if t is None or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+        dq, dk = rotary_backward(fit(dq), fit(dk), positions, ctx.freqs,
+                                 interleaved=ctx.interleaved)
+        return dq, dk, None, None, None
+
+
+def rotary(q, k, positions, freqs: RotaryFrequencies, *, interleaved=False):
+    """Rotary positions of q and k with gradients for both."""
+    return RotaryFunction.apply(q, k, positions, freqs, interleaved)
