@@ -53,7 +53,7 @@ typedef struct {
     int64_t batch, q_len, k_len;
     int32_t q_heads, k_heads, dim;
     int32_t causal;               /* 0 or 1                                   */
-    float scale;                  /* finite                                   */
+    float scale;                  /* finite, > 0                              */
     float softcap;                /* > 0: the cap; 0: none                    */
     int64_t q[3], k[3], v[3], o[3];         /* strides: batch, token, head    */
     int64_t d_o[3], dq[3], dk[3], dv[3];    /* same, backward only            */

@@ -1,0 +1,228 @@
+// attn.cuh -- device code shared by the tensor-core attention kernels:
+// 128 x 128 tiles of scores, which of them a mask leaves (wholly or partly),
+// the transform of a score, and the tcgen05 forms with an operand in TMEM.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <climits>
+
+#include "attn.h"
+#include "ptx.cuh"
+
+namespace lora {
+
+constexpr int kTile = 128;  // rows of a query tile, and of a key tile
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// ---------------------------------------------------------------- PTX forms
+// D(tmem) (+)= A(tmem) * B(smem)^T: A is bf16, lane = row, two K elements per
+// 32-bit column (16 K elements: 8 columns).  Issued by one thread.
+__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                               uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_ld() {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// 32 columns of the warp's 32 lanes; the values are there after tmem_wait_ld
+// and pin.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+  uint32_t *r = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// Keeps the uses of loaded registers after the wait before it.
+template <int N>
+__device__ __forceinline__ void pin(float *v) {
+#pragma unroll
+  for (int i = 0; i < N; i += 8)
+    asm volatile("" : "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]),
+                      "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float *v) {
+  const uint32_t *r = reinterpret_cast<const uint32_t *>(v);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// Tiled copies over [batch][head][token][dim] maps: x is the element of the head.
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *tm, uint32_t bar,
+                                            int32_t x, int32_t token, int32_t head, int32_t batch) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(token), "r"(head), "r"(batch)
+      : "memory");
+}
+__device__ __forceinline__ void tma_store_4d(const CUtensorMap *tm, uint32_t src, int32_t x,
+                                             int32_t token, int32_t head, int32_t batch) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%2, %3, %4, %5}], [%1];" ::"l"(
+          reinterpret_cast<uint64_t>(tm)),
+      "r"(src), "r"(x), "r"(token), "r"(head), "r"(batch)
+      : "memory");
+}
+
+// A warpgroup gives back registers above N, or waits for N to be free.
+template <int N>
+__device__ __forceinline__ void set_max_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_max_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)),
+        "l"(reinterpret_cast<uint64_t &>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t &>(d))
+      : "l"(reinterpret_cast<uint64_t &>(a)), "l"(reinterpret_cast<uint64_t &>(b)));
+  return d;
+}
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 p = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&p);
+}
+
+// ---------------------------------------------------------------- masks
+// Documents of one 128-token tile: the range of those >= 0 (lo > hi: none),
+// and whether some token is padding.
+struct DocRange {
+  int lo, hi, padded, unused;
+};
+__device__ __forceinline__ DocRange doc_range(const int4 *ranges, int64_t i) {
+  const int4 r = __ldg(ranges + i);
+  return {r.x, r.y, r.z, r.w};
+}
+__device__ __forceinline__ bool docs_meet(const DocRange &a, const DocRange &b) {
+  return a.lo <= b.hi && b.lo <= a.hi;  // an empty range has lo = INT_MAX, hi = -1
+}
+__device__ __forceinline__ bool docs_equal(const DocRange &a, const DocRange &b) {
+  return a.lo == a.hi && b.lo == a.lo && b.hi == a.lo && !a.padded && !b.padded;
+}
+
+// What a query of position p (its row's index + Sk - Sq) sees without
+// documents: the keys up to this one (below 0: none).
+__device__ __forceinline__ int last_key(const AttnArgs &a, int p, int prefix) {
+  const int lim = a.causal ? max(p, prefix - 1) : a.Sk - 1;
+  return min(lim, a.Sk - 1);
+}
+
+// The score of a raw product z = q . k, in units of log 2, without the mask.
+// CAP: c = cap tanh(z scale / cap) through tanh x = 1 - 2 / (1 + e^2x); r is
+// that reciprocal, dc/dz = scale * 4 r (1 - r).  The absolute error, which is
+// what the softmax sees, stays near 2^-23 cap.
+struct ScoreConst {
+  float scale2;    // scale * log2 e
+  float tanh_in;   // 2 log2 e * scale / cap
+  float cap2;      // cap * log2 e
+  float slope2;    // slope * log2 e
+};
+__device__ __forceinline__ ScoreConst score_const(const AttnArgs &a, int head) {
+  ScoreConst c;
+  c.scale2 = a.scale * kLog2e;
+  c.tanh_in = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
+  c.cap2 = a.cap * kLog2e;
+  c.slope2 = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
+  return c;
+}
+template <bool CAP, bool BIAS>
+__device__ __forceinline__ float score2(const ScoreConst &c, float z, float distance, float &r) {
+  float s;
+  if constexpr (CAP) {
+    r = rcp(1.f + ex2(z * c.tanh_in));
+    s = fmaf(-2.f * c.cap2, r, c.cap2);
+  } else {
+    s = z * c.scale2;
+  }
+  if constexpr (BIAS) s = fmaf(-c.slope2, fabsf(distance), s);
+  return s;
+}
+
+// Zeroes the rows of a [128][DH] tile (64-wide boxes of 128-byte rows) whose
+// token is padding, by one warp, so that an operand's rows that no score
+// uses cannot turn a zero weight into NaN.  docs: the tile's first token.
+template <int DH>
+__device__ __forceinline__ void zero_padding_rows(uint8_t *tile, const int *docs, int rows) {
+  for (int r = threadIdx.x % 32; r < kTile; r += 32)
+    if (r < rows && docs[r] < 0)
+      for (int box = 0; box < DH / 64; ++box)
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4 *>(tile + box * kTile * 128 + r * 128 + i * 16) =
+              make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+// Operand descriptors of a [128][DH] tile as TMA leaves it (128-byte swizzle,
+// boxes of 64 columns): K step kk of 16 along the head (K-major), or of 16
+// tokens (MN-major).
+__device__ __forceinline__ uint64_t desc_head(uint32_t tile, int kk) {
+  return sdesc_sw128(tile + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024);
+}
+__device__ __forceinline__ uint64_t desc_token(uint32_t tile, int kk) {
+  return sdesc_sw128(tile + kk * 2048, kTile * 128, 1024);
+}
+
+}  // namespace lora

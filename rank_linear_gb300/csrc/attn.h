@@ -20,10 +20,19 @@ struct AttnArgs {
   const float *slopes = nullptr;
   const int *q_docs = nullptr, *k_docs = nullptr, *prefix = nullptr, *lengths = nullptr;
   int64_t qds = 0, kds = 0;
+  // documents of every 128-token tile ([batch][tiles] DocRange), with q_docs
+  const int4 *q_ranges = nullptr, *k_ranges = nullptr;
   unsigned *dev_status = nullptr;
 };
 
-cudaError_t launch_attn_fwd(const AttnArgs &a, cudaStream_t s);
+// A [batch][token][head][dim] bf16 tensor's map: boxes of 64 elements x 128
+// tokens of one head, 128-byte swizzle, zeros outside.
+struct AttnMaps {
+  CUtensorMap q, k, v, o;
+};
+
+cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, cudaStream_t s);
 cudaError_t launch_attn_dq(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_dkv(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_token(const AttnArgs &a, cudaStream_t s);

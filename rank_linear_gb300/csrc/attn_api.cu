@@ -19,7 +19,8 @@ lora_status_t check_shape(const lora_attention_t *p) {
     return fail(LORA_ERR_INVALID_ARG, "%d query heads over %d key heads", p->q_heads, p->k_heads);
   if (p->dim < 1) return fail(LORA_ERR_INVALID_ARG, "dim = %d", p->dim);
   if ((p->causal | 1) != 1) return fail(LORA_ERR_INVALID_ARG, "causal = %d is not 0 or 1", p->causal);
-  if (!std::isfinite(p->scale)) return fail(LORA_ERR_INVALID_ARG, "scale is not finite");
+  if (!(p->scale > 0.f) || !std::isfinite(p->scale))
+    return fail(LORA_ERR_INVALID_ARG, "scale must be finite and above 0");
   if (!(p->softcap >= 0.f) || !std::isfinite(p->softcap))
     return fail(LORA_ERR_INVALID_ARG, "softcap must be finite and >= 0");
   if ((p->q_docs == nullptr) != (p->k_docs == nullptr))
@@ -86,19 +87,59 @@ AttnArgs make_args(const lora_attention_t *p, const DevInfo &di) {
   return a;
 }
 
-// Workspace: [delta].
+int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
+
+// Map of a [batch][token][head][dim] tensor (see AttnMaps).  An empty tensor
+// gets a map over one element row that no copy reads.
+lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], const AttnArgs &a,
+                         int len, int heads, const char *what) {
+  auto fn = encode_fn();
+  if (!fn) return fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const uint64_t n[3] = {uint64_t(len), uint64_t(heads), uint64_t(a.B)};
+  const int64_t by[3] = {s[1], s[2], s[0]};
+  cuuint64_t dims[4] = {uint64_t(a.D), 1, 1, 1};
+  cuuint64_t strides[3];
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = n[i] > 0 ? n[i] : 1;
+    strides[i] = n[i] > 1 ? uint64_t(by[i]) * 2 : uint64_t(a.D) * 2;
+  }
+  cuuint32_t box[4] = {64, 128, 1, 1};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(LORA_ERR_CUDA, "tensor map for %s (strides %lld, %lld, %lld) failed: CUresult %d",
+                what, (long long)s[0], (long long)s[1], (long long)s[2], static_cast<int>(r));
+  return LORA_OK;
+}
+
+// Workspace: [document ranges of the query tiles, of the key tiles][delta].
 struct Plan {
-  size_t delta = 0, bytes = 0;
+  size_t q_ranges = 0, k_ranges = 0, delta = 0, bytes = 0;
 };
 Plan make_plan(const lora_attention_t *p, bool backward) {
   Plan w;
   size_t off = 0;
+  if (p->q_docs != nullptr) {
+    w.q_ranges = off;
+    off += rup(size_t(p->batch) * tiles_of(p->q_len) * 16, 256);
+    w.k_ranges = off;
+    off += rup(size_t(p->batch) * tiles_of(p->k_len) * 16, 256);
+  }
   if (backward) {
     w.delta = off;
     off += rup(size_t(p->batch) * p->q_heads * p->q_len * 4, 256);
   }
   w.bytes = off;
   return w;
+}
+
+lora_status_t make_ranges(AttnArgs &a, const Plan &w, void *ws, cudaStream_t st) {
+  if (a.q_docs == nullptr) return LORA_OK;
+  a.q_ranges = reinterpret_cast<const int4 *>(at(ws, w.q_ranges));
+  a.k_ranges = reinterpret_cast<const int4 *>(at(ws, w.k_ranges));
+  return run(LORA_K_ATTN_PREP, st, "document ranges", [&] { return launch_attn_ranges(a, st); });
 }
 
 }  // namespace
@@ -139,7 +180,17 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   a.o = o;
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, st); });
+  AttnMaps m;
+  LORA_TRY(tensor_map(&m.q, q, shape->q, a, a.Sq, a.Hq, "q"));
+  LORA_TRY(tensor_map(&m.o, o, shape->o, a, a.Sq, a.Hq, "o"));
+  if (no_k) {
+    m.k = m.v = m.q;
+  } else {
+    LORA_TRY(tensor_map(&m.k, k, shape->k, a, a.Sk, a.Hk, "k"));
+    LORA_TRY(tensor_map(&m.v, v, shape->v, a, a.Sk, a.Hk, "v"));
+  }
+  LORA_TRY(make_ranges(a, w, workspace, st));
+  return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, m, st); });
 }
 
 lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o, const void *q,

@@ -1,0 +1,481 @@
+// attn_fwd.cu -- attention forward on the tensor cores (include/lora_attention.h).
+//
+// A CTA takes 256 queries of one head as two tiles of 128 and passes once
+// over the keys in tiles of 128: S = Q K^T into TMEM, softmax in registers (a
+// thread owns a whole row: no shuffles), P back into TMEM as bf16 over S, and
+// O += P V with P as the TMEM operand.  While the softmax of one tile runs,
+// the tensor core works for the other.  The running maximum is only followed
+// when it has moved by more than 2^8: until then P is relative to the old one
+// (at most 256, exact in fp32 sums and no worse rounded to bf16), so that O
+// in TMEM is hardly ever rescaled.
+//
+// TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
+#include "attn.cuh"
+#include "host.h"
+
+namespace lora {
+namespace {
+
+// Two softmax warpgroups, and one of which two warps issue the copies and the
+// MMAs.  168 registers a thread at launch; the softmax threads, which hold a
+// row of scores, take 224 and leave the others 56 (2 * 224 + 56 = 3 * 168).
+constexpr int kThreads = 384, kSoftmaxRegs = 224, kIssueRegs = 56;
+constexpr float kRescaleAt = 8.f;
+
+template <int DH>
+struct Layout {
+  static constexpr uint32_t kTileBytes = kTile * DH * 2;
+  static constexpr int kSlots = DH == 64 ? 8 : 4;  // ring of K and V tiles
+  static constexpr uint32_t kBytes = (2 + kSlots) * kTileBytes;
+};
+
+struct Tail {
+  uint64_t q_full;
+  uint64_t full[8], empty[8];
+  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint32_t tmem;
+  int abort_flag;
+  int lo[2], hi[2];
+};
+
+struct Params {
+  AttnArgs a;
+  AttnMaps m;
+};
+
+template <int DH, bool CAP, bool BIAS>
+__global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ Params p) {
+  using L = Layout<DH>;
+  extern __shared__ uint8_t raw[];
+  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  Tail *tail = reinterpret_cast<Tail *>(smem + L::kBytes);
+  const AttnArgs &a = p.a;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  volatile int *abort_flag = &tail->abort_flag;
+
+  // the blocks with most keys first: the last queries of a causal mask
+  const int heads = a.B * a.Hq;
+  const int blocks_q = (a.Sq + 2 * kTile - 1) / (2 * kTile);
+  const int qb = blocks_q - 1 - static_cast<int>(blockIdx.x / heads);
+  const int bh = blockIdx.x % heads, b = bh / a.Hq, h = bh % a.Hq, g = h / a.group;
+  const int row0 = qb * 2 * kTile, off = a.Sk - a.Sq;
+
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&tail->q_full), 1);
+    for (int s = 0; s < L::kSlots; ++s) {
+      mbar_init(smem_u32(&tail->full[s]), 1);
+      mbar_init(smem_u32(&tail->empty[s]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&tail->s_full[t]), 1);
+      mbar_init(smem_u32(&tail->p_full[t]), kTile);
+      mbar_init(smem_u32(&tail->o_done[t]), 1);
+    }
+    mbar_init(smem_u32(&tail->drain), 1);
+    tail->abort_flag = 0;
+    for (int t = 0; t < 2; ++t) {
+      tail->lo[t] = a.q_docs != nullptr ? INT_MAX : 0;
+      tail->hi[t] = 0;
+    }
+    fence_barrier_init();
+    tma_prefetch(&p.m.q);
+    tma_prefetch(&p.m.k);
+    tma_prefetch(&p.m.v);
+  }
+  griddep_wait();
+  griddep_launch_dependents();
+  if (warp == 9) {
+    tmem_alloc(smem_u32(&tail->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tail->tmem;
+
+  // ---- the key tiles [lo, hi) that some row of each query tile sees
+  const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
+  const int ktiles = (a.Sk + kTile - 1) / kTile, qtiles = (a.Sq + kTile - 1) / kTile;
+  int most[2];
+  for (int t = 0; t < 2; ++t) {
+    const int first = row0 + t * kTile, last = min(first + kTile, a.Sq) - 1;
+    most[t] = first < a.Sq ? (last_key(a, last + off, prefix) + kTile) / kTile : 0;
+  }
+  if (a.q_docs != nullptr) {
+    for (int t = 0; t < 2; ++t) {
+      if (most[t] <= 0) continue;
+      const DocRange qr = doc_range(a.q_ranges, int64_t(b) * qtiles + 2 * qb + t);
+      for (int n = threadIdx.x; n < most[t]; n += kThreads)
+        if (docs_meet(qr, doc_range(a.k_ranges, int64_t(b) * ktiles + n))) {
+          atomicMin(&tail->lo[t], n);
+          atomicMax(&tail->hi[t], n + 1);
+        }
+    }
+  } else if (threadIdx.x < 2) {
+    tail->hi[threadIdx.x] = threadIdx.x == 0 ? most[0] : most[1];
+  }
+  __syncthreads();
+  int lo[2], hi[2];
+  for (int t = 0; t < 2; ++t) {
+    hi[t] = max(tail->hi[t], 0);
+    lo[t] = min(tail->lo[t], hi[t]);
+  }
+  // the tiles either passes over
+  const int begin = hi[0] == lo[0] ? lo[1] : hi[1] == lo[1] ? lo[0] : min(lo[0], lo[1]);
+  const int end = hi[0] == lo[0] ? hi[1] : hi[1] == lo[1] ? hi[0] : max(hi[0], hi[1]);
+
+  if (warp >= 8) {
+    set_max_regs_down<kIssueRegs>();
+    if (warp == 8) {
+      // ------------------------------------------------------ TMA
+      if (lane == 0 && begin < end) {
+        const uint32_t q_full = smem_u32(&tail->q_full);
+        mbar_expect_tx(q_full, 2 * L::kTileBytes);
+        for (int t = 0; t < 2; ++t)  // a second tile past the end reads as zeros
+          for (int c = 0; c < DH / 64; ++c)
+            tma_load_4d(smem_u32(smem) + t * L::kTileBytes + c * kTile * 128, &p.m.q, q_full, c * 64,
+                        row0 + t * kTile, h, b);
+        int issued = 0;
+        bool ok = true;
+        for (int n = begin; n < end && ok; ++n)
+          for (int kv = 0; kv < 2; ++kv, ++issued) {
+            const int s = issued % L::kSlots, use = issued / L::kSlots;
+            if (use > 0 &&
+                !mbar_wait(smem_u32(&tail->empty[s]), (use - 1) & 1, abort_flag, a.dev_status)) {
+              ok = false;
+              break;
+            }
+            const uint32_t bar = smem_u32(&tail->full[s]);
+            mbar_expect_tx(bar, L::kTileBytes);
+            for (int c = 0; c < DH / 64; ++c)
+              tma_load_4d(smem_u32(smem) + (2 + s) * L::kTileBytes + c * kTile * 128,
+                          kv ? &p.m.v : &p.m.k, bar, c * 64, n * kTile, g, b);
+          }
+        // copies in flight land before the CTA leaves (in the ordinary course
+        // the MMA warp has consumed them all; after an abort it has not)
+        mbar_wait_drain(q_full, 0);
+        for (int s = 0; s < L::kSlots && s < issued; ++s) {
+          const int uses = (issued - 1 - s) / L::kSlots + 1;
+          mbar_wait_drain(smem_u32(&tail->full[s]), (uses - 1) & 1);
+        }
+      }
+    } else if (warp == 9) {
+      // ------------------------------------------------------ MMA
+      if (begin < end) {
+        const uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
+        const uint32_t idesc_o = idesc_bf16(kTile, DH, false, true);
+        const uint32_t q_tile = smem_u32(smem), ring = q_tile + 2 * L::kTileBytes;
+        int turn[2] = {0, 0};  // score tiles done of each query tile
+        auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
+          return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
+        };
+        auto wait_tile = [&](int i) {  // i-th tile of the ring
+          return wait(tail->full[i % L::kSlots], i / L::kSlots);
+        };
+        bool ok = wait(tail->q_full, 0);
+        auto scores = [&](int t, int i) {
+          if (lane == 0) {
+            const uint32_t kt = ring + (i % L::kSlots) * L::kTileBytes;
+#pragma unroll
+            for (int kk = 0; kk < DH / 16; ++kk)
+              tc_mma_bf16(tmem + t * kTile, desc_head(q_tile + t * L::kTileBytes, kk),
+                          desc_head(kt, kk), idesc_s, kk > 0);
+            tc_commit(smem_u32(&tail->s_full[t]));
+          }
+        };
+        if (ok) ok = wait_tile(0);
+        tc_fence_after();
+        if (ok) {
+          for (int t = 0; t < 2; ++t)
+            if (begin >= lo[t] && begin < hi[t]) scores(t, 0);
+          if (lane == 0) tc_commit(smem_u32(&tail->empty[0]));
+        }
+        for (int n = begin; n < end && ok; ++n) {
+          const int iv = 2 * (n - begin) + 1, ik = iv + 1;
+          if (!(ok = wait_tile(iv))) break;
+          if (a.q_docs != nullptr && doc_range(a.k_ranges, int64_t(b) * ktiles + n).padded)
+            zero_padding_rows<DH>(smem + (2 + iv % L::kSlots) * L::kTileBytes,
+                                  a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile);
+          bool have_k = false;
+          for (int t = 0; t < 2 && ok; ++t) {
+            if (n >= lo[t] && n < hi[t]) {
+              if (!(ok = wait(tail->p_full[t], turn[t]))) break;
+              tc_fence_after();
+              if (lane == 0) {
+                const uint32_t vt = ring + (iv % L::kSlots) * L::kTileBytes;
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                  tc_mma_bf16_ts(tmem + 256 + t * kTile, tmem + t * kTile + kk * 8,
+                                 desc_token(vt, kk), idesc_o, turn[t] > 0 || kk > 0);
+                tc_commit(smem_u32(&tail->o_done[t]));
+              }
+              ++turn[t];
+            }
+            if (n + 1 >= lo[t] && n + 1 < hi[t]) {
+              if (!have_k) {
+                if (!(ok = wait_tile(ik))) break;
+                tc_fence_after();
+                have_k = true;
+              }
+              scores(t, ik);
+            }
+          }
+          // a slot is given back only once its copy has landed
+          if (ok && n + 1 < end && !have_k) ok = wait_tile(ik);
+          if (ok && lane == 0) {
+            tc_commit(smem_u32(&tail->empty[iv % L::kSlots]));
+            if (n + 1 < end) tc_commit(smem_u32(&tail->empty[ik % L::kSlots]));
+          }
+          __syncwarp();
+        }
+        if (lane == 0) {  // nothing of this CTA is in flight when it leaves
+          tc_commit(smem_u32(&tail->drain));
+          mbar_wait_drain(smem_u32(&tail->drain), 0);
+        }
+        __syncwarp();
+      }
+    }
+  } else {
+    set_max_regs_up<kSoftmaxRegs>();
+    // ------------------------------------------------------ softmax
+    const int t = warp / 4;
+    const int row = row0 + t * kTile + (threadIdx.x & 127);
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t s_addr = tmem + lanes + t * kTile, o_addr = tmem + lanes + 256 + t * kTile;
+    const ScoreConst sc = score_const(a, h);
+    const int pos = row + off;
+    const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
+    const int first_last = last_key(a, row0 + t * kTile + off, prefix);  // of the tile's first row
+    DocRange qr = {0, 0, 0, 0};
+    int qd = 0;
+    if (a.q_docs != nullptr && row0 + t * kTile < a.Sq) {
+      qr = doc_range(a.q_ranges, int64_t(b) * qtiles + 2 * qb + t);
+      qd = row < a.Sq ? a.q_docs[b * a.qds + row] : -1;
+    }
+    float m = -INFINITY;  // the maximum that P is relative to, in log2 units
+    float2 l2 = make_float2(0.f, 0.f);
+    bool ok = true;
+    int turn = 0;
+    for (int n = lo[t]; n < hi[t]; ++n, ++turn) {
+      // does the mask leave the whole tile?
+      bool whole = n * kTile + kTile - 1 <= first_last;
+      if (a.q_docs != nullptr)
+        whole = whole && docs_equal(qr, doc_range(a.k_ranges, int64_t(b) * ktiles + n));
+      ok = mbar_wait(smem_u32(&tail->s_full[t]), turn & 1, abort_flag, a.dev_status);
+      if (!__all_sync(~0u, ok)) {
+        ok = false;
+        break;
+      }
+      tc_fence_after();
+      float s[kTile];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s + c * 32);
+      tmem_wait_ld();
+      pin<kTile>(s);
+      if constexpr (CAP || BIAS) {
+        const float d0 = static_cast<float>(pos - n * kTile);
+        float r;
+#pragma unroll
+        for (int j = 0; j < kTile; ++j) s[j] = score2<CAP, BIAS>(sc, s[j], d0 - j, r);
+      }
+      if (!whole) {
+        const int lim = last - n * kTile;
+        if (a.q_docs == nullptr) {
+#pragma unroll
+          for (int j = 0; j < kTile; ++j)
+            if (j > lim) s[j] = -INFINITY;
+        } else {
+          const int *kd = a.k_docs + b * a.kds + n * kTile;
+          const int have = a.Sk - n * kTile;
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) {
+            const int d = j < have ? __ldg(kd + j) : -1;
+            if (j > lim || d != qd || d < 0) s[j] = -INFINITY;
+          }
+        }
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int j = 4; j < kTile; j += 4)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[j + i]);
+      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      if constexpr (!CAP && !BIAS) top *= sc.scale2;
+      float by = 1.f;
+      if (m == -INFINITY) {
+        m = top;  // nothing summed so far: O's row is zero or not begun
+      } else if (top > m + kRescaleAt) {
+        by = ex2(m - top);
+        m = top;
+      }
+      if (__any_sync(~0u, by != 1.f)) {
+        // P V of the tile before has to be in O
+        ok = mbar_wait(smem_u32(&tail->o_done[t]), (turn - 1) & 1, abort_flag, a.dev_status);
+        if (!__all_sync(~0u, ok)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        l2.x *= by;
+        l2.y *= by;
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 32) {
+          float o[32];
+          tmem_ld32(o_addr + c, o);
+          tmem_wait_ld();
+          pin<32>(o);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] *= by;
+          tmem_st32(o_addr + c, o);
+        }
+      }
+      const float sub = m == -INFINITY ? 0.f : -m;
+      const float2 sub2 = make_float2(sub, sub);
+      const float2 sl2 = make_float2(sc.scale2, sc.scale2);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 x = make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]);
+          if constexpr (CAP || BIAS)
+            x = add2(x, sub2);
+          else
+            x = fma2(x, sl2, sub2);
+          x.x = ex2(x.x);
+          x.y = ex2(x.y);
+          l2 = add2(l2, x);
+          w[i] = pack_bf16(x.x, x.y);
+        }
+        tmem_st16(s_addr + c * 16, w);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      mbar_arrive(smem_u32(&tail->p_full[t]));
+    }
+    if (row0 + t * kTile < a.Sq) {
+      if (ok && turn > 0) {
+        ok = mbar_wait(smem_u32(&tail->o_done[t]), (turn - 1) & 1, abort_flag, a.dev_status);
+        ok = __all_sync(~0u, ok);
+      } else if (ok && begin < end) {  // Q's copy has landed before its memory is reused
+        ok = mbar_wait(smem_u32(&tail->q_full), 0, abort_flag, a.dev_status);
+        ok = __all_sync(~0u, ok);
+      }
+      const float l = l2.x + l2.y;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      if (ok) {
+        // O through this tile's part of Q's shared memory: every product that
+        // reads it is done
+        tc_fence_after();
+        uint8_t *stage = smem + t * L::kTileBytes;
+        const int r = threadIdx.x & 127;
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 32) {
+          float o[32];
+          if (turn > 0) {
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+            pin<32>(o);
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = l > 0.f ? pack_bf16(o[i * 8 + 2 * e] * inv, o[i * 8 + 2 * e + 1] * inv) : 0u;
+            const int seg = (c % 64) / 8 + i;
+            *reinterpret_cast<uint4 *>(stage + (c / 64) * kTile * 128 + r * 128 +
+                                       ((seg ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (a.lse != nullptr && row < a.Sq)
+          a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row] =
+              l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        fence_proxy_async_smem();
+      }
+      // stored only if every warp of the tile has its rows staged
+      const bool failed = named_bar_red_or(1 + t, kTile, !ok);
+      if (!failed) {
+        uint8_t *stage = smem + t * L::kTileBytes;
+        if ((threadIdx.x & 127) == 0) {
+          for (int c = 0; c < DH / 64; ++c)
+            if (c * 64 < a.D)
+              tma_store_4d(&p.m.o, smem_u32(stage) + c * kTile * 128, c * 64, row0 + t * kTile, h, b);
+          bulk_commit_group();
+          bulk_wait_group0();
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Ranges of the documents of 128-token tiles, one warp per tile.
+__global__ void k_attn_ranges(const int *docs, int64_t stride, int B, int S, int4 *out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int tiles = (S + kTile - 1) / kTile;
+  const int w = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
+  if (w >= B * tiles) return;
+  const int b = w / tiles, n = w % tiles;
+  int lo = INT_MAX, hi = -1, padded = 0;
+  for (int i = lane; i < kTile; i += 32) {
+    const int at = n * kTile + i;
+    if (at >= S) break;
+    const int d = docs[b * stride + at];
+    if (d < 0) {
+      padded = 1;
+    } else {
+      lo = min(lo, d);
+      hi = max(hi, d);
+    }
+  }
+  lo = __reduce_min_sync(~0u, lo);
+  hi = __reduce_max_sync(~0u, hi);
+  padded = __any_sync(~0u, padded);
+  if (lane == 0) out[w] = make_int4(lo, hi, padded, 0);
+}
+
+template <int DH, bool CAP, bool BIAS>
+cudaError_t launch(const Params &p, cudaStream_t s) {
+  const size_t smem = Layout<DH>::kBytes + sizeof(Tail) + 1024;
+  auto *kernel = k_attn_fwd<DH, CAP, BIAS>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t grid = int64_t(p.a.B) * p.a.Hq * ((p.a.Sq + 2 * kTile - 1) / (2 * kTile));
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s) {
+  for (int side = 0; side < 2; ++side) {
+    const int S = side ? a.Sk : a.Sq;
+    const int64_t tiles = int64_t(a.B) * ((S + kTile - 1) / kTile);
+    if (tiles == 0) continue;
+    const cudaError_t e = launch_pdl(
+        k_attn_ranges, dim3(static_cast<unsigned>((tiles + 7) / 8)), dim3(256), 0, s,
+        side ? a.k_docs : a.q_docs, side ? a.kds : a.qds, a.B, S,
+        const_cast<int4 *>(side ? a.k_ranges : a.q_ranges));
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, cudaStream_t s) {
+  const Params p{a, m};
+  const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
+  if (a.D <= 64)
+    return cap ? (bias ? launch<64, true, true>(p, s) : launch<64, true, false>(p, s))
+               : (bias ? launch<64, false, true>(p, s) : launch<64, false, false>(p, s));
+  return cap ? (bias ? launch<128, true, true>(p, s) : launch<128, true, false>(p, s))
+             : (bias ? launch<128, false, true>(p, s) : launch<128, false, false>(p, s));
+}
+
+}  // namespace lora

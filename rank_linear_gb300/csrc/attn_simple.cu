@@ -1,4 +1,5 @@
-// attn_simple.cu -- attention with one warp per row, on CUDA cores.
+// attn_simple.cu -- attention gradients and the one-token form with one warp per
+// row, on CUDA cores.
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -149,9 +150,6 @@ dim3 blocks(int64_t rows) { return dim3(static_cast<unsigned>((rows + kWarps - 1
 
 }  // namespace
 
-cudaError_t launch_attn_fwd(const AttnArgs &a, cudaStream_t s) {
-  return launch_pdl(k_attn_fwd_simple<false>, blocks(int64_t(a.B) * a.Hq * a.Sq), dim3(32 * kWarps), 0, s, a);
-}
 cudaError_t launch_attn_token(const AttnArgs &a, cudaStream_t s) {
   return launch_pdl(k_attn_fwd_simple<true>, blocks(int64_t(a.B) * a.Hq * a.Sq), dim3(32 * kWarps), 0, s, a);
 }

@@ -132,7 +132,7 @@ def backward(ptr=None, **kw):
 SHAPES = [
     (dict(batch=-1), BAD), (dict(q_len=-1), BAD), (dict(q_heads=3), BAD), (dict(k_heads=0), BAD),
     (dict(dim=0), BAD), (dict(dim=60), UNSUP), (dict(dim=136), UNSUP), (dict(causal=2), BAD),
-    (dict(scale=math.inf), BAD), (dict(softcap=-1.0), BAD), (dict(softcap=math.nan), BAD),
+    (dict(scale=math.inf), BAD), (dict(scale=0.0), BAD), (dict(scale=-1.0), BAD), (dict(softcap=-1.0), BAD), (dict(softcap=math.nan), BAD),
     (dict(q_docs=FAKE), BAD), (dict(causal=0, prefix=FAKE), BAD), (dict(slopes=FAKE + 2), BAD),
     (dict(k_len=1 << 24), UNSUP), (dict(q=(0, 4 * 64 + 4, 64)), UNSUP),
     (dict(v=(0, -128, 64)), UNSUP),
