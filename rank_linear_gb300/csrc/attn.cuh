@@ -151,7 +151,7 @@ struct DocRange {
   int lo, hi, padded, unused;
 };
 __device__ __forceinline__ DocRange doc_range(const int4 *ranges, int64_t i) {
-  const int4 r = __ldg(ranges + i);
+  const int4 r = __ldcg(ranges + i);
   return {r.x, r.y, r.z, r.w};
 }
 __device__ __forceinline__ bool docs_meet(const DocRange &a, const DocRange &b) {
@@ -213,6 +213,21 @@ __device__ __forceinline__ void zero_padding_rows(uint8_t *tile, const int *docs
               make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
   __syncwarp();
+}
+
+// Writes 32 columns from c on (times by, as bf16) of row r of a [128][DH] tile
+// in shared memory, in the layout of the maps' copies.
+__device__ __forceinline__ void stage_row32(uint8_t *tile, int r, int c, const float *v, float by) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      w[e] = pack_bf16(v[i * 8 + 2 * e] * by, v[i * 8 + 2 * e + 1] * by);
+    const int seg = (c % 64) / 8 + i;
+    *reinterpret_cast<uint4 *>(tile + (c / 64) * kTile * 128 + r * 128 + ((seg ^ (r & 7)) << 4)) =
+        make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // Operand descriptors of a [128][DH] tile as TMA leaves it (128-byte swizzle,

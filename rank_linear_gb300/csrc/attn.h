@@ -30,11 +30,14 @@ struct AttnArgs {
 struct AttnMaps {
   CUtensorMap q, k, v, o;
 };
+struct AttnBwdMaps {
+  CUtensorMap q, k, v, d_o, dq, dk, dv;
+};
 
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, cudaStream_t s);
-cudaError_t launch_attn_dq(const AttnArgs &a, cudaStream_t s);
-cudaError_t launch_attn_dkv(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
+cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
 cudaError_t launch_attn_token(const AttnArgs &a, cudaStream_t s);
 
 }  // namespace lora

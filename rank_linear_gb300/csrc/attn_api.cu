@@ -90,7 +90,7 @@ AttnArgs make_args(const lora_attention_t *p, const DevInfo &di) {
 int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
 
 // Map of a [batch][token][head][dim] tensor (see AttnMaps).  An empty tensor
-// gets a map over one element row that no copy reads.
+// gets a map over another's first row, which no copy reads.
 lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], const AttnArgs &a,
                          int len, int heads, const char *what) {
   auto fn = encode_fn();
@@ -183,12 +183,8 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   AttnMaps m;
   LORA_TRY(tensor_map(&m.q, q, shape->q, a, a.Sq, a.Hq, "q"));
   LORA_TRY(tensor_map(&m.o, o, shape->o, a, a.Sq, a.Hq, "o"));
-  if (no_k) {
-    m.k = m.v = m.q;
-  } else {
-    LORA_TRY(tensor_map(&m.k, k, shape->k, a, a.Sk, a.Hk, "k"));
-    LORA_TRY(tensor_map(&m.v, v, shape->v, a, a.Sk, a.Hk, "v"));
-  }
+  LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
+  LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
   LORA_TRY(make_ranges(a, w, workspace, st));
   return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, m, st); });
 }
@@ -228,9 +224,20 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
   a.dv = dv;
   a.delta = reinterpret_cast<float *>(at(workspace, w.delta));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!no_q) LORA_TRY(run(LORA_K_ATTN_DQ, st, "attention dq", [&] { return launch_attn_dq(a, st); }));
+  AttnBwdMaps m;
+  LORA_TRY(tensor_map(&m.q, no_q ? k : q, shape->q, a, a.Sq, a.Hq, "q"));
+  LORA_TRY(tensor_map(&m.d_o, no_q ? k : d_o, shape->d_o, a, a.Sq, a.Hq, "do"));
+  LORA_TRY(tensor_map(&m.dq, no_q ? k : dq, shape->dq, a, a.Sq, a.Hq, "dq"));
+  LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
+  LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
+  LORA_TRY(tensor_map(&m.dk, no_k ? q : dk, shape->dk, a, a.Sk, a.Hk, "dk"));
+  LORA_TRY(tensor_map(&m.dv, no_k ? q : dv, shape->dv, a, a.Sk, a.Hk, "dv"));
+  LORA_TRY(make_ranges(a, w, workspace, st));
+  if (!no_q)
+    LORA_TRY(run(LORA_K_ATTN_DQ, st, "attention dq", [&] { return launch_attn_dq(a, m, st); }));
   if (!no_k)
-    LORA_TRY(run(LORA_K_ATTN_DKV, st, "attention dk and dv", [&] { return launch_attn_dkv(a, st); }));
+    LORA_TRY(run(LORA_K_ATTN_DKV, st, "attention dk and dv",
+                 [&] { return launch_attn_dkv(a, m, st); }));
   return LORA_OK;
 }
 

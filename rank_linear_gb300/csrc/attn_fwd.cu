@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           const int have = a.Sk - n * kTile;
 #pragma unroll
           for (int j = 0; j < kTile; ++j) {
-            const int d = j < have ? __ldg(kd + j) : -1;
+            const int d = j < have ? kd[j] : -1;
             if (j > lim || d != qd || d < 0) s[j] = -INFINITY;
           }
         }
@@ -368,7 +368,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         // reads it is done
         tc_fence_after();
         uint8_t *stage = smem + t * L::kTileBytes;
-        const int r = threadIdx.x & 127;
 #pragma unroll 1
         for (int c = 0; c < DH; c += 32) {
           float o[32];
@@ -377,16 +376,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             tmem_wait_ld();
             pin<32>(o);
           }
+          if (!(l > 0.f))
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              w[e] = l > 0.f ? pack_bf16(o[i * 8 + 2 * e] * inv, o[i * 8 + 2 * e + 1] * inv) : 0u;
-            const int seg = (c % 64) / 8 + i;
-            *reinterpret_cast<uint4 *>(stage + (c / 64) * kTile * 128 + r * 128 +
-                                       ((seg ^ (r & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
+            for (int i = 0; i < 32; ++i) o[i] = 0.f;
+          stage_row32(stage, threadIdx.x & 127, c, o, inv);
         }
         if (a.lse != nullptr && row < a.Sq)
           a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row] =

@@ -40,8 +40,8 @@ static_assert(sizeof(PlanHead) % 32 == 0 || sizeof(PlanHead) % 16 == 0, "chunks 
 
 __device__ __forceinline__ Chunk load_chunk(const Chunk *p) {
   Chunk c;
-  const int4 a = __ldg(reinterpret_cast<const int4 *>(p));
-  const int4 b = __ldg(reinterpret_cast<const int4 *>(p) + 1);
+  const int4 a = __ldcg(reinterpret_cast<const int4 *>(p));
+  const int4 b = __ldcg(reinterpret_cast<const int4 *>(p) + 1);
   reinterpret_cast<int4 *>(&c)[0] = a;
   reinterpret_cast<int4 *>(&c)[1] = b;
   return c;
@@ -89,7 +89,7 @@ __device__ void add_chunk(const Chunk &c, double &acc) {
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     const int i = tid + u * kThreads;
-    v[u] = i < vecs ? __ldg(body + i) : make_uint4(0, 0, 0, 0);
+    v[u] = i < vecs ? __ldcg(body + i) : make_uint4(0, 0, 0, 0);
   }
   // the elements outside whole vectors: fewer than 2 N of them
   const int rest = c.count - vecs * N;
@@ -143,7 +143,7 @@ __device__ void add_chunk(const Chunk &c, double &acc) {
           const int i = tid + u * kThreads;
           if (i >= vecs) break;
           float f[N];
-          unpack<BF>(__ldg(body + i), f);
+          unpack<BF>(__ldcg(body + i), f);
 #pragma unroll
           for (int e = 0; e < N; ++e) d += static_cast<double>(f[e]) * f[e];
         }
@@ -245,7 +245,7 @@ __device__ __forceinline__ void scale_chunk(const Chunk &c, float f) {
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     const int i = tid + u * kThreads;
-    if (i < vecs) v[u] = src[i];
+    if (i < vecs) v[u] = __ldcg(src + i);
   }
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
