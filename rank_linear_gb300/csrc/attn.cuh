@@ -16,15 +16,52 @@ constexpr int kTile = 128;  // rows of a query tile, and of a key tile
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 // ---------------------------------------------------------------- PTX forms
-// D(tmem) (+)= A(tmem) * B(smem)^T: A is bf16, lane = row, two K elements per
-// 32-bit column (16 K elements: 8 columns).  Issued by one thread.
-__device__ __forceinline__ void tc_mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                               uint32_t idesc, uint32_t accumulate) {
+// The MMAs of a tile are issued by a whole warp with all but one lane
+// predicated off: no divergent branch, so that descriptors stay in uniform
+// registers.  (Under `if (lane == 0)` each issue took about 100 cycles, longer
+// than the 64 of the MMA itself.)
+//
+// 1 in one lane of the warp.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t e;
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.b32 %0, 1, 0, p;\n\t}"
+      : "=r"(e));
+  return e;
+}
+// A value that all lanes hold, as one the compiler knows to be uniform.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(~0u, x, 0); }
+// D(tmem) (+)= A(smem) * B(smem)^T.
+__device__ __forceinline__ void mma_ss(uint32_t on, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+// D(tmem) (+)= A(tmem) * B(smem)^T: A is bf16, lane = row, two K elements per
+// 32-bit column (16 K elements: 8 columns).
+__device__ __forceinline__ void mma_ts(uint32_t on, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                       uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(on)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t on, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(on)
       : "memory");
 }
 __device__ __forceinline__ void tmem_wait_ld() {
@@ -111,6 +148,11 @@ __device__ __forceinline__ float ex2(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+  return m;
+}
 __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -159,6 +201,39 @@ __device__ __forceinline__ bool docs_meet(const DocRange &a, const DocRange &b) 
 }
 __device__ __forceinline__ bool docs_equal(const DocRange &a, const DocRange &b) {
   return a.lo == a.hi && b.lo == a.lo && b.hi == a.lo && !a.padded && !b.padded;
+}
+
+// Bits 0..n of a word (none for n < 0, all for n >= 31).
+__device__ __forceinline__ uint32_t bits_to(int n) {
+  return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1u;
+}
+// For each lane's own document, which of 32 W tokens share it: bit i of word c
+// is token 32 c + i, whose document lane i holds in theirs[c] (below zero:
+// padding).  A turn for every distinct document among the lanes.
+template <int W>
+__device__ __forceinline__ void same_doc(int own, const int (&theirs)[W], uint32_t (&keep)[W]) {
+  uint32_t todo = __ballot_sync(~0u, own >= 0);
+#pragma unroll
+  for (int c = 0; c < W; ++c) keep[c] = 0u;
+  while (todo != 0u) {
+    const int doc = __shfl_sync(~0u, own, __ffs(todo) - 1);
+    const bool mine = own == doc;
+#pragma unroll
+    for (int c = 0; c < W; ++c) {
+      const uint32_t b = __ballot_sync(~0u, theirs[c] == doc);
+      if (mine) keep[c] = b;
+    }
+    todo &= ~__ballot_sync(~0u, mine);
+  }
+}
+// Documents of 32 W tokens from docs on, `have` of them there.
+template <int W>
+__device__ __forceinline__ void load_docs(const int *docs, int have, int (&out)[W]) {
+#pragma unroll
+  for (int c = 0; c < W; ++c) {
+    const int i = 32 * c + static_cast<int>(threadIdx.x % 32);
+    out[c] = i < have ? docs[i] : -1;
+  }
 }
 
 // What a query of position p (its row's index + Sk - Sq) sees without
@@ -231,13 +306,36 @@ __device__ __forceinline__ void stage_row32(uint8_t *tile, int r, int c, const f
 }
 
 // Operand descriptors of a [128][DH] tile as TMA leaves it (128-byte swizzle,
-// boxes of 64 columns): K step kk of 16 along the head (K-major), or of 16
-// tokens (MN-major).
-__device__ __forceinline__ uint64_t desc_head(uint32_t tile, int kk) {
-  return sdesc_sw128(tile + (kk >> 2) * (kTile * 128) + (kk & 3) * 32, 16, 1024);
+// boxes of 64 columns): with the head as K (K-major), or the tokens
+// (MN-major); and what K step kk of 16 adds to each.
+__device__ __forceinline__ uint64_t desc_head(uint32_t tile) { return sdesc_sw128(tile, 16, 1024); }
+__device__ __forceinline__ constexpr uint64_t head_step(int kk) {
+  return ((kk >> 2) * (kTile * 128) + (kk & 3) * 32) >> 4;
 }
-__device__ __forceinline__ uint64_t desc_token(uint32_t tile, int kk) {
-  return sdesc_sw128(tile + kk * 2048, kTile * 128, 1024);
+__device__ __forceinline__ uint64_t desc_token(uint32_t tile) {
+  return sdesc_sw128(tile, kTile * 128, 1024);
+}
+__device__ __forceinline__ constexpr uint64_t token_step(int kk) { return (kk * 2048) >> 4; }
+
+// D = X Y^T over the head, X and Y [128][DH] tiles.
+template <int DH>
+__device__ __forceinline__ void mma_over_head(uint32_t on, uint32_t d_tmem, uint32_t x, uint32_t y) {
+  const uint64_t xd = desc_head(x), yd = desc_head(y);
+#pragma unroll
+  for (int kk = 0; kk < DH / 16; ++kk)
+    mma_ss(on, d_tmem, xd + head_step(kk), yd + head_step(kk),
+           idesc_bf16(kTile, kTile, false, false), kk > 0);
+}
+// D (+)= W Y over the tokens of K steps [FROM, TO) of a tile, W the TMEM
+// operand whose K step kk is at column cols(kk), Y a [128][DH] tile.
+template <int DH, int FROM, int TO, class F>
+__device__ __forceinline__ void mma_over_tokens(uint32_t on, uint32_t d_tmem, uint32_t w_tmem, F cols,
+                                                uint32_t y, bool accumulate) {
+  const uint64_t yd = desc_token(y);
+#pragma unroll
+  for (int kk = FROM; kk < TO; ++kk)
+    mma_ts(on, d_tmem, w_tmem + cols(kk), yd + token_step(kk), idesc_bf16(kTile, DH, false, true),
+           accumulate || kk > FROM);
 }
 
 }  // namespace lora

@@ -26,7 +26,7 @@ struct Params {
 // The columns of a 128-wide TMEM region that hold K step kk of a bf16 operand:
 // the warpgroup of columns 0..63 writes columns 0..31, the other 64..95, each
 // over scores that it alone reads.
-__device__ __forceinline__ uint32_t operand_cols(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
+__device__ __forceinline__ constexpr uint32_t operand_cols(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
 
 // P (to p) and P dc/dz (in s) of 64 raw products of one thread; distances
 // d0 + step * j; sub = -lse in log2 units (or one per column in sub_col).
@@ -81,8 +81,8 @@ struct DqLayout {
   static constexpr uint32_t kAsked = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
 };
 struct DqTail {
-  uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2];
-  uint64_t s_full[2], dp_full, dp_free, dz_full, done, drain;
+  uint64_t q_full, k_full[3], k_empty[3], v_full[2];
+  uint64_t s_full[2], dp_full[2], dp_free, dz_full, done, drain;
   uint32_t tmem;
   int abort_flag, lo, hi;
   float delta[2][kTile];
@@ -110,13 +110,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       mbar_init(smem_u32(&tail->k_full[s]), 1);
       mbar_init(smem_u32(&tail->k_empty[s]), 1);
     }
-    for (int s = 0; s < L::kVSlots; ++s) {
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&tail->v_full[s]), 1);
-      mbar_init(smem_u32(&tail->v_empty[s]), 1);
+      mbar_init(smem_u32(&tail->s_full[s]), 1);
+      mbar_init(smem_u32(&tail->dp_full[s]), 1);
     }
-    mbar_init(smem_u32(&tail->s_full[0]), 1);
-    mbar_init(smem_u32(&tail->s_full[1]), 1);
-    mbar_init(smem_u32(&tail->dp_full), 1);
     mbar_init(smem_u32(&tail->dp_free), kPairThreads);
     mbar_init(smem_u32(&tail->dz_full), kPairThreads);
     mbar_init(smem_u32(&tail->done), 1);
@@ -139,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tail->tmem;
+  const uint32_t tmem = uniform(tail->tmem);
 
   // ---- the key tiles that some row sees
   const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
@@ -157,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     tail->hi = most;
   }
   __syncthreads();
-  const int end = tail->hi, begin = min(tail->lo, end);
+  const int end = uniform(tail->hi), begin = uniform(min(tail->lo, end));
   const int count = end - begin;
 
   if (warp >= 8) {
@@ -183,7 +181,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
           mbar_expect_tx(smem_u32(&tail->k_full[ks]), L::kTileBytes);
           load(k_ring + ks * L::kTileBytes, &p.m.k, tail->k_full[ks], (begin + i) * kTile, g);
           ++nk;
-          if (i >= L::kVSlots && !mbar_wait(smem_u32(&tail->v_empty[vs]), (i / L::kVSlots - 1) & 1,
+          // dP of the tile before in this slot is done
+          if (i >= L::kVSlots && !mbar_wait(smem_u32(&tail->dp_full[vs]), (i / L::kVSlots - 1) & 1,
                                             abort_flag, a.dev_status))
             break;
           mbar_expect_tx(smem_u32(&tail->v_full[vs]), L::kTileBytes);
@@ -199,38 +198,35 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       }
     } else if (warp == 9 && count > 0) {
       // ------------------------------------------------------ MMA
-      const uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
-      const uint32_t idesc_q = idesc_bf16(kTile, DH, false, true);
+      const uint32_t on = elect_one();
       auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
         return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
       };
+      auto padded = [&](int i) {
+        return a.q_docs != nullptr && i < count &&
+               doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded;
+      };
       // K's tile i has landed, without the rows of padding
+      bool pads = padded(0);
       auto wait_k = [&](int i) {
         const int s = i % L::kKSlots;
         if (!wait(tail->k_full[s], i / L::kKSlots)) return false;
-        if (a.q_docs != nullptr && doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded)
+        const bool now = pads;
+        pads = padded(i + 1);
+        if (now)
           zero_padding_rows<DH>(smem + (2 + s) * L::kTileBytes,
                                 a.k_docs + b * a.kds + (begin + i) * kTile,
                                 a.Sk - (begin + i) * kTile);
         return true;
       };
-      auto product = [&](uint32_t d, uint32_t x, uint32_t y) {  // d = x y^T over the head
-#pragma unroll
-        for (int kk = 0; kk < DH / 16; ++kk)
-          tc_mma_bf16(d, desc_head(x, kk), desc_head(y, kk), idesc_s, kk > 0);
-      };
       auto scores = [&](int i) {
-        if (lane == 0) {
-          product(tmem + (i & 1) * kTile, q_tile, k_ring + (i % L::kKSlots) * L::kTileBytes);
-          tc_commit(smem_u32(&tail->s_full[i & 1]));
-        }
+        mma_over_head<DH>(on, tmem + (i & 1) * kTile, q_tile,
+                          k_ring + (i % L::kKSlots) * L::kTileBytes);
+        commit(on, smem_u32(&tail->s_full[i & 1]));
       };
       auto do_v = [&](int i) {
-        if (lane == 0) {
-          product(tmem + 256, do_tile, v_ring + (i % L::kVSlots) * L::kTileBytes);
-          tc_commit(smem_u32(&tail->dp_full));
-          tc_commit(smem_u32(&tail->v_empty[i % L::kVSlots]));
-        }
+        mma_over_head<DH>(on, tmem + 256, do_tile, v_ring + (i % L::kVSlots) * L::kTileBytes);
+        commit(on, smem_u32(&tail->dp_full[i % L::kVSlots]));
       };
       bool ok = wait(tail->q_full, 0) && wait_k(0);
       tc_fence_after();
@@ -252,21 +248,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         }
         if (!(ok = wait(tail->dz_full, i))) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t kt = k_ring + (i % L::kKSlots) * L::kTileBytes;
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_bf16_ts(tmem + 384, tmem + (i & 1) * kTile + operand_cols(kk),
-                           desc_token(kt, kk), idesc_q, i > 0 || kk > 0);
-          tc_commit(smem_u32(&tail->k_empty[i % L::kKSlots]));
-        }
+        mma_over_tokens<DH, 0, 8>(on, tmem + 384, tmem + (i & 1) * kTile, operand_cols,
+                            k_ring + (i % L::kKSlots) * L::kTileBytes, i > 0);
+        commit(on, smem_u32(&tail->k_empty[i % L::kKSlots]));
         __syncwarp();
       }
-      if (lane == 0) {
-        if (ok) tc_commit(smem_u32(&tail->done));
-        tc_commit(smem_u32(&tail->drain));
-        mbar_wait_drain(smem_u32(&tail->drain), 0);
-      }
+      if (ok) commit(on, smem_u32(&tail->done));
+      commit(on, smem_u32(&tail->drain));
+      mbar_wait_drain(smem_u32(&tail->drain), 0);
       __syncwarp();
     }
   } else {
@@ -307,11 +296,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     delta = tail->delta[0][r] + tail->delta[1][r];
     if (half == 0 && row < a.Sq) a.delta[stat] = delta;
     bool ok = true;
+    DocRange kr = {0, 0, 0, 0};
+    if (a.q_docs != nullptr && count > 0) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + begin);
     for (int i = 0; i < count; ++i) {
       const int n = begin + i, key0 = n * kTile + half * 64;
       bool whole = n * kTile + kTile - 1 <= first_last;
-      if (a.q_docs != nullptr)
-        whole = whole && docs_equal(qr, doc_range(a.k_ranges, int64_t(b) * ktiles + n));
+      int kd[2];
+      if (a.q_docs != nullptr) {
+        whole = whole && docs_equal(qr, kr);
+        if (!whole) load_docs(a.k_docs + b * a.kds + key0, a.Sk - key0, kd);
+        if (i + 1 < count) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
+      }
       const uint32_t s_addr = tmem + lanes + (i & 1) * kTile + half * 64;
       ok = mbar_wait(smem_u32(&tail->s_full[i & 1]), (i >> 1) & 1, abort_flag, a.dev_status);
       if (!(ok = __all_sync(~0u, ok))) break;
@@ -323,22 +318,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       pin<64>(w);
       weights<CAP, BIAS, false>(sc, w, nullptr, sub, nullptr, static_cast<float>(pos - key0), -1.f);
       if (!whole) {
-        const int lim = last - key0;
-        if (a.q_docs == nullptr) {
+        uint32_t keep[2] = {~0u, ~0u};
+        if (a.q_docs != nullptr) same_doc(qd, kd, keep);
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (j > lim) w[j] = 0.f;
-        } else {
-          const int *kd = a.k_docs + b * a.kds + key0;
-          const int have = a.Sk - key0;
+        for (int c = 0; c < 2; ++c) {
+          keep[c] &= bits_to(last - key0 - 32 * c);
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const int d = j < have ? kd[j] : -1;
-            if (j > lim || d != qd || d < 0) w[j] = 0.f;
-          }
+          for (int j = 0; j < 32; ++j)
+            if (!(keep[c] >> j & 1u)) w[c * 32 + j] = 0.f;
         }
       }
-      ok = mbar_wait(smem_u32(&tail->dp_full), i & 1, abort_flag, a.dev_status);
+      ok = mbar_wait(smem_u32(&tail->dp_full[i & 1]), (i >> 1) & 1, abort_flag, a.dev_status);
       if (!(ok = __all_sync(~0u, ok))) break;
       tc_fence_after();
       float dp[64];
@@ -414,14 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
 template <int DH>
 struct DkvLayout {
   static constexpr uint32_t kTileBytes = kTile * DH * 2;
-  static constexpr int kSlots = 2;
-  static constexpr uint32_t kBytes = (2 + 2 * kSlots) * kTileBytes;
+  // Q is asked for half a step before dO
+  static constexpr int kQSlots = 3, kESlots = 2;
+  // the tiles follow the tail (DkvTail), which for a head of 128 fills what
+  // they leave of an SM's 227 KB: no room to align a base that is not aligned
+  static constexpr uint32_t kTailBytes = 3072;
+  static constexpr uint32_t kBytes = kTailBytes + (2 + kQSlots + kESlots) * kTileBytes;
   static constexpr uint32_t kAsked = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
 };
 struct DkvTail {
   // per tile of queries: -lse in log2 units, and -delta
   float sub[2][kTile], neg_delta[2][kTile];
-  uint64_t k_full, q_full[2], q_empty[2], e_full[2], e_empty[2];
+  uint64_t k_full, q_full[3], e_full[2];
   uint64_t s_full, dp_full, p_full, dz_full, done, drain;
   uint32_t tmem;
   int abort_flag, lo, hi;
@@ -430,10 +424,15 @@ struct DkvTail {
 template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ Params p) {
   using L = DkvLayout<DH>;
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  DkvTail *tail = reinterpret_cast<DkvTail *>(smem + L::kBytes);
+  extern __shared__ __align__(1024) uint8_t raw_dkv[];
+  uint8_t *smem = raw_dkv + L::kTailBytes;
+  DkvTail *tail = reinterpret_cast<DkvTail *>(raw_dkv);
+  static_assert(sizeof(DkvTail) <= L::kTailBytes, "tail");
   const AttnArgs &a = p.a;
+  if ((smem_u32(raw_dkv) & 1023) != 0) {  // not met: the tiles' layout needs it
+    if (threadIdx.x == 0) atomicOr(a.dev_status, kDevErrTimeout);
+    return;
+  }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort_flag = &tail->abort_flag;
 
@@ -446,12 +445,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&tail->k_full), 1);
-    for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(smem_u32(&tail->q_full[s]), 1);
-      mbar_init(smem_u32(&tail->q_empty[s]), 1);
-      mbar_init(smem_u32(&tail->e_full[s]), 1);
-      mbar_init(smem_u32(&tail->e_empty[s]), 1);
-    }
+    for (int s = 0; s < L::kQSlots; ++s) mbar_init(smem_u32(&tail->q_full[s]), 1);
+    for (int s = 0; s < L::kESlots; ++s) mbar_init(smem_u32(&tail->e_full[s]), 1);
     mbar_init(smem_u32(&tail->s_full), 1);
     mbar_init(smem_u32(&tail->dp_full), 1);
     mbar_init(smem_u32(&tail->p_full), kPairThreads);
@@ -476,7 +471,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tail->tmem;
+  const uint32_t tmem = uniform(tail->tmem);
 
   // ---- the query tiles that see some key
   const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
@@ -494,14 +489,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     tail->hi = qtiles;
   }
   __syncthreads();
-  const int end = tail->hi, begin = min(tail->lo, end);
+  const int end = uniform(tail->hi), begin = uniform(min(tail->lo, end));
   const int per_head = end - begin, count = per_head * a.group;
   // step i: query head g * group + i / per_head, tile begin + i % per_head
 
   if (warp >= 8) {
     set_max_regs_down<kIssueRegs>();
     const uint32_t k_tile = smem_u32(smem), v_tile = k_tile + L::kTileBytes;
-    const uint32_t q_ring = v_tile + L::kTileBytes, e_ring = q_ring + L::kSlots * L::kTileBytes;
+    const uint32_t q_ring = v_tile + L::kTileBytes, e_ring = q_ring + L::kQSlots * L::kTileBytes;
     if (warp == 8) {
       // ------------------------------------------------------ TMA
       if (lane == 0 && count > 0) {
@@ -513,95 +508,107 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         load(k_tile, &p.m.k, tail->k_full, key0, g);
         load(v_tile, &p.m.v, tail->k_full, key0, g);
         int nq = 0, ne = 0;
-        for (int i = 0; i < count; ++i) {
-          const int s = i % L::kSlots, head = g * a.group + i / per_head;
-          const int token = (begin + i % per_head) * kTile, before = (i / L::kSlots - 1) & 1;
-          if (i >= L::kSlots &&
-              !mbar_wait(smem_u32(&tail->q_empty[s]), before, abort_flag, a.dev_status))
-            break;
+        auto load_q = [&](int i) {
+          const int s = i % L::kQSlots;
           mbar_expect_tx(smem_u32(&tail->q_full[s]), L::kTileBytes);
-          load(q_ring + s * L::kTileBytes, &p.m.q, tail->q_full[s], token, head);
+          load(q_ring + s * L::kTileBytes, &p.m.q, tail->q_full[s],
+               (begin + i % per_head) * kTile, g * a.group + i / per_head);
           ++nq;
-          if (i >= L::kSlots &&
-              !mbar_wait(smem_u32(&tail->e_empty[s]), before, abort_flag, a.dev_status))
+        };
+        load_q(0);
+        for (int i = 0; i < count; ++i) {
+          // dP of step i - 1 is done, hence everything of step i - 2: the slots
+          // of Q's tile i - 2 and dO's
+          // (every phase in turn: a wait for phase 1 would pass before phase 0)
+          if (i == L::kESlots && !mbar_wait(smem_u32(&tail->dp_full), 0, abort_flag, a.dev_status))
             break;
+          if (i >= L::kESlots &&
+              !mbar_wait(smem_u32(&tail->dp_full), (i - 1) & 1, abort_flag, a.dev_status))
+            break;
+          const int s = i % L::kESlots;
           mbar_expect_tx(smem_u32(&tail->e_full[s]), L::kTileBytes);
-          load(e_ring + s * L::kTileBytes, &p.m.d_o, tail->e_full[s], token, head);
+          load(e_ring + s * L::kTileBytes, &p.m.d_o, tail->e_full[s],
+               (begin + i % per_head) * kTile, g * a.group + i / per_head);
           ++ne;
+          if (i + 1 < count) load_q(i + 1);
         }
         // copies in flight land before the CTA leaves
         mbar_wait_drain(smem_u32(&tail->k_full), 0);
-        for (int s = 0; s < L::kSlots && s < nq; ++s)
-          mbar_wait_drain(smem_u32(&tail->q_full[s]), ((nq - 1 - s) / L::kSlots) & 1);
-        for (int s = 0; s < L::kSlots && s < ne; ++s)
-          mbar_wait_drain(smem_u32(&tail->e_full[s]), ((ne - 1 - s) / L::kSlots) & 1);
+        for (int s = 0; s < L::kQSlots && s < nq; ++s)
+          mbar_wait_drain(smem_u32(&tail->q_full[s]), ((nq - 1 - s) / L::kQSlots) & 1);
+        for (int s = 0; s < L::kESlots && s < ne; ++s)
+          mbar_wait_drain(smem_u32(&tail->e_full[s]), ((ne - 1 - s) / L::kESlots) & 1);
       }
     } else if (warp == 9 && count > 0) {
       // ------------------------------------------------------ MMA
-      const uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
-      const uint32_t idesc_d = idesc_bf16(kTile, DH, false, true);
+      const uint32_t on = elect_one();
       auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
         return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
       };
-      // tile i of a ring has landed, without the rows of padding
-      auto wait_tile = [&](const uint64_t (&full)[2], int i, int ring) {
-        const int s = i % L::kSlots, n = begin + i % per_head;
-        if (!wait(full[s], i / L::kSlots)) return false;
-        if (a.q_docs != nullptr && doc_range(a.q_ranges, int64_t(b) * qtiles + n).padded)
-          zero_padding_rows<DH>(smem + (2 + ring * L::kSlots + s) * L::kTileBytes,
-                                a.q_docs + b * a.qds + n * kTile, a.Sq - n * kTile);
+      auto padded = [&](int i) {
+        return a.q_docs != nullptr && i < count &&
+               doc_range(a.q_ranges, int64_t(b) * qtiles + begin + i % per_head).padded;
+      };
+      bool pads_q = padded(0), pads_e = pads_q;
+      // a tile of step i has landed; without the rows of padding
+      auto clear = [&](bool now, int tile, int i) {
+        const int token = (begin + i % per_head) * kTile;
+        if (now)
+          zero_padding_rows<DH>(smem + tile * L::kTileBytes, a.q_docs + b * a.qds + token,
+                                a.Sq - token);
+      };
+      auto wait_q = [&](int i) {
+        const int s = i % L::kQSlots;
+        if (!wait(tail->q_full[s], i / L::kQSlots)) return false;
+        clear(pads_q, 2 + s, i);
+        pads_q = padded(i + 1);
         return true;
       };
-      auto scores = [&](uint32_t d, uint32_t x, uint32_t ring, int i, uint64_t &bar) {
-        if (lane == 0) {  // d = x y^T over the head
-          const uint32_t y = ring + (i % L::kSlots) * L::kTileBytes;
-#pragma unroll
-          for (int kk = 0; kk < DH / 16; ++kk)
-            tc_mma_bf16(d, desc_head(x, kk), desc_head(y, kk), idesc_s, kk > 0);
-          tc_commit(smem_u32(&bar));
-        }
+      auto wait_e = [&](int i) {
+        const int s = i % L::kESlots;
+        if (!wait(tail->e_full[s], i / L::kESlots)) return false;
+        clear(pads_e, 2 + L::kQSlots + s, i);
+        pads_e = padded(i + 1);
+        return true;
       };
-      auto gather = [&](uint32_t d, uint32_t op, uint32_t ring, int i, uint64_t &empty) {
-        if (lane == 0) {  // d += (operand in TMEM) y over the queries
-          const uint32_t y = ring + (i % L::kSlots) * L::kTileBytes;
-#pragma unroll
-          for (int kk = 0; kk < kTile / 16; ++kk)
-            tc_mma_bf16_ts(d, op + operand_cols(kk), desc_token(y, kk), idesc_d, i > 0 || kk > 0);
-          tc_commit(smem_u32(&empty));
-        }
+      auto q_at = [&](int i) { return q_ring + (i % L::kQSlots) * L::kTileBytes; };
+      auto e_at = [&](int i) { return e_ring + (i % L::kESlots) * L::kTileBytes; };
+      auto scores = [&](int i) {
+        mma_over_head<DH>(on, tmem, k_tile, q_at(i));
+        commit(on, smem_u32(&tail->s_full));
       };
-      bool ok = wait(tail->k_full, 0) && wait_tile(tail->q_full, 0, 0);
+      auto do_v = [&](int i) {
+        mma_over_head<DH>(on, tmem + 128, v_tile, e_at(i));
+        commit(on, smem_u32(&tail->dp_full));
+      };
+      bool ok = wait(tail->k_full, 0) && wait_q(0);
       tc_fence_after();
-      if (ok) scores(tmem, k_tile, q_ring, 0, tail->s_full);
-      if (ok) ok = wait_tile(tail->e_full, 0, 1);
+      if (ok) scores(0);
+      if (ok) ok = wait_e(0);
       tc_fence_after();
-      if (ok) scores(tmem + 128, v_tile, e_ring, 0, tail->dp_full);
+      if (ok) do_v(0);
       for (int i = 0; i < count && ok; ++i) {
-        const int s = i % L::kSlots;
         if (!(ok = wait(tail->p_full, i))) break;
         tc_fence_after();
-        // dO's slot is free after this product: dP of the step is done
-        gather(tmem + 256, tmem, e_ring, i, tail->e_empty[s]);
+        mma_over_tokens<DH, 0, 8>(on, tmem + 256, tmem, operand_cols, e_at(i), i > 0);
         if (i + 1 < count) {  // over P^T, which the product before reads first
-          if (!(ok = wait_tile(tail->q_full, i + 1, 0))) break;
+          if (!(ok = wait_q(i + 1))) break;
           tc_fence_after();
-          scores(tmem, k_tile, q_ring, i + 1, tail->s_full);
+          scores(i + 1);
         }
         if (!(ok = wait(tail->dz_full, i))) break;
         tc_fence_after();
-        gather(tmem + 384, tmem + 128, q_ring, i, tail->q_empty[s]);
+        mma_over_tokens<DH, 0, 8>(on, tmem + 384, tmem + 128, operand_cols, q_at(i), i > 0);
         if (i + 1 < count) {
-          if (!(ok = wait_tile(tail->e_full, i + 1, 1))) break;
+          if (!(ok = wait_e(i + 1))) break;
           tc_fence_after();
-          scores(tmem + 128, v_tile, e_ring, i + 1, tail->dp_full);
+          do_v(i + 1);
         }
         __syncwarp();
       }
-      if (lane == 0) {
-        if (ok) tc_commit(smem_u32(&tail->done));
-        tc_commit(smem_u32(&tail->drain));
-        mbar_wait_drain(smem_u32(&tail->drain), 0);
-      }
+      if (ok) commit(on, smem_u32(&tail->done));
+      commit(on, smem_u32(&tail->drain));
+      mbar_wait_drain(smem_u32(&tail->drain), 0);
       __syncwarp();
     }
   } else {
@@ -611,9 +618,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lanes + half * 64, dp_addr = s_addr + 128;
     // the first query that sees this key, and the last of the tile's keys
-    const int from = a.causal && key >= prefix ? key - off : -(1 << 30);
+    const int from = a.causal && key >= prefix ? key - off : -(1 << 28);
     const int tile_last = key0 + kTile - 1;
-    const int all_from = a.causal && tile_last >= prefix ? tile_last - off : -(1 << 30);
+    const int all_from = a.causal && tile_last >= prefix ? tile_last - off : -(1 << 28);
     const int kd = a.q_docs != nullptr && key < a.Sk ? a.k_docs[b * a.kds + key] : -1;
     // one of the two statistics of a query, fetched a step ahead
     auto fetch = [&](int i) {
@@ -626,6 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     };
     auto put = [&](int i, float v) { (half == 0 ? tail->sub : tail->neg_delta)[i & 1][r] = v; };
     bool ok = true;
+    DocRange qr = {0, 0, 0, 0};
+    if (a.q_docs != nullptr && count > 0) qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin);
     if (count > 0) put(0, fetch(0));
     for (int i = 0; i < count; ++i) {
       const int head = g * a.group + i / per_head, n = begin + i % per_head;
@@ -634,8 +643,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       float ahead = 0.f;
       if (i + 1 < count) ahead = fetch(i + 1);
       bool whole = n * kTile >= all_from;
-      if (a.q_docs != nullptr)
-        whole = whole && docs_equal(kr, doc_range(a.q_ranges, int64_t(b) * qtiles + n));
+      int qd[2];
+      if (a.q_docs != nullptr) {
+        whole = whole && docs_equal(kr, qr);
+        if (!whole) load_docs(a.q_docs + b * a.qds + q0, a.Sq - q0, qd);
+        if (i + 1 < count)
+          qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin + (i + 1) % per_head);
+      }
       ok = ok && mbar_wait(smem_u32(&tail->s_full), i & 1, abort_flag, a.dev_status);
       // everyone's statistics of this step are written, those of the step
       // before are no longer read
@@ -649,19 +663,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       weights<CAP, BIAS, true>(sc, w, pr, 0.f, tail->sub[i & 1] + half * 64,
                                static_cast<float>(q0 + off - key), 1.f);
       if (!whole) {
-        const int lim = from - q0;
-        if (a.q_docs == nullptr) {
+        uint32_t keep[2] = {~0u, ~0u};
+        if (a.q_docs != nullptr) same_doc(kd, qd, keep);
 #pragma unroll
-          for (int j = 0; j < 64; ++j)
-            if (j < lim) w[j] = pr[j] = 0.f;
-        } else {
-          const int *qd = a.q_docs + b * a.qds + q0;
-          const int have = a.Sq - q0;
+        for (int c = 0; c < 2; ++c) {
+          keep[c] &= ~bits_to(from - 1 - q0 - 32 * c);
 #pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const int d = j < have ? qd[j] : -1;
-            if (j < lim || d != kd || d < 0) w[j] = pr[j] = 0.f;
-          }
+          for (int j = 0; j < 32; ++j)
+            if (!(keep[c] >> j & 1u)) w[c * 32 + j] = pr[c * 32 + j] = 0.f;
         }
       }
       {
@@ -765,7 +774,7 @@ cudaError_t start_dq(const Params &p, cudaStream_t s) {
 }
 template <int DH, bool CAP, bool BIAS>
 cudaError_t start_dkv(const Params &p, cudaStream_t s) {
-  return start(k_attn_dkv<DH, CAP, BIAS>, DkvLayout<DH>::kAsked + sizeof(DkvTail) + 1024,
+  return start(k_attn_dkv<DH, CAP, BIAS>, DkvLayout<DH>::kAsked,
                int64_t(p.a.B) * p.a.Hk * ((p.a.Sk + kTile - 1) / kTile), p, s);
 }
 

@@ -25,14 +25,15 @@ constexpr float kRescaleAt = 8.f;
 template <int DH>
 struct Layout {
   static constexpr uint32_t kTileBytes = kTile * DH * 2;
-  static constexpr int kSlots = DH == 64 ? 8 : 4;  // ring of K and V tiles
-  static constexpr uint32_t kBytes = (2 + kSlots) * kTileBytes;
+  // rings of K and V tiles; a V tile is asked for first and given back last
+  static constexpr int kKSlots = DH == 64 ? 4 : 2, kVSlots = kKSlots + 1;
+  static constexpr uint32_t kBytes = (2 + kKSlots + kVSlots) * kTileBytes;
 };
 
 struct Tail {
-  uint64_t q_full;
-  uint64_t full[8], empty[8];
-  uint64_t s_full[2], p_full[2], o_done[2], drain;
+  uint64_t q_full, k_full[4], v_full[5];
+  uint64_t passed[5];  // the products before step i, at i modulo kVSlots
+  uint64_t s_full[2], p_full[2][2], o_done[2], drain;
   uint32_t tmem;
   int abort_flag;
   int lo[2], hi[2];
@@ -62,13 +63,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&tail->q_full), 1);
-    for (int s = 0; s < L::kSlots; ++s) {
-      mbar_init(smem_u32(&tail->full[s]), 1);
-      mbar_init(smem_u32(&tail->empty[s]), 1);
+    for (int s = 0; s < L::kKSlots; ++s) mbar_init(smem_u32(&tail->k_full[s]), 1);
+    for (int s = 0; s < L::kVSlots; ++s) {
+      mbar_init(smem_u32(&tail->v_full[s]), 1);
+      mbar_init(smem_u32(&tail->passed[s]), 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(smem_u32(&tail->s_full[t]), 1);
-      mbar_init(smem_u32(&tail->p_full[t]), kTile);
+      mbar_init(smem_u32(&tail->p_full[t][0]), kTile);
+      mbar_init(smem_u32(&tail->p_full[t][1]), kTile);
       mbar_init(smem_u32(&tail->o_done[t]), 1);
     }
     mbar_init(smem_u32(&tail->drain), 1);
@@ -91,7 +94,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tail->tmem;
+  const uint32_t tmem = uniform(tail->tmem);
 
   // ---- the key tiles [lo, hi) that some row of each query tile sees
   const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
@@ -117,123 +120,124 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   __syncthreads();
   int lo[2], hi[2];
   for (int t = 0; t < 2; ++t) {
-    hi[t] = max(tail->hi[t], 0);
-    lo[t] = min(tail->lo[t], hi[t]);
+    hi[t] = uniform(max(tail->hi[t], 0));
+    lo[t] = uniform(min(tail->lo[t], hi[t]));
   }
   // the tiles either passes over
   const int begin = hi[0] == lo[0] ? lo[1] : hi[1] == lo[1] ? lo[0] : min(lo[0], lo[1]);
   const int end = hi[0] == lo[0] ? hi[1] : hi[1] == lo[1] ? hi[0] : max(hi[0], hi[1]);
 
+  // step i: P V of tile begin + i, and the scores of tile begin + i + 1
+  const int count = end - begin;
+
   if (warp >= 8) {
     set_max_regs_down<kIssueRegs>();
+    const uint32_t q_tile = smem_u32(smem), k_ring = q_tile + 2 * L::kTileBytes;
+    const uint32_t v_ring = k_ring + L::kKSlots * L::kTileBytes;
     if (warp == 8) {
       // ------------------------------------------------------ TMA
-      if (lane == 0 && begin < end) {
-        const uint32_t q_full = smem_u32(&tail->q_full);
-        mbar_expect_tx(q_full, 2 * L::kTileBytes);
-        for (int t = 0; t < 2; ++t)  // a second tile past the end reads as zeros
+      if (lane == 0 && count > 0) {
+        auto load = [&](uint32_t dst, const CUtensorMap *tm, uint64_t &bar, int token, int head) {
           for (int c = 0; c < DH / 64; ++c)
-            tma_load_4d(smem_u32(smem) + t * L::kTileBytes + c * kTile * 128, &p.m.q, q_full, c * 64,
-                        row0 + t * kTile, h, b);
-        int issued = 0;
-        bool ok = true;
-        for (int n = begin; n < end && ok; ++n)
-          for (int kv = 0; kv < 2; ++kv, ++issued) {
-            const int s = issued % L::kSlots, use = issued / L::kSlots;
-            if (use > 0 &&
-                !mbar_wait(smem_u32(&tail->empty[s]), (use - 1) & 1, abort_flag, a.dev_status)) {
-              ok = false;
-              break;
-            }
-            const uint32_t bar = smem_u32(&tail->full[s]);
-            mbar_expect_tx(bar, L::kTileBytes);
-            for (int c = 0; c < DH / 64; ++c)
-              tma_load_4d(smem_u32(smem) + (2 + s) * L::kTileBytes + c * kTile * 128,
-                          kv ? &p.m.v : &p.m.k, bar, c * 64, n * kTile, g, b);
-          }
-        // copies in flight land before the CTA leaves (in the ordinary course
-        // the MMA warp has consumed them all; after an abort it has not)
-        mbar_wait_drain(q_full, 0);
-        for (int s = 0; s < L::kSlots && s < issued; ++s) {
-          const int uses = (issued - 1 - s) / L::kSlots + 1;
-          mbar_wait_drain(smem_u32(&tail->full[s]), (uses - 1) & 1);
+            tma_load_4d(dst + c * kTile * 128, tm, smem_u32(&bar), c * 64, token, head, b);
+        };
+        auto load_k = [&](int i) {
+          const int s = i % L::kKSlots;
+          mbar_expect_tx(smem_u32(&tail->k_full[s]), L::kTileBytes);
+          load(k_ring + s * L::kTileBytes, &p.m.k, tail->k_full[s], (begin + i) * kTile, g);
+        };
+        mbar_expect_tx(smem_u32(&tail->q_full), 2 * L::kTileBytes);
+        for (int t = 0; t < 2; ++t)  // a second tile past the end reads as zeros
+          load(q_tile + t * L::kTileBytes, &p.m.q, tail->q_full, row0 + t * kTile, h);
+        load_k(0);
+        int nk = 1, nv = 0;
+        for (int i = 0; i < count; ++i) {
+          const int s = i % L::kVSlots;
+          mbar_expect_tx(smem_u32(&tail->v_full[s]), L::kTileBytes);
+          load(v_ring + s * L::kTileBytes, &p.m.v, tail->v_full[s], (begin + i) * kTile, g);
+          ++nv;
+          if (i + 1 == count) break;
+          // K's slot was scored before this step; so was V's next one
+          const int gone = i + 1 - L::kKSlots;
+          if (gone >= 0 && !mbar_wait(smem_u32(&tail->passed[gone % L::kVSlots]),
+                                      (gone / L::kVSlots) & 1, abort_flag, a.dev_status))
+            break;
+          load_k(i + 1);
+          ++nk;
         }
+        // copies in flight land before the CTA leaves
+        mbar_wait_drain(smem_u32(&tail->q_full), 0);
+        for (int s = 0; s < L::kKSlots && s < nk; ++s)
+          mbar_wait_drain(smem_u32(&tail->k_full[s]), ((nk - 1 - s) / L::kKSlots) & 1);
+        for (int s = 0; s < L::kVSlots && s < nv; ++s)
+          mbar_wait_drain(smem_u32(&tail->v_full[s]), ((nv - 1 - s) / L::kVSlots) & 1);
       }
-    } else if (warp == 9) {
+    } else if (warp == 9 && count > 0) {
       // ------------------------------------------------------ MMA
-      if (begin < end) {
-        const uint32_t idesc_s = idesc_bf16(kTile, kTile, false, false);
-        const uint32_t idesc_o = idesc_bf16(kTile, DH, false, true);
-        const uint32_t q_tile = smem_u32(smem), ring = q_tile + 2 * L::kTileBytes;
-        int turn[2] = {0, 0};  // score tiles done of each query tile
-        auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
-          return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
-        };
-        auto wait_tile = [&](int i) {  // i-th tile of the ring
-          return wait(tail->full[i % L::kSlots], i / L::kSlots);
-        };
-        bool ok = wait(tail->q_full, 0);
-        auto scores = [&](int t, int i) {
-          if (lane == 0) {
-            const uint32_t kt = ring + (i % L::kSlots) * L::kTileBytes;
-#pragma unroll
-            for (int kk = 0; kk < DH / 16; ++kk)
-              tc_mma_bf16(tmem + t * kTile, desc_head(q_tile + t * L::kTileBytes, kk),
-                          desc_head(kt, kk), idesc_s, kk > 0);
-            tc_commit(smem_u32(&tail->s_full[t]));
+      // (a commit holds the queue of MMAs for some 90 cycles: as few as will do)
+      const uint32_t on = elect_one();
+      auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
+        return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
+      };
+      auto wait_k = [&](int i) { return wait(tail->k_full[i % L::kKSlots], i / L::kKSlots); };
+      auto scores = [&](int t, int i) {
+        mma_over_head<DH>(on, tmem + t * kTile, q_tile + t * L::kTileBytes,
+                          k_ring + (i % L::kKSlots) * L::kTileBytes);
+        commit(on, smem_u32(&tail->s_full[t]));
+      };
+      auto padded = [&](int i) {
+        return a.q_docs != nullptr && i < count &&
+               doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded;
+      };
+      const auto p_cols = [](int kk) { return kk * 8; };
+      int turn[2] = {0, 0};  // score tiles done of each query tile
+      bool ok = wait(tail->q_full, 0) && wait_k(0);
+      tc_fence_after();
+      if (ok)
+        for (int t = 0; t < 2; ++t)
+          if (begin >= lo[t] && begin < hi[t]) scores(t, 0);
+      commit(on, smem_u32(&tail->passed[0]));
+      bool pads = padded(0);
+      for (int i = 0; i < count && ok; ++i) {
+        const int n = begin + i, vs = i % L::kVSlots;
+        if (!(ok = wait(tail->v_full[vs], i / L::kVSlots))) break;
+        if (pads)
+          zero_padding_rows<DH>(smem + (2 + L::kKSlots + vs) * L::kTileBytes,
+                                a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile);
+        pads = padded(i + 1);
+        bool have_k = i + 1 == count;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (n >= lo[t] && n < hi[t]) {
+            const uint32_t o = tmem + 256 + t * kTile, w = tmem + t * kTile;
+            const uint32_t vt = v_ring + vs * L::kTileBytes;
+            if (!(ok = wait(tail->p_full[t][0], turn[t]))) break;
+            tc_fence_after();
+            mma_over_tokens<DH, 0, 4>(on, o, w, p_cols, vt, turn[t] > 0);
+            if (!(ok = wait(tail->p_full[t][1], turn[t]))) break;
+            tc_fence_after();
+            mma_over_tokens<DH, 4, 8>(on, o, w, p_cols, vt, true);
+            if (n + 1 == hi[t]) commit(on, smem_u32(&tail->o_done[t]));
+            ++turn[t];
           }
-        };
-        if (ok) ok = wait_tile(0);
-        tc_fence_after();
-        if (ok) {
-          for (int t = 0; t < 2; ++t)
-            if (begin >= lo[t] && begin < hi[t]) scores(t, 0);
-          if (lane == 0) tc_commit(smem_u32(&tail->empty[0]));
-        }
-        for (int n = begin; n < end && ok; ++n) {
-          const int iv = 2 * (n - begin) + 1, ik = iv + 1;
-          if (!(ok = wait_tile(iv))) break;
-          if (a.q_docs != nullptr && doc_range(a.k_ranges, int64_t(b) * ktiles + n).padded)
-            zero_padding_rows<DH>(smem + (2 + iv % L::kSlots) * L::kTileBytes,
-                                  a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile);
-          bool have_k = false;
-          for (int t = 0; t < 2 && ok; ++t) {
-            if (n >= lo[t] && n < hi[t]) {
-              if (!(ok = wait(tail->p_full[t], turn[t]))) break;
+          // the step before is given back here, where the queue is not empty
+          if (t == 0 && i > 0) commit(on, smem_u32(&tail->passed[vs]));
+          if (n + 1 >= lo[t] && n + 1 < hi[t]) {
+            if (!have_k) {
+              if (!(ok = wait_k(i + 1))) break;
               tc_fence_after();
-              if (lane == 0) {
-                const uint32_t vt = ring + (iv % L::kSlots) * L::kTileBytes;
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                  tc_mma_bf16_ts(tmem + 256 + t * kTile, tmem + t * kTile + kk * 8,
-                                 desc_token(vt, kk), idesc_o, turn[t] > 0 || kk > 0);
-                tc_commit(smem_u32(&tail->o_done[t]));
-              }
-              ++turn[t];
+              have_k = true;
             }
-            if (n + 1 >= lo[t] && n + 1 < hi[t]) {
-              if (!have_k) {
-                if (!(ok = wait_tile(ik))) break;
-                tc_fence_after();
-                have_k = true;
-              }
-              scores(t, ik);
-            }
+            scores(t, i + 1);
           }
-          // a slot is given back only once its copy has landed
-          if (ok && n + 1 < end && !have_k) ok = wait_tile(ik);
-          if (ok && lane == 0) {
-            tc_commit(smem_u32(&tail->empty[iv % L::kSlots]));
-            if (n + 1 < end) tc_commit(smem_u32(&tail->empty[ik % L::kSlots]));
-          }
-          __syncwarp();
         }
-        if (lane == 0) {  // nothing of this CTA is in flight when it leaves
-          tc_commit(smem_u32(&tail->drain));
-          mbar_wait_drain(smem_u32(&tail->drain), 0);
-        }
+        // a slot is given back only once its copy has landed
+        if (ok && !have_k) ok = wait_k(i + 1);
         __syncwarp();
       }
+      // nothing of this CTA is in flight when it leaves
+      commit(on, smem_u32(&tail->drain));
+      mbar_wait_drain(smem_u32(&tail->drain), 0);
+      __syncwarp();
     }
   } else {
     set_max_regs_up<kSoftmaxRegs>();
@@ -256,11 +260,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     float2 l2 = make_float2(0.f, 0.f);
     bool ok = true;
     int turn = 0;
+    DocRange kr = {0, 0, 0, 0};
+    if (a.q_docs != nullptr && lo[t] < hi[t])
+      kr = doc_range(a.k_ranges, int64_t(b) * ktiles + lo[t]);
     for (int n = lo[t]; n < hi[t]; ++n, ++turn) {
       // does the mask leave the whole tile?
       bool whole = n * kTile + kTile - 1 <= first_last;
-      if (a.q_docs != nullptr)
-        whole = whole && docs_equal(qr, doc_range(a.k_ranges, int64_t(b) * ktiles + n));
+      int kd[4];
+      if (a.q_docs != nullptr) {
+        whole = whole && docs_equal(qr, kr);
+        if (!whole) load_docs(a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile, kd);
+        if (n + 1 < hi[t]) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
+      }
       ok = mbar_wait(smem_u32(&tail->s_full[t]), turn & 1, abort_flag, a.dev_status);
       if (!__all_sync(~0u, ok)) {
         ok = false;
@@ -279,27 +290,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         for (int j = 0; j < kTile; ++j) s[j] = score2<CAP, BIAS>(sc, s[j], d0 - j, r);
       }
       if (!whole) {
-        const int lim = last - n * kTile;
-        if (a.q_docs == nullptr) {
+        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+        if (a.q_docs != nullptr) same_doc(qd, kd, keep);
 #pragma unroll
-          for (int j = 0; j < kTile; ++j)
-            if (j > lim) s[j] = -INFINITY;
-        } else {
-          const int *kd = a.k_docs + b * a.kds + n * kTile;
-          const int have = a.Sk - n * kTile;
+        for (int c = 0; c < 4; ++c) {
+          keep[c] &= bits_to(last - n * kTile - 32 * c);
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) {
-            const int d = j < have ? kd[j] : -1;
-            if (j > lim || d != qd || d < 0) s[j] = -INFINITY;
-          }
+          for (int j = 0; j < 32; ++j)
+            if (!(keep[c] >> j & 1u)) s[c * 32 + j] = -INFINITY;
         }
       }
       float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int j = 4; j < kTile; j += 4)
+      for (int j = 4; j < kTile - 4; j += 8)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[j + i]);
-      float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[j + 2 * i], s[j + 2 * i + 1]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[kTile - 4 + i]);
+      float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       if constexpr (!CAP && !BIAS) top *= sc.scale2;
       float by = 1.f;
       if (m == -INFINITY) {
@@ -309,13 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         m = top;
       }
       if (__any_sync(~0u, by != 1.f)) {
-        // P V of the tile before has to be in O
-        ok = mbar_wait(smem_u32(&tail->o_done[t]), (turn - 1) & 1, abort_flag, a.dev_status);
-        if (!__all_sync(~0u, ok)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+        // (the scores of this tile were issued after P V of the one before:
+        // that is in O)
         l2.x *= by;
         l2.y *= by;
 #pragma unroll 1
@@ -348,16 +351,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           w[i] = pack_bf16(x.x, x.y);
         }
         tmem_st16(s_addr + c * 16, w);
+        if (c & 1) {  // P V may begin on the first half
+          tmem_wait_st();
+          tc_fence_before();
+          mbar_arrive(smem_u32(&tail->p_full[t][c >> 1]));
+        }
       }
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&tail->p_full[t]));
     }
     if (row0 + t * kTile < a.Sq) {
       if (ok && turn > 0) {
-        ok = mbar_wait(smem_u32(&tail->o_done[t]), (turn - 1) & 1, abort_flag, a.dev_status);
+        ok = mbar_wait(smem_u32(&tail->o_done[t]), 0, abort_flag, a.dev_status);
         ok = __all_sync(~0u, ok);
-      } else if (ok && begin < end) {  // Q's copy has landed before its memory is reused
+      } else if (ok && count > 0) {  // Q's copy has landed before its memory is reused
         ok = mbar_wait(smem_u32(&tail->q_full), 0, abort_flag, a.dev_status);
         ok = __all_sync(~0u, ok);
       }
