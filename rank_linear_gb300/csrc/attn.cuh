@@ -186,6 +186,28 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return *reinterpret_cast<const uint32_t *>(&p);
 }
 
+// A bounded wait of a whole warp: one answer for all lanes, and little code
+// (the issuing warp's path from one product to the next is what the tensor
+// core waits for).
+__device__ __forceinline__ bool wait_warp(const uint64_t &bar, int phase, volatile int *abort_flag,
+                                          unsigned *dev_status) {
+  const uint32_t at = smem_u32(&bar);
+  uint64_t t0 = 0;
+  while (!__all_sync(~0u, mbar_test(at, phase & 1))) {
+    const uint64_t now = globaltimer_ns();
+    if (t0 == 0) t0 = now;
+    const bool late = now - t0 > kWaitLimitNs;
+    if (__any_sync(~0u, late || *abort_flag != 0)) {
+      if (threadIdx.x % 32 == 0 && *abort_flag == 0) {
+        *abort_flag = 1;
+        atomicOr(dev_status, kDevErrTimeout);
+      }
+      return false;
+    }
+  }
+  return true;
+}
+
 // ---------------------------------------------------------------- masks
 // Documents of one 128-token tile: the range of those >= 0 (lo > hi: none),
 // and whether some token is padding.

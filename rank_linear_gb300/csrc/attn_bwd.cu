@@ -200,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       // ------------------------------------------------------ MMA
       const uint32_t on = elect_one();
       auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
-        return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
+        return wait_warp(bar, phase, abort_flag, a.dev_status);
       };
       auto padded = [&](int i) {
         return a.q_docs != nullptr && i < count &&
@@ -308,8 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         if (i + 1 < count) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
       }
       const uint32_t s_addr = tmem + lanes + (i & 1) * kTile + half * 64;
-      ok = mbar_wait(smem_u32(&tail->s_full[i & 1]), (i >> 1) & 1, abort_flag, a.dev_status);
-      if (!(ok = __all_sync(~0u, ok))) break;
+      if (!(ok = wait_warp(tail->s_full[i & 1], i >> 1, abort_flag, a.dev_status))) break;
       tc_fence_after();
       float w[64];
       tmem_ld32(s_addr, w);
@@ -328,8 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
             if (!(keep[c] >> j & 1u)) w[c * 32 + j] = 0.f;
         }
       }
-      ok = mbar_wait(smem_u32(&tail->dp_full[i & 1]), (i >> 1) & 1, abort_flag, a.dev_status);
-      if (!(ok = __all_sync(~0u, ok))) break;
+      if (!(ok = wait_warp(tail->dp_full[i & 1], i >> 1, abort_flag, a.dev_status))) break;
       tc_fence_after();
       float dp[64];
       tmem_ld32(tmem + lanes + 256 + half * 64, dp);
@@ -361,8 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       mbar_arrive(smem_u32(&tail->dz_full));
     }
     if (ok && count > 0) {
-      ok = mbar_wait(smem_u32(&tail->done), 0, abort_flag, a.dev_status);
-      ok = __all_sync(~0u, ok);
+      ok = wait_warp(tail->done, 0, abort_flag, a.dev_status);
     }
     if (ok) {  // dq through Q's shared memory, half of the columns each
       tc_fence_after();
@@ -543,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       // ------------------------------------------------------ MMA
       const uint32_t on = elect_one();
       auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
-        return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
+        return wait_warp(bar, phase, abort_flag, a.dev_status);
       };
       auto padded = [&](int i) {
         return a.q_docs != nullptr && i < count &&
@@ -622,35 +619,42 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     const int tile_last = key0 + kTile - 1;
     const int all_from = a.causal && tile_last >= prefix ? tile_last - off : -(1 << 28);
     const int kd = a.q_docs != nullptr && key < a.Sk ? a.k_docs[b * a.kds + key] : -1;
-    // one of the two statistics of a query, fetched a step ahead
-    auto fetch = [&](int i) {
-      const int head = g * a.group + i / per_head, q = (begin + i % per_head) * kTile + r;
-      const int64_t at = (static_cast<int64_t>(b) * a.Hq + head) * a.Sq + q;
-      if (q >= a.Sq) return half == 0 ? -INFINITY : 0.f;
-      if (half != 0) return -__ldcg(a.delta + at);
-      const float lse = __ldcg(a.lse + at);
-      return lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // sees nothing: P = 0
+    // one of the two statistics of a query, fetched a step ahead: lse or delta
+    const float *stat = (half == 0 ? a.lse : a.delta) + static_cast<int64_t>(b) * a.Hq * a.Sq;
+    auto fetch = [&](int head, int n) {
+      const int q = n * kTile + r;
+      return q < a.Sq ? __ldcg(stat + static_cast<int64_t>(head) * a.Sq + q)
+                      : half == 0 ? -INFINITY : 0.f;
     };
-    auto put = [&](int i, float v) { (half == 0 ? tail->sub : tail->neg_delta)[i & 1][r] = v; };
+    auto put = [&](int i, float v) {
+      if (half == 0)  // a query that sees nothing (lse = -inf): P = 0
+        tail->sub[i & 1][r] = v == -INFINITY ? -INFINITY : -v * kLog2e;
+      else
+        tail->neg_delta[i & 1][r] = -v;
+    };
     bool ok = true;
     DocRange qr = {0, 0, 0, 0};
     if (a.q_docs != nullptr && count > 0) qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin);
-    if (count > 0) put(0, fetch(0));
-    for (int i = 0; i < count; ++i) {
-      const int head = g * a.group + i / per_head, n = begin + i % per_head;
+    if (count > 0) put(0, fetch(g * a.group, begin));
+    int head = g * a.group, n = begin, head1 = head, n1 = begin;  // this step, the next
+    for (int i = 0; i < count; ++i, head = head1, n = n1) {
+      if (++n1 == end) {
+        n1 = begin;
+        ++head1;
+      }
       const int q0 = n * kTile + half * 64;
       const ScoreConst sc = score_const(a, head);
       float ahead = 0.f;
-      if (i + 1 < count) ahead = fetch(i + 1);
+      if (i + 1 < count) ahead = fetch(head1, n1);
       bool whole = n * kTile >= all_from;
       int qd[2];
       if (a.q_docs != nullptr) {
         whole = whole && docs_equal(kr, qr);
         if (!whole) load_docs(a.q_docs + b * a.qds + q0, a.Sq - q0, qd);
         if (i + 1 < count)
-          qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin + (i + 1) % per_head);
+          qr = doc_range(a.q_ranges, int64_t(b) * qtiles + n1);
       }
-      ok = ok && mbar_wait(smem_u32(&tail->s_full), i & 1, abort_flag, a.dev_status);
+      ok = ok && wait_warp(tail->s_full, i, abort_flag, a.dev_status);
       // everyone's statistics of this step are written, those of the step
       // before are no longer read
       if (!(ok = !named_bar_red_or(1, kPairThreads, !ok))) break;
@@ -684,8 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       tc_fence_before();
       mbar_arrive(smem_u32(&tail->p_full));
       if (i + 1 < count) put(i + 1, ahead);
-      ok = mbar_wait(smem_u32(&tail->dp_full), i & 1, abort_flag, a.dev_status);
-      if (!(ok = __all_sync(~0u, ok))) continue;  // leave together, at the next barrier
+      if (!(ok = wait_warp(tail->dp_full, i, abort_flag, a.dev_status))) continue;  // leave together, at the next barrier
       tc_fence_after();
       float dp[64];
       tmem_ld32(dp_addr, dp);
@@ -720,8 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       mbar_arrive(smem_u32(&tail->dz_full));
     }
     if (ok && count > 0) {
-      ok = mbar_wait(smem_u32(&tail->done), 0, abort_flag, a.dev_status);
-      ok = __all_sync(~0u, ok);
+      ok = wait_warp(tail->done, 0, abort_flag, a.dev_status);
     }
     // one warpgroup stages dk (in K's memory), the other dv (in V's)
     uint8_t *stage = smem + half * L::kTileBytes;

@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       // (a commit holds the queue of MMAs for some 90 cycles: as few as will do)
       const uint32_t on = elect_one();
       auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
-        return __all_sync(~0u, mbar_wait(smem_u32(&bar), phase & 1, abort_flag, a.dev_status)) != 0;
+        return wait_warp(bar, phase, abort_flag, a.dev_status);
       };
       auto wait_k = [&](int i) { return wait(tail->k_full[i % L::kKSlots], i / L::kKSlots); };
       auto scores = [&](int t, int i) {
@@ -191,25 +191,32 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       };
       const auto p_cols = [](int kk) { return kk * 8; };
       int turn[2] = {0, 0};  // score tiles done of each query tile
+      // V's tile i has landed; without the rows of padding
+      bool pads = padded(0);
+      auto wait_v = [&](int i) {
+        const int s = i % L::kVSlots, token = (begin + i) * kTile;
+        if (!wait(tail->v_full[s], i / L::kVSlots)) return false;
+        if (pads)
+          zero_padding_rows<DH>(smem + (2 + L::kKSlots + s) * L::kTileBytes,
+                                a.k_docs + b * a.kds + token, a.Sk - token);
+        pads = padded(i + 1);
+        return true;
+      };
       bool ok = wait(tail->q_full, 0) && wait_k(0);
       tc_fence_after();
       if (ok)
         for (int t = 0; t < 2; ++t)
           if (begin >= lo[t] && begin < hi[t]) scores(t, 0);
       commit(on, smem_u32(&tail->passed[0]));
-      bool pads = padded(0);
+      if (ok) ok = wait_v(0);
       for (int i = 0; i < count && ok; ++i) {
         const int n = begin + i, vs = i % L::kVSlots;
-        if (!(ok = wait(tail->v_full[vs], i / L::kVSlots))) break;
-        if (pads)
-          zero_padding_rows<DH>(smem + (2 + L::kKSlots + vs) * L::kTileBytes,
-                                a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile);
-        pads = padded(i + 1);
-        bool have_k = i + 1 == count;
-        for (int t = 0; t < 2 && ok; ++t) {
+        const bool more = i + 1 < count;
+        const uint32_t vt = v_ring + vs * L::kTileBytes;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
           if (n >= lo[t] && n < hi[t]) {
             const uint32_t o = tmem + 256 + t * kTile, w = tmem + t * kTile;
-            const uint32_t vt = v_ring + vs * L::kTileBytes;
             if (!(ok = wait(tail->p_full[t][0], turn[t]))) break;
             tc_fence_after();
             mma_over_tokens<DH, 0, 4>(on, o, w, p_cols, vt, turn[t] > 0);
@@ -219,20 +226,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             if (n + 1 == hi[t]) commit(on, smem_u32(&tail->o_done[t]));
             ++turn[t];
           }
-          // the step before is given back here, where the queue is not empty
-          if (t == 0 && i > 0) commit(on, smem_u32(&tail->passed[vs]));
-          if (n + 1 >= lo[t] && n + 1 < hi[t]) {
-            if (!have_k) {
-              if (!(ok = wait_k(i + 1))) break;
-              tc_fence_after();
-              have_k = true;
-            }
-            scores(t, i + 1);
+          // While the queue is full: the step before is given back, and the
+          // waits for what the next step reads.
+          if (t == 0) {
+            if (i > 0) commit(on, smem_u32(&tail->passed[vs]));
+            if (more && !(ok = wait_k(i + 1))) break;
+          } else if (more) {
+            if (!(ok = wait_v(i + 1))) break;
           }
+          tc_fence_after();
+          if (n + 1 >= lo[t] && n + 1 < hi[t]) scores(t, i + 1);
         }
-        // a slot is given back only once its copy has landed
-        if (ok && !have_k) ok = wait_k(i + 1);
-        __syncwarp();
       }
       // nothing of this CTA is in flight when it leaves
       commit(on, smem_u32(&tail->drain));
@@ -272,11 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (!whole) load_docs(a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile, kd);
         if (n + 1 < hi[t]) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
       }
-      ok = mbar_wait(smem_u32(&tail->s_full[t]), turn & 1, abort_flag, a.dev_status);
-      if (!__all_sync(~0u, ok)) {
-        ok = false;
-        break;
-      }
+      if (!(ok = wait_warp(tail->s_full[t], turn, abort_flag, a.dev_status))) break;
       tc_fence_after();
       float s[kTile];
 #pragma unroll
@@ -360,11 +360,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     }
     if (row0 + t * kTile < a.Sq) {
       if (ok && turn > 0) {
-        ok = mbar_wait(smem_u32(&tail->o_done[t]), 0, abort_flag, a.dev_status);
-        ok = __all_sync(~0u, ok);
+        ok = wait_warp(tail->o_done[t], 0, abort_flag, a.dev_status);
       } else if (ok && count > 0) {  // Q's copy has landed before its memory is reused
-        ok = mbar_wait(smem_u32(&tail->q_full), 0, abort_flag, a.dev_status);
-        ok = __all_sync(~0u, ok);
+        ok = wait_warp(tail->q_full, 0, abort_flag, a.dev_status);
       }
       const float l = l2.x + l2.y;
       const float inv = l > 0.f ? 1.f / l : 0.f;
