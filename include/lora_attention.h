@@ -88,8 +88,8 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
  *   lengths    in, device int32 [batch]; clamped to [0, k_len].  With 0 the
  *              output is zero.  What lies past a length is not read.
  *   workspace  device scratch of lora_attention_token_workspace_bytes.
- * One launch: the cache's length is split over blocks, and the last block of
- * a sequence and key head joins the parts in a fixed order.
+ * One launch, or two where the cache's length is split over blocks: the second
+ * joins the parts in a fixed order.
  */
 size_t lora_attention_token_workspace_bytes(const lora_attention_t *shape);
 lora_status_t lora_attention_token(const lora_attention_t *shape, const void *q, const void *k,

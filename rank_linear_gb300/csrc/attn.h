@@ -38,6 +38,18 @@ cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, cudaStream_t s);
 cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
 cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
-cudaError_t launch_attn_token(const AttnArgs &a, cudaStream_t s);
+
+// One token: the cache's length in `splits` chunks of `chunk` keys, the heads
+// of a group in head_chunks blocks; partial results of [batch][q_heads][splits]
+// (maximum and sum: float2; output: dim rounded up to 64 floats), joined by the
+// second launch where splits > 1.
+struct AttnTokenPlan {
+  int chunk = 64, splits = 1, head_chunks = 1;
+};
+AttnTokenPlan attn_token_plan(int64_t B, int64_t Hk, int group, int64_t Sk);
+cudaError_t launch_attn_token(const AttnArgs &a, const AttnTokenPlan &t, void *stat, void *part,
+                              cudaStream_t s);
+cudaError_t launch_attn_token_join(const AttnArgs &a, const AttnTokenPlan &t, void *stat,
+                                   void *part, cudaStream_t s);
 
 }  // namespace lora

@@ -135,6 +135,22 @@ Plan make_plan(const lora_attention_t *p, bool backward) {
   return w;
 }
 
+// Workspace of the one-token form: [maximum and sum][output] of the chunks.
+struct TokenSpace {
+  AttnTokenPlan plan;
+  size_t part = 0, bytes = 0;
+};
+TokenSpace make_token_space(const lora_attention_t *p) {
+  TokenSpace w;
+  w.plan = attn_token_plan(p->batch, p->k_heads, p->q_heads / p->k_heads, p->k_len);
+  if (w.plan.splits > 1) {
+    const size_t rows = size_t(p->batch) * p->q_heads * w.plan.splits;
+    w.part = rup(rows * 8, 256);
+    w.bytes = w.part + rows * (p->dim <= 64 ? 64 : 128) * 4;
+  }
+  return w;
+}
+
 lora_status_t make_ranges(AttnArgs &a, const Plan &w, void *ws, cudaStream_t st) {
   if (a.q_docs == nullptr) return LORA_OK;
   a.q_ranges = reinterpret_cast<const int4 *>(at(ws, w.q_ranges));
@@ -244,7 +260,7 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
 size_t lora_attention_token_workspace_bytes(const lora_attention_t *shape) {
   clear_error();
   if (check_shape(shape) != LORA_OK) return 0;
-  return 0;
+  return make_token_space(shape).bytes;
 }
 
 lora_status_t lora_attention_token(const lora_attention_t *shape, const void *q, const void *k,
@@ -261,6 +277,8 @@ lora_status_t lora_attention_token(const lora_attention_t *shape, const void *q,
   LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
   if ((lengths == nullptr && !empty) || reinterpret_cast<uintptr_t>(lengths) % 4 != 0)
     return fail(LORA_ERR_INVALID_ARG, "lengths is NULL or not 4-byte aligned");
+  const TokenSpace w = make_token_space(shape);
+  LORA_TRY(check_ws(workspace, workspace_bytes, w.bytes));
   if (empty) return LORA_OK;
   DevInfo di;
   LORA_TRY(device_info(di));
@@ -271,7 +289,12 @@ lora_status_t lora_attention_token(const lora_attention_t *shape, const void *q,
   a.o = o;
   a.lengths = lengths;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  return run(LORA_K_ATTN_TOKEN, st, "attention of one token", [&] { return launch_attn_token(a, st); });
+  void *part = w.bytes > 0 ? at(workspace, w.part) : nullptr;
+  LORA_TRY(run(LORA_K_ATTN_TOKEN, st, "attention of one token",
+               [&] { return launch_attn_token(a, w.plan, workspace, part, st); }));
+  if (w.plan.splits == 1) return LORA_OK;
+  return run(LORA_K_ATTN_TOKEN, st, "join of one token's attention",
+             [&] { return launch_attn_token_join(a, w.plan, workspace, part, st); });
 }
 
 }  // extern "C"
