@@ -10,9 +10,9 @@
  * are.  Tensors may mix bf16 and fp32, have any size and any alignment of
  * their type.
  *
- * Sums: at most 32 squares in fp32, then fp64 throughout; where a partial
- * sum leaves the range fp32 squares can hold, it is taken again in fp64, so
- * that the norm is right over the whole range of the inputs.  The order of
+ * Sums: at most 33 squares in fp32, then unevaluated pairs of fp32 and fp64;
+ * where a partial sum leaves the range fp32 squares can hold, it is taken
+ * again in fp64, so that the norm is right over the whole range of the inputs.  The order of
  * every sum is fixed: the same plan and values give the same bits.  NaN or
  * infinite gradients give a NaN or infinite norm, and c as the formula has
  * it (NaN, or 0).

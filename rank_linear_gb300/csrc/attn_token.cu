@@ -64,12 +64,14 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_attn_token(const Params p) {
   const int quad = lane / 4, part = lane % 4;
   griddep_wait();
   griddep_launch_dependents();
+  // neighbouring blocks take the key heads of the same keys, which lie side by
+  // side in a [positions][heads] cache
   int id = blockIdx.x;
-  const int split = id % p.splits;
-  id /= p.splits;
+  const int g = id % a.Hk;
+  id /= a.Hk;
   const int hc = id % p.head_chunks;
   id /= p.head_chunks;
-  const int g = id % a.Hk, b = id / a.Hk;
+  const int split = id % p.splits, b = id / p.splits;
   const int len = min(max(a.lengths[b], 0), a.Sk);
   const int from = split * p.chunk, to = min(from + p.chunk, len);
   const int h0 = g * a.group + hc * kHeads;               // the block's first head
@@ -119,10 +121,24 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_attn_token(const Params p) {
     }
   };
 
+  // lines of 128 bytes of a step's K (V) rows, one a lane, towards L2
+  auto prefetch = [&](int key0) {
+    const int key = key0 + (NB == 2 ? lane / 2 : lane % 16);
+    const int e = NB == 2 ? lane % 2 * 64 : 0;
+    if (key >= to || e >= a.D) return;
+    if (NB == 2 || lane < 16)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(kp - 8 * part + key * a.sk[1] + e));
+    if (NB == 2 || lane >= 16)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(vp - 8 * quad + key * a.sv[1] + e));
+  };
+  constexpr int kStep = kWarps * kKeys, kAhead = 3;
   int key0 = from + warp * kKeys;
   if (key0 < to) load_k(key0);
-  for (; key0 < to; key0 += kWarps * kKeys) {
+#pragma unroll
+  for (int i = 1; i < kAhead; ++i) prefetch(key0 + i * kStep);
+  for (; key0 < to; key0 += kStep) {
     load_v(key0);
+    prefetch(key0 + kAhead * kStep);
     float s[4] = {0.f, 0.f, 0.f, 0.f};  // keys quad, quad + 8 x heads 2 part, 2 part + 1
 #pragma unroll
     for (int c = 0; c < 2 * NB; ++c) {
@@ -131,7 +147,7 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_attn_token(const Params p) {
       mma_16816(s, lo, q[c].x, q[c].y);
       mma_16816(s, hi, q[c].z, q[c].w);
     }
-    if (key0 + kWarps * kKeys < to) load_k(key0 + kWarps * kKeys);
+    if (key0 + kStep < to) load_k(key0 + kStep);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + quad + 8 * (i >> 1);
@@ -236,52 +252,81 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_attn_token(const Params p) {
 }
 
 // Joins the chunks of one head per block: a thread takes 4 elements of every
-// kLanes-th chunk, and the lanes' sums meet in shared memory in their order.
-constexpr int kLanes = 8;
+// lanes-th chunk, and the lanes' sums meet in shared memory in their order.
 template <int NB>
-__global__ void __launch_bounds__(16 * NB * kLanes) k_attn_token_join(const Params p) {
+struct Join {
+  static constexpr int kCols = 16 * NB, kLanes = 512 / kCols;
+};
+template <int NB>
+__global__ void __launch_bounds__(512) k_attn_token_join(const Params p) {
+  constexpr int kCols = Join<NB>::kCols, kLanes = Join<NB>::kLanes;
   const AttnArgs &a = p.a;
-  __shared__ float4 acc_s[kLanes][16 * NB];
+  __shared__ float4 acc_s[kLanes][kCols];
   __shared__ float sum_s[kLanes], top_s[kLanes];
-  const int y = threadIdx.x / (16 * NB), x = threadIdx.x % (16 * NB);
+  const int y = threadIdx.x / kCols, x = threadIdx.x % kCols;
   const int h = blockIdx.x % a.Hq, b = blockIdx.x / a.Hq;
   griddep_wait();
   griddep_launch_dependents();
   const int len = min(max(a.lengths[b], 0), a.Sk);
   const int n = (len + p.chunk - 1) / p.chunk;
   const int64_t row = (static_cast<int64_t>(b) * a.Hq + h) * p.splits;
-  float top = -INFINITY;
-  for (int i = y; i < n; i += kLanes) top = fmaxf(top, __ldcg(&p.stat[row + i]).x);
-  if (x == 0) top_s[y] = top;
+  // each lane relative to its own maximum
+  float top = -INFINITY, sum = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  constexpr int U = 4;
+  for (int i0 = y; i0 < n; i0 += U * kLanes) {
+    float2 st[U];
+    float4 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * kLanes;
+      st[u] = make_float2(-INFINITY, 0.f);
+      v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        st[u] = __ldcg(&p.stat[row + i]);
+        v[u] = __ldcg(reinterpret_cast<const float4 *>(p.part + (row + i) * (4 * kCols)) + x);
+      }
+    }
+    float t1 = top;
+#pragma unroll
+    for (int u = 0; u < U; ++u) t1 = fmaxf(t1, st[u].x);
+    const float keep = top == -INFINITY ? 0.f : ex2(top - t1);
+    top = t1;
+    sum *= keep;
+    acc.x *= keep;
+    acc.y *= keep;
+    acc.z *= keep;
+    acc.w *= keep;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const float by = st[u].x == -INFINITY ? 0.f : ex2(st[u].x - top);
+      sum = fmaf(by, st[u].y, sum);
+      acc.x = fmaf(by, v[u].x, acc.x);
+      acc.y = fmaf(by, v[u].y, acc.y);
+      acc.z = fmaf(by, v[u].z, acc.z);
+      acc.w = fmaf(by, v[u].w, acc.w);
+    }
+  }
+  acc_s[y][x] = acc;
+  if (x == 0) {
+    sum_s[y] = sum;
+    top_s[y] = top;
+  }
   __syncthreads();
-  top = top_s[0];
+  if (y != 0 || 4 * x >= a.D) return;
 #pragma unroll
   for (int i = 1; i < kLanes; ++i) top = fmaxf(top, top_s[i]);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  float sum = 0.f;
-#pragma unroll 4
-  for (int i = y; i < n; i += kLanes) {
-    const float2 st = __ldcg(&p.stat[row + i]);
-    const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + (row + i) * (64 * NB)) + x);
-    const float by = ex2(st.x - top);
-    sum = fmaf(by, st.y, sum);
+  acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < kLanes; ++i) {
+    const float by = top_s[i] == -INFINITY ? 0.f : ex2(top_s[i] - top);
+    const float4 v = acc_s[i][x];
+    sum = fmaf(by, sum_s[i], sum);
     acc.x = fmaf(by, v.x, acc.x);
     acc.y = fmaf(by, v.y, acc.y);
     acc.z = fmaf(by, v.z, acc.z);
     acc.w = fmaf(by, v.w, acc.w);
-  }
-  acc_s[y][x] = acc;
-  if (x == 0) sum_s[y] = sum;
-  __syncthreads();
-  if (y != 0 || 4 * x >= a.D) return;
-#pragma unroll
-  for (int i = 1; i < kLanes; ++i) {
-    const float4 v = acc_s[i][x];
-    acc.x += v.x;
-    acc.y += v.y;
-    acc.z += v.z;
-    acc.w += v.w;
-    sum += sum_s[i];
   }
   const float inv = sum > 0.f ? 1.f / sum : 0.f;
   *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2] + 4 * x) =
@@ -300,18 +345,20 @@ cudaError_t launch(const Params &p, cudaStream_t s) {
 
 }  // namespace
 
-// Chunks of the cache's length: about two blocks for each place of a GB300's
-// 152 SMs x 4 (ragged batches leave some without work), of 64 keys (a step of
-// the block) at the least, and no more chunks than the joining kernel passes
-// over in little time.
+// Chunks of the cache's length.  A GB300's 152 SMs hold 4 blocks each: enough
+// chunks for about 6 rounds of them (ragged batches leave some without work,
+// and the last round is rarely full), of 256 keys at the least where one round
+// is full with those, else of 64 (a step of the block).
 AttnTokenPlan attn_token_plan(int64_t B, int64_t Hk, int group, int64_t Sk) {
   AttnTokenPlan t;
   t.head_chunks = (group + kHeads - 1) / kHeads;
-  const int64_t blocks = B * Hk * t.head_chunks, places = 2 * 152 * 4;
-  int64_t splits = blocks > 0 ? (places + blocks - 1) / blocks : 1;
-  splits = splits > 128 ? 128 : splits;
-  int64_t chunk = (Sk + splits - 1) / splits;
-  chunk = (chunk + 63) / 64 * 64;
+  const int64_t rows = B * Hk * t.head_chunks, places = 152 * 4;
+  auto chunk_of = [&](int64_t blocks) {
+    const int64_t splits = rows > 0 && blocks > rows ? blocks / rows : 1;
+    return (Sk + splits * 64 - 1) / (splits * 64) * 64;
+  };
+  int64_t chunk = chunk_of(6 * places);
+  if (chunk < 256) chunk = chunk_of(places) < 256 ? chunk_of(places) : 256;
   t.chunk = static_cast<int>(chunk < 64 ? 64 : chunk);
   t.splits = static_cast<int>(Sk > 0 ? (Sk + t.chunk - 1) / t.chunk : 1);
   return t;
@@ -328,8 +375,8 @@ cudaError_t launch_attn_token_join(const AttnArgs &a, const AttnTokenPlan &t, vo
   const Params p{a, static_cast<float2 *>(stat), static_cast<float *>(part), t.chunk, t.splits,
                  t.head_chunks};
   const dim3 grid(static_cast<unsigned>(int64_t(a.B) * a.Hq));
-  return a.D <= 64 ? launch_pdl(k_attn_token_join<1>, grid, dim3(16 * kLanes), 0, s, p)
-                   : launch_pdl(k_attn_token_join<2>, grid, dim3(32 * kLanes), 0, s, p);
+  return a.D <= 64 ? launch_pdl(k_attn_token_join<1>, grid, dim3(512), 0, s, p)
+                   : launch_pdl(k_attn_token_join<2>, grid, dim3(512), 0, s, p);
 }
 
 }  // namespace lora

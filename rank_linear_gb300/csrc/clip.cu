@@ -30,13 +30,18 @@ struct Chunk {
 };
 static_assert(sizeof(Chunk) == 32, "chunk record");
 
+// A block's part of the norm: in fp32 (a pair for the sum of squares), and in
+// fp64, which counts where the fp32 one is out of range (see out_of_range).
+struct Partial {
+  float hi, lo;
+  double full;
+};
 struct PlanHead {
   unsigned ticket;  // blocks of the norm pass done; 0 between calls
-  float factor;
-  int64_t pad;
-  double partial[kMaxBlocks];
+  int pad[3];
+  Partial partial[kMaxBlocks];
 };
-static_assert(sizeof(PlanHead) % 32 == 0 || sizeof(PlanHead) % 16 == 0, "chunks stay aligned");
+static_assert(sizeof(PlanHead) % 16 == 0, "chunks stay aligned");
 
 __device__ __forceinline__ Chunk load_chunk(const Chunk *p) {
   Chunk c;
@@ -78,8 +83,21 @@ __device__ __forceinline__ void unpack(const uint4 &v, float (&f)[BF ? 8 : 4]) {
 // underflow or overflow (each square kept to 2^-24 above 2^-126).
 constexpr float kSafeLow = 1e-30f, kSafeHigh = 1e30f;
 
+// A thread's sum: fast as an unevaluated sum of two fp32 (fp64 adds are some
+// 30 times dearer here), wide for what does not fit fp32.
+struct Sum {
+  float hi = 0.f, lo = 0.f;
+  double wide = 0.0;
+};
+// hi + lo += x + y (|x| arbitrary): the exact sum of hi and x, its error kept.
+__device__ __forceinline__ void add_to(float &hi, float &lo, float x, float y) {
+  const float s = hi + x, t = s - hi;
+  lo += ((hi - (s - t)) + (x - t)) + y;
+  hi = s;
+}
+
 template <bool BF, bool LARGEST>
-__device__ void add_chunk(const Chunk &c, double &acc) {
+__device__ void add_chunk(const Chunk &c, Sum &acc) {
   constexpr int N = BF ? 8 : 4, ES = 16 / N;
   int head, vecs;
   split_run<ES>(c.in, c.count, head, vecs);
@@ -103,7 +121,7 @@ __device__ void add_chunk(const Chunk &c, double &acc) {
   }
   if constexpr (LARGEST) {
     // fmaxf drops NaN: a NaN is carried over by the comparison
-    float m = static_cast<float>(acc);
+    float m = acc.hi;
     auto top = [&](float x) {
       x = fabsf(x);
       if (!(x <= m)) m = (m != m) ? m : x;
@@ -116,7 +134,7 @@ __device__ void add_chunk(const Chunk &c, double &acc) {
       for (int e = 0; e < N; ++e) top(f[e]);
     }
     top(lone);
-    acc = m;
+    acc.hi = m;
   } else {
     float s0 = lone * lone, s1 = 0.f;
 #pragma unroll
@@ -131,7 +149,7 @@ __device__ void add_chunk(const Chunk &c, double &acc) {
     }
     const float s = s0 + s1;
     if (s >= kSafeLow && s <= kSafeHigh) {
-      acc += static_cast<double>(s);
+      add_to(acc.hi, acc.lo, s, 0.f);
     } else {  // all zero, far off scale, or not finite: again in fp64
       unsigned any = __float_as_uint(lone) << 1;
 #pragma unroll
@@ -147,39 +165,85 @@ __device__ void add_chunk(const Chunk &c, double &acc) {
 #pragma unroll
           for (int e = 0; e < N; ++e) d += static_cast<double>(f[e]) * f[e];
         }
-        acc += d;
+        acc.wide += d;
       }
     }
   }
 }
 
-template <bool LARGEST>
-__device__ __forceinline__ double join(double a, double b) {
-  if constexpr (LARGEST) return (a != a) ? a : (b <= a ? a : b);  // NaN wins
-  return a + b;
+// NaN wins.
+__device__ __forceinline__ float larger(float a, float b) {
+  return (a != a) ? a : (b <= a ? a : b);
 }
 
-// The block's value in thread 0; the order depends on the block size only.
+// The threads' values in every thread; the order depends on the block size only.
 template <bool LARGEST>
+__device__ float2 join_block(float hi, float lo) {
+  __shared__ float2 part[kThreads / 32];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const float x = __shfl_xor_sync(~0u, hi, o);
+    if constexpr (LARGEST)
+      hi = larger(hi, x);
+    else
+      add_to(hi, lo, x, __shfl_xor_sync(~0u, lo, o));
+  }
+  if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = make_float2(hi, lo);
+  __syncthreads();
+  float2 v = part[0];
+  for (int i = 1; i < kThreads / 32; ++i) {
+    if constexpr (LARGEST)
+      v.x = larger(v.x, part[i].x);
+    else
+      add_to(v.x, v.y, part[i].x, part[i].y);
+  }
+  __syncthreads();
+  return v;
+}
 __device__ double join_block(double v) {
   __shared__ double part[kThreads / 32];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = join<LARGEST>(v, __shfl_xor_sync(~0u, v, o));
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
   if (threadIdx.x % 32 == 0) part[threadIdx.x / 32] = v;
   __syncthreads();
   v = part[0];
-  if (threadIdx.x == 0)
-    for (int i = 1; i < kThreads / 32; ++i) v = join<LARGEST>(v, part[i]);
+  for (int i = 1; i < kThreads / 32; ++i) v += part[i];
+  __syncthreads();
   return v;
 }
 
+// Joins the blocks' parts in the order of their numbers; the norm, in every
+// thread.
 template <bool LARGEST>
+__device__ float join_parts(const PlanHead *head, int blocks) {
+  float hi = 0.f, lo = 0.f;
+  for (int b = threadIdx.x; b < blocks; b += kThreads) {
+    const float2 v = __ldcg(reinterpret_cast<const float2 *>(&head->partial[b]));
+    if constexpr (LARGEST)
+      hi = larger(hi, v.x);
+    else
+      add_to(hi, lo, v.x, v.y);
+  }
+  const float2 v = join_block<LARGEST>(hi, lo);
+  if constexpr (LARGEST) return v.x;
+  const float total = v.x + v.y;
+  if (total > kSafeLow && total < kSafeHigh) return sqrtf(total);
+  // nothing at all, far off scale, or not finite
+  double full = 0.0;
+  for (int b = threadIdx.x; b < blocks; b += kThreads) full += __ldcg(&head->partial[b].full);
+  return static_cast<float>(sqrt(join_block(full)));
+}
+
+// JOIN: the last block done also joins the parts into norm[0] (else the
+// clipping pass does, in each of its blocks: cheaper than the ticket and one
+// block's work behind it).
+template <bool LARGEST, bool JOIN>
 __global__ void __launch_bounds__(kThreads) k_grad_norm(PlanHead *head, const Chunk *chunks,
-                                                        int n, float max_norm, float *norm) {
+                                                        int n, float *norm) {
   __shared__ bool last;
   griddep_wait();
   griddep_launch_dependents();
-  double acc = 0.0;
+  Sum sum;
   int i = blockIdx.x;
   if (i < n) {
     Chunk c = load_chunk(chunks + i);
@@ -188,40 +252,68 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(PlanHead *head, const Ch
       Chunk cn = c;
       if (next < n) cn = load_chunk(chunks + next);
       if (c.dtype == LORA_BF16)
-        add_chunk<true, LARGEST>(c, acc);
+        add_chunk<true, LARGEST>(c, sum);
       else
-        add_chunk<false, LARGEST>(c, acc);
+        add_chunk<false, LARGEST>(c, sum);
       if (next >= n) break;
       c = cn;
       i = next;
     }
   }
-  acc = join_block<LARGEST>(acc);
-  if (threadIdx.x == 0) {
-    head->partial[blockIdx.x] = acc;
-    __threadfence();
-    last = atomicAdd(&head->ticket, 1u) == gridDim.x - 1;
+  float2 v = join_block<LARGEST>(sum.hi, sum.lo);
+  Partial p = {v.x, v.y, 0.0};
+  if constexpr (!LARGEST) {
+    const bool wide = __syncthreads_or(sum.wide != 0.0);  // NaN is not 0
+    double full = 0.0;
+    if (wide) full = join_block(sum.wide);
+    p.full = static_cast<double>(v.x) + v.y + full;
+    if (wide) {  // as fp32 has it: out of its safe range, or good to 2^-24
+      p.hi = static_cast<float>(p.full);
+      p.lo = p.hi - p.hi != 0.f ? 0.f : static_cast<float>(p.full - p.hi);
+    }
   }
-  __syncthreads();
-  if (!last) return;
-  // the last block joins the partials in the order of the blocks' numbers
-  __threadfence();
-  double v = 0.0;
-  for (int b = threadIdx.x; b < gridDim.x; b += kThreads)
-    v = join<LARGEST>(v, __ldcg(&head->partial[b]));
-  __syncthreads();
-  v = join_block<LARGEST>(v);
-  if (threadIdx.x == 0) {
-    const double total = LARGEST ? v : sqrt(v);
-    const double by = static_cast<double>(max_norm) / (total + 1e-6);
-    norm[0] = static_cast<float>(total);
-    head->factor = by > 1.0 ? 1.f : static_cast<float>(by);  // NaN stays NaN
-    head->ticket = 0;
+  if (threadIdx.x == 0) head->partial[blockIdx.x] = p;
+  if constexpr (JOIN) {
+    if (threadIdx.x == 0) {
+      __threadfence();
+      last = atomicAdd(&head->ticket, 1u) == gridDim.x - 1;
+    }
+    __syncthreads();
+    if (!last) return;
+    __threadfence();
+    const float total = join_parts<LARGEST>(head, gridDim.x);
+    if (threadIdx.x == 0) {
+      norm[0] = total;
+      head->ticket = 0;
+    }
+  }
+}
+
+// A chunk's vectors, where input and output share their alignment.
+struct Held {
+  uint4 v[kVecs];
+};
+__device__ __forceinline__ bool aligned_alike(const Chunk &c) {
+  return ((reinterpret_cast<uintptr_t>(c.in) ^ reinterpret_cast<uintptr_t>(c.out)) & 15) == 0;
+}
+__device__ __forceinline__ void hold(const Chunk &c, Held &h) {
+  if (!aligned_alike(c)) return;
+  int head, vecs;
+  if (c.dtype == LORA_BF16)
+    split_run<2>(c.in, c.count, head, vecs);
+  else
+    split_run<4>(c.in, c.count, head, vecs);
+  const uint4 *src = reinterpret_cast<const uint4 *>(
+      static_cast<const char *>(c.in) + head * (c.dtype == LORA_BF16 ? 2 : 4));
+#pragma unroll
+  for (int u = 0; u < kVecs; ++u) {
+    const int i = threadIdx.x + u * kThreads;
+    if (i < vecs) h.v[u] = __ldcg(src + i);
   }
 }
 
 template <bool BF>
-__device__ __forceinline__ void scale_chunk(const Chunk &c, float f) {
+__device__ __forceinline__ void scale_chunk(const Chunk &c, const Held &h, float f) {
   constexpr int N = BF ? 8 : 4, ES = 16 / N;
   using T = typename std::conditional<BF, __nv_bfloat16, float>::type;
   const T *in = static_cast<const T *>(c.in);
@@ -233,26 +325,20 @@ __device__ __forceinline__ void scale_chunk(const Chunk &c, float f) {
       out[i] = in[i] * f;
   };
   const int tid = threadIdx.x;
-  if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15) != 0) {
-    for (int i = tid; i < c.count; i += kThreads) one(i);  // no common alignment
+  if (!aligned_alike(c)) {
+#pragma unroll 4
+    for (int i = tid; i < c.count; i += kThreads) one(i);
     return;
   }
   int head, vecs;
   split_run<ES>(c.in, c.count, head, vecs);
-  const uint4 *src = reinterpret_cast<const uint4 *>(in + head);
   uint4 *dst = reinterpret_cast<uint4 *>(out + head);
-  uint4 v[kVecs];
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const int i = tid + u * kThreads;
-    if (i < vecs) v[u] = __ldcg(src + i);
-  }
 #pragma unroll
   for (int u = 0; u < kVecs; ++u) {
     const int i = tid + u * kThreads;
     if (i >= vecs) continue;
     float x[N];
-    unpack<BF>(v[u], x);
+    unpack<BF>(h.v[u], x);
     uint4 o;
     unsigned *w = reinterpret_cast<unsigned *>(&o);
 #pragma unroll
@@ -264,30 +350,43 @@ __device__ __forceinline__ void scale_chunk(const Chunk &c, float f) {
         w[e] = __float_as_uint(x[e] * f);
       }
     }
-    dst[i] = o;
+    __stcs(dst + i, o);  // read by no one here: leaves L2 to the gradients
   }
   if (tid < c.count - vecs * N) one(tid < head ? tid : tid + vecs * N);
 }
 
-__global__ void __launch_bounds__(kThreads) k_grad_clip(const PlanHead *head, const Chunk *chunks,
-                                                        int n) {
-  // the chunk records do not depend on the norm pass
+template <bool LARGEST>
+__global__ void __launch_bounds__(kThreads, 6) k_grad_clip(const PlanHead *head,
+                                                           const Chunk *chunks, int n, int parts,
+                                                           float max_norm, float *norm) {
+  // Records and gradients do not depend on the norm pass (which let this
+  // kernel start when all before it was done): the first chunk is asked for
+  // ahead of the wait.
   int i = n - 1 - static_cast<int>(blockIdx.x);
-  Chunk c = load_chunk(chunks + max(i, 0));
+  Chunk c = {};
+  Held h;
+  if (i >= 0) {
+    c = load_chunk(chunks + i);
+    hold(c, h);
+  }
   griddep_wait();
   griddep_launch_dependents();
-  const float f = __ldcg(&head->factor);
+  const float total = join_parts<LARGEST>(head, parts);
+  if (blockIdx.x == 0 && threadIdx.x == 0) norm[0] = total;
+  const float by = max_norm / (total + 1e-6f);
+  const float f = by > 1.f ? 1.f : by;  // NaN stays NaN
   while (i >= 0) {
     const int next = i - static_cast<int>(gridDim.x);
-    Chunk cn = c;
+    Chunk cn = {};
     if (next >= 0) cn = load_chunk(chunks + next);
     if (f != 1.f || c.in != c.out) {
       if (c.dtype == LORA_BF16)
-        scale_chunk<true>(c, f);
+        scale_chunk<true>(c, h, f);
       else
-        scale_chunk<false>(c, f);
+        scale_chunk<false>(c, h, f);
     }
     c = cn;
+    if (next >= 0 && (f != 1.f || c.in != c.out)) hold(c, h);
     i = next;
   }
 }
@@ -342,17 +441,17 @@ lora_status_t check_plan(const void *plan, size_t bytes, int largest, const floa
   return LORA_OK;
 }
 
-lora_status_t norm_pass(const DevInfo &di, void *plan, int n, float max_norm, int largest,
-                        float *norm, cudaStream_t st) {
-  PlanHead *head = static_cast<PlanHead *>(plan);
-  const Chunk *chunks = reinterpret_cast<const Chunk *>(head + 1);
+int norm_blocks(const DevInfo &di, int n) {
   const int most = di.sms * kBlocksPerSm < kMaxBlocks ? di.sms * kBlocksPerSm : kMaxBlocks;
-  const int grid = n < 1 ? 1 : n < most ? n : most;
+  return n < 1 ? 1 : n < most ? n : most;
+}
+lora_status_t norm_pass(const DevInfo &di, PlanHead *head, int n, int largest, bool join,
+                        float *norm, cudaStream_t st) {
+  const Chunk *chunks = reinterpret_cast<const Chunk *>(head + 1);
+  auto *kernel = largest ? (join ? k_grad_norm<true, true> : k_grad_norm<true, false>)
+                         : (join ? k_grad_norm<false, true> : k_grad_norm<false, false>);
   return run(LORA_K_GRAD_NORM, st, "gradient norm", [&] {
-    return largest ? launch_pdl(k_grad_norm<true>, dim3(grid), dim3(kThreads), 0, st, head, chunks,
-                                n, max_norm, norm)
-                   : launch_pdl(k_grad_norm<false>, dim3(grid), dim3(kThreads), 0, st, head,
-                                chunks, n, max_norm, norm);
+    return launch_pdl(kernel, dim3(norm_blocks(di, n)), dim3(kThreads), 0, st, head, chunks, n, norm);
   });
 }
 
@@ -407,7 +506,8 @@ lora_status_t lora_clip_norm(void *plan, size_t plan_bytes, int largest, float *
   LORA_TRY(check_plan(plan, plan_bytes, largest, norm, &n));
   DevInfo di;
   LORA_TRY(device_info(di));
-  return norm_pass(di, plan, n, 0.f, largest, norm, static_cast<cudaStream_t>(stream));
+  return norm_pass(di, static_cast<PlanHead *>(plan), n, largest, true, norm,
+                   static_cast<cudaStream_t>(stream));
 }
 
 lora_status_t lora_clip(void *plan, size_t plan_bytes, float max_norm, int largest, float *norm,
@@ -419,13 +519,14 @@ lora_status_t lora_clip(void *plan, size_t plan_bytes, float max_norm, int large
   DevInfo di;
   LORA_TRY(device_info(di));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  LORA_TRY(norm_pass(di, plan, n, max_norm, largest, norm, st));
-  if (n == 0) return LORA_OK;
   PlanHead *head = static_cast<PlanHead *>(plan);
+  if (n == 0) return norm_pass(di, head, n, largest, true, norm, st);
+  LORA_TRY(norm_pass(di, head, n, largest, false, norm, st));
   const Chunk *chunks = reinterpret_cast<const Chunk *>(head + 1);
-  const int most = di.sms * kBlocksPerSm;
+  const int blocks = n < di.sms * 6 ? n : di.sms * 6;
   return run(LORA_K_GRAD_CLIP, st, "gradient clip", [&] {
-    return launch_pdl(k_grad_clip, dim3(n < most ? n : most), dim3(kThreads), 0, st, head, chunks, n);
+    return launch_pdl(largest ? k_grad_clip<true> : k_grad_clip<false>, dim3(blocks),
+                      dim3(kThreads), 0, st, head, chunks, n, norm_blocks(di, n), max_norm, norm);
   });
 }
 
