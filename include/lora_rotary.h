@@ -53,8 +53,8 @@ lora_status_t lora_rotary_turns(const double *radians, int n, uint64_t *turns);
  *   q_out, k_out  out, device, same dtype.  An output may be its input (same
  *                 address and strides: in place); otherwise it must not
  *                 overlap any input.
- * batch * seq == 0 launches nothing.  (q_heads + k_heads) * (dim / 2 + 1) may
- * be up to 65535, batch * seq less than 2^31 (LORA_ERR_UNSUPPORTED).
+ * batch * seq == 0 launches nothing; it has to be less than 2^31
+ * (LORA_ERR_UNSUPPORTED).
  */
 lora_status_t lora_rotary(const lora_rotary_t *shape, const void *q, const void *k,
                           const void *positions, const uint64_t *turns, lora_dtype_t dtype,

@@ -114,6 +114,8 @@ class LoraError(RuntimeError):
 def lib():
     """The loaded library (built on first use if sources are present)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):

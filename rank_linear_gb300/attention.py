@@ -10,8 +10,8 @@ import ctypes
 import torch
 
 from . import _lib
-from .lora import _stream_ptr
-from .rotary import _on
+from .lora import _ptr, _stream_ptr
+from .rotary import _block, _layout, _on
 
 
 def _strides(t, name):
@@ -23,15 +23,16 @@ def _strides(t, name):
     return s[:3]
 
 
-def _word(t, dtype, name, shape):
+def _check_word(t, dtype, name, shape):
     if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
-    return t.data_ptr() or None
 
 
-def _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix):
+def _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix, like_q, like_k):
+    """The argument block without addresses; like_q, like_k: the other tensors
+    by their names in it, of q's (k's) shape."""
     if q.dim() != 4 or k.dim() != 4 or v.shape != k.shape:
         raise ValueError("q is [batch, q_len, q_heads, dim], k and v [batch, k_len, k_heads, dim]")
     b, sq, hq, d = q.shape
@@ -42,22 +43,44 @@ def _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix):
                              causal=int(causal), scale=d ** -0.5 if scale is None else scale,
                              softcap=softcap or 0.0)
     sh.q, sh.k, sh.v = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
+    for like, others in ((q, like_q), (k, like_k)):
+        for name, t in others.items():
+            if t.shape != like.shape:
+                raise ValueError(f"{name} {tuple(t.shape)} is not {tuple(like.shape)}")
+            setattr(sh, name, _strides(t, name))
     if slopes is not None:
-        sh.slopes = _word(slopes, torch.float32, "slopes", (hq,))
+        _check_word(slopes, torch.float32, "slopes", (hq,))
+    if qd is not None:
+        _check_word(qd, torch.int32, "q documents", (b, sq))
+        _check_word(kd, torch.int32, "k documents", (b, sk))
+        sh.q_docs_stride, sh.k_docs_stride = qd.stride(0), kd.stride(0)
+    if prefix is not None:
+        _check_word(prefix, torch.int32, "prefix", (b,))
+    return sh
+
+
+def _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix, like_q, like_k):
+    qd = kd = None
     if documents is not None:
         if isinstance(documents, (tuple, list)):
             qd, kd = documents
         else:
+            sq, sk = q.shape[1], k.shape[1]
             if sq > sk:
                 raise ValueError("one documents tensor needs q_len <= k_len")
             kd = documents
             qd = documents if sq == sk else documents[:, sk - sq:]
-        sh.q_docs, sh.q_docs_stride = _word(qd, torch.int32, "q documents", (b, sq)), qd.stride(0)
-        sh.k_docs, sh.k_docs_stride = _word(kd, torch.int32, "k documents", (b, sk)), kd.stride(0)
-        if sh.q_docs is None or sh.k_docs is None:  # an empty side: nothing to mask
-            sh.q_docs = sh.k_docs = None
-    if prefix is not None:
-        sh.prefix = _word(prefix, torch.int32, "prefix", (b,))
+    key = (_layout(q), _layout(k), _layout(v), scale, causal, softcap, _layout(slopes),
+           _layout(qd), _layout(kd), _layout(prefix), tuple(like_q),
+           *map(_layout, like_q.values()), *map(_layout, like_k.values()))
+    block = _block(key, lambda: _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd,
+                                            prefix, like_q, like_k))
+    if slopes is None and qd is None and prefix is None:
+        return block
+    sh = _lib.AttentionShape.from_buffer_copy(block)
+    sh.slopes, sh.prefix = _ptr(slopes), _ptr(prefix)
+    if qd is not None and qd.numel() and kd.numel():  # an empty side: nothing to mask
+        sh.q_docs, sh.k_docs = _ptr(qd), _ptr(kd)
     return sh
 
 
@@ -65,10 +88,6 @@ def _scratch(nbytes, like, workspace):
     if workspace is not None:
         return workspace
     return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
-
-
-def _ptr(t):
-    return None if t is None else t.data_ptr() or None
 
 
 def _size(t):
@@ -90,7 +109,6 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
     prefix     int32 [batch]: keys before it are visible to every query
                (with causal).
     """
-    sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix)
     L = _lib.lib()
     with _on(stream):
         if out is None:
@@ -98,13 +116,12 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
         if lse is None:
             lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], dtype=torch.float32,
                               device=q.device)
-        if out.shape != q.shape:
-            raise ValueError(f"out {tuple(out.shape)} is not {tuple(q.shape)}")
-        sh.o = _strides(out, "out")
+        sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix, {"o": out}, {})
         workspace = _scratch(L.lora_attention_workspace_bytes(ctypes.byref(sh), 0), q, workspace)
-    _lib.check(L.lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                    _ptr(lse), _ptr(workspace), _size(workspace),
-                                    _stream_ptr(stream)), "lora_attention_fwd")
+    st = L.lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
+                              _ptr(workspace), _size(workspace), _stream_ptr(stream))
+    if st:
+        _lib.check(st, "lora_attention_fwd")
     return out, lse
 
 
@@ -112,26 +129,22 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
                        slopes=None, documents=None, prefix=None, dq=None, dk=None, dv=None,
                        workspace=None, stream=None):
     """(dq, dk, dv) from the gradient of attention_forward's output."""
-    sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix)
     L = _lib.lib()
-    if out.shape != q.shape or dout.shape != q.shape:
-        raise ValueError("out and dout must have q's shape")
     if lse.dtype != torch.float32 or not lse.is_contiguous() or \
-            tuple(lse.shape) != (q.shape[0], q.shape[2], q.shape[1]):
+            lse.shape != (q.shape[0], q.shape[2], q.shape[1]):
         raise ValueError("lse must be the forward's: float32 [batch, q_heads, q_len]")
     with _on(stream):
         dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
         dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
         dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-        if dq.shape != q.shape or dk.shape != k.shape or dv.shape != v.shape:
-            raise ValueError("dq, dk and dv must have the shapes of q, k and v")
-        sh.o, sh.d_o = _strides(out, "out"), _strides(dout, "dout")
-        sh.dq, sh.dk, sh.dv = _strides(dq, "dq"), _strides(dk, "dk"), _strides(dv, "dv")
+        sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix,
+                    {"o": out, "d_o": dout, "dq": dq}, {"dk": dk, "dv": dv})
         workspace = _scratch(L.lora_attention_workspace_bytes(ctypes.byref(sh), 1), q, workspace)
-    _lib.check(L.lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
-                                    _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                                    _ptr(workspace), _size(workspace), _stream_ptr(stream)),
-               "lora_attention_bwd")
+    st = L.lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                              _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
+                              _size(workspace), _stream_ptr(stream))
+    if st:
+        _lib.check(st, "lora_attention_bwd")
     return dq, dk, dv
 
 
@@ -142,21 +155,33 @@ def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, s
     [batch, positions, k_heads, dim].  Returns o like q; zero where the length is."""
     if q.dim() != 3:
         raise ValueError("q must be [batch, q_heads, dim]")
-    sh = _shape(q.unsqueeze(1), k_cache, v_cache, scale, False, softcap, slopes, None, None)
     L = _lib.lib()
-    n = _word(lengths, torch.int32, "lengths", (q.shape[0],))
     with _on(stream):
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if out.shape != q.shape:
-            raise ValueError(f"out {tuple(out.shape)} is not {tuple(q.shape)}")
-        sh.o = _strides(out.unsqueeze(1), "out")
-        workspace = _scratch(L.lora_attention_token_workspace_bytes(ctypes.byref(sh)), q,
-                             workspace)
-    _lib.check(L.lora_attention_token(ctypes.byref(sh), _ptr(q), _ptr(k_cache), _ptr(v_cache), n,
-                                      _ptr(out), _ptr(workspace), _size(workspace),
-                                      _stream_ptr(stream)), "lora_attention_token")
+        key = ("token", _layout(q), _layout(k_cache), _layout(v_cache), _layout(lengths), scale,
+               softcap, _layout(slopes), _layout(out))
+        sh, need = _block(key, lambda: _make_token(q, k_cache, v_cache, lengths, scale, softcap,
+                                                   slopes, out))
+        if slopes is not None:
+            sh = _lib.AttentionShape.from_buffer_copy(sh)
+            sh.slopes = _ptr(slopes)
+        workspace = _scratch(need, q, workspace)
+    st = L.lora_attention_token(ctypes.byref(sh), _ptr(q), _ptr(k_cache), _ptr(v_cache),
+                                _ptr(lengths), _ptr(out), _ptr(workspace), _size(workspace),
+                                _stream_ptr(stream))
+    if st:
+        _lib.check(st, "lora_attention_token")
     return out
+
+
+def _make_token(q, k_cache, v_cache, lengths, scale, softcap, slopes, out):
+    if out.shape != q.shape:
+        raise ValueError(f"out {tuple(out.shape)} is not {tuple(q.shape)}")
+    _check_word(lengths, torch.int32, "lengths", (q.shape[0],))
+    sh = _make_shape(q.unsqueeze(1), k_cache, v_cache, scale, False, softcap, slopes, None, None,
+                     None, {"o": out.unsqueeze(1)}, {})
+    return sh, _lib.lib().lora_attention_token_workspace_bytes(ctypes.byref(sh))
 
 
 def _fit(t):

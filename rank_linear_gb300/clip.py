@@ -46,6 +46,7 @@ class GradClip:
         _lib.check(L.lora_clip_plan_build(table, len(self.grads), image.data_ptr(), self.bytes),
                    "lora_clip_plan_build")
         self.plan = image.to(device if device is not None else torch.device("cuda"))
+        self.device, self._at = self.plan.device, self.plan.data_ptr()
 
     @staticmethod
     def _largest(norm_type) -> int:
@@ -53,26 +54,31 @@ class GradClip:
             return int(norm_type == math.inf)
         raise ValueError(f"norm_type = {norm_type} is not 2 or inf")
 
-    def _norm_out(self, norm):
+    def _norm_out(self, norm, stream):
         if norm is None:
-            return torch.empty((), dtype=torch.float32, device=self.plan.device)
-        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != self.plan.device:
+            if stream is not None:
+                with torch.cuda.stream(stream):
+                    return torch.empty((), dtype=torch.float32, device=self.device)
+            return torch.empty((), dtype=torch.float32, device=self.device)
+        if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != self.device:
             raise ValueError("norm must be one float32 on the gradients' device")
         return norm
 
     def norm(self, *, norm_type: float = 2.0, norm=None, stream=None):
         """The global norm (a device scalar); nothing is scaled."""
-        norm = self._norm_out(norm)
-        _lib.check(_lib.lib().lora_clip_norm(self.plan.data_ptr(), self.bytes,
-                                             self._largest(norm_type), norm.data_ptr(),
-                                             _stream_ptr(stream)), "lora_clip_norm")
+        norm = self._norm_out(norm, stream)
+        st = _lib.lib().lora_clip_norm(self._at, self.bytes, self._largest(norm_type),
+                                       norm.data_ptr(), _stream_ptr(stream))
+        if st:
+            _lib.check(st, "lora_clip_norm")
         return norm
 
     def clip(self, max_norm: float, *, norm_type: float = 2.0, norm=None, stream=None):
         """Scales every gradient by min(1, max_norm / (norm + 1e-6)); returns the
         norm before it (a device scalar)."""
-        norm = self._norm_out(norm)
-        _lib.check(_lib.lib().lora_clip(self.plan.data_ptr(), self.bytes, float(max_norm),
-                                        self._largest(norm_type), norm.data_ptr(),
-                                        _stream_ptr(stream)), "lora_clip")
+        norm = self._norm_out(norm, stream)
+        st = _lib.lib().lora_clip(self._at, self.bytes, float(max_norm), self._largest(norm_type),
+                                  norm.data_ptr(), _stream_ptr(stream))
+        if st:
+            _lib.check(st, "lora_clip")
         return norm

@@ -762,22 +762,25 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   }
 }
 
-template <class F>
-cudaError_t start(F *kernel, uint32_t smem, int64_t grid, const Params &p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p);
-}
 template <int DH, bool CAP, bool BIAS>
 cudaError_t start_dq(const Params &p, cudaStream_t s) {
-  return start(k_attn_dq<DH, CAP, BIAS>, DqLayout<DH>::kAsked + sizeof(DqTail) + 1024,
-               int64_t(p.a.B) * p.a.Hq * ((p.a.Sq + kTile - 1) / kTile), p, s);
+  constexpr size_t smem = DqLayout<DH>::kAsked + sizeof(DqTail) + 1024;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k_attn_dq<DH, CAP, BIAS>, smem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = int64_t(p.a.B) * p.a.Hq * ((p.a.Sq + kTile - 1) / kTile);
+  return launch_pdl(k_attn_dq<DH, CAP, BIAS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                    smem, s, p);
 }
 template <int DH, bool CAP, bool BIAS>
 cudaError_t start_dkv(const Params &p, cudaStream_t s) {
-  return start(k_attn_dkv<DH, CAP, BIAS>, DkvLayout<DH>::kAsked,
-               int64_t(p.a.B) * p.a.Hk * ((p.a.Sk + kTile - 1) / kTile), p, s);
+  constexpr size_t smem = DkvLayout<DH>::kAsked;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k_attn_dkv<DH, CAP, BIAS>, smem, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = int64_t(p.a.B) * p.a.Hk * ((p.a.Sk + kTile - 1) / kTile);
+  return launch_pdl(k_attn_dkv<DH, CAP, BIAS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+                    smem, s, p);
 }
 
 }  // namespace

@@ -441,8 +441,8 @@ template <int DH, bool CAP, bool BIAS>
 cudaError_t launch(const Params &p, cudaStream_t s) {
   const size_t smem = Layout<DH>::kBytes + sizeof(Tail) + 1024;
   auto *kernel = k_attn_fwd<DH, CAP, BIAS>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
   const int64_t grid = int64_t(p.a.B) * p.a.Hq * ((p.a.Sq + 2 * kTile - 1) / (2 * kTile));
   return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p);

@@ -2,12 +2,14 @@
 //
 // One pass over q and k, bound by HBM (or by the launch where the tokens are
 // few).  The angles are not read from a table: position * turns modulo 2^64
-// is the angle's exact fraction of a turn.  A block takes a few tokens: it
-// asks for its first vectors, turns the positions into cosines and sines in
-// shared memory meanwhile (once for all heads), and passes over its heads in
-// items of two vectors.  (With the angles in each thread's registers for
-// eight heads, 124 registers and little in flight: 54 us instead of 17 at
-// 4096 tokens x 40 heads of 128, bf16.)
+// is the angle's exact fraction of a turn.  A block takes a few neighbouring
+// tokens: its warps ask for their first heads, form the cosines and sines of
+// all its tokens in shared memory meanwhile, and pass over the heads side by
+// side, a lane keeping its place in the head.  Measured at 4096 tokens x 40
+// heads of 128 in bf16, one pass: angles in registers of threads that turn
+// eight heads 54 us; items divided among threads 20 us (300 instructions an
+// item); a token to a warp 17 us, but in fp32 141 us where the warps of a
+// block side by side take 120 us (5461 x 3 tokens x 48 heads).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -19,19 +21,7 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256;
-
-// n / d for n, d < 2^16: mul = ceil(2^32 / d).
-struct Divide {
-  uint32_t d, mul;
-  __device__ __forceinline__ int by(int n) const {
-    return d == 1 ? n : static_cast<int>(__umulhi(static_cast<uint32_t>(n), mul));
-  }
-};
-Divide divide(int d) {
-  return {static_cast<uint32_t>(d),
-          static_cast<uint32_t>(((uint64_t(1) << 32) + d - 1) / static_cast<uint64_t>(d))};
-}
+constexpr int kWarps = 8;
 
 struct RotaryArgs {
   const void *in[2];
@@ -41,11 +31,13 @@ struct RotaryArgs {
   int64_t ps[2];
   const uint64_t *turns;
   int64_t seq, all_tokens;
-  int q_heads, heads, dim, rot;
-  int rot_chunks, chunks;  // of a head: VEC pairs each; then 2 VEC copied elements each
-  int tokens;              // of a block
-  Divide by_chunks, by_heads;
-  int interleaved, pos64;
+  int heads[2], dim, rot;
+  // A head is rot_chunks chunks of VEC pairs, then chunks of 2 VEC copied
+  // elements; the lanes take lane_heads heads at once (or 32 chunks of one).
+  int rot_chunks, chunks, lane_heads;
+  int groups[2];    // of lane_heads heads of q, of k
+  int tokens;       // of a block
+  int pos64;
   float mag, sin_sign;
 };
 
@@ -67,121 +59,188 @@ struct alignas(sizeof(T) * VEC) Pack {
   T v[VEC];
 };
 
-// An item: one chunk (VEC pairs, or up to 2 VEC copied elements) of one head
-// of one token, as two vectors.
+// Cosines and sines of the VEC pairs of a lane's two vectors x and y.
+template <int VEC>
+struct Angles {
+  float c[VEC], s[VEC];
+};
+// Turns the pairs (x[e], y[e]); with NEIGHBOURS those of neighbours in x, then
+// in y (one element each: x and y are the pair).
+template <class T, int VEC, bool NEIGHBOURS>
+__device__ __forceinline__ void turn(Pack<T, VEC> &x, Pack<T, VEC> &y, const Angles<VEC> &a) {
+  if constexpr (sizeof(T) == 2 && VEC == 8) {  // bf16, two elements a word
+    uint32_t *xw = reinterpret_cast<uint32_t *>(x.v), *yw = reinterpret_cast<uint32_t *>(y.v);
+    auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+    auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+    auto pack = [](float u, float v) {
+      const __nv_bfloat162 p = __floats2bfloat162_rn(u, v);
+      return *reinterpret_cast<const uint32_t *>(&p);
+    };
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float x0 = lo(xw[i]), x1 = hi(xw[i]), y0 = lo(yw[i]), y1 = hi(yw[i]);
+      if constexpr (NEIGHBOURS) {
+        const float cx = a.c[i], sx = a.s[i], cy = a.c[4 + i], sy = a.s[4 + i];
+        xw[i] = pack(fmaf(x0, cx, -(x1 * sx)), fmaf(x1, cx, x0 * sx));
+        yw[i] = pack(fmaf(y0, cy, -(y1 * sy)), fmaf(y1, cy, y0 * sy));
+      } else {
+        const float c0 = a.c[2 * i], s0 = a.s[2 * i], c1 = a.c[2 * i + 1], s1 = a.s[2 * i + 1];
+        xw[i] = pack(fmaf(x0, c0, -(y0 * s0)), fmaf(x1, c1, -(y1 * s1)));
+        yw[i] = pack(fmaf(y0, c0, x0 * s0), fmaf(y1, c1, x1 * s1));
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      constexpr bool kWithin = NEIGHBOURS && VEC > 1;
+      T &xe = !kWithin ? x.v[e] : 2 * e < VEC ? x.v[2 * e] : y.v[2 * e - VEC];
+      T &ye = !kWithin ? y.v[e] : 2 * e + 1 < VEC ? x.v[2 * e + 1] : y.v[2 * e + 1 - VEC];
+      const float xf = to_f(xe), yf = to_f(ye);
+      xe = from_f<T>(fmaf(xf, a.c[e], -(yf * a.s[e])));
+      ye = from_f<T>(fmaf(yf, a.c[e], xf * a.s[e]));
+    }
+  }
+}
+
+// The block's cosines and sines, an angle a thread.
+template <class F>
+__device__ __forceinline__ void form_angles(const RotaryArgs &a, float *shared, int tokens, F place) {
+  const int half = a.rot / 2;
+#pragma unroll 1
+  for (int i = threadIdx.x; i < tokens * half; i += 32 * kWarps) {
+    const int tk = i / half, pair = i - tk * half;
+    unsigned b, s;
+    place(tk, b, s);
+    const int64_t at = b * a.ps[0] + s * a.ps[1];
+    const uint64_t p = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t *>(a.pos)[at])
+                               : static_cast<uint64_t>(static_cast<int64_t>(
+                                     static_cast<const int32_t *>(a.pos)[at]));
+    // the turn's fraction in [-1/2, 1/2) as a signed 64-bit fraction, rounded
+    // once to 24 bits; sincospi takes half turns
+    const int64_t frac = static_cast<int64_t>(p * a.turns[pair]);
+    float sv, cv;
+    sincospif(__ll2float_rn(frac) * 0x1p-63f, &sv, &cv);
+    shared[tk * a.rot + pair] = cv * a.mag;
+    shared[tk * a.rot + half + pair] = sv * (a.mag * a.sin_sign);
+  }
+}
+
 template <class T, int VEC, bool NEIGHBOURS>  // pairs (2i, 2i + 1), else (i, i + rot / 2)
-__global__ void __launch_bounds__(kThreads, 4) k_rotary(const RotaryArgs a) {
+__global__ void __launch_bounds__(32 * kWarps, 4) k_rotary(const RotaryArgs a) {
   using P = Pack<T, VEC>;
-  extern __shared__ float angles[];  // [tokens][2][rot / 2]: cosines, sines
+  extern __shared__ float shared[];  // [tokens][cosines, sines][rot / 2]
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, half = a.rot / 2;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t token0 = static_cast<int64_t>(blockIdx.x) * a.tokens;
-  const int tokens = static_cast<int>(
-      a.all_tokens - token0 < a.tokens ? a.all_tokens - token0 : a.tokens);
-  const int half = a.rot / 2, items = tokens * a.heads * a.chunks;
-  const int64_t b0 = token0 / a.seq, s0 = token0 - b0 * a.seq;
+  const unsigned token0 = blockIdx.x * static_cast<unsigned>(a.tokens);
+  const int tokens = static_cast<int>(min(static_cast<unsigned>(a.tokens),
+                                          static_cast<unsigned>(a.all_tokens) - token0));
+  const unsigned seq = static_cast<unsigned>(a.seq), b0 = token0 / seq, s0 = token0 - b0 * seq;
+  auto place = [&](int tk, unsigned &b, unsigned &s) {  // a block may cross sequences
+    b = b0;
+    s = s0 + tk;
+    while (s >= seq) {
+      s -= seq;
+      ++b;
+    }
+  };
+  const int groups = a.groups[0] + a.groups[1], units = tokens * groups;
 
-  constexpr int U = 2;  // items of a thread in flight
-  bool angles_there = false;
-  for (int base = threadIdx.x; base - static_cast<int>(threadIdx.x) < items; base += U * kThreads) {
-    P x[U], y[U];
-    T *dst[U];
-    int chunk[U], tok[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int item = base + u * kThreads;
-      chunk[u] = -1;
-      if (item < items) {
-        const int row = a.by_chunks.by(item), c = item - row * a.chunks;
-        const int tk = a.by_heads.by(row), h = row - tk * a.heads;
-        int64_t b = b0, s = s0 + tk;
-        while (s >= a.seq) {  // a block may cross into the next sequences
-          s -= a.seq;
-          ++b;
-        }
-        const int t = h >= a.q_heads, ht = h - (t ? a.q_heads : 0);
-        const T *src = static_cast<const T *>(a.in[t]) + b * a.is[t][0] + s * a.is[t][1] +
-                       ht * a.is[t][2];
-        dst[u] = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1] + ht * a.os[t][2];
-        chunk[u] = c;
-        tok[u] = tk;
-        const bool turn = c < a.rot_chunks;
-        const int e0 = !turn ? a.rot + (c - a.rot_chunks) * 2 * VEC
-                             : NEIGHBOURS ? 2 * VEC * c : VEC * c;
-        const int e1 = turn && !NEIGHBOURS ? e0 + half : e0 + VEC;
-        x[u] = *reinterpret_cast<const P *>(src + e0);
-        if (turn || e1 < a.dim) y[u] = *reinterpret_cast<const P *>(src + e1);
-      }
+  constexpr int U = VEC == 8 ? 2 : 4;  // head groups of a warp in flight
+  bool formed = false;
+  // chunks of a head beyond 32 take further passes
+  for (int c0 = 0; c0 < a.chunks; c0 += 32) {
+    const int lane_head = a.chunks > 32 ? 0 : lane / a.chunks;
+    const int c = a.chunks > 32 ? c0 + lane : lane - lane_head * a.chunks;
+    const bool turned = c < a.rot_chunks;
+    // its two vectors: the same places in either layout of the pairs
+    const bool apart = NEIGHBOURS && VEC == 1;
+    const int copied = c - a.rot_chunks, copies = a.chunks - a.rot_chunks;
+    const int e0 = !turned ? a.rot + VEC * copied : apart ? 2 * c : VEC * c;
+    const int e1 = e0 + (!turned ? VEC * copies : apart ? 1 : half);
+    const bool on = lane_head < a.lane_heads && c < a.chunks, two = on && e1 < a.dim;
+    // the angles' places: NEIGHBOURS, those of x and of y a quarter of rot apart
+    constexpr int kHalf = VEC > 1 ? VEC / 2 : 1;
+    const int p0 = NEIGHBOURS && VEC > 1 ? e0 / 2 : c * VEC;
+    const int p1 = NEIGHBOURS && VEC > 1 ? e1 / 2 : p0 + kHalf;
+
+    int tk = 0, g = warp;  // unit: a head group of a token
+    while (g >= groups) {
+      g -= groups;
+      ++tk;
     }
-    if (!angles_there) {
-      for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
-        const int tk = i / half, pair = i - tk * half;
-        int64_t b = b0, s = s0 + tk;
-        while (s >= a.seq) {
-          s -= a.seq;
-          ++b;
+    for (int unit = warp; unit < units; unit += U * kWarps) {
+      P x[U], y[U];
+      T *dst[U];
+      int token[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const int t = g >= a.groups[0], h = (g - (t ? a.groups[0] : 0)) * a.lane_heads + lane_head;
+        token[i] = on && h < a.heads[t] && tk < tokens ? tk : -1;
+        if (token[i] >= 0) {
+          unsigned b, s;
+          place(tk, b, s);
+          const T *src = static_cast<const T *>(a.in[t]) + b * a.is[t][0] + s * a.is[t][1] +
+                         h * a.is[t][2];
+          dst[i] = static_cast<T *>(a.out[t]) + b * a.os[t][0] + s * a.os[t][1] + h * a.os[t][2];
+          x[i] = *reinterpret_cast<const P *>(src + e0);
+          if (two) y[i] = *reinterpret_cast<const P *>(src + e1);
         }
-        const int64_t at = b * a.ps[0] + s * a.ps[1];
-        const uint64_t p = a.pos64 ? static_cast<uint64_t>(static_cast<const int64_t *>(a.pos)[at])
-                                   : static_cast<uint64_t>(static_cast<int64_t>(
-                                         static_cast<const int32_t *>(a.pos)[at]));
-        // the turn's fraction in [-1/2, 1/2) as a signed 64-bit fraction,
-        // rounded once to 24 bits; sincospi takes half turns
-        const int64_t frac = static_cast<int64_t>(p * a.turns[pair]);
-        float sv, cv;
-        sincospif(__ll2float_rn(frac) * 0x1p-63f, &sv, &cv);
-        angles[(2 * tk) * half + pair] = cv * a.mag;
-        angles[(2 * tk + 1) * half + pair] = sv * (a.mag * a.sin_sign);
+        g += kWarps;
+        while (g >= groups) {
+          g -= groups;
+          ++tk;
+        }
       }
+      if (!formed) {
+        form_angles(a, shared, tokens, place);
+        __syncthreads();
+        formed = true;
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i)
+        if (token[i] >= 0) {
+          if (turned) {
+            const float *cosines = shared + token[i] * a.rot, *sines = cosines + half;
+            Angles<VEC> angles;
+            if constexpr (VEC > 1) {
+              using H = Pack<float, kHalf>;
+              *reinterpret_cast<H *>(angles.c) = *reinterpret_cast<const H *>(cosines + p0);
+              *reinterpret_cast<H *>(angles.c + kHalf) = *reinterpret_cast<const H *>(cosines + p1);
+              *reinterpret_cast<H *>(angles.s) = *reinterpret_cast<const H *>(sines + p0);
+              *reinterpret_cast<H *>(angles.s + kHalf) = *reinterpret_cast<const H *>(sines + p1);
+            } else {
+              angles.c[0] = cosines[p0];
+              angles.s[0] = sines[p0];
+            }
+            turn<T, VEC, NEIGHBOURS>(x[i], y[i], angles);
+          }
+          *reinterpret_cast<P *>(dst[i] + e0) = x[i];
+          if (two) *reinterpret_cast<P *>(dst[i] + e1) = y[i];
+        }
+    }
+    if (!formed) {  // a warp without a unit helps all the same
+      form_angles(a, shared, tokens, place);
       __syncthreads();
-      angles_there = true;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int c = chunk[u];
-      if (c < 0) continue;
-      const bool turn = c < a.rot_chunks;
-      const int e0 = !turn ? a.rot + (c - a.rot_chunks) * 2 * VEC
-                           : NEIGHBOURS ? 2 * VEC * c : VEC * c;
-      const int e1 = turn && !NEIGHBOURS ? e0 + half : e0 + VEC;
-      if (turn) {
-        const float *cs = angles + 2 * tok[u] * half + VEC * c, *sn = cs + half;
-        const Pack<float, VEC> cv = *reinterpret_cast<const Pack<float, VEC> *>(cs);
-        const Pack<float, VEC> sv = *reinterpret_cast<const Pack<float, VEC> *>(sn);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          // NEIGHBOURS: element 2e and 2e + 1 of the run x, y
-          T &xe = !NEIGHBOURS ? x[u].v[e] : 2 * e < VEC ? x[u].v[2 * e] : y[u].v[2 * e - VEC];
-          T &ye = !NEIGHBOURS       ? y[u].v[e]
-                  : 2 * e + 1 < VEC ? x[u].v[2 * e + 1]
-                                    : y[u].v[2 * e + 1 - VEC];
-          const float xf = to_f(xe), yf = to_f(ye);
-          xe = from_f<T>(fmaf(xf, cv.v[e], -(yf * sv.v[e])));
-          ye = from_f<T>(fmaf(yf, cv.v[e], xf * sv.v[e]));
-        }
-      }
-      *reinterpret_cast<P *>(dst[u] + e0) = x[u];
-      if (turn || e1 < a.dim) *reinterpret_cast<P *>(dst[u] + e1) = y[u];
+      formed = true;
     }
   }
 }
 
 template <class T, int VEC>
-cudaError_t launch_rotary(RotaryArgs &a, bool copy_tail, int sms, cudaStream_t s) {
+cudaError_t launch_rotary(RotaryArgs &a, bool neighbours, bool copy_tail, int sms, cudaStream_t s) {
   a.rot_chunks = a.rot / 2 / VEC;
   a.chunks = a.rot_chunks + (copy_tail ? (a.dim - a.rot + 2 * VEC - 1) / (2 * VEC) : 0);
-  // tokens of a block: up to 4, fewer while that would leave SMs without a
-  // block or a block with more items than its 16-bit divisions take
-  a.tokens = 4;
-  while (a.tokens > 1 && (a.all_tokens < int64_t(a.tokens) * 2 * sms ||
-                          int64_t(a.tokens) * a.heads * a.chunks > 65535))
+  a.lane_heads = a.chunks > 32 ? 1 : 32 / a.chunks;
+  for (int t = 0; t < 2; ++t) a.groups[t] = (a.heads[t] + a.lane_heads - 1) / a.lane_heads;
+  // tokens of a block: an angle for each thread or so, fewer tokens while that
+  // would leave SMs idle
+  a.tokens = 8;
+  while (a.tokens > 1 && (a.tokens * a.rot > 1024 || a.all_tokens < int64_t(a.tokens) * 4 * sms))
     a.tokens /= 2;
-  if (int64_t(a.heads) * a.chunks > 65535) return cudaErrorInvalidValue;
-  a.by_chunks = divide(a.chunks);
-  a.by_heads = divide(a.heads);
   const int64_t blocks = (a.all_tokens + a.tokens - 1) / a.tokens;
-  return launch_pdl(a.interleaved ? k_rotary<T, VEC, true> : k_rotary<T, VEC, false>,
-                    dim3(static_cast<unsigned>(blocks)), dim3(kThreads),
+  return launch_pdl(neighbours ? k_rotary<T, VEC, true> : k_rotary<T, VEC, false>,
+                    dim3(static_cast<unsigned>(blocks)), dim3(32 * kWarps),
                     size_t(a.tokens) * a.rot * sizeof(float), s, a);
 }
 
@@ -272,27 +331,22 @@ lora_status_t lora_rotary(const lora_rotary_t *sh, const void *q, const void *k,
   a.pos64 = sh->position_bits == 64;
   a.turns = turns;
   a.seq = sh->seq;
-  a.q_heads = sh->q_heads;
-  a.heads = sh->q_heads + sh->k_heads;
+  a.heads[0] = sh->q_heads;
+  a.heads[1] = sh->k_heads;
   a.dim = sh->dim;
   a.rot = sh->rot;
-  a.interleaved = sh->interleaved;
   a.mag = sh->magnitude;
   a.sin_sign = sh->inverse ? -1.f : 1.f;
   a.all_tokens = tokens;
-  // a token's items, one pair (or copied pair) each at the most
-  if (int64_t(a.heads) * ((sh->dim + 1) / 2 + 1) > 65535)
-    return fail(LORA_ERR_UNSUPPORTED, "%d heads of %d: too many elements in a token", a.heads,
-                sh->dim);
   DevInfo di;
   LORA_TRY(device_info(di));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return run(LORA_K_ROTARY, st, "rotary", [&] {
     if (dtype == LORA_BF16)
-      return wide ? launch_rotary<__nv_bfloat16, 8>(a, copy_tail, di.sms, st)
-                  : launch_rotary<__nv_bfloat16, 1>(a, copy_tail, di.sms, st);
-    return wide ? launch_rotary<float, 4>(a, copy_tail, di.sms, st)
-                : launch_rotary<float, 1>(a, copy_tail, di.sms, st);
+      return wide ? launch_rotary<__nv_bfloat16, 8>(a, sh->interleaved != 0, copy_tail, di.sms, st)
+                  : launch_rotary<__nv_bfloat16, 1>(a, sh->interleaved != 0, copy_tail, di.sms, st);
+    return wide ? launch_rotary<float, 4>(a, sh->interleaved != 0, copy_tail, di.sms, st)
+                : launch_rotary<float, 1>(a, sh->interleaved != 0, copy_tail, di.sms, st);
   });
 }
 

@@ -47,8 +47,9 @@ def _buffer(nbytes: int, device) -> torch.Tensor:
 
 
 def _stream_ptr(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream or None
+    if stream is None:  # the current one's handle, without making an object of it
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device()) or None
+    return stream.cuda_stream or None
 
 
 def forward(X, W, A, B, alpha: float, *, Y=None, saved=None, workspace=None, stream=None):

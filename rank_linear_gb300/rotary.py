@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import _lib
-from .lora import _dtype_code, _stream_ptr
+from .lora import _dtype_code, _ptr, _stream_ptr
 
 
 class RotaryFrequencies:
@@ -29,10 +29,7 @@ class RotaryFrequencies:
                                                 words), "lora_rotary_turns")
         signed = [w - (1 << 64) if w >> 63 else w for w in words[:n]]
         self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
-
-    @property
-    def rot(self) -> int:
-        return 2 * len(self.radians)
+        self.rot = 2 * n
 
 
 def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling: dict | None = None,
@@ -122,20 +119,35 @@ def _on(stream):
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
-def _turn(q, k, positions, freqs, interleaved, inverse, q_out, k_out, stream):
+def _layout(t):
+    return None if t is None else (t.shape, t.stride(), t.dtype, t.device)
+
+
+# Argument blocks by the layouts that they describe (sizes, strides, types;
+# no addresses): checking and filling one takes longer than a small launch.
+_blocks: dict = {}
+_MOST_BLOCKS = 4096
+
+
+def _block(key, make):
+    block = _blocks.get(key)
+    if block is None:
+        block = make()
+        if len(_blocks) >= _MOST_BLOCKS:
+            _blocks.clear()
+        _blocks[key] = block
+    return block
+
+
+def _make_shape(q, k, positions, freqs, interleaved, inverse, q_out, k_out):
     first = q if q is not None else k
-    if first is None:
-        raise ValueError("q and k are both None")
     sh = _lib.RotaryShape()
     lead = first.shape[:-2]
+    if len(lead) not in (1, 2):
+        raise ValueError("q and k must be [batch, seq, heads, dim] or [tokens, heads, dim]")
     sh.batch, sh.seq = (1, lead[0]) if len(lead) == 1 else lead
     sh.dim, sh.rot = first.shape[-1], freqs.rot
     sh.interleaved, sh.inverse, sh.magnitude = int(interleaved), int(inverse), freqs.magnitude
-    with _on(stream):
-        if q is not None and q_out is None:
-            q_out = _empty_like(q)
-        if k is not None and k_out is None:
-            k_out = _empty_like(k)
     for name, x, out in (("q", q, q_out), ("k", k, k_out)):
         if x is None:
             continue
@@ -157,10 +169,27 @@ def _turn(q, k, positions, freqs, interleaved, inverse, q_out, k_out, stream):
         raise ValueError(f"positions {tuple(positions.shape)} do not fit tokens {tuple(lead)}")
     if freqs.turns.device != first.device:
         raise ValueError("the frequencies are on another device")
-    ptr = lambda t: None if t is None else t.data_ptr() or None
-    _lib.check(_lib.lib().lora_rotary(ctypes.byref(sh), ptr(q), ptr(k), ptr(positions),
-                                      ptr(freqs.turns), _dtype_code(first), ptr(q_out),
-                                      ptr(k_out), _stream_ptr(stream)), "lora_rotary")
+    return sh, _dtype_code(first)
+
+
+def _turn(q, k, positions, freqs, interleaved, inverse, q_out, k_out, stream):
+    if q is None and k is None:
+        raise ValueError("q and k are both None")
+    if (q is not None and q_out is None) or (k is not None and k_out is None):
+        with _on(stream):
+            if q is not None and q_out is None:
+                q_out = _empty_like(q)
+            if k is not None and k_out is None:
+                k_out = _empty_like(k)
+    key = (_layout(q), _layout(k), _layout(positions), _layout(q_out), _layout(k_out),
+           freqs.rot, freqs.magnitude, freqs.turns.device, interleaved, inverse)
+    sh, dtype = _block(key, lambda: _make_shape(q, k, positions, freqs, interleaved, inverse,
+                                                q_out, k_out))
+    st = _lib.lib().lora_rotary(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(positions),
+                                _ptr(freqs.turns), dtype, _ptr(q_out), _ptr(k_out),
+                                _stream_ptr(stream))
+    if st:
+        _lib.check(st, "lora_rotary")
     return q_out, k_out
 
 
