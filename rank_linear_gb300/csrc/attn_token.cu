@@ -13,6 +13,12 @@
 //     elements 64 e + 8 (lane / 4) + 0..7; word j of two keys, byte-permuted
 //     into pairs of keys, is rows 2j and 2j + 1 of its eight.
 //
+// The keys of the next step are asked for before the present one's softmax, its
+// values at the start of the step: with 3 blocks an SM (168 registers, nothing
+// spilled) that keeps HBM busy.  (Measured and not kept: 4 blocks of 128
+// registers 118 us for the ragged batch where 3 take 95; L2 prefetches 1 to 6
+// steps ahead, values a step ahead in registers, all slower.)
+//
 // P is transposed between the two by movmatrix.  The running maximum is
 // followed only when some score exceeds it by 2^8 (a vote instead of
 // shuffles); sums in fp32, P rounded to bf16.
@@ -58,7 +64,7 @@ __device__ __forceinline__ uint4 load_if(bool there, const __nv_bfloat16 *p) {
 }
 
 template <int NB, bool CAP, bool BIAS>  // NB blocks of 64 elements of a head
-__global__ void __launch_bounds__(32 * kWarps, 4) k_attn_token(const Params p) {
+__global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
   const AttnArgs &a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int quad = lane / 4, part = lane % 4;
@@ -121,24 +127,11 @@ __global__ void __launch_bounds__(32 * kWarps, 4) k_attn_token(const Params p) {
     }
   };
 
-  // lines of 128 bytes of a step's K (V) rows, one a lane, towards L2
-  auto prefetch = [&](int key0) {
-    const int key = key0 + (NB == 2 ? lane / 2 : lane % 16);
-    const int e = NB == 2 ? lane % 2 * 64 : 0;
-    if (key >= to || e >= a.D) return;
-    if (NB == 2 || lane < 16)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(kp - 8 * part + key * a.sk[1] + e));
-    if (NB == 2 || lane >= 16)
-      asm volatile("prefetch.global.L2 [%0];" ::"l"(vp - 8 * quad + key * a.sv[1] + e));
-  };
-  constexpr int kStep = kWarps * kKeys, kAhead = 3;
+  constexpr int kStep = kWarps * kKeys;
   int key0 = from + warp * kKeys;
   if (key0 < to) load_k(key0);
-#pragma unroll
-  for (int i = 1; i < kAhead; ++i) prefetch(key0 + i * kStep);
   for (; key0 < to; key0 += kStep) {
     load_v(key0);
-    prefetch(key0 + kAhead * kStep);
     float s[4] = {0.f, 0.f, 0.f, 0.f};  // keys quad, quad + 8 x heads 2 part, 2 part + 1
 #pragma unroll
     for (int c = 0; c < 2 * NB; ++c) {
@@ -345,19 +338,21 @@ cudaError_t launch(const Params &p, cudaStream_t s) {
 
 }  // namespace
 
-// Chunks of the cache's length.  A GB300's 152 SMs hold 4 blocks each: enough
-// chunks for about 6 rounds of them (ragged batches leave some without work,
-// and the last round is rarely full), of 256 keys at the least where one round
-// is full with those, else of 64 (a step of the block).
+// Chunks of the cache's length.  A GB300's 152 SMs hold 3 blocks each: enough
+// chunks for two rounds of them, of 256 keys at the least where one round is
+// full with those, else of 64 (a step of the block).  Measured, rounds 1 / 2 /
+// 4 / 8: 80 / 83 / 87 / 95 us for one sequence of 131071 positions, 152 / 95 /
+// 102 / 99 us for 32 ragged ones (the shortest a tenth of 8192), which leave
+// blocks of one round without work.
 AttnTokenPlan attn_token_plan(int64_t B, int64_t Hk, int group, int64_t Sk) {
   AttnTokenPlan t;
   t.head_chunks = (group + kHeads - 1) / kHeads;
-  const int64_t rows = B * Hk * t.head_chunks, places = 152 * 4;
+  const int64_t rows = B * Hk * t.head_chunks, places = 152 * 3;
   auto chunk_of = [&](int64_t blocks) {
     const int64_t splits = rows > 0 && blocks > rows ? blocks / rows : 1;
     return (Sk + splits * 64 - 1) / (splits * 64) * 64;
   };
-  int64_t chunk = chunk_of(6 * places);
+  int64_t chunk = chunk_of(2 * places);
   if (chunk < 256) chunk = chunk_of(places) < 256 ? chunk_of(places) : 256;
   t.chunk = static_cast<int>(chunk < 64 ? 64 : chunk);
   t.splits = static_cast<int>(Sk > 0 ? (Sk + t.chunk - 1) / t.chunk : 1);
