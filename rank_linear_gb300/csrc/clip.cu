@@ -20,7 +20,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 256, kVecs = 4;  // 16-byte vectors of a thread per 16 KB chunk
-constexpr int kBlocksPerSm = 8, kMaxBlocks = 4096;
+constexpr int kNormBlocks = 4, kClipBlocks = 6, kMaxBlocks = 4096;  // blocks of an SM
 
 struct Chunk {
   const void *in;
@@ -96,21 +96,37 @@ __device__ __forceinline__ void add_to(float &hi, float &lo, float x, float y) {
   hi = s;
 }
 
+// A chunk's vectors (of its input).
+struct Held {
+  uint4 v[kVecs];
+};
+template <int ES>
+__device__ __forceinline__ const uint4 *body_of(const Chunk &c, int &head, int &vecs) {
+  split_run<ES>(c.in, c.count, head, vecs);
+  return reinterpret_cast<const uint4 *>(static_cast<const char *>(c.in) + head * ES);
+}
+__device__ __forceinline__ void hold(const Chunk &c, Held &h) {
+  int head, vecs;
+  const uint4 *body = c.dtype == LORA_BF16 ? body_of<2>(c, head, vecs) : body_of<4>(c, head, vecs);
+  body += threadIdx.x;
+  if (vecs == kVecs * kThreads) {
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u) h.v[u] = __ldcg(body + u * kThreads);
+  } else {
+    vecs -= threadIdx.x;
+#pragma unroll
+    for (int u = 0; u < kVecs; ++u)
+      h.v[u] = u * kThreads < vecs ? __ldcg(body + u * kThreads) : make_uint4(0, 0, 0, 0);
+  }
+}
+
 template <bool BF, bool LARGEST>
-__device__ void add_chunk(const Chunk &c, Sum &acc) {
+__device__ __forceinline__ void add_chunk(const Chunk &c, const Held &h, Sum &acc) {
   constexpr int N = BF ? 8 : 4, ES = 16 / N;
   int head, vecs;
   split_run<ES>(c.in, c.count, head, vecs);
-  const uint4 *body = reinterpret_cast<const uint4 *>(static_cast<const char *>(c.in) + head * ES);
-  const int tid = threadIdx.x;
-  uint4 v[kVecs];
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const int i = tid + u * kThreads;
-    v[u] = i < vecs ? __ldcg(body + i) : make_uint4(0, 0, 0, 0);
-  }
   // the elements outside whole vectors: fewer than 2 N of them
-  const int rest = c.count - vecs * N;
+  const int tid = threadIdx.x, rest = c.count - vecs * N;
   float lone = 0.f;
   if (tid < rest) {
     const int i = tid < head ? tid : tid + vecs * N;
@@ -120,16 +136,15 @@ __device__ void add_chunk(const Chunk &c, Sum &acc) {
       lone = static_cast<const float *>(c.in)[i];
   }
   if constexpr (LARGEST) {
-    // fmaxf drops NaN: a NaN is carried over by the comparison
     float m = acc.hi;
-    auto top = [&](float x) {
+    auto top = [&](float x) {  // fmaxf would drop NaN
       x = fabsf(x);
       if (!(x <= m)) m = (m != m) ? m : x;
     };
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       float f[N];
-      unpack<BF>(v[u], f);
+      unpack<BF>(h.v[u], f);
 #pragma unroll
       for (int e = 0; e < N; ++e) top(f[e]);
     }
@@ -140,7 +155,7 @@ __device__ void add_chunk(const Chunk &c, Sum &acc) {
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       float f[N];
-      unpack<BF>(v[u], f);
+      unpack<BF>(h.v[u], f);
 #pragma unroll
       for (int e = 0; e < N; e += 2) {
         s0 = fmaf(f[e], f[e], s0);
@@ -153,13 +168,12 @@ __device__ void add_chunk(const Chunk &c, Sum &acc) {
     } else {  // all zero, far off scale, or not finite: again in fp64
       unsigned any = __float_as_uint(lone) << 1;
 #pragma unroll
-      for (int u = 0; u < kVecs; ++u) any |= v[u].x | v[u].y | v[u].z | v[u].w;
+      for (int u = 0; u < kVecs; ++u) any |= h.v[u].x | h.v[u].y | h.v[u].z | h.v[u].w;
       if (any != 0) {
         double d = static_cast<double>(lone) * lone;
+        const uint4 *body = body_of<ES>(c, head, vecs);
 #pragma unroll 1
-        for (int u = 0; u < kVecs; ++u) {
-          const int i = tid + u * kThreads;
-          if (i >= vecs) break;
+        for (int i = tid; i < vecs; i += kThreads) {
           float f[N];
           unpack<BF>(__ldcg(body + i), f);
 #pragma unroll
@@ -238,26 +252,34 @@ __device__ float join_parts(const PlanHead *head, int blocks) {
 // clipping pass does, in each of its blocks: cheaper than the ticket and one
 // block's work behind it).
 template <bool LARGEST, bool JOIN>
-__global__ void __launch_bounds__(kThreads) k_grad_norm(PlanHead *head, const Chunk *chunks,
+__global__ void __launch_bounds__(kThreads, kNormBlocks) k_grad_norm(PlanHead *head, const Chunk *chunks,
                                                         int n, float *norm) {
   __shared__ bool last;
   griddep_wait();
   griddep_launch_dependents();
   Sum sum;
+  const int step = gridDim.x;
   int i = blockIdx.x;
   if (i < n) {
-    Chunk c = load_chunk(chunks + i);
+    // a chunk's vectors are asked for before the one ahead of it is summed,
+    // its record before that
+    Chunk c = load_chunk(chunks + i), cn = c;
+    if (i + step < n) cn = load_chunk(chunks + i + step);
+    Held h, hn;
+    hold(c, h);
     while (true) {
-      const int next = i + gridDim.x;
-      Chunk cn = c;
-      if (next < n) cn = load_chunk(chunks + next);
+      Chunk c2 = cn;
+      if (i + 2 * step < n) c2 = load_chunk(chunks + i + 2 * step);
+      if (i + step < n) hold(cn, hn);
       if (c.dtype == LORA_BF16)
-        add_chunk<true, LARGEST>(c, sum);
+        add_chunk<true, LARGEST>(c, h, sum);
       else
-        add_chunk<false, LARGEST>(c, sum);
-      if (next >= n) break;
+        add_chunk<false, LARGEST>(c, h, sum);
+      i += step;
+      if (i >= n) break;
       c = cn;
-      i = next;
+      cn = c2;
+      h = hn;
     }
   }
   float2 v = join_block<LARGEST>(sum.hi, sum.lo);
@@ -289,27 +311,8 @@ __global__ void __launch_bounds__(kThreads) k_grad_norm(PlanHead *head, const Ch
   }
 }
 
-// A chunk's vectors, where input and output share their alignment.
-struct Held {
-  uint4 v[kVecs];
-};
 __device__ __forceinline__ bool aligned_alike(const Chunk &c) {
   return ((reinterpret_cast<uintptr_t>(c.in) ^ reinterpret_cast<uintptr_t>(c.out)) & 15) == 0;
-}
-__device__ __forceinline__ void hold(const Chunk &c, Held &h) {
-  if (!aligned_alike(c)) return;
-  int head, vecs;
-  if (c.dtype == LORA_BF16)
-    split_run<2>(c.in, c.count, head, vecs);
-  else
-    split_run<4>(c.in, c.count, head, vecs);
-  const uint4 *src = reinterpret_cast<const uint4 *>(
-      static_cast<const char *>(c.in) + head * (c.dtype == LORA_BF16 ? 2 : 4));
-#pragma unroll
-  for (int u = 0; u < kVecs; ++u) {
-    const int i = threadIdx.x + u * kThreads;
-    if (i < vecs) h.v[u] = __ldcg(src + i);
-  }
 }
 
 template <bool BF>
@@ -356,7 +359,7 @@ __device__ __forceinline__ void scale_chunk(const Chunk &c, const Held &h, float
 }
 
 template <bool LARGEST>
-__global__ void __launch_bounds__(kThreads, 6) k_grad_clip(const PlanHead *head,
+__global__ void __launch_bounds__(kThreads, kClipBlocks) k_grad_clip(const PlanHead *head,
                                                            const Chunk *chunks, int n, int parts,
                                                            float max_norm, float *norm) {
   // Records and gradients do not depend on the norm pass (which let this
@@ -442,7 +445,7 @@ lora_status_t check_plan(const void *plan, size_t bytes, int largest, const floa
 }
 
 int norm_blocks(const DevInfo &di, int n) {
-  const int most = di.sms * kBlocksPerSm < kMaxBlocks ? di.sms * kBlocksPerSm : kMaxBlocks;
+  const int most = di.sms * kNormBlocks < kMaxBlocks ? di.sms * kNormBlocks : kMaxBlocks;
   return n < 1 ? 1 : n < most ? n : most;
 }
 lora_status_t norm_pass(const DevInfo &di, PlanHead *head, int n, int largest, bool join,
@@ -523,7 +526,7 @@ lora_status_t lora_clip(void *plan, size_t plan_bytes, float max_norm, int large
   if (n == 0) return norm_pass(di, head, n, largest, true, norm, st);
   LORA_TRY(norm_pass(di, head, n, largest, false, norm, st));
   const Chunk *chunks = reinterpret_cast<const Chunk *>(head + 1);
-  const int blocks = n < di.sms * 6 ? n : di.sms * 6;
+  const int blocks = n < di.sms * kClipBlocks ? n : di.sms * kClipBlocks;
   return run(LORA_K_GRAD_CLIP, st, "gradient clip", [&] {
     return launch_pdl(largest ? k_grad_clip<true> : k_grad_clip<false>, dim3(blocks),
                       dim3(kThreads), 0, st, head, chunks, n, norm_blocks(di, n), max_norm, norm);
