@@ -327,6 +327,20 @@ __device__ __forceinline__ void stage_row32(uint8_t *tile, int r, int c, const f
   }
 }
 
+// Stores 32 columns from c on (times by, as bf16) of a row of D elements.
+__device__ __forceinline__ void store_row32(__nv_bfloat16 *row, int c, int D, const float *v,
+                                            float by) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + 8 * i < D) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        w[e] = pack_bf16(v[i * 8 + 2 * e] * by, v[i * 8 + 2 * e + 1] * by);
+      *reinterpret_cast<uint4 *>(row + c + 8 * i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
 // Operand descriptors of a [128][DH] tile as TMA leaves it (128-byte swizzle,
 // boxes of 64 columns): with the head as K (K-major), or the tokens
 // (MN-major); and what K step kk of 16 adds to each.

@@ -22,20 +22,24 @@ struct AttnArgs {
   int64_t qds = 0, kds = 0;
   // documents of every 128-token tile ([batch][tiles] DocRange), with q_docs
   const int4 *q_ranges = nullptr, *k_ranges = nullptr;
+  // with documents: counters (kAttnCounters, zeroed with the ranges) that the
+  // persistent blocks take their items from
+  unsigned *counter = nullptr;
   unsigned *dev_status = nullptr;
 };
+constexpr int kAttnCounters = 2;
 
 // A [batch][token][head][dim] bf16 tensor's map: boxes of 64 elements x 128
 // tokens of one head, 128-byte swizzle, zeros outside.
 struct AttnMaps {
-  CUtensorMap q, k, v, o;
+  CUtensorMap q, k, v;
 };
 struct AttnBwdMaps {
   CUtensorMap q, k, v, d_o, dq, dk, dv;
 };
 
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
-cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, cudaStream_t s);
+cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s);
 cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
 cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
 

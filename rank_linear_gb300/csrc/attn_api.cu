@@ -114,9 +114,10 @@ lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], 
   return LORA_OK;
 }
 
-// Workspace: [document ranges of the query tiles, of the key tiles][delta].
+// Workspace: [document ranges of the query tiles, of the key tiles][item
+// counters][delta].
 struct Plan {
-  size_t q_ranges = 0, k_ranges = 0, delta = 0, bytes = 0;
+  size_t q_ranges = 0, k_ranges = 0, counter = 0, delta = 0, bytes = 0;
 };
 Plan make_plan(const lora_attention_t *p, bool backward) {
   Plan w;
@@ -126,6 +127,8 @@ Plan make_plan(const lora_attention_t *p, bool backward) {
     off += rup(size_t(p->batch) * tiles_of(p->q_len) * 16, 256);
     w.k_ranges = off;
     off += rup(size_t(p->batch) * tiles_of(p->k_len) * 16, 256);
+    w.counter = off;
+    off += 256;
   }
   if (backward) {
     w.delta = off;
@@ -155,6 +158,7 @@ lora_status_t make_ranges(AttnArgs &a, const Plan &w, void *ws, cudaStream_t st)
   if (a.q_docs == nullptr) return LORA_OK;
   a.q_ranges = reinterpret_cast<const int4 *>(at(ws, w.q_ranges));
   a.k_ranges = reinterpret_cast<const int4 *>(at(ws, w.k_ranges));
+  a.counter = reinterpret_cast<unsigned *>(at(ws, w.counter));
   return run(LORA_K_ATTN_PREP, st, "document ranges", [&] { return launch_attn_ranges(a, st); });
 }
 
@@ -198,11 +202,10 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   AttnMaps m;
   LORA_TRY(tensor_map(&m.q, q, shape->q, a, a.Sq, a.Hq, "q"));
-  LORA_TRY(tensor_map(&m.o, o, shape->o, a, a.Sq, a.Hq, "o"));
   LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
   LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
   LORA_TRY(make_ranges(a, w, workspace, st));
-  return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, m, st); });
+  return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, m, di.sms, st); });
 }
 
 lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o, const void *q,

@@ -1,13 +1,18 @@
 // attn_fwd.cu -- attention forward on the tensor cores (include/lora_attention.h).
 //
-// A CTA takes 256 queries of one head as two tiles of 128 and passes once
-// over the keys in tiles of 128: S = Q K^T into TMEM, softmax in registers (a
+// An item is 256 queries of one head, as two tiles of 128, and one pass over
+// the keys in tiles of 128: S = Q K^T into TMEM, softmax in registers (a
 // thread owns a whole row: no shuffles), P back into TMEM as bf16 over S, and
 // O += P V with P as the TMEM operand.  While the softmax of one tile runs,
 // the tensor core works for the other.  The running maximum is only followed
 // when it has moved by more than 2^8: until then P is relative to the old one
 // (at most 256, exact in fp32 sums and no worse rounded to bf16), so that O
 // in TMEM is hardly ever rescaled.
+//
+// Blocks stay (one per SM) and take item after item, so that an item's copies
+// and first scores run while the one before it is written out.  A scheduling
+// warp hands items out: in order of falling work without documents, from a
+// counter with them (their work varies).
 //
 // TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
 #include "attn.cuh"
@@ -16,11 +21,12 @@
 namespace lora {
 namespace {
 
-// Two softmax warpgroups, and one of which two warps issue the copies and the
-// MMAs.  168 registers a thread at launch; the softmax threads, which hold a
-// row of scores, take 224 and leave the others 56 (2 * 224 + 56 = 3 * 168).
+// Two softmax warpgroups, and one whose warps issue the copies, the MMAs and
+// the items.  168 registers a thread at launch; the softmax threads, which
+// hold a row of scores, take 224 and leave the others 56 (2 * 224 + 56 = 3 * 168).
 constexpr int kThreads = 384, kSoftmaxRegs = 224, kIssueRegs = 56;
 constexpr float kRescaleAt = 8.f;
+constexpr int kItemSlots = 2, kItemReaders = 10;  // warps that read an item
 
 template <int DH>
 struct Layout {
@@ -30,19 +36,39 @@ struct Layout {
   static constexpr uint32_t kBytes = (2 + kKSlots + kVSlots) * kTileBytes;
 };
 
+// 256 queries from row0 of head h, batch entry b, and the key tiles [lo, hi)
+// that some row of each of the two tiles sees; [begin, begin + count) covers
+// both.  count < 0: no more items.
+struct Item {
+  int row0, h, b, lo[2], hi[2], begin, count;
+};
+
 struct Tail {
-  uint64_t q_full, k_full[4], v_full[5];
-  uint64_t passed[5];  // the products before step i, at i modulo kVSlots
+  uint64_t q_full, q_free, k_full[4], v_full[5];
+  uint64_t passed[5];  // the products before step x (over all items), at x modulo kVSlots
   uint64_t s_full[2], p_full[2][2], o_done[2], drain;
+  uint64_t item_full[kItemSlots], item_free[kItemSlots];
+  Item item[kItemSlots];
   uint32_t tmem;
   int abort_flag;
-  int lo[2], hi[2];
 };
 
 struct Params {
   AttnArgs a;
   AttnMaps m;
+  int items;
 };
+
+// Reads item n of the block: false where there is none (or on an abort).
+__device__ __forceinline__ bool next_item(Tail *tail, int n, Item &item, volatile int *abort_flag,
+                                          unsigned *dev_status) {
+  const int s = n % kItemSlots;
+  if (!wait_warp(tail->item_full[s], n / kItemSlots, abort_flag, dev_status)) return false;
+  item = tail->item[s];
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(smem_u32(&tail->item_free[s]));
+  return item.count >= 0;
+}
 
 template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ Params p) {
@@ -54,15 +80,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort_flag = &tail->abort_flag;
 
-  // the blocks with most keys first: the last queries of a causal mask
-  const int heads = a.B * a.Hq;
-  const int blocks_q = (a.Sq + 2 * kTile - 1) / (2 * kTile);
-  const int qb = blocks_q - 1 - static_cast<int>(blockIdx.x / heads);
-  const int bh = blockIdx.x % heads, b = bh / a.Hq, h = bh % a.Hq, g = h / a.group;
-  const int row0 = qb * 2 * kTile, off = a.Sk - a.Sq;
+  const int off = a.Sk - a.Sq;
+  const int ktiles = (a.Sk + kTile - 1) / kTile, qtiles = (a.Sq + kTile - 1) / kTile;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&tail->q_full), 1);
+    mbar_init(smem_u32(&tail->q_free), 1);
     for (int s = 0; s < L::kKSlots; ++s) mbar_init(smem_u32(&tail->k_full[s]), 1);
     for (int s = 0; s < L::kVSlots; ++s) {
       mbar_init(smem_u32(&tail->v_full[s]), 1);
@@ -74,12 +97,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       mbar_init(smem_u32(&tail->p_full[t][1]), kTile);
       mbar_init(smem_u32(&tail->o_done[t]), 1);
     }
+    for (int s = 0; s < kItemSlots; ++s) {
+      mbar_init(smem_u32(&tail->item_full[s]), 1);
+      mbar_init(smem_u32(&tail->item_free[s]), kItemReaders);
+    }
     mbar_init(smem_u32(&tail->drain), 1);
     tail->abort_flag = 0;
-    for (int t = 0; t < 2; ++t) {
-      tail->lo[t] = a.q_docs != nullptr ? INT_MAX : 0;
-      tail->hi[t] = 0;
-    }
     fence_barrier_init();
     tma_prefetch(&p.m.q);
     tma_prefetch(&p.m.k);
@@ -96,147 +119,193 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   tc_fence_after();
   const uint32_t tmem = uniform(tail->tmem);
 
-  // ---- the key tiles [lo, hi) that some row of each query tile sees
-  const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
-  const int ktiles = (a.Sk + kTile - 1) / kTile, qtiles = (a.Sq + kTile - 1) / kTile;
-  int most[2];
-  for (int t = 0; t < 2; ++t) {
-    const int first = row0 + t * kTile, last = min(first + kTile, a.Sq) - 1;
-    most[t] = first < a.Sq ? (last_key(a, last + off, prefix) + kTile) / kTile : 0;
-  }
-  if (a.q_docs != nullptr) {
-    for (int t = 0; t < 2; ++t) {
-      if (most[t] <= 0) continue;
-      const DocRange qr = doc_range(a.q_ranges, int64_t(b) * qtiles + 2 * qb + t);
-      for (int n = threadIdx.x; n < most[t]; n += kThreads)
-        if (docs_meet(qr, doc_range(a.k_ranges, int64_t(b) * ktiles + n))) {
-          atomicMin(&tail->lo[t], n);
-          atomicMax(&tail->hi[t], n + 1);
-        }
-    }
-  } else if (threadIdx.x < 2) {
-    tail->hi[threadIdx.x] = threadIdx.x == 0 ? most[0] : most[1];
-  }
-  __syncthreads();
-  int lo[2], hi[2];
-  for (int t = 0; t < 2; ++t) {
-    hi[t] = uniform(max(tail->hi[t], 0));
-    lo[t] = uniform(min(tail->lo[t], hi[t]));
-  }
-  // the tiles either passes over
-  const int begin = hi[0] == lo[0] ? lo[1] : hi[1] == lo[1] ? lo[0] : min(lo[0], lo[1]);
-  const int end = hi[0] == lo[0] ? hi[1] : hi[1] == lo[1] ? hi[0] : max(hi[0], hi[1]);
-
-  // step i: P V of tile begin + i, and the scores of tile begin + i + 1
-  const int count = end - begin;
-
   if (warp >= 8) {
     set_max_regs_down<kIssueRegs>();
     const uint32_t q_tile = smem_u32(smem), k_ring = q_tile + 2 * L::kTileBytes;
     const uint32_t v_ring = k_ring + L::kKSlots * L::kTileBytes;
-    if (warp == 8) {
+    if (warp == 10) {
+      // ------------------------------------------------------ items
+      const int heads = a.B * a.Hq, blocks_q = p.items / heads;
+      for (int n = 0;; ++n) {
+        const int s = n % kItemSlots;
+        if (n >= kItemSlots &&
+            !wait_warp(tail->item_free[s], n / kItemSlots - 1, abort_flag, a.dev_status))
+          break;
+        // to and fro over the blocks, so that their sums of falling work match
+        const int blocks = gridDim.x, place = blockIdx.x;
+        int id = n * blocks + (n & 1 ? blocks - 1 - place : place);
+        if (a.counter != nullptr && n > 0) {  // the first of each block is its own
+          if (lane == 0) id = blocks + static_cast<int>(atomicAdd(a.counter, 1u));
+          id = __shfl_sync(~0u, id, 0);
+        }
+        Item it = {};
+        it.count = -1;
+        if (id < p.items) {
+          // the last queries, which see most keys of a causal mask, first
+          const int qb = blocks_q - 1 - id / heads, bh = id % heads;
+          it.b = bh / a.Hq;
+          it.h = bh % a.Hq;
+          it.row0 = qb * 2 * kTile;
+          const int prefix = a.prefix != nullptr ? a.prefix[it.b] : 0;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int first = it.row0 + t * kTile, last = min(first + kTile, a.Sq) - 1;
+            int lo = 0;
+            int hi = first < a.Sq ? max(0, (last_key(a, last + off, prefix) + kTile) / kTile) : 0;
+            if (a.q_docs != nullptr && hi > 0) {
+              const DocRange qr = doc_range(a.q_ranges, int64_t(it.b) * qtiles + 2 * qb + t);
+              int from = INT_MAX, to = 0;
+              for (int x = lane; x < hi; x += 32)
+                if (docs_meet(qr, doc_range(a.k_ranges, int64_t(it.b) * ktiles + x))) {
+                  from = min(from, x);
+                  to = x + 1;
+                }
+              hi = __reduce_max_sync(~0u, to);
+              lo = min(__reduce_min_sync(~0u, from), hi);
+            }
+            it.lo[t] = lo;
+            it.hi[t] = hi;
+          }
+          // the tiles either passes over
+          const bool none0 = it.hi[0] == it.lo[0], none1 = it.hi[1] == it.lo[1];
+          it.begin = none0 ? it.lo[1] : none1 ? it.lo[0] : min(it.lo[0], it.lo[1]);
+          it.count = (none0 ? it.hi[1] : none1 ? it.hi[0] : max(it.hi[0], it.hi[1])) - it.begin;
+        }
+        if (lane == 0) {
+          tail->item[s] = it;
+          mbar_arrive(smem_u32(&tail->item_full[s]));  // releases the item's words
+        }
+        __syncwarp();
+        if (it.count < 0) break;
+      }
+    } else if (warp == 8) {
       // ------------------------------------------------------ TMA
-      if (lane == 0 && count > 0) {
+      int x = 0, used = 0;  // tiles loaded so far, items with tiles
+      bool ok = true;
+      Item it;
+      for (int n = 0; ok && next_item(tail, n, it, abort_flag, a.dev_status); ++n) {
+        if (it.count == 0) continue;
+        if (used > 0) ok = wait_warp(tail->q_free, used - 1, abort_flag, a.dev_status);
+        if (!ok) break;
+        const int g = it.h / a.group;
         auto load = [&](uint32_t dst, const CUtensorMap *tm, uint64_t &bar, int token, int head) {
           for (int c = 0; c < DH / 64; ++c)
-            tma_load_4d(dst + c * kTile * 128, tm, smem_u32(&bar), c * 64, token, head, b);
+            tma_load_4d(dst + c * kTile * 128, tm, smem_u32(&bar), c * 64, token, head, it.b);
         };
-        auto load_k = [&](int i) {
-          const int s = i % L::kKSlots;
-          mbar_expect_tx(smem_u32(&tail->k_full[s]), L::kTileBytes);
-          load(k_ring + s * L::kTileBytes, &p.m.k, tail->k_full[s], (begin + i) * kTile, g);
-        };
-        mbar_expect_tx(smem_u32(&tail->q_full), 2 * L::kTileBytes);
-        for (int t = 0; t < 2; ++t)  // a second tile past the end reads as zeros
-          load(q_tile + t * L::kTileBytes, &p.m.q, tail->q_full, row0 + t * kTile, h);
-        load_k(0);
-        int nk = 1, nv = 0;
-        for (int i = 0; i < count; ++i) {
-          const int s = i % L::kVSlots;
-          mbar_expect_tx(smem_u32(&tail->v_full[s]), L::kTileBytes);
-          load(v_ring + s * L::kTileBytes, &p.m.v, tail->v_full[s], (begin + i) * kTile, g);
-          ++nv;
-          if (i + 1 == count) break;
-          // K's slot was scored before this step; so was V's next one
-          const int gone = i + 1 - L::kKSlots;
-          if (gone >= 0 && !mbar_wait(smem_u32(&tail->passed[gone % L::kVSlots]),
-                                      (gone / L::kVSlots) & 1, abort_flag, a.dev_status))
-            break;
-          load_k(i + 1);
-          ++nk;
+        if (lane == 0) {
+          mbar_expect_tx(smem_u32(&tail->q_full), 2 * L::kTileBytes);
+          for (int t = 0; t < 2; ++t)  // a second tile past the end reads as zeros
+            load(q_tile + t * L::kTileBytes, &p.m.q, tail->q_full, it.row0 + t * kTile, it.h);
         }
-        // copies in flight land before the CTA leaves
-        mbar_wait_drain(smem_u32(&tail->q_full), 0);
-        for (int s = 0; s < L::kKSlots && s < nk; ++s)
-          mbar_wait_drain(smem_u32(&tail->k_full[s]), ((nk - 1 - s) / L::kKSlots) & 1);
-        for (int s = 0; s < L::kVSlots && s < nv; ++s)
-          mbar_wait_drain(smem_u32(&tail->v_full[s]), ((nv - 1 - s) / L::kVSlots) & 1);
+        ++used;
+        for (int i = 0; i < it.count; ++i, ++x) {
+          // K's slot is scored, and V's is read, before step x - kKSlots
+          const int gone = x - L::kKSlots;
+          if (gone >= 0 && !(ok = wait_warp(tail->passed[gone % L::kVSlots], gone / L::kVSlots,
+                                            abort_flag, a.dev_status)))
+            break;
+          if (lane == 0) {
+            const int ks = x % L::kKSlots, vs = x % L::kVSlots, token = (it.begin + i) * kTile;
+            mbar_expect_tx(smem_u32(&tail->k_full[ks]), L::kTileBytes);
+            load(k_ring + ks * L::kTileBytes, &p.m.k, tail->k_full[ks], token, g);
+            mbar_expect_tx(smem_u32(&tail->v_full[vs]), L::kTileBytes);
+            load(v_ring + vs * L::kTileBytes, &p.m.v, tail->v_full[vs], token, g);
+          }
+          __syncwarp();
+        }
       }
-    } else if (warp == 9 && count > 0) {
+      // copies in flight land before the CTA leaves
+      if (lane == 0) {
+        if (used > 0) mbar_wait_drain(smem_u32(&tail->q_full), (used - 1) & 1);
+        for (int s = 0; s < L::kKSlots && s < x; ++s)
+          mbar_wait_drain(smem_u32(&tail->k_full[s]), ((x - 1 - s) / L::kKSlots) & 1);
+        for (int s = 0; s < L::kVSlots && s < x; ++s)
+          mbar_wait_drain(smem_u32(&tail->v_full[s]), ((x - 1 - s) / L::kVSlots) & 1);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
       // ------------------------------------------------------ MMA
       // (a commit holds the queue of MMAs for some 90 cycles: as few as will do)
       const uint32_t on = elect_one();
-      auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
+      auto wait = [&](const uint64_t &bar, int phase) {
         return wait_warp(bar, phase, abort_flag, a.dev_status);
       };
-      auto wait_k = [&](int i) { return wait(tail->k_full[i % L::kKSlots], i / L::kKSlots); };
-      auto scores = [&](int t, int i) {
-        mma_over_head<DH>(on, tmem + t * kTile, q_tile + t * L::kTileBytes,
-                          k_ring + (i % L::kKSlots) * L::kTileBytes);
-        commit(on, smem_u32(&tail->s_full[t]));
-      };
-      auto padded = [&](int i) {
-        return a.q_docs != nullptr && i < count &&
-               doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded;
-      };
       const auto p_cols = [](int kk) { return kk * 8; };
-      int turn[2] = {0, 0};  // score tiles done of each query tile
-      // V's tile i has landed; without the rows of padding
-      bool pads = padded(0);
-      auto wait_v = [&](int i) {
-        const int s = i % L::kVSlots, token = (begin + i) * kTile;
-        if (!wait(tail->v_full[s], i / L::kVSlots)) return false;
-        if (pads)
-          zero_padding_rows<DH>(smem + (2 + L::kKSlots + s) * L::kTileBytes,
-                                a.k_docs + b * a.kds + token, a.Sk - token);
-        pads = padded(i + 1);
-        return true;
-      };
-      bool ok = wait(tail->q_full, 0) && wait_k(0);
-      tc_fence_after();
-      if (ok)
+      int base = 0, used = 0;  // tiles and items with tiles before this item
+      int turn[2] = {0, 0};    // score tiles done of each query tile
+      bool ok = true;
+      Item it;
+      for (int n = 0; ok && next_item(tail, n, it, abort_flag, a.dev_status); ++n) {
+        const int count = uniform(it.count), begin = uniform(it.begin), b = uniform(it.b);
+        if (count == 0) continue;
+        const int lo[2] = {uniform(it.lo[0]), uniform(it.lo[1])};
+        const int hi[2] = {uniform(it.hi[0]), uniform(it.hi[1])};
+        auto wait_k = [&](int i) {
+          const int x = base + i;
+          return wait(tail->k_full[x % L::kKSlots], x / L::kKSlots);
+        };
+        auto scores = [&](int t, int i) {
+          mma_over_head<DH>(on, tmem + t * kTile, q_tile + t * L::kTileBytes,
+                            k_ring + ((base + i) % L::kKSlots) * L::kTileBytes);
+          commit(on, smem_u32(&tail->s_full[t]));
+        };
+        auto padded = [&](int i) {
+          return a.q_docs != nullptr && i < count &&
+                 doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded;
+        };
+        // V's tile i has landed; without the rows of padding
+        bool pads = padded(0);
+        auto wait_v = [&](int i) {
+          const int s = (base + i) % L::kVSlots, token = (begin + i) * kTile;
+          if (!wait(tail->v_full[s], (base + i) / L::kVSlots)) return false;
+          if (pads)
+            zero_padding_rows<DH>(smem + (2 + L::kKSlots + s) * L::kTileBytes,
+                                  a.k_docs + b * a.kds + token, a.Sk - token);
+          pads = padded(i + 1);
+          return true;
+        };
+        if (!(ok = wait(tail->q_full, used) && wait_k(0))) break;
+        tc_fence_after();
+#pragma unroll
         for (int t = 0; t < 2; ++t)
           if (begin >= lo[t] && begin < hi[t]) scores(t, 0);
-      commit(on, smem_u32(&tail->passed[0]));
-      if (ok) ok = wait_v(0);
-      for (int i = 0; i < count && ok; ++i) {
-        const int n = begin + i, vs = i % L::kVSlots;
-        const bool more = i + 1 < count;
-        const uint32_t vt = v_ring + vs * L::kTileBytes;
+        commit(on, smem_u32(&tail->passed[base % L::kVSlots]));
+        if (count == 1) commit(on, smem_u32(&tail->q_free));
+        if (!(ok = wait_v(0))) break;
+        bool first[2] = {true, true};
+        for (int i = 0; i < count && ok; ++i) {
+          const int tile = begin + i;
+          const bool more = i + 1 < count;
+          const uint32_t vt = v_ring + ((base + i) % L::kVSlots) * L::kTileBytes;
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          if (n >= lo[t] && n < hi[t]) {
-            const uint32_t o = tmem + 256 + t * kTile, w = tmem + t * kTile;
-            if (!(ok = wait(tail->p_full[t][0], turn[t]))) break;
+          for (int t = 0; t < 2; ++t) {
+            if (tile >= lo[t] && tile < hi[t]) {
+              const uint32_t o = tmem + 256 + t * kTile, w = tmem + t * kTile;
+              if (!(ok = wait(tail->p_full[t][0], turn[t]))) break;
+              tc_fence_after();
+              mma_over_tokens<DH, 0, 4>(on, o, w, p_cols, vt, !first[t]);
+              if (!(ok = wait(tail->p_full[t][1], turn[t]))) break;
+              tc_fence_after();
+              mma_over_tokens<DH, 4, 8>(on, o, w, p_cols, vt, true);
+              if (tile + 1 == hi[t]) commit(on, smem_u32(&tail->o_done[t]));
+              first[t] = false;
+              ++turn[t];
+            }
+            // While the queue is full: the steps before are given back, and the
+            // waits for what the next step reads.
+            if (t == 0) {
+              if (i > 0) commit(on, smem_u32(&tail->passed[(base + i) % L::kVSlots]));
+              if (more && !(ok = wait_k(i + 1))) break;
+            } else if (more) {
+              if (!(ok = wait_v(i + 1))) break;
+            }
             tc_fence_after();
-            mma_over_tokens<DH, 0, 4>(on, o, w, p_cols, vt, turn[t] > 0);
-            if (!(ok = wait(tail->p_full[t][1], turn[t]))) break;
-            tc_fence_after();
-            mma_over_tokens<DH, 4, 8>(on, o, w, p_cols, vt, true);
-            if (n + 1 == hi[t]) commit(on, smem_u32(&tail->o_done[t]));
-            ++turn[t];
+            if (tile + 1 >= lo[t] && tile + 1 < hi[t]) scores(t, i + 1);
           }
-          // While the queue is full: the step before is given back, and the
-          // waits for what the next step reads.
-          if (t == 0) {
-            if (i > 0) commit(on, smem_u32(&tail->passed[vs]));
-            if (more && !(ok = wait_k(i + 1))) break;
-          } else if (more) {
-            if (!(ok = wait_v(i + 1))) break;
-          }
-          tc_fence_after();
-          if (n + 1 >= lo[t] && n + 1 < hi[t]) scores(t, i + 1);
+          if (i + 2 == count) commit(on, smem_u32(&tail->q_free));  // Q has been read
         }
+        base += count;
+        ++used;
       }
       // nothing of this CTA is in flight when it leaves
       commit(on, smem_u32(&tail->drain));
@@ -247,160 +316,149 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     set_max_regs_up<kSoftmaxRegs>();
     // ------------------------------------------------------ softmax
     const int t = warp / 4;
-    const int row = row0 + t * kTile + (threadIdx.x & 127);
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t s_addr = tmem + lanes + t * kTile, o_addr = tmem + lanes + 256 + t * kTile;
-    const ScoreConst sc = score_const(a, h);
-    const int pos = row + off;
-    const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
-    const int first_last = last_key(a, row0 + t * kTile + off, prefix);  // of the tile's first row
-    DocRange qr = {0, 0, 0, 0};
-    int qd = 0;
-    if (a.q_docs != nullptr && row0 + t * kTile < a.Sq) {
-      qr = doc_range(a.q_ranges, int64_t(b) * qtiles + 2 * qb + t);
-      qd = row < a.Sq ? a.q_docs[b * a.qds + row] : -1;
-    }
-    float m = -INFINITY;  // the maximum that P is relative to, in log2 units
-    float2 l2 = make_float2(0.f, 0.f);
+    int turn = 0, done = 0;  // score tiles, and items with tiles, of this query tile
     bool ok = true;
-    int turn = 0;
-    DocRange kr = {0, 0, 0, 0};
-    if (a.q_docs != nullptr && lo[t] < hi[t])
-      kr = doc_range(a.k_ranges, int64_t(b) * ktiles + lo[t]);
-    for (int n = lo[t]; n < hi[t]; ++n, ++turn) {
-      // does the mask leave the whole tile?
-      bool whole = n * kTile + kTile - 1 <= first_last;
-      int kd[4];
+    Item it;
+    for (int item = 0; ok && next_item(tail, item, it, abort_flag, a.dev_status); ++item) {
+      const int b = it.b, h = it.h, first = it.row0 + t * kTile;
+      if (first >= a.Sq) continue;
+      const int lo = it.lo[t], hi = it.hi[t], row = first + (threadIdx.x & 127);
+      const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
+      const ScoreConst sc = score_const(a, h);
+      const int pos = row + off;
+      const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
+      const int first_last = last_key(a, first + off, prefix);  // of the tile's first row
+      DocRange qr = {0, 0, 0, 0}, kr = {0, 0, 0, 0};
+      int qd = 0;
       if (a.q_docs != nullptr) {
-        whole = whole && docs_equal(qr, kr);
-        if (!whole) load_docs(a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile, kd);
-        if (n + 1 < hi[t]) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
+        qr = doc_range(a.q_ranges, int64_t(b) * qtiles + first / kTile);
+        qd = row < a.Sq ? a.q_docs[b * a.qds + row] : -1;
+        if (lo < hi) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + lo);
       }
-      if (!(ok = wait_warp(tail->s_full[t], turn, abort_flag, a.dev_status))) break;
-      tc_fence_after();
-      float s[kTile];
-#pragma unroll
-      for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s + c * 32);
-      tmem_wait_ld();
-      pin<kTile>(s);
-      if constexpr (CAP || BIAS) {
-        const float d0 = static_cast<float>(pos - n * kTile);
-        float r;
-#pragma unroll
-        for (int j = 0; j < kTile; ++j) s[j] = score2<CAP, BIAS>(sc, s[j], d0 - j, r);
-      }
-      if (!whole) {
-        uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-        if (a.q_docs != nullptr) same_doc(qd, kd, keep);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          keep[c] &= bits_to(last - n * kTile - 32 * c);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!(keep[c] >> j & 1u)) s[c * 32 + j] = -INFINITY;
+      float m = -INFINITY;  // the maximum that P is relative to, in log2 units
+      float2 l2 = make_float2(0.f, 0.f);
+      for (int n = lo; n < hi; ++n, ++turn) {
+        // does the mask leave the whole tile?
+        bool whole = n * kTile + kTile - 1 <= first_last;
+        int kd[4];
+        if (a.q_docs != nullptr) {
+          whole = whole && docs_equal(qr, kr);
+          if (!whole) load_docs(a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile, kd);
+          if (n + 1 < hi) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
         }
-      }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int j = 4; j < kTile - 4; j += 8)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[j + 2 * i], s[j + 2 * i + 1]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[kTile - 4 + i]);
-      float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-      if constexpr (!CAP && !BIAS) top *= sc.scale2;
-      float by = 1.f;
-      if (m == -INFINITY) {
-        m = top;  // nothing summed so far: O's row is zero or not begun
-      } else if (top > m + kRescaleAt) {
-        by = ex2(m - top);
-        m = top;
-      }
-      if (__any_sync(~0u, by != 1.f)) {
-        // (the scores of this tile were issued after P V of the one before:
-        // that is in O)
-        l2.x *= by;
-        l2.y *= by;
-#pragma unroll 1
-        for (int c = 0; c < DH; c += 32) {
-          float o[32];
-          tmem_ld32(o_addr + c, o);
-          tmem_wait_ld();
-          pin<32>(o);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] *= by;
-          tmem_st32(o_addr + c, o);
-        }
-      }
-      const float sub = m == -INFINITY ? 0.f : -m;
-      const float2 sub2 = make_float2(sub, sub);
-      const float2 sl2 = make_float2(sc.scale2, sc.scale2);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 x = make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]);
-          if constexpr (CAP || BIAS)
-            x = add2(x, sub2);
-          else
-            x = fma2(x, sl2, sub2);
-          x.x = ex2(x.x);
-          x.y = ex2(x.y);
-          l2 = add2(l2, x);
-          w[i] = pack_bf16(x.x, x.y);
-        }
-        tmem_st16(s_addr + c * 16, w);
-        if (c & 1) {  // P V may begin on the first half
-          tmem_wait_st();
-          tc_fence_before();
-          mbar_arrive(smem_u32(&tail->p_full[t][c >> 1]));
-        }
-      }
-    }
-    if (row0 + t * kTile < a.Sq) {
-      if (ok && turn > 0) {
-        ok = wait_warp(tail->o_done[t], 0, abort_flag, a.dev_status);
-      } else if (ok && count > 0) {  // Q's copy has landed before its memory is reused
-        ok = wait_warp(tail->q_full, 0, abort_flag, a.dev_status);
-      }
-      const float l = l2.x + l2.y;
-      const float inv = l > 0.f ? 1.f / l : 0.f;
-      if (ok) {
-        // O through this tile's part of Q's shared memory: every product that
-        // reads it is done
+        if (!(ok = wait_warp(tail->s_full[t], turn, abort_flag, a.dev_status))) break;
         tc_fence_after();
-        uint8_t *stage = smem + t * L::kTileBytes;
+        float s[kTile];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(s_addr + c * 32, s + c * 32);
+        tmem_wait_ld();
+        pin<kTile>(s);
+        if constexpr (CAP || BIAS) {
+          const float d0 = static_cast<float>(pos - n * kTile);
+          float r;
+#pragma unroll
+          for (int j = 0; j < kTile; ++j) s[j] = score2<CAP, BIAS>(sc, s[j], d0 - j, r);
+        }
+        if (!whole) {
+          uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
+          if (a.q_docs != nullptr) same_doc(qd, kd, keep);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            keep[c] &= bits_to(last - n * kTile - 32 * c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(keep[c] >> j & 1u)) s[c * 32 + j] = -INFINITY;
+          }
+        }
+        float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int j = 4; j < kTile - 4; j += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = max3(mx[i], s[j + 2 * i], s[j + 2 * i + 1]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mx[i] = fmaxf(mx[i], s[kTile - 4 + i]);
+        float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+        if constexpr (!CAP && !BIAS) top *= sc.scale2;
+        float by = 1.f;
+        if (m == -INFINITY) {
+          m = top;  // nothing summed so far: O's row is zero or not begun
+        } else if (top > m + kRescaleAt) {
+          by = ex2(m - top);
+          m = top;
+        }
+        if (__any_sync(~0u, by != 1.f)) {
+          // (the scores of this tile were issued after P V of the one before:
+          // that is in O)
+          l2.x *= by;
+          l2.y *= by;
 #pragma unroll 1
-        for (int c = 0; c < DH; c += 32) {
-          float o[32];
-          if (turn > 0) {
+          for (int c = 0; c < DH; c += 32) {
+            float o[32];
             tmem_ld32(o_addr + c, o);
             tmem_wait_ld();
             pin<32>(o);
-          }
-          if (!(l > 0.f))
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0.f;
-          stage_row32(stage, threadIdx.x & 127, c, o, inv);
+            for (int i = 0; i < 32; ++i) o[i] *= by;
+            tmem_st32(o_addr + c, o);
+          }
         }
-        if (a.lse != nullptr && row < a.Sq)
-          a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row] =
-              l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-        fence_proxy_async_smem();
-      }
-      // stored only if every warp of the tile has its rows staged
-      const bool failed = named_bar_red_or(1 + t, kTile, !ok);
-      if (!failed) {
-        uint8_t *stage = smem + t * L::kTileBytes;
-        if ((threadIdx.x & 127) == 0) {
-          for (int c = 0; c < DH / 64; ++c)
-            if (c * 64 < a.D)
-              tma_store_4d(&p.m.o, smem_u32(stage) + c * kTile * 128, c * 64, row0 + t * kTile, h, b);
-          bulk_commit_group();
-          bulk_wait_group0();
+        const float sub = m == -INFINITY ? 0.f : -m;
+        const float2 sub2 = make_float2(sub, sub);
+        const float2 sl2 = make_float2(sc.scale2, sc.scale2);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            float2 x = make_float2(s[c * 32 + 2 * i], s[c * 32 + 2 * i + 1]);
+            if constexpr (CAP || BIAS)
+              x = add2(x, sub2);
+            else
+              x = fma2(x, sl2, sub2);
+            x.x = ex2(x.x);
+            x.y = ex2(x.y);
+            l2 = add2(l2, x);
+            w[i] = pack_bf16(x.x, x.y);
+          }
+          tmem_st16(s_addr + c * 16, w);
+          if (c & 1) {  // P V may begin on the first half
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&tail->p_full[t][c >> 1]));
+          }
         }
       }
+      if (!ok) break;
+      if (lo < hi) {
+        if (!(ok = wait_warp(tail->o_done[t], done, abort_flag, a.dev_status))) break;
+        ++done;
+        tc_fence_after();
+      }
+      // a thread's row straight to global memory: its shared memory is already
+      // the next item's
+      const float l = l2.x + l2.y;
+      const float inv = l > 0.f ? 1.f / l : 0.f;
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + row * a.so[1] +
+                           h * a.so[2];
+#pragma unroll 1
+      for (int c = 0; c < DH; c += 32) {
+        float o[32];
+        if (lo < hi) {
+          tmem_ld32(o_addr + c, o);
+          tmem_wait_ld();
+          pin<32>(o);
+        }
+        if (!(l > 0.f))
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = 0.f;
+        if (row < a.Sq) store_row32(out, c, a.D, o, inv);
+      }
+      tc_fence_before();  // O has been read before the next item's P is announced
+      if (a.lse != nullptr && row < a.Sq)
+        a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row] =
+            l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
   }
   tc_fence_before();
@@ -411,10 +469,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   }
 }
 
-// Ranges of the documents of 128-token tiles, one warp per tile.
-__global__ void k_attn_ranges(const int *docs, int64_t stride, int B, int S, int4 *out) {
+// Ranges of the documents of 128-token tiles, one warp per tile; zeroes the
+// counters that items are handed out from.
+__global__ void k_attn_ranges(const int *docs, int64_t stride, int B, int S, int4 *out,
+                              unsigned *counters) {
   griddep_wait();
   griddep_launch_dependents();
+  if (counters != nullptr && blockIdx.x == 0 && threadIdx.x < kAttnCounters)
+    counters[threadIdx.x] = 0;
   const int tiles = (S + kTile - 1) / kTile;
   const int w = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
   if (w >= B * tiles) return;
@@ -438,14 +500,13 @@ __global__ void k_attn_ranges(const int *docs, int64_t stride, int B, int S, int
 }
 
 template <int DH, bool CAP, bool BIAS>
-cudaError_t launch(const Params &p, cudaStream_t s) {
+cudaError_t launch(const Params &p, int sms, cudaStream_t s) {
   const size_t smem = Layout<DH>::kBytes + sizeof(Tail) + 1024;
   auto *kernel = k_attn_fwd<DH, CAP, BIAS>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = int64_t(p.a.B) * p.a.Hq * ((p.a.Sq + 2 * kTile - 1) / (2 * kTile));
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p);
+  return launch_pdl(kernel, dim3(p.items < sms ? p.items : sms), dim3(kThreads), smem, s, p);
 }
 
 }  // namespace
@@ -458,20 +519,20 @@ cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s) {
     const cudaError_t e = launch_pdl(
         k_attn_ranges, dim3(static_cast<unsigned>((tiles + 7) / 8)), dim3(256), 0, s,
         side ? a.k_docs : a.q_docs, side ? a.kds : a.qds, a.B, S,
-        const_cast<int4 *>(side ? a.k_ranges : a.q_ranges));
+        const_cast<int4 *>(side ? a.k_ranges : a.q_ranges), side ? nullptr : a.counter);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
 }
 
-cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, cudaStream_t s) {
-  const Params p{a, m};
+cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s) {
+  const Params p{a, m, a.B * a.Hq * ((a.Sq + 2 * kTile - 1) / (2 * kTile))};
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
   if (a.D <= 64)
-    return cap ? (bias ? launch<64, true, true>(p, s) : launch<64, true, false>(p, s))
-               : (bias ? launch<64, false, true>(p, s) : launch<64, false, false>(p, s));
-  return cap ? (bias ? launch<128, true, true>(p, s) : launch<128, true, false>(p, s))
-             : (bias ? launch<128, false, true>(p, s) : launch<128, false, false>(p, s));
+    return cap ? (bias ? launch<64, true, true>(p, sms, s) : launch<64, true, false>(p, sms, s))
+               : (bias ? launch<64, false, true>(p, sms, s) : launch<64, false, false>(p, sms, s));
+  return cap ? (bias ? launch<128, true, true>(p, sms, s) : launch<128, true, false>(p, sms, s))
+             : (bias ? launch<128, false, true>(p, sms, s) : launch<128, false, false>(p, sms, s));
 }
 
 }  // namespace lora
