@@ -25,9 +25,12 @@ struct AttnArgs {
   // with documents: counters (kAttnCounters, zeroed with the ranges) that the
   // persistent blocks take their items from
   unsigned *counter = nullptr;
+  // with documents, backward: the key tiles ([batch][tiles] numbers) in the
+  // order of falling work
+  const int *order = nullptr;
   unsigned *dev_status = nullptr;
 };
-constexpr int kAttnCounters = 2;
+constexpr int kAttnCounters = 1;
 
 // A [batch][token][head][dim] bf16 tensor's map: boxes of 64 elements x 128
 // tokens of one head, 128-byte swizzle, zeros outside.
@@ -35,13 +38,15 @@ struct AttnMaps {
   CUtensorMap q, k, v;
 };
 struct AttnBwdMaps {
-  CUtensorMap q, k, v, d_o, dq, dk, dv;
+  CUtensorMap q, k, v, d_o;
 };
 
+// Ranges of the documents (and counters zeroed); then the order, if asked for.
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
+cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s);
-cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
-cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s);
+cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s);
+cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s);
 
 // One token: the cache's length in `splits` chunks of `chunk` keys, the heads
 // of a group in head_chunks blocks; partial results of [batch][q_heads][splits]

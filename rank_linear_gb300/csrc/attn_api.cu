@@ -115,9 +115,9 @@ lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], 
 }
 
 // Workspace: [document ranges of the query tiles, of the key tiles][item
-// counters][delta].
+// counters][order of the key tiles][delta].
 struct Plan {
-  size_t q_ranges = 0, k_ranges = 0, counter = 0, delta = 0, bytes = 0;
+  size_t q_ranges = 0, k_ranges = 0, counter = 0, order = 0, delta = 0, bytes = 0;
 };
 Plan make_plan(const lora_attention_t *p, bool backward) {
   Plan w;
@@ -129,6 +129,8 @@ Plan make_plan(const lora_attention_t *p, bool backward) {
     off += rup(size_t(p->batch) * tiles_of(p->k_len) * 16, 256);
     w.counter = off;
     off += 256;
+    w.order = off;
+    if (backward) off += rup(size_t(p->batch) * tiles_of(p->k_len) * 4, 256);
   }
   if (backward) {
     w.delta = off;
@@ -154,12 +156,15 @@ TokenSpace make_token_space(const lora_attention_t *p) {
   return w;
 }
 
-lora_status_t make_ranges(AttnArgs &a, const Plan &w, void *ws, cudaStream_t st) {
+lora_status_t make_ranges(AttnArgs &a, const Plan &w, void *ws, bool backward, cudaStream_t st) {
   if (a.q_docs == nullptr) return LORA_OK;
   a.q_ranges = reinterpret_cast<const int4 *>(at(ws, w.q_ranges));
   a.k_ranges = reinterpret_cast<const int4 *>(at(ws, w.k_ranges));
   a.counter = reinterpret_cast<unsigned *>(at(ws, w.counter));
-  return run(LORA_K_ATTN_PREP, st, "document ranges", [&] { return launch_attn_ranges(a, st); });
+  LORA_TRY(run(LORA_K_ATTN_PREP, st, "document ranges", [&] { return launch_attn_ranges(a, st); }));
+  if (!backward || a.Sk == 0) return LORA_OK;
+  a.order = reinterpret_cast<const int *>(at(ws, w.order));
+  return run(LORA_K_ATTN_PREP, st, "key tiles by work", [&] { return launch_attn_order(a, st); });
 }
 
 }  // namespace
@@ -204,7 +209,7 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   LORA_TRY(tensor_map(&m.q, q, shape->q, a, a.Sq, a.Hq, "q"));
   LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
   LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
-  LORA_TRY(make_ranges(a, w, workspace, st));
+  LORA_TRY(make_ranges(a, w, workspace, false, st));
   return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, m, di.sms, st); });
 }
 
@@ -246,17 +251,14 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
   AttnBwdMaps m;
   LORA_TRY(tensor_map(&m.q, no_q ? k : q, shape->q, a, a.Sq, a.Hq, "q"));
   LORA_TRY(tensor_map(&m.d_o, no_q ? k : d_o, shape->d_o, a, a.Sq, a.Hq, "do"));
-  LORA_TRY(tensor_map(&m.dq, no_q ? k : dq, shape->dq, a, a.Sq, a.Hq, "dq"));
   LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
   LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
-  LORA_TRY(tensor_map(&m.dk, no_k ? q : dk, shape->dk, a, a.Sk, a.Hk, "dk"));
-  LORA_TRY(tensor_map(&m.dv, no_k ? q : dv, shape->dv, a, a.Sk, a.Hk, "dv"));
-  LORA_TRY(make_ranges(a, w, workspace, st));
+  LORA_TRY(make_ranges(a, w, workspace, true, st));
   if (!no_q)
-    LORA_TRY(run(LORA_K_ATTN_DQ, st, "attention dq", [&] { return launch_attn_dq(a, m, st); }));
+    LORA_TRY(run(LORA_K_ATTN_DQ, st, "attention dq", [&] { return launch_attn_dq(a, m, di.sms, st); }));
   if (!no_k)
     LORA_TRY(run(LORA_K_ATTN_DKV, st, "attention dk and dv",
-                 [&] { return launch_attn_dkv(a, m, st); }));
+                 [&] { return launch_attn_dkv(a, m, di.sms, st); }));
   return LORA_OK;
 }
 

@@ -8,19 +8,26 @@
 // pair, dz = P dc/dz (dP - delta) with P = exp(s - lse), goes back into TMEM
 // as bf16 over the scores (or over dP) and is the TMEM operand of the products
 // that follow; nothing of size q_len x k_len leaves the SM.
+//
+// The dq blocks stay and take item after item, as the forward's do.  A dk/dv
+// item has a group's heads times as much work; where there are too few for the
+// SMs, the blocks of a cluster share one, each with its part of the steps, and
+// add their sums through distributed shared memory in the order of their ranks.
 #include "attn.cuh"
 #include "host.h"
 
 namespace lora {
 namespace {
 
-// Two warpgroups for the pairs (128 rows, 64 columns each) and one of which
-// two warps issue the copies and the MMAs; registers as in the forward.
+// Two warpgroups for the pairs (128 rows, 64 columns each) and one whose warps
+// issue the copies, the MMAs and the items; registers as in the forward.
 constexpr int kThreads = 384, kPairThreads = 256, kPairRegs = 224, kIssueRegs = 56;
+constexpr int kItemSlots = 2, kItemReaders = 10;
 
 struct Params {
   AttnArgs a;
   AttnBwdMaps m;
+  int items, cluster;
 };
 
 // The columns of a 128-wide TMEM region that hold K step kk of a bf16 operand:
@@ -70,42 +77,65 @@ __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], flo
 }
 
 // ---------------------------------------------------------------- dq
-// Shared memory: Q, dO, then rings of K and V tiles.  TMEM: the scores (then
+// Shared memory: Q, dO, then rings of K and V tiles (counted on over the items).  TMEM: the scores (then
 // dz) of two tiles at 0 and 128, dP at 256, dq at 384.
 template <int DH>
 struct DqLayout {
   static constexpr uint32_t kTileBytes = kTile * DH * 2;
   static constexpr int kKSlots = 3, kVSlots = 2;
-  static constexpr uint32_t kBytes = (2 + kKSlots + kVSlots) * kTileBytes;
+  // the tiles follow the tail (DqTail), which for a head of 128 fills what
+  // they leave of an SM's 227 KB: no room to align a base that is not aligned
+  static constexpr uint32_t kTailBytes = 3072;
+  static constexpr uint32_t kBytes = kTailBytes + (2 + kKSlots + kVSlots) * kTileBytes;
   // one block per SM (TMEM): more than half of its shared memory
   static constexpr uint32_t kAsked = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
 };
-struct DqTail {
-  uint64_t q_full, k_full[3], k_empty[3], v_full[2];
-  uint64_t s_full[2], dp_full[2], dp_free, dz_full, done, drain;
-  uint32_t tmem;
-  int abort_flag, lo, hi;
-  float delta[2][kTile];
+// 128 queries from row0 of head h, batch entry b, and the key tiles [begin,
+// begin + count) that some row sees.  count < 0: no more items.
+struct DqItem {
+  int row0, h, b, begin, count;
 };
+struct DqTail {
+  uint64_t q_full, q_free, k_full[3], k_empty[3], v_full[2];
+  uint64_t s_full[2], dp_full[2], dp_free, dz_full, delta_full, done, drain;
+  uint64_t item_full[kItemSlots], item_free[kItemSlots];
+  DqItem item[kItemSlots];
+  uint32_t tmem;
+  int abort_flag;
+  float delta[2][2][kTile];  // by item modulo 2, half of the head
+};
+
+__device__ __forceinline__ bool next_item(DqTail *tail, int n, DqItem &item,
+                                          volatile int *abort_flag, unsigned *dev_status) {
+  const int s = n % kItemSlots;
+  if (!wait_warp(tail->item_full[s], n / kItemSlots, abort_flag, dev_status)) return false;
+  item = tail->item[s];
+  __syncwarp();
+  if (threadIdx.x % 32 == 0) mbar_arrive(smem_u32(&tail->item_free[s]));
+  return item.count >= 0;
+}
 
 template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ Params p) {
   using L = DqLayout<DH>;
-  extern __shared__ uint8_t raw[];
-  uint8_t *smem = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
-  DqTail *tail = reinterpret_cast<DqTail *>(smem + L::kBytes);
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t *smem = raw + L::kTailBytes;
+  DqTail *tail = reinterpret_cast<DqTail *>(raw);
+  static_assert(sizeof(DqTail) <= L::kTailBytes, "tail");
+  if ((smem_u32(raw) & 1023) != 0) {  // not met: the tiles' layout needs it
+    if (threadIdx.x == 0) atomicOr(p.a.dev_status, kDevErrTimeout);
+    return;
+  }
   const AttnArgs &a = p.a;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort_flag = &tail->abort_flag;
 
-  const int heads = a.B * a.Hq;
   const int qtiles = (a.Sq + kTile - 1) / kTile, ktiles = (a.Sk + kTile - 1) / kTile;
-  const int qt = qtiles - 1 - static_cast<int>(blockIdx.x / heads);
-  const int bh = blockIdx.x % heads, b = bh / a.Hq, h = bh % a.Hq, g = h / a.group;
-  const int row0 = qt * kTile, off = a.Sk - a.Sq;
+  const int off = a.Sk - a.Sq;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&tail->q_full), 1);
+    mbar_init(smem_u32(&tail->q_free), 1);
     for (int s = 0; s < L::kKSlots; ++s) {
       mbar_init(smem_u32(&tail->k_full[s]), 1);
       mbar_init(smem_u32(&tail->k_empty[s]), 1);
@@ -117,11 +147,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     }
     mbar_init(smem_u32(&tail->dp_free), kPairThreads);
     mbar_init(smem_u32(&tail->dz_full), kPairThreads);
+    mbar_init(smem_u32(&tail->delta_full), kPairThreads);
+    for (int s = 0; s < kItemSlots; ++s) {
+      mbar_init(smem_u32(&tail->item_full[s]), 1);
+      mbar_init(smem_u32(&tail->item_free[s]), kItemReaders);
+    }
     mbar_init(smem_u32(&tail->done), 1);
     mbar_init(smem_u32(&tail->drain), 1);
     tail->abort_flag = 0;
-    tail->lo = a.q_docs != nullptr ? INT_MAX : 0;
-    tail->hi = 0;
     fence_barrier_init();
     tma_prefetch(&p.m.q);
     tma_prefetch(&p.m.k);
@@ -139,121 +172,176 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = uniform(tail->tmem);
 
-  // ---- the key tiles that some row sees
-  const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
-  const int most =
-      max(0, (last_key(a, min(row0 + kTile, a.Sq) - 1 + off, prefix) + kTile) / kTile);
-  DocRange qr = {0, 0, 0, 0};
-  if (a.q_docs != nullptr) {
-    qr = doc_range(a.q_ranges, int64_t(b) * qtiles + qt);
-    for (int n = threadIdx.x; n < most; n += kThreads)
-      if (docs_meet(qr, doc_range(a.k_ranges, int64_t(b) * ktiles + n))) {
-        atomicMin(&tail->lo, n);
-        atomicMax(&tail->hi, n + 1);
-      }
-  } else if (threadIdx.x == 0) {
-    tail->hi = most;
-  }
-  __syncthreads();
-  const int end = uniform(tail->hi), begin = uniform(min(tail->lo, end));
-  const int count = end - begin;
-
   if (warp >= 8) {
     set_max_regs_down<kIssueRegs>();
     const uint32_t q_tile = smem_u32(smem), do_tile = q_tile + L::kTileBytes;
     const uint32_t k_ring = do_tile + L::kTileBytes, v_ring = k_ring + L::kKSlots * L::kTileBytes;
-    if (warp == 8) {
+    auto wait = [&](const uint64_t &bar, int phase) {
+      return wait_warp(bar, phase, abort_flag, a.dev_status);
+    };
+    if (warp == 10) {
+      // ------------------------------------------------------ items
+      const int heads = a.B * a.Hq;
+      for (int n = 0;; ++n) {
+        const int s = n % kItemSlots;
+        if (n >= kItemSlots && !wait(tail->item_free[s], n / kItemSlots - 1)) break;
+        // to and fro over the blocks, or from the counter, as in the forward
+        const int blocks = gridDim.x, place = blockIdx.x;
+        int id = n * blocks + (n & 1 ? blocks - 1 - place : place);
+        if (a.counter != nullptr && n > 0) {
+          if (lane == 0) id = blocks + static_cast<int>(atomicAdd(a.counter, 1u));
+          id = __shfl_sync(~0u, id, 0);
+        }
+        DqItem it = {};
+        it.count = -1;
+        if (id < p.items) {
+          const int qt = qtiles - 1 - id / heads, bh = id % heads;
+          it.b = bh / a.Hq;
+          it.h = bh % a.Hq;
+          it.row0 = qt * kTile;
+          const int prefix = a.prefix != nullptr ? a.prefix[it.b] : 0;
+          int lo = 0, hi = max(0, (last_key(a, min(it.row0 + kTile, a.Sq) - 1 + off, prefix) +
+                                   kTile) / kTile);
+          if (a.q_docs != nullptr && hi > 0) {
+            const DocRange qr = doc_range(a.q_ranges, int64_t(it.b) * qtiles + qt);
+            int from = INT_MAX, to = 0;
+            for (int x = lane; x < hi; x += 32)
+              if (docs_meet(qr, doc_range(a.k_ranges, int64_t(it.b) * ktiles + x))) {
+                from = min(from, x);
+                to = x + 1;
+              }
+            hi = __reduce_max_sync(~0u, to);
+            lo = min(__reduce_min_sync(~0u, from), hi);
+          }
+          it.begin = lo;
+          it.count = hi - lo;
+        }
+        if (lane == 0) {
+          tail->item[s] = it;
+          mbar_arrive(smem_u32(&tail->item_full[s]));  // releases the item's words
+        }
+        __syncwarp();
+        if (it.count < 0) break;
+      }
+    } else if (warp == 8) {
       // ------------------------------------------------------ TMA
-      if (lane == 0 && count > 0) {
+      int x = 0, used = 0, nv = 0;  // tiles loaded so far, items with tiles
+      bool ok = true;
+      DqItem it;
+      for (int n = 0; ok && next_item(tail, n, it, abort_flag, a.dev_status); ++n) {
+        if (it.count == 0) continue;
+        if (used > 0 && !(ok = wait(tail->q_free, used - 1))) break;
+        const int g = it.h / a.group;
         auto load = [&](uint32_t dst, const CUtensorMap *tm, uint64_t &bar, int token, int head) {
           for (int c = 0; c < DH / 64; ++c)
-            tma_load_4d(dst + c * kTile * 128, tm, smem_u32(&bar), c * 64, token, head, b);
+            tma_load_4d(dst + c * kTile * 128, tm, smem_u32(&bar), c * 64, token, head, it.b);
         };
-        mbar_expect_tx(smem_u32(&tail->q_full), 2 * L::kTileBytes);
-        load(q_tile, &p.m.q, tail->q_full, row0, h);
-        load(do_tile, &p.m.d_o, tail->q_full, row0, h);
-        int nk = 0, nv = 0;
-        for (int i = 0; i < count; ++i) {
-          const int ks = i % L::kKSlots, vs = i % L::kVSlots;
-          if (i >= L::kKSlots && !mbar_wait(smem_u32(&tail->k_empty[ks]), (i / L::kKSlots - 1) & 1,
-                                            abort_flag, a.dev_status))
-            break;
-          mbar_expect_tx(smem_u32(&tail->k_full[ks]), L::kTileBytes);
-          load(k_ring + ks * L::kTileBytes, &p.m.k, tail->k_full[ks], (begin + i) * kTile, g);
-          ++nk;
-          // dP of the tile before in this slot is done
-          if (i >= L::kVSlots && !mbar_wait(smem_u32(&tail->dp_full[vs]), (i / L::kVSlots - 1) & 1,
-                                            abort_flag, a.dev_status))
-            break;
-          mbar_expect_tx(smem_u32(&tail->v_full[vs]), L::kTileBytes);
-          load(v_ring + vs * L::kTileBytes, &p.m.v, tail->v_full[vs], (begin + i) * kTile, g);
-          ++nv;
+        if (lane == 0) {
+          mbar_expect_tx(smem_u32(&tail->q_full), 2 * L::kTileBytes);
+          load(q_tile, &p.m.q, tail->q_full, it.row0, it.h);
+          load(do_tile, &p.m.d_o, tail->q_full, it.row0, it.h);
         }
-        // copies in flight land before the CTA leaves
-        mbar_wait_drain(smem_u32(&tail->q_full), 0);
-        for (int s = 0; s < L::kKSlots && s < nk; ++s)
-          mbar_wait_drain(smem_u32(&tail->k_full[s]), ((nk - 1 - s) / L::kKSlots) & 1);
+        ++used;
+        for (int i = 0; i < it.count; ++i, ++x) {
+          const int ks = x % L::kKSlots, vs = x % L::kVSlots, token = (it.begin + i) * kTile;
+          if (x >= L::kKSlots && !(ok = wait(tail->k_empty[ks], x / L::kKSlots - 1))) break;
+          if (lane == 0) {
+            mbar_expect_tx(smem_u32(&tail->k_full[ks]), L::kTileBytes);
+            load(k_ring + ks * L::kTileBytes, &p.m.k, tail->k_full[ks], token, g);
+          }
+          // dP of the tile before in this slot is done
+          if (x >= L::kVSlots && !(ok = wait(tail->dp_full[vs], x / L::kVSlots - 1))) {
+            ++x;  // K's copy alone is in flight
+            break;
+          }
+          if (lane == 0) {
+            mbar_expect_tx(smem_u32(&tail->v_full[vs]), L::kTileBytes);
+            load(v_ring + vs * L::kTileBytes, &p.m.v, tail->v_full[vs], token, g);
+          }
+          ++nv;
+          __syncwarp();
+        }
+      }
+      // copies in flight land before the CTA leaves
+      if (lane == 0) {
+        if (used > 0) mbar_wait_drain(smem_u32(&tail->q_full), (used - 1) & 1);
+        for (int s = 0; s < L::kKSlots && s < x; ++s)
+          mbar_wait_drain(smem_u32(&tail->k_full[s]), ((x - 1 - s) / L::kKSlots) & 1);
         for (int s = 0; s < L::kVSlots && s < nv; ++s)
           mbar_wait_drain(smem_u32(&tail->v_full[s]), ((nv - 1 - s) / L::kVSlots) & 1);
       }
-    } else if (warp == 9 && count > 0) {
+      __syncwarp();
+    } else if (warp == 9) {
       // ------------------------------------------------------ MMA
       const uint32_t on = elect_one();
-      auto wait = [&](const uint64_t &bar, int phase) {  // one answer for the warp
-        return wait_warp(bar, phase, abort_flag, a.dev_status);
-      };
-      auto padded = [&](int i) {
-        return a.q_docs != nullptr && i < count &&
-               doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded;
-      };
-      // K's tile i has landed, without the rows of padding
-      bool pads = padded(0);
-      auto wait_k = [&](int i) {
-        const int s = i % L::kKSlots;
-        if (!wait(tail->k_full[s], i / L::kKSlots)) return false;
-        const bool now = pads;
-        pads = padded(i + 1);
-        if (now)
-          zero_padding_rows<DH>(smem + (2 + s) * L::kTileBytes,
-                                a.k_docs + b * a.kds + (begin + i) * kTile,
-                                a.Sk - (begin + i) * kTile);
-        return true;
-      };
-      auto scores = [&](int i) {
-        mma_over_head<DH>(on, tmem + (i & 1) * kTile, q_tile,
-                          k_ring + (i % L::kKSlots) * L::kTileBytes);
-        commit(on, smem_u32(&tail->s_full[i & 1]));
-      };
-      auto do_v = [&](int i) {
-        mma_over_head<DH>(on, tmem + 256, do_tile, v_ring + (i % L::kVSlots) * L::kTileBytes);
-        commit(on, smem_u32(&tail->dp_full[i % L::kVSlots]));
-      };
-      bool ok = wait(tail->q_full, 0) && wait_k(0);
-      tc_fence_after();
-      if (ok) scores(0);
-      if (ok) ok = wait(tail->v_full[0], 0);
-      tc_fence_after();
-      if (ok) do_v(0);
-      for (int i = 0; i < count && ok; ++i) {
-        if (i + 1 < count) {
-          // over the dz of tile i - 1, which its product (issued) reads first
-          if (!(ok = wait_k(i + 1))) break;
-          tc_fence_after();
-          scores(i + 1);
-          if (!(ok = wait(tail->v_full[(i + 1) % L::kVSlots], (i + 1) / L::kVSlots) &&
-                     wait(tail->dp_free, i)))
-            break;
-          tc_fence_after();
-          do_v(i + 1);
-        }
-        if (!(ok = wait(tail->dz_full, i))) break;
+      int base = 0, used = 0;  // tiles and items with tiles before this item
+      bool ok = true;
+      DqItem it;
+      for (int n = 0; ok && next_item(tail, n, it, abort_flag, a.dev_status); ++n) {
+        const int count = uniform(it.count), begin = uniform(it.begin), b = uniform(it.b);
+        if (count == 0) continue;
+        auto padded = [&](int i) {
+          return a.q_docs != nullptr && i < count
+                     ? doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded
+                     : 0;
+        };
+        // K's tile i has landed, without the rows of padding
+        int pads = padded(0);  // looked at a step later: not waited for here
+        auto wait_k = [&](int i) {
+          const int s = (base + i) % L::kKSlots, token = (begin + i) * kTile;
+          if (!wait(tail->k_full[s], (base + i) / L::kKSlots)) return false;
+          const int now = pads;
+          pads = padded(i + 1);
+          if (now != 0)
+            zero_padding_rows<DH>(smem + (2 + s) * L::kTileBytes, a.k_docs + b * a.kds + token,
+                                  a.Sk - token);
+          return true;
+        };
+        auto scores = [&](int i) {
+          const int x = base + i;
+          mma_over_head<DH>(on, tmem + (x & 1) * kTile, q_tile,
+                            k_ring + (x % L::kKSlots) * L::kTileBytes);
+          commit(on, smem_u32(&tail->s_full[x & 1]));
+        };
+        // V's tile has landed, dP of the tile before is in registers
+        auto wait_v = [&](int i) {
+          const int x = base + i;
+          return wait(tail->v_full[x % L::kVSlots], x / L::kVSlots) &&
+                 (x == 0 || wait(tail->dp_free, x - 1));
+        };
+        auto do_v = [&](int i) {
+          const int x = base + i;
+          mma_over_head<DH>(on, tmem + 256, do_tile, v_ring + (x % L::kVSlots) * L::kTileBytes);
+          commit(on, smem_u32(&tail->dp_full[x % L::kVSlots]));
+          if (i + 1 == count) commit(on, smem_u32(&tail->q_free));  // Q and dO have been read
+        };
+        if (!(ok = wait(tail->q_full, used) && wait_k(0))) break;
         tc_fence_after();
-        mma_over_tokens<DH, 0, 8>(on, tmem + 384, tmem + (i & 1) * kTile, operand_cols,
-                            k_ring + (i % L::kKSlots) * L::kTileBytes, i > 0);
-        commit(on, smem_u32(&tail->k_empty[i % L::kKSlots]));
-        __syncwarp();
+        scores(0);
+        if (!(ok = wait_v(0))) break;
+        tc_fence_after();
+        do_v(0);
+        for (int i = 0; i < count; ++i) {
+          const int x = base + i;
+          if (i + 1 < count) {
+            // over the dz of tile i - 1, which its product (issued) reads first
+            if (!(ok = wait_k(i + 1))) break;
+            tc_fence_after();
+            scores(i + 1);
+            if (!(ok = wait_v(i + 1))) break;
+            tc_fence_after();
+            do_v(i + 1);
+          }
+          if (!(ok = wait(tail->dz_full, x))) break;
+          tc_fence_after();
+          mma_over_tokens<DH, 0, 8>(on, tmem + 384, tmem + (x & 1) * kTile, operand_cols,
+                                    k_ring + (x % L::kKSlots) * L::kTileBytes, i > 0);
+          commit(on, smem_u32(&tail->k_empty[x % L::kKSlots]));
+        }
+        if (ok) commit(on, smem_u32(&tail->done));
+        base += count;
+        ++used;
       }
-      if (ok) commit(on, smem_u32(&tail->done));
       commit(on, smem_u32(&tail->drain));
       mbar_wait_drain(smem_u32(&tail->drain), 0);
       __syncwarp();
@@ -261,108 +349,131 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
   } else {
     set_max_regs_up<kPairRegs>();
     // ------------------------------------------------------ pairs
-    const int half = warp / 4, r = threadIdx.x & 127, row = row0 + r;
+    const int half = warp / 4, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const ScoreConst sc = score_const(a, h);
-    const int pos = row + off;
-    const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
-    const int first_last = last_key(a, row0 + off, prefix);
-    const int64_t stat = (static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row;
-    const int qd = a.q_docs != nullptr && row < a.Sq ? a.q_docs[b * a.qds + row] : -1;
-    // delta = do . o, half of the head in each warpgroup
-    float delta = 0.f, sub = -INFINITY;
-    if (row < a.Sq) {
-      const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(a.o) + b * a.so[0] +
-                               row * a.so[1] + h * a.so[2];
-      const __nv_bfloat16 *e = static_cast<const __nv_bfloat16 *>(a.d_o) + b * a.sdo[0] +
-                               row * a.sdo[1] + h * a.sdo[2];
-#pragma unroll 4
-      for (int c = half * 8; c < a.D; c += 16) {
-        const uint4 x = *reinterpret_cast<const uint4 *>(o + c);
-        const uint4 y = *reinterpret_cast<const uint4 *>(e + c);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          delta = fmaf(__uint_as_float(xs[i] << 16), __uint_as_float(ys[i] << 16), delta);
-          delta = fmaf(__uint_as_float(xs[i] & 0xffff0000u), __uint_as_float(ys[i] & 0xffff0000u),
-                       delta);
-        }
-      }
-      const float lse = a.lse[stat];
-      sub = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that sees nothing: P = 0
-    }
-    tail->delta[half][r] = delta;
-    named_bar_sync(1, kPairThreads);
-    delta = tail->delta[0][r] + tail->delta[1][r];
-    if (half == 0 && row < a.Sq) a.delta[stat] = delta;
+    int x = 0, used = 0;  // tiles, and items with tiles, before this one
     bool ok = true;
-    DocRange kr = {0, 0, 0, 0};
-    if (a.q_docs != nullptr && count > 0) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + begin);
-    for (int i = 0; i < count; ++i) {
-      const int n = begin + i, key0 = n * kTile + half * 64;
-      bool whole = n * kTile + kTile - 1 <= first_last;
-      int kd[2];
-      if (a.q_docs != nullptr) {
-        whole = whole && docs_equal(qr, kr);
-        if (!whole) load_docs(a.k_docs + b * a.kds + key0, a.Sk - key0, kd);
-        if (i + 1 < count) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
-      }
-      const uint32_t s_addr = tmem + lanes + (i & 1) * kTile + half * 64;
-      if (!(ok = wait_warp(tail->s_full[i & 1], i >> 1, abort_flag, a.dev_status))) break;
-      tc_fence_after();
-      float w[64];
-      tmem_ld32(s_addr, w);
-      tmem_ld32(s_addr + 32, w + 32);
-      tmem_wait_ld();
-      pin<64>(w);
-      weights<CAP, BIAS, false>(sc, w, nullptr, sub, nullptr, static_cast<float>(pos - key0), -1.f);
-      if (!whole) {
-        uint32_t keep[2] = {~0u, ~0u};
-        if (a.q_docs != nullptr) same_doc(qd, kd, keep);
+    DqItem it;
+    for (int item = 0; ok && next_item(tail, item, it, abort_flag, a.dev_status); ++item) {
+      const int b = it.b, h = it.h, row = it.row0 + r, count = it.count;
+      // delta = do . o, half of the head in each warpgroup
+      float delta = 0.f, sub = -INFINITY;
+      const int64_t stat = (static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row;
+      if (row < a.Sq) {
+        const float lse = __ldcg(a.lse + stat);
+        const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(a.o) + b * a.so[0] +
+                                 row * a.so[1] + h * a.so[2];
+        const __nv_bfloat16 *e = static_cast<const __nv_bfloat16 *>(a.d_o) + b * a.sdo[0] +
+                                 row * a.sdo[1] + h * a.sdo[2];
+        uint4 xo[DH / 16], xe[DH / 16];
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          keep[c] &= bits_to(last - key0 - 32 * c);
-#pragma unroll
-          for (int j = 0; j < 32; ++j)
-            if (!(keep[c] >> j & 1u)) w[c * 32 + j] = 0.f;
+        for (int c = 0; c < DH / 16; ++c) {
+          const int at = (2 * c + half) * 8;
+          xo[c] = xe[c] = make_uint4(0, 0, 0, 0);
+          if (at < a.D) {
+            xo[c] = *reinterpret_cast<const uint4 *>(o + at);
+            xe[c] = *reinterpret_cast<const uint4 *>(e + at);
+          }
         }
-      }
-      if (!(ok = wait_warp(tail->dp_full[i & 1], i >> 1, abort_flag, a.dev_status))) break;
-      tc_fence_after();
-      float dp[64];
-      tmem_ld32(tmem + lanes + 256 + half * 64, dp);
-      tmem_ld32(tmem + lanes + 256 + half * 64 + 32, dp + 32);
-      tmem_wait_ld();
-      pin<64>(dp);
-      tc_fence_before();
-      mbar_arrive(smem_u32(&tail->dp_free));
-      const float2 nd = make_float2(-delta, -delta);
 #pragma unroll
-      for (int j = 0; j < 64; j += 2) {
-        const float2 x = mul2(make_float2(w[j], w[j + 1]),
-                              add2(make_float2(dp[j], dp[j + 1]), nd));
-        dp[j] = x.x;
-        dp[j + 1] = x.y;
-      }
-      if (!whole) {  // a masked pair's dP may be anything
+        for (int c = 0; c < DH / 16; ++c) {
+          const uint32_t u[4] = {xo[c].x, xo[c].y, xo[c].z, xo[c].w};
+          const uint32_t v[4] = {xe[c].x, xe[c].y, xe[c].z, xe[c].w};
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (w[j] == 0.f) dp[j] = 0.f;
+          for (int i = 0; i < 4; ++i) {
+            delta = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), delta);
+            delta = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u),
+                         delta);
+          }
+        }
+        sub = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that sees nothing: P = 0
       }
-      uint32_t z[32];
+      tail->delta[item & 1][half][r] = delta;
+      mbar_arrive(smem_u32(&tail->delta_full));
+      const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
+      const ScoreConst sc = score_const(a, h);
+      const int pos = row + off;
+      const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
+      const int first_last = last_key(a, it.row0 + off, prefix);
+      DocRange qr = {0, 0, 0, 0}, kr = {0, 0, 0, 0};
+      int qd = -1;
+      if (a.q_docs != nullptr) {
+        qr = doc_range(a.q_ranges, int64_t(b) * qtiles + it.row0 / kTile);
+        if (row < a.Sq) qd = a.q_docs[b * a.qds + row];
+        if (count > 0) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + it.begin);
+      }
+      if (!(ok = wait_warp(tail->delta_full, item, abort_flag, a.dev_status))) break;
+      delta = tail->delta[item & 1][0][r] + tail->delta[item & 1][1][r];
+      if (half == 0 && row < a.Sq) a.delta[stat] = delta;
+      for (int i = 0; i < count; ++i, ++x) {
+        const int n = it.begin + i, key0 = n * kTile + half * 64;
+        bool whole = n * kTile + kTile - 1 <= first_last;
+        int kd[2];
+        if (a.q_docs != nullptr) {
+          whole = whole && docs_equal(qr, kr);
+          if (!whole) load_docs(a.k_docs + b * a.kds + key0, a.Sk - key0, kd);
+          if (i + 1 < count) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
+        }
+        const uint32_t s_addr = tmem + lanes + (x & 1) * kTile + half * 64;
+        if (!(ok = wait_warp(tail->s_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
+        tc_fence_after();
+        float w[64];
+        tmem_ld32(s_addr, w);
+        tmem_ld32(s_addr + 32, w + 32);
+        tmem_wait_ld();
+        pin<64>(w);
+        weights<CAP, BIAS, false>(sc, w, nullptr, sub, nullptr, static_cast<float>(pos - key0), -1.f);
+        if (!whole) {
+          uint32_t keep[2] = {~0u, ~0u};
+          if (a.q_docs != nullptr) same_doc(qd, kd, keep);
 #pragma unroll
-      for (int j = 0; j < 32; ++j) z[j] = pack_bf16(dp[2 * j], dp[2 * j + 1]);
-      tmem_st16(s_addr, z);
-      tmem_st16(s_addr + 16, z + 16);
-      tmem_wait_st();
-      tc_fence_before();
-      mbar_arrive(smem_u32(&tail->dz_full));
-    }
-    if (ok && count > 0) {
-      ok = wait_warp(tail->done, 0, abort_flag, a.dev_status);
-    }
-    if (ok) {  // dq through Q's shared memory, half of the columns each
-      tc_fence_after();
+          for (int c = 0; c < 2; ++c) {
+            keep[c] &= bits_to(last - key0 - 32 * c);
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(keep[c] >> j & 1u)) w[c * 32 + j] = 0.f;
+          }
+        }
+        if (!(ok = wait_warp(tail->dp_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
+        tc_fence_after();
+        float dp[64];
+        tmem_ld32(tmem + lanes + 256 + half * 64, dp);
+        tmem_ld32(tmem + lanes + 256 + half * 64 + 32, dp + 32);
+        tmem_wait_ld();
+        pin<64>(dp);
+        tc_fence_before();
+        mbar_arrive(smem_u32(&tail->dp_free));
+        const float2 nd = make_float2(-delta, -delta);
+#pragma unroll
+        for (int j = 0; j < 64; j += 2) {
+          const float2 y = mul2(make_float2(w[j], w[j + 1]),
+                                add2(make_float2(dp[j], dp[j + 1]), nd));
+          dp[j] = y.x;
+          dp[j + 1] = y.y;
+        }
+        if (!whole) {  // a masked pair's dP may be anything
+#pragma unroll
+          for (int j = 0; j < 64; ++j)
+            if (w[j] == 0.f) dp[j] = 0.f;
+        }
+        uint32_t z[32];
+#pragma unroll
+        for (int j = 0; j < 32; ++j) z[j] = pack_bf16(dp[2 * j], dp[2 * j + 1]);
+        tmem_st16(s_addr, z);
+        tmem_st16(s_addr + 16, z + 16);
+        tmem_wait_st();
+        tc_fence_before();
+        mbar_arrive(smem_u32(&tail->dz_full));
+      }
+      if (!ok) break;
+      if (count > 0) {
+        if (!(ok = wait_warp(tail->done, used, abort_flag, a.dev_status))) break;
+        ++used;
+        tc_fence_after();
+      }
+      // dq, half of the columns in each warpgroup
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.dq) + b * a.sdq[0] + row * a.sdq[1] +
+                           h * a.sdq[2];
 #pragma unroll 1
       for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 32) {
         float o[32];
@@ -374,17 +485,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        stage_row32(smem, r, c, o, a.scale);
+        if (row < a.Sq) store_row32(out, c, a.D, o, a.scale);
       }
-      fence_proxy_async_smem();
-    }
-    const bool failed = named_bar_red_or(1, kPairThreads, !ok);
-    if (!failed && threadIdx.x == 0) {
-      for (int c = 0; c < DH / 64; ++c)
-        if (c * 64 < a.D)
-          tma_store_4d(&p.m.dq, smem_u32(smem) + c * kTile * 128, c * 64, row0, h, b);
-      bulk_commit_group();
-      bulk_wait_group0();
+      tc_fence_before();  // dq has been read before the next item's dz is announced
     }
   }
   tc_fence_before();
@@ -403,9 +506,7 @@ struct DkvLayout {
   static constexpr uint32_t kTileBytes = kTile * DH * 2;
   // Q is asked for half a step before dO
   static constexpr int kQSlots = 3, kESlots = 2;
-  // the tiles follow the tail (DkvTail), which for a head of 128 fills what
-  // they leave of an SM's 227 KB: no room to align a base that is not aligned
-  static constexpr uint32_t kTailBytes = 3072;
+  static constexpr uint32_t kTailBytes = 3072;  // as for dq
   static constexpr uint32_t kBytes = kTailBytes + (2 + kQSlots + kESlots) * kTileBytes;
   static constexpr uint32_t kAsked = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
 };
@@ -417,27 +518,37 @@ struct DkvTail {
   uint32_t tmem;
   int abort_flag, lo, hi;
 };
+// Where the blocks of a cluster add up (over the tiles): fp32 rows of dk, then
+// of dv, from every rank.
+template <int DH>
+constexpr int kJoinPitch = DH + 4;
+
 
 template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant__ Params p) {
   using L = DkvLayout<DH>;
-  extern __shared__ __align__(1024) uint8_t raw_dkv[];
-  uint8_t *smem = raw_dkv + L::kTailBytes;
-  DkvTail *tail = reinterpret_cast<DkvTail *>(raw_dkv);
+  extern __shared__ __align__(1024) uint8_t raw[];
+  uint8_t *smem = raw + L::kTailBytes;
+  DkvTail *tail = reinterpret_cast<DkvTail *>(raw);
   static_assert(sizeof(DkvTail) <= L::kTailBytes, "tail");
   const AttnArgs &a = p.a;
-  if ((smem_u32(raw_dkv) & 1023) != 0) {  // not met: the tiles' layout needs it
+  if ((smem_u32(raw) & 1023) != 0) {  // not met: the tiles' layout needs it
     if (threadIdx.x == 0) atomicOr(a.dev_status, kDevErrTimeout);
-    return;
+    return;  // (the same in every block: none waits for another)
   }
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   volatile int *abort_flag = &tail->abort_flag;
 
-  // the first keys of a causal mask are seen by most queries: first
-  const int heads = a.B * a.Hk;
+  // the first keys of a causal mask are seen by most queries: first; with
+  // documents in the order of falling work that was found with their ranges
   const int qtiles = (a.Sq + kTile - 1) / kTile, ktiles = (a.Sk + kTile - 1) / kTile;
-  const int kt = blockIdx.x / heads;
-  const int bg = blockIdx.x % heads, b = bg / a.Hk, g = bg % a.Hk;
+  const int ranks = p.cluster, rank = static_cast<int>(blockIdx.x) % ranks;
+  const int item = static_cast<int>(blockIdx.x) / ranks, g = item % a.Hk;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int entry = a.order != nullptr ? __ldcg(a.order + item / a.Hk) : item / a.Hk;
+  const int b = a.order != nullptr ? entry / ktiles : entry % a.B;
+  const int kt = a.order != nullptr ? entry % ktiles : entry / a.B;
   const int key0 = kt * kTile, off = a.Sk - a.Sq;
 
   if (threadIdx.x == 0) {
@@ -459,8 +570,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     tma_prefetch(&p.m.v);
     tma_prefetch(&p.m.d_o);
   }
-  griddep_wait();
-  griddep_launch_dependents();
   if (warp == 9) {
     tmem_alloc(smem_u32(&tail->tmem), 512);
     tmem_relinquish();
@@ -487,8 +596,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   }
   __syncthreads();
   const int end = uniform(tail->hi), begin = uniform(min(tail->lo, end));
-  const int per_head = end - begin, count = per_head * a.group;
-  // step i: query head g * group + i / per_head, tile begin + i % per_head
+  const int per_head = end - begin, all = per_head * a.group;
+  // step i of the item: query head g * group + i / per_head, tile begin + i %
+  // per_head; this rank's are `count` from step0 on
+  const int step0 = static_cast<int>(int64_t(all) * rank / ranks);
+  const int count = static_cast<int>(int64_t(all) * (rank + 1) / ranks) - step0;
 
   if (warp >= 8) {
     set_max_regs_down<kIssueRegs>();
@@ -509,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
           const int s = i % L::kQSlots;
           mbar_expect_tx(smem_u32(&tail->q_full[s]), L::kTileBytes);
           load(q_ring + s * L::kTileBytes, &p.m.q, tail->q_full[s],
-               (begin + i % per_head) * kTile, g * a.group + i / per_head);
+               (begin + (step0 + i) % per_head) * kTile,
+               g * a.group + (step0 + i) / per_head);
           ++nq;
         };
         load_q(0);
@@ -525,7 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
           const int s = i % L::kESlots;
           mbar_expect_tx(smem_u32(&tail->e_full[s]), L::kTileBytes);
           load(e_ring + s * L::kTileBytes, &p.m.d_o, tail->e_full[s],
-               (begin + i % per_head) * kTile, g * a.group + i / per_head);
+               (begin + (step0 + i) % per_head) * kTile,
+               g * a.group + (step0 + i) / per_head);
           ++ne;
           if (i + 1 < count) load_q(i + 1);
         }
@@ -543,14 +657,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         return wait_warp(bar, phase, abort_flag, a.dev_status);
       };
       auto padded = [&](int i) {
-        return a.q_docs != nullptr && i < count &&
-               doc_range(a.q_ranges, int64_t(b) * qtiles + begin + i % per_head).padded;
+        return a.q_docs != nullptr && i < count
+                   ? doc_range(a.q_ranges, int64_t(b) * qtiles + begin + (step0 + i) % per_head).padded
+                   : 0;
       };
-      bool pads_q = padded(0), pads_e = pads_q;
+      int pads_q = padded(0), pads_e = pads_q;
       // a tile of step i has landed; without the rows of padding
-      auto clear = [&](bool now, int tile, int i) {
-        const int token = (begin + i % per_head) * kTile;
-        if (now)
+      auto clear = [&](int now, int tile, int i) {
+        const int token = (begin + (step0 + i) % per_head) * kTile;
+        if (now != 0)
           zero_padding_rows<DH>(smem + tile * L::kTileBytes, a.q_docs + b * a.qds + token,
                                 a.Sq - token);
       };
@@ -608,6 +723,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       mbar_wait_drain(smem_u32(&tail->drain), 0);
       __syncwarp();
     }
+    if (ranks > 1) {  // the pairs' two barriers of the cluster
+      __syncwarp();
+      cluster_sync();
+      cluster_sync();
+    }
   } else {
     set_max_regs_up<kPairRegs>();
     // ------------------------------------------------------ pairs
@@ -634,9 +754,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     };
     bool ok = true;
     DocRange qr = {0, 0, 0, 0};
-    if (a.q_docs != nullptr && count > 0) qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin);
-    if (count > 0) put(0, fetch(g * a.group, begin));
-    int head = g * a.group, n = begin, head1 = head, n1 = begin;  // this step, the next
+    if (a.q_docs != nullptr && count > 0) qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin + step0 % per_head);
+    int head = g * a.group, n = begin;  // of this step
+    if (count > 0) {
+      head += step0 / per_head;
+      n += step0 % per_head;
+      put(0, fetch(head, n));
+    }
+    int head1 = head, n1 = n;  // of the next
     for (int i = 0; i < count; ++i, head = head1, n = n1) {
       if (++n1 == end) {
         n1 = begin;
@@ -725,33 +850,65 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     if (ok && count > 0) {
       ok = wait_warp(tail->done, 0, abort_flag, a.dev_status);
     }
-    // one warpgroup stages dk (in K's memory), the other dv (in V's)
-    uint8_t *stage = smem + half * L::kTileBytes;
-    if (ok) {
-      tc_fence_after();
+    ok = !named_bar_red_or(1, kPairThreads, !ok);
+    // one warpgroup has dk, the other dv
+    const uint32_t sum_addr = tmem + lanes + (half == 0 ? 384 : 256);
+    const int64_t *stride = half == 0 ? a.sdk : a.sdv;
+    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(half == 0 ? a.dk : a.dv) + b * stride[0] +
+                         g * stride[2];
+    const float by = half == 0 ? a.scale : 1.f;
+    auto sum_of = [&](int c, float (&o)[32]) {
+      if (count > 0) {
+        tmem_ld32(sum_addr + c, o);
+        tmem_wait_ld();
+        pin<32>(o);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = 0.f;
+      }
+    };
+    tc_fence_after();
+    if (ranks == 1) {
+      if (ok)
+#pragma unroll 1
+        for (int c = 0; c < DH; c += 32) {
+          float o[32];
+          sum_of(c, o);
+          if (key < a.Sk) store_row32(out + key * stride[1], c, a.D, o, by);
+        }
+    } else {
+      cluster_sync();  // every block is done with the tiles that the sums go over
+      const int rows = kTile / ranks;  // of each rank
+      constexpr int kPitch = kJoinPitch<DH>;
+      float *join = reinterpret_cast<float *>(smem) + half * kTile * kPitch;
+      const uint32_t to = dsmem_map(
+          smem_u32(join + (rank * rows + r % rows) * kPitch), static_cast<uint32_t>(r / rows));
 #pragma unroll 1
       for (int c = 0; c < DH; c += 32) {
         float o[32];
-        if (count > 0) {
-          tmem_ld32(tmem + lanes + (half == 0 ? 384 : 256) + c, o);
-          tmem_wait_ld();
-          pin<32>(o);
-        } else {
+        sum_of(c, o);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) o[e] = 0.f;
-        }
-        stage_row32(stage, r, c, o, half == 0 ? a.scale : 1.f);
+        for (int e = 0; e < 32; e += 4)
+          dsmem_st_f4(to + (c + e) * 4, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]));
       }
-      fence_proxy_async_smem();
-    }
-    const bool failed = named_bar_red_or(1, kPairThreads, !ok);
-    if (!failed && r == 0) {
-      for (int c = 0; c < DH / 64; ++c)
-        if (c * 64 < a.D)
-          tma_store_4d(half == 0 ? &p.m.dk : &p.m.dv, smem_u32(stage) + c * kTile * 128, c * 64,
-                       key0, g, b);
-      bulk_commit_group();
-      bulk_wait_group0();
+      cluster_sync();
+      // this rank's rows, the ranks' sums in order
+      if (ok)
+        for (int x = r; x < rows * (DH / 4); x += kTile) {
+          const int lr = x / (DH / 4), c = x % (DH / 4) * 4, at = key0 + rank * rows + lr;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int s = 0; s < ranks; ++s) {
+            const float4 v =
+                *reinterpret_cast<const float4 *>(join + (s * rows + lr) * kPitch + c);
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+          }
+          if (at < a.Sk && c < a.D)
+            *reinterpret_cast<uint2 *>(out + at * stride[1] + c) =
+                make_uint2(pack_bf16(acc.x * by, acc.y * by), pack_bf16(acc.z * by, acc.w * by));
+        }
     }
   }
   tc_fence_before();
@@ -763,41 +920,56 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
 }
 
 template <int DH, bool CAP, bool BIAS>
-cudaError_t start_dq(const Params &p, cudaStream_t s) {
-  constexpr size_t smem = DqLayout<DH>::kAsked + sizeof(DqTail) + 1024;
+cudaError_t start_dq(const Params &p, int sms, cudaStream_t s) {
+  constexpr size_t smem = DqLayout<DH>::kAsked;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(k_attn_dq<DH, CAP, BIAS>, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = int64_t(p.a.B) * p.a.Hq * ((p.a.Sq + kTile - 1) / kTile);
-  return launch_pdl(k_attn_dq<DH, CAP, BIAS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
+  return launch_pdl(k_attn_dq<DH, CAP, BIAS>, dim3(p.items < sms ? p.items : sms), dim3(kThreads),
                     smem, s, p);
 }
 template <int DH, bool CAP, bool BIAS>
-cudaError_t start_dkv(const Params &p, cudaStream_t s) {
+cudaError_t start_dkv(const Params &p, int, cudaStream_t s) {
   constexpr size_t smem = DkvLayout<DH>::kAsked;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(k_attn_dkv<DH, CAP, BIAS>, smem, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = int64_t(p.a.B) * p.a.Hk * ((p.a.Sk + kTile - 1) / kTile);
-  return launch_pdl(k_attn_dkv<DH, CAP, BIAS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads),
-                    smem, s, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.items) * p.cluster);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_attn_dkv<DH, CAP, BIAS>, p);
 }
 
 }  // namespace
 
 #define LORA_ATTN_VARIANT(f)                                                            \
-  const Params p{a, m};                                                                 \
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;                             \
   if (a.D <= 64)                                                                        \
-    return cap ? (bias ? f<64, true, true>(p, s) : f<64, true, false>(p, s))            \
-               : (bias ? f<64, false, true>(p, s) : f<64, false, false>(p, s));         \
-  return cap ? (bias ? f<128, true, true>(p, s) : f<128, true, false>(p, s))            \
-             : (bias ? f<128, false, true>(p, s) : f<128, false, false>(p, s))
+    return cap ? (bias ? f<64, true, true>(p, sms, s) : f<64, true, false>(p, sms, s))  \
+               : (bias ? f<64, false, true>(p, sms, s) : f<64, false, false>(p, sms, s)); \
+  return cap ? (bias ? f<128, true, true>(p, sms, s) : f<128, true, false>(p, sms, s))  \
+             : (bias ? f<128, false, true>(p, sms, s) : f<128, false, false>(p, sms, s))
 
-cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s) {
+cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s) {
+  const Params p{a, m, a.B * a.Hq * ((a.Sq + kTile - 1) / kTile), 1};
   LORA_ATTN_VARIANT(start_dq);
 }
-cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, cudaStream_t s) {
+
+cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s) {
+  Params p{a, m, a.B * a.Hk * ((a.Sk + kTile - 1) / kTile), 1};
+  // blocks of an item: enough for two rounds of the SMs, as far as its steps go
+  const int steps = a.group * ((a.Sq + kTile - 1) / kTile);
+  while (p.cluster < 8 && p.items * p.cluster < 2 * sms && steps >= 4 * p.cluster) p.cluster *= 2;
   LORA_ATTN_VARIANT(start_dkv);
 }
 

@@ -250,15 +250,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           commit(on, smem_u32(&tail->s_full[t]));
         };
         auto padded = [&](int i) {
-          return a.q_docs != nullptr && i < count &&
-                 doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded;
+          return a.q_docs != nullptr && i < count
+                     ? doc_range(a.k_ranges, int64_t(b) * ktiles + begin + i).padded
+                     : 0;
         };
         // V's tile i has landed; without the rows of padding
-        bool pads = padded(0);
+        int pads = padded(0);  // looked at a step later: not waited for here
         auto wait_v = [&](int i) {
           const int s = (base + i) % L::kVSlots, token = (begin + i) * kTile;
           if (!wait(tail->v_full[s], (base + i) / L::kVSlots)) return false;
-          if (pads)
+          if (pads != 0)
             zero_padding_rows<DH>(smem + (2 + L::kKSlots + s) * L::kTileBytes,
                                   a.k_docs + b * a.kds + token, a.Sk - token);
           pads = padded(i + 1);
@@ -469,34 +470,90 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   }
 }
 
-// Ranges of the documents of 128-token tiles, one warp per tile; zeroes the
-// counters that items are handed out from.
-__global__ void k_attn_ranges(const int *docs, int64_t stride, int B, int S, int4 *out,
-                              unsigned *counters) {
+// Ranges of the documents of 128-token tiles of the queries, then of the keys,
+// one warp per tile; zeroes the counters that items are handed out from.
+__global__ void k_attn_ranges(const AttnArgs a) {
   griddep_wait();
   griddep_launch_dependents();
-  if (counters != nullptr && blockIdx.x == 0 && threadIdx.x < kAttnCounters)
-    counters[threadIdx.x] = 0;
-  const int tiles = (S + kTile - 1) / kTile;
+  if (blockIdx.x == 0 && threadIdx.x < kAttnCounters) a.counter[threadIdx.x] = 0;
+  const int qtiles = (a.Sq + kTile - 1) / kTile, ktiles = (a.Sk + kTile - 1) / kTile;
   const int w = (blockIdx.x * blockDim.x + threadIdx.x) / 32, lane = threadIdx.x % 32;
-  if (w >= B * tiles) return;
-  const int b = w / tiles, n = w % tiles;
+  const bool keys = w >= a.B * qtiles;
+  const int i = keys ? w - a.B * qtiles : w, tiles = keys ? ktiles : qtiles;
+  if (i >= a.B * tiles) return;
+  const int b = i / tiles, n = i % tiles, S = keys ? a.Sk : a.Sq;
+  const int *docs = keys ? a.k_docs + b * a.kds : a.q_docs + b * a.qds;
   int lo = INT_MAX, hi = -1, padded = 0;
-  for (int i = lane; i < kTile; i += 32) {
-    const int at = n * kTile + i;
-    if (at >= S) break;
-    const int d = docs[b * stride + at];
-    if (d < 0) {
-      padded = 1;
-    } else {
-      lo = min(lo, d);
-      hi = max(hi, d);
+#pragma unroll
+  for (int c = 0; c < kTile / 32; ++c) {
+    const int at = n * kTile + 32 * c + lane;
+    if (at < S) {
+      const int d = docs[at];
+      if (d < 0) {
+        padded = 1;
+      } else {
+        lo = min(lo, d);
+        hi = max(hi, d);
+      }
     }
   }
   lo = __reduce_min_sync(~0u, lo);
   hi = __reduce_max_sync(~0u, hi);
   padded = __any_sync(~0u, padded);
-  if (lane == 0) out[w] = make_int4(lo, hi, padded, 0);
+  if (lane == 0) const_cast<int4 *>(keys ? a.k_ranges : a.q_ranges)[i] = make_int4(lo, hi, padded, 0);
+}
+
+// Key tiles in the order of falling work (the query tiles that see them), by
+// one block: a counting sort into kBuckets.  The order inside a bucket may
+// differ from run to run; no result depends on it.
+constexpr int kOrderThreads = 1024, kBuckets = 1024;
+__global__ void __launch_bounds__(kOrderThreads) k_attn_order(const AttnArgs a) {
+  __shared__ int count[kBuckets];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int qtiles = (a.Sq + kTile - 1) / kTile, ktiles = (a.Sk + kTile - 1) / kTile;
+  const int off = a.Sk - a.Sq, tiles = a.B * ktiles;
+  count[threadIdx.x] = 0;
+  __syncthreads();
+  auto bucket = [&](int i) {  // 0: most work
+    const int b = i / ktiles, n = i % ktiles;
+    const DocRange kr = doc_range(a.k_ranges, i);
+    const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
+    const int first = a.causal && n * kTile >= prefix ? max(0, n * kTile - off) / kTile : 0;
+    int from = INT_MAX, to = 0;
+    for (int x = first; x < qtiles; ++x)
+      if (docs_meet(kr, doc_range(a.q_ranges, int64_t(b) * qtiles + x))) {
+        from = min(from, x);
+        to = x + 1;
+      }
+    const int work = max(0, to - min(from, to));
+    return kBuckets - 1 - static_cast<int>(int64_t(work) * (kBuckets - 1) / max(qtiles, 1));
+  };
+  // (a tile's bucket is found twice where a thread has more than one)
+  const int mine = threadIdx.x < tiles ? bucket(threadIdx.x) : 0;
+  if (threadIdx.x < tiles) atomicAdd(&count[mine], 1);
+  for (int i = threadIdx.x + kOrderThreads; i < tiles; i += kOrderThreads)
+    atomicAdd(&count[bucket(i)], 1);
+  __syncthreads();
+  // each bucket's first place
+  const int own = count[threadIdx.x];
+  int sum = own;
+#pragma unroll
+  for (int d = 1; d < 32; d *= 2) {
+    const int y = __shfl_up_sync(~0u, sum, d);
+    if (threadIdx.x % 32 >= d) sum += y;
+  }
+  __shared__ int warps[32];
+  if (threadIdx.x % 32 == 31) warps[threadIdx.x / 32] = sum;
+  __syncthreads();
+  int before = 0;
+  for (int w = 0; w < static_cast<int>(threadIdx.x) / 32; ++w) before += warps[w];
+  count[threadIdx.x] = before + sum - own;
+  __syncthreads();
+  int *order = const_cast<int *>(a.order);
+  if (threadIdx.x < tiles) order[atomicAdd(&count[mine], 1)] = threadIdx.x;
+  for (int i = threadIdx.x + kOrderThreads; i < tiles; i += kOrderThreads)
+    order[atomicAdd(&count[bucket(i)], 1)] = i;
 }
 
 template <int DH, bool CAP, bool BIAS>
@@ -512,17 +569,11 @@ cudaError_t launch(const Params &p, int sms, cudaStream_t s) {
 }  // namespace
 
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s) {
-  for (int side = 0; side < 2; ++side) {
-    const int S = side ? a.Sk : a.Sq;
-    const int64_t tiles = int64_t(a.B) * ((S + kTile - 1) / kTile);
-    if (tiles == 0) continue;
-    const cudaError_t e = launch_pdl(
-        k_attn_ranges, dim3(static_cast<unsigned>((tiles + 7) / 8)), dim3(256), 0, s,
-        side ? a.k_docs : a.q_docs, side ? a.kds : a.qds, a.B, S,
-        const_cast<int4 *>(side ? a.k_ranges : a.q_ranges), side ? nullptr : a.counter);
-    if (e != cudaSuccess) return e;
-  }
-  return cudaSuccess;
+  const int64_t tiles = int64_t(a.B) * ((a.Sq + kTile - 1) / kTile + (a.Sk + kTile - 1) / kTile);
+  return launch_pdl(k_attn_ranges, dim3(static_cast<unsigned>((tiles + 7) / 8)), dim3(256), 0, s, a);
+}
+cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s) {
+  return launch_pdl(k_attn_order, dim3(1), dim3(kOrderThreads), 0, s, a);
 }
 
 cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s) {
