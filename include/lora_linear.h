@@ -207,9 +207,9 @@ typedef enum {
     LORA_K_ROTARY = 11,         /* rotary positions of q and k               */
     LORA_K_GRAD_NORM = 12,      /* global gradient norm                      */
     LORA_K_GRAD_CLIP = 13,      /* gradients scaled by the clip factor       */
-    LORA_K_ATTN_PREP = 14,      /* attention: document ranges of the tiles   */
+    LORA_K_ATTN_PREP = 14,      /* attention: document ranges, row statistics */
     LORA_K_ATTN_FWD = 15,       /* attention: output and log-sum-exp         */
-    LORA_K_ATTN_DQ = 16,        /* attention: dq (and rowsum(do * o))        */
+    LORA_K_ATTN_DQ = 16,        /* attention: dq                             */
     LORA_K_ATTN_DKV = 17,       /* attention: dk and dv                      */
     LORA_K_ATTN_TOKEN = 18      /* attention: one new token over a cache     */
 } lora_kernel_kind_t;

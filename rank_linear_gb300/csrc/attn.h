@@ -16,7 +16,10 @@ struct AttnArgs {
   int64_t sdo[3] = {}, sdq[3] = {}, sdk[3] = {}, sdv[3] = {};
   const void *q = nullptr, *k = nullptr, *v = nullptr, *d_o = nullptr;
   void *o = nullptr, *dq = nullptr, *dk = nullptr, *dv = nullptr;
-  float *lse = nullptr, *delta = nullptr;
+  float *lse = nullptr;
+  // backward, [batch][q_heads][q_len rounded up to a tile]: -lse in log2 units
+  // (-inf where nothing is seen, and past the end), and -do . o
+  float *sub = nullptr, *neg_delta = nullptr;
   const float *slopes = nullptr;
   const int *q_docs = nullptr, *k_docs = nullptr, *prefix = nullptr, *lengths = nullptr;
   int64_t qds = 0, kds = 0;
@@ -45,6 +48,7 @@ struct AttnBwdMaps {
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s);
+cudaError_t launch_attn_stats(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s);
 cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s);
 

@@ -115,9 +115,9 @@ lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], 
 }
 
 // Workspace: [document ranges of the query tiles, of the key tiles][item
-// counters][order of the key tiles][delta].
+// counters][order of the key tiles][statistics of the query rows, two].
 struct Plan {
-  size_t q_ranges = 0, k_ranges = 0, counter = 0, order = 0, delta = 0, bytes = 0;
+  size_t q_ranges = 0, k_ranges = 0, counter = 0, order = 0, sub = 0, neg_delta = 0, bytes = 0;
 };
 Plan make_plan(const lora_attention_t *p, bool backward) {
   Plan w;
@@ -133,8 +133,11 @@ Plan make_plan(const lora_attention_t *p, bool backward) {
     if (backward) off += rup(size_t(p->batch) * tiles_of(p->k_len) * 4, 256);
   }
   if (backward) {
-    w.delta = off;
-    off += rup(size_t(p->batch) * p->q_heads * p->q_len * 4, 256);
+    const size_t rows = size_t(p->batch) * p->q_heads * tiles_of(p->q_len) * 128;
+    w.sub = off;
+    off += rup(rows * 4, 256);
+    w.neg_delta = off;
+    off += rup(rows * 4, 256);
   }
   w.bytes = off;
   return w;
@@ -246,7 +249,8 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
   a.dq = dq;
   a.dk = dk;
   a.dv = dv;
-  a.delta = reinterpret_cast<float *>(at(workspace, w.delta));
+  a.sub = reinterpret_cast<float *>(at(workspace, w.sub));
+  a.neg_delta = reinterpret_cast<float *>(at(workspace, w.neg_delta));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   AttnBwdMaps m;
   LORA_TRY(tensor_map(&m.q, no_q ? k : q, shape->q, a, a.Sq, a.Hq, "q"));
@@ -254,6 +258,9 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
   LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
   LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
   LORA_TRY(make_ranges(a, w, workspace, true, st));
+  if (!no_q)
+    LORA_TRY(run(LORA_K_ATTN_PREP, st, "statistics of the rows",
+                 [&] { return launch_attn_stats(a, st); }));
   if (!no_q)
     LORA_TRY(run(LORA_K_ATTN_DQ, st, "attention dq", [&] { return launch_attn_dq(a, m, di.sms, st); }));
   if (!no_k)

@@ -9,6 +9,11 @@
 // as bf16 over the scores (or over dP) and is the TMEM operand of the products
 // that follow; nothing of size q_len x k_len leaves the SM.
 //
+// A small pass before them leaves two numbers of each query row, -lse in log2
+// units and -delta = -do . o, in rows of whole tiles: read once for both
+// kernels.  (Formed in the dq kernel they cost an item 3600 to 10000 cycles,
+// or 22000 of the first one in warps of their own.)
+//
 // The dq blocks stay and take item after item, as the forward's do.  A dk/dv
 // item has a group's heads times as much work; where there are too few for the
 // SMs, the blocks of a cluster share one, each with its part of the steps, and
@@ -76,6 +81,68 @@ __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], flo
   }
 }
 
+// ---------------------------------------------------------------- statistics
+// A warp takes 32 queries of one head (its neighbours the next heads, which
+// lie beside it), DH / 8 lanes to a row.
+constexpr int kStatWarps = 8;
+template <int DH>
+__global__ void __launch_bounds__(32 * kStatWarps) k_attn_stats(const AttnArgs a) {
+  constexpr int kLanes = DH / 8, kRows = 32 / kLanes, kLoads = 8;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int lane = threadIdx.x % 32, groups = (a.Hq + kStatWarps - 1) / kStatWarps;
+  const int padded = (a.Sq + kTile - 1) / kTile * kTile, blocks = padded / 32;
+  int id = blockIdx.x;
+  const int h = id % groups * kStatWarps + threadIdx.x / 32;
+  id /= groups;
+  const int row0 = id % blocks * 32, b = id / blocks;
+  if (h >= a.Hq) return;
+  const int e = lane % kLanes * 8;
+  const __nv_bfloat16 *o =
+      static_cast<const __nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2] + e;
+  const __nv_bfloat16 *g =
+      static_cast<const __nv_bfloat16 *>(a.d_o) + b * a.sdo[0] + h * a.sdo[2] + e;
+  const int64_t row = static_cast<int64_t>(b) * a.Hq + h;
+  float lse = -INFINITY, delta = 0.f;  // of query row0 + lane
+  if (row0 + lane < a.Sq) lse = __ldcg(a.lse + row * a.Sq + row0 + lane);
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kLoads * kRows) {
+    uint4 xo[kLoads], xg[kLoads];
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const int64_t at = row0 + r0 + i * kRows + lane / kLanes;
+      xo[i] = xg[i] = make_uint4(0, 0, 0, 0);
+      if (at < a.Sq && e < a.D) {
+        xo[i] = __ldcg(reinterpret_cast<const uint4 *>(o + at * a.so[1]));
+        xg[i] = __ldcg(reinterpret_cast<const uint4 *>(g + at * a.sdo[1]));
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i) {
+      const uint32_t u[4] = {xo[i].x, xo[i].y, xo[i].z, xo[i].w};
+      const uint32_t v[4] = {xg[i].x, xg[i].y, xg[i].z, xg[i].w};
+      float d = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        d = fmaf(__uint_as_float(u[k] << 16), __uint_as_float(v[k] << 16), d);
+        d = fmaf(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(v[k] & 0xffff0000u), d);
+      }
+#pragma unroll
+      for (int y = 1; y < kLanes; y *= 2) d += __shfl_xor_sync(~0u, d, y);
+      // row r0 + i kRows + j is in the lanes of group j: hand it to its owner
+#pragma unroll
+      for (int j = 0; j < kRows; ++j) {
+        const float x = __shfl_sync(~0u, d, j * kLanes);
+        if (lane == r0 + i * kRows + j) delta = x;
+      }
+    }
+  }
+  const int64_t at = row * padded + row0 + lane;
+  // a query that sees nothing, or lies past the end: P = 0
+  a.sub[at] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;
+  a.neg_delta[at] = -delta;
+}
+
 // ---------------------------------------------------------------- dq
 // Shared memory: Q, dO, then rings of K and V tiles (counted on over the items).  TMEM: the scores (then
 // dz) of two tiles at 0 and 128, dP at 256, dq at 384.
@@ -97,12 +164,12 @@ struct DqItem {
 };
 struct DqTail {
   uint64_t q_full, q_free, k_full[3], k_empty[3], v_full[2];
-  uint64_t s_full[2], dp_full[2], dp_free, dz_full, delta_full, done, drain;
+  uint64_t s_full[2], dp_full[2], dp_free, done, drain;
+  uint64_t dz_full[2];  // by tile modulo 2: tile x + 1's may come before x's is waited for
   uint64_t item_full[kItemSlots], item_free[kItemSlots];
   DqItem item[kItemSlots];
   uint32_t tmem;
   int abort_flag;
-  float delta[2][2][kTile];  // by item modulo 2, half of the head
 };
 
 __device__ __forceinline__ bool next_item(DqTail *tail, int n, DqItem &item,
@@ -144,10 +211,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       mbar_init(smem_u32(&tail->v_full[s]), 1);
       mbar_init(smem_u32(&tail->s_full[s]), 1);
       mbar_init(smem_u32(&tail->dp_full[s]), 1);
+      mbar_init(smem_u32(&tail->dz_full[s]), kPairThreads);
     }
     mbar_init(smem_u32(&tail->dp_free), kPairThreads);
-    mbar_init(smem_u32(&tail->dz_full), kPairThreads);
-    mbar_init(smem_u32(&tail->delta_full), kPairThreads);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(smem_u32(&tail->item_full[s]), 1);
       mbar_init(smem_u32(&tail->item_free[s]), kItemReaders);
@@ -219,6 +285,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         if (lane == 0) {
           tail->item[s] = it;
           mbar_arrive(smem_u32(&tail->item_full[s]));  // releases the item's words
+          if (it.count > 0)  // what it begins with, towards L2
+            for (int c = 0; c < DH; c += 64) {
+              tma_prefetch_4d(&p.m.q, c, it.row0, it.h, it.b);
+              tma_prefetch_4d(&p.m.d_o, c, it.row0, it.h, it.b);
+              tma_prefetch_4d(&p.m.k, c, it.begin * kTile, it.h / a.group, it.b);
+              tma_prefetch_4d(&p.m.v, c, it.begin * kTile, it.h / a.group, it.b);
+            }
         }
         __syncwarp();
         if (it.count < 0) break;
@@ -332,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
             tc_fence_after();
             do_v(i + 1);
           }
-          if (!(ok = wait(tail->dz_full, x))) break;
+          if (!(ok = wait(tail->dz_full[x & 1], x >> 1))) break;
           tc_fence_after();
           mma_over_tokens<DH, 0, 8>(on, tmem + 384, tmem + (x & 1) * kTile, operand_cols,
                                     k_ring + (x % L::kKSlots) * L::kTileBytes, i > 0);
@@ -356,40 +429,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     DqItem it;
     for (int item = 0; ok && next_item(tail, item, it, abort_flag, a.dev_status); ++item) {
       const int b = it.b, h = it.h, row = it.row0 + r, count = it.count;
-      // delta = do . o, half of the head in each warpgroup
-      float delta = 0.f, sub = -INFINITY;
-      const int64_t stat = (static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row;
-      if (row < a.Sq) {
-        const float lse = __ldcg(a.lse + stat);
-        const __nv_bfloat16 *o = static_cast<const __nv_bfloat16 *>(a.o) + b * a.so[0] +
-                                 row * a.so[1] + h * a.so[2];
-        const __nv_bfloat16 *e = static_cast<const __nv_bfloat16 *>(a.d_o) + b * a.sdo[0] +
-                                 row * a.sdo[1] + h * a.sdo[2];
-        uint4 xo[DH / 16], xe[DH / 16];
-#pragma unroll
-        for (int c = 0; c < DH / 16; ++c) {
-          const int at = (2 * c + half) * 8;
-          xo[c] = xe[c] = make_uint4(0, 0, 0, 0);
-          if (at < a.D) {
-            xo[c] = *reinterpret_cast<const uint4 *>(o + at);
-            xe[c] = *reinterpret_cast<const uint4 *>(e + at);
-          }
-        }
-#pragma unroll
-        for (int c = 0; c < DH / 16; ++c) {
-          const uint32_t u[4] = {xo[c].x, xo[c].y, xo[c].z, xo[c].w};
-          const uint32_t v[4] = {xe[c].x, xe[c].y, xe[c].z, xe[c].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            delta = fmaf(__uint_as_float(u[i] << 16), __uint_as_float(v[i] << 16), delta);
-            delta = fmaf(__uint_as_float(u[i] & 0xffff0000u), __uint_as_float(v[i] & 0xffff0000u),
-                         delta);
-          }
-        }
-        sub = lse == -INFINITY ? -INFINITY : -lse * kLog2e;  // a row that sees nothing: P = 0
-      }
-      tail->delta[item & 1][half][r] = delta;
-      mbar_arrive(smem_u32(&tail->delta_full));
+      const int64_t stat = (static_cast<int64_t>(b) * a.Hq + h) * (qtiles * kTile) + row;
+      const float sub = __ldcg(a.sub + stat), neg_delta = __ldcg(a.neg_delta + stat);
       const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
       const ScoreConst sc = score_const(a, h);
       const int pos = row + off;
@@ -402,9 +443,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         if (row < a.Sq) qd = a.q_docs[b * a.qds + row];
         if (count > 0) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + it.begin);
       }
-      if (!(ok = wait_warp(tail->delta_full, item, abort_flag, a.dev_status))) break;
-      delta = tail->delta[item & 1][0][r] + tail->delta[item & 1][1][r];
-      if (half == 0 && row < a.Sq) a.delta[stat] = delta;
       for (int i = 0; i < count; ++i, ++x) {
         const int n = it.begin + i, key0 = n * kTile + half * 64;
         bool whole = n * kTile + kTile - 1 <= first_last;
@@ -443,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         pin<64>(dp);
         tc_fence_before();
         mbar_arrive(smem_u32(&tail->dp_free));
-        const float2 nd = make_float2(-delta, -delta);
+        const float2 nd = make_float2(neg_delta, neg_delta);
 #pragma unroll
         for (int j = 0; j < 64; j += 2) {
           const float2 y = mul2(make_float2(w[j], w[j + 1]),
@@ -463,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         tmem_st16(s_addr + 16, z + 16);
         tmem_wait_st();
         tc_fence_before();
-        mbar_arrive(smem_u32(&tail->dz_full));
+        mbar_arrive(smem_u32(&tail->dz_full[x & 1]));
       }
       if (!ok) break;
       if (count > 0) {
@@ -472,8 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         tc_fence_after();
       }
       // dq, half of the columns in each warpgroup
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.dq) + b * a.sdq[0] + row * a.sdq[1] +
-                           h * a.sdq[2];
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.dq) + b * a.sdq[0] + h * a.sdq[2];
 #pragma unroll 1
       for (int c = half * (DH / 2); c < (half + 1) * (DH / 2); c += 32) {
         float o[32];
@@ -485,7 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
 #pragma unroll
           for (int e = 0; e < 32; ++e) o[e] = 0.f;
         }
-        if (row < a.Sq) store_row32(out, c, a.D, o, a.scale);
+        store_rows32(out, a.sdq[1], row - lane, a.Sq, c, a.D, o, a.scale);
       }
       tc_fence_before();  // dq has been read before the next item's dz is announced
     }
@@ -511,8 +548,7 @@ struct DkvLayout {
   static constexpr uint32_t kAsked = kBytes > 120 * 1024 ? kBytes : 120 * 1024;
 };
 struct DkvTail {
-  // per tile of queries: -lse in log2 units, and -delta
-  float sub[2][kTile], neg_delta[2][kTile];
+  float sub[2][kTile], neg_delta[2][kTile];  // of a step's queries, copied with dO
   uint64_t k_full, q_full[3], e_full[2];
   uint64_t s_full, dp_full, p_full, dz_full, done, drain;
   uint32_t tmem;
@@ -636,7 +672,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
               !mbar_wait(smem_u32(&tail->dp_full), (i - 1) & 1, abort_flag, a.dev_status))
             break;
           const int s = i % L::kESlots;
-          mbar_expect_tx(smem_u32(&tail->e_full[s]), L::kTileBytes);
+          mbar_expect_tx(smem_u32(&tail->e_full[s]), L::kTileBytes + 2 * kTile * 4);
+          const int64_t stat =
+              ((static_cast<int64_t>(b) * a.Hq + g * a.group + (step0 + i) / per_head) * qtiles +
+               begin + (step0 + i) % per_head) * kTile;
+          bulk_load(smem_u32(tail->sub[s]), a.sub + stat, kTile * 4, smem_u32(&tail->e_full[s]));
+          bulk_load(smem_u32(tail->neg_delta[s]), a.neg_delta + stat, kTile * 4,
+                    smem_u32(&tail->e_full[s]));
           load(e_ring + s * L::kTileBytes, &p.m.d_o, tail->e_full[s],
                (begin + (step0 + i) % per_head) * kTile,
                g * a.group + (step0 + i) / per_head);
@@ -739,19 +781,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     const int tile_last = key0 + kTile - 1;
     const int all_from = a.causal && tile_last >= prefix ? tile_last - off : -(1 << 28);
     const int kd = a.q_docs != nullptr && key < a.Sk ? a.k_docs[b * a.kds + key] : -1;
-    // one of the two statistics of a query, fetched a step ahead: lse or delta
-    const float *stat = (half == 0 ? a.lse : a.delta) + static_cast<int64_t>(b) * a.Hq * a.Sq;
-    auto fetch = [&](int head, int n) {
-      const int q = n * kTile + r;
-      return q < a.Sq ? __ldcg(stat + static_cast<int64_t>(head) * a.Sq + q)
-                      : half == 0 ? -INFINITY : 0.f;
-    };
-    auto put = [&](int i, float v) {
-      if (half == 0)  // a query that sees nothing (lse = -inf): P = 0
-        tail->sub[i & 1][r] = v == -INFINITY ? -INFINITY : -v * kLog2e;
-      else
-        tail->neg_delta[i & 1][r] = -v;
-    };
     bool ok = true;
     DocRange qr = {0, 0, 0, 0};
     if (a.q_docs != nullptr && count > 0) qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin + step0 % per_head);
@@ -759,7 +788,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     if (count > 0) {
       head += step0 / per_head;
       n += step0 % per_head;
-      put(0, fetch(head, n));
     }
     int head1 = head, n1 = n;  // of the next
     for (int i = 0; i < count; ++i, head = head1, n = n1) {
@@ -769,8 +797,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       }
       const int q0 = n * kTile + half * 64;
       const ScoreConst sc = score_const(a, head);
-      float ahead = 0.f;
-      if (i + 1 < count) ahead = fetch(head1, n1);
       bool whole = n * kTile >= all_from;
       int qd[2];
       if (a.q_docs != nullptr) {
@@ -779,10 +805,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         if (i + 1 < count)
           qr = doc_range(a.q_ranges, int64_t(b) * qtiles + n1);
       }
-      ok = ok && wait_warp(tail->s_full, i, abort_flag, a.dev_status);
-      // everyone's statistics of this step are written, those of the step
-      // before are no longer read
-      if (!(ok = !named_bar_red_or(1, kPairThreads, !ok))) break;
+      // the step's scores, and its statistics
+      if (!(ok = wait_warp(tail->s_full, i, abort_flag, a.dev_status) &&
+                 wait_warp(tail->e_full[i % L::kESlots], i / L::kESlots, abort_flag, a.dev_status)))
+        break;
       tc_fence_after();
       float w[64], pr[64];
       tmem_ld32(s_addr, w);
@@ -812,8 +838,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&tail->p_full));
-      if (i + 1 < count) put(i + 1, ahead);
-      if (!(ok = wait_warp(tail->dp_full, i, abort_flag, a.dev_status))) continue;  // leave together, at the next barrier
+      if (!(ok = wait_warp(tail->dp_full, i, abort_flag, a.dev_status))) break;
       tc_fence_after();
       float dp[64];
       tmem_ld32(dp_addr, dp);
@@ -874,7 +899,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         for (int c = 0; c < DH; c += 32) {
           float o[32];
           sum_of(c, o);
-          if (key < a.Sk) store_row32(out + key * stride[1], c, a.D, o, by);
+          store_rows32(out, stride[1], key - lane, a.Sk, c, a.D, o, by);
         }
     } else {
       cluster_sync();  // every block is done with the tiles that the sums go over
@@ -959,6 +984,13 @@ cudaError_t start_dkv(const Params &p, int, cudaStream_t s) {
                : (bias ? f<64, false, true>(p, sms, s) : f<64, false, false>(p, sms, s)); \
   return cap ? (bias ? f<128, true, true>(p, sms, s) : f<128, true, false>(p, sms, s))  \
              : (bias ? f<128, false, true>(p, sms, s) : f<128, false, false>(p, sms, s))
+
+cudaError_t launch_attn_stats(const AttnArgs &a, cudaStream_t s) {
+  const int64_t blocks = int64_t(a.B) * ((a.Sq + kTile - 1) / kTile * (kTile / 32)) *
+                         ((a.Hq + kStatWarps - 1) / kStatWarps);
+  return launch_pdl(a.D <= 64 ? k_attn_stats<64> : k_attn_stats<128>,
+                    dim3(static_cast<unsigned>(blocks)), dim3(32 * kStatWarps), 0, s, a);
+}
 
 cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s) {
   const Params p{a, m, a.B * a.Hq * ((a.Sq + kTile - 1) / kTile), 1};

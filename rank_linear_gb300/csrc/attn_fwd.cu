@@ -174,6 +174,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (lane == 0) {
           tail->item[s] = it;
           mbar_arrive(smem_u32(&tail->item_full[s]));  // releases the item's words
+          if (it.count > 0)  // what it begins with, towards L2
+            for (int c = 0; c < DH; c += 64) {
+              tma_prefetch_4d(&p.m.q, c, it.row0, it.h, it.b);
+              tma_prefetch_4d(&p.m.q, c, it.row0 + kTile, it.h, it.b);
+              tma_prefetch_4d(&p.m.k, c, it.begin * kTile, it.h / a.group, it.b);
+              tma_prefetch_4d(&p.m.v, c, it.begin * kTile, it.h / a.group, it.b);
+            }
         }
         __syncwarp();
         if (it.count < 0) break;
@@ -437,12 +444,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         ++done;
         tc_fence_after();
       }
-      // a thread's row straight to global memory: its shared memory is already
-      // the next item's
+      // straight to global memory: Q's shared memory is already the next item's
       const float l = l2.x + l2.y;
       const float inv = l > 0.f ? 1.f / l : 0.f;
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + row * a.so[1] +
-                           h * a.so[2];
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2];
 #pragma unroll 1
       for (int c = 0; c < DH; c += 32) {
         float o[32];
@@ -454,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (!(l > 0.f))
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        if (row < a.Sq) store_row32(out, c, a.D, o, inv);
+        store_rows32(out, a.so[1], row - lane, a.Sq, c, a.D, o, inv);
       }
       tc_fence_before();  // O has been read before the next item's P is announced
       if (a.lse != nullptr && row < a.Sq)
