@@ -999,9 +999,14 @@ cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cud
 
 cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s) {
   Params p{a, m, a.B * a.Hk * ((a.Sk + kTile - 1) / kTile), 1};
-  // blocks of an item: enough for two rounds of the SMs, as far as its steps go
+  // Blocks of an item: while a cluster of twice as many fits the SMs at once,
+  // or would leave each at least 16 steps (of some 1.5 us; a block's beginning
+  // and end, and the meeting of the cluster, take some 12 us).
   const int steps = a.group * ((a.Sq + kTile - 1) / kTile);
-  while (p.cluster < 8 && p.items * p.cluster < 2 * sms && steps >= 4 * p.cluster) p.cluster *= 2;
+  while (p.cluster < 8 && steps >= 4 * p.cluster &&
+         (p.items * p.cluster * 2 <= sms ||
+          (p.items * p.cluster < sms && steps >= 32 * p.cluster)))
+    p.cluster *= 2;
   LORA_ATTN_VARIANT(start_dkv);
 }
 
