@@ -59,22 +59,20 @@ def _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix, like_q,
     return sh
 
 
-def _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix, like_q, like_k):
-    qd = kd = None
-    if documents is not None:
-        if isinstance(documents, (tuple, list)):
-            qd, kd = documents
-        else:
-            sq, sk = q.shape[1], k.shape[1]
-            if sq > sk:
-                raise ValueError("one documents tensor needs q_len <= k_len")
-            kd = documents
-            qd = documents if sq == sk else documents[:, sk - sq:]
-    key = (_layout(q), _layout(k), _layout(v), scale, causal, softcap, _layout(slopes),
-           _layout(qd), _layout(kd), _layout(prefix), tuple(like_q),
-           *map(_layout, like_q.values()), *map(_layout, like_k.values()))
-    block = _block(key, lambda: _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd,
-                                            prefix, like_q, like_k))
+def _doc_pair(documents, q, k):
+    """(queries' documents, keys')."""
+    if documents is None:
+        return None, None
+    if isinstance(documents, (tuple, list)):
+        return documents
+    sq, sk = q.shape[1], k.shape[1]
+    if sq > sk:
+        raise ValueError("one documents tensor needs q_len <= k_len")
+    return (documents if sq == sk else documents[:, sk - sq:]), documents
+
+
+def _filled(block, slopes, qd, kd, prefix):
+    """The block with this call's addresses."""
     if slopes is None and qd is None and prefix is None:
         return block
     sh = _lib.AttentionShape.from_buffer_copy(block)
@@ -82,6 +80,13 @@ def _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix, like_q, l
     if qd is not None and qd.numel() and kd.numel():  # an empty side: nothing to mask
         sh.q_docs, sh.k_docs = _ptr(qd), _ptr(kd)
     return sh
+
+
+def _workspace_bytes(sh, documents, backward):
+    if documents:  # sizes only: any address stands for them
+        sh = _lib.AttentionShape.from_buffer_copy(sh)
+        sh.q_docs = sh.k_docs = 16
+    return _lib.lib().lora_attention_workspace_bytes(ctypes.byref(sh), backward)
 
 
 def _scratch(nbytes, like, workspace):
@@ -109,17 +114,26 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
     prefix     int32 [batch]: keys before it are visible to every query
                (with causal).
     """
-    L = _lib.lib()
+    qd, kd = _doc_pair(documents, q, k)
     with _on(stream):
         if out is None:
             out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         if lse is None:
             lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], dtype=torch.float32,
                               device=q.device)
-        sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix, {"o": out}, {})
-        workspace = _scratch(L.lora_attention_workspace_bytes(ctypes.byref(sh), 0), q, workspace)
-    st = L.lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(lse),
-                              _ptr(workspace), _size(workspace), _stream_ptr(stream))
+        key = ("forward", _layout(q), _layout(k), _layout(v), _layout(out), scale, causal, softcap,
+               _layout(slopes), _layout(qd), _layout(kd), _layout(prefix))
+
+        def make():
+            sh = _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix,
+                             {"o": out}, {})
+            return sh, _workspace_bytes(sh, qd is not None, 0)
+        block, need = _block(key, make)
+        workspace = _scratch(need, q, workspace)
+    sh = _filled(block, slopes, qd, kd, prefix)
+    st = _lib.lib().lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                       _ptr(lse), _ptr(workspace), _size(workspace),
+                                       _stream_ptr(stream))
     if st:
         _lib.check(st, "lora_attention_fwd")
     return out, lse
@@ -129,20 +143,44 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
                        slopes=None, documents=None, prefix=None, dq=None, dk=None, dv=None,
                        workspace=None, stream=None):
     """(dq, dk, dv) from the gradient of attention_forward's output."""
-    L = _lib.lib()
     if lse.dtype != torch.float32 or not lse.is_contiguous() or \
             lse.shape != (q.shape[0], q.shape[2], q.shape[1]):
         raise ValueError("lse must be the forward's: float32 [batch, q_heads, q_len]")
+    qd, kd = _doc_pair(documents, q, k)
+    own = dq is None and dk is None and dv is None and workspace is None
     with _on(stream):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-        dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-        dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
-        sh = _shape(q, k, v, scale, causal, softcap, slopes, documents, prefix,
-                    {"o": out, "d_o": dout, "dq": dq}, {"dk": dk, "dv": dv})
-        workspace = _scratch(L.lora_attention_workspace_bytes(ctypes.byref(sh), 1), q, workspace)
-    st = L.lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                              _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(workspace),
-                              _size(workspace), _stream_ptr(stream))
+        if not own:
+            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
+            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
+            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+        key = ("backward", _layout(q), _layout(k), _layout(v), _layout(out), _layout(dout),
+               _layout(dq), _layout(dk), _layout(dv), scale, causal, softcap, _layout(slopes),
+               _layout(qd), _layout(kd), _layout(prefix))
+
+        def make():
+            like = lambda t: torch.empty(t.shape, dtype=t.dtype, device="meta").stride()
+            sh = _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix,
+                             {"o": out, "d_o": dout, **({} if own else {"dq": dq})},
+                             {} if own else {"dk": dk, "dv": dv})
+            if own:
+                sh.dq, sh.dk, sh.dv = like(q)[:3], like(k)[:3], like(k)[:3]
+            pad = lambda n: (n + 127) // 128 * 128  # 256 bytes
+            return (sh, _workspace_bytes(sh, qd is not None, 1), like(q), like(k),
+                    pad(q.numel()), pad(k.numel()))
+        block, need, q_like, k_like, nq, nk = _block(key, make)
+        if own:  # one buffer for the three gradients and the scratch behind them
+            buf = torch.empty(nq + 2 * nk + (need + 1) // 2, dtype=q.dtype, device=q.device)
+            dq = buf.as_strided(q.shape, q_like, 0)
+            dk = buf.as_strided(k.shape, k_like, nq)
+            dv = buf.as_strided(k.shape, k_like, nq + nk)
+            scratch, have = (buf.data_ptr() + 2 * (nq + 2 * nk) if need else None), need
+        else:
+            workspace = _scratch(need, q, workspace)
+            scratch, have = _ptr(workspace), _size(workspace)
+    sh = _filled(block, slopes, qd, kd, prefix)
+    st = _lib.lib().lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
+                                       _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                                       scratch, have, _stream_ptr(stream))
     if st:
         _lib.check(st, "lora_attention_bwd")
     return dq, dk, dv
@@ -163,9 +201,7 @@ def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, s
                softcap, _layout(slopes), _layout(out))
         sh, need = _block(key, lambda: _make_token(q, k_cache, v_cache, lengths, scale, softcap,
                                                    slopes, out))
-        if slopes is not None:
-            sh = _lib.AttentionShape.from_buffer_copy(sh)
-            sh.slopes = _ptr(slopes)
+        sh = _filled(sh, slopes, None, None, None)
         workspace = _scratch(need, q, workspace)
     st = L.lora_attention_token(ctypes.byref(sh), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                 _ptr(lengths), _ptr(out), _ptr(workspace), _size(workspace),
