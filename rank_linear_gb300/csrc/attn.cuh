@@ -264,33 +264,81 @@ __device__ __forceinline__ int last_key(const AttnArgs &a, int p, int prefix) {
 }
 
 // The score of a raw product z = q . k, in units of log 2, without the mask.
-// CAP: c = cap tanh(z scale / cap) through tanh x = 1 - 2 / (1 + e^2x); r is
-// that reciprocal, dc/dz = scale * 4 r (1 - r).  The absolute error, which is
-// what the softmax sees, stays near 2^-23 cap.
+// CAP: c = cap tanh(z scale / cap), by one of two ways for all of a warp's
+// pairs at hand:
+//  - |z| scale <= cap for all of them: x P(x^2), P the polynomial of degree 5
+//    next to tanh(x) / x on [0, 1] (a reweighted least-squares fit; the error
+//    of tanh is 2.4e-7 at the most), two pairs an instruction;
+//  - else tanh x = 1 - 2 r, r = 1 / (1 + e^2x): two more special functions a
+//    pair, of which an SM does 32 a cycle.
+// The absolute error, which is what the softmax sees, stays near 2^-22 cap.
 struct ScoreConst {
   float scale2;    // scale * log2 e
   float tanh_in;   // 2 log2 e * scale / cap
   float cap2;      // cap * log2 e
   float slope2;    // slope * log2 e
+  float most;      // cap / scale: the largest |z| for the polynomial
+  float less;      // 1 / cap2^2: dc/dz = scale (1 - c^2 less), |tanh| up to tanh 1
+  float poly[6];   // of z^2, times scale2
 };
 __device__ __forceinline__ ScoreConst score_const(const AttnArgs &a, int head) {
   ScoreConst c;
   c.scale2 = a.scale * kLog2e;
-  c.tanh_in = a.cap > 0.f ? 2.f * kLog2e * a.scale / a.cap : 0.f;
-  c.cap2 = a.cap * kLog2e;
   c.slope2 = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
+  c.tanh_in = c.cap2 = c.most = c.less = 0.f;
+  if (a.cap > 0.f) {
+    const float x = a.scale / a.cap;
+    c.tanh_in = 2.f * kLog2e * x;
+    c.cap2 = a.cap * kLog2e;
+    c.most = a.cap / a.scale;
+    c.less = 1.f / (c.cap2 * c.cap2);
+    const float p[6] = {0.99999685f, -0.33324004f, 0.13253524f, -0.050972835f, 0.016114152f,
+                        -0.0028394550f};
+    float by = c.scale2;
+#pragma unroll
+    for (int i = 0; i < 6; ++i) {
+      c.poly[i] = p[i] * by;
+      by *= x * x;  // may underflow to 0 where z^2 is far below what counts
+    }
+  }
   return c;
 }
+// May the polynomial be used for the N products of every lane?
+template <int N>
+__device__ __forceinline__ bool all_small(const ScoreConst &c, const float *z) {
+  float m[2] = {fabsf(z[0]), fabsf(z[1])};
+#pragma unroll
+  for (int j = 2; j + 2 < N; j += 4)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) m[i] = max3(m[i], fabsf(z[j + 2 * i]), fabsf(z[j + 2 * i + 1]));
+  m[0] = max3(m[0], fabsf(z[N - 2]), fabsf(z[N - 1]));
+  return __all_sync(~0u, fmaxf(m[0], m[1]) <= c.most);
+}
+__device__ __forceinline__ float2 cap_small(const ScoreConst &c, float2 z) {
+  const float2 u = mul2(z, z);
+  float2 p = make_float2(c.poly[5], c.poly[5]);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) p = fma2(p, u, make_float2(c.poly[i], c.poly[i]));
+  return mul2(z, p);
+}
+// r as above: dc/dz = scale * 4 r (1 - r), good where tanh is next to 1 too.
+__device__ __forceinline__ float cap_any(const ScoreConst &c, float z, float &r) {
+  r = rcp(1.f + ex2(z * c.tanh_in));
+  return fmaf(-2.f * c.cap2, r, c.cap2);
+}
+// Two scores; small: what all_small said of them.
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ float score2(const ScoreConst &c, float z, float distance, float &r) {
-  float s;
-  if constexpr (CAP) {
-    r = rcp(1.f + ex2(z * c.tanh_in));
-    s = fmaf(-2.f * c.cap2, r, c.cap2);
-  } else {
-    s = z * c.scale2;
+__device__ __forceinline__ float2 scores2(const ScoreConst &c, float2 z, float distance, float step,
+                                          bool small) {
+  float2 s, r;
+  if constexpr (CAP)
+    s = small ? cap_small(c, z) : make_float2(cap_any(c, z.x, r.x), cap_any(c, z.y, r.y));
+  else
+    s = mul2(z, make_float2(c.scale2, c.scale2));
+  if constexpr (BIAS) {
+    s.x = fmaf(-c.slope2, fabsf(distance), s.x);
+    s.y = fmaf(-c.slope2, fabsf(distance + step), s.y);
   }
-  if constexpr (BIAS) s = fmaf(-c.slope2, fabsf(distance), s);
   return s;
 }
 

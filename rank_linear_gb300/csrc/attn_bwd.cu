@@ -40,45 +40,64 @@ struct Params {
 // over scores that it alone reads.
 __device__ __forceinline__ constexpr uint32_t operand_cols(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
 
-// P (to p) and P dc/dz (in s) of 64 raw products of one thread; distances
-// d0 + step * j; sub = -lse in log2 units (or one per column in sub_col).
+// P (to p) and P dc/dz / scale (in s) of 64 raw products of one thread;
+// distances d0 + step * j; sub = -lse in log2 units (or one per column in
+// sub_col).
 template <bool CAP, bool BIAS, bool PER_COLUMN>
 __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], float *p, float sub,
                                         const float *sub_col, float d0, float step) {
+  auto all = [&](bool small) {
 #pragma unroll
-  for (int j = 0; j < 64; j += 4) {
-    float4 sc;
-    if constexpr (PER_COLUMN)
-      sc = *reinterpret_cast<const float4 *>(sub_col + j);
-    else
-      sc = make_float4(sub, sub, sub, sub);
-    const float add[4] = {sc.x, sc.y, sc.z, sc.w};
+    for (int j = 0; j < 64; j += 4) {
+      float4 sc;
+      if constexpr (PER_COLUMN)
+        sc = *reinterpret_cast<const float4 *>(sub_col + j);
+      else
+        sc = make_float4(sub, sub, sub, sub);
+      const float add[4] = {sc.x, sc.y, sc.z, sc.w};
 #pragma unroll
-    for (int i = 0; i < 4; i += 2) {
-      float2 x = make_float2(s[j + i], s[j + i + 1]);
-      const float2 y = make_float2(add[i], add[i + 1]);
-      float r0 = 0.f, r1 = 0.f;
-      if constexpr (CAP || BIAS) {
-        x.x = score2<CAP, BIAS>(c, x.x, d0 + step * (j + i), r0);
-        x.y = score2<CAP, BIAS>(c, x.y, d0 + step * (j + i + 1), r1);
-        x = add2(x, y);
-      } else {
-        x = fma2(x, make_float2(c.scale2, c.scale2), y);
+      for (int i = 0; i < 4; i += 2) {
+        float2 x = make_float2(s[j + i], s[j + i + 1]);
+        const float2 y = make_float2(add[i], add[i + 1]);
+        float2 f = make_float2(1.f, 1.f);
+        if constexpr (CAP || BIAS) {
+          if constexpr (CAP) {
+            if (small) {
+              x = cap_small(c, x);
+              f = fma2(mul2(x, x), make_float2(-c.less, -c.less), f);
+            } else {
+              float2 r;
+              x = make_float2(cap_any(c, x.x, r.x), cap_any(c, x.y, r.y));
+              f = make_float2(4.f * r.x * (1.f - r.x), 4.f * r.y * (1.f - r.y));
+            }
+          } else {
+            x = mul2(x, make_float2(c.scale2, c.scale2));
+          }
+          if constexpr (BIAS) {
+            const float d = d0 + step * (j + i);
+            x.x = fmaf(-c.slope2, fabsf(d), x.x);
+            x.y = fmaf(-c.slope2, fabsf(d + step), x.y);
+          }
+          x = add2(x, y);
+        } else {
+          x = fma2(x, make_float2(c.scale2, c.scale2), y);
+        }
+        x.x = ex2(x.x);
+        x.y = ex2(x.y);
+        if (p != nullptr) {
+          p[j + i] = x.x;
+          p[j + i + 1] = x.y;
+        }
+        if constexpr (CAP) x = mul2(x, f);
+        s[j + i] = x.x;
+        s[j + i + 1] = x.y;
       }
-      x.x = ex2(x.x);
-      x.y = ex2(x.y);
-      if (p != nullptr) {
-        p[j + i] = x.x;
-        p[j + i + 1] = x.y;
-      }
-      if constexpr (CAP) {  // dc/dz = 1 - tanh^2 = 4 r (1 - r)
-        x.x *= 4.f * r0 * (1.f - r0);
-        x.y *= 4.f * r1 * (1.f - r1);
-      }
-      s[j + i] = x.x;
-      s[j + i + 1] = x.y;
     }
-  }
+  };
+  if (!CAP || all_small<64>(c, s))
+    all(true);
+  else
+    all(false);
 }
 
 // ---------------------------------------------------------------- statistics

@@ -365,9 +365,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         pin<kTile>(s);
         if constexpr (CAP || BIAS) {
           const float d0 = static_cast<float>(pos - n * kTile);
-          float r;
+          auto transform = [&](bool small) {
 #pragma unroll
-          for (int j = 0; j < kTile; ++j) s[j] = score2<CAP, BIAS>(sc, s[j], d0 - j, r);
+            for (int j = 0; j < kTile; j += 2) {
+              const float2 x =
+                  scores2<CAP, BIAS>(sc, make_float2(s[j], s[j + 1]), d0 - j, -1.f, small);
+              s[j] = x.x;
+              s[j + 1] = x.y;
+            }
+          };
+          if (!CAP || all_small<kTile>(sc, s))
+            transform(true);
+          else
+            transform(false);
         }
         if (!whole) {
           uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};

@@ -144,9 +144,11 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + quad + 8 * (i >> 1);
+      const ScoreConst &c = sc[i & 1];
       float r;
-      s[i] = key < to ? score2<CAP, BIAS>(sc[i & 1], s[i], static_cast<float>(len - 1 - key), r)
-                      : -INFINITY;
+      s[i] = CAP ? cap_any(c, s[i], r) : s[i] * c.scale2;
+      if constexpr (BIAS) s[i] = fmaf(-c.slope2, static_cast<float>(len - 1 - key), s[i]);
+      if (key >= to) s[i] = -INFINITY;
     }
     float top[2] = {fmaxf(s[0], s[2]), fmaxf(s[1], s[3])};
     if (__any_sync(~0u, top[0] > m[0] + kRescaleAt || top[1] > m[1] + kRescaleAt)) {

@@ -89,6 +89,16 @@ def test_head_sizes(d, cap):
     check(*draw(2, 200, 200, 2, 1, d, d, gain=3.0 if cap else 1.0), causal=True, cap=cap)
 
 
+@pytest.mark.parametrize("cap", [1.5, 4.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_beyond_the_cap(d, cap):
+    """Most tiles have a score above the cap, some (quiet keys) have none."""
+    q, k, v, do = draw(2, 390, 390, 4, 2, d, 40, gain=2.0)
+    k[:, 128:256] *= 0.1
+    check(q, k, v, do, causal=True, cap=cap)
+    check(q, k, v, do, cap=cap, slopes=slopes_of(4))
+
+
 @pytest.mark.parametrize("hq,hk", [(1, 1), (3, 1), (8, 8), (8, 1), (10, 2), (40, 8)])
 def test_head_groups(hq, hk):
     check(*draw(2, 150, 150, hq, hk, 128 if hq < 10 else 64, hq), causal=True)
