@@ -73,7 +73,8 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
                                  const void *v, void *o, float *lse, void *workspace,
                                  size_t workspace_bytes, void *stream);
 
-/* dq, dk and dv from do and the forward's tensors.  Outputs are overwritten. */
+/* dq, dk and dv from do and the forward's tensors.  Outputs are overwritten;
+ * they must not overlap an input. */
 lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o, const void *q,
                                  const void *k, const void *v, const void *o, const float *lse,
                                  void *dq, void *dk, void *dv, void *workspace,

@@ -599,7 +599,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   const int qtiles = (a.Sq + kTile - 1) / kTile, ktiles = (a.Sk + kTile - 1) / kTile;
   const int ranks = p.cluster, rank = static_cast<int>(blockIdx.x) % ranks;
   const int item = static_cast<int>(blockIdx.x) / ranks, g = item % a.Hk;
-  griddep_wait();
+  // The dq kernel before this one writes nothing that is read here, and lets
+  // it start only when what came before dq has finished: no wait, so that
+  // blocks begin on the SMs that dq leaves first.  They wait before they
+  // leave instead: this kernel ends after dq.  (Without queries there is no dq.)
+  if (a.Sq == 0) griddep_wait();
   griddep_launch_dependents();
   const int entry = a.order != nullptr ? __ldcg(a.order + item / a.Hk) : item / a.Hk;
   const int b = a.order != nullptr ? entry / ktiles : entry % a.B;
@@ -961,6 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  griddep_wait();
 }
 
 template <int DH, bool CAP, bool BIAS>
