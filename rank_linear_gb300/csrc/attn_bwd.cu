@@ -12,7 +12,12 @@
 // A small pass before them leaves two numbers of each query row, -lse in log2
 // units and -delta = -do . o, in rows of whole tiles: read once for both
 // kernels.  (Formed in the dq kernel they cost an item 3600 to 10000 cycles,
-// or 22000 of the first one in warps of their own.)
+// or 22000 of the first one in warps of their own.)  o there has been rounded
+// to bf16, which is most of the error of a gradient that nearly cancels: with
+// few keys, a query that looks almost wholly at one of them.  Where all keys
+// lie in one tile, the dq kernel therefore forms delta = sum_j P dP itself and
+// leaves it for dk and dv (of two tokens dq was off by up to 0.2 of its norm).
+// That is not done for more keys: it would take the scores twice.
 //
 // The dq blocks stay and take item after item, as the forward's do.  A dk/dv
 // item has a group's heads times as much work; where there are too few for the
@@ -186,6 +191,8 @@ struct DqTail {
   uint64_t s_full[2], dp_full[2], dp_free, done, drain;
   uint64_t dz_full[2];  // by tile modulo 2: tile x + 1's may come before x's is waited for
   uint64_t item_full[kItemSlots], item_free[kItemSlots];
+  uint64_t part_full;
+  float part[2][2][kTile];  // sums of P dP, of item modulo 2 and half: ONE_TILE
   DqItem item[kItemSlots];
   uint32_t tmem;
   int abort_flag;
@@ -201,7 +208,7 @@ __device__ __forceinline__ bool next_item(DqTail *tail, int n, DqItem &item,
   return item.count >= 0;
 }
 
-template <int DH, bool CAP, bool BIAS>
+template <int DH, bool CAP, bool BIAS, bool ONE_TILE>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ Params p) {
   using L = DqLayout<DH>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -233,6 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       mbar_init(smem_u32(&tail->dz_full[s]), kPairThreads);
     }
     mbar_init(smem_u32(&tail->dp_free), kPairThreads);
+    mbar_init(smem_u32(&tail->part_full), kPairThreads);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(smem_u32(&tail->item_full[s]), 1);
       mbar_init(smem_u32(&tail->item_free[s]), kItemReaders);
@@ -449,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     for (int item = 0; ok && next_item(tail, item, it, abort_flag, a.dev_status); ++item) {
       const int b = it.b, h = it.h, row = it.row0 + r, count = it.count;
       const int64_t stat = (static_cast<int64_t>(b) * a.Hq + h) * (qtiles * kTile) + row;
-      const float sub = __ldcg(a.sub + stat), neg_delta = __ldcg(a.neg_delta + stat);
+      const float sub = __ldcg(a.sub + stat);
+      float neg_delta = ONE_TILE ? 0.f : __ldcg(a.neg_delta + stat);
       const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
       const ScoreConst sc = score_const(a, h);
       const int pos = row + off;
@@ -474,12 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         const uint32_t s_addr = tmem + lanes + (x & 1) * kTile + half * 64;
         if (!(ok = wait_warp(tail->s_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
         tc_fence_after();
-        float w[64];
+        constexpr bool kKeepP = ONE_TILE && CAP;  // without a cap w is P
+        float w[64], pr[kKeepP ? 64 : 1];
         tmem_ld32(s_addr, w);
         tmem_ld32(s_addr + 32, w + 32);
         tmem_wait_ld();
         pin<64>(w);
-        weights<CAP, BIAS, false>(sc, w, nullptr, sub, nullptr, static_cast<float>(pos - key0), -1.f);
+        weights<CAP, BIAS, false>(sc, w, kKeepP ? pr : nullptr, sub, nullptr,
+                                  static_cast<float>(pos - key0), -1.f);
         if (!whole) {
           uint32_t keep[2] = {~0u, ~0u};
           if (a.q_docs != nullptr) same_doc(qd, kd, keep);
@@ -488,7 +499,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
             keep[c] &= bits_to(last - key0 - 32 * c);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(keep[c] >> j & 1u)) w[c * 32 + j] = 0.f;
+              if (!(keep[c] >> j & 1u)) {
+                w[c * 32 + j] = 0.f;
+                if constexpr (kKeepP) pr[c * 32 + j] = 0.f;
+              }
           }
         }
         if (!(ok = wait_warp(tail->dp_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
@@ -500,6 +514,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         pin<64>(dp);
         tc_fence_before();
         mbar_arrive(smem_u32(&tail->dp_free));
+        if constexpr (ONE_TILE) {  // count is 1: an item, a tile
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            const float y = kKeepP ? pr[kKeepP ? j : 0] : w[j];
+            sum[j & 3] = y == 0.f ? sum[j & 3] : fmaf(y, dp[j], sum[j & 3]);
+          }
+          float *part = tail->part[used & 1][0];
+          part[half * kTile + r] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          mbar_arrive(smem_u32(&tail->part_full));
+          if (!(ok = wait_warp(tail->part_full, used, abort_flag, a.dev_status))) break;
+          neg_delta = -(part[r] + part[kTile + r]);
+          if (half == 0) a.neg_delta[stat] = neg_delta;
+        }
         const float2 nd = make_float2(neg_delta, neg_delta);
 #pragma unroll
         for (int j = 0; j < 64; j += 2) {
@@ -602,7 +630,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   // The dq kernel before this one writes nothing that is read here, and lets
   // it start only when what came before dq has finished: no wait, so that
   // blocks begin on the SMs that dq leaves first.  They wait before they
-  // leave instead: this kernel ends after dq.  (Without queries there is no dq.)
+  // leave instead: this kernel ends after dq.  (Without queries there is no dq;
+  // where dq forms delta, the copying thread waits before it reads that.)
   if (a.Sq == 0) griddep_wait();
   griddep_launch_dependents();
   const int entry = a.order != nullptr ? __ldcg(a.order + item / a.Hk) : item / a.Hk;
@@ -685,6 +714,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
           ++nq;
         };
         load_q(0);
+        if (a.Sk <= kTile) griddep_wait();
         for (int i = 0; i < count; ++i) {
           // dP of step i - 1 is done, hence everything of step i - 2: the slots
           // of Q's tile i - 2 and dO's
@@ -968,14 +998,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   griddep_wait();
 }
 
-template <int DH, bool CAP, bool BIAS>
-cudaError_t start_dq(const Params &p, int sms, cudaStream_t s) {
+template <int DH, bool CAP, bool BIAS, bool ONE_TILE>
+cudaError_t start_dq_of(const Params &p, int sms, cudaStream_t s) {
   constexpr size_t smem = DqLayout<DH>::kAsked;
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(k_attn_dq<DH, CAP, BIAS>, smem, done);
+  const cudaError_t e = allow_smem(k_attn_dq<DH, CAP, BIAS, ONE_TILE>, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_attn_dq<DH, CAP, BIAS>, dim3(p.items < sms ? p.items : sms), dim3(kThreads),
-                    smem, s, p);
+  return launch_pdl(k_attn_dq<DH, CAP, BIAS, ONE_TILE>, dim3(p.items < sms ? p.items : sms),
+                    dim3(kThreads), smem, s, p);
+}
+template <int DH, bool CAP, bool BIAS>
+cudaError_t start_dq(const Params &p, int sms, cudaStream_t s) {
+  return p.a.Sk <= kTile ? start_dq_of<DH, CAP, BIAS, true>(p, sms, s)
+                         : start_dq_of<DH, CAP, BIAS, false>(p, sms, s);
 }
 template <int DH, bool CAP, bool BIAS>
 cudaError_t start_dkv(const Params &p, int, cudaStream_t s) {

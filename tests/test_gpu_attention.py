@@ -125,6 +125,58 @@ def packed(lengths, pad, B=1):
     return torch.tensor([row] * B, dtype=torch.int32)
 
 
+def few_keys(gpu, q, k, v, do, cap=0.0, causal=True, docs=None):
+    """dq and dk where delta is not taken from the rounded o.  Sums over at most
+    128 products in fp32 are off by 2^-16 of their terms' magnitude (128
+    roundings of 2^-24, twice that where the tensor cores truncate), scores of
+    sum |q k| scale <= 24 by 24 * 2^-17, hence P by less than 2^-12 of itself
+    (the exponential and the cap add 2^-20).  dz = P (dP - delta), delta the
+    sum of the same P dP, is then off by 2^-12 P (|dP| + sum P |dP|) and the
+    error of dP, and is rounded to bf16 once, as its sums are."""
+    G, M = 2.0 ** -12, 2.0 ** -16
+    scale = q.shape[-1] ** -0.5
+    for b in range(q.shape[0]):
+        see = oa.visible(q.shape[1], k.shape[1], causal, 0, *((None, None) if docs is None else (docs[b],) * 2))
+        for g in range(k.shape[2]):
+            dk, dkb = 0.0, TINY
+            for h in range(g * (q.shape[2] // k.shape[2]), (g + 1) * (q.shape[2] // k.shape[2])):
+                p, sl, o, _, qkv = oa.head(q[b, :, h], k[b, :, g], v[b, :, g], scale=scale, see=see, cap=cap)
+                grad = oa.head_backward(do[b, :, h], p, sl, o, qkv, scale=scale, see=see)
+                dp = np.abs(grad[4] @ qkv[2].T)
+                size = np.abs(grad[4]) @ np.abs(qkv[2]).T
+                off = p * sl * (G * (dp + (p * dp).sum(1, keepdims=True)) + M * (size + (p * size).sum(1, keepdims=True)))
+                dz = 2 * oa.U * np.abs(grad[3]) + off
+                err = np.abs(gpu["dq"][b, :, h].double().cpu().numpy() - grad[0])
+                assert np.all(err <= scale * dz @ np.abs(qkv[1]) + TINY), ("dq", b, h, err.max())
+                dk, dkb = dk + grad[1], dkb + scale * dz.T @ np.abs(qkv[0])
+            err = np.abs(gpu["dk"][b, :, g].double().cpu().numpy() - dk)
+            assert np.all(err <= dkb), ("dk", b, g, err.max())
+
+
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("sq,sk,d,causal", [(2, 2, 128, True), (2, 2, 80, False), (3, 3, 96, True), (8, 8, 64, True),
+                                            (100, 100, 128, True), (128, 128, 64, True), (300, 128, 128, False),
+                                            (37, 125, 64, True)])
+def test_gradients_that_nearly_cancel(sq, sk, d, causal, cap):
+    """Few keys, a query that looks almost wholly at one of them."""
+    q, k, v, do = draw(2, sq, sk, 8, 2, d, sq + sk + d)
+    k[:, 0] *= 3  # the first key draws most of its queries' weight, or none
+    got = check(q, k, v, do, causal=causal, cap=cap)
+    few_keys(got, host(q), host(k), host(v), host(do), cap, causal)
+
+
+def test_few_keys_and_padding():
+    q, k, v, do = draw(1, 90, 90, 4, 2, 64, 9)
+    docs = torch.tensor([[0] * 40 + [1] * 1 + [2] * 2 + [3] * 30 + [-1] * 17], dtype=torch.int32)
+    for t in (q, k, v, do):
+        t[:, -17:] = float("nan")
+    got = check(q, k, v, do, causal=True, docs=docs)
+    zero = [t.nan_to_num(0.0) for t in (q, k, v, do)]
+    few_keys(got, *map(host, zero), docs=host(docs))
+    for n in ("dq", "dk", "dv"):
+        assert not got[n][:, -17:].any(), n
+
+
 @pytest.mark.parametrize("causal", [False, True])
 @pytest.mark.parametrize("lengths,pad", [([300], 0), ([128, 128, 256], 0), ([1, 127, 130, 42], 0),
                                          ([5] * 60, 0), ([100, 200], 84), ([1], 399), ([], 300)])
