@@ -82,10 +82,13 @@ def _filled(block, slopes, qd, kd, prefix):
     return sh
 
 
-def _workspace_bytes(sh, documents, backward):
-    if documents:  # sizes only: any address stands for them
+def _workspace_bytes(sh, documents, prefix, backward):
+    if documents or prefix:  # given or not: any address stands for them
         sh = _lib.AttentionShape.from_buffer_copy(sh)
-        sh.q_docs = sh.k_docs = 16
+        if documents:
+            sh.q_docs = sh.k_docs = 16
+        if prefix:
+            sh.prefix = 16
     return _lib.lib().lora_attention_workspace_bytes(ctypes.byref(sh), backward)
 
 
@@ -127,7 +130,7 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
         def make():
             sh = _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix,
                              {"o": out}, {})
-            return sh, _workspace_bytes(sh, qd is not None, 0)
+            return sh, _workspace_bytes(sh, qd is not None, prefix is not None, 0)
         block, need = _block(key, make)
         workspace = _scratch(need, q, workspace)
     sh = _filled(block, slopes, qd, kd, prefix)
@@ -165,7 +168,7 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
             if own:
                 sh.dq, sh.dk, sh.dv = like(q)[:3], like(k)[:3], like(k)[:3]
             pad = lambda n: (n + 127) // 128 * 128  # 256 bytes
-            return (sh, _workspace_bytes(sh, qd is not None, 1), like(q), like(k),
+            return (sh, _workspace_bytes(sh, qd is not None, prefix is not None, 1), like(q), like(k),
                     pad(q.numel()), pad(k.numel()))
         block, need, q_like, k_like, nq, nk = _block(key, make)
         if own:  # one buffer for the three gradients and the scratch behind them

@@ -44,10 +44,30 @@ struct AttnBwdMaps {
   CUtensorMap q, k, v, d_o;
 };
 
+// Forward: how the items (kQueries queries of a head) are shared out.  The first
+// `rounds` rounds of whole items, one to a block, are handed out to and fro;
+// what is left of the items, fewer than there are blocks, is cut along the
+// keys: `tail` items in equal shares for `workers` blocks, each share part of
+// one item or of two.  An item has up to `segments` parts, joined by a second
+// launch.  tail = 0: nothing is cut (rounds is not used).
+struct AttnFwdPlan {
+  int rounds = 0, tail = 0, workers = 0, segments = 0;
+};
+constexpr int kAttnQueries = 256;
+// The parts' maxima and sums (float2 [tail][segments][kAttnQueries]), and their
+// outputs ([tail][segments][dim rounded up to 64 / 4][kAttnQueries] float4).
+size_t attn_fwd_stat_bytes(const AttnFwdPlan &t);
+size_t attn_fwd_part_bytes(const AttnFwdPlan &t, int D);
+AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, bool causal,
+                          bool prefix, bool docs);
+
 // Ranges of the documents (and counters zeroed); then the order, if asked for.
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s);
-cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s);
+cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, const AttnFwdPlan &t, void *stat,
+                            void *part, int sms, cudaStream_t s);
+cudaError_t launch_attn_fwd_join(const AttnArgs &a, const AttnFwdPlan &t, const void *stat,
+                                 const void *part, cudaStream_t s);
 cudaError_t launch_attn_stats(const AttnArgs &a, cudaStream_t s);
 cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s);
 cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s);

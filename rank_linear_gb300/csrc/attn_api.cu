@@ -115,9 +115,12 @@ lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], 
 }
 
 // Workspace: [document ranges of the query tiles, of the key tiles][item
-// counters][order of the key tiles][statistics of the query rows, two].
+// counters][order of the key tiles][statistics of the query rows, two]; the
+// forward's [maxima and sums][outputs] of the parts of items it cuts.
 struct Plan {
   size_t q_ranges = 0, k_ranges = 0, counter = 0, order = 0, sub = 0, neg_delta = 0, bytes = 0;
+  AttnFwdPlan fwd;
+  size_t stat = 0, part = 0;
 };
 Plan make_plan(const lora_attention_t *p, bool backward) {
   Plan w;
@@ -138,6 +141,13 @@ Plan make_plan(const lora_attention_t *p, bool backward) {
     off += rup(rows * 4, 256);
     w.neg_delta = off;
     off += rup(rows * 4, 256);
+  } else {
+    w.fwd = attn_fwd_plan(p->batch, p->q_heads, p->q_len, p->k_len, p->dim, p->causal != 0,
+                          p->prefix != nullptr, p->q_docs != nullptr);
+    w.stat = off;
+    off += rup(attn_fwd_stat_bytes(w.fwd), 256);
+    w.part = off;
+    off += rup(attn_fwd_part_bytes(w.fwd, p->dim), 256);
   }
   w.bytes = off;
   return w;
@@ -213,7 +223,13 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
   LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
   LORA_TRY(make_ranges(a, w, workspace, false, st));
-  return run(LORA_K_ATTN_FWD, st, "attention forward", [&] { return launch_attn_fwd(a, m, di.sms, st); });
+  const bool cut = w.fwd.tail > 0;
+  void *stat = cut ? at(workspace, w.stat) : nullptr, *part = cut ? at(workspace, w.part) : nullptr;
+  LORA_TRY(run(LORA_K_ATTN_FWD, st, "attention forward",
+               [&] { return launch_attn_fwd(a, m, w.fwd, stat, part, di.sms, st); }));
+  if (!cut) return LORA_OK;
+  return run(LORA_K_ATTN_FWD, st, "join of the attention forward",
+             [&] { return launch_attn_fwd_join(a, w.fwd, stat, part, st); });
 }
 
 lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o, const void *q,

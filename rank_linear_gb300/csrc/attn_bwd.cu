@@ -23,6 +23,14 @@
 // item has a group's heads times as much work; where there are too few for the
 // SMs, the blocks of a cluster share one, each with its part of the steps, and
 // add their sums through distributed shared memory in the order of their ranks.
+//
+// Measured (32 heads of 128, 8 key heads), all three: 8192 x 8192 without a
+// mask 2465 us (1115 TFLOP/s of the formula's five products, 1560 of the seven
+// done), causal 1194 us (1150), 4096 causal 342 us (1005), five documents in
+// 8192 486 us (statistics 28, dq 198, dk/dv 263 when timed one by one), heads
+// of 64 causal 926 us (740).  Bound by shared memory: a dk/dv step's products
+// read 256 KB of operands, 2000 cycles at 128 B a cycle, as long as the
+// products themselves take.
 #include "attn.cuh"
 #include "host.h"
 

@@ -15,6 +15,15 @@
 // counter with them (their work varies).
 //
 // TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
+//
+// Measured (32 heads of 128, 8 key heads): 8192 x 8192 without a mask 630 us
+// (1750 TFLOP/s, 0.89 of what a large bf16 product reaches), causal 338 us
+// (1625), heads of 64 causal 286 us (960: the exponentials take as long as the
+// products), 4096 causal 101 us (1360); with capped scores 162 us, with a
+// distance bias 143 us (one or two more operations a pair).  Bound by the
+// tensor cores where a block has many steps; an item begins and ends in some
+// 4 us that overlap its neighbours' steps only in part, and 256-row items
+// leave work unused along the diagonal and at documents' edges.
 #include "attn.cuh"
 #include "host.h"
 
@@ -57,7 +66,27 @@ struct Params {
   AttnArgs a;
   AttnMaps m;
   int items;
+  AttnFwdPlan t;
+  float2 *stat;
+  float4 *part;
 };
+
+// The first worker that has part of item i, and the last (see AttnFwdPlan:
+// worker j's share is [j tail / workers, (j + 1) tail / workers) of the items).
+__device__ __forceinline__ int first_worker(const AttnFwdPlan &t, int i) {
+  return i * t.workers / t.tail;
+}
+__device__ __forceinline__ int last_worker(const AttnFwdPlan &t, int i) {
+  return ((i + 1) * t.workers - 1) / t.tail;
+}
+
+// The result of the block's item n has this place among the parts of cut
+// items; -1: it is a whole item's.
+__device__ __forceinline__ int part_of(const AttnFwdPlan &t, int n) {
+  if (n < t.rounds) return -1;
+  const int place = blockIdx.x, i = place * t.tail / t.workers + n - t.rounds;
+  return i * t.segments + place - first_worker(t, i);
+}
 
 // Reads item n of the block: false where there is none (or on an abort).
 __device__ __forceinline__ bool next_item(Tail *tail, int n, Item &item, volatile int *abort_flag,
@@ -70,7 +99,9 @@ __device__ __forceinline__ bool next_item(Tail *tail, int n, Item &item, volatil
   return item.count >= 0;
 }
 
-template <int DH, bool CAP, bool BIAS>
+// CUT: items of the last round are cut along the keys (a variant: in the same
+// kernel it costs the softmax registers, and packed documents 4 %).
+template <int DH, bool CAP, bool BIAS, bool CUT>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ Params p) {
   using L = Layout<DH>;
   extern __shared__ uint8_t raw[];
@@ -138,6 +169,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           if (lane == 0) id = blocks + static_cast<int>(atomicAdd(a.counter, 1u));
           id = __shfl_sync(~0u, id, 0);
         }
+        int from_part = 0, to_part = 1, parts = 0;
+        if (CUT && n >= p.t.rounds) {  // this block's share of the items that are cut
+          const int i = place * p.t.tail / p.t.workers + n - p.t.rounds;
+          parts = p.t.workers;
+          from_part = max(place * p.t.tail - i * parts, 0);
+          to_part = min((place + 1) * p.t.tail - i * parts, parts);
+          id = place < parts && from_part < to_part ? p.t.rounds * blocks + i : p.items;
+        }
         Item it = {};
         it.count = -1;
         if (id < p.items) {
@@ -145,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           const int qb = blocks_q - 1 - id / heads, bh = id % heads;
           it.b = bh / a.Hq;
           it.h = bh % a.Hq;
-          it.row0 = qb * 2 * kTile;
+          it.row0 = qb * kAttnQueries;
           const int prefix = a.prefix != nullptr ? a.prefix[it.b] : 0;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
@@ -170,6 +209,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           const bool none0 = it.hi[0] == it.lo[0], none1 = it.hi[1] == it.lo[1];
           it.begin = none0 ? it.lo[1] : none1 ? it.lo[0] : min(it.lo[0], it.lo[1]);
           it.count = (none0 ? it.hi[1] : none1 ? it.hi[0] : max(it.hi[0], it.hi[1])) - it.begin;
+          if (CUT && parts > 0) {
+            const int lo = it.begin + it.count * from_part / parts;
+            const int hi = it.begin + it.count * to_part / parts;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              it.lo[t] = max(it.lo[t], lo);
+              it.hi[t] = max(min(it.hi[t], hi), it.lo[t]);
+            }
+            // (a tile of the range that neither sees, between the two, is passed over)
+            it.begin = lo;
+            it.count = hi - lo;
+          }
         }
         if (lane == 0) {
           tail->item[s] = it;
@@ -454,8 +505,28 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         ++done;
         tc_fence_after();
       }
-      // straight to global memory: Q's shared memory is already the next item's
       const float l = l2.x + l2.y;
+      const int part = CUT ? part_of(p.t, item) : -1;
+      if (part >= 0) {  // part of an item: joined with the others later
+        const int r = threadIdx.x & 127;
+        p.stat[static_cast<int64_t>(part) * kAttnQueries + t * kTile + r] = make_float2(m, l);
+        float4 *to =
+            p.part + static_cast<int64_t>(part) * (DH / 4) * kAttnQueries + t * kTile + r;
+        if (lo < hi)
+#pragma unroll 1
+          for (int c = 0; c < DH; c += 32) {
+            float o[32];
+            tmem_ld32(o_addr + c, o);
+            tmem_wait_ld();
+            pin<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              to[(c + e) / 4 * kAttnQueries] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        tc_fence_before();
+        continue;
+      }
+      // straight to global memory: Q's shared memory is already the next item's
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2];
 #pragma unroll 1
@@ -482,6 +553,66 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
   if (warp == 9) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
+  }
+}
+
+// Joins the parts of the items that were cut, in the order of the keys: 32
+// queries x 32 elements of the head a block, a thread four elements of a query.
+constexpr int kJoinWarps = 8;
+template <int DH>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_attn_fwd_join(const __grid_constant__ Params p) {
+  __shared__ float tile[32][33];
+  const AttnArgs &a = p.a;
+  const int lane = threadIdx.x % 32, warp = threadIdx.x / 32;
+  constexpr int kRows = kAttnQueries / 32, kCols = DH / 32;
+  const int i = blockIdx.x / (kRows * kCols), col = blockIdx.x / kRows % kCols * 32;
+  const int r = blockIdx.x % kRows * 32 + lane;
+  const int heads = a.B * a.Hq, blocks_q = p.items / heads, id = p.items - p.t.tail + i;
+  const int row0 = (blocks_q - 1 - id / heads) * kAttnQueries, bh = id % heads;
+  const int parts = last_worker(p.t, i) - first_worker(p.t, i) + 1;
+  griddep_wait();
+  griddep_launch_dependents();
+  if (row0 + r - lane >= a.Sq) return;
+  const float2 *stat = p.stat + static_cast<int64_t>(i) * p.t.segments * kAttnQueries + r;
+  const float4 *from = p.part +
+                       (static_cast<int64_t>(i) * p.t.segments * (DH / 4) + col / 4 + warp) *
+                           kAttnQueries + r;
+  float m = -INFINITY;
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float2 x = __ldcg(stat + s * kAttnQueries);
+    if (x.y > 0.f) m = fmaxf(m, x.x);
+  }
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < parts; ++s) {
+    const float2 x = __ldcg(stat + s * kAttnQueries);
+    if (x.y > 0.f) {  // else nothing was seen, and there may be no output
+      const float by = ex2(x.x - m);
+      const float4 v = __ldcg(from + static_cast<int64_t>(s) * (DH / 4) * kAttnQueries);
+      l = fmaf(by, x.y, l);
+      o.x = fmaf(by, v.x, o.x);
+      o.y = fmaf(by, v.y, o.y);
+      o.z = fmaf(by, v.z, o.z);
+      o.w = fmaf(by, v.w, o.w);
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : 0.f;
+  tile[lane][warp * 4] = o.x * inv;
+  tile[lane][warp * 4 + 1] = o.y * inv;
+  tile[lane][warp * 4 + 2] = o.z * inv;
+  tile[lane][warp * 4 + 3] = o.w * inv;
+  if (a.lse != nullptr && col == 0 && warp == 0 && row0 + r < a.Sq)
+    a.lse[static_cast<int64_t>(bh) * a.Sq + row0 + r] =
+        l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  __syncthreads();
+  // eight lanes to a row of 32 elements
+  const int y = threadIdx.x / 8, c = threadIdx.x % 8 * 4, row = row0 + r - lane + y;
+  if (row < a.Sq && col + c < a.D) {
+    const int64_t at = bh / a.Hq * a.so[0] + static_cast<int64_t>(row) * a.so[1] + bh % a.Hq * a.so[2];
+    *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at + col + c) =
+        make_uint2(pack_bf16(tile[y][c], tile[y][c + 1]), pack_bf16(tile[y][c + 2], tile[y][c + 3]));
   }
 }
 
@@ -571,14 +702,22 @@ __global__ void __launch_bounds__(kOrderThreads) k_attn_order(const AttnArgs a) 
     order[atomicAdd(&count[bucket(i)], 1)] = i;
 }
 
-template <int DH, bool CAP, bool BIAS>
-cudaError_t launch(const Params &p, int sms, cudaStream_t s) {
+constexpr int kPlanSms = 152;  // of a GB300: the plan is one of sizes alone
+
+template <int DH, bool CAP, bool BIAS, bool CUT>
+cudaError_t launch_as(const Params &p, int blocks, cudaStream_t s) {
   const size_t smem = Layout<DH>::kBytes + sizeof(Tail) + 1024;
-  auto *kernel = k_attn_fwd<DH, CAP, BIAS>;
+  auto *kernel = k_attn_fwd<DH, CAP, BIAS, CUT>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(p.items < sms ? p.items : sms), dim3(kThreads), smem, s, p);
+  return launch_pdl(kernel, dim3(blocks), dim3(kThreads), smem, s, p);
+}
+template <int DH, bool CAP, bool BIAS>
+cudaError_t launch(const Params &p, int sms, cudaStream_t s) {
+  if (p.t.tail > 0)
+    return launch_as<DH, CAP, BIAS, true>(p, p.t.rounds == 0 ? p.t.workers : kPlanSms, s);
+  return launch_as<DH, CAP, BIAS, false>(p, p.items < sms ? p.items : sms, s);
 }
 
 }  // namespace
@@ -591,14 +730,67 @@ cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s) {
   return launch_pdl(k_attn_order, dim3(1), dim3(kOrderThreads), 0, s, a);
 }
 
-cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, int sms, cudaStream_t s) {
-  const Params p{a, m, a.B * a.Hq * ((a.Sq + 2 * kTile - 1) / (2 * kTile))};
+// Cuts the items of the last round, which fewer than all blocks would have,
+// where that is worth it.  In steps (256 queries x 128 keys, 1.4 us): whole,
+// they take as long as the longest; in shares, that times items / workers, and
+// on top some 7 steps for the second item of a share and the join's launch,
+// and for the parts' way out and back some 1 / 27 each (at 5 TB/s, heads of
+// 128).  No share of less than 4 steps, at most some 32 parts of an item.
+// With documents the items' work is not known here: they are cut only where
+// there is less than a round of them, else taken from a counter.
+AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, bool causal,
+                          bool prefix, bool docs) {
+  AttnFwdPlan t;
+  const int64_t heads = B * Hq, blocks_q = (Sq + kAttnQueries - 1) / kAttnQueries;
+  const int64_t items = heads * blocks_q, rounds = items / kPlanSms;
+  const int64_t tail = items - rounds * kPlanSms;
+  if (tail == 0 || Sk == 0 || (docs && rounds > 0)) return t;
+  int64_t keys = Sk;  // that the longest of the tail sees
+  if (causal && !prefix) {
+    const int64_t end = (blocks_q - rounds * kPlanSms / heads) * kAttnQueries;
+    keys = (end < Sq ? end : Sq) + Sk - Sq;
+  }
+  const int64_t steps = keys > 0 ? (keys + kTile - 1) / kTile : 0;
+  int64_t workers = tail * steps / 4;
+  if (workers > 32 * tail) workers = 32 * tail;
+  if (workers > kPlanSms) workers = kPlanSms;
+  if (workers <= tail) return t;
+  const double saved = steps - double(steps) * tail / workers;
+  const double cost = 7 + double(tail + workers) * (D <= 64 ? 64 : 128) / 128 / 27;
+  if (saved < 1.25 * cost) return t;
+  t.rounds = static_cast<int>(rounds);
+  t.tail = static_cast<int>(tail);
+  t.workers = static_cast<int>(workers);
+  t.segments = static_cast<int>((workers + tail - 1) / tail + 1);
+  return t;
+}
+size_t attn_fwd_stat_bytes(const AttnFwdPlan &t) {
+  return size_t(t.tail) * t.segments * kAttnQueries * sizeof(float2);
+}
+size_t attn_fwd_part_bytes(const AttnFwdPlan &t, int D) {
+  return size_t(t.tail) * t.segments * kAttnQueries * (D <= 64 ? 64 : 128) * sizeof(float);
+}
+
+cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, const AttnFwdPlan &t, void *stat,
+                            void *part, int sms, cudaStream_t s) {
+  const Params p{a, m, a.B * a.Hq * ((a.Sq + kAttnQueries - 1) / kAttnQueries), t,
+                 static_cast<float2 *>(stat), static_cast<float4 *>(part)};
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
   if (a.D <= 64)
     return cap ? (bias ? launch<64, true, true>(p, sms, s) : launch<64, true, false>(p, sms, s))
                : (bias ? launch<64, false, true>(p, sms, s) : launch<64, false, false>(p, sms, s));
   return cap ? (bias ? launch<128, true, true>(p, sms, s) : launch<128, true, false>(p, sms, s))
              : (bias ? launch<128, false, true>(p, sms, s) : launch<128, false, false>(p, sms, s));
+}
+cudaError_t launch_attn_fwd_join(const AttnArgs &a, const AttnFwdPlan &t, const void *stat,
+                                 const void *part, cudaStream_t s) {
+  const Params p{a, {}, a.B * a.Hq * ((a.Sq + kAttnQueries - 1) / kAttnQueries), t,
+                 static_cast<float2 *>(const_cast<void *>(stat)),
+                 static_cast<float4 *>(const_cast<void *>(part))};
+  const int cols = a.D <= 64 ? 2 : 4;
+  return launch_pdl(a.D <= 64 ? k_attn_fwd_join<64> : k_attn_fwd_join<128>,
+                    dim3(static_cast<unsigned>(t.tail) * (kAttnQueries / 32) * cols),
+                    dim3(32 * kJoinWarps), 0, s, p);
 }
 
 }  // namespace lora

@@ -262,6 +262,49 @@ def test_large_scores():
     check(q, k, v, do, causal=False, backward=False)
 
 
+CUT = [
+    # batch, q_len, k_len, q_heads, k_heads, dim, causal: few queries over many keys
+    (1, 1, 5000, 8, 2, 64, True), (2, 17, 4999, 4, 1, 128, True), (1, 300, 6000, 4, 2, 128, True),
+    (3, 129, 3333, 2, 2, 80, False), (1, 255, 20001, 1, 1, 128, True), (1, 2048, 2048, 1, 1, 128, True),
+    (5, 256, 2500, 8, 4, 40, False),
+    # more items than blocks: the last round's are cut
+    (1, 1025, 5100, 40, 8, 16, True), (2, 600, 6001, 27, 27, 8, False),
+]
+
+
+@pytest.mark.parametrize("B,sq,sk,hq,hk,d,causal", CUT)
+def test_few_items_are_cut_along_the_keys(B, sq, sk, hq, hk, d, causal):
+    q, k, v, do = draw(B, sq, sk, hq, hk, d, sk)
+    before = rl.launch_count()
+    check(q, k, v, do, causal=causal, backward=False)
+    assert rl.launch_count() == before + 2, "attention and a join"
+
+
+def test_cut_items_with_every_score_and_mask():
+    q, k, v, do = draw(2, 200, 4100, 4, 2, 64, 5, gain=2.0)
+    check(q, k, v, do, causal=True, cap=5.0, backward=False)
+    check(q, k, v, do, causal=True, slopes=slopes_of(4), backward=False)
+    check(q, k, v, do, causal=True, prefix=torch.tensor([0, 4000], dtype=torch.int32), backward=False)
+    # documents: rows whose keys lie in one part only, in several, or nowhere
+    docs = packed([1000, 2500, 17, 33, 400, 50], 100, 2)
+    docs[1, :3000] = 7
+    check(q, k, v, do, causal=True, docs=docs, backward=False)
+    qd = torch.full((2, 200), 5, dtype=torch.int32)
+    qd[:, 50:] = 3
+    check(q, k, v, do, docs=(qd, docs), backward=False)
+    # the gradients take the joined lse
+    check(q[:, :, :2], k[:, :, :1], v[:, :, :1], do[:, :, :2], causal=True, cap=30.0)
+
+
+@pytest.mark.parametrize("shape", [(1, 300, 6000, 4, 2, 128), (1, 1025, 5100, 40, 8, 16)])
+def test_cut_items_repeat_bit_for_bit(shape):
+    q, k, v, _ = (t.to(DEV) for t in draw(*shape, 3))
+    o, lse = rl.attention_forward(q, k, v, causal=True)
+    for _ in range(3):
+        o1, lse1 = rl.attention_forward(q, k, v, causal=True)
+        assert torch.equal(o, o1) and torch.equal(lse, lse1)
+
+
 def test_same_bits_each_time():
     q, k, v, do = (t.to(DEV) for t in draw(2, 700, 700, 8, 2, 128, 4))
     runs = []
