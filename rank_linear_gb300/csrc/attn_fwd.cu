@@ -527,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         continue;
       }
       // straight to global memory: Q's shared memory is already the next item's
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: nothing was seen (NaN stays NaN)
       __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2];
 #pragma unroll 1
       for (int c = 0; c < DH; c += 32) {
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           tmem_wait_ld();
           pin<32>(o);
         }
-        if (!(l > 0.f))
+        if (l == 0.f)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
         store_rows32(out, a.so[1], row - lane, a.Sq, c, a.D, o, inv);
@@ -545,7 +545,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       tc_fence_before();  // O has been read before the next item's P is announced
       if (a.lse != nullptr && row < a.Sq)
         a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row] =
-            l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   }
   tc_fence_before();
@@ -581,14 +581,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_fwd_join(const __grid_
 #pragma unroll 4
   for (int s = 0; s < parts; ++s) {
     const float2 x = __ldcg(stat + s * kAttnQueries);
-    if (x.y > 0.f) m = fmaxf(m, x.x);
+    if (x.y != 0.f) m = fmaxf(m, x.x);
   }
   float l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
   for (int s = 0; s < parts; ++s) {
     const float2 x = __ldcg(stat + s * kAttnQueries);
-    if (x.y > 0.f) {  // else nothing was seen, and there may be no output
+    if (x.y != 0.f) {  // else nothing was seen, and there may be no output
       const float by = ex2(x.x - m);
       const float4 v = __ldcg(from + static_cast<int64_t>(s) * (DH / 4) * kAttnQueries);
       l = fmaf(by, x.y, l);
@@ -598,14 +598,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_fwd_join(const __grid_
       o.w = fmaf(by, v.w, o.w);
     }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
   tile[lane][warp * 4] = o.x * inv;
   tile[lane][warp * 4 + 1] = o.y * inv;
   tile[lane][warp * 4 + 2] = o.z * inv;
   tile[lane][warp * 4 + 3] = o.w * inv;
   if (a.lse != nullptr && col == 0 && warp == 0 && row0 + r < a.Sq)
     a.lse[static_cast<int64_t>(bh) * a.Sq + row0 + r] =
-        l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   __syncthreads();
   // eight lanes to a row of 32 elements
   const int y = threadIdx.x / 8, c = threadIdx.x % 8 * 4, row = row0 + r - lane + y;

@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
     }
     const int64_t row = static_cast<int64_t>(b) * a.Hq + h0 + head;
     if (p.splits == 1) {
-      const float inv = sum > 0.f ? 1.f / sum : 0.f;
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
       if (e < a.D)
         *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] +
                                    (h0 + head) * a.so[2] + e) =
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(512) k_attn_token_join(const Params p) {
     acc.z = fmaf(by, v.z, acc.z);
     acc.w = fmaf(by, v.w, acc.w);
   }
-  const float inv = sum > 0.f ? 1.f / sum : 0.f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2] + 4 * x) =
       make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
 }

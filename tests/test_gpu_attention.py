@@ -305,6 +305,27 @@ def test_cut_items_repeat_bit_for_bit(shape):
         assert torch.equal(o, o1) and torch.equal(lse, lse1)
 
 
+@pytest.mark.parametrize("sk", [300, 6000])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_what_is_not_finite_shows(sk, bad):
+    """A query that is not finite makes its own row NaN, and no other one; a key
+    every row that sees it."""
+    q, k, v, do = (t.to(DEV) for t in draw(1, 200, sk, 2, 1, 64, 8))
+    o, lse = rl.attention_forward(q, k, v)
+    dq = rl.attention_backward(do, q, k, v, o, lse)[0]
+    q[0, 77, 1, 3] = bad
+    o1, lse1 = rl.attention_forward(q, k, v)
+    dq1 = rl.attention_backward(do, q, k, v, o1, lse1)[0]
+    assert o1[0, 77, 1].isnan().all() and lse1[0, 1, 77].isnan() and dq1[0, 77, 1].isnan().all()
+    for clean, other in ((o, o1), (dq, dq1), (lse.transpose(1, 2), lse1.transpose(1, 2))):
+        other[0, 77, 1] = clean[0, 77, 1]
+        assert torch.equal(clean, other)
+    k[0, 250] = float("nan")
+    assert rl.attention_forward(q, k, v)[0].isnan().all()
+    n = torch.tensor([sk], dtype=torch.int32, device=DEV)
+    assert rl.attention_decode(q[:, 0], k, v, n).isnan().all()
+
+
 def test_same_bits_each_time():
     q, k, v, do = (t.to(DEV) for t in draw(2, 700, 700, 8, 2, 128, 4))
     runs = []
