@@ -115,7 +115,8 @@ __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], flo
 
 // ---------------------------------------------------------------- statistics
 // A warp takes 32 queries of one head (its neighbours the next heads, which
-// lie beside it), DH / 8 lanes to a row.
+// lie beside it), DH / 8 lanes to a row.  Bound by HBM and its few waves: 8192
+// queries of 32 heads of 128, 134 MB, 28 us from a cold L2.
 constexpr int kStatWarps = 8;
 template <int DH>
 __global__ void __launch_bounds__(32 * kStatWarps) k_attn_stats(const AttnArgs a) {

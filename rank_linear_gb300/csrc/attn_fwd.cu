@@ -12,7 +12,10 @@
 // Blocks stay (one per SM) and take item after item, so that an item's copies
 // and first scores run while the one before it is written out.  A scheduling
 // warp hands items out: in order of falling work without documents, from a
-// counter with them (their work varies).
+// counter with them (their work varies).  Where the last round would leave
+// SMs without an item, its items are cut along the keys (see attn_fwd_plan):
+// 2048 queries over 16000 keys 329 -> 306 us, 50 over 30000 with 4 heads 277 ->
+// 39 us.
 //
 // TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
 //

