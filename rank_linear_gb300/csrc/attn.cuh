@@ -223,6 +223,31 @@ __device__ __forceinline__ bool docs_equal(const DocRange &a, const DocRange &b)
   return a.lo == a.hi && b.lo == a.lo && b.hi == a.lo && !a.padded && !b.padded;
 }
 
+// By a whole warp, for a query tile of documents qr over the key tiles [0, hi):
+// those from lo on that it may see (to the new hi), and of them those that
+// share its one document, if they lie in one run: [same[0], same[1]).
+__device__ __forceinline__ void doc_tiles(const DocRange &qr, const int4 *k_ranges, int &lo,
+                                          int &hi, int (&same)[2]) {
+  int from = INT_MAX, to = 0, first = INT_MAX, last = 0, equal = 0;
+  for (int x = threadIdx.x % 32; x < hi; x += 32) {
+    const DocRange kr = doc_range(k_ranges, x);
+    if (docs_meet(qr, kr)) {
+      from = min(from, x);
+      to = x + 1;
+    }
+    if (docs_equal(qr, kr)) {
+      first = min(first, x);
+      last = x + 1;
+      ++equal;
+    }
+  }
+  hi = __reduce_max_sync(~0u, to);
+  lo = min(__reduce_min_sync(~0u, from), hi);
+  same[0] = __reduce_min_sync(~0u, first);
+  same[1] = __reduce_max_sync(~0u, last);
+  if (__reduce_add_sync(~0u, equal) != same[1] - same[0]) same[1] = same[0];
+}
+
 // Bits 0..n of a word (none for n < 0, all for n >= 31).
 __device__ __forceinline__ uint32_t bits_to(int n) {
   return n < 0 ? 0u : n >= 31 ? ~0u : (2u << n) - 1u;

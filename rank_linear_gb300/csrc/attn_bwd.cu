@@ -194,6 +194,7 @@ struct DqLayout {
 // begin + count) that some row sees.  count < 0: no more items.
 struct DqItem {
   int row0, h, b, begin, count;
+  int same[2];  // key tiles [0], ..., [1] - 1 of the queries' one document
 };
 struct DqTail {
   uint64_t q_full, q_free, k_full[3], k_empty[3], v_full[2];
@@ -304,17 +305,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
           const int prefix = a.prefix != nullptr ? a.prefix[it.b] : 0;
           int lo = 0, hi = max(0, (last_key(a, min(it.row0 + kTile, a.Sq) - 1 + off, prefix) +
                                    kTile) / kTile);
-          if (a.q_docs != nullptr && hi > 0) {
-            const DocRange qr = doc_range(a.q_ranges, int64_t(it.b) * qtiles + qt);
-            int from = INT_MAX, to = 0;
-            for (int x = lane; x < hi; x += 32)
-              if (docs_meet(qr, doc_range(a.k_ranges, int64_t(it.b) * ktiles + x))) {
-                from = min(from, x);
-                to = x + 1;
-              }
-            hi = __reduce_max_sync(~0u, to);
-            lo = min(__reduce_min_sync(~0u, from), hi);
-          }
+          it.same[0] = 0;
+          it.same[1] = INT_MAX;  // no documents: one
+          if (a.q_docs != nullptr && hi > 0)
+            doc_tiles(doc_range(a.q_ranges, int64_t(it.b) * qtiles + qt),
+                      a.k_ranges + int64_t(it.b) * ktiles, lo, hi, it.same);
           it.begin = lo;
           it.count = hi - lo;
         }
@@ -473,22 +468,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       const int pos = row + off;
       const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
       const int first_last = last_key(a, it.row0 + off, prefix);
-      DocRange qr = {0, 0, 0, 0}, kr = {0, 0, 0, 0};
+      const int same0 = it.same[0], same1 = it.same[1];
       int qd = -1;
-      if (a.q_docs != nullptr) {
-        qr = doc_range(a.q_ranges, int64_t(b) * qtiles + it.row0 / kTile);
-        if (row < a.Sq) qd = a.q_docs[b * a.qds + row];
-        if (count > 0) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + it.begin);
-      }
+      if (a.q_docs != nullptr && row < a.Sq) qd = a.q_docs[b * a.qds + row];
       for (int i = 0; i < count; ++i, ++x) {
         const int n = it.begin + i, key0 = n * kTile + half * 64;
-        bool whole = n * kTile + kTile - 1 <= first_last;
+        const bool same = n >= same0 && n < same1;
+        const bool whole = same && n * kTile + kTile - 1 <= first_last;
         int kd[2];
-        if (a.q_docs != nullptr) {
-          whole = whole && docs_equal(qr, kr);
-          if (!whole) load_docs(a.k_docs + b * a.kds + key0, a.Sk - key0, kd);
-          if (i + 1 < count) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
-        }
+        if (!same) load_docs(a.k_docs + b * a.kds + key0, a.Sk - key0, kd);
         const uint32_t s_addr = tmem + lanes + (x & 1) * kTile + half * 64;
         if (!(ok = wait_warp(tail->s_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
         tc_fence_after();
@@ -502,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
                                   static_cast<float>(pos - key0), -1.f);
         if (!whole) {
           uint32_t keep[2] = {~0u, ~0u};
-          if (a.q_docs != nullptr) same_doc(qd, kd, keep);
+          if (!same) same_doc(qd, kd, keep);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
             keep[c] &= bits_to(last - key0 - 32 * c);

@@ -53,6 +53,7 @@ struct Layout {
 // both.  count < 0: no more items.
 struct Item {
   int row0, h, b, lo[2], hi[2], begin, count;
+  int same[2][2];  // key tiles [0], ..., [1] - 1 of the query tile's one document
 };
 
 struct Tail {
@@ -194,17 +195,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
             const int first = it.row0 + t * kTile, last = min(first + kTile, a.Sq) - 1;
             int lo = 0;
             int hi = first < a.Sq ? max(0, (last_key(a, last + off, prefix) + kTile) / kTile) : 0;
-            if (a.q_docs != nullptr && hi > 0) {
-              const DocRange qr = doc_range(a.q_ranges, int64_t(it.b) * qtiles + 2 * qb + t);
-              int from = INT_MAX, to = 0;
-              for (int x = lane; x < hi; x += 32)
-                if (docs_meet(qr, doc_range(a.k_ranges, int64_t(it.b) * ktiles + x))) {
-                  from = min(from, x);
-                  to = x + 1;
-                }
-              hi = __reduce_max_sync(~0u, to);
-              lo = min(__reduce_min_sync(~0u, from), hi);
-            }
+            it.same[t][0] = 0;
+            it.same[t][1] = INT_MAX;  // no documents: one
+            if (a.q_docs != nullptr && hi > 0)
+              doc_tiles(doc_range(a.q_ranges, int64_t(it.b) * qtiles + 2 * qb + t),
+                        a.k_ranges + int64_t(it.b) * ktiles, lo, hi, it.same[t]);
             it.lo[t] = lo;
             it.hi[t] = hi;
           }
@@ -392,24 +387,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       const int pos = row + off;
       const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
       const int first_last = last_key(a, first + off, prefix);  // of the tile's first row
-      DocRange qr = {0, 0, 0, 0}, kr = {0, 0, 0, 0};
-      int qd = 0;
-      if (a.q_docs != nullptr) {
-        qr = doc_range(a.q_ranges, int64_t(b) * qtiles + first / kTile);
-        qd = row < a.Sq ? a.q_docs[b * a.qds + row] : -1;
-        if (lo < hi) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + lo);
-      }
+      const int same0 = it.same[t][0], same1 = it.same[t][1];
+      int qd = -1;
+      if (a.q_docs != nullptr && row < a.Sq) qd = a.q_docs[b * a.qds + row];
       float m = -INFINITY;  // the maximum that P is relative to, in log2 units
       float2 l2 = make_float2(0.f, 0.f);
       for (int n = lo; n < hi; ++n, ++turn) {
         // does the mask leave the whole tile?
-        bool whole = n * kTile + kTile - 1 <= first_last;
+        const bool same = n >= same0 && n < same1;
+        const bool whole = same && n * kTile + kTile - 1 <= first_last;
         int kd[4];
-        if (a.q_docs != nullptr) {
-          whole = whole && docs_equal(qr, kr);
-          if (!whole) load_docs(a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile, kd);
-          if (n + 1 < hi) kr = doc_range(a.k_ranges, int64_t(b) * ktiles + n + 1);
-        }
+        if (!same) load_docs(a.k_docs + b * a.kds + n * kTile, a.Sk - n * kTile, kd);
         if (!(ok = wait_warp(tail->s_full[t], turn, abort_flag, a.dev_status))) break;
         tc_fence_after();
         float s[kTile];
@@ -435,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         }
         if (!whole) {
           uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-          if (a.q_docs != nullptr) same_doc(qd, kd, keep);
+          if (!same) same_doc(qd, kd, keep);
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             keep[c] &= bits_to(last - n * kTile - 32 * c);
