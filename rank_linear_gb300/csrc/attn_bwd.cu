@@ -597,6 +597,7 @@ struct DkvTail {
   uint64_t s_full, dp_full, p_full, dz_full, done, drain;
   uint32_t tmem;
   int abort_flag, lo, hi;
+  int same[2], equal;  // query tiles that share the keys' one document: first, end, count
 };
 // Where the blocks of a cluster add up (over the tiles): fp32 rows of dk, then
 // of dv, from every rank.
@@ -647,8 +648,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     mbar_init(smem_u32(&tail->done), 1);
     mbar_init(smem_u32(&tail->drain), 1);
     tail->abort_flag = 0;
-    tail->lo = INT_MAX;
-    tail->hi = 0;
+    tail->lo = tail->same[0] = INT_MAX;
+    tail->hi = tail->same[1] = tail->equal = 0;
     fence_barrier_init();
     tma_prefetch(&p.m.q);
     tma_prefetch(&p.m.k);
@@ -667,17 +668,24 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   // ---- the query tiles that see some key
   const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
   const int first = a.causal && key0 >= prefix ? max(0, key0 - off) / kTile : 0;
-  DocRange kr = {0, 0, 0, 0};
   if (a.q_docs != nullptr) {
-    kr = doc_range(a.k_ranges, int64_t(b) * ktiles + kt);
-    for (int n = first + threadIdx.x; n < qtiles; n += kThreads)
-      if (docs_meet(kr, doc_range(a.q_ranges, int64_t(b) * qtiles + n))) {
+    const DocRange kr = doc_range(a.k_ranges, int64_t(b) * ktiles + kt);
+    for (int n = first + threadIdx.x; n < qtiles; n += kThreads) {
+      const DocRange qr = doc_range(a.q_ranges, int64_t(b) * qtiles + n);
+      if (docs_meet(kr, qr)) {
         atomicMin(&tail->lo, n);
         atomicMax(&tail->hi, n + 1);
       }
+      if (docs_equal(kr, qr)) {
+        atomicMin(&tail->same[0], n);
+        atomicMax(&tail->same[1], n + 1);
+        atomicAdd(&tail->equal, 1);
+      }
+    }
   } else if (threadIdx.x == 0) {
     tail->lo = first;
-    tail->hi = qtiles;
+    tail->hi = tail->same[1] = tail->equal = qtiles;
+    tail->same[0] = 0;
   }
   __syncthreads();
   const int end = uniform(tail->hi), begin = uniform(min(tail->lo, end));
@@ -832,29 +840,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     const int all_from = a.causal && tile_last >= prefix ? tile_last - off : -(1 << 28);
     const int kd = a.q_docs != nullptr && key < a.Sk ? a.k_docs[b * a.kds + key] : -1;
     bool ok = true;
-    DocRange qr = {0, 0, 0, 0};
-    if (a.q_docs != nullptr && count > 0) qr = doc_range(a.q_ranges, int64_t(b) * qtiles + begin + step0 % per_head);
+    // query tiles of the keys' one document, where they lie in one run
+    const int same0 = tail->same[0];
+    const int same1 = tail->equal == tail->same[1] - same0 ? tail->same[1] : same0;
     int head = g * a.group, n = begin;  // of this step
     if (count > 0) {
       head += step0 / per_head;
       n += step0 % per_head;
     }
-    int head1 = head, n1 = n;  // of the next
-    for (int i = 0; i < count; ++i, head = head1, n = n1) {
-      if (++n1 == end) {
-        n1 = begin;
-        ++head1;
-      }
+    for (int i = 0; i < count; ++i) {
       const int q0 = n * kTile + half * 64;
       const ScoreConst sc = score_const(a, head);
-      bool whole = n * kTile >= all_from;
+      const bool same = n >= same0 && n < same1;
+      const bool whole = same && n * kTile >= all_from;
       int qd[2];
-      if (a.q_docs != nullptr) {
-        whole = whole && docs_equal(kr, qr);
-        if (!whole) load_docs(a.q_docs + b * a.qds + q0, a.Sq - q0, qd);
-        if (i + 1 < count)
-          qr = doc_range(a.q_ranges, int64_t(b) * qtiles + n1);
-      }
+      if (!same) load_docs(a.q_docs + b * a.qds + q0, a.Sq - q0, qd);
       // the step's scores, and its statistics
       if (!(ok = wait_warp(tail->s_full, i, abort_flag, a.dev_status) &&
                  wait_warp(tail->e_full[i % L::kESlots], i / L::kESlots, abort_flag, a.dev_status)))
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
                                static_cast<float>(q0 + off - key), 1.f);
       if (!whole) {
         uint32_t keep[2] = {~0u, ~0u};
-        if (a.q_docs != nullptr) same_doc(kd, qd, keep);
+        if (!same) same_doc(kd, qd, keep);
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           keep[c] &= ~bits_to(from - 1 - q0 - 32 * c);
@@ -921,6 +921,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&tail->dz_full));
+      if (++n == end) {
+        n = begin;
+        ++head;
+      }
     }
     if (ok && count > 0) {
       ok = wait_warp(tail->done, 0, abort_flag, a.dev_status);
