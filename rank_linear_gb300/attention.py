@@ -11,7 +11,7 @@ import torch
 
 from . import _lib
 from .lora import _ptr, _stream_ptr
-from .rotary import _block, _layout, _on
+from .rotary import _block, _empty_like, _layout, _on
 
 
 def _strides(t, name):
@@ -119,19 +119,23 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
     """
     qd, kd = _doc_pair(documents, q, k)
     with _on(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(q.shape[0], q.shape[2], q.shape[1], dtype=torch.float32,
-                              device=q.device)
+        # (an output made here has the layout that q's decides)
         key = ("forward", _layout(q), _layout(k), _layout(v), _layout(out), scale, causal, softcap,
                _layout(slopes), _layout(qd), _layout(kd), _layout(prefix))
+        if out is None:
+            out = _empty_like(q)
 
         def make():
             sh = _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix,
                              {"o": out}, {})
-            return sh, _workspace_bytes(sh, qd is not None, prefix is not None, 0)
-        block, need = _block(key, make)
+            need = _workspace_bytes(sh, qd is not None, prefix is not None, 0)
+            return sh, need, (sh.batch, sh.q_heads, sh.q_len)
+        block, need, rows = _block(key, make)
+        if lse is None:
+            lse = torch.empty(rows, dtype=torch.float32, device=q.device)
+        elif lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != rows or \
+                lse.device != q.device:
+            raise ValueError(f"lse must be a contiguous float32 tensor of shape {rows}")
         workspace = _scratch(need, q, workspace)
     sh = _filled(block, slopes, qd, kd, prefix)
     st = _lib.lib().lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
@@ -153,9 +157,9 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
     own = dq is None and dk is None and dv is None and workspace is None
     with _on(stream):
         if not own:
-            dq = torch.empty(q.shape, dtype=q.dtype, device=q.device) if dq is None else dq
-            dk = torch.empty(k.shape, dtype=k.dtype, device=k.device) if dk is None else dk
-            dv = torch.empty(v.shape, dtype=v.dtype, device=v.device) if dv is None else dv
+            dq = _empty_like(q) if dq is None else dq
+            dk = _empty_like(k) if dk is None else dk
+            dv = _empty_like(v) if dv is None else dv
         key = ("backward", _layout(q), _layout(k), _layout(v), _layout(out), _layout(dout),
                _layout(dq), _layout(dk), _layout(dv), scale, causal, softcap, _layout(slopes),
                _layout(qd), _layout(kd), _layout(prefix))
@@ -198,10 +202,10 @@ def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, s
         raise ValueError("q must be [batch, q_heads, dim]")
     L = _lib.lib()
     with _on(stream):
-        if out is None:
-            out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         key = ("token", _layout(q), _layout(k_cache), _layout(v_cache), _layout(lengths), scale,
                softcap, _layout(slopes), _layout(out))
+        if out is None:
+            out = _empty_like(q)
         sh, need = _block(key, lambda: _make_token(q, k_cache, v_cache, lengths, scale, softcap,
                                                    slopes, out))
         sh = _filled(sh, slopes, None, None, None)

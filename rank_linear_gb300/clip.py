@@ -29,15 +29,19 @@ class GradClip:
         table = (_lib.ClipTensor * max(len(self.grads), 1))()
         device = None
         for i, (g, o) in enumerate(zip(self.grads, self.out)):
+            where = g.device
             if not g.is_cuda or not g.is_contiguous() or not o.is_contiguous():
                 raise ValueError(f"gradient {i}: contiguous CUDA tensors are needed")
-            if o.shape != g.shape or o.dtype != g.dtype or o.device != g.device:
+            if o is not g and (o.shape != g.shape or o.dtype != g.dtype or o.device != where):
                 raise ValueError(f"gradient {i}: its output has another shape, type or device")
-            if device is not None and g.device != device:
+            if device is None:
+                device = where
+            elif where != device:
                 raise ValueError(f"gradient {i} is on another device")
-            device = g.device
-            table[i] = _lib.ClipTensor(g.data_ptr() or None, o.data_ptr() or None, g.numel(),
-                                       _dtype_code(g))
+            row, at = table[i], g.data_ptr()
+            row.in_ = at
+            row.out = at if o is g else o.data_ptr()
+            row.count, row.dtype = g.numel(), _dtype_code(g)
         L = _lib.lib()
         self.bytes = int(L.lora_clip_plan_bytes(table, len(self.grads)))
         if self.bytes == 0:
@@ -47,6 +51,7 @@ class GradClip:
                    "lora_clip_plan_build")
         self.plan = image.to(device if device is not None else torch.device("cuda"))
         self.device, self._at = self.plan.device, self.plan.data_ptr()
+        self._scalar = torch.empty((), dtype=torch.float32, device=self.device)
 
     @staticmethod
     def _largest(norm_type) -> int:
@@ -58,8 +63,8 @@ class GradClip:
         if norm is None:
             if stream is not None:
                 with torch.cuda.stream(stream):
-                    return torch.empty((), dtype=torch.float32, device=self.device)
-            return torch.empty((), dtype=torch.float32, device=self.device)
+                    return torch.empty_like(self._scalar)
+            return torch.empty_like(self._scalar)
         if norm.dtype != torch.float32 or norm.numel() != 1 or norm.device != self.device:
             raise ValueError("norm must be one float32 on the gradients' device")
         return norm

@@ -477,6 +477,16 @@ def test_token_repeats_bit_for_bit():
         assert torch.equal(first, rl.attention_decode(q[:, 0], k, v, n))
 
 
+def test_refuses_a_wrong_lse():
+    q, k, v, _ = (t.to(DEV) for t in draw(2, 30, 30, 2, 1, 64, 1))
+    good = torch.empty(2, 2, 30, device=DEV)
+    rl.attention_forward(q, k, v, lse=good)
+    for bad in (good[:, :1], good.half(), good.transpose(1, 2).contiguous(), good.cpu(),
+                torch.empty(2, 2, 60, device=DEV)[:, :, ::2]):
+        with pytest.raises(ValueError, match="lse"):
+            rl.attention_forward(q, k, v, lse=bad)
+
+
 def test_nothing_to_do():
     e = lambda *s: torch.empty(*s, dtype=torch.bfloat16, device=DEV)
     o, lse = rl.attention_forward(e(0, 5, 4, 64), e(0, 5, 2, 64), e(0, 5, 2, 64))
