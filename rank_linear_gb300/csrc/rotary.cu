@@ -10,8 +10,8 @@
 // eight heads 54 us; items divided among threads 20 us (300 instructions an
 // item); a token to a warp 17 us, but in fp32 141 us where the warps of a
 // block side by side take 120 us (5461 x 3 tokens x 48 heads), as here: 17 us
-// (84 MB: 4.9 TB/s, much of it the launch's ramps), 120 us (805 MB: 6.7 TB/s, a
-// copy's bandwidth).
+// (84 MB: 4.9 TB/s, much of it the launch's ramps), and 115 to 121 us (805 MB:
+// 6.7 to 7.0 TB/s, a copy's bandwidth).
 #include <cuda_bf16.h>
 
 #include <cmath>
@@ -235,10 +235,13 @@ cudaError_t launch_rotary(RotaryArgs &a, bool neighbours, bool copy_tail, int sm
   a.chunks = a.rot_chunks + (copy_tail ? (a.dim - a.rot + 2 * VEC - 1) / (2 * VEC) : 0);
   a.lane_heads = a.chunks > 32 ? 1 : 32 / a.chunks;
   for (int t = 0; t < 2; ++t) a.groups[t] = (a.heads[t] + a.lane_heads - 1) / a.lane_heads;
-  // tokens of a block: an angle for each thread or so, fewer tokens while that
-  // would leave SMs idle
-  a.tokens = 8;
-  while (a.tokens > 1 && (a.tokens * a.rot > 1024 || a.all_tokens < int64_t(a.tokens) * 4 * sms))
+  // Tokens of a block: some 32 KB of heads (in bf16, 10 KB a token, one token
+  // takes 43 us where three to eight take 35 for 8192; in fp32, 24 KB a token,
+  // eight take 131 us where one takes 121 for 16383), no more than 1024 angles,
+  // and fewer while that would leave less than two blocks to an SM.
+  const int64_t bytes = int64_t(a.heads[0] + a.heads[1]) * a.dim * sizeof(T);
+  a.tokens = static_cast<int>(bytes > 32768 ? 1 : bytes * 8 < 32768 ? 8 : 32768 / bytes);
+  while (a.tokens > 1 && (a.tokens * a.rot > 1024 || a.all_tokens < int64_t(a.tokens) * 2 * sms))
     a.tokens /= 2;
   const int64_t blocks = (a.all_tokens + a.tokens - 1) / a.tokens;
   return launch_pdl(neighbours ? k_rotary<T, VEC, true> : k_rotary<T, VEC, false>,
