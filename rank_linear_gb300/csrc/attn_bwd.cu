@@ -457,22 +457,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int x = 0, used = 0;  // tiles, and items with tiles, before this one
     bool ok = true;
+    // an item, and what is read for its row: asked for before the item ahead
+    // of it is written out
     DqItem it;
-    for (int item = 0; ok && next_item(tail, item, it, abort_flag, a.dev_status); ++item) {
+    float sub = 0.f, neg_delta = 0.f;
+    int prefix = 0, qd = -1;
+    auto take = [&](int n) {
+      if (!next_item(tail, n, it, abort_flag, a.dev_status)) return false;
+      const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + it.h) * (qtiles * kTile) + it.row0 + r;
+      sub = __ldcg(a.sub + at);
+      if constexpr (!ONE_TILE) neg_delta = __ldcg(a.neg_delta + at);
+      if (a.prefix != nullptr) prefix = a.prefix[it.b];
+      if (a.q_docs != nullptr)
+        qd = it.row0 + r < a.Sq ? a.q_docs[it.b * a.qds + it.row0 + r] : -1;
+      return true;
+    };
+    bool more = take(0);
+    for (int item = 0; more; ++item) {
       const int b = it.b, h = it.h, row = it.row0 + r, count = it.count;
-      const int64_t stat = (static_cast<int64_t>(b) * a.Hq + h) * (qtiles * kTile) + row;
-      const float sub = __ldcg(a.sub + stat);
-      float neg_delta = ONE_TILE ? 0.f : __ldcg(a.neg_delta + stat);
-      const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
       const ScoreConst sc = score_const(a, h);
       const int pos = row + off;
       const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
       const int first_last = last_key(a, it.row0 + off, prefix);
-      const int same0 = it.same[0], same1 = it.same[1];
-      int qd = -1;
-      if (a.q_docs != nullptr && row < a.Sq) qd = a.q_docs[b * a.qds + row];
+      const int same0 = it.same[0], same1 = it.same[1], begin = it.begin;
       for (int i = 0; i < count; ++i, ++x) {
-        const int n = it.begin + i, key0 = n * kTile + half * 64;
+        const int n = begin + i, key0 = n * kTile + half * 64;
         const bool same = n >= same0 && n < same1;
         const bool whole = same && n * kTile + kTile - 1 <= first_last;
         int kd[2];
@@ -523,7 +532,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
           mbar_arrive(smem_u32(&tail->part_full));
           if (!(ok = wait_warp(tail->part_full, used, abort_flag, a.dev_status))) break;
           neg_delta = -(part[r] + part[kTile + r]);
-          if (half == 0) a.neg_delta[stat] = neg_delta;
+          if (half == 0)
+            a.neg_delta[(static_cast<int64_t>(b) * a.Hq + h) * (qtiles * kTile) + row] = neg_delta;
         }
         const float2 nd = make_float2(neg_delta, neg_delta);
 #pragma unroll
@@ -548,6 +558,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         mbar_arrive(smem_u32(&tail->dz_full[x & 1]));
       }
       if (!ok) break;
+      more = take(item + 1);
       if (count > 0) {
         if (!(ok = wait_warp(tail->done, used, abort_flag, a.dev_status))) break;
         ++used;
