@@ -26,8 +26,8 @@
 //
 // Measured (32 heads of 128, 8 key heads), all three: 8192 x 8192 without a
 // mask 2465 us (1115 TFLOP/s of the formula's five products, 1560 of the seven
-// done), causal 1194 us (1150), 4096 causal 342 us (1005), five documents in
-// 8192 486 us (statistics 28, dq 198, dk/dv 263 when timed one by one), heads
+// done), causal 1200 us (1145), 4096 causal 346 us (995), five documents in
+// 8192 465 us (statistics 27, dq 181, dk/dv 256 when timed one by one), heads
 // of 64 causal 926 us (740).  Bound by shared memory: a dk/dv step's products
 // read 256 KB of operands, 2000 cycles at 128 B a cycle, as long as the
 // products themselves take.

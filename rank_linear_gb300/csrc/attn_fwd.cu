@@ -19,11 +19,12 @@
 //
 // TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
 //
-// Measured (32 heads of 128, 8 key heads): 8192 x 8192 without a mask 630 us
-// (1750 TFLOP/s, 0.89 of what a large bf16 product reaches), causal 338 us
-// (1625), heads of 64 causal 286 us (960: the exponentials take as long as the
-// products), 4096 causal 101 us (1360); with capped scores 162 us, with a
-// distance bias 143 us (one or two more operations a pair).  Bound by the
+// Measured (32 heads of 128, 8 key heads): 8192 x 8192 without a mask 620 us
+// (1775 TFLOP/s, 0.91 of what a large bf16 product reaches), causal 334 us
+// (1645), heads of 64 causal 284 us (965: the exponentials take as long as the
+// products), 4096 causal 100 us (1370); with capped scores 162 us, with a
+// distance bias 134 us (one or two more operations a pair); five documents in
+// 8192 148 us.  Bound by the
 // tensor cores where a block has many steps; an item begins and ends in some
 // 4 us that overlap its neighbours' steps only in part, and 256-row items
 // leave work unused along the diagonal and at documents' edges.

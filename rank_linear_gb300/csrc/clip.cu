@@ -24,7 +24,7 @@ namespace lora {
 namespace {
 
 constexpr int kThreads = 256, kVecs = 4;  // 16-byte vectors of a thread per 16 KB chunk
-constexpr int kNormBlocks = 4, kClipBlocks = 6, kMaxBlocks = 4096;  // blocks of an SM
+constexpr int kNormBlocks = 4, kClipBlocks = 6, kMaxBlocks = 1024;  // blocks of an SM (two), of all
 
 struct Chunk {
   const void *in;
