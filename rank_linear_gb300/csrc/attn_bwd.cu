@@ -1071,12 +1071,16 @@ cudaError_t launch_attn_dq(const AttnArgs &a, const AttnBwdMaps &m, int sms, cud
 cudaError_t launch_attn_dkv(const AttnArgs &a, const AttnBwdMaps &m, int sms, cudaStream_t s) {
   Params p{a, m, a.B * a.Hk * ((a.Sk + kTile - 1) / kTile), 1};
   // Blocks of an item: while a cluster of twice as many fits the SMs at once,
-  // or would leave each at least 16 steps (of some 1.5 us; a block's beginning
-  // and end, and the meeting of the cluster, take some 12 us).
+  // or, where the items differ in work, would leave each at least 16 steps (of
+  // some 1.5 us; a block's beginning and end, and the meeting of the cluster,
+  // take some 12 us).  Items, steps, and backward by blocks of an item, 1 / 2 /
+  // 4 / 8: causal 128, 64: 144 / 117 / 146 / 220 us; 64, 128: 220 / 142 / 113 /
+  // 158; 128, 16: 62 / 72 / 97 / 165; without a mask 128, 64: 182 / 197 / 219 / 281.
   const int steps = a.group * ((a.Sq + kTile - 1) / kTile);
   while (p.cluster < 8 && steps >= 4 * p.cluster &&
          (p.items * p.cluster * 2 <= sms ||
-          (p.items * p.cluster < sms && steps >= 32 * p.cluster)))
+          ((a.causal || a.q_docs != nullptr) && p.items * p.cluster < sms &&
+           steps >= 32 * p.cluster)))
     p.cluster *= 2;
   LORA_ATTN_VARIANT(start_dkv);
 }
