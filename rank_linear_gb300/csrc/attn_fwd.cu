@@ -725,9 +725,12 @@ cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s) {
 // Cuts the items of the last round, which fewer than all blocks would have,
 // where that is worth it.  In steps (256 queries x 128 keys, 1.4 us): whole,
 // they take as long as the longest; in shares, that times items / workers, and
-// on top some 7 steps for the second item of a share and the join's launch,
-// and for the parts' way out and back some 1 / 27 each (at 5 TB/s, heads of
-// 128).  No share of less than 4 steps, at most some 32 parts of an item.
+// on top some 5 steps for the second item of a share and the join's launch,
+// and for the parts' way out and back some 1 / 22 each (heads of 128;
+// half that where only the first 128 of the queries are there).
+// Measured, whole and cut, by what this makes of it (steps saved over their
+// cost): 0.6: 33 and 35 us, 33 and 33; 1.0: 625 and 625; 1.1: 164 and 164; 1.2:
+// 23 and 18, 53 and 45; 1.4: 31 and 23, 29 and 21; 2.1: 66 and 51; 6: 475 and 367.  No share of less than 4 steps, at most some 32 parts of an item.
 // With documents the items' work is not known here: they are cut only where
 // there is less than a round of them, else taken from a counter.
 AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, bool causal,
@@ -748,8 +751,9 @@ AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, 
   if (workers > kPlanSms) workers = kPlanSms;
   if (workers <= tail) return t;
   const double saved = steps - double(steps) * tail / workers;
-  const double cost = 7 + double(tail + workers) * (D <= 64 ? 64 : 128) / 128 / 27;
-  if (saved < 1.25 * cost) return t;
+  const double part = (D <= 64 ? 0.5 : 1.0) * (Sq <= kTile ? 0.5 : 1.0) / 22;
+  const double cost = 5 + part * (tail + workers);
+  if (saved < 1.1 * cost) return t;
   t.rounds = static_cast<int>(rounds);
   t.tail = static_cast<int>(tail);
   t.workers = static_cast<int>(workers);
