@@ -124,6 +124,17 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap *tm,
       "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(token), "r"(head), "r"(batch)
       : "memory");
 }
+// The same over [batch][head / P][token][head modulo P][dim] maps, P heads of a
+// token side by side.
+__device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap *tm, uint32_t bar,
+                                            int32_t x, int32_t token, int32_t heads, int32_t batch) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(tm)), "r"(bar), "r"(x), "r"(0), "r"(token), "r"(heads),
+      "r"(batch)
+      : "memory");
+}
 __device__ __forceinline__ void tma_prefetch_4d(const CUtensorMap *tm, int32_t x, int32_t token,
                                                 int32_t head, int32_t batch) {
   asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(
@@ -388,9 +399,11 @@ __device__ __forceinline__ void zero_padding_rows(uint8_t *tile, const int *docs
 // those from `end` on left out.  Four lanes first exchange 16-byte pieces so
 // that a store writes 64 bytes of a row side by side: straight from the row
 // owners it takes a request for every 16 bytes (2500 against 900 cycles for a
-// tile of dq).
+// tile of dq).  shift > 0: the rows are 2^shift heads, `head_stride` apart, of
+// one token after the other.
 __device__ __forceinline__ void store_rows32(__nv_bfloat16 *base, int64_t stride, int row0, int end,
-                                             int c, int D, const float *v, float by) {
+                                             int c, int D, const float *v, float by, int shift = 0,
+                                             int64_t head_stride = 0) {
   const int lane = threadIdx.x % 32;
   uint32_t w[4][4];  // pieces of this lane's row
 #pragma unroll
@@ -426,7 +439,8 @@ __device__ __forceinline__ void store_rows32(__nv_bfloat16 *base, int64_t stride
   for (int i = 0; i < 4; ++i) {
     const int row = row0 + (lane & ~3) + i;
     if (row < end && col < D)
-      *reinterpret_cast<uint4 *>(base + row * stride + col) =
+      *reinterpret_cast<uint4 *>(base + (row >> shift) * stride +
+                                 (row & ((1 << shift) - 1)) * head_stride + col) =
           make_uint4(w[i][0], w[i][1], w[i][2], w[i][3]);
   }
 }

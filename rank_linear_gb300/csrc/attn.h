@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdint>
 
 #include "internal.h"
@@ -49,17 +50,20 @@ struct AttnBwdMaps {
 // what is left of the items, fewer than there are blocks, is cut along the
 // keys: `tail` items in equal shares for `workers` blocks, each share part of
 // one item or of two.  An item has up to `segments` parts, joined by a second
-// launch.  tail = 0: nothing is cut (rounds is not used).
+// launch.  tail = 0: nothing is cut.  shift > 0: an item's rows are 2^shift
+// heads of a group, side by side for one query after the other (the map of q
+// is then one of five dimensions).
 struct AttnFwdPlan {
-  int rounds = 0, tail = 0, workers = 0, segments = 0;
+  int rounds = INT_MAX, tail = 0, workers = 0, segments = 0, shift = 0;
+  bool special() const { return tail > 0 || shift > 0; }
 };
 constexpr int kAttnQueries = 256;
 // The parts' maxima and sums (float2 [tail][segments][kAttnQueries]), and their
 // outputs ([tail][segments][dim rounded up to 64 / 4][kAttnQueries] float4).
 size_t attn_fwd_stat_bytes(const AttnFwdPlan &t);
 size_t attn_fwd_part_bytes(const AttnFwdPlan &t, int D);
-AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, bool causal,
-                          bool prefix, bool docs);
+AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int group, int64_t Sq, int64_t Sk, int D,
+                          bool causal, bool prefix, bool docs);
 
 // Ranges of the documents (and counters zeroed); then the order, if asked for.
 cudaError_t launch_attn_ranges(const AttnArgs &a, cudaStream_t s);

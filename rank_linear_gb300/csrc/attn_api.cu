@@ -114,6 +114,29 @@ lora_status_t tensor_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], 
   return LORA_OK;
 }
 
+// Map of q with 2^shift heads of a token side by side: boxes of 64 elements x
+// those heads x as many tokens as make 128 rows.
+lora_status_t grouped_map(CUtensorMap *tm, const void *p, const int64_t (&s)[3], const AttnArgs &a,
+                          int shift) {
+  auto fn = encode_fn();
+  if (!fn) return fail(LORA_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+  const int heads = 1 << shift;
+  cuuint64_t dims[5] = {uint64_t(a.D), uint64_t(heads), uint64_t(a.Sq), uint64_t(a.Hq / heads),
+                        uint64_t(a.B)};
+  const int64_t by[4] = {s[2], s[1], s[2] * heads, s[0]};
+  cuuint64_t strides[4];
+  for (int i = 0; i < 4; ++i) strides[i] = uint64_t(dims[i + 1] > 1 ? by[i] : a.D) * 2;
+  cuuint32_t box[5] = {64, uint32_t(heads), uint32_t(128 / heads), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  CUresult r = fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(p), dims, strides, box,
+                  es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(LORA_ERR_CUDA, "tensor map for groups of q (strides %lld, %lld, %lld) failed: CUresult %d",
+                (long long)s[0], (long long)s[1], (long long)s[2], static_cast<int>(r));
+  return LORA_OK;
+}
+
 // Workspace: [document ranges of the query tiles, of the key tiles][item
 // counters][order of the key tiles][statistics of the query rows, two]; the
 // forward's [maxima and sums][outputs] of the parts of items it cuts.
@@ -142,7 +165,7 @@ Plan make_plan(const lora_attention_t *p, bool backward) {
     w.neg_delta = off;
     off += rup(rows * 4, 256);
   } else {
-    w.fwd = attn_fwd_plan(p->batch, p->q_heads, p->q_len, p->k_len, p->dim, p->causal != 0,
+    w.fwd = attn_fwd_plan(p->batch, p->q_heads, p->q_heads / p->k_heads, p->q_len, p->k_len, p->dim, p->causal != 0,
                           p->prefix != nullptr, p->q_docs != nullptr);
     w.stat = off;
     off += rup(attn_fwd_stat_bytes(w.fwd), 256);
@@ -219,7 +242,8 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   a.lse = lse;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   AttnMaps m;
-  LORA_TRY(tensor_map(&m.q, q, shape->q, a, a.Sq, a.Hq, "q"));
+  LORA_TRY(w.fwd.special() ? grouped_map(&m.q, q, shape->q, a, w.fwd.shift)
+                           : tensor_map(&m.q, q, shape->q, a, a.Sq, a.Hq, "q"));
   LORA_TRY(tensor_map(&m.k, no_k ? q : k, shape->k, a, a.Sk, a.Hk, "k"));
   LORA_TRY(tensor_map(&m.v, no_k ? q : v, shape->v, a, a.Sk, a.Hk, "v"));
   LORA_TRY(make_ranges(a, w, workspace, false, st));

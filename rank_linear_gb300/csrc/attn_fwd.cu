@@ -15,7 +15,8 @@
 // counter with them (their work varies).  Where the last round would leave
 // SMs without an item, its items are cut along the keys (see attn_fwd_plan):
 // 2048 queries over 16000 keys 329 -> 306 us, 50 over 30000 with 4 heads 277 ->
-// 39 us.
+// 39 us.  Few queries share an item with the heads of their group, which read
+// the same keys: 16 over 8192, four times 32 heads over 8, 85 -> 45 us.
 //
 // TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
 //
@@ -104,9 +105,10 @@ __device__ __forceinline__ bool next_item(Tail *tail, int n, Item &item, volatil
   return item.count >= 0;
 }
 
-// CUT: items of the last round are cut along the keys (a variant: in the same
-// kernel it costs the softmax registers, and packed documents 4 %).
-template <int DH, bool CAP, bool BIAS, bool CUT>
+// SPECIAL: items of the last round are cut along the keys, or rows are heads of
+// a group side by side (a variant: in the same kernel it costs the softmax
+// registers, and packed documents 4 %).
+template <int DH, bool CAP, bool BIAS, bool SPECIAL>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant__ Params p) {
   using L = Layout<DH>;
   extern __shared__ uint8_t raw[];
@@ -118,6 +120,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
 
   const int off = a.Sk - a.Sq;
   const int ktiles = (a.Sk + kTile - 1) / kTile, qtiles = (a.Sq + kTile - 1) / kTile;
+  // rows: queries, or 2^shift heads of each
+  const int shift = SPECIAL ? p.t.shift : 0, rows = a.Sq << shift;
 
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&tail->q_full), 1);
@@ -161,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     const uint32_t v_ring = k_ring + L::kKSlots * L::kTileBytes;
     if (warp == 10) {
       // ------------------------------------------------------ items
-      const int heads = a.B * a.Hq, blocks_q = p.items / heads;
+      const int sets = a.Hq >> shift, heads = a.B * sets, blocks_q = p.items / heads;
       for (int n = 0;; ++n) {
         const int s = n % kItemSlots;
         if (n >= kItemSlots &&
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           id = __shfl_sync(~0u, id, 0);
         }
         int from_part = 0, to_part = 1, parts = 0;
-        if (CUT && n >= p.t.rounds) {  // this block's share of the items that are cut
+        if (SPECIAL && n >= p.t.rounds) {  // this block's share of the items that are cut
           const int i = place * p.t.tail / p.t.workers + n - p.t.rounds;
           parts = p.t.workers;
           from_part = max(place * p.t.tail - i * parts, 0);
@@ -187,19 +191,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (id < p.items) {
           // the last queries, which see most keys of a causal mask, first
           const int qb = blocks_q - 1 - id / heads, bh = id % heads;
-          it.b = bh / a.Hq;
-          it.h = bh % a.Hq;
+          it.b = bh / sets;
+          it.h = bh % sets << shift;
           it.row0 = qb * kAttnQueries;
           const int prefix = a.prefix != nullptr ? a.prefix[it.b] : 0;
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            const int first = it.row0 + t * kTile, last = min(first + kTile, a.Sq) - 1;
+            const int first = it.row0 + t * kTile, last = (min(first + kTile, rows) - 1) >> shift;
             int lo = 0;
-            int hi = first < a.Sq ? max(0, (last_key(a, last + off, prefix) + kTile) / kTile) : 0;
+            int hi = first < rows ? max(0, (last_key(a, last + off, prefix) + kTile) / kTile) : 0;
             it.same[t][0] = 0;
             it.same[t][1] = INT_MAX;  // no documents: one
             if (a.q_docs != nullptr && hi > 0)
-              doc_tiles(doc_range(a.q_ranges, int64_t(it.b) * qtiles + 2 * qb + t),
+              doc_tiles(doc_range(a.q_ranges, int64_t(it.b) * qtiles + (first >> shift) / kTile),
                         a.k_ranges + int64_t(it.b) * ktiles, lo, hi, it.same[t]);
             it.lo[t] = lo;
             it.hi[t] = hi;
@@ -208,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           const bool none0 = it.hi[0] == it.lo[0], none1 = it.hi[1] == it.lo[1];
           it.begin = none0 ? it.lo[1] : none1 ? it.lo[0] : min(it.lo[0], it.lo[1]);
           it.count = (none0 ? it.hi[1] : none1 ? it.hi[0] : max(it.hi[0], it.hi[1])) - it.begin;
-          if (CUT && parts > 0) {
+          if (SPECIAL && parts > 0) {
             const int lo = it.begin + it.count * from_part / parts;
             const int hi = it.begin + it.count * to_part / parts;
 #pragma unroll
@@ -226,8 +230,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
           mbar_arrive(smem_u32(&tail->item_full[s]));  // releases the item's words
           if (it.count > 0)  // what it begins with, towards L2
             for (int c = 0; c < DH; c += 64) {
-              tma_prefetch_4d(&p.m.q, c, it.row0, it.h, it.b);
-              tma_prefetch_4d(&p.m.q, c, it.row0 + kTile, it.h, it.b);
+              if (!SPECIAL) {
+                tma_prefetch_4d(&p.m.q, c, it.row0, it.h, it.b);
+                tma_prefetch_4d(&p.m.q, c, it.row0 + kTile, it.h, it.b);
+              }
               tma_prefetch_4d(&p.m.k, c, it.begin * kTile, it.h / a.group, it.b);
               tma_prefetch_4d(&p.m.v, c, it.begin * kTile, it.h / a.group, it.b);
             }
@@ -252,7 +258,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (lane == 0) {
           mbar_expect_tx(smem_u32(&tail->q_full), 2 * L::kTileBytes);
           for (int t = 0; t < 2; ++t)  // a second tile past the end reads as zeros
-            load(q_tile + t * L::kTileBytes, &p.m.q, tail->q_full, it.row0 + t * kTile, it.h);
+            if constexpr (SPECIAL)
+              for (int c = 0; c < DH / 64; ++c)
+                tma_load_5d(q_tile + t * L::kTileBytes + c * kTile * 128, &p.m.q,
+                            smem_u32(&tail->q_full), c * 64, (it.row0 + t * kTile) >> shift,
+                            it.h >> shift, it.b);
+            else
+              load(q_tile + t * L::kTileBytes, &p.m.q, tail->q_full, it.row0 + t * kTile, it.h);
         }
         ++used;
         for (int i = 0; i < it.count; ++i, ++x) {
@@ -380,17 +392,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
     bool ok = true;
     Item it;
     for (int item = 0; ok && next_item(tail, item, it, abort_flag, a.dev_status); ++item) {
-      const int b = it.b, h = it.h, first = it.row0 + t * kTile;
-      if (first >= a.Sq) continue;
+      const int b = it.b, first = it.row0 + t * kTile;
+      if (first >= rows) continue;
       const int lo = it.lo[t], hi = it.hi[t], row = first + (threadIdx.x & 127);
+      const int query = row >> shift, h = it.h + (row & ((1 << shift) - 1));
       const int prefix = a.prefix != nullptr ? a.prefix[b] : 0;
       const ScoreConst sc = score_const(a, h);
-      const int pos = row + off;
-      const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
-      const int first_last = last_key(a, first + off, prefix);  // of the tile's first row
+      const int pos = query + off;
+      const int last = row < rows ? last_key(a, pos, prefix) : -1;
+      const int first_last = last_key(a, (first >> shift) + off, prefix);  // of the first row
       const int same0 = it.same[t][0], same1 = it.same[t][1];
       int qd = -1;
-      if (a.q_docs != nullptr && row < a.Sq) qd = a.q_docs[b * a.qds + row];
+      if (a.q_docs != nullptr && row < rows) qd = a.q_docs[b * a.qds + query];
       float m = -INFINITY;  // the maximum that P is relative to, in log2 units
       float2 l2 = make_float2(0.f, 0.f);
       for (int n = lo; n < hi; ++n, ++turn) {
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         tc_fence_after();
       }
       const float l = l2.x + l2.y;
-      const int part = CUT ? part_of(p.t, item) : -1;
+      const int part = SPECIAL ? part_of(p.t, item) : -1;
       if (part >= 0) {  // part of an item: joined with the others later
         const int r = threadIdx.x & 127;
         p.stat[static_cast<int64_t>(part) * kAttnQueries + t * kTile + r] = make_float2(m, l);
@@ -520,7 +533,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
       }
       // straight to global memory: Q's shared memory is already the next item's
       const float inv = l == 0.f ? 0.f : 1.f / l;  // l = 0: nothing was seen (NaN stays NaN)
-      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] + h * a.so[2];
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(a.o) + b * a.so[0] +
+                           (SPECIAL ? h & ~((1 << shift) - 1) : h) * a.so[2];
 #pragma unroll 1
       for (int c = 0; c < DH; c += 32) {
         float o[32];
@@ -532,11 +546,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_fwd(const __grid_constant_
         if (l == 0.f)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0.f;
-        store_rows32(out, a.so[1], row - lane, a.Sq, c, a.D, o, inv);
+        store_rows32(out, a.so[1], row - lane, rows, c, a.D, o, inv, shift, SPECIAL ? a.so[2] : 0);
       }
       tc_fence_before();  // O has been read before the next item's P is announced
-      if (a.lse != nullptr && row < a.Sq)
-        a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + row] =
+      if (a.lse != nullptr && row < rows)
+        a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Sq + query] =
             l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
   }
@@ -559,12 +573,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_fwd_join(const __grid_
   constexpr int kRows = kAttnQueries / 32, kCols = DH / 32;
   const int i = blockIdx.x / (kRows * kCols), col = blockIdx.x / kRows % kCols * 32;
   const int r = blockIdx.x % kRows * 32 + lane;
-  const int heads = a.B * a.Hq, blocks_q = p.items / heads, id = p.items - p.t.tail + i;
+  const int shift = p.t.shift, rows = a.Sq << shift, sets = a.Hq >> shift;
+  const int heads = a.B * sets, blocks_q = p.items / heads, id = p.items - p.t.tail + i;
   const int row0 = (blocks_q - 1 - id / heads) * kAttnQueries, bh = id % heads;
   const int parts = last_worker(p.t, i) - first_worker(p.t, i) + 1;
   griddep_wait();
   griddep_launch_dependents();
-  if (row0 + r - lane >= a.Sq) return;
+  if (row0 + r - lane >= rows) return;
   const float2 *stat = p.stat + static_cast<int64_t>(i) * p.t.segments * kAttnQueries + r;
   const float4 *from = p.part +
                        (static_cast<int64_t>(i) * p.t.segments * (DH / 4) + col / 4 + warp) *
@@ -595,14 +610,16 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_attn_fwd_join(const __grid_
   tile[lane][warp * 4 + 1] = o.y * inv;
   tile[lane][warp * 4 + 2] = o.z * inv;
   tile[lane][warp * 4 + 3] = o.w * inv;
-  if (a.lse != nullptr && col == 0 && warp == 0 && row0 + r < a.Sq)
-    a.lse[static_cast<int64_t>(bh) * a.Sq + row0 + r] =
+  const int b = bh / sets, h0 = bh % sets << shift, mask = (1 << shift) - 1;
+  if (a.lse != nullptr && col == 0 && warp == 0 && row0 + r < rows)
+    a.lse[(static_cast<int64_t>(b) * a.Hq + h0 + (r & mask)) * a.Sq + ((row0 + r) >> shift)] =
         l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
   __syncthreads();
   // eight lanes to a row of 32 elements
   const int y = threadIdx.x / 8, c = threadIdx.x % 8 * 4, row = row0 + r - lane + y;
-  if (row < a.Sq && col + c < a.D) {
-    const int64_t at = bh / a.Hq * a.so[0] + static_cast<int64_t>(row) * a.so[1] + bh % a.Hq * a.so[2];
+  if (row < rows && col + c < a.D) {
+    const int64_t at = b * a.so[0] + static_cast<int64_t>(row >> shift) * a.so[1] +
+                       (h0 + (row & mask)) * a.so[2];
     *reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(a.o) + at + col + c) =
         make_uint2(pack_bf16(tile[y][c], tile[y][c + 1]), pack_bf16(tile[y][c + 2], tile[y][c + 3]));
   }
@@ -696,10 +713,10 @@ __global__ void __launch_bounds__(kOrderThreads) k_attn_order(const AttnArgs a) 
 
 constexpr int kPlanSms = 152;  // of a GB300: the plan is one of sizes alone
 
-template <int DH, bool CAP, bool BIAS, bool CUT>
+template <int DH, bool CAP, bool BIAS, bool SPECIAL>
 cudaError_t launch_as(const Params &p, int blocks, cudaStream_t s) {
   const size_t smem = Layout<DH>::kBytes + sizeof(Tail) + 1024;
-  auto *kernel = k_attn_fwd<DH, CAP, BIAS, CUT>;
+  auto *kernel = k_attn_fwd<DH, CAP, BIAS, SPECIAL>;
   static std::atomic<uint64_t> done{0};
   const cudaError_t e = allow_smem(kernel, smem, done);
   if (e != cudaSuccess) return e;
@@ -707,8 +724,10 @@ cudaError_t launch_as(const Params &p, int blocks, cudaStream_t s) {
 }
 template <int DH, bool CAP, bool BIAS>
 cudaError_t launch(const Params &p, int sms, cudaStream_t s) {
-  if (p.t.tail > 0)
-    return launch_as<DH, CAP, BIAS, true>(p, p.t.rounds == 0 ? p.t.workers : kPlanSms, s);
+  if (p.t.special()) {
+    const int whole = p.items < kPlanSms ? p.items : kPlanSms;
+    return launch_as<DH, CAP, BIAS, true>(p, p.t.rounds == 0 ? p.t.workers : whole, s);
+  }
   return launch_as<DH, CAP, BIAS, false>(p, p.items < sms ? p.items : sms, s);
 }
 
@@ -733,17 +752,25 @@ cudaError_t launch_attn_order(const AttnArgs &a, cudaStream_t s) {
 // 23 and 18, 53 and 45; 1.4: 31 and 23, 29 and 21; 2.1: 66 and 51; 6: 475 and 367.  No share of less than 4 steps, at most some 32 parts of an item.
 // With documents the items' work is not known here: they are cut only where
 // there is less than a round of them, else taken from a counter.
-AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, bool causal,
-                          bool prefix, bool docs) {
+//
+// Before that, where a group's heads fit an item together, as many as do share
+// one: K and V are then read and multiplied once for them.
+AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int group, int64_t Sq, int64_t Sk, int D,
+                          bool causal, bool prefix, bool docs) {
   AttnFwdPlan t;
-  const int64_t heads = B * Hq, blocks_q = (Sq + kAttnQueries - 1) / kAttnQueries;
+  const int64_t queries = Sq;
+  while (t.shift < 7 && group % (2 << t.shift) == 0 && 2 * Sq <= kAttnQueries) {
+    ++t.shift;
+    Sq *= 2;
+  }
+  const int64_t heads = B * (Hq >> t.shift), blocks_q = (Sq + kAttnQueries - 1) / kAttnQueries;
   const int64_t items = heads * blocks_q, rounds = items / kPlanSms;
   const int64_t tail = items - rounds * kPlanSms;
   if (tail == 0 || Sk == 0 || (docs && rounds > 0)) return t;
   int64_t keys = Sk;  // that the longest of the tail sees
   if (causal && !prefix) {
     const int64_t end = (blocks_q - rounds * kPlanSms / heads) * kAttnQueries;
-    keys = (end < Sq ? end : Sq) + Sk - Sq;
+    keys = ((end < Sq ? end : Sq) >> t.shift) + Sk - queries;
   }
   const int64_t steps = keys > 0 ? (keys + kTile - 1) / kTile : 0;
   int64_t workers = tail * steps / 4;
@@ -760,6 +787,9 @@ AttnFwdPlan attn_fwd_plan(int64_t B, int64_t Hq, int64_t Sq, int64_t Sk, int D, 
   t.segments = static_cast<int>((workers + tail - 1) / tail + 1);
   return t;
 }
+static int items_of(const AttnArgs &a, const AttnFwdPlan &t) {
+  return a.B * (a.Hq >> t.shift) * (((a.Sq << t.shift) + kAttnQueries - 1) / kAttnQueries);
+}
 size_t attn_fwd_stat_bytes(const AttnFwdPlan &t) {
   return size_t(t.tail) * t.segments * kAttnQueries * sizeof(float2);
 }
@@ -769,7 +799,7 @@ size_t attn_fwd_part_bytes(const AttnFwdPlan &t, int D) {
 
 cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, const AttnFwdPlan &t, void *stat,
                             void *part, int sms, cudaStream_t s) {
-  const Params p{a, m, a.B * a.Hq * ((a.Sq + kAttnQueries - 1) / kAttnQueries), t,
+  const Params p{a, m, items_of(a, t), t,
                  static_cast<float2 *>(stat), static_cast<float4 *>(part)};
   const bool cap = a.cap > 0.f, bias = a.slopes != nullptr;
   if (a.D <= 64)
@@ -780,7 +810,7 @@ cudaError_t launch_attn_fwd(const AttnArgs &a, const AttnMaps &m, const AttnFwdP
 }
 cudaError_t launch_attn_fwd_join(const AttnArgs &a, const AttnFwdPlan &t, const void *stat,
                                  const void *part, cudaStream_t s) {
-  const Params p{a, {}, a.B * a.Hq * ((a.Sq + kAttnQueries - 1) / kAttnQueries), t,
+  const Params p{a, {}, items_of(a, t), t,
                  static_cast<float2 *>(const_cast<void *>(stat)),
                  static_cast<float4 *>(const_cast<void *>(part))};
   const int cols = a.D <= 64 ? 2 : 4;

@@ -280,6 +280,30 @@ def test_few_items_are_cut_along_the_keys(B, sq, sk, hq, hk, d, causal):
     assert rl.launch_count() == before + 2, "attention and a join"
 
 
+@pytest.mark.parametrize("hq,hk,sq", [(8, 1, 32), (8, 1, 33), (16, 2, 16), (4, 2, 64), (4, 2, 65), (4, 2, 128),
+                                      (12, 1, 20), (12, 2, 100), (5, 1, 7), (64, 1, 3), (128, 1, 1), (24, 3, 31)])
+@pytest.mark.parametrize("sk", [130, 3000])
+def test_heads_of_a_group_side_by_side(hq, hk, sq, sk):
+    """Few queries, alone and cut along the keys; full and ragged tiles."""
+    d = 64 if sk > 1000 else 128
+    q, k, v, do = draw(2, sq, sk, hq, hk, d, hq * sq)
+    check(q, k, v, do, causal=True, slopes=slopes_of(hq), backward=sk < 1000)
+    check(q, k, v, do, causal=True, cap=8.0, prefix=torch.tensor([sk // 2, 0], dtype=torch.int32),
+          backward=False)
+    docs = torch.arange(sk, dtype=torch.int32)[None].repeat(2, 1) // 50
+    docs[1, -sq:] = torch.arange(sq, dtype=torch.int32) % 3 - 1 + sk // 50 - 2
+    check(q, k, v, do, docs=docs, backward=False)
+    # q is a view of a fused q|k|v output, o is given with strides of its own
+    wide = torch.randn(2, sq, hq + 2, d).bfloat16()
+    wide[:, :, 1:-1] = q
+    dev = wide.to(DEV)[:, :, 1:-1]
+    out = torch.full((2, sq, hq + 1, 2 * d), 7.0, dtype=torch.bfloat16, device=DEV)
+    o, lse = rl.attention_forward(dev, k.to(DEV), v.to(DEV), out=out[:, :, :hq, :d])
+    want, lse1 = rl.attention_forward(q.to(DEV), k.to(DEV), v.to(DEV))
+    assert torch.equal(o, want) and torch.equal(lse, lse1)
+    assert bool((out[:, :, hq:] == 7).all()) and bool((out[..., d:] == 7).all())
+
+
 def test_cut_items_with_every_score_and_mask():
     q, k, v, do = draw(2, 200, 4100, 4, 2, 64, 5, gain=2.0)
     check(q, k, v, do, causal=True, cap=5.0, backward=False)
