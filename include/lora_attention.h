@@ -29,10 +29,11 @@
  * constants).
  *
  * Types: bf16 tensors, fp32 lse.  Scores, softmax statistics and all sums in
- * fp32; P and dz are rounded to bf16 as tensor-core operands, and delta comes
- * from o as it was stored (for at most 128 keys from P and dP): dq and dk are
- * off by 0.0025 to 0.0035 of their norm where rounding them alone takes
- * 0.0017, more in a row that looks almost wholly at one key.  Layout: any
+ * fp32; P and dz are rounded to bf16 as tensor-core operands (P not with one
+ * token), and delta comes from o as it was stored (for at most 128 keys from P
+ * and dP): dq and dk are off by 0.0025 to 0.0035 of their norm where rounding
+ * them alone takes 0.0017, more in a row that looks almost wholly at one key.
+ * Layout: any
  * strides in elements for (batch, token, head), a head's dim elements
  * contiguous; q [batch, q_len, q_heads, dim], k and v [batch, k_len, k_heads,
  * dim], o like q, lse [batch, q_heads, q_len] contiguous.  Query head h reads

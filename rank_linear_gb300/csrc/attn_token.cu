@@ -14,16 +14,18 @@
 //     into pairs of keys, is rows 2j and 2j + 1 of its eight.
 //
 // The keys of the next step are asked for before the present one's softmax, its
-// values at the start of the step: with 3 blocks an SM (168 registers, nothing
-// spilled) that keeps HBM busy.  (Measured and not kept: 4 blocks of 128
+// values at the start of the step: with 3 blocks an SM (168 registers, a
+// few words spilled) that keeps HBM busy.  (Measured and not kept: 4 blocks of 128
 // registers 118 us for the ragged batch where 3 take 95; L2 prefetches 1 to 6
 // steps ahead, values a step ahead in registers, all slower.)  131071 positions
-// of one sequence, 8 key heads of 128: 81 us (6.6 TB/s, 0.98 of a copy); 32
-// ragged ones up to 8192 long 94 us (6.3 TB/s).
+// of one sequence, 8 key heads of 128: 84 us (6.4 TB/s, 0.95 of a copy); 32
+// ragged ones up to 8192 long 97 us (6.1 TB/s).
 //
 // P is transposed between the two by movmatrix.  The running maximum is
 // followed only when some score exceeds it by 2^8 (a vote instead of
-// shuffles); sums in fp32, P rounded to bf16.
+// shuffles); sums in fp32.  P is taken as the sum of two bf16 numbers, 16 bits
+// of it, two MMAs: o is then off by its own rounding alone (0.0017 of its norm
+// where P in one bf16 made it 0.0023), for 1.5 % of the time.
 //
 // The cache's length is cut into `splits` chunks; a second kernel joins their
 // partial results in order.
@@ -174,8 +176,14 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
       s[i] = ex2(s[i] - (m[i & 1] == -INFINITY ? 0.f : m[i & 1]));
       l[i & 1] += s[i];
     }
-    const uint32_t p0 = transpose_8x8(pack_bf16(s[0], s[1]));
-    const uint32_t p1 = transpose_8x8(pack_bf16(s[2], s[3]));
+    // P as a sum of two bf16: the tensor core has time for both
+    const uint32_t h0 = pack_bf16(s[0], s[1]), h1 = pack_bf16(s[2], s[3]);
+    const uint32_t p0 = transpose_8x8(h0), p1 = transpose_8x8(h1);
+    auto rest = [](uint32_t h, float x, float y) {
+      return pack_bf16(x - __uint_as_float(h << 16), y - __uint_as_float(h & 0xffff0000u));
+    };
+    const uint32_t r0 = transpose_8x8(rest(h0, s[0], s[1]));
+    const uint32_t r1 = transpose_8x8(rest(h1, s[2], s[3]));
 #pragma unroll
     for (int e = 0; e < NB; ++e) {
       const uint32_t w[4][4] = {{vw[0][e].x, vw[0][e].y, vw[0][e].z, vw[0][e].w},
@@ -189,6 +197,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
                                __byte_perm(w[2][j], w[3][j], 0x5410),
                                __byte_perm(w[2][j], w[3][j], 0x7632)};
         mma_16816(o[4 * e + j], x, p0, p1);
+        mma_16816(o[4 * e + j], x, r0, r1);
       }
     }
   }
