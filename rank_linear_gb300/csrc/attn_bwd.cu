@@ -605,7 +605,8 @@ struct DkvLayout {
 struct DkvTail {
   float sub[2][kTile], neg_delta[2][kTile];  // of a step's queries, copied with dO
   uint64_t k_full, q_full[3], e_full[2];
-  uint64_t s_full, dp_full, p_full, dz_full, done, drain;
+  uint64_t s_full, p_full, dz_full, done, drain;
+  uint64_t dp_full[2];  // by step modulo 2: two may be done before the copying thread looks
   uint32_t tmem;
   int abort_flag, lo, hi;
   int same[2], equal;  // query tiles that share the keys' one document: first, end, count
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     for (int s = 0; s < L::kQSlots; ++s) mbar_init(smem_u32(&tail->q_full[s]), 1);
     for (int s = 0; s < L::kESlots; ++s) mbar_init(smem_u32(&tail->e_full[s]), 1);
     mbar_init(smem_u32(&tail->s_full), 1);
-    mbar_init(smem_u32(&tail->dp_full), 1);
+    for (int s = 0; s < 2; ++s) mbar_init(smem_u32(&tail->dp_full[s]), 1);
     mbar_init(smem_u32(&tail->p_full), kPairThreads);
     mbar_init(smem_u32(&tail->dz_full), kPairThreads);
     mbar_init(smem_u32(&tail->done), 1);
@@ -733,12 +734,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
         if (a.Sk <= kTile) griddep_wait();
         for (int i = 0; i < count; ++i) {
           // dP of step i - 1 is done, hence everything of step i - 2: the slots
-          // of Q's tile i - 2 and dO's
-          // (every phase in turn: a wait for phase 1 would pass before phase 0)
-          if (i == L::kESlots && !mbar_wait(smem_u32(&tail->dp_full), 0, abort_flag, a.dev_status))
-            break;
+          // of Q's tile i - 2 and dO's.  (dP of step i + 1, the next on its
+          // barrier, needs the copy that is asked for after this wait: the phase
+          // waited for is the barrier's open one or the one before.)
           if (i >= L::kESlots &&
-              !mbar_wait(smem_u32(&tail->dp_full), (i - 1) & 1, abort_flag, a.dev_status))
+              !mbar_wait(smem_u32(&tail->dp_full[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort_flag,
+                         a.dev_status))
             break;
           const int s = i % L::kESlots;
           mbar_expect_tx(smem_u32(&tail->e_full[s]), L::kTileBytes + 2 * kTile * 4);
@@ -802,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       };
       auto do_v = [&](int i) {
         mma_over_head<DH>(on, tmem + 128, v_tile, e_at(i));
-        commit(on, smem_u32(&tail->dp_full));
+        commit(on, smem_u32(&tail->dp_full[i & 1]));
       };
       bool ok = wait(tail->k_full, 0) && wait_q(0);
       tc_fence_after();
@@ -899,7 +900,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&tail->p_full));
-      if (!(ok = wait_warp(tail->dp_full, i, abort_flag, a.dev_status))) break;
+      if (!(ok = wait_warp(tail->dp_full[i & 1], i >> 1, abort_flag, a.dev_status))) break;
       tc_fence_after();
       float dp[64];
       tmem_ld32(dp_addr, dp);
