@@ -11,6 +11,8 @@ namespace {
 
 constexpr int64_t kMaxLen = int64_t(1) << 24;
 
+int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
+
 lora_status_t check_shape(const lora_attention_t *p) {
   if (p == nullptr) return fail(LORA_ERR_INVALID_ARG, "shape is NULL");
   if (p->batch < 0 || p->q_len < 0 || p->k_len < 0)
@@ -38,6 +40,12 @@ lora_status_t check_shape(const lora_attention_t *p) {
   if (p->batch > 65535 || p->q_heads > 65535 ||
       p->batch * p->q_heads * (p->q_len + p->k_len + 1) > (int64_t(1) << 33))
     return fail(LORA_ERR_UNSUPPORTED, "too many heads or rows for one launch");
+  // Tiles of all heads are numbered in 32 bits, with room for the blocks' next
+  // numbers past the end; a launch of the one-token form has at most a block
+  // more for every 64 positions of a head, which is less than 2^27 (above).
+  const int64_t longest = p->q_len > p->k_len ? p->q_len : p->k_len;
+  if (p->batch * p->q_heads * (longest > 0 ? tiles_of(longest) : 1) > (int64_t(1) << 30))
+    return fail(LORA_ERR_UNSUPPORTED, "more than 2^30 tiles of 128 tokens over all heads");
   return LORA_OK;
 }
 
@@ -86,8 +94,6 @@ AttnArgs make_args(const lora_attention_t *p, const DevInfo &di) {
   a.dev_status = di.status;
   return a;
 }
-
-int64_t tiles_of(int64_t n) { return (n + 127) / 128; }
 
 // Map of a [batch][token][head][dim] tensor (see AttnMaps).  An empty tensor
 // gets a map over another's first row, which no copy reads.
