@@ -39,7 +39,8 @@
  * dim], o like q, lse [batch, q_heads, q_len] contiguous.  Query head h reads
  * key head h / (q_heads / k_heads).  Requirements: dim % 8 == 0, 8 <= dim <=
  * 128, q_heads % k_heads == 0, 16-byte aligned pointers, strides of multiples
- * of 8 elements, q_len and k_len < 2^24, batch, q_heads < 2^16, at most 2^33
+ * of 8 elements (above 0, but for o in the backward and q, k and v with one
+ * token, which may be broadcast), q_len and k_len < 2^24, batch, q_heads < 2^16, at most 2^33
  * rows (batch * q_heads * (q_len + k_len + 1)) and 2^30 tiles of 128 tokens.
  *
  * Errors, streams, determinism, the status word and the timing hook are those

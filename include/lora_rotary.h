@@ -52,7 +52,7 @@ lora_status_t lora_rotary_turns(const double *radians, int n, uint64_t *turns);
  *   turns         in, device, rot / 2 words.
  *   q_out, k_out  out, device, same dtype.  An output may be its input (same
  *                 address and strides: in place); otherwise it must not
- *                 overlap any input.
+ *                 overlap any input.  Not broadcast (strides other than 0).
  * batch * seq == 0 launches nothing; it has to be less than 2^31
  * (LORA_ERR_UNSUPPORTED).
  */

@@ -228,9 +228,10 @@ def _make_token(q, k_cache, v_cache, lengths, scale, softcap, slopes, out):
 
 
 def _fit(t):
-    """t itself where its strides suit the kernels, else a contiguous copy."""
-    ok = (t.stride(-1) == 1 or t.shape[-1] == 1) and all(s % 8 == 0 for s in t.stride()[:3]) \
-        and t.data_ptr() % 16 == 0
+    """t itself where its strides suit the kernels, else a contiguous copy (of an
+    expanded tensor too)."""
+    ok = (t.stride(-1) == 1 or t.shape[-1] == 1) and t.data_ptr() % 16 == 0 and \
+        all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()))
     return t if ok else t.contiguous()
 
 

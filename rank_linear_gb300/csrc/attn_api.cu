@@ -50,16 +50,23 @@ lora_status_t check_shape(const lora_attention_t *p) {
 }
 
 // A tensor of the op: its pointer, and the strides of the dimensions that have
-// more than one entry (16-byte rows).
+// more than one entry (16-byte rows).  Only what is read with plain loads may
+// be broadcast (stride 0): a tensor map's strides are not below its rows, and
+// an output's entries have a place each.
+enum Use { kLoaded, kMapped, kWritten };
 lora_status_t check_tensor(const char *name, const void *p, const int64_t (&s)[3], int64_t batch,
-                           int64_t len, int64_t heads) {
+                           int64_t len, int64_t heads, Use use) {
   const int64_t n[3] = {batch, len, heads};
   LORA_TRY(check_ptr(p, name, batch * len == 0));
-  for (int i = 0; i < 3; ++i)
+  for (int i = 0; i < 3; ++i) {
     if (n[i] > 1 && (s[i] < 0 || s[i] % 8 != 0))
       return fail(LORA_ERR_UNSUPPORTED,
                   "%s: stride %lld is not a non-negative multiple of 8 elements", name,
                   (long long)s[i]);
+    if (n[i] > 1 && s[i] == 0 && use != kLoaded)
+      return fail(LORA_ERR_UNSUPPORTED, "%s is broadcast (stride 0): a tensor of its own is needed",
+                  name);
+  }
   return LORA_OK;
 }
 
@@ -229,10 +236,10 @@ lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, c
   LORA_TRY(check_shape(shape));
   const bool no_q = shape->batch == 0 || shape->q_len == 0;
   const bool no_k = shape->batch == 0 || shape->k_len == 0;
-  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads));
-  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads, kMapped));
+  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads, kMapped));
+  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads, kMapped));
+  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads, kWritten));
   if (reinterpret_cast<uintptr_t>(lse) % 4 != 0)
     return fail(LORA_ERR_INVALID_ARG, "lse is not 4-byte aligned");
   const Plan w = make_plan(shape, false);
@@ -270,14 +277,14 @@ lora_status_t lora_attention_bwd(const lora_attention_t *shape, const void *d_o,
   LORA_TRY(check_shape(shape));
   const bool no_q = shape->batch == 0 || shape->q_len == 0;
   const bool no_k = shape->batch == 0 || shape->k_len == 0;
-  LORA_TRY(check_tensor("do", d_o, shape->d_o, shape->batch, shape->q_len, shape->q_heads));
-  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads));
-  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
-  LORA_TRY(check_tensor("dq", dq, shape->dq, shape->batch, shape->q_len, shape->q_heads));
-  LORA_TRY(check_tensor("dk", dk, shape->dk, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("dv", dv, shape->dv, shape->batch, shape->k_len, shape->k_heads));
+  LORA_TRY(check_tensor("do", d_o, shape->d_o, shape->batch, shape->q_len, shape->q_heads, kMapped));
+  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads, kMapped));
+  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads, kMapped));
+  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads, kMapped));
+  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads, kLoaded));
+  LORA_TRY(check_tensor("dq", dq, shape->dq, shape->batch, shape->q_len, shape->q_heads, kWritten));
+  LORA_TRY(check_tensor("dk", dk, shape->dk, shape->batch, shape->k_len, shape->k_heads, kWritten));
+  LORA_TRY(check_tensor("dv", dv, shape->dv, shape->batch, shape->k_len, shape->k_heads, kWritten));
   if ((lse == nullptr && !no_q) || reinterpret_cast<uintptr_t>(lse) % 4 != 0)
     return fail(LORA_ERR_INVALID_ARG, "lse is NULL or not 4-byte aligned");
   const Plan w = make_plan(shape, true);
@@ -329,10 +336,10 @@ lora_status_t lora_attention_token(const lora_attention_t *shape, const void *q,
   if (shape->q_len != 1 || shape->causal || shape->q_docs != nullptr || shape->prefix != nullptr)
     return fail(LORA_ERR_INVALID_ARG, "one token: q_len = 1 and no causal, documents or prefix");
   const bool empty = shape->batch == 0;
-  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads));
-  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads));
-  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads));
+  LORA_TRY(check_tensor("q", q, shape->q, shape->batch, shape->q_len, shape->q_heads, kLoaded));
+  LORA_TRY(check_tensor("k", k, shape->k, shape->batch, shape->k_len, shape->k_heads, kLoaded));
+  LORA_TRY(check_tensor("v", v, shape->v, shape->batch, shape->k_len, shape->k_heads, kLoaded));
+  LORA_TRY(check_tensor("o", o, shape->o, shape->batch, shape->q_len, shape->q_heads, kWritten));
   if ((lengths == nullptr && !empty) || reinterpret_cast<uintptr_t>(lengths) % 4 != 0)
     return fail(LORA_ERR_INVALID_ARG, "lengths is NULL or not 4-byte aligned");
   const TokenSpace w = make_token_space(shape);

@@ -324,6 +324,10 @@ lora_status_t lora_rotary(const lora_rotary_t *sh, const void *q, const void *k,
       same = same && is[t][j] == os[t][j];
       wide = wide && is[t][j] % vec == 0 && os[t][j] % vec == 0;
     }
+    const int64_t entries[3] = {sh->batch, sh->seq, heads[t]};
+    for (int j = 0; j < 3; ++j)
+      if (entries[j] > 1 && os[t][j] == 0)
+        return fail(LORA_ERR_INVALID_ARG, "%s_out is broadcast (stride 0)", name);
     if (in[t] == out[t] && !same)
       return fail(LORA_ERR_INVALID_ARG, "%s_out is %s with other strides", name, name);
     copy_tail = copy_tail || (!same && sh->rot < sh->dim);

@@ -5,6 +5,7 @@ import ctypes
 import pytest
 
 import test_block_ops_abi_cpu as abi
+from rank_linear_gb300 import _lib
 from test_block_ops_abi_cpu import FAKE, UNSUP, backward, forward, shape
 
 
@@ -40,3 +41,38 @@ def test_as_many_tiles_as_their_numbers_hold():
     assert abi.L.lora_attention_workspace_bytes(ctypes.byref(s), 1) > 0
     s = shape(batch=32768, q_heads=32768, k_heads=1, q_len=1, k_len=1, dim=8, causal=0)
     assert abi.L.lora_attention_workspace_bytes(ctypes.byref(s), 1) > 0
+
+
+TWO = dict(batch=2, q_len=10, k_len=20, q_heads=4, k_heads=2, dim=64)
+
+
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_broadcast_tensors_of_maps_and_outputs(at):
+    """A tensor map's strides are not 0, and an output's entries have a place each."""
+    for name, heads in (("q", 4), ("k", 2), ("v", 2), ("o", 4), ("d_o", 4), ("dq", 4), ("dk", 2), ("dv", 2)):
+        strides = [20 * heads * 64, heads * 64, 64]
+        strides[at] = 0
+        kw = dict(TWO, **{name: tuple(strides)})
+        if name in ("q", "k", "v", "o"):
+            assert forward(dict(n=1 << 40), **kw) == UNSUP, name
+            assert "broadcast" in abi.L.lora_last_error().decode()
+        if name != "o":
+            assert backward(dict(n=1 << 40), **kw) == UNSUP, name
+            assert "broadcast" in abi.L.lora_last_error().decode()
+    assert token(**dict(TWO, q_len=1, o=(0, 64, 64))) == UNSUP
+
+
+def test_strides_of_single_entries_are_free():
+    """Dimensions of one entry: their strides are never used (the workspace is refused next)."""
+    one = dict(batch=1, q_len=1, k_len=1, q_heads=1, k_heads=1)
+    kw = {n: (0, 0, 0) for n in ("q", "k", "v", "o", "d_o", "dq", "dk", "dv")}
+    assert backward(dict(n=0), **one, **kw) == _lib.LORA_ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_broadcast_rotary_outputs(at):
+    strides = [2560, 256, 64]
+    strides[at] = 0
+    assert abi.rotary(q_out=tuple(strides)) == _lib.LORA_ERR_INVALID_ARG
+    assert abi.rotary(p_q_out=FAKE, q_in=tuple(strides), q_out=tuple(strides)) == _lib.LORA_ERR_INVALID_ARG
+    assert "broadcast" in abi.L.lora_last_error().decode()
