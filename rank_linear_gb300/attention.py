@@ -232,7 +232,8 @@ def _fit(t):
     expanded tensor too)."""
     ok = (t.stride(-1) == 1 or t.shape[-1] == 1) and t.data_ptr() % 16 == 0 and \
         all(n == 1 or (s > 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()))
-    return t if ok else t.contiguous()
+    # (contiguous() would give back a contiguous tensor at an odd address)
+    return t if ok else t.clone(memory_format=torch.contiguous_format)
 
 
 class AttentionFunction(torch.autograd.Function):

@@ -33,11 +33,13 @@ def test_key_gradients_over_every_number_of_steps(d):
 
 def expanded(x, d):
     """x and its views with a broadcast head, a broadcast token, a broadcast batch
-    entry, a strided head; each with the values it stands for."""
+    entry, a strided head, an odd address; each with the values it stands for."""
     b, n, h, _ = x.shape
     wide = torch.randn(b, n, h, 2 * d, generator=torch.Generator().manual_seed(1)).bfloat16().to(DEV)
+    odd = torch.empty(x.numel() + 1, dtype=x.dtype, device=DEV)[1:].view(x.shape)
+    odd.copy_(x)
     return [x[:, :, :1].expand(b, n, h, d), x[:, :1].expand(b, n, h, d), x[:1].expand(b, n, h, d),
-            wide[..., ::2], x[..., :1].expand(b, n, h, d), x.transpose(1, 2).contiguous().transpose(1, 2)]
+            wide[..., ::2], odd, x[..., :1].expand(b, n, h, d), x.transpose(1, 2).contiguous().transpose(1, 2)]
 
 
 @pytest.mark.parametrize("which", range(4))
@@ -52,7 +54,7 @@ def test_views_that_autograd_copies(which):
         leaf = [y.detach().requires_grad_() for y in t[:3]]
         o = rl.attention(*leaf, causal=True)
         o.backward(t[3])
-        plain = [y.contiguous() for y in t]
+        plain = [y.clone(memory_format=torch.contiguous_format) for y in t]
         o1, lse = rl.attention_forward(*plain[:3], causal=True)
         want = rl.attention_backward(plain[3], *plain[:3], o1, lse, causal=True)
         assert torch.equal(o, o1)
