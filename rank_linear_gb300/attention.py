@@ -10,22 +10,24 @@ import ctypes
 import torch
 
 from . import _lib
-from .lora import _ptr, _stream_ptr
-from .rotary import _block, _empty_like, _layout, _on
+from .lora import _ptr
+from .rotary import _block, _empty_like, _layout, _on, _same_device, _stream_on
 
 
-def _strides(t, name):
+def _strides(t, name, device):
     if t.dtype != torch.bfloat16 or not t.is_cuda:
         raise TypeError(f"{name} must be a bfloat16 CUDA tensor")
+    _same_device(t, name, device)
     s = t.stride()
     if s[-1] != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
     return s[:3]
 
 
-def _check_word(t, dtype, name, shape):
+def _check_word(t, dtype, name, shape, device):
     if t.dtype != dtype or not t.is_cuda or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
+    _same_device(t, name, device)
     if t.dim() and t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name}: the last dimension must be contiguous")
 
@@ -42,20 +44,21 @@ def _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix, like_q,
     sh = _lib.AttentionShape(batch=b, q_len=sq, k_len=sk, q_heads=hq, k_heads=hk, dim=d,
                              causal=int(causal), scale=d ** -0.5 if scale is None else scale,
                              softcap=softcap or 0.0)
-    sh.q, sh.k, sh.v = _strides(q, "q"), _strides(k, "k"), _strides(v, "v")
+    on = q.device
+    sh.q, sh.k, sh.v = _strides(q, "q", on), _strides(k, "k", on), _strides(v, "v", on)
     for like, others in ((q, like_q), (k, like_k)):
         for name, t in others.items():
             if t.shape != like.shape:
                 raise ValueError(f"{name} {tuple(t.shape)} is not {tuple(like.shape)}")
-            setattr(sh, name, _strides(t, name))
+            setattr(sh, name, _strides(t, name, on))
     if slopes is not None:
-        _check_word(slopes, torch.float32, "slopes", (hq,))
+        _check_word(slopes, torch.float32, "slopes", (hq,), on)
     if qd is not None:
-        _check_word(qd, torch.int32, "q documents", (b, sq))
-        _check_word(kd, torch.int32, "k documents", (b, sk))
+        _check_word(qd, torch.int32, "q documents", (b, sq), on)
+        _check_word(kd, torch.int32, "k documents", (b, sk), on)
         sh.q_docs_stride, sh.k_docs_stride = qd.stride(0), kd.stride(0)
     if prefix is not None:
-        _check_word(prefix, torch.int32, "prefix", (b,))
+        _check_word(prefix, torch.int32, "prefix", (b,), on)
     return sh
 
 
@@ -94,6 +97,8 @@ def _workspace_bytes(sh, documents, prefix, backward):
 
 def _scratch(nbytes, like, workspace):
     if workspace is not None:
+        if workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the device of q")
         return workspace
     return torch.empty(nbytes, dtype=torch.uint8, device=like.device) if nbytes else None
 
@@ -140,7 +145,7 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
     sh = _filled(block, slopes, qd, kd, prefix)
     st = _lib.lib().lora_attention_fwd(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(v), _ptr(out),
                                        _ptr(lse), _ptr(workspace), _size(workspace),
-                                       _stream_ptr(stream))
+                                       _stream_on(q.device, stream))
     if st:
         _lib.check(st, "lora_attention_fwd")
     return out, lse
@@ -151,7 +156,7 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
                        workspace=None, stream=None):
     """(dq, dk, dv) from the gradient of attention_forward's output."""
     if lse.dtype != torch.float32 or not lse.is_contiguous() or \
-            lse.shape != (q.shape[0], q.shape[2], q.shape[1]):
+            lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or lse.device != q.device:
         raise ValueError("lse must be the forward's: float32 [batch, q_heads, q_len]")
     qd, kd = _doc_pair(documents, q, k)
     own = dq is None and dk is None and dv is None and workspace is None
@@ -187,7 +192,7 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
     sh = _filled(block, slopes, qd, kd, prefix)
     st = _lib.lib().lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
                                        _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                                       scratch, have, _stream_ptr(stream))
+                                       scratch, have, _stream_on(q.device, stream))
     if st:
         _lib.check(st, "lora_attention_bwd")
     return dq, dk, dv
@@ -212,7 +217,7 @@ def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, s
         workspace = _scratch(need, q, workspace)
     st = L.lora_attention_token(ctypes.byref(sh), _ptr(q), _ptr(k_cache), _ptr(v_cache),
                                 _ptr(lengths), _ptr(out), _ptr(workspace), _size(workspace),
-                                _stream_ptr(stream))
+                                _stream_on(q.device, stream))
     if st:
         _lib.check(st, "lora_attention_token")
     return out
@@ -221,7 +226,7 @@ def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, s
 def _make_token(q, k_cache, v_cache, lengths, scale, softcap, slopes, out):
     if out.shape != q.shape:
         raise ValueError(f"out {tuple(out.shape)} is not {tuple(q.shape)}")
-    _check_word(lengths, torch.int32, "lengths", (q.shape[0],))
+    _check_word(lengths, torch.int32, "lengths", (q.shape[0],), q.device)
     sh = _make_shape(q.unsqueeze(1), k_cache, v_cache, scale, False, softcap, slopes, None, None,
                      None, {"o": out.unsqueeze(1)}, {})
     return sh, _lib.lib().lora_attention_token_workspace_bytes(ctypes.byref(sh))

@@ -7,7 +7,8 @@ import math
 import torch
 
 from . import _lib
-from .lora import _dtype_code, _stream_ptr
+from .lora import _dtype_code
+from .rotary import _stream_on
 
 
 class GradClip:
@@ -73,7 +74,7 @@ class GradClip:
         """The global norm (a device scalar); nothing is scaled."""
         norm = self._norm_out(norm, stream)
         st = _lib.lib().lora_clip_norm(self._at, self.bytes, self._largest(norm_type),
-                                       norm.data_ptr(), _stream_ptr(stream))
+                                       norm.data_ptr(), _stream_on(self.device, stream))
         if st:
             _lib.check(st, "lora_clip_norm")
         return norm
@@ -83,7 +84,7 @@ class GradClip:
         norm before it (a device scalar)."""
         norm = self._norm_out(norm, stream)
         st = _lib.lib().lora_clip(self._at, self.bytes, float(max_norm), self._largest(norm_type),
-                                  norm.data_ptr(), _stream_ptr(stream))
+                                  norm.data_ptr(), _stream_on(self.device, stream))
         if st:
             _lib.check(st, "lora_clip")
         return norm

@@ -12,7 +12,7 @@ import math
 import torch
 
 from . import _lib
-from .lora import _dtype_code, _ptr, _stream_ptr
+from .lora import _dtype_code, _ptr
 
 
 class RotaryFrequencies:
@@ -96,10 +96,11 @@ def rotary_frequencies(rot: int, *, base: float = 10000.0, scaling: dict | None 
     return RotaryFrequencies(w, magnitude, device)
 
 
-def _strides(t, name):
+def _strides(t, name, device):
     """(batch, token, head) strides of [batch, seq, heads, dim] or [tokens, heads, dim]."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    _same_device(t, name, device)
     if t.dim() == 4:
         s = t.stride()
     elif t.dim() == 3:
@@ -122,6 +123,22 @@ _here = contextlib.nullcontext()
 def _on(stream):
     """Buffers made for work on another stream come from that stream's pool."""
     return _here if stream is None else torch.cuda.stream(stream)
+
+
+def _same_device(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _stream_on(device, stream):
+    """The handle to launch on: the current stream's where none is given.  The
+    library launches on the current device, which has to be the tensors'."""
+    at = torch.cuda.current_device()
+    if at != device.index:
+        raise ValueError(f"the tensors are on {device}, the current device is cuda:{at}")
+    if stream is None:  # without making an object of it
+        return torch._C._cuda_getCurrentRawStream(at) or None
+    return stream.cuda_stream or None
 
 
 def _layout(t):
@@ -161,10 +178,11 @@ def _make_shape(q, k, positions, freqs, interleaved, inverse, q_out, k_out):
         if x.dtype != first.dtype or out.dtype != first.dtype:
             raise TypeError("q, k and the outputs must share one dtype")
         setattr(sh, name + "_heads", x.shape[-2])
-        setattr(sh, name + "_in", _strides(x, name))
-        setattr(sh, name + "_out", _strides(out, name + "_out"))
+        setattr(sh, name + "_in", _strides(x, name, first.device))
+        setattr(sh, name + "_out", _strides(out, name + "_out", first.device))
     if positions.dtype not in (torch.int32, torch.int64) or not positions.is_cuda:
         raise TypeError("positions must be an int32 or int64 CUDA tensor")
+    _same_device(positions, "positions", first.device)
     sh.position_bits = 64 if positions.dtype == torch.int64 else 32
     if positions.shape == lead:
         sh.position = positions.stride() if len(lead) == 2 else (0, positions.stride(0))
@@ -193,7 +211,7 @@ def _turn(q, k, positions, freqs, interleaved, inverse, q_out, k_out, stream):
                                                 q_out, k_out))
     st = _lib.lib().lora_rotary(ctypes.byref(sh), _ptr(q), _ptr(k), _ptr(positions),
                                 _ptr(freqs.turns), dtype, _ptr(q_out), _ptr(k_out),
-                                _stream_ptr(stream))
+                                _stream_on((k if q is None else q).device, stream))
     if st:
         _lib.check(st, "lora_rotary")
     return q_out, k_out
