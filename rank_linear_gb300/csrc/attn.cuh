@@ -300,46 +300,44 @@ __device__ __forceinline__ int last_key(const AttnArgs &a, int p, int prefix) {
 }
 
 // The score of a raw product z = q . k, in units of log 2, without the mask.
-// CAP: c = cap tanh(z scale / cap), by one of two ways for all of a warp's
-// pairs at hand:
-//  - |z| scale <= cap for all of them: x P(x^2), P the polynomial of degree 5
-//    next to tanh(x) / x on [0, 1] (a reweighted least-squares fit; the error
-//    of tanh is 2.4e-7 at the most), two pairs an instruction;
-//  - else tanh x = 1 - 2 r, r = 1 / (1 + e^2x): two more special functions a
-//    pair, of which an SM does 32 a cycle.
-// The absolute error, which is what the softmax sees, stays near 2^-22 cap.
+// CAP: c = cap tanh x, x = z scale / cap, by one of two ways:
+//  - |x| <= 1: x P(x^2), P the polynomial of degree 5 next to tanh(x) / x on
+//    [0, 1] (a reweighted least-squares fit; the error of tanh is 2.4e-7 at the
+//    most, 3.1e-6 of itself next to 0), two pairs an instruction;
+//  - else |tanh x| = 1 - 2 r, r = 1 / (1 + e^2|x|): two more special functions
+//    a pair, of which an SM does 32 a cycle.  Its absolute error is 2^-22 of the
+//    cap, which would drown scores far below the cap: they stay with the first.
+// The second is formed where some pair of a warp's needs it.  What x is formed
+// from is bounded, so that no cap, however small or large, makes 0 times
+// infinity of a product that is 0 (as rows past the end are) or of its tanh.
 struct ScoreConst {
   float scale2;    // scale * log2 e
-  float tanh_in;   // 2 log2 e * scale / cap
+  float x_by;      // scale / cap
   float cap2;      // cap * log2 e
   float slope2;    // slope * log2 e
   float most;      // cap / scale: the largest |z| for the polynomial
-  float less;      // 1 / cap2^2: dc/dz = scale (1 - c^2 less), |tanh| up to tanh 1
-  float poly[6];   // of z^2, times scale2
+  float top;       // what tanh is multiplied by at once: cap2, or 1
+  float poly[6];   // P times that
 };
-__device__ __forceinline__ ScoreConst score_const(const AttnArgs &a, int head) {
+__device__ __forceinline__ ScoreConst score_const(const AttnArgs &a, int head, bool unit = false) {
+  constexpr float kBig = 3e38f;
   ScoreConst c;
   c.scale2 = a.scale * kLog2e;
   c.slope2 = a.slopes != nullptr ? a.slopes[head] * kLog2e : 0.f;
-  c.tanh_in = c.cap2 = c.most = c.less = 0.f;
+  c.x_by = c.cap2 = c.most = c.top = 0.f;
   if (a.cap > 0.f) {
-    const float x = a.scale / a.cap;
-    c.tanh_in = 2.f * kLog2e * x;
-    c.cap2 = a.cap * kLog2e;
-    c.most = a.cap / a.scale;
-    c.less = 1.f / (c.cap2 * c.cap2);
+    c.x_by = fminf(a.scale / a.cap, kBig / 4.f);  // (its e^2x takes 2 log2 e of it)
+    c.cap2 = fminf(a.cap * kLog2e, kBig / 2.f);   // (1 - 2 r takes 2 of it)
+    c.most = fminf(a.cap / a.scale, kBig);        // infinite products are beyond it
+    c.top = unit ? 1.f : c.cap2;
     const float p[6] = {0.99999685f, -0.33324004f, 0.13253524f, -0.050972835f, 0.016114152f,
                         -0.0028394550f};
-    float by = c.scale2;
 #pragma unroll
-    for (int i = 0; i < 6; ++i) {
-      c.poly[i] = p[i] * by;
-      by *= x * x;  // may underflow to 0 where z^2 is far below what counts
-    }
+    for (int i = 0; i < 6; ++i) c.poly[i] = p[i] * c.top;
   }
   return c;
 }
-// May the polynomial be used for the N products of every lane?
+// Are the N products of every lane the polynomial's?
 template <int N>
 __device__ __forceinline__ bool all_small(const ScoreConst &c, const float *z) {
   float m[2] = {fabsf(z[0]), fabsf(z[1])};
@@ -350,27 +348,34 @@ __device__ __forceinline__ bool all_small(const ScoreConst &c, const float *z) {
   m[0] = max3(m[0], fabsf(z[N - 2]), fabsf(z[N - 1]));
   return __all_sync(~0u, fmaxf(m[0], m[1]) <= c.most);
 }
+// top tanh x of two pairs that are.
 __device__ __forceinline__ float2 cap_small(const ScoreConst &c, float2 z) {
-  const float2 u = mul2(z, z);
+  const float2 x = mul2(z, make_float2(c.x_by, c.x_by)), u = mul2(x, x);
   float2 p = make_float2(c.poly[5], c.poly[5]);
 #pragma unroll
   for (int i = 4; i >= 0; --i) p = fma2(p, u, make_float2(c.poly[i], c.poly[i]));
-  return mul2(z, p);
+  return mul2(x, p);
 }
-// r as above: dc/dz = scale * 4 r (1 - r), good where tanh is next to 1 too.
-__device__ __forceinline__ float cap_any(const ScoreConst &c, float z, float &r) {
-  r = rcp(1.f + ex2(z * c.tanh_in));
-  return fmaf(-2.f * c.cap2, r, c.cap2);
+// r as above: dc/dz = scale * 4 r (1 - r), good where |tanh| is next to 1 too.
+__device__ __forceinline__ float cap_r(const ScoreConst &c, float z) {
+  return rcp(1.f + ex2(fabsf(z) * (2.f * kLog2e * c.x_by)));
+}
+// top tanh x of any pair, whose r is at hand and whose polynomial is `small`.
+__device__ __forceinline__ float cap_any(const ScoreConst &c, float z, float r, float small) {
+  return fabsf(z) <= c.most ? small : copysignf(fmaf(-2.f * c.top, r, c.top), z);
 }
 // Two scores; small: what all_small said of them.
 template <bool CAP, bool BIAS>
 __device__ __forceinline__ float2 scores2(const ScoreConst &c, float2 z, float distance, float step,
                                           bool small) {
-  float2 s, r;
-  if constexpr (CAP)
-    s = small ? cap_small(c, z) : make_float2(cap_any(c, z.x, r.x), cap_any(c, z.y, r.y));
-  else
+  float2 s;
+  if constexpr (CAP) {
+    s = cap_small(c, z);
+    if (!small)
+      s = make_float2(cap_any(c, z.x, cap_r(c, z.x), s.x), cap_any(c, z.y, cap_r(c, z.y), s.y));
+  } else {
     s = mul2(z, make_float2(c.scale2, c.scale2));
+  }
   if constexpr (BIAS) {
     s.x = fmaf(-c.slope2, fabsf(distance), s.x);
     s.y = fmaf(-c.slope2, fabsf(distance + step), s.y);

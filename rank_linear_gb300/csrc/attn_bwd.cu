@@ -74,18 +74,19 @@ __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], flo
         const float2 y = make_float2(add[i], add[i + 1]);
         float2 f = make_float2(1.f, 1.f);
         if constexpr (CAP || BIAS) {
+          float2 t = x;  // tanh: 1 - t^2 is its slope
           if constexpr (CAP) {
+            t = cap_small(c, x);
             if (small) {
-              x = cap_small(c, x);
-              f = fma2(mul2(x, x), make_float2(-c.less, -c.less), f);
+              f = fma2(make_float2(-t.x, -t.y), t, f);
             } else {
-              float2 r;
-              x = make_float2(cap_any(c, x.x, r.x), cap_any(c, x.y, r.y));
+              const float2 r = make_float2(cap_r(c, x.x), cap_r(c, x.y));
+              t = make_float2(cap_any(c, x.x, r.x, t.x), cap_any(c, x.y, r.y, t.y));
               f = make_float2(4.f * r.x * (1.f - r.x), 4.f * r.y * (1.f - r.y));
             }
-          } else {
-            x = mul2(x, make_float2(c.scale2, c.scale2));
           }
+          const float by = CAP ? c.cap2 : c.scale2;
+          x = mul2(t, make_float2(by, by));
           if constexpr (BIAS) {
             const float d = d0 + step * (j + i);
             x.x = fmaf(-c.slope2, fabsf(d), x.x);
@@ -475,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     bool more = take(0);
     for (int item = 0; more; ++item) {
       const int b = it.b, h = it.h, row = it.row0 + r, count = it.count;
-      const ScoreConst sc = score_const(a, h);
+      const ScoreConst sc = score_const(a, h, true);
       const int pos = row + off;
       const int last = row < a.Sq ? last_key(a, pos, prefix) : -1;
       const int first_last = last_key(a, it.row0 + off, prefix);
@@ -862,7 +863,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     }
     for (int i = 0; i < count; ++i) {
       const int q0 = n * kTile + half * 64;
-      const ScoreConst sc = score_const(a, head);
+      const ScoreConst sc = score_const(a, head, true);
       const bool same = n >= same0 && n < same1;
       const bool whole = same && n * kTile >= all_from;
       int qd[2];

@@ -149,8 +149,7 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + quad + 8 * (i >> 1);
       const ScoreConst &c = sc[i & 1];
-      float r;
-      s[i] = CAP ? cap_any(c, s[i], r) : s[i] * c.scale2;
+      s[i] = CAP ? copysignf(fmaf(-2.f * c.top, cap_r(c, s[i]), c.top), s[i]) : s[i] * c.scale2;
       if constexpr (BIAS) s[i] = fmaf(-c.slope2, static_cast<float>(len - 1 - key), s[i]);
       if (key >= to) s[i] = -INFINITY;
     }

@@ -72,3 +72,56 @@ def test_broadcast_tensors_are_refused_or_read():
     one = rl.attention_decode(q[:, 0], k[:1].expand(2, 60, 2, 64), many, n)  # one prompt's cache for both
     two = rl.attention_decode(q[:, 0], k[:1].repeat(2, 1, 1, 1), many.contiguous(), n)
     assert torch.equal(one, two)
+
+
+def whole_numbers(B, sq, sk, hq, hk, d, seed):
+    """q and k of -1, 0 and 1: every score is exact in fp32, many are 0."""
+    q, k, v, do = draw(B, sq, sk, hq, hk, d, seed)
+    g = torch.Generator().manual_seed(seed)
+    w = lambda t: torch.randint(-1, 2, t.shape, generator=g).bfloat16()
+    return w(q), w(k), v, do
+
+
+@pytest.mark.parametrize("cap", [1e-40, 1e-30, 1e-20, 1e-10, 1e-6, 1e-5, 2e-5, 1e-4, 1e-3])
+@pytest.mark.parametrize("d", [64, 128])
+def test_small_caps(cap, d):
+    """Scores of 0, whose slope is 1, beside scores far beyond the cap; rows past the
+    end in the last tile."""
+    check(*whole_numbers(1, 190, 190, 4, 2, d, 3), causal=True, cap=cap)
+    check(*whole_numbers(2, 50, 210, 2, 2, d, 4), cap=cap, scale=1.0)
+    check(*whole_numbers(1, 150, 150, 2, 1, d, 5), causal=True, cap=cap,
+          slopes=torch.tensor([0.25, 0.0625]))
+
+
+@pytest.mark.parametrize("cap", [1.0, 50.0, 1e3, 1e4, 1e5, 1e7, 1e15, 1e25, 1e37])
+@pytest.mark.parametrize("d", [64, 128])
+def test_scores_below_at_and_beyond_any_cap(cap, d):
+    """Each query sees one key, its own document's: lse is the score, from 1/1000 of the
+    cap to 10 times it within one warp.  q and k are positive: a score is off by 2^-17
+    of itself (128 roundings of 2^-24), tanh by less than 2^-18, the unit of lse by 2^-22."""
+    n = 256
+    q, k, v, _ = draw(1, n, n, 2, 1, d, 11)
+    q, k = q.abs(), k.abs()
+    far = torch.logspace(-3, 1, n)[torch.randperm(n, generator=torch.Generator().manual_seed(2))]
+    q = (q * far[None, :, None, None]).bfloat16()
+    scale = float(np.float32(cap / (0.64 * d)))
+    docs = torch.arange(n, dtype=torch.int32)[None]
+    _, lse = rl.attention_forward(q.to(DEV), k.to(DEV), v.to(DEV), softcap=cap, scale=scale,
+                                  documents=docs.to(DEV))
+    z = scale * np.einsum("ihd,id->hi", q[0].double().numpy(), k[0, :, 0].double().numpy())
+    capped = float(np.float32(cap))
+    want = capped * np.tanh(z / capped)
+    got = lse[0].double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= 2.0 ** -16 * want)
+
+
+@pytest.mark.parametrize("cap", [30.0, 1e4, 1e6])
+@pytest.mark.parametrize("d", [64, 128])
+def test_what_padding_holds_leaves_scores_below_a_large_cap_alone(cap, d):
+    docs = torch.zeros(1, 300, dtype=torch.int32)
+    docs[0, ::31] = -1
+    q, k, v, do = draw(1, 300, 300, 2, 1, d, 8)
+    for t in (q, k):
+        t[docs < 0] = 1e15
+    check(q, k, v, do, causal=True, cap=cap, docs=docs)
+    check(q, k, v, do, cap=cap, docs=docs, slopes=torch.tensor([0.25, 0.0625]))
