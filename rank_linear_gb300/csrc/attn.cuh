@@ -310,6 +310,10 @@ __device__ __forceinline__ int last_key(const AttnArgs &a, int p, int prefix) {
 // The second is formed where some pair of a warp's needs it.  What x is formed
 // from is bounded, so that no cap, however small or large, makes 0 times
 // infinity of a product that is 0 (as rows past the end are) or of its tanh.
+__device__ __forceinline__ constexpr float tanh_poly(int i) {  // P's coefficients
+  return i == 0 ? 0.99999685f : i == 1 ? -0.33324004f : i == 2 ? 0.13253524f : i == 3 ? -0.050972835f
+         : i == 4 ? 0.016114152f : -0.0028394550f;
+}
 struct ScoreConst {
   float scale2;    // scale * log2 e
   float x_by;      // scale / cap
@@ -330,10 +334,8 @@ __device__ __forceinline__ ScoreConst score_const(const AttnArgs &a, int head, b
     c.cap2 = fminf(a.cap * kLog2e, kBig / 2.f);   // (1 - 2 r takes 2 of it)
     c.most = fminf(a.cap / a.scale, kBig);        // infinite products are beyond it
     c.top = unit ? 1.f : c.cap2;
-    const float p[6] = {0.99999685f, -0.33324004f, 0.13253524f, -0.050972835f, 0.016114152f,
-                        -0.0028394550f};
 #pragma unroll
-    for (int i = 0; i < 6; ++i) c.poly[i] = p[i] * c.top;
+    for (int i = 0; i < 6; ++i) c.poly[i] = tanh_poly(i) * c.top;
   }
   return c;
 }

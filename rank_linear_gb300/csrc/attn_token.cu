@@ -145,11 +145,21 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
       mma_16816(s, hi, q[c].z, q[c].w);
     }
     if (key0 + kStep < to) load_k(key0 + kStep);
+    const bool small = !CAP || all_small<4>(sc[0], s);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int key = key0 + quad + 8 * (i >> 1);
       const ScoreConst &c = sc[i & 1];
-      s[i] = CAP ? copysignf(fmaf(-2.f * c.top, cap_r(c, s[i]), c.top), s[i]) : s[i] * c.scale2;
+      if constexpr (CAP) {  // the polynomial of one score: its coefficients take no registers
+        const float x = s[i] * c.x_by, u = x * x;
+        float p = tanh_poly(5);
+#pragma unroll
+        for (int j = 4; j >= 0; --j) p = fmaf(p, u, tanh_poly(j));
+        p *= x * c.cap2;
+        s[i] = small ? p : cap_any(c, s[i], cap_r(c, s[i]), p);
+      } else {
+        s[i] *= c.scale2;
+      }
       if constexpr (BIAS) s[i] = fmaf(-c.slope2, static_cast<float>(len - 1 - key), s[i]);
       if (key >= to) s[i] = -INFINITY;
     }

@@ -9,7 +9,8 @@ import pytest
 import torch
 
 import rank_linear_gb300 as rl
-from test_gpu_attention import DEV, check, draw
+from oracle import attention as oa
+from test_gpu_attention import DEV, check, draw, host
 
 pytestmark = pytest.mark.gpu
 
@@ -125,3 +126,31 @@ def test_what_padding_holds_leaves_scores_below_a_large_cap_alone(cap, d):
         t[docs < 0] = 1e15
     check(q, k, v, do, causal=True, cap=cap, docs=docs)
     check(q, k, v, do, cap=cap, docs=docs, slopes=torch.tensor([0.25, 0.0625]))
+
+
+@pytest.mark.parametrize("cap", [1e-30, 1e-5, 1.0, 1e2, 1e3, 1e4, 1e5, 1e6, 1e15, 1e30])
+@pytest.mark.parametrize("n", [2, 5, 700])
+@pytest.mark.parametrize("d", [64, 128])
+def test_token_with_any_cap(n, cap, d):
+    """One new token's output: rounded once (U), from weights good to F in scores and
+    2^-16 in their two bf16 parts; pv is what the weights' error goes through."""
+    B, hq, hk = 2, 8, 2
+    q, k, v, _ = (whole_numbers if cap < 1e-3 else draw)(B, 1, n, hq, hk, d, n + d)
+    length = torch.full((B,), n, dtype=torch.int32)
+    o = rl.attention_decode(q[:, 0].to(DEV), k.to(DEV), v.to(DEV), length.to(DEV), softcap=cap)
+    ref = oa.run(host(q), host(k), host(v), scale=d ** -0.5, cap=cap)
+    pv = ref["bound"]["o"][:, 0] / (2 * oa.U + oa.F)
+    err = np.abs(o.double().cpu().numpy() - ref["o"][:, 0])
+    assert np.all(err <= (oa.U + 2 * oa.F) * pv + 1e-30), (err / (pv + 1e-30)).max()
+
+
+def test_token_beyond_the_cap_and_below_it():
+    """Heads far beyond a large cap beside heads far below it in one warp."""
+    q, k, v, _ = draw(1, 1, 40, 8, 1, 64, 5)
+    q[:, :, 1::2] *= 1e7
+    o = rl.attention_decode(q[:, 0].to(DEV), k.to(DEV), v.to(DEV),
+                            torch.tensor([40], dtype=torch.int32, device=DEV), softcap=1e5)
+    ref = oa.run(host(q), host(k), host(v), scale=0.125, cap=1e5)
+    pv = ref["bound"]["o"][:, 0] / (2 * oa.U + oa.F)
+    err = np.abs(o.double().cpu().numpy() - ref["o"][:, 0])[:, ::2]
+    assert np.all(err <= (oa.U + 2 * oa.F) * pv[:, ::2])
