@@ -30,9 +30,11 @@
  *
  * Types: bf16 tensors, fp32 lse.  Scores, softmax statistics and all sums in
  * fp32; P and dz are rounded to bf16 as tensor-core operands (P not with one
- * token), and delta comes from o as it was stored (for at most 128 keys from P
- * and dP): dq and dk are off by 0.0025 to 0.0035 of their norm where rounding
- * them alone takes 0.0017, more in a row that looks almost wholly at one key.
+ * token), and delta comes from o as it was stored, but from P and dP for queries
+ * whose keys lie in one 128-aligned tile of keys (the first of a causal mask,
+ * short documents, at most 128 keys): dq and dk are off by 0.0025 to 0.0035 of
+ * their norm where rounding them alone takes 0.0017, more in a row of keys in
+ * several tiles that looks almost wholly at one of them.
  * Layout: any
  * strides in elements for (batch, token, head), a head's dim elements
  * contiguous; q [batch, q_len, q_heads, dim], k and v [batch, k_len, k_heads,
@@ -40,8 +42,9 @@
  * key head h / (q_heads / k_heads).  Requirements: dim % 8 == 0, 8 <= dim <=
  * 128, q_heads % k_heads == 0, 16-byte aligned pointers, strides of multiples
  * of 8 elements (above 0, but for o in the backward and q, k and v with one
- * token, which may be broadcast), q_len and k_len < 2^24, batch, q_heads < 2^16, at most 2^33
- * rows (batch * q_heads * (q_len + k_len + 1)) and 2^30 tiles of 128 tokens.
+ * token, which may be broadcast), q_len and k_len < 2^24, batch and q_heads <
+ * 2^16, at most 2^33 rows (batch * q_heads * (q_len + k_len + 1)) and 2^30 tiles
+ * of 128 tokens over all heads.
  *
  * Errors, streams, determinism, the status word and the timing hook are those
  * of lora_linear.h.  Nothing is allocated; no host synchronisation.

@@ -14,10 +14,15 @@
 // kernels.  (Formed in the dq kernel they cost an item 3600 to 10000 cycles,
 // or 22000 of the first one in warps of their own.)  o there has been rounded
 // to bf16, which is most of the error of a gradient that nearly cancels: with
-// few keys, a query that looks almost wholly at one of them.  Where all keys
-// lie in one tile, the dq kernel therefore forms delta = sum_j P dP itself and
-// leaves it for dk and dv (of two tokens dq was off by up to 0.2 of its norm).
-// That is not done for more keys: it would take the scores twice.
+// few keys, a query that looks almost wholly at one of them (of two keys dq is
+// off by 0.006 of its norm in the median, by 0.2 in a row of ten).  Rows whose
+// keys lie in one tile therefore have delta = sum_j P dP formed in the dq
+// kernel, whose tile has both, and left for dk and dv: the first rows of a
+// causal mask, short documents, and whatever looks at 128 keys or fewer.  It is
+// a pass of its own over such tiles, which are few, so that the registers and
+// the code of the others stay as they are (in one pass, heads of 64 causal at
+// 8192: dq 430 us; in two, 415; without, 400).  Rows that see more keep delta
+// from o: for them it would take the scores of all their tiles twice.
 //
 // The dq blocks stay and take item after item, as the forward's do.  A dk/dv
 // item has a group's heads times as much work; where there are too few for the
@@ -53,15 +58,15 @@ struct Params {
 // over scores that it alone reads.
 __device__ __forceinline__ constexpr uint32_t operand_cols(int kk) { return (kk >> 2) * 64 + (kk & 3) * 8; }
 
-// P (to p) and P dc/dz / scale (in s) of 64 raw products of one thread;
+// P (to p) and P dc/dz / scale (in s) of N raw products of one thread;
 // distances d0 + step * j; sub = -lse in log2 units (or one per column in
 // sub_col).
-template <bool CAP, bool BIAS, bool PER_COLUMN>
-__device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], float *p, float sub,
+template <bool CAP, bool BIAS, bool PER_COLUMN, int N>
+__device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[N], float *p, float sub,
                                         const float *sub_col, float d0, float step) {
   auto all = [&](bool small) {
 #pragma unroll
-    for (int j = 0; j < 64; j += 4) {
+    for (int j = 0; j < N; j += 4) {
       float4 sc;
       if constexpr (PER_COLUMN)
         sc = *reinterpret_cast<const float4 *>(sub_col + j);
@@ -108,7 +113,7 @@ __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[64], flo
       }
     }
   };
-  if (!CAP || all_small<64>(c, s))
+  if (!CAP || all_small<N>(c, s))
     all(true);
   else
     all(false);
@@ -202,8 +207,8 @@ struct DqTail {
   uint64_t s_full[2], dp_full[2], dp_free, done, drain;
   uint64_t dz_full[2];  // by tile modulo 2: tile x + 1's may come before x's is waited for
   uint64_t item_full[kItemSlots], item_free[kItemSlots];
-  uint64_t part_full;
-  float part[2][2][kTile];  // sums of P dP, of item modulo 2 and half: ONE_TILE
+  uint64_t own;            // a half row's sums are there, then: they have been read
+  float2 part[2][kTile];   // sums of P and of P dP in a tile, of each half
   DqItem item[kItemSlots];
   uint32_t tmem;
   int abort_flag;
@@ -219,7 +224,7 @@ __device__ __forceinline__ bool next_item(DqTail *tail, int n, DqItem &item,
   return item.count >= 0;
 }
 
-template <int DH, bool CAP, bool BIAS, bool ONE_TILE>
+template <int DH, bool CAP, bool BIAS>
 __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__ Params p) {
   using L = DqLayout<DH>;
   extern __shared__ __align__(1024) uint8_t raw[];
@@ -251,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       mbar_init(smem_u32(&tail->dz_full[s]), kPairThreads);
     }
     mbar_init(smem_u32(&tail->dp_free), kPairThreads);
-    mbar_init(smem_u32(&tail->part_full), kPairThreads);
+    mbar_init(smem_u32(&tail->own), kPairThreads);
     for (int s = 0; s < kItemSlots; ++s) {
       mbar_init(smem_u32(&tail->item_full[s]), 1);
       mbar_init(smem_u32(&tail->item_free[s]), kItemReaders);
@@ -457,6 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
     const int half = warp / 4, r = threadIdx.x & 127;
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     int x = 0, used = 0;  // tiles, and items with tiles, before this one
+    int owned = 0;        // tiles whose sums were shared before this one
     bool ok = true;
     // an item, and what is read for its row: asked for before the item ahead
     // of it is written out
@@ -467,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
       if (!next_item(tail, n, it, abort_flag, a.dev_status)) return false;
       const int64_t at = (static_cast<int64_t>(it.b) * a.Hq + it.h) * (qtiles * kTile) + it.row0 + r;
       sub = __ldcg(a.sub + at);
-      if constexpr (!ONE_TILE) neg_delta = __ldcg(a.neg_delta + at);
+      neg_delta = __ldcg(a.neg_delta + at);
       if (a.prefix != nullptr) prefix = a.prefix[it.b];
       if (a.q_docs != nullptr)
         qd = it.row0 + r < a.Sq ? a.q_docs[it.b * a.qds + it.row0 + r] : -1;
@@ -488,15 +494,62 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         int kd[2];
         if (!same) load_docs(a.k_docs + b * a.kds + key0, a.Sk - key0, kd);
         const uint32_t s_addr = tmem + lanes + (x & 1) * kTile + half * 64;
+        const uint32_t dp_addr = tmem + lanes + 256 + half * 64;
         if (!(ok = wait_warp(tail->s_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
+        // May some row see this tile's keys only?  (Of a causal mask each row
+        // sees itself: in a tile that reaches the first row's place.)
+        const bool close = a.q_docs == nullptr ? n == 0 && first_last < kTile
+                           : a.causal && a.prefix == nullptr
+                               ? count == 1 || n * kTile + kTile > first_last
+                               : count == 1 || !whole;
+        if (close) {  // a pass of its own, so that the other tiles' registers stay as they are
+          if (!(ok = wait_warp(tail->dp_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
+          tc_fence_after();
+          uint32_t keep[2] = {~0u, ~0u};
+          if (!same) same_doc(qd, kd, keep);
+          float2 all = make_float2(0.f, 0.f), sum = all;  // of P, of P dP
+#pragma unroll 1
+          for (int c = 0; c < 64; c += 32) {
+            float w[32], pr[32], dp[32];
+            tmem_ld32(s_addr + c, w);
+            tmem_ld32(dp_addr + c, dp);
+            tmem_wait_ld();
+            pin<32>(w);
+            pin<32>(dp);
+            weights<CAP, BIAS, false>(sc, w, pr, sub, nullptr, static_cast<float>(pos - key0 - c),
+                                      -1.f);
+            const uint32_t see = (c == 0 ? keep[0] : keep[1]) & bits_to(last - key0 - c);
+#pragma unroll
+            for (int j = 0; j < 32; j += 2) {  // (a masked pair's dP may be anything)
+              const bool one = see >> j & 1u, two = see >> j & 2u;
+              const float2 y = make_float2(one ? pr[j] : 0.f, two ? pr[j + 1] : 0.f);
+              all = add2(all, y);
+              sum = fma2(y, make_float2(one ? dp[j] : 0.f, two ? dp[j + 1] : 0.f), sum);
+            }
+          }
+          if (owned > 0 && !(ok = wait_warp(tail->own, 2 * owned - 1, abort_flag, a.dev_status)))
+            break;
+          tail->part[half][r] = make_float2(all.x + all.y, sum.x + sum.y);
+          mbar_arrive(smem_u32(&tail->own));
+          if (!(ok = wait_warp(tail->own, 2 * owned, abort_flag, a.dev_status))) break;
+          const float2 one = tail->part[0][r], two = tail->part[1][r];
+          mbar_arrive(smem_u32(&tail->own));
+          ++owned;
+          // by the mask; with documents by the weight (what is left of it is
+          // less than 2^-12, and moves delta by that of what dP differs)
+          if (a.q_docs != nullptr ? one.x + two.x >= 1.f - 0x1p-12f : last < kTile) {
+            neg_delta = -(one.y + two.y);
+            if (half == 0)
+              a.neg_delta[(static_cast<int64_t>(b) * a.Hq + h) * (qtiles * kTile) + row] = neg_delta;
+          }
+        }
         tc_fence_after();
-        constexpr bool kKeepP = ONE_TILE && CAP;  // without a cap w is P
-        float w[64], pr[kKeepP ? 64 : 1];
+        float w[64];
         tmem_ld32(s_addr, w);
         tmem_ld32(s_addr + 32, w + 32);
         tmem_wait_ld();
         pin<64>(w);
-        weights<CAP, BIAS, false>(sc, w, kKeepP ? pr : nullptr, sub, nullptr,
+        weights<CAP, BIAS, false>(sc, w, nullptr, sub, nullptr,
                                   static_cast<float>(pos - key0), -1.f);
         if (!whole) {
           uint32_t keep[2] = {~0u, ~0u};
@@ -506,36 +559,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
             keep[c] &= bits_to(last - key0 - 32 * c);
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-              if (!(keep[c] >> j & 1u)) {
-                w[c * 32 + j] = 0.f;
-                if constexpr (kKeepP) pr[c * 32 + j] = 0.f;
-              }
+              if (!(keep[c] >> j & 1u)) w[c * 32 + j] = 0.f;
           }
         }
         if (!(ok = wait_warp(tail->dp_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
         tc_fence_after();
         float dp[64];
-        tmem_ld32(tmem + lanes + 256 + half * 64, dp);
-        tmem_ld32(tmem + lanes + 256 + half * 64 + 32, dp + 32);
+        tmem_ld32(dp_addr, dp);
+        tmem_ld32(dp_addr + 32, dp + 32);
         tmem_wait_ld();
         pin<64>(dp);
         tc_fence_before();
         mbar_arrive(smem_u32(&tail->dp_free));
-        if constexpr (ONE_TILE) {  // count is 1: an item, a tile
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-          for (int j = 0; j < 64; ++j) {
-            const float y = kKeepP ? pr[kKeepP ? j : 0] : w[j];
-            sum[j & 3] = y == 0.f ? sum[j & 3] : fmaf(y, dp[j], sum[j & 3]);
-          }
-          float *part = tail->part[used & 1][0];
-          part[half * kTile + r] = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-          mbar_arrive(smem_u32(&tail->part_full));
-          if (!(ok = wait_warp(tail->part_full, used, abort_flag, a.dev_status))) break;
-          neg_delta = -(part[r] + part[kTile + r]);
-          if (half == 0)
-            a.neg_delta[(static_cast<int64_t>(b) * a.Hq + h) * (qtiles * kTile) + row] = neg_delta;
-        }
         const float2 nd = make_float2(neg_delta, neg_delta);
 #pragma unroll
         for (int j = 0; j < 64; j += 2) {
@@ -642,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   // it start only when what came before dq has finished: no wait, so that
   // blocks begin on the SMs that dq leaves first.  They wait before they
   // leave instead: this kernel ends after dq.  (Without queries there is no dq;
-  // where dq forms delta, the copying thread waits before it reads that.)
+  // where dq forms delta of some row, the copying thread waits before it reads that.)
   if (a.Sq == 0) griddep_wait();
   griddep_launch_dependents();
   const int entry = a.order != nullptr ? __ldcg(a.order + item / a.Hk) : item / a.Hk;
@@ -703,8 +738,19 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   __syncthreads();
   const int end = uniform(tail->hi), begin = uniform(min(tail->lo, end));
   const int per_head = end - begin, all = per_head * a.group;
-  // step i of the item: query head g * group + i / per_head, tile begin + i %
-  // per_head; this rank's are `count` from step0 on
+  // Queries that see the keys of one tile only have delta from dq: with
+  // documents any may, else those that see the first key tile alone.  Where
+  // these all lie in the first of a head's query tiles, its step comes last.
+  const bool from_dq =
+      a.q_docs != nullptr || (kt == 0 && (a.causal ? off < kTile : a.Sk <= kTile));
+  const int turn =
+      from_dq && a.q_docs == nullptr && a.causal && off >= 0 && per_head > 1 ? 1 : 0;
+  auto tile_at = [&](int place) {
+    place += turn;
+    return begin + (place < per_head ? place : place - per_head);
+  };
+  // step i of the item: query head g * group + i / per_head, tile tile_at(i %
+  // per_head); this rank's are `count` from step0 on
   const int step0 = static_cast<int>(int64_t(all) * rank / ranks);
   const int count = static_cast<int>(int64_t(all) * (rank + 1) / ranks) - step0;
 
@@ -727,12 +773,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
           const int s = i % L::kQSlots;
           mbar_expect_tx(smem_u32(&tail->q_full[s]), L::kTileBytes);
           load(q_ring + s * L::kTileBytes, &p.m.q, tail->q_full[s],
-               (begin + (step0 + i) % per_head) * kTile,
+               tile_at((step0 + i) % per_head) * kTile,
                g * a.group + (step0 + i) / per_head);
           ++nq;
         };
         load_q(0);
-        if (a.Sk <= kTile) griddep_wait();
         for (int i = 0; i < count; ++i) {
           // dP of step i - 1 is done, hence everything of step i - 2: the slots
           // of Q's tile i - 2 and dO's.  (dP of step i + 1, the next on its
@@ -742,16 +787,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
               !mbar_wait(smem_u32(&tail->dp_full[(i - 1) & 1]), ((i - 1) >> 1) & 1, abort_flag,
                          a.dev_status))
             break;
-          const int s = i % L::kESlots;
+          const int s = i % L::kESlots, tile = tile_at((step0 + i) % per_head);
+          if (from_dq && (turn == 0 || tile == begin)) griddep_wait();
           mbar_expect_tx(smem_u32(&tail->e_full[s]), L::kTileBytes + 2 * kTile * 4);
           const int64_t stat =
               ((static_cast<int64_t>(b) * a.Hq + g * a.group + (step0 + i) / per_head) * qtiles +
-               begin + (step0 + i) % per_head) * kTile;
+               tile) * kTile;
           bulk_load(smem_u32(tail->sub[s]), a.sub + stat, kTile * 4, smem_u32(&tail->e_full[s]));
           bulk_load(smem_u32(tail->neg_delta[s]), a.neg_delta + stat, kTile * 4,
                     smem_u32(&tail->e_full[s]));
-          load(e_ring + s * L::kTileBytes, &p.m.d_o, tail->e_full[s],
-               (begin + (step0 + i) % per_head) * kTile,
+          load(e_ring + s * L::kTileBytes, &p.m.d_o, tail->e_full[s], tile * kTile,
                g * a.group + (step0 + i) / per_head);
           ++ne;
           if (i + 1 < count) load_q(i + 1);
@@ -771,13 +816,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       };
       auto padded = [&](int i) {
         return a.q_docs != nullptr && i < count
-                   ? doc_range(a.q_ranges, int64_t(b) * qtiles + begin + (step0 + i) % per_head).padded
+                   ? doc_range(a.q_ranges, int64_t(b) * qtiles + tile_at((step0 + i) % per_head)).padded
                    : 0;
       };
       int pads_q = padded(0), pads_e = pads_q;
       // a tile of step i has landed; without the rows of padding
       auto clear = [&](int now, int tile, int i) {
-        const int token = (begin + (step0 + i) % per_head) * kTile;
+        const int token = tile_at((step0 + i) % per_head) * kTile;
         if (now != 0)
           zero_padding_rows<DH>(smem + tile * L::kTileBytes, a.q_docs + b * a.qds + token,
                                 a.Sq - token);
@@ -856,13 +901,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
     // query tiles of the keys' one document, where they lie in one run
     const int same0 = tail->same[0];
     const int same1 = tail->equal == tail->same[1] - same0 ? tail->same[1] : same0;
-    int head = g * a.group, n = begin;  // of this step
+    int head = g * a.group, place = 0;  // of this step
     if (count > 0) {
       head += step0 / per_head;
-      n += step0 % per_head;
+      place = step0 % per_head;
     }
     for (int i = 0; i < count; ++i) {
-      const int q0 = n * kTile + half * 64;
+      const int n = tile_at(place), q0 = n * kTile + half * 64;
       const ScoreConst sc = score_const(a, head, true);
       const bool same = n >= same0 && n < same1;
       const bool whole = same && n * kTile >= all_from;
@@ -934,8 +979,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
       tmem_wait_st();
       tc_fence_before();
       mbar_arrive(smem_u32(&tail->dz_full));
-      if (++n == end) {
-        n = begin;
+      if (++place == per_head) {
+        place = 0;
         ++head;
       }
     }
@@ -1012,19 +1057,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dkv(const __grid_constant_
   griddep_wait();
 }
 
-template <int DH, bool CAP, bool BIAS, bool ONE_TILE>
-cudaError_t start_dq_of(const Params &p, int sms, cudaStream_t s) {
-  constexpr size_t smem = DqLayout<DH>::kAsked;
-  static std::atomic<uint64_t> done{0};
-  const cudaError_t e = allow_smem(k_attn_dq<DH, CAP, BIAS, ONE_TILE>, smem, done);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(k_attn_dq<DH, CAP, BIAS, ONE_TILE>, dim3(p.items < sms ? p.items : sms),
-                    dim3(kThreads), smem, s, p);
-}
 template <int DH, bool CAP, bool BIAS>
 cudaError_t start_dq(const Params &p, int sms, cudaStream_t s) {
-  return p.a.Sk <= kTile ? start_dq_of<DH, CAP, BIAS, true>(p, sms, s)
-                         : start_dq_of<DH, CAP, BIAS, false>(p, sms, s);
+  constexpr size_t smem = DqLayout<DH>::kAsked;
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(k_attn_dq<DH, CAP, BIAS>, smem, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_attn_dq<DH, CAP, BIAS>, dim3(p.items < sms ? p.items : sms), dim3(kThreads),
+                    smem, s, p);
 }
 template <int DH, bool CAP, bool BIAS>
 cudaError_t start_dkv(const Params &p, int, cudaStream_t s) {

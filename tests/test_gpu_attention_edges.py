@@ -154,3 +154,108 @@ def test_token_beyond_the_cap_and_below_it():
     pv = ref["bound"]["o"][:, 0] / (2 * oa.U + oa.F)
     err = np.abs(o.double().cpu().numpy() - ref["o"][:, 0])[:, ::2]
     assert np.all(err <= (oa.U + 2 * oa.F) * pv[:, ::2])
+
+
+def check_rows_of_one_tile(q, k, v, do, *, causal=False, cap=0.0, slopes=None, prefix=None, docs=None):
+    """dq and dk with the bound of test_gpu_attention.few_keys for every query whose
+    keys lie in one tile of 128, however many keys there are, and the reference's
+    general bound for the others; how many such queries there were."""
+    dev = lambda t: None if t is None else t.to(DEV)
+    opts = dict(causal=causal, softcap=cap, slopes=dev(slopes), documents=dev(docs), prefix=dev(prefix))
+    g = [dev(t) for t in (q, k, v, do)]
+    o, lse = rl.attention_forward(*g[:3], **opts)
+    got = dict(zip(("dq", "dk", "dv"), rl.attention_backward(g[3], *g[:3], o, lse, **opts)))
+    torch.cuda.synchronize()
+    rl.device_status()
+    (B, sq, hq, d), (sk, hk) = q.shape, k.shape[1:3]
+    scale, (q, k, v, do) = d ** -0.5, map(host, (q, k, v, do))
+    G, M = 2.0 ** -12, 2.0 ** -16
+    rows = 0
+    for b in range(B):
+        kd = None if docs is None else docs[b].numpy()
+        see = oa.visible(sq, sk, causal, 0 if prefix is None else int(prefix[b]),
+                         None if kd is None else kd[sk - sq:], kd)
+        tiles = sum(see[:, t:t + 128].any(1).astype(int) for t in range(0, sk, 128))
+        one = (tiles <= 1)[:, None]
+        rows += int((tiles == 1).sum())
+        for n in range(hk):
+            dk, dkb = 0.0, 1e-30
+            for h in range(n * (hq // hk), (n + 1) * (hq // hk)):
+                p, sl, oo, _, qkv = oa.head(q[b, :, h], k[b, :, n], v[b, :, n], scale=scale, see=see, cap=cap,
+                                            slope=0.0 if slopes is None else float(slopes[h]))
+                grad = oa.head_backward(do[b, :, h], p, sl, oo, qkv, scale=scale, see=see)
+                e, vv = np.abs(grad[4]), np.abs(qkv[2])
+                dp, size, pv = np.abs(grad[4] @ qkv[2].T), e @ vv.T, p @ vv
+                few = p * sl * (G * (dp + (p * dp).sum(1, keepdims=True))
+                                + M * (size + (p * size).sum(1, keepdims=True)))
+                many = p * sl * ((e * (2 * oa.U + oa.F) * pv).sum(1, keepdims=True)
+                                 + oa.F * (size + (e * pv).sum(1, keepdims=True)))
+                dz = np.where(one, 2 * oa.U * np.abs(grad[3]) + few,
+                              (2 * oa.U + 2 * oa.F) * np.abs(grad[3]) + many)
+                err = np.abs(got["dq"][b, :, h].double().cpu().numpy() - grad[0])
+                bound = scale * dz @ np.abs(qkv[1]) + 1e-30
+                assert np.all(err <= bound), ("dq", b, h, np.argwhere(err > bound)[:4].tolist(), (err / bound).max())
+                dk, dkb = dk + grad[1], dkb + scale * dz.T @ np.abs(qkv[0])
+            err = np.abs(got["dk"][b, :, n].double().cpu().numpy() - dk)
+            assert np.all(err <= dkb), ("dk", b, n, (err / dkb).max())
+    return rows
+
+
+def uneven(B, sq, sk, hq, hk, d, seed):
+    """Some keys draw most of their queries' weight, or none."""
+    q, k, v, do = draw(B, sq, sk, hq, hk, d, seed)
+    k[:, ::3] *= 3
+    return q, k, v, do
+
+
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (30.0, False), (0.0, True), (30.0, True)])
+@pytest.mark.parametrize("sq,sk,d", [(129, 129, 128), (300, 300, 64), (520, 520, 128), (200, 260, 128),
+                                     (260, 200, 64), (500, 129, 128)])
+def test_first_rows_of_long_sequences(sq, sk, d, cap, bias):
+    """The first queries of a causal mask see few keys, of however many there are."""
+    slopes = torch.tensor([0.5, 0.25, 0.125, 0.0625]) if bias else None
+    assert check_rows_of_one_tile(*uneven(2, sq, sk, 4, 2, d, sq + sk), causal=True, cap=cap, slopes=slopes) > 0
+
+
+def test_first_rows_with_a_prefix():
+    x = uneven(2, 400, 400, 4, 2, 64, 6)
+    assert check_rows_of_one_tile(*x, causal=True, prefix=torch.tensor([3, 100], dtype=torch.int32)) > 0
+    x = uneven(2, 400, 250, 4, 2, 64, 7)
+    assert check_rows_of_one_tile(*x, causal=True, prefix=torch.tensor([5, 200], dtype=torch.int32)) > 0
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("cap", [0.0, 30.0])
+@pytest.mark.parametrize("d", [64, 128])
+def test_short_documents_among_many_keys(d, cap, causal):
+    """Documents of 1 to 8 tokens, and longer ones between them; a document that a
+    tile's edge cuts shares its tiles with whole ones."""
+    g = torch.Generator().manual_seed(d)
+    sizes = torch.randint(1, 9, (200,), generator=g).tolist()
+    sizes[20], sizes[50], sizes[51] = 130, 100, 37
+    row = sum(([i] * n for i, n in enumerate(sizes)), [])[:680]
+    docs = torch.tensor([row + [-1] * 20, [-1] * 5 + row + [-1] * 15], dtype=torch.int32)
+    rows = check_rows_of_one_tile(*uneven(2, 700, 700, 4, 2, d, 9), causal=causal, cap=cap, docs=docs)
+    # of each row's 680 tokens the longer documents have 267, tiles' edges cut 5 others at most
+    assert rows >= 2 * (680 - 267 - 5 * 8)
+    # the last queries only
+    q, k, v, do = uneven(2, 150, 700, 4, 2, d, 10)
+    assert check_rows_of_one_tile(q, k, v, do, causal=causal, cap=cap, docs=docs) > 100
+
+
+@pytest.mark.parametrize("sq,sk,kw", [
+    (1500, 1500, {}), (1500, 1437, {}), (1437, 1500, {}), (1500, 1244, {}), (1500, 100, {}), (100, 1500, {}),
+    (1500, 1437, dict(prefix=torch.tensor([90], dtype=torch.int32))),
+    (1500, 1500, dict(prefix=torch.tensor([90], dtype=torch.int32))),
+    (1500, 1500, dict(documents=(torch.arange(1500, dtype=torch.int32) // 7)[None]))])
+def test_gradients_of_few_keys_repeat_bit_for_bit(sq, sk, kw):
+    """dk and dv take delta that dq leaves: always the same one."""
+    kw = {n: t.to(DEV) for n, t in kw.items()}
+    g = [t.to(DEV) for t in uneven(1, sq, sk, 32, 2, 128, 3)]
+    o, lse = rl.attention_forward(*g[:3], causal=True, **kw)
+    first = rl.attention_backward(g[3], *g[:3], o, lse, causal=True, **kw)
+    for _ in range(20):
+        again = rl.attention_backward(g[3], *g[:3], o, lse, causal=True, **kw)
+        for a, b in zip(first, again):
+            assert torch.equal(a, b)
+    rl.device_status()
