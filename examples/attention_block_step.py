@@ -89,7 +89,7 @@ def main(steps=5, tokens=1024, device="cuda:0"):
     x, target = r(1, tokens, width), r(1, tokens, width)
     live = (documents >= 0)[..., None].float()
 
-    clip = rl.GradClip([t.grad for t in block.adapters])
+    clip = rl.GradClip(params=block.adapters)
     losses = []
     for step in range(steps):
         y = block.forward(x, positions, documents)

@@ -7,7 +7,8 @@
  * A fine-tuning step ends with it over the dA and dB of every LoRA layer
  * (lora_linear.h).  The tensors' addresses, sizes and types are laid out once
  * in a plan, which the caller keeps as long as the tensors stay where they
- * are.  Tensors may mix bf16 and fp32, have any size and any alignment of
+ * are (a training loop that makes new gradients each step, as PyTorch's
+ * zero_grad() does by default, has to make a new plan or clear them in place).  Tensors may mix bf16 and fp32, have any size and any alignment of
  * their type.
  *
  * Sums: at most 33 squares in fp32, then unevaluated pairs of fp32 and fp64;

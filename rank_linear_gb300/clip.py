@@ -14,16 +14,32 @@ from .rotary import _stream_on
 class GradClip:
     """The plan over a list of gradient tensors, laid out once on the device.
 
-    grads    contiguous CUDA tensors, bf16 and fp32 in any mix; the plan keeps
-             them alive and reads the values they hold at each call.
+    grads    contiguous CUDA tensors, bf16 and fp32 in any mix; None: those of
+             `params`.  The plan holds their addresses: it keeps this memory and
+             reads the values that are in it at each call.  Gradients have to
+             stay there: zero_grad(set_to_none=False) or grad.zero_() between
+             steps.  What zero_grad() does by default, dropping them for the
+             next backward() to make new ones, leaves the plan with the old.
     out      tensors of the same shapes and types for the clipped gradients;
              None: in place.
+    params   the parameters whose .grad these are, where that is to be made
+             sure of: a call then raises if one of them has another gradient by
+             now, or none, instead of clipping what is no longer in use.
 
     Calls that overlap on the GPU (other streams) need a plan each.
     """
 
-    def __init__(self, grads, out=None):
+    def __init__(self, grads=None, out=None, *, params=None):
+        self.params = None if params is None else list(params)
+        if grads is None:
+            if params is None:
+                raise ValueError("grads or params are needed")
+            grads = [p.grad for p in self.params]
         self.grads = list(grads)
+        if any(g is None for g in self.grads):
+            raise ValueError("a parameter has no gradient yet")
+        if self.params is not None and len(self.params) != len(self.grads):
+            raise ValueError(f"{len(self.params)} parameters for {len(self.grads)} gradients")
         self.out = self.grads if out is None else list(out)
         if len(self.out) != len(self.grads):
             raise ValueError(f"{len(self.out)} outputs for {len(self.grads)} gradients")
@@ -52,7 +68,18 @@ class GradClip:
                    "lora_clip_plan_build")
         self.plan = image.to(device if device is not None else torch.device("cuda"))
         self.device, self._at = self.plan.device, self.plan.data_ptr()
+        # (a tensor may be given other memory: what the plan points to stays)
+        self._memory = [t.detach() for t in (*self.grads, *self.out)]
+        self._places = [g.data_ptr() for g in self.grads]
+        self._check_params()
         self._scalar = torch.empty((), dtype=torch.float32, device=self.device)
+
+    def _check_params(self):
+        if self.params is not None:
+            for i, (p, at) in enumerate(zip(self.params, self._places)):
+                if p.grad is None or p.grad.data_ptr() != at:
+                    raise RuntimeError(f"parameter {i} no longer has the gradient that the plan was made for: "
+                                       "clear gradients in place (zero_grad(set_to_none=False))")
 
     @staticmethod
     def _largest(norm_type) -> int:
@@ -72,6 +99,7 @@ class GradClip:
 
     def norm(self, *, norm_type: float = 2.0, norm=None, stream=None):
         """The global norm (a device scalar); nothing is scaled."""
+        self._check_params()
         norm = self._norm_out(norm, stream)
         st = _lib.lib().lora_clip_norm(self._at, self.bytes, self._largest(norm_type),
                                        norm.data_ptr(), _stream_on(self.device, stream))
@@ -82,6 +110,7 @@ class GradClip:
     def clip(self, max_norm: float, *, norm_type: float = 2.0, norm=None, stream=None):
         """Scales every gradient by min(1, max_norm / (norm + 1e-6)); returns the
         norm before it (a device scalar)."""
+        self._check_params()
         norm = self._norm_out(norm, stream)
         st = _lib.lib().lora_clip(self._at, self.bytes, float(max_norm), self._largest(norm_type),
                                   norm.data_ptr(), _stream_on(self.device, stream))
