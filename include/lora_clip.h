@@ -32,7 +32,8 @@ extern "C" {
 
 typedef struct {
     const void *in; /* device, aligned to its type                          */
-    void *out;      /* device; `in` itself (in place) or no overlap with it  */
+    void *out;      /* device; `in` itself (in place), or memory of its own:
+                       no other tensor's, in or out                          */
     int64_t count;  /* elements, >= 0 (0: the pointers may be NULL)          */
     int32_t dtype;  /* lora_dtype_t of both                                  */
 } lora_clip_tensor_t;
@@ -40,7 +41,8 @@ typedef struct {
 /* Bytes of the plan of these tensors; 0 for bad arguments. */
 size_t lora_clip_plan_bytes(const lora_clip_tensor_t *tensors, int n);
 
-/* Writes the plan's image to HOST memory.  The caller copies it to a 16-byte
+/* Writes the plan's image to HOST memory (outputs that share memory are
+ * refused).  The caller copies it to a 16-byte
  * aligned device buffer of the same size, which lora_clip_norm and lora_clip
  * take.  The device copy holds scratch too: calls with one plan that overlap
  * on the GPU race on it. */

@@ -13,8 +13,11 @@
 // 2.6 MB in 14 tensors 10 us (two launches).
 #include <cuda_bf16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <new>
+#include <vector>
 
 #include "host.h"
 #include "lora_clip.h"
@@ -422,6 +425,42 @@ lora_status_t check_tensors(const lora_clip_tensor_t *t, int n, int64_t *bytes) 
   return LORA_OK;
 }
 
+// No output may share memory with another tensor (but for its own input, in
+// place): blocks read and write them in any order.  One sweep over the tensors
+// by address.
+lora_status_t check_overlap(const lora_clip_tensor_t *t, int n) {
+  struct Run {
+    uintptr_t from, to;
+    int tensor;
+    bool written;
+  };
+  try {
+    std::vector<Run> runs;
+    runs.reserve(2 * size_t(n));
+    for (int i = 0; i < n; ++i) {
+      const uintptr_t size = uintptr_t(t[i].count) * (t[i].dtype == LORA_BF16 ? 2 : 4);
+      if (size == 0) continue;
+      const uintptr_t in = reinterpret_cast<uintptr_t>(t[i].in);
+      const uintptr_t out = reinterpret_cast<uintptr_t>(t[i].out);
+      runs.push_back({out, out + size, i, true});
+      if (in != out) runs.push_back({in, in + size, i, false});
+    }
+    std::sort(runs.begin(), runs.end(), [](const Run &a, const Run &b) { return a.from < b.from; });
+    Run any = {0, 0, -1, false}, written = any;  // of those before, the one that ends last
+    for (const Run &r : runs) {
+      const Run &other = r.written ? any : written;
+      if (r.from < other.to)
+        return fail(LORA_ERR_INVALID_ARG, "the output of tensor %d shares memory with tensor %d",
+                    r.written ? r.tensor : other.tensor, r.written ? other.tensor : r.tensor);
+      if (r.to > any.to) any = r;
+      if (r.written && r.to > written.to) written = r;
+    }
+  } catch (const std::bad_alloc &) {
+    return fail(LORA_ERR_WORKSPACE, "no host memory to compare %d tensors", n);
+  }
+  return LORA_OK;
+}
+
 // 4 KB chunks (one vector a thread) where 16 KB ones would not give a GB300's
 // 152 SMs four blocks each.
 int chunk_bytes(int64_t total) { return total < int64_t(152) * 4 * 16384 ? 4096 : 16384; }
@@ -481,6 +520,7 @@ lora_status_t lora_clip_plan_build(const lora_clip_tensor_t *tensors, int n, voi
   clear_error();
   int64_t total = 0;
   LORA_TRY(check_tensors(tensors, n, &total));
+  LORA_TRY(check_overlap(tensors, n));
   const int cb = chunk_bytes(total);
   const size_t need = sizeof(PlanHead) + size_t(count_chunks(tensors, n, cb)) * sizeof(Chunk);
   if (image == nullptr || image_bytes != need)
