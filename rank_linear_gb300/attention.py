@@ -43,7 +43,7 @@ def _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix, like_q,
         raise ValueError(f"q {tuple(q.shape)} and k {tuple(k.shape)} do not fit")
     sh = _lib.AttentionShape(batch=b, q_len=sq, k_len=sk, q_heads=hq, k_heads=hk, dim=d,
                              causal=int(causal), scale=d ** -0.5 if scale is None else scale,
-                             softcap=softcap or 0.0)
+                             softcap=softcap)
     on = q.device
     sh.q, sh.k, sh.v = _strides(q, "q", on), _strides(k, "k", on), _strides(v, "v", on)
     for like, others in ((q, like_q), (k, like_k)):
@@ -60,6 +60,12 @@ def _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix, like_q,
     if prefix is not None:
         _check_word(prefix, torch.int32, "prefix", (b,), on)
     return sh
+
+
+def _options(scale, causal, softcap):
+    """As plain numbers: a tensor's value is read at each call, as it is then (what
+    is kept by layout is kept by these values too)."""
+    return (None if scale is None else float(scale)), bool(causal), float(softcap or 0.0)
 
 
 def _doc_pair(documents, q, k):
@@ -123,6 +129,7 @@ def attention_forward(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=
                (with causal).
     """
     qd, kd = _doc_pair(documents, q, k)
+    scale, causal, softcap = _options(scale, causal, softcap)
     with _on(stream):
         # (an output made here has the layout that q's decides)
         key = ("forward", _layout(q), _layout(k), _layout(v), _layout(out), scale, causal, softcap,
@@ -159,6 +166,7 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
             lse.shape != (q.shape[0], q.shape[2], q.shape[1]) or lse.device != q.device:
         raise ValueError("lse must be the forward's: float32 [batch, q_heads, q_len]")
     qd, kd = _doc_pair(documents, q, k)
+    scale, causal, softcap = _options(scale, causal, softcap)
     own = dq is None and dk is None and dv is None and workspace is None
     with _on(stream):
         if not own:
@@ -206,6 +214,7 @@ def attention_decode(q, k_cache, v_cache, lengths, *, scale=None, softcap=0.0, s
     if q.dim() != 3:
         raise ValueError("q must be [batch, q_heads, dim]")
     L = _lib.lib()
+    scale, _, softcap = _options(scale, False, softcap)
     with _on(stream):
         key = ("token", _layout(q), _layout(k_cache), _layout(v_cache), _layout(lengths), scale,
                softcap, _layout(slopes), _layout(out))
@@ -247,7 +256,8 @@ class AttentionFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, slopes, documents, prefix, scale, causal, softcap):
         q, k, v = _fit(q), _fit(k), _fit(v)
-        ctx.opts = dict(scale=scale, causal=causal, softcap=softcap)
+        # (the backward's are the forward's, whatever a tensor of them holds then)
+        ctx.opts = dict(zip(("scale", "causal", "softcap"), _options(scale, causal, softcap)))
         pair = isinstance(documents, (tuple, list))
         docs = tuple(documents) if pair else (documents,)
         out, lse = attention_forward(q, k, v, slopes=slopes, documents=documents, prefix=prefix,

@@ -199,8 +199,9 @@ def _turn(q, k, positions, freqs, interleaved, inverse, q_out, k_out, stream):
     if q is None and k is None:
         raise ValueError("q and k are both None")
     # (an output made here has the layout that its input's decides)
+    interleaved, magnitude = bool(interleaved), float(freqs.magnitude)  # a tensor's: as it is now
     key = (_layout(q), _layout(k), _layout(positions), _layout(q_out), _layout(k_out),
-           freqs.rot, freqs.magnitude, freqs.device, interleaved, inverse)
+           freqs.rot, magnitude, freqs.device, interleaved, inverse)
     if q_out is None or k_out is None:
         with _on(stream):
             if q is not None and q_out is None:

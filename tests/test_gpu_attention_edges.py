@@ -259,3 +259,29 @@ def test_gradients_of_few_keys_repeat_bit_for_bit(sq, sk, kw):
         for a, b in zip(first, again):
             assert torch.equal(a, b)
     rl.device_status()
+
+
+def test_options_given_as_tensors_are_read_at_each_call():
+    q, k, v, do = (t.to(DEV) for t in draw(1, 70, 70, 2, 1, 64, 4))
+    scale, cap, causal = torch.tensor(0.1), torch.tensor(5.0), torch.tensor(False)
+    n = torch.tensor([70], dtype=torch.int32, device=DEV)
+
+    def both(scale, cap, causal):
+        o, lse = rl.attention_forward(q, k, v, scale=scale, softcap=cap, causal=causal)
+        grads = rl.attention_backward(do, q, k, v, o, lse, scale=scale, softcap=cap, causal=causal)
+        return (o, lse) + grads + (rl.attention_decode(q[:, 0], k, v, n, scale=scale, softcap=cap),)
+
+    for s, c, m in ((0.1, 5.0, False), (0.2, 5.0, False), (0.2, 9.0, False), (0.2, 9.0, True)):
+        scale.fill_(s), cap.fill_(c), causal.fill_(m)
+        for a, b in zip(both(scale, cap, causal), both(scale.item(), cap.item(), causal.item())):
+            assert torch.equal(a, b), (s, c, m)
+    # and the backward of attention() is that of its forward
+    x = [t.clone().requires_grad_() for t in (q, k, v)]
+    o = rl.attention(*x, scale=scale, softcap=cap)
+    was = scale.item()
+    scale.fill_(0.7)
+    o.backward(do)
+    y = [t.clone().requires_grad_() for t in (q, k, v)]
+    rl.attention(*y, scale=was, softcap=9.0).backward(do)
+    for a, b in zip(x, y):
+        assert torch.equal(a.grad, b.grad)
