@@ -8,6 +8,7 @@ from __future__ import annotations
 import ctypes
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .lora import _ptr
@@ -251,7 +252,8 @@ def _fit(t):
 
 
 class AttentionFunction(torch.autograd.Function):
-    """Autograd function: saves q, k, v, the output and its log-sum-exp."""
+    """Autograd function: saves q, k, v, the output and its log-sum-exp.  Gradients
+    for q, k and v, once (not gradients of gradients)."""
 
     @staticmethod
     def forward(ctx, q, k, v, slopes, documents, prefix, scale, causal, softcap):
@@ -267,6 +269,7 @@ class AttentionFunction(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dout):
         q, k, v, out, lse, slopes, prefix, *docs = ctx.saved_tensors
         dq, dk, dv = attention_backward(_fit(dout), q, k, v, out, lse, slopes=slopes,

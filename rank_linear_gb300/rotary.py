@@ -10,6 +10,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .lora import _dtype_code, _ptr
@@ -235,7 +236,8 @@ def rotary_backward(dq, dk, positions, freqs: RotaryFrequencies, *, interleaved=
 
 
 class RotaryFunction(torch.autograd.Function):
-    """Autograd function: saves the positions only."""
+    """Autograd function: saves the positions only.  Gradients once (not gradients
+    of gradients)."""
 
     @staticmethod
     def forward(ctx, q, k, positions, freqs, interleaved):
@@ -244,6 +246,7 @@ class RotaryFunction(torch.autograd.Function):
         return rotary_forward(q, k, positions, freqs, interleaved=interleaved)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dq, dk):
         positions, = ctx.saved_tensors
         fit = lambda t: t if t is None or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()

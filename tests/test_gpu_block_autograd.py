@@ -1,0 +1,26 @@
+"""What autograd may and may not ask of rotary positions and attention (needs a GB300)."""
+import pytest
+import torch
+
+import rank_linear_gb300 as rl
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+
+
+def draw(*shape, seed=0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)).bfloat16().to(DEV)
+
+
+def test_no_gradients_of_gradients():
+    """A loss of gradients says that it cannot be had, instead of leaving them out."""
+    q, k, v = draw(1, 30, 2, 64).requires_grad_(), draw(1, 30, 1, 64, seed=1), draw(1, 30, 1, 64, seed=2)
+    g, = torch.autograd.grad(rl.attention(q, k, v, causal=True).float().square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        (g.float().square().sum() + q.float().square().sum()).backward()
+    f = rl.rotary_frequencies(64, device=DEV)
+    a, _ = rl.rotary(q, k, torch.arange(30, device=DEV), f)
+    g, = torch.autograd.grad(a.float().square().sum(), q, create_graph=True)
+    with pytest.raises(RuntimeError, match="differentiate twice"):
+        (g.float().square().sum() + q.float().square().sum()).backward()
