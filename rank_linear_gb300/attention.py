@@ -253,7 +253,7 @@ def _fit(t):
 
 class AttentionFunction(torch.autograd.Function):
     """Autograd function: saves q, k, v, the output and its log-sum-exp.  Gradients
-    for q, k and v, once (not gradients of gradients)."""
+    for q, k and v, once (not gradients of gradients); slopes are constants."""
 
     @staticmethod
     def forward(ctx, q, k, v, slopes, documents, prefix, scale, causal, softcap):
@@ -271,6 +271,8 @@ class AttentionFunction(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dout):
+        if ctx.needs_input_grad[3]:
+            raise RuntimeError("slopes get no gradient: give them detached")
         q, k, v, out, lse, slopes, prefix, *docs = ctx.saved_tensors
         dq, dk, dv = attention_backward(_fit(dout), q, k, v, out, lse, slopes=slopes,
                                         documents=tuple(docs) if ctx.pair else docs[0],
@@ -280,5 +282,7 @@ class AttentionFunction(torch.autograd.Function):
 
 def attention(q, k, v, *, scale=None, causal=False, softcap=0.0, slopes=None, documents=None,
               prefix=None):
-    """attention_forward's output with gradients for q, k and v."""
+    """attention_forward's output with gradients for q, k and v (whose strides may be
+    any: what the kernels do not take as it is is copied).  Slopes are constants:
+    a backward with slopes that require a gradient raises."""
     return AttentionFunction.apply(q, k, v, slopes, documents, prefix, scale, causal, softcap)

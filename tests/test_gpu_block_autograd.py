@@ -24,3 +24,16 @@ def test_no_gradients_of_gradients():
     g, = torch.autograd.grad(a.float().square().sum(), q, create_graph=True)
     with pytest.raises(RuntimeError, match="differentiate twice"):
         (g.float().square().sum() + q.float().square().sum()).backward()
+
+
+def test_slopes_get_no_gradient_and_say_so():
+    q, k, v = draw(1, 30, 2, 64).requires_grad_(), draw(1, 30, 1, 64, seed=1), draw(1, 30, 1, 64, seed=2)
+    slopes = torch.tensor([0.5, 0.25], device=DEV, requires_grad=True)
+    o = rl.attention(q, k, v, causal=True, slopes=slopes)
+    with pytest.raises(RuntimeError, match="slopes"):
+        o.float().sum().backward()
+    with torch.no_grad():
+        a = rl.attention(q, k, v, causal=True, slopes=slopes)
+    b = rl.attention(q, k, v, causal=True, slopes=slopes.detach())
+    b.float().sum().backward()
+    assert torch.equal(a, b) and q.grad.isfinite().all()
