@@ -223,8 +223,8 @@ def rotary_forward(q, k, positions, freqs: RotaryFrequencies, *, interleaved=Fal
                    k_out=None, stream=None):
     """(q, k) turned by their tokens' positions; q or k may be None.
 
-    q and k are [batch, seq, heads, dim] or [tokens, heads, dim] with any
-    strides (views of a fused q|k|v output); positions [batch, seq], [seq] or
+    q and k are [batch, seq, heads, dim] or [tokens, heads, dim], the elements of
+    a head side by side, with any other strides (views of a fused q|k|v output); positions [batch, seq], [seq] or
     [tokens].  q_out / k_out may be q / k themselves (in place)."""
     return _turn(q, k, positions, freqs, interleaved, False, q_out, k_out, stream)
 
@@ -235,6 +235,11 @@ def rotary_backward(dq, dk, positions, freqs: RotaryFrequencies, *, interleaved=
     return _turn(dq, dk, positions, freqs, interleaved, True, dq_out, dk_out, stream)
 
 
+def _fit(t):
+    """t itself where a head's elements lie side by side, else a copy."""
+    return t if t is None or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
+
+
 class RotaryFunction(torch.autograd.Function):
     """Autograd function: saves the positions only.  Gradients once (not gradients
     of gradients)."""
@@ -243,18 +248,17 @@ class RotaryFunction(torch.autograd.Function):
     def forward(ctx, q, k, positions, freqs, interleaved):
         ctx.save_for_backward(positions)
         ctx.freqs, ctx.interleaved = freqs, interleaved
-        return rotary_forward(q, k, positions, freqs, interleaved=interleaved)
+        return rotary_forward(_fit(q), _fit(k), positions, freqs, interleaved=interleaved)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dq, dk):
         positions, = ctx.saved_tensors
-        fit = lambda t: t if t is None or t.stride(-1) == 1 or t.shape[-1] == 1 else t.contiguous()
-        dq, dk = rotary_backward(fit(dq), fit(dk), positions, ctx.freqs,
+        dq, dk = rotary_backward(_fit(dq), _fit(dk), positions, ctx.freqs,
                                  interleaved=ctx.interleaved)
         return dq, dk, None, None, None
 
 
 def rotary(q, k, positions, freqs: RotaryFrequencies, *, interleaved=False):
-    """Rotary positions of q and k with gradients for both."""
+    """Rotary positions of q and k (with any strides) with gradients for both."""
     return RotaryFunction.apply(q, k, positions, freqs, interleaved)

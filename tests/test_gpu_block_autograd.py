@@ -37,3 +37,19 @@ def test_slopes_get_no_gradient_and_say_so():
     b = rl.attention(q, k, v, causal=True, slopes=slopes.detach())
     b.float().sum().backward()
     assert torch.equal(a, b) and q.grad.isfinite().all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rotary_of_strided_heads(dtype):
+    f = rl.rotary_frequencies(64, device=DEV)
+    pos = torch.arange(30, device=DEV)
+    x = draw(2, 30, 4, 128).to(dtype)
+    q = x[..., ::2].detach().requires_grad_()
+    k = draw(2, 30, 64, 2, seed=1).to(dtype).transpose(2, 3).detach().requires_grad_()
+    gq, gk = draw(2, 30, 4, 64, seed=2).to(dtype), draw(2, 30, 2, 64, seed=3).to(dtype)
+    a, b = rl.rotary(q, k, pos, f)
+    torch.autograd.backward((a, b), (gq, gk))
+    a1, b1 = rl.rotary_forward(q.detach().contiguous(), k.detach().contiguous(), pos, f)
+    dq, dk = rl.rotary_backward(gq, gk, pos, f)
+    for got, want in ((a, a1), (b, b1), (q.grad, dq), (k.grad, dk)):
+        assert torch.equal(got, want)
