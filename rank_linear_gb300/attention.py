@@ -168,40 +168,27 @@ def attention_backward(dout, q, k, v, out, lse, *, scale=None, causal=False, sof
         raise ValueError("lse must be the forward's: float32 [batch, q_heads, q_len]")
     qd, kd = _doc_pair(documents, q, k)
     scale, causal, softcap = _options(scale, causal, softcap)
-    own = dq is None and dk is None and dv is None and workspace is None
     with _on(stream):
-        if not own:
-            dq = _empty_like(q) if dq is None else dq
-            dk = _empty_like(k) if dk is None else dk
-            dv = _empty_like(v) if dv is None else dv
+        # (outputs made here have the layouts that q's, k's and v's decide, and
+        # memory of their own: what keeps one of them does not keep the others)
         key = ("backward", _layout(q), _layout(k), _layout(v), _layout(out), _layout(dout),
                _layout(dq), _layout(dk), _layout(dv), scale, causal, softcap, _layout(slopes),
                _layout(qd), _layout(kd), _layout(prefix))
+        dq = _empty_like(q) if dq is None else dq
+        dk = _empty_like(k) if dk is None else dk
+        dv = _empty_like(v) if dv is None else dv
 
         def make():
-            like = lambda t: torch.empty(t.shape, dtype=t.dtype, device="meta").stride()
             sh = _make_shape(q, k, v, scale, causal, softcap, slopes, qd, kd, prefix,
-                             {"o": out, "d_o": dout, **({} if own else {"dq": dq})},
-                             {} if own else {"dk": dk, "dv": dv})
-            if own:
-                sh.dq, sh.dk, sh.dv = like(q)[:3], like(k)[:3], like(k)[:3]
-            pad = lambda n: (n + 127) // 128 * 128  # 256 bytes
-            return (sh, _workspace_bytes(sh, qd is not None, prefix is not None, 1), like(q), like(k),
-                    pad(q.numel()), pad(k.numel()))
-        block, need, q_like, k_like, nq, nk = _block(key, make)
-        if own:  # one buffer for the three gradients and the scratch behind them
-            buf = torch.empty(nq + 2 * nk + (need + 1) // 2, dtype=q.dtype, device=q.device)
-            dq = buf.as_strided(q.shape, q_like, 0)
-            dk = buf.as_strided(k.shape, k_like, nq)
-            dv = buf.as_strided(k.shape, k_like, nq + nk)
-            scratch, have = (buf.data_ptr() + 2 * (nq + 2 * nk) if need else None), need
-        else:
-            workspace = _scratch(need, q, workspace)
-            scratch, have = _ptr(workspace), _size(workspace)
+                             {"o": out, "d_o": dout, "dq": dq}, {"dk": dk, "dv": dv})
+            return sh, _workspace_bytes(sh, qd is not None, prefix is not None, 1)
+        block, need = _block(key, make)
+        workspace = _scratch(need, q, workspace)
     sh = _filled(block, slopes, qd, kd, prefix)
     st = _lib.lib().lora_attention_bwd(ctypes.byref(sh), _ptr(dout), _ptr(q), _ptr(k), _ptr(v),
                                        _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                                       scratch, have, _stream_on(q.device, stream))
+                                       _ptr(workspace), _size(workspace),
+                                       _stream_on(q.device, stream))
     if st:
         _lib.check(st, "lora_attention_bwd")
     return dq, dk, dv

@@ -53,3 +53,16 @@ def test_rotary_of_strided_heads(dtype):
     dq, dk = rl.rotary_backward(gq, gk, pos, f)
     for got, want in ((a, a1), (b, b1), (q.grad, dq), (k.grad, dk)):
         assert torch.equal(got, want)
+
+
+def test_gradients_have_memory_of_their_own():
+    """Keeping, saving or changing one gradient does nothing with the others."""
+    q, k, v = (draw(1, 300, h, 64, seed=s).requires_grad_() for s, h in enumerate((4, 2, 2)))
+    rl.attention(q, k, v, causal=True).float().square().sum().backward()
+    grads = [t.grad for t in (q, k, v)]
+    assert len({g.untyped_storage().data_ptr() for g in grads}) == 3
+    for g in grads:
+        assert g.untyped_storage().nbytes() <= g.numel() * g.element_size() + 512
+    before = [g._version for g in grads]
+    grads[0].mul_(0.5)
+    assert [g._version for g in grads[1:]] == before[1:]
