@@ -12,10 +12,11 @@
  * (2i, 2i + 1) (interleaved); elements from `rot` on are copied.  The
  * backward of the operator is the same with -a (inverse = 1).
  *
- * Frequencies are given in turns per position as 64-bit fractions,
- * turns_i = frac(w_i / 2 pi) * 2^64 (lora_rotary_turns): position times
- * turns modulo 2^64 is the reduced angle without rounding, so that the
- * error does not grow with the position (negative positions included).
+ * Frequencies are given in turns per position as 64-bit fractions, turns_i =
+ * frac(w_i / 2 pi) * 2^64 to the nearest (lora_rotary_turns; w_i as the double
+ * that it is).  Position times turns modulo 2^64 is the reduced angle (negative
+ * positions included): off by at most 2^-65 of a turn for every position, below
+ * the 2^-24 that the angle is then rounded to up to position 2^41.
  *
  * Errors, streams and the timing hook are those of lora_linear.h.  Nothing
  * is allocated; no host synchronisation.  One launch.
@@ -42,7 +43,8 @@ typedef struct {
     int64_t position[2];           /* strides of the positions: batch, token  */
 } lora_rotary_t;
 
-/* turns[i] = frac(radians[i] / 2 pi) * 2^64 for n frequencies, on the host. */
+/* turns[i] = frac(radians[i] / 2 pi) * 2^64, to the nearest, for n finite
+ * frequencies, on the host. */
 lora_status_t lora_rotary_turns(const double *radians, int n, uint64_t *turns);
 
 /*

@@ -2,7 +2,7 @@
 //
 // One pass over q and k, bound by HBM (or by the launch where the tokens are
 // few).  The angles are not read from a table: position * turns modulo 2^64
-// is the angle's exact fraction of a turn.  A block takes a few neighbouring
+// is the angle's fraction of a turn, off by the position times 2^-65.  A block takes a few neighbouring
 // tokens: its warps ask for their first heads, form the cosines and sines of
 // all its tokens in shared memory meanwhile, and pass over the heads side by
 // side, a lane keeping its place in the head.  Measured at 4096 tokens x 40
@@ -249,6 +249,36 @@ cudaError_t launch_rotary(RotaryArgs &a, bool neighbours, bool copy_tail, int sm
                     size_t(a.tokens) * a.rot * sizeof(float), s, a);
 }
 
+// The first 1152 binary places of 1 / (2 pi).
+constexpr uint64_t kOverTwoPi[18] = {
+    0x28be60db9391054aull, 0x7f09d5f47d4d3770ull, 0x36d8a5664f10e410ull,
+    0x7f9458eaf7aef158ull, 0x6dc91b8e909374b8ull, 0x01924bba82746487ull,
+    0x3f877ac72c4a69cfull, 0xba208d7d4baed121ull, 0x3a671c09ad17df90ull,
+    0x4e64758e60d4ce7dull, 0x272117e2ef7e4a0eull, 0xc7fe25fff7816603ull,
+    0xfbcbc462d6829b47ull, 0xdb4d9fb3c9f2c26dull, 0xd3d18fd9a797fa8bull,
+    0x5d49eeb1faf97c5eull, 0xcf41ce7de294a4baull, 0x9afed7ec47e35742ull};
+// Its 64 places from place `at` + 1 on (places before the first: 0).
+uint64_t places(int at) {
+  auto word = [](int i) { return i >= 0 && i < 18 ? kOverTwoPi[i] : uint64_t(0); };
+  if (at <= -64) return 0;
+  const int i = at < 0 ? -1 : at / 64, shift = at - 64 * i;  // 0 .. 63
+  return shift == 0 ? word(i) : word(i) << shift | word(i + 1) >> (64 - shift);
+}
+// frac(w / 2 pi) * 2^64 to the nearest, for any finite w: w = m 2^e with whole m
+// times those places of 1 / (2 pi) that count, as Payne and Hanek (1983) do it.
+// (A quotient of doubles would be off by 2^-54 of a turn, times the position.)
+uint64_t turns_of(double w) {
+  int e;
+  const double f = std::frexp(std::fabs(w), &e);  // in [1/2, 1)
+  const uint64_t m = static_cast<uint64_t>(std::ldexp(f, 53));
+  // T = m 2^(e - 53 + 64) / (2 pi) modulo 2^64: 64 places above 1 and 64 below
+  const int s = e - 53 + 64;
+  const uint64_t hi = places(s - 64), lo = places(s);
+  const unsigned __int128 below = static_cast<unsigned __int128>(m) * lo + (uint64_t(1) << 63);
+  const uint64_t t = m * hi + static_cast<uint64_t>(below >> 64);
+  return w < 0 ? uint64_t(0) - t : t;
+}
+
 }  // namespace
 }  // namespace lora
 
@@ -264,10 +294,7 @@ lora_status_t lora_rotary_turns(const double *radians, int n, uint64_t *turns) {
   for (int i = 0; i < n; ++i) {
     if (!std::isfinite(radians[i]))
       return fail(LORA_ERR_INVALID_ARG, "radians[%d] is not finite", i);
-    double t = radians[i] / 6.283185307179586476925286766559;
-    t -= std::floor(t);
-    const double v = std::ldexp(t, 64);  // t == 1.0 (rounded up) is a whole turn: 0
-    turns[i] = v >= 18446744073709551616.0 ? 0 : static_cast<uint64_t>(v);
+    turns[i] = turns_of(radians[i]);
   }
   return LORA_OK;
 }

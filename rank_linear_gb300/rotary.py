@@ -1,7 +1,7 @@
 """Rotary positions of q and k (ch05 "Acceleration principles: Triton kernels
 and fused LoRA", §5.5): what stands between the q and k LoRA layers and the
 attention.  Both tensors are turned in one launch of the CUDA library; angles
-are exact at any position (see include/lora_rotary.h).
+are as good at position 2^41 as at 1 (see include/lora_rotary.h).
 """
 from __future__ import annotations
 

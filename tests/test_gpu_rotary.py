@@ -198,3 +198,22 @@ def test_refusals(kw, error):
 def test_frequency_refusals(kw):
     with pytest.raises(ValueError):
         rl.rotary_frequencies(kw.pop("rot", 64), device=DEV, **kw)
+
+
+@pytest.mark.parametrize("top", [2 ** 20, 2 ** 31, 2 ** 36, 2 ** 40, 2 ** 41])
+def test_far_positions_against_whole_numbers(top):
+    """The angle's fraction of a turn from exact arithmetic: no allowance for the position."""
+    from fractions import Fraction
+    from test_rotary_turns_cpu import over_two_pi
+    c = over_two_pi()
+    f = rl.rotary_frequencies(64, base=500000.0, device=DEV)
+    q = draw((40, 2, 64), torch.float32, 3)
+    pos = torch.randint(top // 2, top, (40,), device=DEV)
+    pos[::2] *= -1
+    got = rl.rotary_forward(q, None, pos, f)[0].double().cpu().numpy()
+    turn = np.array([[float(p * Fraction(w) * c % 1) for w in f.radians] for p in pos.tolist()])
+    x = q.double().cpu().numpy()
+    z = (x[..., :32] + 1j * x[..., 32:]) * np.exp(2j * np.pi * turn)[:, None]
+    size = np.abs(x[..., :32]) + np.abs(x[..., 32:])
+    assert np.all(np.abs(got[..., :32] - z.real) <= 2.0 ** -20 * size)
+    assert np.all(np.abs(got[..., 32:] - z.imag) <= 2.0 ** -20 * size)
