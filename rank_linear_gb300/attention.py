@@ -74,6 +74,8 @@ def _doc_pair(documents, q, k):
     if documents is None:
         return None, None
     if isinstance(documents, (tuple, list)):
+        if len(documents) != 2 or (documents[0] is None) != (documents[1] is None):
+            raise ValueError("documents is one tensor, or the queries' and the keys'")
         return documents
     sq, sk = q.shape[1], k.shape[1]
     if sq > sk:

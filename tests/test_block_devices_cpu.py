@@ -105,3 +105,15 @@ def test_the_current_device(monkeypatch):
     monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
     with pytest.raises(ValueError, match="current device"):
         rotary._stream_on(HERE, None)
+
+
+def test_documents_of_one_side_are_refused():
+    """The queries' alone or the keys' alone say nothing; the keys' were left out."""
+    t = lambda h: torch.zeros(1, 3, h, 64, dtype=torch.bfloat16)
+    d = torch.zeros(1, 3, dtype=torch.int32)
+    for bad in ((None, d), (d, None), (d,), (d, d, d), []):
+        with pytest.raises(ValueError, match="documents"):
+            rl.attention_forward(t(4), t(2), t(2), documents=bad)
+        with pytest.raises(ValueError, match="documents"):
+            rl.attention_backward(t(4), t(4), t(2), t(2), t(4), torch.zeros(1, 4, 3), documents=bad)
+    assert attention._doc_pair((None, None), t(4), t(2)) == (None, None)
