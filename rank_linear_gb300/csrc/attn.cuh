@@ -300,16 +300,18 @@ __device__ __forceinline__ int last_key(const AttnArgs &a, int p, int prefix) {
 }
 
 // The score of a raw product z = q . k, in units of log 2, without the mask.
-// CAP: c = cap tanh x, x = z scale / cap, by one of two ways:
-//  - |x| <= 1: x P(x^2), P the polynomial of degree 5 next to tanh(x) / x on
+// CAP: c = cap tanh x, x = z scale / cap, by one of two ways for all of a
+// warp's pairs at hand:
+//  - |x| <= 1 for all of them: x P(x^2), P the polynomial of degree 5 next to tanh(x) / x on
 //    [0, 1] (a reweighted least-squares fit; the error of tanh is 2.4e-7 at the
 //    most, 3.1e-6 of itself next to 0), two pairs an instruction;
-//  - else |tanh x| = 1 - 2 r, r = 1 / (1 + e^2|x|): two more special functions
-//    a pair, of which an SM does 32 a cycle.  Its absolute error is 2^-22 of the
-//    cap, which would drown scores far below the cap: they stay with the first.
-// The second is formed where some pair of a warp's needs it.  What x is formed
-// from is bounded, so that no cap, however small or large, makes 0 times
-// infinity of a product that is 0 (as rows past the end are) or of its tanh.
+//  - else tanh x = 1 - 2 r, r = 1 / (1 + e^2x): two more special functions a
+//    pair, of which an SM does 32 a cycle.  Its absolute error is 2^-22 of the
+//    cap, which would drown scores far below a large cap: for |x| <= 1/8 the
+//    series' first terms, x - x^3 / 3 + 2 x^5 / 15 (2e-7 of it is left out).
+// What x is formed from is bounded, so that no cap, however small or large,
+// makes 0 times infinity of a product that is 0 (as rows past the end are) or
+// of its tanh.
 __device__ __forceinline__ constexpr float tanh_poly(int i) {  // P's coefficients
   return i == 0 ? 0.99999685f : i == 1 ? -0.33324004f : i == 2 ? 0.13253524f : i == 3 ? -0.050972835f
          : i == 4 ? 0.016114152f : -0.0028394550f;
@@ -358,13 +360,21 @@ __device__ __forceinline__ float2 cap_small(const ScoreConst &c, float2 z) {
   for (int i = 4; i >= 0; --i) p = fma2(p, u, make_float2(c.poly[i], c.poly[i]));
   return mul2(x, p);
 }
-// r as above: dc/dz = scale * 4 r (1 - r), good where |tanh| is next to 1 too.
-__device__ __forceinline__ float cap_r(const ScoreConst &c, float z) {
-  return rcp(1.f + ex2(fabsf(z) * (2.f * kLog2e * c.x_by)));
+// The same by the series, good for |x| <= 1/8.
+__device__ __forceinline__ float2 cap_near(const ScoreConst &c, float2 z) {
+  const float2 x = mul2(z, make_float2(c.x_by, c.x_by)), u = mul2(x, x);
+  const float2 y = mul2(x, make_float2(c.top, c.top));
+  const float2 p = fma2(u, make_float2(2.f / 15.f, 2.f / 15.f), make_float2(-1.f / 3.f, -1.f / 3.f));
+  return fma2(mul2(u, p), y, y);
 }
-// top tanh x of any pair, whose r is at hand and whose polynomial is `small`.
-__device__ __forceinline__ float cap_any(const ScoreConst &c, float z, float r, float small) {
-  return fabsf(z) <= c.most ? small : copysignf(fmaf(-2.f * c.top, r, c.top), z);
+// r as above of z, or of |z|: dc/dz = scale * 4 r (1 - r), which is good where
+// |tanh| is next to 1 with the r of |z| only.
+__device__ __forceinline__ float cap_r(const ScoreConst &c, float z) {
+  return rcp(1.f + ex2(z * (2.f * kLog2e * c.x_by)));
+}
+// top tanh x of any pair from its r; near: from the series.
+__device__ __forceinline__ float cap_any(const ScoreConst &c, float z, float r, float near) {
+  return fabsf(z) <= 0.125f * c.most ? near : fmaf(-2.f * c.top, r, c.top);
 }
 // Two scores; small: what all_small said of them.
 template <bool CAP, bool BIAS>
@@ -372,9 +382,12 @@ __device__ __forceinline__ float2 scores2(const ScoreConst &c, float2 z, float d
                                           bool small) {
   float2 s;
   if constexpr (CAP) {
-    s = cap_small(c, z);
-    if (!small)
+    if (small) {
+      s = cap_small(c, z);
+    } else {
+      s = cap_near(c, z);
       s = make_float2(cap_any(c, z.x, cap_r(c, z.x), s.x), cap_any(c, z.y, cap_r(c, z.y), s.y));
+    }
   } else {
     s = mul2(z, make_float2(c.scale2, c.scale2));
   }

@@ -81,12 +81,14 @@ __device__ __forceinline__ void weights(const ScoreConst &c, float (&s)[N], floa
         if constexpr (CAP || BIAS) {
           float2 t = x;  // tanh: 1 - t^2 is its slope
           if constexpr (CAP) {
-            t = cap_small(c, x);
             if (small) {
+              t = cap_small(c, x);
               f = fma2(make_float2(-t.x, -t.y), t, f);
             } else {
-              const float2 r = make_float2(cap_r(c, x.x), cap_r(c, x.y));
-              t = make_float2(cap_any(c, x.x, r.x, t.x), cap_any(c, x.y, r.y, t.y));
+              t = cap_near(c, x);
+              const float2 r = make_float2(cap_r(c, fabsf(x.x)), cap_r(c, fabsf(x.y)));
+              t = make_float2(copysignf(cap_any(c, x.x, r.x, t.x), x.x),
+                              copysignf(cap_any(c, x.y, r.y, t.y), x.y));
               f = make_float2(4.f * r.x * (1.f - r.x), 4.f * r.y * (1.f - r.y));
             }
           }

@@ -151,12 +151,16 @@ __global__ void __launch_bounds__(32 * kWarps, 3) k_attn_token(const Params p) {
       const int key = key0 + quad + 8 * (i >> 1);
       const ScoreConst &c = sc[i & 1];
       if constexpr (CAP) {  // the polynomial of one score: its coefficients take no registers
-        const float x = s[i] * c.x_by, u = x * x;
-        float p = tanh_poly(5);
+        if (small) {
+          const float x = s[i] * c.x_by, u = x * x;
+          float p = tanh_poly(5);
 #pragma unroll
-        for (int j = 4; j >= 0; --j) p = fmaf(p, u, tanh_poly(j));
-        p *= x * c.cap2;
-        s[i] = small ? p : cap_any(c, s[i], cap_r(c, s[i]), p);
+          for (int j = 4; j >= 0; --j) p = fmaf(p, u, tanh_poly(j));
+          s[i] = x * c.cap2 * p;
+        } else {
+          const float2 near = cap_near(c, make_float2(s[i], s[i]));
+          s[i] = cap_any(c, s[i], cap_r(c, s[i]), near.x);
+        }
       } else {
         s[i] *= c.scale2;
       }
