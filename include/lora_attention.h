@@ -77,7 +77,8 @@ typedef struct {
  * pass.  0 for bad arguments. */
 size_t lora_attention_workspace_bytes(const lora_attention_t *shape, int backward);
 
-/* o and lse from q, k and v.  lse may be NULL where no backward follows. */
+/* o and lse from q, k and v, which o must not overlap.  lse may be NULL where no
+ * backward follows. */
 lora_status_t lora_attention_fwd(const lora_attention_t *shape, const void *q, const void *k,
                                  const void *v, void *o, float *lse, void *workspace,
                                  size_t workspace_bytes, void *stream);

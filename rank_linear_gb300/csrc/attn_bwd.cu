@@ -7,7 +7,9 @@
 // sharing them across blocks would take five.  What a thread computes for a
 // pair, dz = P dc/dz (dP - delta) with P = exp(s - lse), goes back into TMEM
 // as bf16 over the scores (or over dP) and is the TMEM operand of the products
-// that follow; nothing of size q_len x k_len leaves the SM.
+// that follow; nothing of size q_len x k_len leaves the SM.  That rounding of
+// dz, and of P for dv, costs what the outputs' own does, 0.0017 of their norm
+// each; two bf16 parts of dz would be nine products instead of seven.
 //
 // A small pass before them leaves two numbers of each query row, -lse in log2
 // units and -delta = -do . o, in rows of whole tiles: read once for both
@@ -30,12 +32,13 @@
 // add their sums through distributed shared memory in the order of their ranks.
 //
 // Measured (32 heads of 128, 8 key heads), all three: 8192 x 8192 without a
-// mask 2465 us (1115 TFLOP/s of the formula's five products, 1560 of the seven
-// done), causal 1200 us (1145), 4096 causal 346 us (995), five documents in
-// 8192 465 us (statistics 27, dq 181, dk/dv 256 when timed one by one), heads
-// of 64 causal 926 us (740).  Bound by shared memory: a dk/dv step's products
-// read 256 KB of operands, 2000 cycles at 128 B a cycle, as long as the
-// products themselves take.
+// mask 2502 us (1100 TFLOP/s of the formula's five products, 1540 of the seven
+// done), causal 1202 us (1145), 4096 causal 337 us (1020), with a cap 478 us,
+// five documents in 8192 477 us, five others 494 us (statistics 27, dq 199,
+// dk/dv 260 when timed one by one), heads of 64 causal 1020 us (675: the
+// exponentials twice more, and half the products to set against them).  Bound
+// by shared memory: a dk/dv step's products read 256 KB of operands, 2000
+// cycles at 128 B a cycle, as long as the products themselves take.
 #include "attn.cuh"
 #include "host.h"
 

@@ -7,25 +7,29 @@
 // the tensor core works for the other.  The running maximum is only followed
 // when it has moved by more than 2^8: until then P is relative to the old one
 // (at most 256, exact in fp32 sums and no worse rounded to bf16), so that O
-// in TMEM is hardly ever rescaled.
+// in TMEM is hardly ever rescaled.  P is rounded to bf16 because the tensor
+// core multiplies it with bf16 V: o is then 0.0019 to 0.0024 of its norm from
+// 64 bits where rounding it alone takes 0.0017; two bf16 parts of P, as with
+// one token, would be a product more for every two.
 //
 // Blocks stay (one per SM) and take item after item, so that an item's copies
 // and first scores run while the one before it is written out.  A scheduling
 // warp hands items out: in order of falling work without documents, from a
 // counter with them (their work varies).  Where the last round would leave
 // SMs without an item, its items are cut along the keys (see attn_fwd_plan):
-// 2048 queries over 16000 keys 329 -> 306 us, 50 over 30000 with 4 heads 277 ->
-// 39 us.  Few queries share an item with the heads of their group, which read
-// the same keys: 16 over 8192, four times 32 heads over 8, 85 -> 45 us.
+// 2048 queries over 16000 keys 329 -> 307 us, 50 over 30000 with 4 heads 277 ->
+// 31 us.  Few queries share an item with the heads of their group, which read
+// the same keys: 16 over 8192, four times 32 heads over 8, 85 -> 44 us (K and V
+// alone take 20: the parts meet in memory, and an item has 64 rows of 256).
 //
 // TMEM: S/P of the two tiles at columns 0 and 128, O at 256 and 384.
 //
-// Measured (32 heads of 128, 8 key heads): 8192 x 8192 without a mask 620 us
-// (1775 TFLOP/s, 0.91 of what a large bf16 product reaches), causal 334 us
-// (1645), heads of 64 causal 284 us (965: the exponentials take as long as the
-// products), 4096 causal 100 us (1370); with capped scores 162 us, with a
-// distance bias 134 us (one or two more operations a pair); five documents in
-// 8192 148 us.  Bound by the
+// Measured (32 heads of 128, 8 key heads): 8192 x 8192 without a mask 623 us
+// (1765 TFLOP/s, 0.90 of what a large bf16 product reaches), causal 334 us
+// (1645), heads of 64 causal 292 us (940: the exponentials take as long as the
+// products), 4096 causal 97 us (1415); with capped scores 168 us, 244 us where
+// many are beyond the cap, with a distance bias 134 us (one or two more
+// operations a pair); five documents in 8192 139 us.  Bound by the
 // tensor cores where a block has many steps; an item begins and ends in some
 // 4 us that overlap its neighbours' steps only in part, and 256-row items
 // leave work unused along the diagonal and at documents' edges.

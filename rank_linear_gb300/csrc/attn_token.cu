@@ -1,8 +1,8 @@
 // attn_token.cu -- attention of one new token over a cache (include/lora_attention.h).
 //
-// Bound by HBM: the live part of K and V is read once, from global memory
-// straight into the registers that mma.sync takes (no shared memory, no
-// barrier in the loop), up to 8 query heads of a group at a time.  What makes
+// Bound by HBM: the live part of K and V is read once for every eight query
+// heads of a group, from global memory straight into the registers that
+// mma.sync takes (no shared memory, no barrier in the loop).  What makes
 // this work is that a dot product does not care about the order of its terms:
 // the 16 bytes of a key that a lane loads are taken to be the elements that
 // the MMA's layout wants there, and the query is laid out to match.
@@ -18,8 +18,10 @@
 // few words spilled) that keeps HBM busy.  (Measured and not kept: 4 blocks of 128
 // registers 118 us for the ragged batch where 3 take 95; L2 prefetches 1 to 6
 // steps ahead, values a step ahead in registers, all slower.)  131071 positions
-// of one sequence, 8 key heads of 128: 84 us (6.4 TB/s, 0.95 of a copy); 32
-// ragged ones up to 8192 long 97 us (6.1 TB/s).
+// of one sequence, 8 key heads of 128: 83 us (6.5 TB/s, 0.95 of a copy); 32
+// ragged ones up to 8192 long 97 us (6.1 TB/s).  That is with a cache that the
+// longest sequence fills: chunks are cut from its capacity, so that in one much
+// larger than its contents few blocks have work.
 //
 // P is transposed between the two by movmatrix.  The running maximum is
 // followed only when some score exceeds it by 2^8 (a vote instead of
