@@ -23,7 +23,9 @@
 // causal mask, short documents, and whatever looks at 128 keys or fewer.  It is
 // a pass of its own over such tiles, which are few, so that the registers and
 // the code of the others stay as they are (in one pass, heads of 64 causal at
-// 8192: dq 430 us; in two, 415; without, 400).  Rows that see more keep delta
+// 8192: dq 430 us; in two, 418; without, 400), and only where the mask may
+// leave some row no other tile (of five documents in 8192: dq 199 us over the
+// last tile of every item, 187 so, 181 without).  Rows that see more keep delta
 // from o: for them it would take the scores of all their tiles twice.
 //
 // The dq blocks stay and take item after item, as the forward's do.  A dk/dv
@@ -34,8 +36,8 @@
 // Measured (32 heads of 128, 8 key heads), all three: 8192 x 8192 without a
 // mask 2502 us (1100 TFLOP/s of the formula's five products, 1540 of the seven
 // done), causal 1202 us (1145), 4096 causal 337 us (1020), with a cap 478 us,
-// five documents in 8192 477 us, five others 494 us (statistics 27, dq 199,
-// dk/dv 260 when timed one by one), heads of 64 causal 1020 us (675: the
+// five documents in 8192 466 us, five others 481 us (statistics 27, dq 186,
+// dk/dv 260 when timed one by one), heads of 64 causal 1007 us (680: the
 // exponentials twice more, and half the products to set against them).  Bound
 // by shared memory: a dk/dv step's products read 256 KB of operands, 2000
 // cycles at 128 B a cycle, as long as the products themselves take.
@@ -502,11 +504,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_attn_dq(const __grid_constant__
         const uint32_t dp_addr = tmem + lanes + 256 + half * 64;
         if (!(ok = wait_warp(tail->s_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
         // May some row see this tile's keys only?  (Of a causal mask each row
-        // sees itself: in a tile that reaches the first row's place.)
+        // sees itself: in a tile that reaches the first row's place.  Not where
+        // every row sees all of another tile.)
         const bool close = a.q_docs == nullptr ? n == 0 && first_last < kTile
-                           : a.causal && a.prefix == nullptr
-                               ? count == 1 || n * kTile + kTile > first_last
-                               : count == 1 || !whole;
+                           : count == 1 ||
+                                 ((a.causal && a.prefix == nullptr ? n * kTile + kTile > first_last
+                                                                   : !whole) &&
+                                  (n == same0 || same0 >= same1 ||
+                                   same0 * kTile + kTile - 1 > first_last));
         if (close) {  // a pass of its own, so that the other tiles' registers stay as they are
           if (!(ok = wait_warp(tail->dp_full[x & 1], x >> 1, abort_flag, a.dev_status))) break;
           tc_fence_after();
