@@ -69,6 +69,19 @@ lora_status_t lora_fp8_fwd(const void *X, const void *Wq, const float *w_scale, 
                            size_t workspace_bytes, void *stream);
 
 /*
+ * The same for an X whose rows came quantised (Xq [M, d_in] e4m3 bytes and
+ * x_scale [M] powers of two, as from lora_fp8_quantize_rows, or from
+ * lora_norm_fwd, which makes them beside X; several layers over one X share
+ * them): Y = (Xq x_scale) Q(W)^T + s (X A^T) B^T.  X is read by the low-rank
+ * pass only.  lora_fp8_bwd is the backward of both.
+ */
+lora_status_t lora_fp8_fwd_rows(const void *X, const void *Xq, const float *x_scale, const void *Wq,
+                                const float *w_scale, const void *A, const void *B, float alpha,
+                                int r, int64_t M, int64_t d_in, int64_t d_out, void *Y,
+                                void *saved, void *workspace, size_t workspace_bytes,
+                                void *stream);
+
+/*
  * Backward from dY and the forward's `saved` buffer (required).  dX may be
  * NULL to skip it.  Gradients are overwritten.
  */

@@ -211,7 +211,10 @@ typedef enum {
     LORA_K_ATTN_FWD = 15,       /* attention: output and log-sum-exp         */
     LORA_K_ATTN_DQ = 16,        /* attention: dq                             */
     LORA_K_ATTN_DKV = 17,       /* attention: dk and dv                      */
-    LORA_K_ATTN_TOKEN = 18      /* attention: one new token over a cache     */
+    LORA_K_ATTN_TOKEN = 18,     /* attention: one new token over a cache     */
+    LORA_K_NORM = 19,           /* root-mean-square norm                     */
+    LORA_K_NORM_BWD = 20,       /* its gradients                             */
+    LORA_K_DROPOUT = 21         /* dropout                                   */
 } lora_kernel_kind_t;
 
 /*

@@ -17,7 +17,8 @@ LORA_OK, LORA_ERR_INVALID_ARG, LORA_ERR_UNSUPPORTED, LORA_ERR_WORKSPACE, \
 LORA_BF16, LORA_FP32 = 0, 1
 KERNEL_KINDS = ["prep", "down_fwd", "main_fwd", "down_bwd", "main_bwd", "grad_a", "grad_b",
                 "down_bwd_grad_b", "swiglu_grad", "quant", "grad_a_b", "rotary", "grad_norm",
-                "grad_clip", "attn_prep", "attn_fwd", "attn_dq", "attn_dkv", "attn_token"]
+                "grad_clip", "attn_prep", "attn_fwd", "attn_dq", "attn_dkv", "attn_token", "norm",
+                "norm_bwd", "dropout"]
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
 _int, _f32 = ctypes.c_int, ctypes.c_float
@@ -49,6 +50,20 @@ class AttentionShape(ctypes.Structure):
                 ("q_docs_stride", _i64), ("k_docs_stride", _i64), ("prefix", _vp)]
 
 
+class Dropout(ctypes.Structure):
+    """lora_dropout_t"""
+    _fields_ = [("p", ctypes.c_double), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint32),
+                ("state", _vp)]
+
+
+class NormShape(ctypes.Structure):
+    """lora_norm_t"""
+    _fields_ = [("outer", _i64), ("inner", _i64), ("dim", _i32), ("weight_fp32", _i32),
+                ("eps", _f32), ("x", _i64 * 2), ("residual", _i64 * 2), ("h", _i64 * 2),
+                ("y", _i64 * 2), ("dy", _i64 * 2), ("dh", _i64 * 2), ("dx", _i64 * 2),
+                ("dresidual", _i64 * 2)]
+
+
 SIGNATURES = {
     "lora_linear_saved_bytes": ([_i64, _int, _int], _sz),
     "lora_linear_workspace_bytes": ([_i64, _i64, _i64, _int, _int], _sz),
@@ -73,6 +88,8 @@ SIGNATURES = {
     "lora_fp8_workspace_bytes": ([_i64, _i64, _i64, _int], _sz),
     "lora_fp8_fwd": ([_vp, _vp, _vp, _vp, _vp, _f32, _int, _i64, _i64, _i64, _vp, _vp, _vp,
                       _sz, _vp], _int),
+    "lora_fp8_fwd_rows": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _int, _i64, _i64, _i64, _vp,
+                           _vp, _vp, _sz, _vp], _int),
     "lora_fp8_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _f32, _int, _i64, _i64, _i64, _vp,
                       _vp, _vp, _vp, _sz, _vp], _int),
     "lora_q4_quantize_w": ([_vp, _i64, _i64, _vp, _vp, _vp], _int),
@@ -98,6 +115,11 @@ SIGNATURES = {
     "lora_attention_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp],
                            _int),
     "lora_attention_token_workspace_bytes": ([_vp], _sz),
+    "lora_dropout": ([_vp, _i64, _i64, _i64, _i64, _vp, _int, _vp, _vp], _int),
+    "lora_norm_fwd": ([_vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "lora_norm_workspace_bytes": ([_vp, _int], _sz),
+    "lora_norm_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp],
+                      _int),
     "lora_attention_token": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
 }
 

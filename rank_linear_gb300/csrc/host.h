@@ -45,6 +45,10 @@ lora_status_t run(lora_kernel_kind_t kind, cudaStream_t s, const char *what, F &
   return timing_after(slot, s, what);
 }
 
+// out[row] = scale[row] * mul[0] (simt.cu): scales of rows that came quantised.
+cudaError_t launch_scale_rows(const float *scale, const float *mul, int64_t rows, float *out,
+                              cudaStream_t s);
+
 inline int64_t rup(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
 inline uint8_t *at(void *base, size_t off) { return static_cast<uint8_t *>(base) + off; }
 

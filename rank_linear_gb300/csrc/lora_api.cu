@@ -1066,9 +1066,10 @@ FpPlan make_fp_plan(int64_t M, int64_t d_in, int64_t d_out, int r, int pairs_f, 
   return P;
 }
 
-lora_status_t fp8_fwd(const void *X, const void *Wq, const float *w_scale, const void *A,
-                      const void *B, float alpha, int r, int64_t M, int64_t d_in, int64_t d_out,
-                      void *Y, void *saved, void *ws, size_t ws_bytes, cudaStream_t st) {
+// X's rows as codes and scales may be given (rows_q, rows_scale); else they are made here.
+lora_status_t fp8_fwd(const void *X, const void *rows_q, const float *rows_scale, const void *Wq,
+                      const float *w_scale, const void *A, const void *B, float alpha, int r,
+                      int64_t M, int64_t d_in, int64_t d_out, void *Y, void *saved, void *ws, size_t ws_bytes, cudaStream_t st) {
   DevInfo di;
   LORA_TRY(device_info(di));
   FpPlan P = make_fp_plan(M, d_in, d_out, r, main_gemm_pairs(false, di.sms), 0);
@@ -1078,10 +1079,15 @@ lora_status_t fp8_fwd(const void *X, const void *Wq, const float *w_scale, const
   unsigned *counters = split ? reinterpret_cast<unsigned *>(at(ws, P.fcnt_off)) : nullptr;
   const Plan L = make_plan(M, d_in, d_out, r, LORA_BF16);  // the saved buffer's layout
   const float s = alpha / static_cast<float>(r);
-  void *xq = at(ws, P.xq_off);
+  const void *xq = rows_q != nullptr ? rows_q : at(ws, P.xq_off);
   float *xs = reinterpret_cast<float *>(at(ws, P.xs_off));  // x_scale * w_scale per row
-  LORA_TRY(run(LORA_K_QUANT, st, "quantise X",
-               [&] { return launch_quant_rows_e4m3(X, M, d_in, xq, xs, w_scale, st); }));
+  if (rows_q != nullptr)
+    LORA_TRY(run(LORA_K_QUANT, st, "scales of X",
+                 [&] { return launch_scale_rows(rows_scale, w_scale, M, xs, st); }));
+  else
+    LORA_TRY(run(LORA_K_QUANT, st, "quantise X", [&] {
+      return launch_quant_rows_e4m3(X, M, d_in, at(ws, P.xq_off), xs, w_scale, st);
+    }));
   const void *Bsrc = B;
   int64_t b_inner = r;
   if (r % 8 != 0) {  // B's row pitch is not a multiple of 16 bytes: pad it
@@ -1549,14 +1555,20 @@ size_t lora_fp8_workspace_bytes(int64_t M, int64_t d_in, int64_t d_out, int r) {
   return need;
 }
 
-lora_status_t lora_fp8_fwd(const void *X, const void *Wq, const float *w_scale, const void *A,
-                           const void *B, float alpha, int r, int64_t M, int64_t d_in,
-                           int64_t d_out, void *Y, void *saved, void *workspace,
-                           size_t workspace_bytes, void *stream) {
+static lora_status_t fp8_fwd_entry(const void *X, const void *Xq, const float *x_scale,
+                                   bool quantised, const void *Wq, const float *w_scale,
+                                   const void *A, const void *B, float alpha, int r, int64_t M,
+                                   int64_t d_in, int64_t d_out, void *Y, void *saved,
+                                   void *workspace, size_t workspace_bytes, void *stream) {
   t_err.clear();
   LORA_TRY(check_fp8_shape(r, M, d_in, d_out, alpha));
   const bool empty = M == 0;
   LORA_TRY(check_ptr(X, "X", empty));
+  if (quantised) {
+    LORA_TRY(check_ptr(Xq, "Xq", empty));
+    if (!empty && (x_scale == nullptr || reinterpret_cast<uintptr_t>(x_scale) % 4 != 0))
+      return fail(LORA_ERR_INVALID_ARG, "x_scale is NULL or not aligned");
+  }
   LORA_TRY(check_ptr(Wq, "Wq"));
   if (w_scale == nullptr) return fail(LORA_ERR_INVALID_ARG, "w_scale is NULL");
   LORA_TRY(check_ptr(A, "A"));
@@ -1566,8 +1578,25 @@ lora_status_t lora_fp8_fwd(const void *X, const void *Wq, const float *w_scale, 
   const FpPlan P = make_fp_plan(M, d_in, d_out, r, 0, 0);
   LORA_TRY(check_ws(workspace, workspace_bytes, P.fwd_ws_min));
   if (empty) return LORA_OK;
-  return fp8_fwd(X, Wq, w_scale, A, B, alpha, r, M, d_in, d_out, Y, saved, workspace,
-                 workspace_bytes, static_cast<cudaStream_t>(stream));
+  return fp8_fwd(X, quantised ? Xq : nullptr, x_scale, Wq, w_scale, A, B, alpha, r, M, d_in, d_out,
+                 Y, saved, workspace, workspace_bytes, static_cast<cudaStream_t>(stream));
+}
+
+lora_status_t lora_fp8_fwd(const void *X, const void *Wq, const float *w_scale, const void *A,
+                           const void *B, float alpha, int r, int64_t M, int64_t d_in,
+                           int64_t d_out, void *Y, void *saved, void *workspace,
+                           size_t workspace_bytes, void *stream) {
+  return fp8_fwd_entry(X, nullptr, nullptr, false, Wq, w_scale, A, B, alpha, r, M, d_in, d_out, Y,
+                       saved, workspace, workspace_bytes, stream);
+}
+
+lora_status_t lora_fp8_fwd_rows(const void *X, const void *Xq, const float *x_scale, const void *Wq,
+                                const float *w_scale, const void *A, const void *B, float alpha,
+                                int r, int64_t M, int64_t d_in, int64_t d_out, void *Y,
+                                void *saved, void *workspace, size_t workspace_bytes,
+                                void *stream) {
+  return fp8_fwd_entry(X, Xq, x_scale, true, Wq, w_scale, A, B, alpha, r, M, d_in, d_out, Y, saved,
+                       workspace, workspace_bytes, stream);
 }
 
 lora_status_t lora_fp8_bwd(const void *dY, const void *X, const void *WqT, const float *w_scale,

@@ -2,8 +2,8 @@
 // decomposition as the bf16 tensor-core path, and the small copies of the
 // adapter B that the tensor-core path reads.
 #include <cuda_bf16.h>
-#include <cuda_fp8.h>
 
+#include "e4m3.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -157,26 +157,6 @@ __global__ void k_stack_rows(const __nv_bfloat16 *__restrict__ Ag,
 }
 
 // ---- e4m3 quantisation with power-of-two scales (fp8 frozen-W product) ----
-// The scale of a block with absolute maximum a > 0 is 2^e, e the smallest
-// integer with a <= 448 * 2^e (448 = 0.875 * 2^9, the largest e4m3 value);
-// a = 0 gives 2^0.  Dividing by it is exact, so the one rounding is the
-// conversion to e4m3 (nearest, ties to even, saturating).
-__device__ __forceinline__ int pow2_exponent(float a) {
-  if (!(a > 0.f)) return 0;
-  int k;
-  const float m = frexpf(a, &k);  // a = m 2^k, m in [0.5, 1)
-  return m <= 0.875f ? k - 9 : k - 8;
-}
-
-__device__ __forceinline__ uint8_t to_e4m3(float v) {
-  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
-}
-// Two at once: f.x in the low byte, f.y in the high byte (one conversion
-// instruction, the same rounding as to_e4m3).
-__device__ __forceinline__ uint32_t to_e4m3x2(float2 f) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3));
-}
-
 // One block per row of x [rows][cols] (cols a multiple of 8), each thread
 // holding up to 64 of the row's elements in registers (one pass over the
 // row): scale[row] = 2^e * (mul ? mul[0] : 1) and the codes
@@ -288,6 +268,15 @@ __global__ void __launch_bounds__(128) k_quant_rows_warp(const __nv_bfloat16 *__
     }
     *reinterpret_cast<uint2 *>(qr + c) = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
   }
+}
+
+// out[row] = scale[row] * mul[0]: the scales of rows that came quantised.
+__global__ void k_scale_rows(const float *__restrict__ scale, const float *__restrict__ mul,
+                             int64_t rows, float *__restrict__ out) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t row = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+  if (row < rows) out[row] = scale[row] * mul[0];
 }
 
 // amax_bits |= the bit pattern of max |w| (non-negative floats order like
@@ -470,6 +459,13 @@ cudaError_t launch_quant_rows_e4m3(const void *x, int64_t rows, int64_t cols, vo
   return launch_pdl(k_quant_rows, dim3(static_cast<unsigned>(rows)), dim3(threads), s,
                     static_cast<const __nv_bfloat16 *>(x), cols, static_cast<uint8_t *>(q), scale,
                     mul);
+}
+
+cudaError_t launch_scale_rows(const float *scale, const float *mul, int64_t rows, float *out,
+                              cudaStream_t s) {
+  if (rows <= 0) return cudaSuccess;
+  return launch_pdl(k_scale_rows, dim3(static_cast<unsigned>((rows + 255) / 256)), dim3(256), s,
+                    scale, mul, rows, out);
 }
 
 cudaError_t launch_quant_tensor_e4m3(const void *w, int rows, int cols, unsigned *amax_bits,

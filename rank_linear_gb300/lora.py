@@ -290,9 +290,12 @@ def fp8_workspace_bytes(M: int, d_in: int, d_out: int, r: int) -> int:
     return int(_lib.lib().lora_fp8_workspace_bytes(M, d_in, d_out, r))
 
 
-def fp8_forward(X, qw: FP8Weight, A, B, alpha: float, *, Y=None, saved=None, workspace=None,
-                stream=None):
-    """Y = Q(X) Q(W)^T + (alpha/r) X A^T B^T.  Returns (Y, saved)."""
+def fp8_forward(X, qw: FP8Weight, A, B, alpha: float, *, rows=None, Y=None, saved=None,
+                workspace=None, stream=None):
+    """Y = Q(X) Q(W)^T + (alpha/r) X A^T B^T.  Returns (Y, saved).
+
+    rows: X's rows as (codes, scale), where they are there already (from
+    rms_norm_forward with fp8, or quantize_rows_fp8); else they are made."""
     _check_dev(X, A, B)
     M, d_in = X.shape
     d_out, r = B.shape
@@ -303,10 +306,18 @@ def fp8_forward(X, qw: FP8Weight, A, B, alpha: float, *, Y=None, saved=None, wor
         saved = _buffer(L.lora_linear_saved_bytes(M, r, _lib.LORA_BF16), X.device)
     if workspace is None:
         workspace = _buffer(L.lora_fp8_workspace_bytes(M, d_in, d_out, r), X.device)
-    st = L.lora_fp8_fwd(_ptr(X), _ptr(qw.Wq), _ptr(qw.w_scale), _ptr(A), _ptr(B), float(alpha),
-                        r, M, d_in, d_out, _ptr(Y), _ptr(saved), _ptr(workspace),
-                        workspace.numel(), _stream_ptr(stream))
-    _lib.check(st, "lora_fp8_fwd")
+    rest = (_ptr(qw.Wq), _ptr(qw.w_scale), _ptr(A), _ptr(B), float(alpha), r, M, d_in, d_out,
+            _ptr(Y), _ptr(saved), _ptr(workspace), workspace.numel(), _stream_ptr(stream))
+    if rows is None:
+        _lib.check(L.lora_fp8_fwd(_ptr(X), *rest), "lora_fp8_fwd")
+        return Y, saved
+    codes, scale = rows
+    _check_dev(codes, scale)
+    if codes.dtype != torch.uint8 or codes.numel() != M * d_in or codes.shape[-1] != d_in or \
+            scale.dtype != torch.float32 or scale.numel() != M or \
+            codes.device != X.device or scale.device != X.device:
+        raise ValueError(f"rows must be (uint8 [{M}, {d_in}], float32 [{M}]) on the device of X")
+    _lib.check(L.lora_fp8_fwd_rows(_ptr(X), _ptr(codes), _ptr(scale), *rest), "lora_fp8_fwd_rows")
     return Y, saved
 
 
@@ -418,12 +429,13 @@ class LoRAFP8Function(torch.autograd.Function):
     """Autograd function of the layer with an fp8 frozen-W product."""
 
     @staticmethod
-    def forward(ctx, X, Wq, WqT, w_scale, A, B, alpha):
+    def forward(ctx, X, Wq, WqT, w_scale, A, B, alpha, codes=None, scale=None):
         shape = X.shape
         X2 = X.reshape(-1, shape[-1]).contiguous()
         A, B = A.contiguous(), B.contiguous()
         qw = FP8Weight(Wq, WqT, w_scale)
-        Y, saved = fp8_forward(X2, qw, A, B, alpha)
+        rows = None if codes is None else (codes.contiguous(), scale.contiguous())
+        Y, saved = fp8_forward(X2, qw, A, B, alpha, rows=rows)
         ctx.save_for_backward(X2, Wq, WqT, w_scale, A, B, saved)
         ctx.alpha = alpha
         ctx.x_shape = shape
@@ -437,12 +449,14 @@ class LoRAFP8Function(torch.autograd.Function):
                                   need_dX=ctx.needs_input_grad[0])
         if dX is not None:
             dX = dX.reshape(ctx.x_shape)
-        return dX, None, None, None, dA, dB, None
+        return dX, None, None, None, dA, dB, None, None, None
 
 
-def lora_linear_fp8(X, qw: FP8Weight, A, B, alpha: float):
-    """Q(X) Q(W)^T + (alpha/r) (X A^T) B^T with gradients for X, A and B."""
-    return LoRAFP8Function.apply(X, qw.Wq, qw.WqT, qw.w_scale, A, B, alpha)
+def lora_linear_fp8(X, qw: FP8Weight, A, B, alpha: float, rows=None):
+    """Q(X) Q(W)^T + (alpha/r) (X A^T) B^T with gradients for X, A and B; rows: X's rows
+    as (codes, scale) where they are there already (rms_norm with fp8)."""
+    codes, scale = rows if rows is not None else (None, None)
+    return LoRAFP8Function.apply(X, qw.Wq, qw.WqT, qw.w_scale, A, B, alpha, codes, scale)
 
 
 class LoRAQ4Function(torch.autograd.Function):

@@ -1,0 +1,290 @@
+"""The root-mean-square norm, its gradients and its 8-bit output against the 64-bit
+definition (needs a GB300).
+
+Bounds.  U is half a step of the type (bf16 2^-8, fp32 2^-24), F = 2^-24.
+h: the sum of two numbers in fp32 and, with dropout, a product by a factor off
+   by F, then one rounding: U |h| + 3 F (|drop(x)| + |residual|).
+rstd: sums of at most 32 + 10 positive terms a path (F each, halved by the root),
+   a division and a root: 24 F; y adds two products and a rounding:
+   (U + 28 F) |y|.  The norm is of the stored h, which the reference takes too.
+codes: half a step of e4m3 (2^-4 of the value, 2^-10 of the scale below the
+   smallest normal number) and y's own 28 F.
+dh: the mean has 42 terms a path, each of two products (50 F of the sum of
+   magnitudes); d = r (g - hat c) + dh.
+dw: a block adds its rows one after the other, then 8 lines of blocks: at most
+   rows + 8 steps of F of the sum of magnitudes, and a rounding.
+"""
+import numpy as np
+import pytest
+import torch
+
+import rank_linear_gb300 as rl
+from oracle import norm as on
+from rank_linear_gb300 import _lib
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+F = 2.0 ** -24
+U = {torch.bfloat16: 2.0 ** -8, torch.float32: F}
+
+
+def host(t):
+    return t.detach().double().cpu().numpy().reshape(-1, t.shape[-1])
+
+
+def make(rows, dim, dtype, seed=0, scale=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    return ((r(rows, dim) * scale).to(dtype), (r(rows, dim) * 2 * scale).to(dtype),
+            (1 + 0.3 * r(dim)).to(dtype), r(rows, dim).to(dtype), r(rows, dim).to(dtype))
+
+
+def check_forward(x, res, w, eps, out, p=0.0, seed=0, offset=0):
+    y, h, rstd = out[:3]
+    u = U[x.dtype]
+    if res is not None or p:
+        a = on.dropout(host(x), p, seed, offset)
+        b = host(res) if res is not None else 0.0
+        assert np.all(np.abs(host(h) - (a + b)) <= u * np.abs(a + b) + 3 * F * (np.abs(a) + np.abs(b)))
+    else:
+        assert h is x
+    want, r = on.forward(host(h), host(w[None])[0], eps)
+    assert np.all(np.abs(rstd.double().cpu().numpy().ravel() - r) <= 24 * F * r)
+    assert np.all(np.abs(host(y) - want) <= (u + 28 * F) * np.abs(want) + 2.0 ** -133)
+    if len(out) > 3:
+        codes, scale = out[3:]
+        s = scale.double().cpu().numpy().ravel()
+        lo, hi = on.row_scale(want * (1 - 28 * F)), on.row_scale(want * (1 + 28 * F))
+        assert np.all((s == lo) | (s == hi))
+        got = host(codes.view(torch.float8_e4m3fn).float()) * s[:, None]
+        assert np.all(np.abs(got - want) <= (2.0 ** -4 + 30 * F) * np.abs(want) + 2.0 ** -10 * s[:, None])
+
+
+def check_backward(dy, h, w, rstd, dh, got, p=0.0, seed=0, offset=0):
+    dx, dres, dw = got
+    u = U[dy.dtype]
+    y64, h64, w64 = host(dy), host(h), host(w[None])[0]
+    r = rstd.double().cpu().numpy().ravel()
+    d, dw64 = on.backward(y64, h64, w64, r, None if dh is None else host(dh))
+    hat = h64 * r[:, None]
+    g = np.abs(y64 * w64)
+    tol = r[:, None] * (4 * F * g + 60 * F * np.abs(hat) * np.mean(g * np.abs(hat), -1, keepdims=True)) + \
+        2 * F * np.abs(d) + (0 if dh is None else 2 * F * np.abs(host(dh)))
+    assert np.all(np.abs(host(dres) - d) <= u * np.abs(d) + 1.01 * tol + 1e-38)
+    if p:
+        keep = 2.0 ** 32 / (2 ** 32 - round(p * 2 ** 32))
+        want = on.dropout(d, p, seed, offset)
+        assert np.all(np.abs(host(dx) - want) <= (u + 2 * F) * np.abs(want) + 1.01 * keep * tol * (want != 0) + 1e-38)
+    else:
+        assert dx is dres
+    if dw is not None:
+        terms = np.sum(np.abs(y64 * hat), 0)
+        uw = U[dw.dtype]
+        assert np.all(np.abs(host(dw[None])[0] - dw64) <= uw * np.abs(dw64) + (len(r) + 12) * F * terms + 1e-38)
+
+
+DIMS = [1, 2, 7, 8, 31, 64, 100, 128, 136, 256, 264, 511, 512, 1000, 1024, 1032, 2001, 4096, 5120, 8192, 8200]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", DIMS)
+@pytest.mark.parametrize("rows", [1, 37, 700])
+def test_forward_and_backward(rows, dim, dtype):
+    x, res, w, dy, dh = make(rows, dim, dtype, seed=dim)
+    residual, grad_in = (res, dh) if dim % 3 else (None, None)
+    fp8 = rows != 37
+    out = rl.rms_norm_forward(x, w, residual=residual, eps=1e-5, fp8=fp8)
+    check_forward(x, residual, w, 1e-5, out)
+    _, h, rstd = out[:3]
+    got = rl.rms_norm_backward(dy, h, w, rstd, dh=grad_in)
+    check_backward(dy, h, w, rstd, grad_in, got)
+    again = rl.rms_norm_backward(dy, h, w, rstd, dh=grad_in)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[2], again[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", [(3, 32768), (5, 20001), (400, 16384)])
+def test_the_widest(rows, dim, dtype):
+    x, res, w, dy, dh = make(rows, dim, dtype, seed=7)
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-6, fp8=True, dropout=0.2, seed=3)
+    check_forward(x, res, w, 1e-6, out, 0.2, 3)
+    got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh, dropout=0.2, seed=3)
+    check_backward(dy, out[1], w, out[2], dh, got, 0.2, 3)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [5, 96, 777, 4096])
+@pytest.mark.parametrize("residual", [True, False])
+def test_dropout_of_the_branch(dim, residual, dtype):
+    x, res, w, dy, dh = make(350, dim, dtype, seed=dim)
+    res, dh = (res, dh) if residual else (None, None)
+    drop = dict(dropout=0.3, seed=2 ** 63 + 11, offset=4)
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, **drop)
+    check_forward(x, res, w, 1e-5, out, 0.3, 2 ** 63 + 11, 4)
+    got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh, **drop)
+    check_backward(dy, out[1], w, out[2], dh, got, 0.3, 2 ** 63 + 11, 4)
+
+
+def test_fp32_weight_of_bf16_rows():
+    x, res, w, dy, dh = make(65, 640, torch.bfloat16)
+    w = w.float() + 1e-3
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, fp8=True)
+    check_forward(x, res, w, 1e-5, out)
+    got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh)
+    assert got[2].dtype == torch.float32
+    check_backward(dy, out[1], w, out[2], dh, got)
+    assert rl.rms_norm_backward(dy, out[1], w, out[2], need_dweight=False)[2] is None
+
+
+def test_strided_heads_and_odd_addresses():
+    """The q heads of a fused q|k|v output, rows at odd addresses, a broadcast residual."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    qkv = torch.randn(50, 12, 80, generator=g, device=DEV).bfloat16()
+    w = torch.rand(80, generator=g, device=DEV).bfloat16()
+    q = qkv[:, 2:10]
+    out = rl.rms_norm_forward(q, w, eps=1e-6)
+    check_forward(q, None, w, 1e-6, out)
+    dy = torch.randn(50, 8, 80, generator=g, device=DEV).bfloat16()
+    dx = torch.zeros_like(qkv)
+    got = rl.rms_norm_backward(dy, q, w, out[2], dx=dx[:, 2:10])
+    check_backward(dy, q, w, out[2], None, (got[0], got[0], got[2]))
+    assert torch.all(dx[:, :2] == 0) and torch.all(dx[:, 10:] == 0)
+    flat = torch.randn(40 * 101 + 1, generator=g, device=DEV).bfloat16()
+    x = flat[1:].view(40, 101)[:, :80]
+    res = torch.randn(80, generator=g, device=DEV).bfloat16().expand(40, 80)
+    check_forward(x, res, w, 1e-6, rl.rms_norm_forward(x, w, residual=res, eps=1e-6))
+    with pytest.raises(ValueError):
+        rl.rms_norm_forward(qkv.view(5, 10, 12, 80)[:, :7, :5], w)
+    with pytest.raises(ValueError):
+        rl.rms_norm_forward(qkv.transpose(1, 2), w)
+
+
+def test_in_place():
+    x, res, w, dy, dh = make(33, 264, torch.bfloat16)
+    y, h, rstd = rl.rms_norm_forward(x, w, residual=res)
+    a, b = x.clone(), res.clone()
+    y2, h2, _ = rl.rms_norm_forward(a, w, residual=b, out=a, h_out=b)
+    assert y2 is a and h2 is b and torch.equal(a, y) and torch.equal(b, h)
+    dx, _, dw = rl.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    e = dh.clone()
+    dx2, _, dw2 = rl.rms_norm_backward(dy, h, w, rstd, dh=e, dx=e)
+    assert dx2 is e and torch.equal(e, dx) and torch.equal(dw, dw2)
+    with pytest.raises(ValueError):
+        rl.rms_norm_forward(x, w, h_out=b)
+    with pytest.raises(_lib.LoraError):
+        rl.rms_norm_forward(x, w, residual=res, out=a, h_out=a)
+
+
+def test_large_small_and_not_finite_rows():
+    dim = 512
+    x = torch.randn(6, dim, device=DEV)
+    x[0] *= 1e30            # the squares leave fp32
+    x[1] *= 1e-30           # eps decides
+    x[2] = 0
+    x[3, 5] = np.inf
+    x[4, 7] = np.nan
+    w = torch.ones(dim, device=DEV)
+    y, _, rstd, codes, scale = rl.rms_norm_forward(x, w, eps=1e-6, fp8=True)
+    want, r = on.forward(host(x[:3]), np.ones(dim), 1e-6)
+    assert np.all(np.abs(host(y[:3]) - want) <= 40 * F * np.abs(want) + 1e-38)
+    assert np.all(np.abs(rstd[:3].double().cpu().numpy() - r) <= 40 * F * r)
+    assert torch.all(y[2] == 0) and torch.all(codes[2] == 0) and scale[2] == 1
+    assert torch.isnan(y[3, 5]) and torch.all(y[3, :5] == 0)
+    assert torch.isnan(y[4]).all() and torch.isfinite(y[5]).all()
+    big = torch.full((2, 64), 3e38, device=DEV).bfloat16()
+    y = rl.rms_norm_forward(big, torch.ones(64, device=DEV).bfloat16(), eps=0.0)[0]
+    assert torch.all((y.float() - 1).abs() <= 2.0 ** -8)
+
+
+def test_autograd_matches_the_functions_and_differences():
+    x, res, w, dy, dh = make(20, 40, torch.float32)
+    leaves = [t.clone().requires_grad_() for t in (x, w, res)]
+    y, h = rl.rms_norm(leaves[0], leaves[1], residual=leaves[2], eps=1e-3, dropout=0.25, seed=5, offset=2)
+    ((y * dy).sum() + (h * dh).sum()).backward()
+    keep = torch.from_numpy(on.dropout(np.ones((20, 40)), 0.25, 5, 2)).to(DEV)
+    ref = [t.double().requires_grad_() for t in (x, w, res)]
+    h64 = ref[0] * keep + ref[2]
+    y64 = h64 * (h64.square().mean(-1, keepdim=True) + 1e-3).rsqrt() * ref[1]
+    ((y64 * dy.double()).sum() + (h64 * dh.double()).sum()).backward()
+    for a, b in zip(leaves, ref):
+        assert torch.allclose(a.grad.double(), b.grad, rtol=1e-5, atol=2e-5)
+    # only one of the outputs used
+    for pick in (0, 1):
+        for t in leaves:
+            t.grad = None
+        rl.rms_norm(leaves[0], leaves[1], residual=leaves[2])[pick].sum().backward()
+        assert all(torch.isfinite(t.grad).all() for t in leaves)
+    assert torch.equal(leaves[0].grad, torch.ones_like(x)) and torch.all(leaves[1].grad == 0)
+    # strides that the kernels do not take
+    z = torch.randn(40, 20, device=DEV).t().requires_grad_()
+    rl.rms_norm(z, leaves[1]).sum().backward()
+    assert z.grad.shape == z.shape
+    with pytest.raises(RuntimeError):
+        g, = torch.autograd.grad(rl.rms_norm(z, leaves[1]).sum(), z, create_graph=True)
+        g.sum().backward()
+
+
+def test_fp8_rows_feed_the_layer():
+    """norm -> fp8 layer: the layer on the norm's codes, against it on its own, which
+    quantises the rounded y: each within half a step of e4m3 of exact products."""
+    g = torch.Generator(device=DEV).manual_seed(8)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    x, res = r(300, 256).bfloat16(), r(300, 256).bfloat16()
+    w = (1 + 0.1 * r(256)).bfloat16()
+    W = rl.quantize_w_fp8((r(320, 256) / 16).bfloat16())
+    A, B = (r(16, 256) / 16).bfloat16().requires_grad_(), (r(320, 16) * 0.1).bfloat16().requires_grad_()
+    y, h, codes, scale = rl.rms_norm(x, w, residual=res, fp8=True)
+    got = rl.lora_linear_fp8(y, W, A, B, 32.0, rows=(codes, scale))
+    # the same codes through the layer's own quantiser's format
+    q = (codes.view(torch.float8_e4m3fn).float() * scale[:, None]).double()
+    Wd = W.Wq.view(torch.float8_e4m3fn).float().double() * W.w_scale.double()
+    want = q @ Wd.T + 2.0 * (y.double() @ A.double().T) @ B.double().T
+    assert float((got.double() - want).detach().abs().max() / want.detach().abs().max()) <= 1e-2
+    got.sum().backward()
+    ga = A.grad.clone()
+    A.grad = B.grad = None
+    rl.lora_linear_fp8(y, W, A, B, 32.0).sum().backward()
+    assert torch.equal(A.grad, ga)
+    plain, _ = rl.fp8_forward(y, W, A.detach(), B.detach(), 32.0, rows=rl.quantize_rows_fp8(y))
+    own, _ = rl.fp8_forward(y, W, A.detach(), B.detach(), 32.0)
+    assert torch.equal(plain, own)
+    with pytest.raises(ValueError):
+        rl.fp8_forward(y, W, A.detach(), B.detach(), 32.0, rows=(codes[:1], scale[:1]))
+    rl.device_status()
+
+
+def test_no_rows():
+    w = torch.ones(64, device=DEV)
+    x = torch.empty(0, 64, device=DEV)
+    y, h, rstd = rl.rms_norm_forward(x, w, residual=x)
+    dx, _, dw = rl.rms_norm_backward(x, h, w, rstd, dh=x)
+    assert y.shape == dx.shape == (0, 64) and torch.all(dw == 0)
+    with pytest.raises(TypeError):
+        rl.rms_norm_forward(x, w.double())
+    with pytest.raises(ValueError):
+        rl.rms_norm_forward(x, w[:32])
+
+
+def test_graph_replay_and_streams():
+    x, res, w, dy, dh = make(64, 512, torch.bfloat16)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y, h, rstd = rl.rms_norm_forward(x, w, residual=res)
+        rl.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y, h, rstd = rl.rms_norm_forward(x, w, residual=res)
+        dx, _, dw = rl.rms_norm_backward(dy, h, w, rstd, dh=dh)
+    x.mul_(1.5)
+    graph.replay()
+    y2, h2, rstd2 = rl.rms_norm_forward(x, w, residual=res)
+    want = rl.rms_norm_backward(dy, h2, w, rstd2, dh=dh)
+    assert torch.equal(y, y2) and torch.equal(dx, want[0]) and torch.equal(dw, want[2])
+    side.wait_stream(torch.cuda.current_stream())
+    y3, h3, rstd3 = rl.rms_norm_forward(x, w, residual=res, stream=side)
+    got = rl.rms_norm_backward(dy, h3, w, rstd3, dh=dh, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(y3, y2) and torch.equal(got[2], want[2])
