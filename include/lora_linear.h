@@ -214,7 +214,11 @@ typedef enum {
     LORA_K_ATTN_TOKEN = 18,     /* attention: one new token over a cache     */
     LORA_K_NORM = 19,           /* root-mean-square norm                     */
     LORA_K_NORM_BWD = 20,       /* its gradients                             */
-    LORA_K_DROPOUT = 21         /* dropout                                   */
+    LORA_K_DROPOUT = 21,        /* dropout                                   */
+    LORA_K_LOSS_PREP = 22,      /* loss: tokens that count, target logits    */
+    LORA_K_LOSS_LOGITS = 23,    /* loss: exponentials of the logits          */
+    LORA_K_LOSS_ROWS = 24,      /* loss: sums, losses, scaling               */
+    LORA_K_LOSS_GRAD = 25       /* loss: gradient of the hidden states       */
 } lora_kernel_kind_t;
 
 /*

@@ -16,13 +16,16 @@ from .attention import (AttentionFunction, attention, attention_backward, attent
                         attention_forward)
 from .clip import GradClip
 from .dropout import DropoutFunction, dropout, dropout_backward, dropout_forward
+from .loss import (CrossEntropyFunction, cross_entropy, cross_entropy_backward,
+                   cross_entropy_forward)
 from .norm import RMSNormFunction, rms_norm, rms_norm_backward, rms_norm_forward
 from .rotary import (RotaryFrequencies, RotaryFunction, rotary, rotary_backward, rotary_forward,
                      rotary_frequencies)
 
 __all__ = ["AttentionFunction", "attention", "attention_backward", "attention_decode",
            "attention_forward", "DropoutFunction", "dropout", "dropout_backward", "dropout_forward",
-           "RMSNormFunction", "rms_norm", "rms_norm_backward", "rms_norm_forward", "GradClip", "RotaryFrequencies", "RotaryFunction", "rotary",
+           "CrossEntropyFunction", "cross_entropy", "cross_entropy_backward",
+           "cross_entropy_forward", "RMSNormFunction", "rms_norm", "rms_norm_backward", "rms_norm_forward", "GradClip", "RotaryFrequencies", "RotaryFunction", "rotary",
            "rotary_backward", "rotary_forward", "rotary_frequencies",
            "FP8Weight", "Q4Weight", "dequantize_w_q4", "q4_backward", "q4_forward",
            "quantize_w_q4", "LoRAFP8Function", "LoRAQ4Function", "lora_linear_fp8",

@@ -18,7 +18,7 @@ LORA_BF16, LORA_FP32 = 0, 1
 KERNEL_KINDS = ["prep", "down_fwd", "main_fwd", "down_bwd", "main_bwd", "grad_a", "grad_b",
                 "down_bwd_grad_b", "swiglu_grad", "quant", "grad_a_b", "rotary", "grad_norm",
                 "grad_clip", "attn_prep", "attn_fwd", "attn_dq", "attn_dkv", "attn_token", "norm",
-                "norm_bwd", "dropout"]
+                "norm_bwd", "dropout", "loss_prep", "loss_logits", "loss_rows", "loss_grad"]
 
 _vp, _i64, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t
 _int, _f32 = ctypes.c_int, ctypes.c_float
@@ -62,6 +62,12 @@ class NormShape(ctypes.Structure):
                 ("eps", _f32), ("x", _i64 * 2), ("residual", _i64 * 2), ("h", _i64 * 2),
                 ("y", _i64 * 2), ("dy", _i64 * 2), ("dh", _i64 * 2), ("dx", _i64 * 2),
                 ("dresidual", _i64 * 2)]
+
+
+class LossShape(ctypes.Structure):
+    """lora_loss_t"""
+    _fields_ = [("rows", _i64), ("vocab", _i64), ("dim", _i32), ("target_bits", _i32),
+                ("mean", _i32), ("softcap", _f32), ("x", _i64), ("w", _i64), ("dx", _i64)]
 
 
 SIGNATURES = {
@@ -120,6 +126,9 @@ SIGNATURES = {
     "lora_norm_workspace_bytes": ([_vp, _int], _sz),
     "lora_norm_bwd": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp, _sz, _vp],
                       _int),
+    "lora_loss_workspace_bytes": ([_vp, _int], _sz),
+    "lora_loss": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "lora_loss_scale": ([_vp, _vp, _vp, _vp, _vp], _int),
     "lora_attention_token": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
 }
 
