@@ -42,10 +42,10 @@ __device__ __forceinline__ void place(const Args &a, int64_t item, int64_t &row,
 // Rows of whole, aligned vectors of eight: each thread has kItems of them in
 // flight before it makes their masks.
 template <class T, int kItems>
-__global__ void __launch_bounds__(kThreads) k_dropout(Args a) {
+__global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ Args a) {
   griddep_wait();
   griddep_launch_dependents();
-  drop_resolve(a.drop);
+  const DropNow now = drop_now(a.drop);
   Raw8<T> in[kItems];
   int64_t row[kItems];
   uint32_t v[kItems];
@@ -55,25 +55,28 @@ __global__ void __launch_bounds__(kThreads) k_dropout(Args a) {
     const int64_t item = first + j * kThreads;
     if (item < a.total) {
       place(a, item, row[j], v[j]);
-      load_raw(static_cast<const T *>(a.x) + row[j] * a.xs + int64_t(v[j]) * 8, in[j]);
+      in[j].load(static_cast<const T *>(a.x) + row[j] * a.xs + int64_t(v[j]) * 8);
     }
   }
 #pragma unroll
   for (int j = 0; j < kItems; ++j) {
     if (first + j * kThreads >= a.total) break;
-    float f[8];
-    unpack(in[j], f);
-    drop8(a.drop, v[j], row[j], f);
-    store8(static_cast<T *>(a.y) + row[j] * a.ys + int64_t(v[j]) * 8, f);
+    float2 f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = in[j].pair(i);
+    drop8(a.drop, now, v[j], row[j], f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) in[j].set(i, f[i]);
+    in[j].store(static_cast<T *>(a.y) + row[j] * a.ys + int64_t(v[j]) * 8);
   }
 }
 
 // Any width and alignment: four columns (one Philox call) a thread.
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_dropout_any(Args a) {
+__global__ void __launch_bounds__(kThreads) k_dropout_any(const __grid_constant__ Args a) {
   griddep_wait();
   griddep_launch_dependents();
-  drop_resolve(a.drop);
+  const DropNow now = drop_now(a.drop);
   const int64_t item = int64_t(blockIdx.x) * kThreads + threadIdx.x;
   if (item >= a.total) return;
   int64_t row;
@@ -85,10 +88,10 @@ __global__ void __launch_bounds__(kThreads) k_dropout_any(Args a) {
   float f[4];
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i) f[i] = i < n ? to_f32(x[i]) : 0.f;
-  const uint4 w = drop_words(a.drop, b, row);
+  const uint4 w = drop_words(a.drop, now, b, row);
 #pragma unroll
   for (uint32_t i = 0; i < 4; ++i)
-    if (i < n) y[i] = from_f32<T>(word_of(w, i) >= a.drop.threshold ? f[i] * a.drop.scale : 0.f);
+    if (i < n) y[i] = from_f32<T>(drop1(a.drop, word_of(w, i), f[i]));
 }
 
 template <class T>
@@ -120,6 +123,7 @@ lora_status_t drop_args(const lora_dropout_t *d, DropArgs &out) {
   out.seed = d->seed;
   out.offset = d->offset;
   out.state = d->state;
+  drop_keys(out);
   return LORA_OK;
 }
 
