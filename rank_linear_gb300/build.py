@@ -18,7 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "liblora_linear.so")
 SOURCES = ["lora_api.cu", "tc_main.cu", "tc_skinny.cu", "simt.cu", "rotary.cu", "clip.cu",
-           "attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_token.cu", "dropout.cu", "norm.cu",
+           "attn_api.cu", "attn_fwd.cu", "attn_bwd.cu", "attn_token.cu", "dropout.cu", "norm.cu", "norm_fwd.cu", "norm_bwd.cu",
            "loss.cu", "loss_gemm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",

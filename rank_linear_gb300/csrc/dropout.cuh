@@ -56,16 +56,21 @@ __device__ __forceinline__ uint4 philox10(uint32_t c0, uint32_t c1, uint32_t c2,
   return make_uint4(c0, c1, c2, c3);
 }
 
-// The four words of columns 4 b .. 4 b + 3 of a row.
+// The four words of columns 4 b .. 4 b + 3 of a row.  (Where the seed comes from
+// memory the keys are added up, in a function of its own: one copy of the code.)
+static __device__ __noinline__ uint4 drop_words_of(uint64_t seed, uint32_t b, uint32_t lo, uint32_t hi,
+                                            uint32_t offset) {
+  const uint32_t k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
+  return philox10(b, lo, hi, offset, [&](int i) {
+    return i & 1 ? k1 + 0xBB67AE85u * (i >> 1) : k0 + 0x9E3779B9u * (i >> 1);
+  });
+}
 __device__ __forceinline__ uint4 drop_words(const DropArgs &d, const DropNow &now, uint32_t b,
                                             int64_t row) {
   const uint32_t lo = static_cast<uint32_t>(row), hi = static_cast<uint32_t>(uint64_t(row) >> 32);
   if (d.state == nullptr)
     return philox10(b, lo, hi, now.offset, [&](int i) { return d.keys[i]; });
-  const uint32_t k0 = static_cast<uint32_t>(now.seed), k1 = static_cast<uint32_t>(now.seed >> 32);
-  return philox10(b, lo, hi, now.offset, [&](int i) {
-    return i & 1 ? k1 + 0xBB67AE85u * (i >> 1) : k0 + 0x9E3779B9u * (i >> 1);
-  });
+  return drop_words_of(now.seed, b, lo, hi, now.offset);
 }
 __device__ __forceinline__ float drop1(const DropArgs &d, uint32_t word, float x) {
   return word >= d.threshold ? x * d.scale : 0.f;

@@ -116,25 +116,29 @@ struct Strip {
   int *target;
 };
 
-// A warp a token of the strip: X's row copied beside the others, z = c(x . W_t)
+// W warps a token of the strip: X's row copied beside the others, z = c(x . W_t)
 // in fp32; and a line of zeros for each token that does not count among those at
-// the strip's places.
+// the strip's places.  (Few tokens: a block each, so that a row's loads are all on
+// their way at once.)
+template <int W>
 __global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, Strip st,
                                                      const __nv_bfloat16 *__restrict__ w, int64_t ldw,
                                                      int64_t vocab, const __nv_bfloat16 *x,
                                                      int64_t ldx, __nv_bfloat16 *__restrict__ xs,
                                                      __nv_bfloat16 *dx, int64_t lddx, int dim,
                                                      float cap) {
+  __shared__ float sums[8];
   griddep_wait();
   griddep_launch_dependents();
-  const int lane = threadIdx.x & 31;
-  const int i = blockIdx.x * 8 + (threadIdx.x >> 5);
+  constexpr int T = 32 * W;  // threads of a token
+  const int lane = threadIdx.x % T;
+  const int i = blockIdx.x * (8 / W) + threadIdx.x / T;
   const int64_t n0 = int64_t(st.first) + i;  // a token by its own number
   if (dx != nullptr && n0 < tk.rows && tk.target(n0) < 0) {
     uint4 *o = reinterpret_cast<uint4 *>(dx + n0 * lddx);
-    for (int c = lane; c < dim / 8; c += 32) o[c] = make_uint4(0u, 0u, 0u, 0u);
+    for (int c = lane; c < dim / 8; c += T) o[c] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (i >= st.rows || n0 >= st.head->live) return;
+  if (i >= st.rows || n0 >= st.head->live) return;  // the same in a token's threads
   const int64_t n = st.live[i], t = tk.target(n);
   const bool known = t < vocab;
   const uint4 *xr = reinterpret_cast<const uint4 *>(x + n * ldx);
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, Strip st,
   uint4 *out = reinterpret_cast<uint4 *>(xs + int64_t(i) * dim);
   float s = 0.f;
 #pragma unroll 4
-  for (int c = lane; c < dim / 8; c += 32) {
+  for (int c = lane; c < dim / 8; c += T) {
     const uint4 a = xr[c], b = wr[c];
     out[c] = a;
     const uint32_t p[4] = {a.x, a.y, a.z, a.w}, q[4] = {b.x, b.y, b.z, b.w};
@@ -154,6 +158,13 @@ __global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, Strip st,
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if constexpr (W > 1) {
+    if ((threadIdx.x & 31) == 0) sums[threadIdx.x >> 5] = s;
+    __syncthreads();  // W = 8: the block is one token's
+    s = 0.f;
+#pragma unroll
+    for (int k = 0; k < W; ++k) s += sums[k];
+  }
   if (lane == 0) {
     float slope = 1.f;
     if (cap > 0.f) s = loss_cap(s, cap, 1.f / cap, slope);
@@ -181,7 +192,7 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
   {
     float s = 0.f, m = 0.f;
     const LossPart *p = parts + i0 + lane;
-#pragma unroll 4
+#pragma unroll 8
     for (int k = warp; k < pieces; k += 32) {
       const LossPart u = p[int64_t(k) * st.rows];
       if (u.up == m) {
@@ -424,8 +435,12 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
     s.scale = reinterpret_cast<float *>(at(workspace, p.scale));
     s.target = reinterpret_cast<int *>(at(workspace, p.target));
     LORA_TRY(run(LORA_K_LOSS_PREP, st, "loss gather", [&] {
-      return launch_pdl(k_loss_gather, dim3(p.strip / 8), dim3(256), 0, st, tk, s, w, ldw, sh->vocab, x,
-                        ldx, xs, static_cast<__nv_bfloat16 *>(dX), lddx, int(sh->dim), sh->softcap);
+      const int64_t here = sh->rows - first < p.strip ? sh->rows - first : p.strip;
+      const bool few = here <= 4 * di.sms;
+      return launch_pdl(few ? k_loss_gather<8> : k_loss_gather<1>,
+                        dim3(static_cast<unsigned>(few ? here : (here + 7) / 8)), dim3(256), 0, st, tk, s,
+                        w, ldw, sh->vocab, x, ldx, xs, static_cast<__nv_bfloat16 *>(dX), lddx,
+                        int(sh->dim), sh->softcap);
     }));
     LossGemm g;
     LORA_TRY(map2d(&g.a, xs, sh->dim, p.strip, sh->dim, 64, 128, "X"));
@@ -448,7 +463,8 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
     LORA_TRY(run(LORA_K_LOSS_LOGITS, st, "loss logits",
                  [&] { return launch_loss_gemm(grad ? 1 : 0, g, pairs, st); }));
     LORA_TRY(run(LORA_K_LOSS_ROWS, st, "loss rows", [&] {
-      return launch_pdl(k_loss_rows, dim3(p.strip / 32), dim3(1024), 0, st, tk, s, parts, p.pieces, e,
+      const int64_t here = sh->rows - first < p.strip ? sh->rows - first : p.strip;
+      return launch_pdl(k_loss_rows, dim3(static_cast<unsigned>((here + 31) / 32)), dim3(1024), 0, st, tk, s, parts, p.pieces, e,
                         p.lde, int(sh->vocab), losses);
     }));
     if (!grad) continue;

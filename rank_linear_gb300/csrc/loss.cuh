@@ -98,6 +98,21 @@ __host__ __device__ inline bool loss_item(const LossShare &s, int pair, int i, i
   if (s.cuts > 1) slot = rel * s.cuts + c;
   return true;
 }
+// The first product's items: whole tiles in rounds of the pairs; where at most half
+// the pairs have one in the last round, they are taken as two halves of 256 columns
+// each.  half: 0 or 1, or -1 for a whole tile.
+__host__ __device__ inline bool loss_first_item(int tiles, int pairs, int pair, int i, int &tile,
+                                                int &half) {
+  const int rounds = tiles / pairs, rest = tiles % pairs;
+  half = -1;
+  if (i < rounds || 2 * rest > pairs) {
+    tile = i * pairs + pair;
+    return tile < tiles;
+  }
+  tile = rounds * pairs + (pair >> 1);
+  half = pair & 1;
+  return i == rounds && pair < 2 * rest;
+}
 // Tiles of a round share few panels: the rows vary fastest, in groups.
 __host__ __device__ inline void loss_tile(int tile, int m_pairs, int n_tiles, int group, int &mp,
                                           int &nb) {

@@ -34,7 +34,6 @@ constexpr int CLUSTER = 2;
 constexpr uint16_t PAIR_MASK = 0x3;
 constexpr uint32_t A_BYTES = BM * BK * 2, B_HALF = BN / 2 * BK * 2, B_BYTES = 2 * B_HALF;
 constexpr uint32_t STAGE_BYTES = A_BYTES + B_BYTES;  // 48 KB
-constexpr uint32_t PAIR_TX = CLUSTER * STAGE_BYTES, CTA_TX = STAGE_BYTES;
 constexpr int STAGES = 4;
 constexpr uint32_t TMEM_COLS = 2 * BN;
 constexpr int EPI_WARPS = 8, THREADS = 64 + 32 * EPI_WARPS;
@@ -186,24 +185,19 @@ __global__ void __launch_bounds__(THREADS, 1)
   const uint32_t tmem_base = tail->tmem_base;
   griddep_wait();  // the tokens that count, and what the kernels before wrote
   fence_proxy_async_global();  // ... for the copies that this thread issues
+  griddep_launch_dependents();  // (the next kernel waits for this one's end itself)
 
   const int M = max(0, min(g.strip, g.head->live - g.first));
   const int m_pairs = (M + kLossTileM - 1) / kLossTileM, n_tiles = (g.n + TN - 1) / TN;
   const int kb_total = (g.k + BK - 1) / BK;
-  LossShare share;
-  if constexpr (GRAD) {
-    share = loss_share(m_pairs * n_tiles, num_pairs, kb_total);
-  } else {  // many tiles: whole ones
-    share = {m_pairs * n_tiles, num_pairs, 0, 0, 1, kb_total, 0};
-  }
-  // item i of this pair
-  auto item = [&](int i, int &tile, int &lo, int &hi, int &slot) -> bool {
-    if constexpr (GRAD) return loss_item(share, pair_id, i, kb_total, tile, lo, hi, slot);
-    tile = i * num_pairs + pair_id;
+  const LossShare share = loss_share(m_pairs * n_tiles, num_pairs, kb_total);
+  // item i of this pair; part: of the second product the slot of a range, of the
+  // first the half of a tile (-1: none, it is a whole one)
+  auto item = [&](int i, int &tile, int &lo, int &hi, int &part) -> bool {
+    if constexpr (GRAD) return loss_item(share, pair_id, i, kb_total, tile, lo, hi, part);
     lo = 0;
     hi = kb_total;
-    slot = -1;
-    return tile < share.tiles;
+    return loss_first_item(share.tiles, num_pairs, pair_id, i, tile, part);
   };
 
   if (warp == 0) {
@@ -214,11 +208,14 @@ __global__ void __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      int tile, lo, hi, slot;
-      for (int i = 0; ok && item(i, tile, lo, hi, slot); ++i) {
+      int tile, lo, hi, part;
+      uint32_t tx = STAGE_BYTES;  // what each CTA brings to a stage of the item
+      for (int i = 0; ok && item(i, tile, lo, hi, part); ++i) {
         int mp, nb;
         loss_tile(tile, m_pairs, n_tiles, g.group, mp, nb);
-        const int m0 = (2 * mp + q) * BM, n0 = nb * TN + q * (BN / 2);
+        const bool narrow = !GRAD && part >= 0;  // half a tile: it takes the first half's place
+        const int m0 = (2 * mp + q) * BM, n0 = nb * TN + q * (BN / 2) + (narrow ? part * BN : 0);
+        if (narrow) tx = A_BYTES + B_HALF;
         for (int kb = lo; kb < hi; ++kb) {
           if (!mbar_wait(smem_u32(&tail->empty[stage]), phase ^ 1u, abort_flag, g.dev_status)) {
             ok = false;
@@ -226,11 +223,12 @@ __global__ void __launch_bounds__(THREADS, 1)
           }
           const uint32_t full_local = smem_u32(&tail->full[stage]);
           const uint32_t full = dsmem_map(full_local, 0);
-          if (leader) mbar_expect_tx(full_local, PAIR_TX);
+          if (leader) mbar_expect_tx(full_local, CLUSTER * tx);
           const int k0 = kb * BK;
           tma_load_2d_pair(sA + stage * A_BYTES, &g.a, full, k0, m0);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
+            if (h == 1 && narrow) break;
             const uint32_t dst = sB + stage * B_BYTES + h * B_HALF;
             if constexpr (GRAD) {
 #pragma unroll
@@ -259,8 +257,8 @@ __global__ void __launch_bounds__(THREADS, 1)
       // Both CTAs' copies complete on the even CTA's barriers.  The odd CTA
       // hands over how often it filled each stage and, when aborting, stays
       // until the even CTA, which settles the phases that only one of them
-      // armed or filled (their counts differ by one at most), has seen every
-      // copy land.
+      // armed or filled (their counts differ by one at most; such a phase is one
+      // of the item that the even CTA is at), has seen every copy land.
       if (!leader) {
         const uint32_t pi = smem_u32(tail->peer_issued);
         for (int s = 0; s < STAGES; ++s) dsmem_st_u32(dsmem_map(pi + 4u * s, 0), issued[s]);
@@ -277,9 +275,9 @@ __global__ void __launch_bounds__(THREADS, 1)
             if (n == 0) continue;
             const uint32_t fs = smem_u32(&tail->full[s]);
             if (e == o + 1)
-              mbar_complete_tx(fs, CTA_TX);
+              mbar_complete_tx(fs, tx);
             else if (o == e + 1)
-              mbar_expect_tx(fs, CTA_TX);
+              mbar_expect_tx(fs, tx);
             mbar_wait_drain(fs, (n - 1u) & 1u);
           }
         }
@@ -301,8 +299,9 @@ __global__ void __launch_bounds__(THREADS, 1)
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
-      int tile, lo, hi, slot;
-      for (int i = 0; ok && item(i, tile, lo, hi, slot); ++i) {
+      int tile, lo, hi, part;
+      for (int i = 0; ok && item(i, tile, lo, hi, part); ++i) {
+        const bool narrow = !GRAD && part >= 0;
         const uint32_t free = (static_cast<uint32_t>(i) & 1u) ^ 1u;
         if (!mbar_wait(smem_u32(&tail->tempty[0]), free, abort_flag, g.dev_status)) {
           ok = false;
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(THREADS, 1)
           issue(tmem_base, ad, bd, accum);
           accum = 1u;
           bool hold = false;
-          if (!half1_free) {
+          if (!narrow && !half1_free) {
             if (deferred + 1 < STAGES && kb + 1 < hi && !mbar_peek(smem_u32(&tail->tempty[1]), free)) {
               ++deferred;
               hold = true;
@@ -346,7 +345,7 @@ __global__ void __launch_bounds__(THREADS, 1)
             }
           }
           if (!hold) {
-            issue(tmem_base + BN, ad, bd + (B_HALF >> 4), accum1);
+            if (!narrow) issue(tmem_base + BN, ad, bd + (B_HALF >> 4), accum1);
             accum1 = 1u;
             tc_commit_pair_mc(smem_u32(&tail->empty[stage]), PAIR_MASK);
           }
@@ -372,10 +371,11 @@ __global__ void __launch_bounds__(THREADS, 1)
     const int qd = warp & 3, cpart = (warp - 2) >> 2;  // lane quadrant; which 128 columns of a half
     uint8_t *stage = epi_stage + (warp - 2) * EPI_WARP_BYTES;
     const float inv_cap = CAP ? 1.f / g.cap : 0.f;
-    int tile, lo, hi, slot;
-    for (int i = 0; item(i, tile, lo, hi, slot); ++i) {
+    int tile, lo, hi, part;
+    for (int i = 0; item(i, tile, lo, hi, part); ++i) {
       int mp, nb;
       loss_tile(tile, m_pairs, n_tiles, g.group, mp, nb);
+      const bool narrow = !GRAD && part >= 0;
       const int rl = qd * 32 + lane;  // row of this CTA's 128
       const int row0 = (2 * mp + q) * BM + qd * 32, row = row0 + lane;
       float ref = 0.f;  // first product: the row's reference; second: its factor
@@ -391,18 +391,23 @@ __global__ void __launch_bounds__(THREADS, 1)
       const uint32_t taddr = tmem_base + (static_cast<uint32_t>(qd * 32) << 16);
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        const int c0 = h * BN + cpart * kLossPiece;  // first column within the tile
+        if (narrow && h == 1) {  // (nothing there: the barrier's phases go on)
+          if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_u32(&tail->tempty[1]), 0));
+          break;
+        }
+        // first column within the tile, and where it is in TMEM
+        const int c0 = (narrow ? part : h) * BN + cpart * kLossPiece, at = h * BN + cpart * kLossPiece;
         float v[kLossPiece];
 #pragma unroll
         for (int c = 0; c < kLossPiece / 32; ++c)
-          tmem_ld_32cols(taddr + c0 + c * 32, *reinterpret_cast<float(*)[32]>(v + c * 32));
+          tmem_ld_32cols(taddr + at + c * 32, *reinterpret_cast<float(*)[32]>(v + c * 32));
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_u32(&tail->tempty[h]), 0));
         const int col0 = nb * TN + c0;
         if constexpr (!GRAD) {
           const LossPart p = exponentials<CAP>(v, ref, target, col0, g.n, g.cap, inv_cap);
-          g.parts[int64_t(nb * (TN / kLossPiece) + h * 2 + cpart) * g.strip + row] = p;
+          g.parts[int64_t((nb * TN + c0) / kLossPiece) * g.strip + row] = p;
           if constexpr (KIND == 1) {
 #pragma unroll
             for (int c = 0; c < 2; ++c) {  // a box of 32 x 64 each, cut at the vocabulary's end
@@ -417,9 +422,9 @@ __global__ void __launch_bounds__(THREADS, 1)
               }
             }
           }
-        } else if (slot >= 0) {
+        } else if (part >= 0) {
           // a range: the fp32 sums, column by column of 128 rows
-          float *out = g.slots + size_t(slot) * kLossSlotFloats + size_t(q) * (BM * TN) + rl;
+          float *out = g.slots + size_t(part) * kLossSlotFloats + size_t(q) * (BM * TN) + rl;
 #pragma unroll
           for (int c = 0; c < kLossPiece; ++c) out[(c0 + c) * BM] = v[c];
         } else {
@@ -456,12 +461,16 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Ranges of the second product -> dX: a block takes 32 rows and 64 columns of a
-// cut tile, adds the ranges in their order and writes whole 128-byte lines.
-constexpr int JOIN_COLS = 64, JOIN_ROWS = 32;
+// Ranges of the second product -> dX: a block takes 32 rows and 32 columns of a
+// cut tile, a thread four of them over all ranges (in their order, eight loads of
+// each four on their way), and writes whole 64-byte pieces.  (64 columns a block
+// left most SMs idle where there are few tiles and many ranges: 20 us for 31 ranges
+// of 2 tiles.)
+constexpr int JOIN_COLS = 32, JOIN_ROWS = 32;
 __global__ void __launch_bounds__(256) k_loss_join(const __grid_constant__ LossGemm g, int pairs) {
   __shared__ float sums[JOIN_COLS][JOIN_ROWS + 1];
   griddep_wait();
+  griddep_launch_dependents();
   const int M = max(0, min(g.strip, g.head->live - g.first));
   const int m_pairs = (M + kLossTileM - 1) / kLossTileM, n_tiles = (g.n + TN - 1) / TN;
   const int kb = (g.k + BK - 1) / BK;
@@ -484,24 +493,20 @@ __global__ void __launch_bounds__(256) k_loss_join(const __grid_constant__ LossG
     float s[JOIN_COLS / 8];
 #pragma unroll
     for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] = 0.f;
-    for (int k = 0; k < ranges; ++k, in += kLossSlotFloats)
+#pragma unroll 8
+    for (int k = 0; k < ranges; ++k)
 #pragma unroll
-      for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] += in[(j * 8 + w) * BM];
+      for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] += in[k * kLossSlotFloats + (j * 8 + w) * BM];
     const float f = row0 + lane < M ? g.scale[row0 + lane] : 0.f;
     __syncthreads();  // the last unit's sums are out
 #pragma unroll
     for (int j = 0; j < JOIN_COLS / 8; ++j) sums[j * 8 + w][lane] = s[j] * f;
     __syncthreads();
-    // eight threads a row, eight columns each
-    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 8;
-    if (row0 + r < M && col0 + c < g.n) {
-      uint4 o;
-      o.x = pack2(sums[c][r], sums[c + 1][r]);
-      o.y = pack2(sums[c + 2][r], sums[c + 3][r]);
-      o.z = pack2(sums[c + 4][r], sums[c + 5][r]);
-      o.w = pack2(sums[c + 6][r], sums[c + 7][r]);
-      *reinterpret_cast<uint4 *>(g.out + int64_t(g.place[row0 + r]) * g.ldo + col0 + c) = o;
-    }
+    // eight threads a row, four columns each
+    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+    if (row0 + r < M && col0 + c < g.n)  // n is a multiple of 8
+      *reinterpret_cast<uint2 *>(g.out + int64_t(g.place[row0 + r]) * g.ldo + col0 + c) =
+          make_uint2(pack2(sums[c][r], sums[c + 1][r]), pack2(sums[c + 2][r], sums[c + 3][r]));
   }
 }
 

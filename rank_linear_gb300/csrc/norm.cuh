@@ -1,0 +1,390 @@
+// norm.cuh -- what the norm's kernels share: a row's elements among its threads,
+// sums over them, the weight, and the ring of bulk copies (norm_fwd.cu,
+// norm_bwd.cu; norm.cu has the C entry points).
+#pragma once
+
+#include "dropout.cuh"
+#include "host.h"
+#include "ptx.cuh"
+
+namespace lora {
+
+constexpr int kMaxDim = 32768;  // 1024 threads x 4 vectors x 8
+constexpr int kSmallBlock = 128;  // threads of a block where a group is a warp or less
+
+struct NormRows {  // where row r begins
+  int64_t outer, inner;
+};
+
+// The addresses between which a tensor's elements lie.
+struct NormSpan {
+  uint64_t first, last;
+};
+
+struct NormFwdArgs {
+  const void *x, *res, *w;
+  void *h, *y;
+  float *rstd, *scale;
+  uint8_t *codes;
+  NormRows sx, sr, sh, sy;
+  NormSpan span_x, span_r;
+  int64_t rows;
+  uint32_t inner;  // rows an outer entry
+  int dim, group, w32;
+  float eps;
+  int dropped;
+  DropArgs drop;
+};
+
+struct NormBwdArgs {
+  const void *dy, *h, *w, *dh;
+  const float *rstd;
+  void *dx, *dres;
+  float *partial;  // [blocks][dim], or null
+  NormRows sdy, sh, sdh, sdx, sdr;
+  NormSpan span_y, span_h, span_d;
+  int64_t rows;
+  uint32_t inner;
+  int dim, group, w32;
+  int dropped;
+  DropArgs drop;
+};
+
+// At the start of a ring's shared memory.
+struct RingHead {
+  uint64_t full[4];
+  int abort_flag;
+};
+constexpr int kRingHead = 64;
+
+// Vectors a thread: as many as its registers hold (the forward's 80, the
+// backward's 128); the fewer threads a row, the fewer instructions it takes to
+// add up their sums.
+__host__ __device__ constexpr int ring_vectors(int es) { return es == 2 ? 4 : 2; }
+
+// How a call runs.
+struct NormSplit {
+  bool ring;
+  int group, vpt, nr, block, per_block;  // threads and vectors of a row; rows at a time
+  int stages, blocks_sm;                 // of the ring
+  uint32_t buffer;                       // bytes of a row in the ring
+};
+constexpr int kSms = 152;
+constexpr int kRingSmem = 220 * 1024;  // of an SM's, left to its blocks' rings
+// Threads of the ring's blocks on an SM: what their registers (80 a thread forward,
+// 128 backward) leave room for.
+constexpr int kFwdThreads = 768, kBwdThreads = 512;
+
+// Few rows (two an SM at most): as many threads as there are vectors.
+inline bool norm_few_rows(int64_t rows) { return rows <= 2 * kSms; }
+
+// tensors: that are read a row; threads: of an SM.
+inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, int threads_sm, bool codes = false) {
+  const bool wide_codes = codes && es == 4;  // (codes of fp32 rows: not over the ring)
+  NormSplit s = {};
+  const int vectors = (dim + 7) / 8;
+  s.nr = 1;
+  if (norm_few_rows(rows) && vectors <= 1024) {
+    s.vpt = 1;
+  } else if (dim > 1024) {
+    s.vpt = ring_vectors(es);
+    s.group = s.block = ((vectors + s.vpt - 1) / s.vpt + 31) / 32 * 32;
+    s.per_block = 1;
+    // (a row may begin and end inside 16 bytes)
+    s.buffer = static_cast<uint32_t>((dim * es + 15) / 16 * 16 + 16);
+    const int stage = static_cast<int>(s.buffer) * tensors;
+    s.blocks_sm = s.block > 512 ? 1 : s.block > 256 ? 1 : threads_sm / s.block;
+    if (s.blocks_sm > 8) s.blocks_sm = 8;
+    for (; s.blocks_sm > 0; --s.blocks_sm) {
+      s.stages = (kRingSmem / s.blocks_sm - 1024 - kRingHead) / stage;
+      if (s.stages >= 2) break;
+    }
+    s.ring = s.blocks_sm > 0 && s.block <= 512 && !wide_codes;
+    if (s.stages > 4) s.stages = 4;
+    if (s.ring) return s;
+    s.vpt = 4;
+  } else {
+    s.vpt = vectors > 32 ? 4 : 1;
+    if (s.vpt == 1) s.nr = 4;
+  }
+  const int threads = (vectors + s.vpt - 1) / s.vpt;
+  if (threads <= 32) {
+    s.group = 1;
+    while (s.group < threads) s.group *= 2;
+    s.block = kSmallBlock;
+  } else {
+    s.group = s.block = (threads + 31) / 32 * 32;
+  }
+  s.per_block = s.block / s.group * s.nr;
+  return s;
+}
+
+// Blocks of the backward, each with a line of partial sums.
+inline int norm_bwd_blocks(const NormSplit &s, int64_t rows) {
+  const int64_t n = (rows + s.per_block - 1) / s.per_block;
+  const int most = kSms * (s.ring ? s.blocks_sm : 4);
+  return static_cast<int>(n < most ? n : most);
+}
+
+cudaError_t launch_norm_fwd(lora_dtype_t dtype, bool vec, const NormFwdArgs &a, const NormSplit &s, int tensors,
+                            unsigned *status, cudaStream_t st);
+cudaError_t launch_norm_bwd(lora_dtype_t dtype, bool vec, const NormBwdArgs &a, const NormSplit &s, int tensors,
+                            unsigned *status, cudaStream_t st);
+// dw from the blocks' lines of sums (fp32: of that type, else bf16).
+cudaError_t launch_norm_dw(bool fp32, const float *partial, int blocks, int dim, void *dw, cudaStream_t st);
+
+namespace {
+
+struct Where {
+  int64_t o, i;
+  __device__ __forceinline__ int64_t at(const NormRows &s) const { return o * s.outer + i * s.inner; }
+};
+__device__ __forceinline__ Where where(int64_t row, uint32_t inner) {
+  if (inner == 1) return {row, 0};
+  const uint32_t r = static_cast<uint32_t>(row);  // below 2^31
+  return {static_cast<int64_t>(r / inner), static_cast<int64_t>(r % inner)};
+}
+
+// A row belongs to `group` threads, VPT vectors of eight elements each.  Aligned
+// rows (AL): eight that lie side by side (vector t + j group).  Others: eight that
+// lie `group` apart, so that a warp's accesses cover neighbours.
+template <bool AL>
+__device__ __forceinline__ int element(int t, int group, int j, int k) {
+  return AL ? (t + j * group) * 8 + k : (j * 8 + k) * group + t;
+}
+// Thread t's vectors of a row of `dim` elements at p; zeros past its end.
+template <bool AL, class T, int VPT>
+__device__ __forceinline__ void fetch(Raw8<T> (&v)[VPT], const T *p, int t, int group, int dim) {
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    if constexpr (AL) {
+      const int c = (t + j * group) * 8;
+      if (c < dim) {
+        v[j].load(p + c);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[j].set(i, both(0.f));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = element<false>(t, group, j, k);
+        if (k % 2 == 0) v[j].set(k / 2, both(0.f));
+        if (c < dim) v[j].load1(k, p + c);
+      }
+    }
+  }
+}
+template <bool AL, class T>
+__device__ __forceinline__ void put(T *p, const Raw8<T> &v, int t, int group, int j, int dim) {
+  if constexpr (AL) {
+    const int c = (t + j * group) * 8;
+    if (c < dim) v.store(p + c);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = element<false>(t, group, j, k);
+      if (c < dim) v.store1(k, p + c);
+    }
+  }
+}
+template <bool AL, class T>
+__device__ __forceinline__ void put(T *p, const float2 (&v)[4], int t, int group, int j, int dim) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.set(i, v[i]);
+  put<AL>(p, r, t, group, j, dim);
+}
+// Drops out vector j.  Where a thread's elements lie `group` apart (a multiple of
+// 32), a warp's 32 neighbours take the words of eight calls of the generator: each
+// lane makes one of those of four steps, and hands the words round.
+template <bool AL>
+__device__ __forceinline__ void drop_vector(const DropArgs &d, const DropNow &now, int64_t row, int t,
+                                            int group, int j, float2 (&v)[4]) {
+  if constexpr (AL) {
+    drop8(d, now, static_cast<uint32_t>(t + j * group), row, v);
+  } else if (group >= 32) {
+    const int lane = t & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int c = element<false>(t - lane, group, j, 4 * h + (lane >> 3)) + 4 * (lane & 7);
+      const uint4 w = drop_words(d, now, static_cast<uint32_t>(c) >> 2, row);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int from = 8 * k + (lane >> 2);
+        const uint4 all = make_uint4(__shfl_sync(0xffffffffu, w.x, from), __shfl_sync(0xffffffffu, w.y, from),
+                                     __shfl_sync(0xffffffffu, w.z, from), __shfl_sync(0xffffffffu, w.w, from));
+        float &x = k & 1 ? v[2 * h + k / 2].y : v[2 * h + k / 2].x;
+        x = drop1(d, word_of(all, lane & 3), x);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t c = static_cast<uint32_t>(element<false>(t, group, j, k));
+      const uint4 w = drop_words_of(now.seed, c >> 2, static_cast<uint32_t>(row),
+                                    static_cast<uint32_t>(uint64_t(row) >> 32), now.offset);
+      float &x = k & 1 ? v[k / 2].y : v[k / 2].x;
+      x = drop1(d, word_of(w, c & 3), x);
+    }
+  }
+}
+
+// The weight: in bf16 kept in registers, in fp32 (which would take 32 of them)
+// read again for each row.
+template <bool AL, class T, int VPT>
+struct Weight {
+  static constexpr bool kKeep = sizeof(T) == 2;
+  Raw8<T> kept[kKeep ? VPT : 1];
+  const float *wide;
+  __device__ __forceinline__ Weight(const void *w, int w32, int t, int group, int dim)
+      : wide(kKeep && !w32 ? nullptr : static_cast<const float *>(w)) {
+    if constexpr (kKeep)
+      if (wide == nullptr) fetch<AL>(kept, static_cast<const T *>(w), t, group, dim);
+  }
+  __device__ __forceinline__ void get(int j, int t, int group, int dim, float2 (&u)[4]) const {
+    if (kKeep && wide == nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = kept[kKeep ? j : 0].again(i);
+      return;
+    }
+    Raw8<float> o[1];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[0].set(i, both(0.f));
+    if constexpr (AL) {
+      const int c = (t + j * group) * 8;
+      if (c < dim) o[0].load(wide + c);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int c = element<false>(t, group, j, k);
+        if (c < dim) o[0].load1(k, wide + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] = o[0].pair(i);
+  }
+};
+
+// Sum (or largest) over the `group` threads of a row, the same bits in each of
+// them: shuffles, and for a group of several warps (then it is the block) one
+// barrier.  slot: 32 floats that are 0 beyond the block's warps, others than
+// those of the last call.
+template <bool MAX>
+__device__ __forceinline__ float over_group(float v, int group, float *slot) {
+  const int lanes = group < 32 ? group : 32;
+  for (int o = lanes >> 1; o > 0; o >>= 1) {
+    const float u = __shfl_xor_sync(0xffffffffu, v, o);
+    v = MAX ? fmaxf(v, u) : v + u;
+  }
+  if (group <= 32) return v;
+  if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
+  __syncthreads();
+  const float4 *all = reinterpret_cast<const float4 *>(slot);
+  v = 0.f;
+  for (int i = 0; i < group; i += 128) {
+    const float4 q = all[i >> 7];
+    v = MAX ? fmaxf(fmaxf(v, fmaxf(q.x, q.y)), fmaxf(q.z, q.w)) : v + ((q.x + q.y) + (q.z + q.w));
+  }
+  return v;
+}
+__device__ __forceinline__ void clear_slots(float *slots, int n) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) slots[i] = 0.f;
+}
+
+// ---- the ring ----
+// Stage s of it holds one row of each tensor, a buffer apart; bulk copies fill it
+// and count on full[s].  A copy takes whole 16-byte units: of a row that does not
+// begin or end on one, also the neighbours' bytes, which lie between the
+// tensor's first and last element for all but the first and the last row; what
+// these two miss comes straight from memory.
+
+template <class T>
+struct RowCopy {
+  const T *src;
+  int lead, lo, hi;  // elements before the row in the buffer; the row's copied ones
+  __device__ __forceinline__ uint32_t bytes() const {
+    return static_cast<uint32_t>(hi + (lo > 0 ? -lo : lead)) * static_cast<uint32_t>(sizeof(T));
+  }
+};
+// first, last: the addresses between which the tensor lies.
+template <bool AL, class T>
+__device__ __forceinline__ RowCopy<T> row_copy(const T *src, int dim, const NormSpan &span) {
+  RowCopy<T> c = {src, 0, 0, dim};
+  if constexpr (!AL) {
+    const uint64_t a = reinterpret_cast<uint64_t>(src), end = a + uint64_t(dim) * sizeof(T);
+    uint64_t lo = a & ~uint64_t(15), hi = (end + 15) & ~uint64_t(15);
+    c.lead = static_cast<int>((a - lo) / sizeof(T));
+    if (lo < span.first) {
+      lo += 16;
+      c.lo = static_cast<int>((lo - a) / sizeof(T));
+    }
+    if (hi > span.last) hi -= 16;
+    c.hi = hi > lo ? static_cast<int>((int64_t(hi) - int64_t(a)) / int64_t(sizeof(T))) : c.lo - c.lead;
+    if (hi <= lo) {  // nothing between two boundaries
+      c.lo = c.hi = 0;
+      c.lead = 0;
+    }
+  }
+  return c;
+}
+template <class T>
+__device__ __forceinline__ void copy_start(const RowCopy<T> &c, uint32_t buf, uint32_t bar) {
+  const uint32_t n = c.bytes();
+  // (where the first unit is left out, its place in the buffer stays empty)
+  if (n > 0) bulk_load(buf + (c.lo > 0 ? 16u : 0u), c.src + (c.lo > 0 ? c.lo : -c.lead), n, bar);
+}
+// Thread t's vectors of a row that has arrived in buf.
+template <bool AL, class T, int VPT>
+__device__ __forceinline__ void take(Raw8<T> (&v)[VPT], const RowCopy<T> &c, const uint8_t *buf, int t,
+                                     int group, int dim) {
+  const T *in = reinterpret_cast<const T *>(buf) + c.lead;
+  if constexpr (AL) {
+    fetch<true>(v, in, t, group, dim);
+  } else if (c.lo <= 0 && c.hi >= dim) {
+    fetch<false>(v, in, t, group, dim);
+  } else {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = element<false>(t, group, j, k);
+        if (k % 2 == 0) v[j].set(k / 2, both(0.f));
+        if (e < dim) v[j].load1(k, e >= c.lo && e < c.hi ? in + e : c.src + e);
+      }
+  }
+}
+
+// Waits for stage s of row i of this block's; the abort flag is up once a wait
+// ran out.
+__device__ __forceinline__ void ring_wait(RingHead *head, int s, uint32_t phase, unsigned *status) {
+  mbar_wait(smem_u32(&head->full[s]), phase, &head->abort_flag, status);
+}
+// On the way out: the copies in flight land first.
+__device__ __forceinline__ void ring_drain(RingHead *head, int s, uint32_t phase, int rows, int stages) {
+  for (; rows > 0; --rows) {
+    mbar_wait_drain(smem_u32(&head->full[s]), phase);
+    if (++s == stages) s = 0, phase ^= 1u;
+  }
+}
+__device__ __forceinline__ void ring_init(RingHead *head, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&head->full[s]), 1);
+    head->abort_flag = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+}
+
+template <class... P, class A>
+cudaError_t launch_ring(void (*kern)(P...), int blocks, const NormSplit &s, int tensors, const A &a,
+                        unsigned *status, cudaStream_t st) {
+  const size_t smem = kRingHead + size_t(s.stages) * tensors * s.buffer;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(blocks), dim3(s.block), smem, st, a, s.stages, s.buffer, status);
+}
+
+}  // namespace
+}  // namespace lora
