@@ -2,9 +2,12 @@
 // the Unsloth essay's recipe table names the rate).
 //
 // y = keep ? x * scale : 0 with the mask made from (seed, offset, row, column)
-// by both directions.  An element moves 4 bytes (bf16) or 8, and costs 1/4 of a
-// Philox call, some 17 instructions: the rates of memory and of the integer
-// products lie close together.
+// by both directions.  An element moves 4 bytes (bf16) or 8, and takes a quarter
+// of the generator's ten rounds: 1.73e12 words a second is all that an otherwise
+// empty loop of them makes on the 152 SMs (the 32 x 32 -> 64 products bound it),
+// and 1.70e12 elements of bf16 a second is what memory moves.  So what is not the
+// generator is kept small: a block's rows and addresses are worked out once, and
+// where the block has one row, the row's share of the first two rounds as well.
 #include <cmath>
 
 #include "dropout.cuh"
@@ -14,99 +17,119 @@
 namespace lora {
 namespace {
 
-constexpr int kThreads = 256;
-
 struct Args {
   const void *x;
   void *y;
-  int64_t rows, xs, ys, total;  // total: work items
-  uint32_t cols, per_row;       // items a row
-  uint32_t mul;                 // item / per_row = item * mul >> shift for
-  int shift;                    // items below 2^31
+  int64_t rows, xs, ys;
+  uint32_t cols, units;  // units of a row: eight columns, or four (any alignment)
+  // A block takes `segment` units of one row (chunks of them make a row), two a
+  // thread; or, where a row has few, 2^lanes threads a row and two rows each.
+  uint32_t chunks, segment;
+  int lanes;
   DropArgs drop;
 };
 
-// Item -> (row, item within the row).  The quotient of a 31-bit number by a
-// constant is a product and a shift (Granlund and Montgomery, 1994).
-__device__ __forceinline__ void place(const Args &a, int64_t item, int64_t &row, uint32_t &i) {
-  if (a.total < (int64_t(1) << 31)) {
-    const uint32_t r = static_cast<uint32_t>(uint64_t(item) * a.mul >> a.shift);
-    row = r;
-    i = static_cast<uint32_t>(item) - r * a.per_row;
-  } else {
-    row = item / a.per_row;
-    i = static_cast<uint32_t>(item - row * a.per_row);
-  }
-}
-
-// Rows of whole, aligned vectors of eight: each thread has kItems of them in
-// flight before it makes their masks.
-template <class T, int kItems>
-__global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ Args a) {
-  griddep_wait();
-  griddep_launch_dependents();
-  const DropNow now = drop_now(a.drop);
-  Raw8<T> in[kItems];
-  int64_t row[kItems];
-  uint32_t v[kItems];
-  const int64_t first = int64_t(blockIdx.x) * (kThreads * kItems) + threadIdx.x;
-#pragma unroll
-  for (int j = 0; j < kItems; ++j) {
-    const int64_t item = first + j * kThreads;
-    if (item < a.total) {
-      place(a, item, row[j], v[j]);
-      in[j].load(static_cast<const T *>(a.x) + row[j] * a.xs + int64_t(v[j]) * 8);
-    }
-  }
-#pragma unroll
-  for (int j = 0; j < kItems; ++j) {
-    if (first + j * kThreads >= a.total) break;
+// Unit u of a row.
+template <class T, bool VEC>
+struct Unit;
+template <class T>
+struct Unit<T, true> {
+  Raw8<T> v;
+  __device__ __forceinline__ void load(const T *row, uint32_t u, uint32_t) { v.load(row + u * 8); }
+  __device__ __forceinline__ void drop(const Args &a, const DropNow &now, uint32_t u, int64_t row) {
     float2 f[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = in[j].pair(i);
-    drop8(a.drop, now, v[j], row[j], f);
+    for (int i = 0; i < 4; ++i) f[i] = v.pair(i);
+    drop8(a.drop, now, u, row, f);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) in[j].set(i, f[i]);
-    in[j].store(static_cast<T *>(a.y) + row[j] * a.ys + int64_t(v[j]) * 8);
+    for (int i = 0; i < 4; ++i) v.set(i, f[i]);
   }
-}
-
-// Any width and alignment: four columns (one Philox call) a thread.
+  __device__ __forceinline__ void store(T *row, uint32_t u, uint32_t) const { v.store(row + u * 8); }
+};
 template <class T>
-__global__ void __launch_bounds__(kThreads) k_dropout_any(const __grid_constant__ Args a) {
+struct Unit<T, false> {
+  float f[4];
+  __device__ __forceinline__ void load(const T *row, uint32_t u, uint32_t cols) {
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) f[i] = u * 4 + i < cols ? to_f32(row[u * 4 + i]) : 0.f;
+  }
+  __device__ __forceinline__ void drop(const Args &a, const DropNow &now, uint32_t u, int64_t row) {
+    const uint4 w = drop_words(a.drop, now, u, row);
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i) f[i] = drop1(a.drop, word_of(w, i), f[i]);
+  }
+  __device__ __forceinline__ void store(T *row, uint32_t u, uint32_t cols) const {
+#pragma unroll
+    for (uint32_t i = 0; i < 4; ++i)
+      if (u * 4 + i < cols) row[u * 4 + i] = from_f32<T>(f[i]);
+  }
+};
+
+// Rows of many units: one row a block.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) k_dropout(const __grid_constant__ Args a) {
   griddep_wait();
   griddep_launch_dependents();
   const DropNow now = drop_now(a.drop);
-  const int64_t item = int64_t(blockIdx.x) * kThreads + threadIdx.x;
-  if (item >= a.total) return;
-  int64_t row;
-  uint32_t b;
-  place(a, item, row, b);
-  const T *x = static_cast<const T *>(a.x) + row * a.xs + int64_t(b) * 4;
-  T *y = static_cast<T *>(a.y) + row * a.ys + int64_t(b) * 4;
-  const uint32_t n = a.cols - b * 4;  // 4 columns, fewer at the row's end
-  float f[4];
+  const int64_t row = blockIdx.x / a.chunks;
+  const uint32_t first = (blockIdx.x % a.chunks) * a.segment;
+  const uint32_t end = min(first + a.segment, a.units);
+  const T *x = static_cast<const T *>(a.x) + row * a.xs;
+  T *y = static_cast<T *>(a.y) + row * a.ys;
+  Unit<T, VEC> in[2];
 #pragma unroll
-  for (uint32_t i = 0; i < 4; ++i) f[i] = i < n ? to_f32(x[i]) : 0.f;
-  const uint4 w = drop_words(a.drop, now, b, row);
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t u = first + threadIdx.x + j * blockDim.x;
+    if (u < end) in[j].load(x, u, a.cols);
+  }
 #pragma unroll
-  for (uint32_t i = 0; i < 4; ++i)
-    if (i < n) y[i] = from_f32<T>(drop1(a.drop, word_of(w, i), f[i]));
+  for (int j = 0; j < 2; ++j) {
+    const uint32_t u = first + threadIdx.x + j * blockDim.x;
+    if (u >= end) break;
+    in[j].drop(a, now, u, row);
+    in[j].store(y, u, a.cols);
+  }
 }
 
-template <class T>
-cudaError_t launch_dropout(Args a, bool vec, cudaStream_t s) {
-  a.per_row = vec ? a.cols / 8 : (a.cols + 3) / 4;
-  a.total = a.rows * a.per_row;
-  int l = 0;
-  while ((uint64_t(1) << l) < a.per_row) ++l;
-  a.shift = 31 + l;
-  a.mul = static_cast<uint32_t>((uint64_t(1) << a.shift) / a.per_row + 1);
-  const int64_t per_block = vec ? kThreads * 2 : kThreads;
-  const int64_t blocks = (a.total + per_block - 1) / per_block;
-  const dim3 grid(static_cast<unsigned>(blocks));
-  return vec ? launch_pdl(k_dropout<T, 2>, grid, dim3(kThreads), 0, s, a)
-             : launch_pdl(k_dropout_any<T>, grid, dim3(kThreads), 0, s, a);
+// Rows of few units: several a block.
+template <class T, bool VEC>
+__global__ void __launch_bounds__(256) k_dropout_rows(const __grid_constant__ Args a) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const DropNow now = drop_now(a.drop);
+  const uint32_t u = threadIdx.x & ((1u << a.lanes) - 1u), at_once = 256u >> a.lanes;
+  const int64_t first = int64_t(blockIdx.x) * (2 * at_once) + (threadIdx.x >> a.lanes);
+  if (u >= a.units) return;
+  Unit<T, VEC> in[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t row = first + j * at_once;
+    if (row < a.rows) in[j].load(static_cast<const T *>(a.x) + row * a.xs, u, a.cols);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t row = first + j * at_once;
+    if (row >= a.rows) break;
+    in[j].drop(a, now, u, row);
+    in[j].store(static_cast<T *>(a.y) + row * a.ys, u, a.cols);
+  }
+}
+
+template <class T, bool VEC>
+cudaError_t launch_dropout(Args a, cudaStream_t s) {
+  a.units = VEC ? a.cols / 8 : (a.cols + 3) / 4;
+  if (a.units <= 128) {
+    a.lanes = 0;
+    while ((1u << a.lanes) < a.units) ++a.lanes;
+    const int64_t per = 2 * (256 >> a.lanes);
+    return launch_pdl(k_dropout_rows<T, VEC>, dim3(static_cast<unsigned>((a.rows + per - 1) / per)),
+                      dim3(256), 0, s, a);
+  }
+  a.chunks = (a.units + 511) / 512;
+  a.segment = (a.units + a.chunks - 1) / a.chunks;
+  const unsigned threads = ((a.segment + 1) / 2 + 31) / 32 * 32;
+  return launch_pdl(k_dropout<T, VEC>, dim3(static_cast<unsigned>(a.rows * a.chunks)), dim3(threads), 0, s,
+                    a);
 }
 
 }  // namespace
@@ -168,7 +191,8 @@ extern "C" lora_status_t lora_dropout(const void *x, int64_t rows, int64_t cols,
   LORA_TRY(device_info(di));
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return run(LORA_K_DROPOUT, st, "dropout", [&] {
-    return dtype == LORA_BF16 ? launch_dropout<__nv_bfloat16>(a, vec, st)
-                              : launch_dropout<float>(a, vec, st);
+    if (dtype == LORA_BF16)
+      return vec ? launch_dropout<__nv_bfloat16, true>(a, st) : launch_dropout<__nv_bfloat16, false>(a, st);
+    return vec ? launch_dropout<float, true>(a, st) : launch_dropout<float, false>(a, st);
   });
 }

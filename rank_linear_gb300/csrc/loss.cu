@@ -192,16 +192,21 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
   {
     float s = 0.f, m = 0.f;
     const LossPart *p = parts + i0 + lane;
-#pragma unroll 8
-    for (int k = warp; k < pieces; k += 32) {
-      const LossPart u = p[int64_t(k) * st.rows];
-      if (u.up == m) {
-        s += u.sum;
-      } else if (u.up > m) {
-        s = s * exp2f(m - u.up) + u.sum;
-        m = u.up;
-      } else {
-        s += u.sum * exp2f(u.up - m);
+    constexpr int AHEAD = 8;  // on their way at once
+    for (int k = warp; k < pieces; k += 32 * AHEAD) {
+      LossPart u[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j)
+        u[j] = k + 32 * j < pieces ? p[int64_t(k + 32 * j) * st.rows] : LossPart{0.f, 0.f};
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) {
+        if (u[j].up != m) {  // hardly ever: both are 0
+          const float top = fmaxf(u[j].up, m);
+          s *= exp2f(m - top);
+          u[j].sum *= exp2f(u[j].up - top);
+          m = top;
+        }
+        s += u[j].sum;
       }
     }
     sums[warp][lane] = s;
@@ -255,6 +260,7 @@ __global__ void __launch_bounds__(1024) k_loss_mean(Tokens tk, const LossHead *h
   griddep_launch_dependents();
   const int n = head->live;
   double s = 0.0;
+#pragma unroll 4
   for (int k = threadIdx.x; k < n; k += 1024) {
     const int t = live[k];
     s += static_cast<double>(losses[t]) * (tk.weights != nullptr ? tk.weights[t] : 1.f);

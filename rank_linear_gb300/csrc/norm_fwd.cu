@@ -105,40 +105,46 @@ __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (
   }
 }
 
-// Forward, straight into registers: NR rows a group of threads, all of them on
-// their way at once.
+// Forward, straight into registers: blocks stay and take NR rows a group of threads
+// at a time, all of them on their way at once.
 template <class T, int VPT, bool AL, int NR, int MAX>
 __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFwdArgs a) {
-  __shared__ __align__(16) float slots[96];
-  clear_slots(slots, 96);
+  __shared__ __align__(16) float slots[192];  // of a round, and of the next
+  clear_slots(slots, 192);
   __syncthreads();
   griddep_wait();
   griddep_launch_dependents();
   const int group = a.group;
-  const int t = threadIdx.x % group, subs = blockDim.x / group;
-  const int64_t first = int64_t(blockIdx.x) * (subs * NR) + threadIdx.x / group;
+  const int sub = threadIdx.x / group, subs = blockDim.x / group;
   const DropNow now = drop_now(a.drop);
-  Raw8<T> hx[NR][VPT], hr[NR][VPT];
+  const Weight<AL, T, VPT> w(a.w, a.w32, threadIdx.x % group, group, a.dim);
+  float *slot = slots;
+  const int64_t step = int64_t(gridDim.x) * subs * NR;
+  for (int64_t first = int64_t(blockIdx.x) * subs * NR; first < a.rows; first += step) {
+    const int t = each_time(int(threadIdx.x % group));
+    Raw8<T> hx[NR][VPT], hr[NR][VPT];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int64_t row = first + n * subs;
-    const int dim = row < a.rows ? a.dim : 0;  // a group without a row holds zeros
-    const Where at = where(row < a.rows ? row : 0, a.inner);
-    fetch<AL>(hx[n], static_cast<const T *>(a.x) + at.at(a.sx), t, group, dim);
-    if (a.res != nullptr) fetch<AL>(hr[n], static_cast<const T *>(a.res) + at.at(a.sr), t, group, dim);
-  }
-  const Weight<AL, T, VPT> w(a.w, a.w32, t, group, a.dim);
+    for (int n = 0; n < NR; ++n) {
+      const int64_t row = first + n * subs + sub;
+      const int dim = row < a.rows ? a.dim : 0;  // a group without a row holds zeros
+      const Where at = where(row < a.rows ? row : 0, a.inner);
+      fetch<AL>(hx[n], static_cast<const T *>(a.x) + at.at(a.sx), t, group, dim);
+      if (a.res != nullptr) fetch<AL>(hr[n], static_cast<const T *>(a.res) + at.at(a.sr), t, group, dim);
+    }
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int64_t row = first + n * subs;
-    const bool live = row < a.rows;
-    const int dim = live ? a.dim : 0;
-    const Where at = where(live ? row : 0, a.inner);
-    to_stream<AL>(a, now, hx[n], hr[n], a.dropped != 0, row, static_cast<T *>(a.h) + at.at(a.sh), t, group, dim);
-    const float rstd = rstd_of(hx[n], a.dim, a.eps, group, slots, slots + 32);
-    if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
-    to_outputs<AL, true>(a, hx[n], w, rstd, row, static_cast<T *>(a.y) + at.at(a.sy), t, group, dim,
-                        slots + 64);
+    for (int n = 0; n < NR; ++n) {
+      const int64_t row = first + n * subs + sub;
+      const bool live = row < a.rows;
+      const int dim = live ? a.dim : 0;
+      const Where at = where(live ? row : 0, a.inner);
+      to_stream<AL>(a, now, hx[n], hr[n], a.dropped != 0, row, static_cast<T *>(a.h) + at.at(a.sh), t,
+                    group, dim);
+      const float rstd = rstd_of(hx[n], a.dim, a.eps, group, slot, slot + 32);
+      if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
+      to_outputs<AL, true>(a, hx[n], w, rstd, row, static_cast<T *>(a.y) + at.at(a.sy), t, group, dim,
+                           slot + 64);
+      slot = slot == slots ? slots + 96 : slots;
+    }
   }
 }
 
@@ -237,8 +243,10 @@ cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, un
            : s.vpt == 1 ? k_norm_fwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_fwd<T, 4, AL, 1, kSmallBlock>
                                     : k_norm_fwd<T, 4, AL, 1, 1024>;
-  const int64_t blocks = (a.rows + s.per_block - 1) / s.per_block;
-  return launch_pdl(k, dim3(static_cast<unsigned>(blocks)), dim3(s.block), 0, st, a);
+  // (a round of blocks that fills the SMs' threads: 16 of 128, or what fits)
+  const int64_t want = (a.rows + s.per_block - 1) / s.per_block;
+  const int64_t most = int64_t(kSms) * (s.block <= kSmallBlock ? 12 : 2);
+  return launch_pdl(k, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(s.block), 0, st, a);
 }
 }  // namespace
 
