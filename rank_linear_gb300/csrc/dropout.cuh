@@ -81,8 +81,10 @@ __device__ __forceinline__ void drop8(const DropArgs &d, const DropNow &now, uin
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     const uint4 w = drop_words(d, now, 2 * v + h, row);
-    x[2 * h] = make_float2(drop1(d, w.x, x[2 * h].x), drop1(d, w.y, x[2 * h].y));
-    x[2 * h + 1] = make_float2(drop1(d, w.z, x[2 * h + 1].x), drop1(d, w.w, x[2 * h + 1].y));
+    const float2 a = __fmul2_rn(x[2 * h], make_float2(d.scale, d.scale));
+    const float2 b = __fmul2_rn(x[2 * h + 1], make_float2(d.scale, d.scale));
+    x[2 * h] = make_float2(w.x >= d.threshold ? a.x : 0.f, w.y >= d.threshold ? a.y : 0.f);
+    x[2 * h + 1] = make_float2(w.z >= d.threshold ? b.x : 0.f, w.w >= d.threshold ? b.y : 0.f);
   }
 }
 __device__ __forceinline__ uint32_t word_of(const uint4 &w, uint32_t i) {

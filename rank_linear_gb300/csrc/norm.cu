@@ -134,12 +134,12 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
   a.codes = static_cast<uint8_t *>(codes);
   a.scale = scale;
   a.rows = rows;
-  a.inner = static_cast<uint32_t>(sh->inner);
+  a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   a.dim = sh->dim;
   a.eps = sh->eps;
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   const int tensors = residual != nullptr ? 2 : 1;
-  const NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, kFwdThreads, codes != nullptr);
+  const NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, false, codes != nullptr);
   a.group = s.group;
   DevInfo di;
   LORA_TRY(device_info(di));
@@ -156,7 +156,7 @@ size_t lora_norm_workspace_bytes(const lora_norm_t *sh, int with_dw) {
   int most = 0;
   for (int es = 2; es <= 4; es += 2)
     for (int tensors = 2; tensors <= 3; ++tensors) {
-      const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, kBwdThreads), rows);
+      const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, true), rows);
       most = n > most ? n : most;
     }
   return size_t(most) * sh->dim * sizeof(float);
@@ -175,7 +175,7 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   if (dw != nullptr && !aligned(dw, ws_es))
     return fail(LORA_ERR_INVALID_ARG, "dw is not aligned to its type");
   const int tensors = dh != nullptr ? 3 : 2;
-  const NormSplit s = norm_split(sh->dim, rows, dtype == LORA_BF16 ? 2 : 4, tensors, kBwdThreads);
+  const NormSplit s = norm_split(sh->dim, rows, dtype == LORA_BF16 ? 2 : 4, tensors, true);
   const int blocks = norm_bwd_blocks(s, rows);
   bool vec = sh->dim % 8 == 0;
   if (rows > 0) {
@@ -212,7 +212,7 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   a.dres = dresidual;
   a.partial = dw != nullptr ? static_cast<float *>(workspace) : nullptr;
   a.rows = rows;
-  a.inner = static_cast<uint32_t>(sh->inner);
+  a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   a.dim = sh->dim;
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   a.group = s.group;

@@ -16,6 +16,19 @@ struct NormRows {  // where row r begins
   int64_t outer, inner;
 };
 
+// Rows of an outer entry, and what divides a row's number by them: the quotient of
+// a 31-bit number by a constant is a product and a shift (Granlund and Montgomery,
+// 1994).
+struct NormInner {
+  uint32_t n, mul;
+  int shift;
+};
+inline NormInner norm_inner(int64_t n) {
+  int l = 0;
+  while ((int64_t(1) << l) < n) ++l;
+  return {static_cast<uint32_t>(n), static_cast<uint32_t>((uint64_t(1) << (31 + l)) / n + 1), 31 + l};
+}
+
 // The addresses between which a tensor's elements lie.
 struct NormSpan {
   uint64_t first, last;
@@ -29,7 +42,7 @@ struct NormFwdArgs {
   NormRows sx, sr, sh, sy;
   NormSpan span_x, span_r;
   int64_t rows;
-  uint32_t inner;  // rows an outer entry
+  NormInner inner;
   int dim, group, w32;
   float eps;
   int dropped;
@@ -44,7 +57,7 @@ struct NormBwdArgs {
   NormRows sdy, sh, sdh, sdx, sdr;
   NormSpan span_y, span_h, span_d;
   int64_t rows;
-  uint32_t inner;
+  NormInner inner;
   int dim, group, w32;
   int dropped;
   DropArgs drop;
@@ -57,10 +70,10 @@ struct RingHead {
 };
 constexpr int kRingHead = 64;
 
-// Vectors a thread: as many as its registers hold (the forward's 80, the
-// backward's 128); the fewer threads a row, the fewer instructions it takes to
-// add up their sums.
-__host__ __device__ constexpr int ring_vectors(int es) { return es == 2 ? 4 : 2; }
+// Vectors a thread.  A row's work is one chain through its threads (read, sum,
+// barrier, write), so that two vectors a thread and twice the threads take it
+// sooner than four, at as many bytes on their way.
+__host__ __device__ constexpr int ring_vectors(int es, bool backward) { return 2; }
 
 // How a call runs.
 struct NormSplit {
@@ -71,15 +84,14 @@ struct NormSplit {
 };
 constexpr int kSms = 152;
 constexpr int kRingSmem = 220 * 1024;  // of an SM's, left to its blocks' rings
-// Threads of the ring's blocks on an SM: what their registers (80 a thread forward,
-// 128 backward) leave room for.
-constexpr int kFwdThreads = 768, kBwdThreads = 512;
+// Threads of the ring's blocks on an SM, at 80 registers each.
+constexpr int kRingThreads = 768;
 
 // Few rows (two an SM at most): as many threads as there are vectors.
 inline bool norm_few_rows(int64_t rows) { return rows <= 2 * kSms; }
 
 // tensors: that are read a row; threads: of an SM.
-inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, int threads_sm, bool codes = false) {
+inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool backward, bool codes = false) {
   const bool wide_codes = codes && es == 4;  // (codes of fp32 rows: not over the ring)
   NormSplit s = {};
   const int vectors = (dim + 7) / 8;
@@ -87,13 +99,13 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, int thre
   if (norm_few_rows(rows) && vectors <= 1024) {
     s.vpt = 1;
   } else if (dim > 1024) {
-    s.vpt = ring_vectors(es);
+    s.vpt = ring_vectors(es, backward);
     s.group = s.block = ((vectors + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.per_block = 1;
     // (a row may begin and end inside 16 bytes)
     s.buffer = static_cast<uint32_t>((dim * es + 15) / 16 * 16 + 16);
     const int stage = static_cast<int>(s.buffer) * tensors;
-    s.blocks_sm = s.block > 512 ? 1 : s.block > 256 ? 1 : threads_sm / s.block;
+    s.blocks_sm = s.block > 384 ? 1 : kRingThreads / s.block;
     if (s.blocks_sm > 8) s.blocks_sm = 8;
     for (; s.blocks_sm > 0; --s.blocks_sm) {
       s.stages = (kRingSmem / s.blocks_sm - 1024 - kRingHead) / stage;
@@ -139,10 +151,11 @@ struct Where {
   int64_t o, i;
   __device__ __forceinline__ int64_t at(const NormRows &s) const { return o * s.outer + i * s.inner; }
 };
-__device__ __forceinline__ Where where(int64_t row, uint32_t inner) {
-  if (inner == 1) return {row, 0};
+__device__ __forceinline__ Where where(int64_t row, const NormInner &inner) {
+  if (inner.n == 1) return {row, 0};
   const uint32_t r = static_cast<uint32_t>(row);  // below 2^31
-  return {static_cast<int64_t>(r / inner), static_cast<int64_t>(r % inner)};
+  const uint32_t o = static_cast<uint32_t>(uint64_t(r) * inner.mul >> inner.shift);
+  return {static_cast<int64_t>(o), static_cast<int64_t>(r - o * inner.n)};
 }
 
 // A row belongs to `group` threads, VPT vectors of eight elements each.  Aligned
@@ -230,39 +243,46 @@ __device__ __forceinline__ void drop_vector(const DropArgs &d, const DropNow &no
   }
 }
 
-// The weight: in bf16 kept in registers, in fp32 (which would take 32 of them)
-// read again for each row.
-template <bool AL, class T, int VPT>
+// The weight: kept in registers where it is bf16 and KEEP, else read again for each
+// row (from L1: it is the only thing that is read through it).
+template <bool AL, bool KEEP, class T, int VPT>
 struct Weight {
-  static constexpr bool kKeep = sizeof(T) == 2;
+  static constexpr bool kKeep = KEEP && sizeof(T) == 2;
   Raw8<T> kept[kKeep ? VPT : 1];
-  const float *wide;
+  const void *from;
+  bool wide;  // fp32
   __device__ __forceinline__ Weight(const void *w, int w32, int t, int group, int dim)
-      : wide(kKeep && !w32 ? nullptr : static_cast<const float *>(w)) {
+      : from(w), wide(sizeof(T) == 4 || w32 != 0) {
     if constexpr (kKeep)
-      if (wide == nullptr) fetch<AL>(kept, static_cast<const T *>(w), t, group, dim);
+      if (!wide) fetch<AL>(kept, static_cast<const T *>(w), t, group, dim);
   }
-  __device__ __forceinline__ void get(int j, int t, int group, int dim, float2 (&u)[4]) const {
-    if (kKeep && wide == nullptr) {
+  template <class S>
+  __device__ __forceinline__ void read(const S *w, int j, int t, int group, int dim, float2 (&u)[4]) const {
+    Raw8<S> o;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = kept[kKeep ? j : 0].again(i);
-      return;
-    }
-    Raw8<float> o[1];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[0].set(i, both(0.f));
+    for (int i = 0; i < 4; ++i) o.set(i, both(0.f));
     if constexpr (AL) {
       const int c = (t + j * group) * 8;
-      if (c < dim) o[0].load(wide + c);
+      if (c < dim) o.load(w + c);
     } else {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int c = element<false>(t, group, j, k);
-        if (c < dim) o[0].load1(k, wide + c);
+        if (c < dim) o.load1(k, w + c);
       }
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = o[0].pair(i);
+    for (int i = 0; i < 4; ++i) u[i] = o.pair(i);
+  }
+  __device__ __forceinline__ void get(int j, int t, int group, int dim, float2 (&u)[4]) const {
+    if (wide) {
+      read(static_cast<const float *>(from), j, t, group, dim, u);
+    } else if constexpr (kKeep) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) u[i] = kept[j].again(i);
+    } else {
+      read(static_cast<const T *>(from), j, t, group, dim, u);
+    }
   }
 };
 

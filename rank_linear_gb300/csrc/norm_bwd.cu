@@ -7,10 +7,10 @@ namespace {
 // ---- backward ----
 // What a row's threads do with it: g = dy w and h r, their mean product, then
 // d = r (g - h r mean) + dh, dropped out where the branch was.
-template <bool AL, class T, int VPT>
+template <bool AL, bool KEEP, class T, int VPT>
 __device__ __forceinline__ void row_backward(const NormBwdArgs &a, const DropNow &now,
                                              const Raw8<T> (&hy)[VPT], const Raw8<T> (&hh)[VPT],
-                                             const Raw8<T> (&hd)[VPT], const Weight<AL, T, VPT> &w,
+                                             const Raw8<T> (&hd)[VPT], const Weight<AL, KEEP, T, VPT> &w,
                                              float rstd, bool drop, int64_t row, const Where &at, int t,
                                              int group, int dim, float *slot, float2 (&acc)[VPT][4]) {
   float2 s = both(0.f);
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(MAX) k_norm_bwd(const __grid_constant__ NormBw
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
-  const Weight<AL, T, VPT> w(a.w, a.w32, t, group, a.dim);
+  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim);
   int parity = 0;
   const int64_t step = int64_t(gridDim.x) * subs * NR;
   for (int64_t first = int64_t(blockIdx.x) * subs * NR; first < a.rows; first += step) {
@@ -85,7 +85,7 @@ __global__ void __launch_bounds__(MAX) k_norm_bwd(const __grid_constant__ NormBw
     for (int n = 0; n < NR; ++n) {
       const int64_t row = first + n * subs + sub;
       const bool live = row < a.rows;
-      row_backward<AL>(a, now, hy[n], hh[n], hd[n], w, rstd[n], a.dropped != 0, row,
+      row_backward<AL, true>(a, now, hy[n], hh[n], hd[n], w, rstd[n], a.dropped != 0, row,
                              where(live ? row : 0, a.inner), t, group, live ? a.dim : 0,
                              slots + 32 * parity, acc);
       parity ^= 1;
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(MAX) k_norm_bwd(const __grid_constant__ NormBw
 template <class T, bool AL, bool DROP, int MAX, int BLOCKS>
 __global__ void __launch_bounds__(MAX, BLOCKS)
     k_norm_bwd_ring(const __grid_constant__ NormBwdArgs a, int stages, uint32_t buffer, unsigned *status) {
-  constexpr int VPT = ring_vectors(sizeof(T));
+  constexpr int VPT = ring_vectors(sizeof(T), true);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float slots[64];
   auto *head = reinterpret_cast<RingHead *>(smem);
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
-  const Weight<AL, T, VPT> w(a.w, a.w32, t, group, a.dim);
+  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim);
   int s = 0, parity = 0;
   uint32_t phase = 0;
   float rstd = blockIdx.x < a.rows ? a.rstd[blockIdx.x] : 0.f;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     take<AL>(hy, copy_y(at), buf, t, group, a.dim);
     take<AL>(hh, copy_h(at), buf + buffer, t, group, a.dim);
     if (tensors == 3) take<AL>(hd, copy_d(at), buf + 2 * buffer, t, group, a.dim);
-    row_backward<AL>(a, now, hy, hh, hd, w, rstd, DROP, row, at, t, group, a.dim, slots + 32 * parity, acc);
+    row_backward<AL, true>(a, now, hy, hh, hd, w, rstd, DROP, row, at, t, group, a.dim, slots + 32 * parity, acc);
     parity ^= 1;
     rstd = next;
     // (its barrier came after every thread had read the stage)
@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float *__restrict__ parti
 template <class T, bool AL, bool DROP>
 cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
-  auto k = s.block <= 256 ? k_norm_bwd_ring<T, AL, DROP, 256, kBwdThreads / 256>
-                          : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
+  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, kRingThreads / 256>
+           : s.block <= 384 ? k_norm_bwd_ring<T, AL, DROP, 384, kRingThreads / 384>
+                            : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
 }
 template <class T, bool AL>

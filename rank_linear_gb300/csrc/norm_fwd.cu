@@ -64,7 +64,7 @@ __device__ __forceinline__ void to_stream(const NormFwdArgs &a, const DropNow &n
 // y = h r w to memory, and the codes and the scale.
 template <bool AL, bool FP8, class T, int VPT>
 __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (&h)[VPT],
-                                           const Weight<AL, T, VPT> &w, float rstd, int64_t row, T *y,
+                                           const Weight<AL, true, T, VPT> &w, float rstd, int64_t row, T *y,
                                            int t, int group, int dim, float *slot) {
   float2 v[FP8 ? VPT : 1][4];
   float top = 0.f;
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFw
   const int group = a.group;
   const int sub = threadIdx.x / group, subs = blockDim.x / group;
   const DropNow now = drop_now(a.drop);
-  const Weight<AL, T, VPT> w(a.w, a.w32, threadIdx.x % group, group, a.dim);
+  const Weight<AL, true, T, VPT> w(a.w, a.w32, threadIdx.x % group, group, a.dim);
   float *slot = slots;
   const int64_t step = int64_t(gridDim.x) * subs * NR;
   for (int64_t first = int64_t(blockIdx.x) * subs * NR; first < a.rows; first += step) {
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFw
 template <class T, bool AL, bool DROP, bool FP8, int MAX, int BLOCKS>
 __global__ void __launch_bounds__(MAX, BLOCKS)
     k_norm_fwd_ring(const __grid_constant__ NormFwdArgs a, int stages, uint32_t buffer, unsigned *status) {
-  constexpr int VPT = ring_vectors(sizeof(T));
+  constexpr int VPT = ring_vectors(sizeof(T), false);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float slots[128];
   auto *head = reinterpret_cast<RingHead *>(smem);
@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   if (t == 0)
     for (int i = 0; i < stages; ++i)
       if (blockIdx.x + i * step < a.rows) start(blockIdx.x + i * step, i);
-  const Weight<AL, T, VPT> w(a.w, a.w32, t, group, a.dim);
+  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim);
   int s = 0, parity = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += step) {
@@ -224,8 +224,9 @@ cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensor
                             cudaStream_t st) {
   const int64_t most = int64_t(kSms) * s.blocks_sm;
   const int blocks = static_cast<int>(a.rows < most ? a.rows : most);
-  auto k = s.block <= 256 ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, kFwdThreads / 256>
-                          : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
+  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, kRingThreads / 256>
+           : s.block <= 384 ? k_norm_fwd_ring<T, AL, DROP, FP8, 384, kRingThreads / 384>
+                            : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
   return launch_ring(k, blocks, s, tensors, a, status, st);
 }
 template <class T, bool AL>
