@@ -136,10 +136,11 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
   a.rows = rows;
   a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   a.dim = sh->dim;
+  a.inv_dim = 1.f / static_cast<float>(sh->dim);
   a.eps = sh->eps;
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   const int tensors = residual != nullptr ? 2 : 1;
-  const NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, false, codes != nullptr);
+  const NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, ts.vec, codes != nullptr);
   a.group = s.group;
   DevInfo di;
   LORA_TRY(device_info(di));
@@ -151,13 +152,15 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
 size_t lora_norm_workspace_bytes(const lora_norm_t *sh, int with_dw) {
   clear_error();
   if (check_shape(sh, LORA_BF16) != LORA_OK || !with_dw) return 0;
-  // (the type, and whether dh is given, move the blocks: room for the most)
+  // (the type, the alignment and whether dh is given move the blocks: room for the most)
   const int64_t rows = sh->outer * sh->inner;
   int most = 0;
   for (int es = 2; es <= 4; es += 2)
     for (int tensors = 2; tensors <= 3; ++tensors) {
-      const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, true), rows);
-      most = n > most ? n : most;
+      for (int vec = 0; vec < 2; ++vec) {
+        const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, vec != 0), rows);
+        most = n > most ? n : most;
+      }
     }
   return size_t(most) * sh->dim * sizeof(float);
 }
@@ -175,8 +178,6 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   if (dw != nullptr && !aligned(dw, ws_es))
     return fail(LORA_ERR_INVALID_ARG, "dw is not aligned to its type");
   const int tensors = dh != nullptr ? 3 : 2;
-  const NormSplit s = norm_split(sh->dim, rows, dtype == LORA_BF16 ? 2 : 4, tensors, true);
-  const int blocks = norm_bwd_blocks(s, rows);
   bool vec = sh->dim % 8 == 0;
   if (rows > 0) {
     Tensors ts = {sh, dtype == LORA_BF16 ? 2 : 4, vec};
@@ -199,6 +200,8 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
       return fail(LORA_ERR_INVALID_ARG, "rstd is NULL or not aligned");
     vec = ts.vec;
   }
+  const NormSplit s = norm_split(sh->dim, rows, dtype == LORA_BF16 ? 2 : 4, tensors, vec);
+  const int blocks = norm_bwd_blocks(s, rows);
   if (dw != nullptr)
     LORA_TRY(check_ws(workspace, workspace_bytes, size_t(blocks) * sh->dim * sizeof(float)));
   if (rows == 0 && dw == nullptr) return LORA_OK;
@@ -214,6 +217,7 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   a.rows = rows;
   a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   a.dim = sh->dim;
+  a.inv_dim = 1.f / static_cast<float>(sh->dim);
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   a.group = s.group;
   DevInfo di;

@@ -44,7 +44,7 @@ struct NormFwdArgs {
   int64_t rows;
   NormInner inner;
   int dim, group, w32;
-  float eps;
+  float eps, inv_dim;
   int dropped;
   DropArgs drop;
 };
@@ -59,6 +59,7 @@ struct NormBwdArgs {
   int64_t rows;
   NormInner inner;
   int dim, group, w32;
+  float inv_dim;
   int dropped;
   DropArgs drop;
 };
@@ -73,7 +74,7 @@ constexpr int kRingHead = 64;
 // Vectors a thread.  A row's work is one chain through its threads (read, sum,
 // barrier, write), so that two vectors a thread and twice the threads take it
 // sooner than four, at as many bytes on their way.
-__host__ __device__ constexpr int ring_vectors(int es, bool backward) { return 2; }
+constexpr int kRingVectors = 2;
 
 // How a call runs.
 struct NormSplit {
@@ -84,14 +85,16 @@ struct NormSplit {
 };
 constexpr int kSms = 152;
 constexpr int kRingSmem = 220 * 1024;  // of an SM's, left to its blocks' rings
-// Threads of the ring's blocks on an SM, at 80 registers each.
-constexpr int kRingThreads = 768;
+// Threads of the ring's blocks on an SM: at 80 registers each, or 128 where rows are
+// not aligned (at 80 they spill: 5331 x 2001 in fp32, both directions, took 114 us
+// instead of 80).
+__host__ __device__ constexpr int ring_threads(bool vec) { return vec ? 768 : 512; }
 
 // Few rows (two an SM at most): as many threads as there are vectors.
 inline bool norm_few_rows(int64_t rows) { return rows <= 2 * kSms; }
 
 // tensors: that are read a row; threads: of an SM.
-inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool backward, bool codes = false) {
+inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec, bool codes = false) {
   const bool wide_codes = codes && es == 4;  // (codes of fp32 rows: not over the ring)
   NormSplit s = {};
   const int vectors = (dim + 7) / 8;
@@ -99,13 +102,13 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool bac
   if (norm_few_rows(rows) && vectors <= 1024) {
     s.vpt = 1;
   } else if (dim > 1024) {
-    s.vpt = ring_vectors(es, backward);
+    s.vpt = kRingVectors;
     s.group = s.block = ((vectors + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.per_block = 1;
     // (a row may begin and end inside 16 bytes)
     s.buffer = static_cast<uint32_t>((dim * es + 15) / 16 * 16 + 16);
     const int stage = static_cast<int>(s.buffer) * tensors;
-    s.blocks_sm = s.block > 384 ? 1 : kRingThreads / s.block;
+    s.blocks_sm = s.block > (vec ? 384 : 256) ? 1 : ring_threads(vec) / s.block;
     if (s.blocks_sm > 8) s.blocks_sm = 8;
     for (; s.blocks_sm > 0; --s.blocks_sm) {
       s.stages = (kRingSmem / s.blocks_sm - 1024 - kRingHead) / stage;
@@ -152,8 +155,8 @@ struct Where {
   __device__ __forceinline__ int64_t at(const NormRows &s) const { return o * s.outer + i * s.inner; }
 };
 __device__ __forceinline__ Where where(int64_t row, const NormInner &inner) {
-  if (inner.n == 1) return {row, 0};
   const uint32_t r = static_cast<uint32_t>(row);  // below 2^31
+  if (inner.n == 1) return {row, 0};
   const uint32_t o = static_cast<uint32_t>(uint64_t(r) * inner.mul >> inner.shift);
   return {static_cast<int64_t>(o), static_cast<int64_t>(r - o * inner.n)};
 }
@@ -279,7 +282,7 @@ struct Weight {
       read(static_cast<const float *>(from), j, t, group, dim, u);
     } else if constexpr (kKeep) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) u[i] = kept[j].again(i);
+      for (int i = 0; i < 4; ++i) u[i] = VPT == 1 ? kept[j].pair(i) : kept[j].again(i);
     } else {
       read(static_cast<const T *>(from), j, t, group, dim, u);
     }

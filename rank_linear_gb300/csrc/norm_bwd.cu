@@ -25,7 +25,7 @@ __device__ __forceinline__ void row_backward(const NormBwdArgs &a, const DropNow
       s = fma2(mul2(y, u[i]), hat, s);
     }
   }
-  const float along = over_group<false>(s.x + s.y, group, slot) / static_cast<float>(a.dim);
+  const float along = over_group<false>(s.x + s.y, group, slot) * a.inv_dim;
   const float2 back = both(-along * rstd * rstd);  // d = r g - h (r^2 mean) + dh
   T *dx = static_cast<T *>(a.dx) + at.at(a.sdx);
   T *dres = static_cast<T *>(a.dres) + at.at(a.sdr);
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(MAX) k_norm_bwd(const __grid_constant__ NormBw
 template <class T, bool AL, bool DROP, int MAX, int BLOCKS>
 __global__ void __launch_bounds__(MAX, BLOCKS)
     k_norm_bwd_ring(const __grid_constant__ NormBwdArgs a, int stages, uint32_t buffer, unsigned *status) {
-  constexpr int VPT = ring_vectors(sizeof(T), true);
+  constexpr int VPT = kRingVectors;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float slots[64];
   auto *head = reinterpret_cast<RingHead *>(smem);
@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float *__restrict__ parti
 template <class T, bool AL, bool DROP>
 cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
-  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, kRingThreads / 256>
-           : s.block <= 384 ? k_norm_bwd_ring<T, AL, DROP, 384, kRingThreads / 384>
+  constexpr int THREADS = ring_threads(AL);
+  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, THREADS / 256>
+           : s.block <= 384 ? k_norm_bwd_ring<T, AL, DROP, 384, THREADS / 384>
                             : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
 }

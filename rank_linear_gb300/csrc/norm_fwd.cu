@@ -9,7 +9,7 @@ namespace {
 // range of fp32 the sum is taken again of values scaled down by 2^-70 (exact),
 // which the result is scaled by as well.
 template <class T, int VPT>
-__device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], int dim, float eps, int group,
+__device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], float inv_dim, float eps, int group,
                                          float *slot, float *slot2) {
   float2 s = both(0.f);
 #pragma unroll
@@ -17,11 +17,10 @@ __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], int dim, float
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma2(v[j].pair(i), v[j].pair(i), s);
   const float ss = over_group<false>(s.x + s.y, group, slot);
-  const float n = static_cast<float>(dim);
   // the same in every thread of a block-wide group; the smaller groups of a
   // warp shuffle together
   const bool far = !(ss <= 1e38f);
-  if (!(group > 32 ? far : __any_sync(0xffffffffu, far))) return rsqrtf(ss / n + eps);
+  if (!(group > 32 ? far : __any_sync(0xffffffffu, far))) return rsqrtf(fmaf(ss, inv_dim, eps));
   float s2 = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
@@ -31,7 +30,7 @@ __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], int dim, float
       s2 = fmaf(u.x, u.x, fmaf(u.y, u.y, s2));
     }
   s2 = over_group<false>(s2, group, slot2);
-  return far ? 0x1p-70f * rsqrtf(s2 / n + eps * 0x1p-140f) : rsqrtf(ss / n + eps);
+  return far ? 0x1p-70f * rsqrtf(fmaf(s2, inv_dim, eps * 0x1p-140f)) : rsqrtf(fmaf(ss, inv_dim, eps));
 }
 
 // x becomes drop(x) + residual, as the stream holds it (rounded once to the
@@ -75,7 +74,10 @@ __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       o[i] = mul2(mul2(h[j].pair(i), both(rstd)), u[i]);
-      if constexpr (FP8) top = fmaxf(top, fmaxf(fabsf(o[i].x), fabsf(o[i].y)));
+    }
+    if (FP8 && a.codes != nullptr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(o[i].x), fabsf(o[i].y)));
     }
     if (a.y != nullptr) put<AL>(y, o, t, group, j, dim);
   }
@@ -139,7 +141,7 @@ __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFw
       const Where at = where(live ? row : 0, a.inner);
       to_stream<AL>(a, now, hx[n], hr[n], a.dropped != 0, row, static_cast<T *>(a.h) + at.at(a.sh), t,
                     group, dim);
-      const float rstd = rstd_of(hx[n], a.dim, a.eps, group, slot, slot + 32);
+      const float rstd = rstd_of(hx[n], a.inv_dim, a.eps, group, slot, slot + 32);
       if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
       to_outputs<AL, true>(a, hx[n], w, rstd, row, static_cast<T *>(a.y) + at.at(a.sy), t, group, dim,
                            slot + 64);
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFw
 template <class T, bool AL, bool DROP, bool FP8, int MAX, int BLOCKS>
 __global__ void __launch_bounds__(MAX, BLOCKS)
     k_norm_fwd_ring(const __grid_constant__ NormFwdArgs a, int stages, uint32_t buffer, unsigned *status) {
-  constexpr int VPT = ring_vectors(sizeof(T), false);
+  constexpr int VPT = kRingVectors;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ __align__(16) float slots[128];
   auto *head = reinterpret_cast<RingHead *>(smem);
@@ -202,7 +204,7 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
       to_stream<AL>(a, now, x, r, DROP, row, static_cast<T *>(a.h) + at.at(a.sh), t, group, a.dim);
     }
     // its barrier: every thread has read the stage
-    const float rstd = rstd_of(x, a.dim, a.eps, group, slots + 32 * parity, slots + 64);
+    const float rstd = rstd_of(x, a.inv_dim, a.eps, group, slots + 32 * parity, slots + 64);
     parity ^= 1;
     if (*static_cast<volatile int *>(&head->abort_flag)) {  // a copy that never came
       const int64_t left = (a.rows - row + step - 1) / step;
@@ -224,8 +226,9 @@ cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensor
                             cudaStream_t st) {
   const int64_t most = int64_t(kSms) * s.blocks_sm;
   const int blocks = static_cast<int>(a.rows < most ? a.rows : most);
-  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, kRingThreads / 256>
-           : s.block <= 384 ? k_norm_fwd_ring<T, AL, DROP, FP8, 384, kRingThreads / 384>
+  constexpr int THREADS = ring_threads(AL);
+  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, THREADS / 256>
+           : s.block <= 384 ? k_norm_fwd_ring<T, AL, DROP, FP8, 384, THREADS / 384>
                             : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
   return launch_ring(k, blocks, s, tensors, a, status, st);
 }

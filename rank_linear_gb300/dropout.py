@@ -26,15 +26,19 @@ def _seed_of(seed, device):
     return seed % 2 ** 64, None
 
 
+_KEEP = _lib.Dropout()  # p = 0
+
+
 def _drop_block(p, seed, offset, device):
     """The dropout's argument block (None: no dropout) and what keeps its address alive."""
-    p, offset = float(p), int(offset)
+    p = float(p)
     if p == 0.0:
         return None
-    if not 0.0 <= offset < 2 ** 32:
+    offset = int(offset)
+    if not 0 <= offset < 2 ** 32:
         raise ValueError(f"offset = {offset} does not fit 32 bits")
     word, state = _seed_of(seed, device)
-    return _lib.Dropout(p=p, seed=word, offset=offset, state=_ptr(state))
+    return _lib.Dropout(p, word, offset, _ptr(state))
 
 
 def _collapsed(shape, strides):
@@ -85,11 +89,16 @@ def dropout_forward(x, p, seed, offset=0, *, out=None, stream=None):
     offset   32 bits: another mask of the same seed for each use in a step.
     out      may be x itself (in place).
     """
-    with _on(stream):
-        if out is None:
+    # (an output made here has the layout that x's decides)
+    key = ("dropout", _layout(x), _layout(out))
+    if out is None:
+        if stream is None:
             out = _empty_like(x)
-    (rows, cols, xs, ys), dtype = _block(("dropout", _layout(x), _layout(out)), lambda: _make(x, out))
-    block = _drop_block(p, seed, offset, x.device) or _lib.Dropout()
+        else:
+            with _on(stream):
+                out = _empty_like(x)
+    (rows, cols, xs, ys), dtype = _block(key, lambda: _make(x, out))
+    block = _drop_block(p, seed, offset, x.device) or _KEEP
     st = _lib.lib().lora_dropout(_ptr(x), rows, cols, xs, ys, ctypes.byref(block), dtype, _ptr(out),
                                  _stream_on(x.device, stream))
     if st:

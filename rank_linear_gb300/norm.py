@@ -62,6 +62,17 @@ def _row_floats(t, name, like):
         raise ValueError(f"{name} must be a contiguous float32 tensor of shape {tuple(like.shape[:-1])}")
 
 
+def _outputs(x, out, h_out, summed, fp8):
+    if out is None:
+        out = _empty_like(x)
+    if h_out is None and summed:
+        h_out = _empty_like(x)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    if not fp8:
+        return out, h_out, rstd, None, None
+    return out, h_out, rstd, torch.empty(x.shape, dtype=torch.uint8, device=x.device), torch.empty_like(rstd)
+
+
 def rms_norm_forward(x, weight, *, residual=None, eps=1e-6, dropout=0.0, seed=0, offset=0,
                      fp8=False, out=None, h_out=None, stream=None):
     """(y, h, rstd) of x [..., dim]: h = dropout(x) + residual, y = h * rstd * weight
@@ -74,27 +85,22 @@ def rms_norm_forward(x, weight, *, residual=None, eps=1e-6, dropout=0.0, seed=0,
               with a power of two for each row, as fp8_forward takes them (rows=).
     out       may be x; h_out may be residual (the stream updated in place) or x.
     """
-    eps, summed = float(eps), residual is not None or float(dropout) != 0.0
+    drop = _drop_block(dropout, seed, offset, x.device)
+    eps, summed = float(eps), residual is not None or drop is not None
     if h_out is not None and not summed:
         raise ValueError("h is x without residual and dropout")
-    drop = _drop_block(dropout, seed, offset, x.device)
-    with _on(stream):
-        key = ("norm", _layout(x), _layout(weight), _layout(residual), _layout(out), _layout(h_out),
-               summed, eps)
-        if out is None:
-            out = _empty_like(x)
-        if h_out is None and summed:
-            h_out = _empty_like(x)
+    # (outputs made here have the layouts that x's decides)
+    key = ("norm", _layout(x), _layout(weight), _layout(residual), _layout(out), _layout(h_out), summed, eps)
+    if stream is None:
+        out, h_out, rstd, codes, scale = _outputs(x, out, h_out, summed, fp8)
+    else:
+        with _on(stream):
+            out, h_out, rstd, codes, scale = _outputs(x, out, h_out, summed, fp8)
 
-        def make():
-            given = {"x": x, "residual": residual, "h": h_out, "y": out}
-            return _make(x, weight, eps, {n: t for n, t in given.items() if t is not None})
-        sh, dtype = _block(key, make)
-        rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        codes = scale = None
-        if fp8:
-            codes = torch.empty(x.shape, dtype=torch.uint8, device=x.device)
-            scale = torch.empty_like(rstd)
+    def make():
+        given = {"x": x, "residual": residual, "h": h_out, "y": out}
+        return _make(x, weight, eps, {n: t for n, t in given.items() if t is not None})
+    sh, dtype = _block(key, make)
     st = _lib.lib().lora_norm_fwd(ctypes.byref(sh), _ptr(x), _ptr(residual), _ptr(weight),
                                   None if drop is None else ctypes.byref(drop), dtype, _ptr(h_out),
                                   _ptr(out), _ptr(rstd), _ptr(codes), _ptr(scale),
