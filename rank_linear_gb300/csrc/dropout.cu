@@ -23,7 +23,7 @@ struct Args {
   int64_t rows, xs, ys;
   uint32_t cols, units;  // units of a row: eight columns, or four (any alignment)
   // A block takes `segment` units of one row (chunks of them make a row), kItems a
-  // thread; or, where a row has few, 2^lanes threads a row and two rows each.
+  // thread, and kRows rows; or, where a row has few, 2^lanes threads a row and two rows each.
   uint32_t chunks, segment;
   int lanes;
   DropArgs drop;
@@ -65,31 +65,45 @@ struct Unit<T, false> {
   }
 };
 
-constexpr int kItems = 2;  // (four took 5 % longer: fewer threads fit)
+constexpr int kItems = 2;  // units a thread and row (four: 5 % longer, fewer threads fit)
+constexpr int kRows = 4;   // rows a block: their common costs are shared
 
-// Rows of many units: one row a block.
+// Rows of many units: the same segment of kRows rows a block, the next row's units
+// on their way while the masks of one are made.
 template <class T, bool VEC>
 __global__ void __launch_bounds__(256) k_dropout(const __grid_constant__ Args a) {
   griddep_wait();
   griddep_launch_dependents();
   const DropNow now = drop_now(a.drop);
-  const int64_t row = blockIdx.x / a.chunks;
+  int64_t row = int64_t(blockIdx.x / a.chunks) * kRows;
   const uint32_t first = (blockIdx.x % a.chunks) * a.segment;
   const uint32_t end = min(first + a.segment, a.units);
+  const int64_t last = row + kRows < a.rows ? row + kRows : a.rows;
   const T *x = static_cast<const T *>(a.x) + row * a.xs;
   T *y = static_cast<T *>(a.y) + row * a.ys;
-  Unit<T, VEC> in[kItems];
+  Unit<T, VEC> in[kItems], next[kItems];
+  auto load = [&](Unit<T, VEC> (&v)[kItems], const T *from) {
 #pragma unroll
-  for (int j = 0; j < kItems; ++j) {
-    const uint32_t u = first + threadIdx.x + j * blockDim.x;
-    if (u < end) in[j].load(x, u, a.cols);
-  }
+    for (int j = 0; j < kItems; ++j) {
+      const uint32_t u = first + threadIdx.x + j * blockDim.x;
+      if (u < end) v[j].load(from, u, a.cols);
+    }
+  };
+  load(in, x);
+#pragma unroll 1
+  for (; row < last; ++row) {
+    x += a.xs;
+    if (row + 1 < last) load(next, x);
 #pragma unroll
-  for (int j = 0; j < kItems; ++j) {
-    const uint32_t u = first + threadIdx.x + j * blockDim.x;
-    if (u >= end) break;
-    in[j].drop(a, now, u, row);
-    in[j].store(y, u, a.cols);
+    for (int j = 0; j < kItems; ++j) {
+      const uint32_t u = first + threadIdx.x + j * blockDim.x;
+      if (u >= end) break;
+      in[j].drop(a, now, u, row);
+      in[j].store(y, u, a.cols);
+    }
+#pragma unroll
+    for (int j = 0; j < kItems; ++j) in[j] = next[j];
+    y += a.ys;
   }
 }
 
@@ -130,7 +144,7 @@ cudaError_t launch_dropout(Args a, cudaStream_t s) {
   a.chunks = (a.units + 256 * kItems - 1) / (256 * kItems);
   a.segment = (a.units + a.chunks - 1) / a.chunks;
   const unsigned threads = ((a.segment + kItems - 1) / kItems + 31) / 32 * 32;
-  return launch_pdl(k_dropout<T, VEC>, dim3(static_cast<unsigned>(a.rows * a.chunks)), dim3(threads), 0, s,
+  return launch_pdl(k_dropout<T, VEC>, dim3(static_cast<unsigned>((a.rows + kRows - 1) / kRows * a.chunks)), dim3(threads), 0, s,
                     a);
 }
 
