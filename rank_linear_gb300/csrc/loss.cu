@@ -175,29 +175,33 @@ __global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, Strip st,
   }
 }
 
-// 32 tokens a block: a warp adds every 32nd partial sum of all of them, then
-// each warp joins one token's 32 sums.
+// Eight tokens a block (32 left most SMs without one): a thread adds every 128th
+// partial sum of one of them, eight on their way at once, then a warp joins a
+// token's 128.
+constexpr int kRowTokens = 8;
 __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
                                                     const LossPart *__restrict__ parts, int pieces,
                                                     __nv_bfloat16 *e, int64_t lde, int vocab,
                                                     float *__restrict__ losses) {
-  __shared__ float sums[32][33], ups[32][33];
-  __shared__ float far[32];
+  constexpr int PER = 1024 / kRowTokens;
+  __shared__ float sums[kRowTokens][PER + 1], ups[kRowTokens][PER + 1];
+  __shared__ float far[kRowTokens];
   griddep_wait();
   griddep_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int i0 = blockIdx.x * 32;
+  const int i0 = blockIdx.x * kRowTokens;
   const int rows = min(st.rows, st.head->live - st.first);
   if (i0 >= rows) return;
   {
     float s = 0.f, m = 0.f;
-    const LossPart *p = parts + i0 + lane;
-    constexpr int AHEAD = 8;  // on their way at once
-    for (int k = warp; k < pieces; k += 32 * AHEAD) {
+    const int token = threadIdx.x % kRowTokens, from = threadIdx.x / kRowTokens;
+    const LossPart *p = parts + i0 + token;
+    constexpr int AHEAD = 8;
+    for (int k = from; k < pieces; k += PER * AHEAD) {
       LossPart u[AHEAD];
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j)
-        u[j] = k + 32 * j < pieces ? p[int64_t(k + 32 * j) * st.rows] : LossPart{0.f, 0.f};
+        u[j] = k + PER * j < pieces ? p[int64_t(k + PER * j) * st.rows] : LossPart{0.f, 0.f};
 #pragma unroll
       for (int j = 0; j < AHEAD; ++j) {
         if (u[j].up != m) {  // hardly ever: both are 0
@@ -209,19 +213,27 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
         s += u[j].sum;
       }
     }
-    sums[warp][lane] = s;
-    ups[warp][lane] = m;
+    sums[token][from] = s;
+    ups[token][from] = m;
   }
   __syncthreads();
-  const int i = i0 + warp;  // this warp's token
-  float s = sums[lane][warp], m = ups[lane][warp], top = m;
+  const int i = i0 + warp;  // of the first warps: their token
+  float s = 0.f, top = 0.f;
+  if (warp < kRowTokens) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-  if (m != top) s *= exp2f(m - top);
+    for (int k = 0; k < PER / 32; ++k) top = fmaxf(top, ups[warp][lane + 32 * k]);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+#pragma unroll
+    for (int k = 0; k < PER / 32; ++k) {
+      const float m = ups[warp][lane + 32 * k];
+      s += m == top ? sums[warp][lane + 32 * k] : sums[warp][lane + 32 * k] * exp2f(m - top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  }
   const float own = exp2f(-top), all = s + own;  // the target's, and with it
-  if (lane == 0) {
+  if (lane == 0 && warp < kRowTokens) {
     far[warp] = i < rows ? top : 0.f;
     if (i < rows) {
       const int n = st.live[i];
@@ -237,7 +249,7 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
   // Rows with an exponential beyond 2^64: the pieces that were kept on another
   // scale than the row's largest are brought to it (none, for all but rows whose
   // target is hopeless).
-  for (int r = 0; r < 32; ++r) {
+  for (int r = 0; r < kRowTokens; ++r) {
     if (far[r] == 0.f) continue;
     __nv_bfloat16 *row = e + int64_t(i0 + r) * lde;
     for (int c = threadIdx.x; c < vocab; c += 1024) {
@@ -246,7 +258,7 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
     }
   }
   __syncthreads();
-  if (lane == 0 && i < rows && st.target[i] >= 0)
+  if (lane == 0 && warp < kRowTokens && i < rows && st.target[i] >= 0)
     e[int64_t(i) * lde + st.target[i]] = __float2bfloat16_rn(-s * st.slope[i]);
 }
 
@@ -470,7 +482,7 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
                  [&] { return launch_loss_gemm(grad ? 1 : 0, g, pairs, st); }));
     LORA_TRY(run(LORA_K_LOSS_ROWS, st, "loss rows", [&] {
       const int64_t here = sh->rows - first < p.strip ? sh->rows - first : p.strip;
-      return launch_pdl(k_loss_rows, dim3(static_cast<unsigned>((here + 31) / 32)), dim3(1024), 0, st, tk, s, parts, p.pieces, e,
+      return launch_pdl(k_loss_rows, dim3(static_cast<unsigned>((here + kRowTokens - 1) / kRowTokens)), dim3(1024), 0, st, tk, s, parts, p.pieces, e,
                         p.lde, int(sh->vocab), losses);
     }));
     if (!grad) continue;

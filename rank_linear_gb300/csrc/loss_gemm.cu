@@ -547,7 +547,7 @@ cudaError_t launch_loss_gemm(int kind, const LossGemm &g, int pairs, cudaStream_
 }
 
 cudaError_t launch_loss_join(const LossGemm &g, int pairs, cudaStream_t s) {
-  return launch_pdl(k_loss_join, dim3(152 * 4), dim3(256), 0, s, g, pairs);
+  return launch_pdl(k_loss_join, dim3(152 * 8), dim3(256), 0, s, g, pairs);
 }
 
 }  // namespace lora
