@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   clear_slots(slots, 128);
   ring_init(head, stages);
   griddep_wait();
+  fence_proxy_async_global();  // what the kernels before wrote, for this thread's copies
   griddep_launch_dependents();
   const DropNow now = DROP ? drop_now(a.drop) : DropNow{};
   const int group = blockDim.x, t = threadIdx.x, tensors = a.res != nullptr ? 2 : 1;

@@ -79,11 +79,11 @@ def test_rows_beyond_32_bits_of_elements():
 
 
 def test_many_items():
-    """Over 2^31 groups of four: the division's other branch."""
-    rows = 2 ** 31 + 5
+    """Rows past 32 bits: the counter's third word."""
+    rows = 2 ** 32 + 5
     x = torch.ones(rows, 1, device=DEV, dtype=torch.bfloat16)
     rl.dropout_forward(x, 0.5, 21, 3, out=x)
-    for r in (0, 2 ** 31 - 1, 2 ** 31, 2 ** 31 + 4):
+    for r in (0, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1, 2 ** 32, 2 ** 32 + 4):
         assert x[r, 0].item() == on.dropout(np.ones((1, 1)), 0.5, 21, 3, first_row=r)[0, 0]
 
 
