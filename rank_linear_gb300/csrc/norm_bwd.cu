@@ -211,8 +211,10 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float *__restrict__ parti
   const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
   float s = 0.f;
-  if (c < dim)
+  if (c < dim) {
+#pragma unroll 8
     for (int b = slice; b < blocks; b += 8) s += partial[int64_t(b) * dim + c];
+  }
   part[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && c < dim) {
