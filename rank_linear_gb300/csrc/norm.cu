@@ -81,6 +81,25 @@ lora_status_t check_weight(const void *w, int es, const char *name, bool &vec) {
   return LORA_OK;
 }
 
+// Takes narrow rows side by side over the ring where they stand so: the shape's inner
+// rows, if each tensor has them `dim` apart; or, of plain contiguous rows, as many as
+// make some 4096 elements and divide their number.
+void use_heads(const lora_norm_t *sh, bool vec, int es, int tensors, NormRows *const *of,
+               const bool *given, int n, NormInner &inner, NormSplit &s) {
+  if (!vec || s.ring || sh->dim > 256) return;
+  int64_t outer = sh->outer, side = sh->inner;
+  const bool plain = side == 1;
+  if (plain) {
+    while (2 * side * sh->dim <= 4096 && sh->outer % (2 * side) == 0) side *= 2;
+    outer /= side;
+  }
+  for (int i = 0; i < n; ++i)
+    if (given[i] && (plain ? of[i]->outer : of[i]->inner) != sh->dim) return;
+  if (!norm_heads(sh->dim, outer, side, es, tensors, s) || !plain) return;
+  inner = norm_inner(side);
+  for (int i = 0; i < n; ++i) *of[i] = {side * sh->dim, sh->dim};
+}
+
 }  // namespace
 }  // namespace lora
 
@@ -140,7 +159,10 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
   a.eps = sh->eps;
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   const int tensors = residual != nullptr ? 2 : 1;
-  const NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, ts.vec, codes != nullptr);
+  NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, ts.vec, codes != nullptr);
+  NormRows *of[4] = {&a.sx, &a.sr, &a.sh, &a.sy};
+  const bool given[4] = {true, residual != nullptr, h != nullptr, y != nullptr};
+  use_heads(sh, ts.vec, ts.es, tensors, of, given, 4, a.inner, s);
   a.group = s.group;
   DevInfo di;
   LORA_TRY(device_info(di));
@@ -161,6 +183,11 @@ size_t lora_norm_workspace_bytes(const lora_norm_t *sh, int with_dw) {
         const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, vec != 0), rows);
         most = n > most ? n : most;
       }
+  // (narrow rows side by side: eight blocks an SM at most, of two rows at least)
+  if (sh->dim <= 256 && !norm_few_rows(rows / 2)) {
+    const int64_t n = rows / 2 < kSms * 8 ? rows / 2 : kSms * 8;
+    most = n > most ? static_cast<int>(n) : most;
+  }
     }
   return size_t(most) * sh->dim * sizeof(float);
 }
@@ -200,8 +227,13 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
       return fail(LORA_ERR_INVALID_ARG, "rstd is NULL or not aligned");
     vec = ts.vec;
   }
-  const NormSplit s = norm_split(sh->dim, rows, dtype == LORA_BF16 ? 2 : 4, tensors, vec);
-  const int blocks = norm_bwd_blocks(s, rows);
+  const int es = dtype == LORA_BF16 ? 2 : 4;
+  NormSplit s = norm_split(sh->dim, rows, es, tensors, vec);
+  a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
+  NormRows *of[5] = {&a.sdy, &a.sh, &a.sdx, &a.sdh, &a.sdr};
+  const bool given[5] = {true, true, true, dh != nullptr, dresidual != nullptr};
+  if (rows > 0) use_heads(sh, vec, es, tensors, of, given, 5, a.inner, s);
+  const int blocks = norm_bwd_blocks(s, s.heads ? rows / a.inner.n : rows);
   if (dw != nullptr)
     LORA_TRY(check_ws(workspace, workspace_bytes, size_t(blocks) * sh->dim * sizeof(float)));
   if (rows == 0 && dw == nullptr) return LORA_OK;
@@ -215,7 +247,6 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   a.dres = dresidual;
   a.partial = dw != nullptr ? static_cast<float *>(workspace) : nullptr;
   a.rows = rows;
-  a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   a.dim = sh->dim;
   a.inv_dim = 1.f / static_cast<float>(sh->dim);
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;

@@ -78,7 +78,7 @@ constexpr int kRingVectors = 2;
 
 // How a call runs.
 struct NormSplit {
-  bool ring;
+  bool ring, heads;
   int group, vpt, nr, block, per_block;  // threads and vectors of a row; rows at a time
   int stages, blocks_sm;                 // of the ring
   uint32_t buffer;                       // bytes of a row in the ring
@@ -134,10 +134,26 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec
   return s;
 }
 
+// Narrow rows of which `inner` lie side by side in every tensor, as the ring's rows:
+// each of whole vectors, and of 1, 2, 4 ... 32 threads.  False: not so.
+inline bool norm_heads(int dim, int64_t outer, int64_t inner, int es, int tensors, NormSplit &s) {
+  const int lanes = dim / 8;
+  const int64_t wide = inner * dim;
+  if (dim % 8 != 0 || lanes > 32 || (lanes & (lanes - 1)) != 0 || inner < 2 || wide <= 1024 || wide > 6144)
+    return false;
+  const NormSplit t = norm_split(static_cast<int>(wide), outer, es, tensors, true);
+  if (!t.ring || t.block > 384) return false;
+  s = t;
+  s.ring = false;
+  s.heads = true;
+  s.group = lanes;
+  return true;
+}
+
 // Blocks of the backward, each with a line of partial sums.
 inline int norm_bwd_blocks(const NormSplit &s, int64_t rows) {
   const int64_t n = (rows + s.per_block - 1) / s.per_block;
-  const int most = kSms * (s.ring ? s.blocks_sm : 4);
+  const int most = kSms * (s.ring || s.heads ? s.blocks_sm : 4);
   return static_cast<int>(n < most ? n : most);
 }
 

@@ -200,6 +200,86 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     }
 }
 
+// Narrow rows that lie side by side, over the ring (k_norm_fwd_heads).
+template <class T, bool DROP, int MAX, int BLOCKS>
+__global__ void __launch_bounds__(MAX, BLOCKS)
+    k_norm_bwd_heads(const __grid_constant__ NormBwdArgs a, int stages, uint32_t buffer,
+                     unsigned *status) {
+  constexpr int VPT = kRingVectors;
+  extern __shared__ __align__(128) uint8_t smem[];
+  auto *head = reinterpret_cast<RingHead *>(smem);
+  uint8_t *ring = smem + kRingHead;
+  ring_init(head, stages);
+  griddep_wait();
+  fence_proxy_async_global();  // what the kernels before wrote, for this thread's copies
+  griddep_launch_dependents();
+  const DropNow now = DROP ? drop_now(a.drop) : DropNow{};
+  const int lanes = a.group, tl = threadIdx.x % lanes, tensors = a.dh != nullptr ? 3 : 2;
+  const int inner = static_cast<int>(a.inner.n), wide = inner * a.dim;
+  const int64_t entries = a.rows / inner, step = gridDim.x;
+  auto start = [&](int64_t o, int s) {
+    const uint32_t bar = smem_u32(&head->full[s]), buf = smem_u32(ring + s * tensors * buffer);
+    const uint32_t n = static_cast<uint32_t>(wide) * static_cast<uint32_t>(sizeof(T));
+    mbar_expect_tx(bar, n * tensors);
+    bulk_load(buf, static_cast<const T *>(a.dy) + o * a.sdy.outer, n, bar);
+    bulk_load(buf + buffer, static_cast<const T *>(a.h) + o * a.sh.outer, n, bar);
+    if (tensors == 3) bulk_load(buf + 2 * buffer, static_cast<const T *>(a.dh) + o * a.sdh.outer, n, bar);
+  };
+  if (threadIdx.x == 0)
+    for (int i = 0; i < stages; ++i)
+      if (blockIdx.x + i * step < entries) start(blockIdx.x + i * step, i);
+  float2 acc[1][4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc[0][i] = both(0.f);
+  const Weight<true, true, T, 1> w(a.w, a.w32, tl, lanes, a.dim);
+  int s = 0;
+  uint32_t phase = 0;
+  for (int64_t o = blockIdx.x; o < entries; o += step) {
+    const int t = each_time(int(threadIdx.x));
+    float rstd[VPT];  // (on their way while the rows are)
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int sub = (t + j * int(blockDim.x)) / lanes;
+      rstd[j] = sub < inner ? a.rstd[o * inner + sub] : 0.f;
+    }
+    Raw8<T> hy[VPT], hh[VPT], hd[VPT];
+    ring_wait(head, s, phase, status);
+    const uint8_t *buf = ring + s * tensors * buffer;
+    fetch<true>(hy, reinterpret_cast<const T *>(buf), t, blockDim.x, wide);
+    fetch<true>(hh, reinterpret_cast<const T *>(buf + buffer), t, blockDim.x, wide);
+    if (tensors == 3) fetch<true>(hd, reinterpret_cast<const T *>(buf + 2 * buffer), t, blockDim.x, wide);
+    __syncthreads();  // every thread has read the stage
+    if (*static_cast<volatile int *>(&head->abort_flag)) {
+      const int64_t left = (entries - o + step - 1) / step;
+      if (t == 0) ring_drain(head, s, phase, static_cast<int>(left < stages ? left : stages), stages);
+      return;
+    }
+    if (t == 0 && o + stages * step < entries) start(o + stages * step, s);
+    if (++s == stages) s = 0, phase ^= 1u;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int sub = (t + j * int(blockDim.x)) / lanes;
+      const Raw8<T> y1[1] = {hy[j]}, h1[1] = {hh[j]}, d1[1] = {hd[j]};
+      row_backward<true, true>(a, now, y1, h1, d1, w, rstd[j], DROP, o * inner + sub, Where{o, sub}, tl,
+                               lanes, sub < inner ? a.dim : 0, nullptr, acc);
+    }
+  }
+  if (a.partial == nullptr) return;
+  // the sums of the threads with the same columns, in their order; the ring is free
+  float *cols = reinterpret_cast<float *>(ring);
+  const int groups = blockDim.x / lanes, of = threadIdx.x / lanes;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    cols[of * a.dim + tl * 8 + k] = k & 1 ? acc[0][k / 2].y : acc[0][k / 2].x;
+  __syncthreads();
+  for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
+    float sum = 0.f;
+    for (int i = 0; i < groups; ++i) sum += cols[i * a.dim + c];
+    a.partial[int64_t(blockIdx.x) * a.dim + c] = sum;
+  }
+}
+
 // dw = the blocks' sums, added in a fixed order: 32 columns a block, eight
 // threads a column.
 template <class T>
@@ -234,8 +314,17 @@ cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensor
                             : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
 }
+template <class T, bool DROP>
+cudaError_t launch_bwd_heads(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
+                             cudaStream_t st) {
+  auto k = k_norm_bwd_heads<T, DROP, 384, 2>;
+  return launch_ring(k, norm_bwd_blocks(s, a.rows / a.inner.n), s, tensors, a, status, st);
+}
 template <class T, bool AL>
 cudaError_t launch_any(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status, cudaStream_t st) {
+  if (s.heads)
+    return a.dropped ? launch_bwd_heads<T, true>(a, s, tensors, status, st)
+                     : launch_bwd_heads<T, false>(a, s, tensors, status, st);
   if (s.ring)
     return a.dropped ? launch_bwd_ring<T, AL, true>(a, s, tensors, status, st)
                      : launch_bwd_ring<T, AL, false>(a, s, tensors, status, st);

@@ -160,6 +160,44 @@ def test_strided_heads_and_odd_addresses():
         rl.rms_norm_forward(qkv.transpose(1, 2), w)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,heads,dim", [
+    (400, 32, 128), (611, 20, 64), (350, 17, 128), (900, 129, 8), (333, 24, 256), (2048, 40, 32),
+    (310, 6, 256)])
+@pytest.mark.parametrize("strided", [False, True])
+def test_heads_side_by_side(tokens, heads, dim, strided, dtype):
+    """Rows narrow enough for a warp, taken `heads` at a time: with a residual, dropout,
+    codes and every gradient."""
+    g = torch.Generator(device=DEV).manual_seed(dim + heads)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV).to(dtype)
+    x, res, dy, dh = (r(tokens, heads + (3 if strided else 0), dim)[:, :heads] for _ in range(4))
+    w = (1 + 0.3 * torch.randn(dim, generator=g, device=DEV)).to(dtype)
+    out = rl.rms_norm_forward(x, w, eps=1e-5)
+    check_forward(x, None, w, 1e-5, out)
+    got = rl.rms_norm_backward(dy, x, w, out[2])
+    check_backward(dy, x, w, out[2], None, got)
+    drop = dict(dropout=0.3, seed=77, offset=1)
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, fp8=True, **drop)
+    check_forward(x, res, w, 1e-5, out, 0.3, 77, 1)
+    got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh, **drop)
+    check_backward(dy, out[1], w, out[2], dh, got, 0.3, 77, 1)
+    again = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh, **drop)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def test_heads_of_contiguous_rows():
+    """The same of plain rows: [12800, 128] is taken 32 rows at a time, [12801, 128] is not."""
+    for rows in (12800, 12801, 6400 * 3):
+        x, res, w, dy, dh = make(rows, 128, torch.bfloat16, seed=rows)
+        out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5)
+        check_forward(x, res, w, 1e-5, out)
+        a, b = x.clone(), res.clone()
+        y, h, _ = rl.rms_norm_forward(a, w, residual=b, eps=1e-5, out=a, h_out=b)
+        assert torch.equal(y, out[0]) and torch.equal(h, out[1])
+        got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh)
+        check_backward(dy, out[1], w, out[2], dh, got)
+
+
 def test_in_place():
     x, res, w, dy, dh = make(33, 264, torch.bfloat16)
     y, h, rstd = rl.rms_norm_forward(x, w, residual=res)
