@@ -7,8 +7,7 @@
 //   k_loss_gather   a strip of them: X's rows side by side, the target's logit
 //   (first product) sums of exponentials relative to the target's
 //   k_loss_rows     losses, each row's factor, the target's element of E
-//   (second product, and the join of its ranges)
-//   k_loss_mean     the loss
+//   (second product), k_loss_join of its ranges; k_loss_mean or the join: the loss
 //
 // With every exponential relative to the target's own, a row's sum without the
 // target is S = 1 / p_t - 1, the loss log1p(S) and the target's element of
@@ -54,7 +53,8 @@ __device__ __forceinline__ Pair times(float a, float b) {
   const float p = __fmul_rn(a, b);
   return {p, isfinite(p) ? __fmaf_rn(a, b, -p) : 0.f};
 }
-// Over the block of 1024, the same in every thread, in a fixed order.
+// Over the block (of whole warps, 32 at most), the same in every thread, in a fixed
+// order.
 __device__ __forceinline__ Pair block_sum(Pair v, Pair *slot) {
   auto warp_sum = [&] {
 #pragma unroll
@@ -64,7 +64,8 @@ __device__ __forceinline__ Pair block_sum(Pair v, Pair *slot) {
   warp_sum();
   if ((threadIdx.x & 31) == 0) slot[threadIdx.x >> 5] = v;
   __syncthreads();
-  v = slot[threadIdx.x & 31];
+  const bool there = (threadIdx.x & 31) < blockDim.x >> 5;
+  v = there ? slot[threadIdx.x & 31] : Pair{0.f, 0.f};
   warp_sum();
   return v;
 }
@@ -136,10 +137,74 @@ struct Strip {
   int *target;
 };
 
+// Few tokens (1024 at most): each block of the gather finds the token of its place
+// by itself, which saves the index's launch; the first writes what k_loss_index
+// would have.  The token with rank `rank` among those that count (-1: there is none).
+constexpr int kFewTokens = 1024;
+__device__ __forceinline__ int64_t own_index(const Tokens &tk, int mean, int rank, LossHead *head,
+                                             int *__restrict__ live, float *__restrict__ losses) {
+  __shared__ int counts[8];
+  __shared__ int found;
+  __shared__ Pair slot[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const bool first = blockIdx.x == 0;
+  if (threadIdx.x == 0) found = -1;
+  unsigned mask = 0;
+  Pair sum = {0.f, 0.f};
+  const int n0 = threadIdx.x * (kFewTokens / 256);
+#pragma unroll
+  for (int j = 0; j < kFewTokens / 256; ++j) {
+    const int n = n0 + j;
+    if (n >= tk.rows) continue;
+    if (tk.target(n) >= 0) {
+      mask |= 1u << j;
+      if (first && mean && tk.weights != nullptr) sum = plus(sum, Pair{tk.weights[n], 0.f});
+    } else if (first) {
+      losses[n] = 0.f;
+    }
+  }
+  const int mine = __popc(mask);
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += u;
+  }
+  if (lane == 31) counts[warp] = before;
+  __syncthreads();
+  int at = before - mine, all = 0;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    if (k < warp) at += counts[k];
+    all += counts[k];
+  }
+#pragma unroll
+  for (int j = 0; j < kFewTokens / 256; ++j)
+    if (mask >> j & 1u) {
+      if (at == rank) found = n0 + j;
+      if (first) live[at] = n0 + j;
+      ++at;
+    }
+  if (first) {
+    float divisor = 1.f;
+    if (mean) {
+      divisor = tk.weights != nullptr ? block_sum(sum, slot).hi : static_cast<float>(all);
+      if (divisor == 0.f) divisor = 1.f;
+    }
+    if (threadIdx.x == 0) {
+      head->live = all;
+      head->divisor = divisor;
+    }
+  }
+  __syncthreads();
+  return found;
+}
+
 // W warps a token of the strip: X's row copied beside the others, z = c(x . W_t) in fp32; and a line of
 // zeros for each token that does not count among those at the strip's places.
-template <int W>
-__global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, Strip st,
+template <int W, bool OWN>
+__global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, int mean, LossHead *head, int *all_live,
+                                                     float *losses, Strip st,
                                                      const __nv_bfloat16 *__restrict__ w, int64_t ldw,
                                                      int64_t vocab, const __nv_bfloat16 *x,
                                                      int64_t ldx, __nv_bfloat16 *__restrict__ xs,
@@ -156,8 +221,16 @@ __global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, Strip st,
     uint4 *o = reinterpret_cast<uint4 *>(dx + n0 * lddx);
     for (int c = lane; c < dim / 8; c += T) o[c] = make_uint4(0u, 0u, 0u, 0u);
   }
-  if (i >= st.rows || n0 >= st.head->live) return;  // the same in a token's threads
-  const int64_t n = st.live[i], t = tk.target(n);
+  int64_t n;
+  if constexpr (OWN) {
+    static_assert(W == 8, "a block a token");
+    n = own_index(tk, mean, st.first + i, head, all_live, losses);
+    if (n < 0) return;
+  } else {
+    if (i >= st.rows || n0 >= st.head->live) return;  // the same in a token's threads
+    n = st.live[i];
+  }
+  const int64_t t = tk.target(n);
   const bool known = t < vocab;
   const uint4 *xr = reinterpret_cast<const uint4 *>(x + n * ldx);
   const uint4 *wr = reinterpret_cast<const uint4 *>(w + (known ? t : 0) * ldw);
@@ -281,7 +354,22 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
     e[int64_t(i) * lde + st.target[i]] = __float2bfloat16_rn(-s * st.slope[i]);
 }
 
-// loss = sum of w_n loss_n / divisor over the tokens that count.
+// loss = sum of w_n loss_n / divisor over the tokens that count, by one block.
+__device__ __forceinline__ void mean_loss(const Tokens &tk, const LossHead *head,
+                                          const int *__restrict__ live,
+                                          const float *__restrict__ losses, float *__restrict__ loss,
+                                          Pair *slot) {
+  const int n = head->live;
+  const float divisor = head->divisor;
+  Pair s = {0.f, 0.f};
+#pragma unroll 4
+  for (int k = threadIdx.x; k < n; k += blockDim.x) {
+    const int t = live[k];
+    s = plus(s, times(losses[t], tk.weights != nullptr ? tk.weights[t] : 1.f));
+  }
+  s = block_sum(s, slot);
+  if (threadIdx.x == 0) loss[0] = s.hi / divisor;
+}
 __global__ void __launch_bounds__(1024) k_loss_mean(Tokens tk, const LossHead *head,
                                                     const int *__restrict__ live,
                                                     const float *__restrict__ losses,
@@ -289,16 +377,65 @@ __global__ void __launch_bounds__(1024) k_loss_mean(Tokens tk, const LossHead *h
   __shared__ Pair slot[32];
   griddep_wait();
   griddep_launch_dependents();
-  const int n = head->live;
-  const float divisor = head->divisor;
-  Pair s = {0.f, 0.f};
-#pragma unroll 4
-  for (int k = threadIdx.x; k < n; k += 1024) {
-    const int t = live[k];
-    s = plus(s, times(losses[t], tk.weights != nullptr ? tk.weights[t] : 1.f));
+  mean_loss(tk, head, live, losses, loss, slot);
+}
+
+// Ranges of the second product -> dX: a block takes 32 rows and 32 columns of a cut
+// tile, a thread four of them over all ranges (in their order, eight loads of each
+// four on their way), and writes whole 64-byte pieces.  (64 columns a block left most
+// SMs idle where there are few tiles and many ranges: 20 us for 31 ranges of 2
+// tiles.)  The last block takes the mean loss, when the last strip's is there.
+constexpr int JOIN_COLS = 32, JOIN_ROWS = 32, JOIN_HALF = kLossTileM / 2;  // rows of a CTA's half of a tile
+__global__ void __launch_bounds__(256) k_loss_join(const __grid_constant__ LossGemm g, int pairs,
+                                                   Tokens tk, const int *__restrict__ live,
+                                                   const float *__restrict__ losses,
+                                                   float *__restrict__ loss) {
+  __shared__ float sums[JOIN_COLS][JOIN_ROWS + 1];
+  __shared__ Pair mean_slot[8];
+  griddep_wait();
+  griddep_launch_dependents();
+  const int joiners = gridDim.x - 1;
+  if (static_cast<int>(blockIdx.x) == joiners) {
+    if (loss != nullptr) mean_loss(tk, g.head, live, losses, loss, mean_slot);  // after the last strip
+    return;
   }
-  s = block_sum(s, slot);
-  if (threadIdx.x == 0) loss[0] = s.hi / divisor;
+  const int M = max(0, min(g.strip, g.head->live - g.first));
+  const int m_pairs = (M + kLossTileM - 1) / kLossTileM, n_tiles = (g.n + kLossTileN - 1) / kLossTileN;
+  const int kb = (g.k + kLossBlockK - 1) / kLossBlockK;
+  const LossShare share = loss_share(m_pairs * n_tiles, pairs, kb);
+  constexpr int PER_TILE = (kLossTileM / JOIN_ROWS) * (kLossTileN / JOIN_COLS);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  for (int u = blockIdx.x; u < share.rest * PER_TILE; u += joiners) {
+    const int tile = share.whole + u / PER_TILE;
+    int slot = 0;
+    const int ranges = loss_ranges(share, tile, slot);
+    if (ranges < 2) return;  // none is cut
+    const int part = u % PER_TILE, c0 = part % (kLossTileN / JOIN_COLS) * JOIN_COLS;
+    const int r0 = part / (kLossTileN / JOIN_COLS) * JOIN_ROWS;  // of the tile's 256
+    int mp, nb;
+    loss_tile(tile, m_pairs, n_tiles, g.group, mp, nb);
+    const int row0 = mp * kLossTileM + r0, col0 = nb * kLossTileN + c0;
+    if (row0 >= M || col0 >= g.n) continue;  // the same in the whole block
+    const float *in = g.slots + size_t(slot) * kLossSlotFloats + size_t(r0 / JOIN_HALF) * (JOIN_HALF * kLossTileN) +
+                      size_t(c0) * JOIN_HALF + r0 % JOIN_HALF + lane;
+    float s[JOIN_COLS / 8];
+#pragma unroll
+    for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < ranges; ++k)
+#pragma unroll
+      for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] += in[k * kLossSlotFloats + (j * 8 + w) * JOIN_HALF];
+    const float f = row0 + lane < M ? g.scale[row0 + lane] : 0.f;
+    __syncthreads();  // the last unit's sums are out
+#pragma unroll
+    for (int j = 0; j < JOIN_COLS / 8; ++j) sums[j * 8 + w][lane] = s[j] * f;
+    __syncthreads();
+    // eight threads a row, four columns each
+    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
+    if (row0 + r < M && col0 + c < g.n)  // n is a multiple of 8
+      *reinterpret_cast<uint2 *>(g.out + int64_t(g.place[row0 + r]) * g.ldo + col0 + c) =
+          make_uint2(loss_pack(sums[c][r], sums[c + 1][r]), loss_pack(sums[c + 2][r], sums[c + 3][r]));
+  }
 }
 
 __global__ void __launch_bounds__(256) k_loss_scale(const __nv_bfloat16 *dx, int64_t ldi,
@@ -452,9 +589,11 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
   const Tokens tk = {targets, sh->target_bits == 64, weights, sh->rows};
   auto *head = reinterpret_cast<LossHead *>(at(workspace, p.head));
   int *live = reinterpret_cast<int *>(at(workspace, p.live));
-  LORA_TRY(run(LORA_K_LOSS_PREP, st, "loss index", [&] {
-    return launch_pdl(k_loss_index, dim3(1), dim3(1024), 0, st, tk, int(sh->mean), head, live, losses);
-  }));
+  const bool own_index = sh->rows > 0 && sh->rows <= kFewTokens;
+  if (!own_index)
+    LORA_TRY(run(LORA_K_LOSS_PREP, st, "loss index", [&] {
+      return launch_pdl(k_loss_index, dim3(1), dim3(1024), 0, st, tk, int(sh->mean), head, live, losses);
+    }));
   const auto *x = static_cast<const __nv_bfloat16 *>(X), *w = static_cast<const __nv_bfloat16 *>(W);
   auto *xs = reinterpret_cast<__nv_bfloat16 *>(at(workspace, p.xs));
   auto *parts = reinterpret_cast<LossPart *>(at(workspace, p.parts));
@@ -475,10 +614,10 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
     LORA_TRY(run(LORA_K_LOSS_PREP, st, "loss gather", [&] {
       const int64_t here = sh->rows - first < p.strip ? sh->rows - first : p.strip;
       // (a warp a token: 16 us for 2048 of 4096 elements, 6 for 150 of 1000; a block: 10, 3)
-      const bool wide = sh->dim >= 1024 || here <= 4 * di.sms;
-      return launch_pdl(wide ? k_loss_gather<8> : k_loss_gather<1>,
-                        dim3(static_cast<unsigned>(wide ? here : (here + 7) / 8)), dim3(256), 0, st, tk, s,
-                        w, ldw, sh->vocab, x, ldx, xs, static_cast<__nv_bfloat16 *>(dX), lddx,
+      const bool wide = sh->dim >= 1024 || own_index;
+      auto k = own_index ? k_loss_gather<8, true> : wide ? k_loss_gather<8, false> : k_loss_gather<1, false>;
+      return launch_pdl(k, dim3(static_cast<unsigned>(wide ? here : (here + 7) / 8)), dim3(256), 0, st, tk,
+                        int(sh->mean), head, live, losses, s, w, ldw, sh->vocab, x, ldx, xs, static_cast<__nv_bfloat16 *>(dX), lddx,
                         int(sh->dim), sh->softcap);
     }));
     LossGemm g;
@@ -517,9 +656,13 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
     g.ldo = lddx;
     g.slots = reinterpret_cast<float *>(at(workspace, p.ranges));
     LORA_TRY(run(LORA_K_LOSS_GRAD, st, "loss gradient", [&] { return launch_loss_gemm(2, g, pairs, st); }));
-    LORA_TRY(run(LORA_K_LOSS_GRAD, st, "loss gradient join",
-                 [&] { return launch_loss_join(g, pairs, st); }));
+    float *last = first + p.strip >= sh->rows ? loss : nullptr;
+    LORA_TRY(run(LORA_K_LOSS_GRAD, st, "loss gradient join", [&] {
+      return launch_pdl(k_loss_join, dim3(static_cast<unsigned>(di.sms * 8 + 1)), dim3(256), 0, st, g, pairs,
+                        tk, live, losses, last);
+    }));
   }
+  if (grad) return LORA_OK;
   return run(LORA_K_LOSS_ROWS, st, "loss mean", [&] {
     return launch_pdl(k_loss_mean, dim3(1), dim3(1024), 0, st, tk, head, live, losses, loss);
   });

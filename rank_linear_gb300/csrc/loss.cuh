@@ -10,6 +10,7 @@
 namespace lora {
 
 constexpr int kLossTileM = 256, kLossTileN = 512;  // of a CTA pair
+constexpr int kLossBlockK = 64;                    // length of a block of the products
 constexpr int kLossPiece = 128;                    // columns of one partial sum
 constexpr int kLossMaxPairs = 76;                  // of 152 SMs
 constexpr size_t kLossSlotFloats = size_t(kLossTileM) * kLossTileN;
@@ -145,7 +146,11 @@ struct LossGemm {
 cudaError_t launch_loss_gemm(int kind, const LossGemm &g, int pairs, cudaStream_t s);
 // CTA pairs that are resident at once (at most kLossMaxPairs).
 int loss_pairs(int num_sms);
-cudaError_t launch_loss_join(const LossGemm &g, int pairs, cudaStream_t s);
+
+__device__ __forceinline__ uint32_t loss_pack(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t *>(&v);
+}
 
 // c(z) = cap tanh(z / cap) and c'(z), to a few 2^-23 of their size at any cap:
 // for |z| <= cap / 4 the series of tanh (its next term is below 2^-26), beyond

@@ -28,7 +28,7 @@
 namespace lora {
 namespace {
 
-constexpr int BM = 128, BK = 64, BN = 256;  // rows of a CTA; K block; width of one MMA
+constexpr int BM = kLossTileM / 2, BK = kLossBlockK, BN = 256;  // rows of a CTA; K block; width of one MMA
 constexpr int TN = kLossTileN;
 constexpr int CLUSTER = 2;
 constexpr uint16_t PAIR_MASK = 0x3;
@@ -54,10 +54,6 @@ struct __align__(16) Tail {
 constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE_BYTES + EPI_WARPS * EPI_WARP_BYTES + sizeof(Tail);
 static_assert(SMEM <= 227 * 1024, "shared memory per CTA");
 
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t *>(&v);
-}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -70,8 +66,8 @@ __device__ __forceinline__ void stage64(const float *v, uint8_t *stage, int lane
   const int sw = lane & 7;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
-    my[i ^ sw] = make_uint4(pack2(v[8 * i], v[8 * i + 1]), pack2(v[8 * i + 2], v[8 * i + 3]),
-                            pack2(v[8 * i + 4], v[8 * i + 5]), pack2(v[8 * i + 6], v[8 * i + 7]));
+    my[i ^ sw] = make_uint4(loss_pack(v[8 * i], v[8 * i + 1]), loss_pack(v[8 * i + 2], v[8 * i + 3]),
+                            loss_pack(v[8 * i + 4], v[8 * i + 5]), loss_pack(v[8 * i + 6], v[8 * i + 7]));
 }
 
 // The first product's drain of 128 columns of a row (in v): sums, and
@@ -494,55 +490,6 @@ __global__ void __launch_bounds__(THREADS, 1)
   }
 }
 
-// Ranges of the second product -> dX: a block takes 32 rows and 32 columns of a
-// cut tile, a thread four of them over all ranges (in their order, eight loads of
-// each four on their way), and writes whole 64-byte pieces.  (64 columns a block
-// left most SMs idle where there are few tiles and many ranges: 20 us for 31 ranges
-// of 2 tiles.)
-constexpr int JOIN_COLS = 32, JOIN_ROWS = 32;
-__global__ void __launch_bounds__(256) k_loss_join(const __grid_constant__ LossGemm g, int pairs) {
-  __shared__ float sums[JOIN_COLS][JOIN_ROWS + 1];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int M = max(0, min(g.strip, g.head->live - g.first));
-  const int m_pairs = (M + kLossTileM - 1) / kLossTileM, n_tiles = (g.n + TN - 1) / TN;
-  const int kb = (g.k + BK - 1) / BK;
-  const LossShare share = loss_share(m_pairs * n_tiles, pairs, kb);
-  constexpr int PER_TILE = (kLossTileM / JOIN_ROWS) * (TN / JOIN_COLS);
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  for (int u = blockIdx.x; u < share.rest * PER_TILE; u += gridDim.x) {
-    const int tile = share.whole + u / PER_TILE;
-    int slot = 0;
-    const int ranges = loss_ranges(share, tile, slot);
-    if (ranges < 2) return;  // none is cut
-    const int part = u % PER_TILE, c0 = part % (TN / JOIN_COLS) * JOIN_COLS;
-    const int r0 = part / (TN / JOIN_COLS) * JOIN_ROWS;  // of the tile's 256
-    int mp, nb;
-    loss_tile(tile, m_pairs, n_tiles, g.group, mp, nb);
-    const int row0 = mp * kLossTileM + r0, col0 = nb * TN + c0;
-    if (row0 >= M || col0 >= g.n) continue;  // the same in the whole block
-    const float *in = g.slots + size_t(slot) * kLossSlotFloats + size_t(r0 / BM) * (BM * TN) +
-                      size_t(c0) * BM + r0 % BM + lane;
-    float s[JOIN_COLS / 8];
-#pragma unroll
-    for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < ranges; ++k)
-#pragma unroll
-      for (int j = 0; j < JOIN_COLS / 8; ++j) s[j] += in[k * kLossSlotFloats + (j * 8 + w) * BM];
-    const float f = row0 + lane < M ? g.scale[row0 + lane] : 0.f;
-    __syncthreads();  // the last unit's sums are out
-#pragma unroll
-    for (int j = 0; j < JOIN_COLS / 8; ++j) sums[j * 8 + w][lane] = s[j] * f;
-    __syncthreads();
-    // eight threads a row, four columns each
-    const int r = threadIdx.x >> 3, c = (threadIdx.x & 7) * 4;
-    if (row0 + r < M && col0 + c < g.n)  // n is a multiple of 8
-      *reinterpret_cast<uint2 *>(g.out + int64_t(g.place[row0 + r]) * g.ldo + col0 + c) =
-          make_uint2(pack2(sums[c][r], sums[c + 1][r]), pack2(sums[c + 2][r], sums[c + 3][r]));
-  }
-}
-
 template <int KIND, bool CAP>
 cudaError_t launch(const LossGemm &g, int pairs, cudaStream_t s) {
   static std::atomic<uint64_t> allowed{0};
@@ -577,10 +524,6 @@ cudaError_t launch_loss_gemm(int kind, const LossGemm &g, int pairs, cudaStream_
   if (kind == 2) return launch<2, false>(g, pairs, s);
   if (g.cap > 0.f) return kind == 1 ? launch<1, true>(g, pairs, s) : launch<0, true>(g, pairs, s);
   return kind == 1 ? launch<1, false>(g, pairs, s) : launch<0, false>(g, pairs, s);
-}
-
-cudaError_t launch_loss_join(const LossGemm &g, int pairs, cudaStream_t s) {
-  return launch_pdl(k_loss_join, dim3(152 * 8), dim3(256), 0, s, g, pairs);
 }
 
 }  // namespace lora

@@ -54,6 +54,14 @@ def _make(X, W, targets, weights, softcap, mean, dX, losses):
     return sh, need
 
 
+def _workspace(workspace, need, X):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
+    if workspace.device != X.device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the device of X")
+    return workspace
+
+
 def cross_entropy_forward(X, W, targets, *, weights=None, softcap=0.0, reduction="mean",
                           gradient=False, loss=None, losses=None, dX=None, workspace=None,
                           stream=None):
@@ -73,23 +81,28 @@ def cross_entropy_forward(X, W, targets, *, weights=None, softcap=0.0, reduction
     if reduction not in ("mean", "sum"):
         raise ValueError(f"reduction {reduction!r} is not 'mean' or 'sum'")
     gradient, softcap = bool(gradient) or dX is not None, float(softcap or 0.0)
-    with _on(stream):
-        key = ("loss", _layout(X), _layout(W), _layout(targets), _layout(weights), _layout(dX),
-               _layout(losses), softcap, reduction, gradient)
-        if gradient and dX is None:
-            dX = _empty_like(X)
-        if losses is None:
-            losses = torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device)
-        if loss is None:
-            loss = torch.empty((), dtype=torch.float32, device=X.device)
-        elif loss.dtype != torch.float32 or loss.numel() != 1 or loss.device != X.device:
-            raise ValueError("loss must be one float32 on the device of X")
-        sh, need = _block(key, lambda: _make(X, W, targets, weights, softcap, reduction == "mean",
-                                             dX, losses))
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=X.device) if need else None
-        elif workspace.device != X.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the device of X")
+    # (outputs made here have the layouts that X's decides)
+    key = ("loss", _layout(X), _layout(W), _layout(targets), _layout(weights), _layout(dX),
+           _layout(losses), softcap, reduction, gradient)
+    if loss is not None and (loss.dtype != torch.float32 or loss.numel() != 1 or loss.device != X.device):
+        raise ValueError("loss must be one float32 on the device of X")
+
+    def buffers():
+        return (torch.empty((), dtype=torch.float32, device=X.device) if loss is None else loss,
+                torch.empty(X.shape[:-1], dtype=torch.float32, device=X.device) if losses is None else losses,
+                _empty_like(X) if gradient and dX is None else dX)
+
+    def make():
+        return _make(X, W, targets, weights, softcap, reduction == "mean", dX, losses)
+    if stream is None:
+        loss, losses, dX = buffers()
+        sh, need = _block(key, make)
+        workspace = _workspace(workspace, need, X)
+    else:
+        with _on(stream):
+            loss, losses, dX = buffers()
+            sh, need = _block(key, make)
+            workspace = _workspace(workspace, need, X)
     st = _lib.lib().lora_loss(ctypes.byref(sh), _ptr(X), _ptr(W), _ptr(targets), _ptr(weights),
                               _ptr(loss), _ptr(losses), _ptr(dX), _ptr(workspace),
                               0 if workspace is None else workspace.numel() * workspace.element_size(),

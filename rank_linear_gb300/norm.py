@@ -120,30 +120,38 @@ def rms_norm_backward(dy, h, weight, rstd, *, dh=None, dropout=0.0, seed=0, offs
     drop = _drop_block(dropout, seed, offset, dy.device)
     if drop is None and dresidual is not None:
         raise ValueError("without dropout dresidual is dx")
-    with _on(stream):
-        key = ("norm backward", _layout(dy), _layout(h), _layout(weight), _layout(rstd), _layout(dh),
-               _layout(dx), _layout(dresidual), _layout(dweight), drop is None, need_dweight)
-        if dx is None:
-            dx = _empty_like(dy)
-        if dresidual is None and drop is not None:
-            dresidual = _empty_like(dy)
-        if need_dweight and dweight is None:
-            dweight = torch.empty_like(weight)
+    # (gradients made here have the layouts that dy's decides)
+    key = ("norm backward", _layout(dy), _layout(h), _layout(weight), _layout(rstd), _layout(dh),
+           _layout(dx), _layout(dresidual), _layout(dweight), drop is None, need_dweight)
 
-        def make():
-            given = {"dy": dy, "h": h, "dh": dh, "dx": dx, "dresidual": dresidual}
-            sh, dtype = _make(dy, weight, 0.0, {n: t for n, t in given.items() if t is not None})
-            _row_floats(rstd, "rstd", dy)
-            if need_dweight:
-                _check_weight(dweight, dy, "dweight")
-                if dweight.dtype != weight.dtype:
-                    raise TypeError(f"dweight is {dweight.dtype}, not {weight.dtype}")
-            return sh, dtype, _lib.lib().lora_norm_workspace_bytes(ctypes.byref(sh), int(need_dweight))
+    def buffers():
+        return (_empty_like(dy) if dx is None else dx,
+                _empty_like(dy) if dresidual is None and drop is not None else dresidual,
+                torch.empty_like(weight) if need_dweight and dweight is None else dweight)
+
+    def make():
+        given = {"dy": dy, "h": h, "dh": dh, "dx": dx, "dresidual": dresidual}
+        sh, dtype = _make(dy, weight, 0.0, {n: t for n, t in given.items() if t is not None})
+        _row_floats(rstd, "rstd", dy)
+        if need_dweight:
+            _check_weight(dweight, dy, "dweight")
+            if dweight.dtype != weight.dtype:
+                raise TypeError(f"dweight is {dweight.dtype}, not {weight.dtype}")
+        return sh, dtype, _lib.lib().lora_norm_workspace_bytes(ctypes.byref(sh), int(need_dweight))
+
+    def scratch():
+        return torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
+    if workspace is not None and (workspace.device != dy.device or not workspace.is_contiguous()):
+        raise ValueError("workspace must be a contiguous tensor on the device of dy")
+    if stream is None:
+        dx, dresidual, dweight = buffers()
         sh, dtype, need = _block(key, make)
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dy.device) if need else None
-        elif workspace.device != dy.device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on the device of dy")
+        workspace = scratch() if workspace is None else workspace
+    else:
+        with _on(stream):
+            dx, dresidual, dweight = buffers()
+            sh, dtype, need = _block(key, make)
+            workspace = scratch() if workspace is None else workspace
     st = _lib.lib().lora_norm_bwd(ctypes.byref(sh), _ptr(dy), _ptr(h), _ptr(weight), _ptr(rstd),
                                   _ptr(dh), None if drop is None else ctypes.byref(drop), dtype,
                                   _ptr(dx), _ptr(dresidual), _ptr(dweight) if need_dweight else None,
