@@ -159,7 +159,7 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
   a.eps = sh->eps;
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   const int tensors = residual != nullptr ? 2 : 1;
-  NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, ts.vec, codes != nullptr);
+  NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, ts.vec, false, codes != nullptr);
   NormRows *of[4] = {&a.sx, &a.sr, &a.sh, &a.sy};
   const bool given[4] = {true, residual != nullptr, h != nullptr, y != nullptr};
   use_heads(sh, ts.vec, ts.es, tensors, of, given, 4, a.inner, s);
@@ -180,12 +180,12 @@ size_t lora_norm_workspace_bytes(const lora_norm_t *sh, int with_dw) {
   for (int es = 2; es <= 4; es += 2)
     for (int tensors = 2; tensors <= 3; ++tensors) {
       for (int vec = 0; vec < 2; ++vec) {
-        const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, vec != 0), rows);
+        const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, vec != 0, true), rows);
         most = n > most ? n : most;
       }
-  // (narrow rows side by side: eight blocks an SM at most, of two rows at least)
+  // (narrow rows side by side: twelve blocks an SM at most, of two rows at least)
   if (sh->dim <= 256 && !norm_few_rows(rows / 2)) {
-    const int64_t n = rows / 2 < kSms * 8 ? rows / 2 : kSms * 8;
+    const int64_t n = rows / 2 < kSms * 12 ? rows / 2 : kSms * 12;
     most = n > most ? static_cast<int>(n) : most;
   }
     }
@@ -228,7 +228,7 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
     vec = ts.vec;
   }
   const int es = dtype == LORA_BF16 ? 2 : 4;
-  NormSplit s = norm_split(sh->dim, rows, es, tensors, vec);
+  NormSplit s = norm_split(sh->dim, rows, es, tensors, vec, true);
   a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   NormRows *of[5] = {&a.sdy, &a.sh, &a.sdx, &a.sdh, &a.sdr};
   const bool given[5] = {true, true, true, dh != nullptr, dresidual != nullptr};

@@ -85,31 +85,38 @@ struct NormSplit {
 };
 constexpr int kSms = 152;
 constexpr int kRingSmem = 220 * 1024;  // of an SM's, left to its blocks' rings
-// Threads of the ring's blocks on an SM: at 80 registers each, or 128 where rows are
-// not aligned (at 80 they spill: 5331 x 2001 in fp32, both directions, took 114 us
-// instead of 80).
-__host__ __device__ constexpr int ring_threads(bool vec) { return vec ? 768 : 512; }
+// The ring's blocks on an SM, by their threads: at 80 registers a thread, or 128 (96
+// in blocks of over 256 threads) where rows are not aligned (at 80 they spill: 5331 x
+// 2001 in fp32, both directions, took 114 us instead of 80).
+__host__ __device__ constexpr int ring_blocks(int threads, bool vec) {
+  return threads <= 256 ? (vec ? 768 : 512) / threads : threads <= (vec ? 384 : 320) ? 2 : 1;
+}
+
+// Narrow rows that a group has on their way at once straight into registers (four
+// whose elements come one by one take all of them).
+__host__ __device__ constexpr int narrow_rows(bool vec) { return vec ? 4 : 2; }
 
 // Few rows (two an SM at most): as many threads as there are vectors.
 inline bool norm_few_rows(int64_t rows) { return rows <= 2 * kSms; }
 
 // tensors: that are read a row; threads: of an SM.
-inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec, bool codes = false) {
+inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec, bool backward,
+                            bool codes = false) {
   const bool wide_codes = codes && es == 4;  // (codes of fp32 rows: not over the ring)
   NormSplit s = {};
   const int vectors = (dim + 7) / 8;
   s.nr = 1;
   if (norm_few_rows(rows) && vectors <= 1024) {
     s.vpt = 1;
-  } else if (dim > 1024) {
+  } else if (dim > (vec && !backward ? 1024 : 512)) {
     s.vpt = kRingVectors;
     s.group = s.block = ((vectors + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.per_block = 1;
     // (a row may begin and end inside 16 bytes)
     s.buffer = static_cast<uint32_t>((dim * es + 15) / 16 * 16 + 16);
     const int stage = static_cast<int>(s.buffer) * tensors;
-    s.blocks_sm = s.block > (vec ? 384 : 256) ? 1 : ring_threads(vec) / s.block;
-    if (s.blocks_sm > 8) s.blocks_sm = 8;
+    s.blocks_sm = ring_blocks(s.block, vec);
+    if (s.blocks_sm > 12) s.blocks_sm = 12;
     for (; s.blocks_sm > 0; --s.blocks_sm) {
       s.stages = (kRingSmem / s.blocks_sm - 1024 - kRingHead) / stage;
       if (s.stages >= 2) break;
@@ -120,7 +127,7 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec
     s.vpt = 4;
   } else {
     s.vpt = vectors > 32 ? 4 : 1;
-    if (s.vpt == 1) s.nr = 4;
+    if (s.vpt == 1) s.nr = narrow_rows(vec);
   }
   const int threads = (vectors + s.vpt - 1) / s.vpt;
   if (threads <= 32) {
@@ -141,7 +148,7 @@ inline bool norm_heads(int dim, int64_t outer, int64_t inner, int es, int tensor
   const int64_t wide = inner * dim;
   if (dim % 8 != 0 || lanes > 32 || (lanes & (lanes - 1)) != 0 || inner < 2 || wide <= 1024 || wide > 6144)
     return false;
-  const NormSplit t = norm_split(static_cast<int>(wide), outer, es, tensors, true);
+  const NormSplit t = norm_split(static_cast<int>(wide), outer, es, tensors, true, true);
   if (!t.ring || t.block > 384) return false;
   s = t;
   s.ring = false;

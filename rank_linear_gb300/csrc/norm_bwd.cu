@@ -308,9 +308,9 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float *__restrict__ parti
 template <class T, bool AL, bool DROP>
 cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
-  constexpr int THREADS = ring_threads(AL);
-  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, THREADS / 256>
-           : s.block <= 384 ? k_norm_bwd_ring<T, AL, DROP, 384, THREADS / 384>
+  constexpr int MID = AL ? 384 : 320;
+  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, ring_blocks(256, AL)>
+           : s.block <= MID ? k_norm_bwd_ring<T, AL, DROP, MID, ring_blocks(MID, AL)>
                             : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
 }
@@ -328,7 +328,8 @@ cudaError_t launch_any(const NormBwdArgs &a, const NormSplit &s, int tensors, un
   if (s.ring)
     return a.dropped ? launch_bwd_ring<T, AL, true>(a, s, tensors, status, st)
                      : launch_bwd_ring<T, AL, false>(a, s, tensors, status, st);
-  auto k = s.nr == 4    ? k_norm_bwd<T, 1, AL, 4, kSmallBlock>
+  constexpr int NR = narrow_rows(AL);
+  auto k = s.nr == NR   ? k_norm_bwd<T, 1, AL, NR, kSmallBlock>
            : s.vpt == 1 ? k_norm_bwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_bwd<T, 4, AL, 1, kSmallBlock>
                                     : k_norm_bwd<T, 4, AL, 1, 1024>;

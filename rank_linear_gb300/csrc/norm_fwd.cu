@@ -289,9 +289,9 @@ cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensor
                             cudaStream_t st) {
   const int64_t most = int64_t(kSms) * s.blocks_sm;
   const int blocks = static_cast<int>(a.rows < most ? a.rows : most);
-  constexpr int THREADS = ring_threads(AL);
-  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, THREADS / 256>
-           : s.block <= 384 ? k_norm_fwd_ring<T, AL, DROP, FP8, 384, THREADS / 384>
+  constexpr int MID = AL ? 384 : 320;
+  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, ring_blocks(256, AL)>
+           : s.block <= MID ? k_norm_fwd_ring<T, AL, DROP, FP8, MID, ring_blocks(MID, AL)>
                             : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
   return launch_ring(k, blocks, s, tensors, a, status, st);
 }
@@ -316,7 +316,8 @@ cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, un
     return a.dropped ? launch_fwd_ring<T, AL, true, false>(a, s, tensors, status, st)
                      : launch_fwd_ring<T, AL, false, false>(a, s, tensors, status, st);
   }
-  auto k = s.nr == 4    ? k_norm_fwd<T, 1, AL, 4, kSmallBlock>
+  constexpr int NR = narrow_rows(AL);
+  auto k = s.nr == NR   ? k_norm_fwd<T, 1, AL, NR, kSmallBlock>
            : s.vpt == 1 ? k_norm_fwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_fwd<T, 4, AL, 1, kSmallBlock>
                                     : k_norm_fwd<T, 4, AL, 1, 1024>;
