@@ -39,7 +39,7 @@ typedef struct {
     int32_t dim;         /* a multiple of 8, 8 .. 65536                       */
     int32_t target_bits; /* 32 or 64 (signed)                                 */
     int32_t mean;        /* 1: divide by the sum of the weights; 0: do not    */
-    float softcap;       /* 0: none; > 0, finite                              */
+    float softcap;       /* 0: none; else 2^-100 .. 2^100                     */
     int64_t x, w, dx;    /* row strides in elements: multiples of 8, >= dim   */
 } lora_loss_t;
 
@@ -53,7 +53,8 @@ size_t lora_loss_workspace_bytes(const lora_loss_t *shape, int with_dx);
  *   targets    in, device, one integer a token.
  *   weights    in, device, one float a token, or NULL (all 1).
  *   loss       out, device, one float.
- *   losses     out, device, one float a token (not weighted; 0 where t_n < 0).
+ *   losses     out, device, one float a token (not weighted; 0 where t_n < 0);
+ *              not the weights' tensor.
  *   dX         out, device, bf16 [rows, dim], or NULL: the gradient of loss.
  *              It may be X itself (same stride).
  * With no tokens that count, loss is 0.

@@ -517,8 +517,9 @@ lora_status_t check_shape(const lora_loss_t *sh) {
   if (sh->target_bits != 32 && sh->target_bits != 64)
     return fail(LORA_ERR_INVALID_ARG, "target_bits = %d is not 32 or 64", sh->target_bits);
   if ((sh->mean | 1) != 1) return fail(LORA_ERR_INVALID_ARG, "mean is 0 or 1");
-  if (!(sh->softcap >= 0.f) || !std::isfinite(sh->softcap))
-    return fail(LORA_ERR_INVALID_ARG, "softcap = %g is not a finite number >= 0", sh->softcap);
+  // (beyond these its inverse leaves fp32's normal numbers)
+  if (sh->softcap != 0.f && !(sh->softcap >= 0x1p-100f && sh->softcap <= 0x1p100f))
+    return fail(LORA_ERR_INVALID_ARG, "softcap = %g is not 0 or within 2^-100 .. 2^100", sh->softcap);
   return LORA_OK;
 }
 lora_status_t check_rows(const void *p, int64_t stride, int64_t rows, const lora_loss_t *sh,
@@ -579,6 +580,7 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
       return fail(LORA_ERR_INVALID_ARG, "targets or losses is NULL");
     if (!aligned(targets, sh->target_bits / 8) || !aligned(losses, 4) || !aligned(weights, 4))
       return fail(LORA_ERR_INVALID_ARG, "targets, losses or weights is not aligned to its type");
+    if (losses == weights) return fail(LORA_ERR_INVALID_ARG, "losses and weights are the same tensor");
   }
   const bool grad = dX != nullptr && sh->rows > 0;
   const Plan p = make_plan(*sh, grad);

@@ -81,6 +81,8 @@ def cross_entropy_forward(X, W, targets, *, weights=None, softcap=0.0, reduction
     if reduction not in ("mean", "sum"):
         raise ValueError(f"reduction {reduction!r} is not 'mean' or 'sum'")
     gradient, softcap = bool(gradient) or dX is not None, float(softcap or 0.0)
+    if softcap != 0.0 and not 2.0 ** -100 <= softcap <= 2.0 ** 100:
+        raise ValueError(f"softcap = {softcap} is not 0 or within 2^-100 .. 2^100")
     # (outputs made here have the layouts that X's decides)
     key = ("loss", _layout(X), _layout(W), _layout(targets), _layout(weights), _layout(dX),
            _layout(losses), softcap, reduction, gradient)
@@ -174,4 +176,6 @@ def cross_entropy(X, W, targets, *, weights=None, softcap=0.0, reduction="mean")
     """(loss, losses) of cross_entropy_forward, loss with the gradient of X (of any
     strides); losses are values without a gradient.  W and the weights are
     constants: a backward with one that requires a gradient raises."""
+    if not torch.is_grad_enabled():
+        X = X.detach()  # (its gradient is made with the loss: not where none is taken)
     return CrossEntropyFunction.apply(X, W, targets, weights, softcap, reduction)
