@@ -26,6 +26,7 @@ struct Args {
   // thread, and kRows rows; or, where a row has few, 2^lanes threads a row and two rows each.
   uint32_t chunks, segment;
   int lanes;
+  uint32_t groups, inverse;  // k_dropout_shift: groups of segment + 1 threads, a block
   DropArgs drop;
 };
 
@@ -131,8 +132,123 @@ __global__ void __launch_bounds__(256) k_dropout_rows(const __grid_constant__ Ar
   }
 }
 
+// Rows of bf16 that do not begin on 16 bytes, where x and y lie alike past them: a
+// thread takes 16 aligned bytes of four rows, of a row's eight columns from 8 v - m on
+// (m elements lie between the boundary and the row).  It makes the masks of columns
+// 8 v .. 8 v + 7, and has what is before them from its neighbour, by shared memory: a bit
+// an element, one word for the four rows.  A group's first thread makes masks only.
+// ONE: the block is one group (the rows' share of the first two rounds is common).
+// Bound by instructions, at 1.0e12 elements a second: element by element 8191 x 14335
+// took 184 us, so 116 (8192 x 14336, aligned: 91); 1800000 x 65 272, so 159.
+template <bool ONE>
+__global__ void __launch_bounds__(256) k_dropout_shift(const __grid_constant__ Args a) {
+  __shared__ uint32_t masks[256];
+  griddep_wait();
+  griddep_launch_dependents();
+  const DropNow now = drop_now(a.drop);
+  // groups of segment + 1 threads: threadIdx / that, exact below 256
+  const uint32_t group = ONE ? 0 : threadIdx.x * a.inverse >> 16, t = threadIdx.x - group * (a.segment + 1);
+  const uint32_t chunk = blockIdx.x % a.chunks;
+  const int64_t row = (int64_t(blockIdx.x / a.chunks) * (ONE ? 1 : a.groups) + group) * kRows;
+  const int v = static_cast<int>(chunk * a.segment + t) - 1;  // -1: of no column
+  const int n = (ONE ? t > a.segment : group >= a.groups) || row >= a.rows ? 0 : a.rows - row < kRows ? static_cast<int>(a.rows - row) : kRows;
+  const int cols = static_cast<int>(a.cols);
+  const uint64_t x = reinterpret_cast<uint64_t>(a.x), y = reinterpret_cast<uint64_t>(a.y);
+  const uint64_t last = x + (uint64_t(a.rows - 1) * a.xs + a.cols) * 2;  // behind x
+  const bool mine = t > 0;
+  const int64_t at = row * a.xs + 8 * v, to = row * a.ys + 8 * v;
+  const uint32_t base = static_cast<uint32_t>((x >> 1) + row * a.xs), step = static_cast<uint32_t>(a.xs);
+  Raw8<__nv_bfloat16> in[kRows];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int m = static_cast<int>((base + r * step) & 7u), c = 8 * v - m;
+    if (!mine || r >= n || c >= cols) continue;
+    const uint64_t from = x + (at + r * a.xs - m) * 2;
+    const auto *p = reinterpret_cast<const __nv_bfloat16 *>(from);
+    if (from >= x && from + 16 <= last) {  // (may hold the neighbours' elements)
+      in[r].load(p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (k % 2 == 0) in[r].u[k / 2] = 0u;
+        if (c + k >= 0 && c + k < cols) in[r].load1(k, p + k);
+      }
+    }
+  }
+  // word >= T where word + (2^32 - T) carries (T > 0); the last element's bit first
+  uint32_t keep = 0;
+  const uint32_t less = 0u - a.drop.threshold;
+  auto bit = [&](uint32_t word) {
+    uint32_t sum;
+    asm("add.cc.u32 %0, %2, %3;\n\taddc.u32 %1, %4, %4;" : "=r"(sum), "=r"(keep) : "r"(word), "r"(less), "r"(keep));
+  };
+#pragma unroll
+  for (int r = kRows - 1; r >= 0; --r) {
+#pragma unroll
+    for (int h = 1; h >= 0; --h) {
+      const uint4 w = drop_words(a.drop, now, static_cast<uint32_t>(2 * v + h), row + r);
+      bit(w.w), bit(w.z), bit(w.y), bit(w.x);
+    }
+  }
+  masks[threadIdx.x] = keep;
+  __syncthreads();
+  if (!mine) return;
+  const uint32_t before = masks[threadIdx.x - 1];
+#pragma unroll
+  for (int r = 0; r < kRows; ++r) {
+    const int m = static_cast<int>((base + r * step) & 7u), c = 8 * v - m;
+    if (r >= n || c >= cols) continue;
+    uint32_t bits = ((before >> 8 * r & 255u) | (keep >> 8 * r & 255u) << 8) >> (8 - m);
+    bits |= bits << 15;  // elements 2 i and 2 i + 1 at bits 2 i and 16 + 2 i
+    Raw8<__nv_bfloat16> out;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      out.set(i, mul2(in[r].pair(i), both(a.drop.scale)));
+      out.u[i] &= (bits >> 2 * i & 0x10001u) * 0xffffu;
+    }
+    auto *p = reinterpret_cast<__nv_bfloat16 *>(y) + (to + r * a.ys - m);
+    if (c >= 0 && c + 8 <= cols) {
+      out.store(p);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (c + k >= 0 && c + k < cols) out.store1(k, p + k);
+    }
+  }
+}
+
+// (narrower rows leave most threads at a row's ends)
+constexpr uint32_t kShiftCols = 32;
+bool shifted(const Args &a) {
+  return a.drop.threshold > 0 && a.cols >= kShiftCols && a.cols < (1u << 30) &&  // (columns as int)
+         a.xs >= 0 && (reinterpret_cast<uint64_t>(a.x) - reinterpret_cast<uint64_t>(a.y)) % 16 == 0 &&
+         (a.xs - a.ys) % 8 == 0;
+}
+cudaError_t launch_shift(Args a, cudaStream_t s) {
+  const uint32_t vectors = (a.cols + 7 + 7) / 8;  // of a row, at most
+  a.chunks = (vectors + 254) / 255;
+  a.segment = (vectors + a.chunks - 1) / a.chunks;
+  if (a.chunks > 1 || a.segment > 128) {  // the cut that leaves the fewest threads idle
+    auto cost = [&](uint32_t n) { return n * (((vectors + n - 1) / n + 1 + 31) / 32 * 32); };
+    for (uint32_t n = a.chunks + 1, i = 0; i < 8; ++i, ++n)
+      if (cost(n) < cost(a.chunks)) a.chunks = n;
+    a.segment = (vectors + a.chunks - 1) / a.chunks;
+  }
+  a.groups = 256 / (a.segment + 1);
+  // (one group where that leaves few idle threads: 116000 x 1001 took 121 us with two, 116 so)
+  const uint32_t whole = (a.segment + 1 + 31) / 32 * 32;
+  if (a.chunks > 1 || (whole > 64 && 8 * (a.segment + 1) >= 7 * whole)) a.groups = 1;
+  a.inverse = (65536 + a.segment) / (a.segment + 1);
+  const unsigned threads = (a.groups * (a.segment + 1) + 31) / 32 * 32;
+  const int64_t per = int64_t(kRows) * a.groups;
+  return launch_pdl(a.groups == 1 ? k_dropout_shift<true> : k_dropout_shift<false>, dim3(static_cast<unsigned>((a.rows + per - 1) / per * a.chunks)),
+                    dim3(threads), 0, s, a);
+}
+
 template <class T, bool VEC>
 cudaError_t launch_dropout(Args a, cudaStream_t s) {
+  if constexpr (sizeof(T) == 2 && !VEC)
+    if (shifted(a)) return launch_shift(a, s);
   a.units = VEC ? a.cols / 8 : (a.cols + 3) / 4;
   if (a.units <= 128) {
     a.lanes = 0;

@@ -135,3 +135,36 @@ def test_other_stream_and_nothing():
     assert rl.dropout_forward(x[:, :0], 0.5, 1).shape == (100, 0)
     with pytest.raises(TypeError):
         rl.dropout_forward(x.double(), 0.5, 1)
+
+
+@pytest.mark.parametrize("cols", [192, 193, 255, 1001, 2033, 2034, 2046, 4099])
+@pytest.mark.parametrize("lead", [0, 1, 7])
+def test_rows_off_the_16_byte_boundaries(cols, lead):
+    """bf16 rows whose x and y lie alike past a boundary (aligned pieces, masks shifted), and
+    differently (element by element); strides that move the boundary from row to row or not."""
+    g = torch.Generator(device=DEV).manual_seed(cols)
+    for pad in (0, 1, 8 - cols % 8):
+        step = cols + pad
+        room = torch.randn(11 * step + lead + 1, generator=g, device=DEV).bfloat16()
+        x = room[lead:].as_strided((11, cols), (step, 1))
+        want = rl.dropout_forward(x.float().contiguous(), 0.4, SEED, 5).bfloat16()
+        check(x, want, 0.4, SEED, 5)
+        for off in (lead, lead + 1):
+            out = torch.full_like(room, 7.0)
+            y = out[off:].as_strided((11, cols), (step, 1)) if off + 10 * step + cols <= out.numel() else None
+            if y is None:
+                continue
+            rl.dropout_forward(x, 0.4, SEED, 5, out=y)
+            check(x, y, 0.4, SEED, 5)
+            y.fill_(7.0)
+            assert torch.all(out == 7.0)  # nothing beside the rows was written
+        words = torch.tensor([77, 3], device=DEV)
+        assert torch.equal(rl.dropout_forward(x, 0.1, words, 1), rl.dropout_forward(x.contiguous(), 0.1, 77, 4))
+        bad = x.clone()
+        bad[:, ::5] = float("nan")
+        y = rl.dropout_forward(bad, 0.5, 3)
+        keep = rl.dropout_forward(torch.ones_like(bad), 0.5, 3) != 0
+        assert torch.all(y[~keep] == 0) and torch.equal(y.isnan(), bad.isnan() & keep)
+        rl.dropout_forward(x, 0.4, SEED, 5, out=x)  # in place
+        check_again = torch.where(want == 0, 0.0, x.float())
+        assert torch.equal(check_again, x.float())
