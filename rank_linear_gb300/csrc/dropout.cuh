@@ -153,7 +153,6 @@ struct Raw8<__nv_bfloat16> {
   __device__ __forceinline__ void store1(int i, __nv_bfloat16 *p) const {
     *reinterpret_cast<uint16_t *>(p) = static_cast<uint16_t>(i & 1 ? u[i >> 1] >> 16 : u[i >> 1]);
   }
-  __device__ __forceinline__ void zero1(int i) { u[i >> 1] &= i & 1 ? 0xffffu : 0u; }
 };
 template <>
 struct Raw8<float> {
@@ -172,7 +171,6 @@ struct Raw8<float> {
   }
   __device__ __forceinline__ void load1(int i, const float *p) { (i & 1 ? f[i >> 1].y : f[i >> 1].x) = *p; }
   __device__ __forceinline__ void store1(int i, float *p) const { *p = i & 1 ? f[i >> 1].y : f[i >> 1].x; }
-  __device__ __forceinline__ void zero1(int i) { (i & 1 ? f[i >> 1].y : f[i >> 1].x) = 0.f; }
 };
 
 // Host: the argument block of a checked description (dropout.cu).

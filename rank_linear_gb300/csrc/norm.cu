@@ -163,6 +163,19 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
   NormRows *of[4] = {&a.sx, &a.sr, &a.sh, &a.sy};
   const bool given[4] = {true, residual != nullptr, h != nullptr, y != nullptr};
   use_heads(sh, ts.vec, ts.es, tensors, of, given, 4, a.inner, s);
+  if (s.ring && !ts.vec && !a.dropped && sh->inner == 1 && a.w32 == 0) {
+    NormShift shift;
+    shift.add(x, a.sx.outer, ts.es);
+    if (residual != nullptr) shift.add(residual, a.sr.outer, ts.es);
+    if (h != nullptr) shift.add(h, a.sh.outer, ts.es);
+    if (y != nullptr) shift.add(y, a.sy.outer, ts.es);
+    // (a code is a byte: its row lies as far past 8 bytes as a row of bf16 past 16)
+    if (codes != nullptr &&
+        ((reinterpret_cast<uint64_t>(codes) - reinterpret_cast<uint64_t>(x) / 2) % 8 != 0 || (a.sx.outer - sh->dim) % 8 != 0))
+      shift.ok = false;
+    const NormSplit t = norm_split(sh->dim, rows, ts.es, tensors, false, false, codes != nullptr, true);
+    if (shift.ok && t.ring) s = t;
+  }
   a.group = s.group;
   DevInfo di;
   LORA_TRY(device_info(di));
@@ -183,12 +196,14 @@ size_t lora_norm_workspace_bytes(const lora_norm_t *sh, int with_dw) {
         const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, vec != 0, true), rows);
         most = n > most ? n : most;
       }
+      const int n = norm_bwd_blocks(norm_split(sh->dim, rows, es, tensors, false, true, false, true), rows);
+      most = n > most ? n : most;
+    }
   // (narrow rows side by side: twelve blocks an SM at most, of two rows at least)
   if (sh->dim <= 256 && !norm_few_rows(rows / 2)) {
     const int64_t n = rows / 2 < kSms * 12 ? rows / 2 : kSms * 12;
     most = n > most ? static_cast<int>(n) : most;
   }
-    }
   return size_t(most) * sh->dim * sizeof(float);
 }
 
@@ -229,15 +244,26 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   }
   const int es = dtype == LORA_BF16 ? 2 : 4;
   NormSplit s = norm_split(sh->dim, rows, es, tensors, vec, true);
+  a.dropped = dropout != nullptr && a.drop.threshold != 0;
+  a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   a.inner = norm_inner(sh->inner > 0 ? sh->inner : 1);
   NormRows *of[5] = {&a.sdy, &a.sh, &a.sdx, &a.sdh, &a.sdr};
   const bool given[5] = {true, true, true, dh != nullptr, dresidual != nullptr};
   if (rows > 0) use_heads(sh, vec, es, tensors, of, given, 5, a.inner, s);
+  if (rows > 0 && s.ring && !vec && !a.dropped && sh->inner == 1 && a.w32 == 0) {
+    NormShift shift;
+    shift.add(dy, a.sdy.outer, es);
+    shift.add(h, a.sh.outer, es);
+    shift.add(dx, a.sdx.outer, es);
+    if (dh != nullptr) shift.add(dh, a.sdh.outer, es);
+    if (dresidual != nullptr) shift.add(dresidual, a.sdr.outer, es);
+    const NormSplit t = norm_split(sh->dim, rows, es, tensors, false, true, false, true);
+    if (shift.ok && t.ring) s = t;
+  }
   const int blocks = norm_bwd_blocks(s, s.heads ? rows / a.inner.n : rows);
   if (dw != nullptr)
     LORA_TRY(check_ws(workspace, workspace_bytes, size_t(blocks) * sh->dim * sizeof(float)));
   if (rows == 0 && dw == nullptr) return LORA_OK;
-  a.dropped = dropout != nullptr && a.drop.threshold != 0;
   a.dy = dy;
   a.h = h;
   a.w = w;
@@ -249,7 +275,6 @@ lora_status_t lora_norm_bwd(const lora_norm_t *sh, const void *dy, const void *h
   a.rows = rows;
   a.dim = sh->dim;
   a.inv_dim = 1.f / static_cast<float>(sh->dim);
-  a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   a.group = s.group;
   DevInfo di;
   LORA_TRY(device_info(di));

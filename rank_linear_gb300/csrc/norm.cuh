@@ -69,7 +69,7 @@ struct RingHead {
   uint64_t full[4];
   int abort_flag;
 };
-constexpr int kRingHead = 64;
+constexpr int kRingHead = 64, kRingRoom = 2048;
 
 // Vectors a thread.  A row's work is one chain through its threads (read, sum,
 // barrier, write), so that two vectors a thread and twice the threads take it
@@ -78,17 +78,24 @@ constexpr int kRingVectors = 2;
 
 // How a call runs.
 struct NormSplit {
-  bool ring, heads;
+  bool ring, heads, shifted;
   int group, vpt, nr, block, per_block;  // threads and vectors of a row; rows at a time
   int stages, blocks_sm;                 // of the ring
   uint32_t buffer;                       // bytes of a row in the ring
 };
 constexpr int kSms = 152;
 constexpr int kRingSmem = 220 * 1024;  // of an SM's, left to its blocks' rings
+// How a row lies among its threads: kLoose, its elements one by one; kAligned, vectors;
+// kShifted, vectors of rows off the 16-byte boundaries (the ring's only).
+constexpr int kLoose = 0, kAligned = 1, kShifted = 2;
+
 // The ring's blocks on an SM, by their threads: at 80 registers a thread, or 128 (96
 // in blocks of over 256 threads) where rows are not aligned (at 80 they spill: 5331 x
 // 2001 in fp32, both directions, took 114 us instead of 80).
-__host__ __device__ constexpr int ring_blocks(int threads, bool vec) {
+// Shifted rows of fp32: one over 256 threads (two spill: 4096 x 4095 backward, 77 us).
+__host__ __device__ constexpr int ring_blocks(int threads, int lay, int es) {
+  const bool vec = lay == kAligned || (lay == kShifted && es == 2);
+  if (lay == kShifted && !vec && threads > 256) return 1;
   return threads <= 256 ? (vec ? 768 : 512) / threads : threads <= (vec ? 384 : 320) ? 2 : 1;
 }
 
@@ -99,12 +106,12 @@ __host__ __device__ constexpr int narrow_rows(bool vec) { return vec ? 4 : 2; }
 // Few rows (two an SM at most): as many threads as there are vectors.
 inline bool norm_few_rows(int64_t rows) { return rows <= 2 * kSms; }
 
-// tensors: that are read a row; threads: of an SM.
+// tensors: that are read a row.
 inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec, bool backward,
-                            bool codes = false) {
+                            bool codes = false, bool shifted = false) {
   const bool wide_codes = codes && es == 4;  // (codes of fp32 rows: not over the ring)
   NormSplit s = {};
-  const int vectors = (dim + 7) / 8;
+  const int vectors = (dim + (shifted ? 14 : 7)) / 8;
   s.nr = 1;
   if (norm_few_rows(rows) && vectors <= 1024) {
     s.vpt = 1;
@@ -113,12 +120,13 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec
     s.group = s.block = ((vectors + s.vpt - 1) / s.vpt + 31) / 32 * 32;
     s.per_block = 1;
     // (a row may begin and end inside 16 bytes)
-    s.buffer = static_cast<uint32_t>((dim * es + 15) / 16 * 16 + 16);
+    s.buffer = static_cast<uint32_t>((dim * es + 15) / 16 * 16 + (shifted && es == 4 ? 32 : 16));
     const int stage = static_cast<int>(s.buffer) * tensors;
-    s.blocks_sm = ring_blocks(s.block, vec);
+    s.shifted = shifted;
+    s.blocks_sm = ring_blocks(s.block, vec ? kAligned : shifted ? kShifted : kLoose, es);
     if (s.blocks_sm > 12) s.blocks_sm = 12;
     for (; s.blocks_sm > 0; --s.blocks_sm) {
-      s.stages = (kRingSmem / s.blocks_sm - 1024 - kRingHead) / stage;
+      s.stages = (kRingSmem / s.blocks_sm - 1024 - kRingHead - (shifted ? kRingRoom : 0)) / stage;
       if (s.stages >= 2) break;
     }
     s.ring = s.blocks_sm > 0 && s.block <= 512 && !wide_codes;
@@ -164,6 +172,21 @@ inline int norm_bwd_blocks(const NormSplit &s, int64_t rows) {
   return static_cast<int>(n < most ? n : most);
 }
 
+// Whether a ring's rows can be taken as kShifted: each tensor as far past a 16-byte
+// boundary as the others, row by row, and bf16 weights with bf16 rows.
+struct NormShift {
+  uint64_t at = 0;
+  int64_t step = 0;
+  bool any = false, ok = true;
+  // (rows of an input nearer than 16 bytes would end past the tensor with their last 16)
+  void add(const void *p, int64_t stride, int es) {
+    const uint64_t here = reinterpret_cast<uint64_t>(p) % 16;
+    if (any && (here != at || (stride - step) % (16 / es) != 0)) ok = false;
+    if ((stride < 0 ? -stride : stride) < 16 / es) ok = false;
+    if (!any) at = here, step = stride, any = true;
+  }
+};
+
 cudaError_t launch_norm_fwd(lora_dtype_t dtype, bool vec, const NormFwdArgs &a, const NormSplit &s, int tensors,
                             unsigned *status, cudaStream_t st);
 cudaError_t launch_norm_bwd(lora_dtype_t dtype, bool vec, const NormBwdArgs &a, const NormSplit &s, int tensors,
@@ -184,15 +207,17 @@ __device__ __forceinline__ Where where(int64_t row, const NormInner &inner) {
   return {static_cast<int64_t>(o), static_cast<int64_t>(r - o * inner.n)};
 }
 
-// A row belongs to `group` threads, VPT vectors of eight elements each.  Aligned
-// rows (AL): eight that lie side by side (vector t + j group).  Others: eight that
-// lie `group` apart, so that a warp's accesses cover neighbours.
-template <bool AL>
+// A row belongs to `group` threads, VPT vectors of eight elements each.  kAligned:
+// eight that lie side by side (vector t + j group).  kLoose: eight that lie `group`
+// apart, so that a warp's accesses cover neighbours.  kShifted: as kAligned, counted
+// from the 16-byte boundary that is m elements before the row (the first and the last
+// vector hold some elements of it).
+template <int AL>
 __device__ __forceinline__ int element(int t, int group, int j, int k) {
-  return AL ? (t + j * group) * 8 + k : (j * 8 + k) * group + t;
+  return AL != kLoose ? (t + j * group) * 8 + k : (j * 8 + k) * group + t;
 }
 // Thread t's vectors of a row of `dim` elements at p; zeros past its end.
-template <bool AL, class T, int VPT>
+template <int AL, class T, int VPT>
 __device__ __forceinline__ void fetch(Raw8<T> (&v)[VPT], const T *p, int t, int group, int dim) {
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -214,9 +239,51 @@ __device__ __forceinline__ void fetch(Raw8<T> (&v)[VPT], const T *p, int t, int 
     }
   }
 }
-template <bool AL, class T>
-__device__ __forceinline__ void put(T *p, const Raw8<T> &v, int t, int group, int j, int dim) {
-  if constexpr (AL) {
+// Which elements of a thread's vector are the shifted row's: a bit each.
+template <int VPT>
+__device__ __forceinline__ void own_bits(uint32_t (&own)[VPT], int t, int group, int dim, int m) {
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) {
+    const int c = (t + j * group) * 8 - m;
+    own[j] = c >= dim ? 0u : (c < 0 ? 255u << -c : 255u) & (c + 8 > dim ? 255u >> (c + 8 - dim) : 255u) & 255u;
+  }
+}
+__device__ __forceinline__ void keep_only(Raw8<__nv_bfloat16> &v, uint32_t own) {
+  own |= own << 15;  // elements 2 i and 2 i + 1 at bits 2 i and 16 + 2 i
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v.u[i] &= (own >> 2 * i & 0x10001u) * 0xffffu;
+}
+__device__ __forceinline__ void keep_only(Raw8<float> &v, uint32_t own) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v.f[i] = make_float2(own >> 2 * i & 1u ? v.f[i].x : 0.f, own >> 2 * i & 2u ? v.f[i].y : 0.f);
+}
+// The same of a row off the boundaries, one by one; zeros before and past it.
+template <class T, int VPT>
+__device__ __forceinline__ void fetch_cut(Raw8<T> (&v)[VPT], const T *p, int t, int group, int dim, int m) {
+#pragma unroll
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = element<kShifted>(t, group, j, k) - m;
+      if (k % 2 == 0) v[j].set(k / 2, both(0.f));
+      if (c >= 0 && c < dim) v[j].load1(k, p + c);
+    }
+}
+// (m, own: of shifted rows)
+template <int AL, class T>
+__device__ __forceinline__ void put(T *p, const Raw8<T> &v, int t, int group, int j, int dim, int m = 0,
+                                    uint32_t own = 255u) {
+  if constexpr (AL == kShifted) {
+    T *to = p + ((t + j * group) * 8 - m);
+    if (own == 255u) {
+      v.store(to);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (own >> k & 1u) v.store1(k, to + k);
+    }
+  } else if constexpr (AL == kAligned) {
     const int c = (t + j * group) * 8;
     if (c < dim) v.store(p + c);
   } else {
@@ -227,17 +294,18 @@ __device__ __forceinline__ void put(T *p, const Raw8<T> &v, int t, int group, in
     }
   }
 }
-template <bool AL, class T>
-__device__ __forceinline__ void put(T *p, const float2 (&v)[4], int t, int group, int j, int dim) {
+template <int AL, class T>
+__device__ __forceinline__ void put(T *p, const float2 (&v)[4], int t, int group, int j, int dim, int m = 0,
+                                    uint32_t own = 255u) {
   Raw8<T> r;
 #pragma unroll
   for (int i = 0; i < 4; ++i) r.set(i, v[i]);
-  put<AL>(p, r, t, group, j, dim);
+  put<AL>(p, r, t, group, j, dim, m, own);
 }
 // Drops out vector j.  Where a thread's elements lie `group` apart (a multiple of
 // 32), a warp's 32 neighbours take the words of eight calls of the generator: each
 // lane makes one of those of four steps, and hands the words round.
-template <bool AL>
+template <int AL>
 __device__ __forceinline__ void drop_vector(const DropArgs &d, const DropNow &now, int64_t row, int t,
                                             int group, int j, float2 (&v)[4]) {
   if constexpr (AL) {
@@ -270,24 +338,28 @@ __device__ __forceinline__ void drop_vector(const DropArgs &d, const DropNow &no
 }
 
 // The weight: kept in registers where it is bf16 and KEEP, else read again for each
-// row (from L1: it is the only thing that is read through it).
-template <bool AL, bool KEEP, class T, int VPT>
+// row (from L1: it is the only thing that is read through it).  Always kept where rows
+// are shifted.
+template <int AL, bool KEEP, class T, int VPT>
 struct Weight {
-  static constexpr bool kKeep = KEEP && sizeof(T) == 2;
+  static constexpr bool kKeep = KEEP && (sizeof(T) == 2 || AL == kShifted);
   Raw8<T> kept[kKeep ? VPT : 1];
   const void *from;
   bool wide;  // fp32
-  __device__ __forceinline__ Weight(const void *w, int w32, int t, int group, int dim)
-      : from(w), wide(sizeof(T) == 4 || w32 != 0) {
-    if constexpr (kKeep)
+  __device__ __forceinline__ Weight(const void *w, int w32, int t, int group, int dim, int m = 0)
+      : from(w), wide(AL != kShifted && (sizeof(T) == 4 || w32 != 0)) {
+    if constexpr (kKeep && AL == kShifted) {
+      fetch_cut(kept, static_cast<const T *>(w), t, group, dim, m);
+    } else if constexpr (kKeep) {
       if (!wide) fetch<AL>(kept, static_cast<const T *>(w), t, group, dim);
+    }
   }
   template <class S>
   __device__ __forceinline__ void read(const S *w, int j, int t, int group, int dim, float2 (&u)[4]) const {
     Raw8<S> o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) o.set(i, both(0.f));
-    if constexpr (AL) {
+    if constexpr (AL == kAligned) {
       const int c = (t + j * group) * 8;
       if (c < dim) o.load(w + c);
     } else {
@@ -338,6 +410,12 @@ __device__ __forceinline__ void clear_slots(float *slots, int n) {
   for (int i = threadIdx.x; i < n; i += blockDim.x) slots[i] = 0.f;
 }
 
+// How far a shifted row begins past a boundary; the same for all rows of a block whose
+// step is a multiple of eight.
+template <class T>
+__device__ __forceinline__ int row_shift(const T *row) {
+  return static_cast<int>(reinterpret_cast<uint64_t>(row) / sizeof(T) % (16 / sizeof(T)));
+}
 // ---- the ring ----
 // Stage s of it holds one row of each tensor, a buffer apart; bulk copies fill it
 // and count on full[s].  A copy takes whole 16-byte units: of a row that does not
@@ -354,10 +432,10 @@ struct RowCopy {
   }
 };
 // first, last: the addresses between which the tensor lies.
-template <bool AL, class T>
+template <int AL, class T>
 __device__ __forceinline__ RowCopy<T> row_copy(const T *src, int dim, const NormSpan &span) {
   RowCopy<T> c = {src, 0, 0, dim};
-  if constexpr (!AL) {
+  if constexpr (AL != kAligned) {
     const uint64_t a = reinterpret_cast<uint64_t>(src), end = a + uint64_t(dim) * sizeof(T);
     uint64_t lo = a & ~uint64_t(15), hi = (end + 15) & ~uint64_t(15);
     c.lead = static_cast<int>((a - lo) / sizeof(T));
@@ -381,11 +459,11 @@ __device__ __forceinline__ void copy_start(const RowCopy<T> &c, uint32_t buf, ui
   if (n > 0) bulk_load(buf + (c.lo > 0 ? 16u : 0u), c.src + (c.lo > 0 ? c.lo : -c.lead), n, bar);
 }
 // Thread t's vectors of a row that has arrived in buf.
-template <bool AL, class T, int VPT>
+template <int AL, class T, int VPT>
 __device__ __forceinline__ void take(Raw8<T> (&v)[VPT], const RowCopy<T> &c, const uint8_t *buf, int t,
                                      int group, int dim) {
   const T *in = reinterpret_cast<const T *>(buf) + c.lead;
-  if constexpr (AL) {
+  if constexpr (AL == kAligned) {
     fetch<true>(v, in, t, group, dim);
   } else if (c.lo <= 0 && c.hi >= dim) {
     fetch<false>(v, in, t, group, dim);
@@ -413,6 +491,64 @@ __device__ __forceinline__ void ring_drain(RingHead *head, int s, uint32_t phase
     if (++s == stages) s = 0, phase ^= 1u;
   }
 }
+// Shifted rows: all copies of a block are of `bytes` from the boundary before a row,
+// but those of the tensor's first and last row, which may not reach so far (row_copy).
+struct ShiftCopy {
+  int m;
+  uint32_t bytes;
+  int64_t rows;
+  template <class T>
+  __device__ __forceinline__ static ShiftCopy of(const T *row, int dim, int64_t rows) {
+    const int m = row_shift(row);
+    return {m, static_cast<uint32_t>((m + dim) * int(sizeof(T)) + 15) / 16 * 16, rows};
+  }
+  __device__ __forceinline__ bool whole(int64_t row) const { return row > 0 && row < rows - 1; }
+};
+template <class T>
+__device__ __forceinline__ uint32_t copy_bytes(const ShiftCopy &c, const T *src, int64_t row, int dim,
+                                               const NormSpan &span) {
+  return c.whole(row) ? c.bytes : row_copy<kShifted>(src, dim, span).bytes();
+}
+template <class T>
+__device__ __forceinline__ void copy_start(const ShiftCopy &c, const T *src, int64_t row, int dim,
+                                           const NormSpan &span, uint32_t buf, uint32_t bar) {
+  if (c.whole(row))
+    bulk_load(buf, src - c.m, c.bytes, bar);
+  else
+    copy_start(row_copy<kShifted>(src, dim, span), buf, bar);
+}
+// Thread t's vectors, as they lie around the row too (only_own takes that away).
+template <class T, int VPT>
+__device__ __forceinline__ void take(Raw8<T> (&v)[VPT], const ShiftCopy &c, const T *src, int64_t row,
+                                     const NormSpan &span, const uint8_t *buf, int t, int group, int dim) {
+  const T *in = reinterpret_cast<const T *>(buf);
+  if (c.whole(row)) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) v[j].load(in + (t + j * group) * 8);  // (there is room behind the ring)
+  } else {
+    const auto r = row_copy<kShifted>(src, dim, span);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const int e = element<kShifted>(t, group, j, k) - c.m;
+        if (k % 2 == 0) v[j].set(k / 2, both(0.f));
+        if (e >= 0 && e < dim) v[j].load1(k, e >= r.lo && e < r.hi ? in + (c.m + e) : src + e);
+      }
+  }
+}
+template <class T, int VPT>
+__device__ __forceinline__ void only_own(Raw8<T> (&v)[VPT], const uint32_t (&own)[VPT]) {
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) keep_only(v[j], own[j]);
+}
+template <int VPT>
+__device__ __forceinline__ bool all_own(const uint32_t (&own)[VPT]) {
+  uint32_t u = 255u;
+#pragma unroll
+  for (int j = 0; j < VPT; ++j) u &= own[j];
+  return u == 255u;
+}
 __device__ __forceinline__ void ring_init(RingHead *head, int stages) {
   if (threadIdx.x == 0) {
     for (int s = 0; s < stages; ++s) mbar_init(smem_u32(&head->full[s]), 1);
@@ -425,7 +561,8 @@ __device__ __forceinline__ void ring_init(RingHead *head, int stages) {
 template <class... P, class A>
 cudaError_t launch_ring(void (*kern)(P...), int blocks, const NormSplit &s, int tensors, const A &a,
                         unsigned *status, cudaStream_t st) {
-  const size_t smem = kRingHead + size_t(s.stages) * tensors * s.buffer;
+  // (threads past the end of a shifted row read on, by 2 KB at most; the SM has it left)
+  const size_t smem = kRingHead + size_t(s.stages) * tensors * s.buffer + (s.shifted ? kRingRoom : 0);
   const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
   if (e != cudaSuccess) return e;

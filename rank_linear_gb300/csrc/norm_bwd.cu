@@ -7,12 +7,13 @@ namespace {
 // ---- backward ----
 // What a row's threads do with it: g = dy w and h r, their mean product, then
 // d = r (g - h r mean) + dh, dropped out where the branch was.
-template <bool AL, bool KEEP, class T, int VPT>
+template <int AL, bool KEEP, class T, int VPT>
 __device__ __forceinline__ void row_backward(const NormBwdArgs &a, const DropNow &now,
                                              const Raw8<T> (&hy)[VPT], const Raw8<T> (&hh)[VPT],
                                              const Raw8<T> (&hd)[VPT], const Weight<AL, KEEP, T, VPT> &w,
                                              float rstd, bool drop, int64_t row, const Where &at, int t,
-                                             int group, int dim, float *slot, float2 (&acc)[VPT][4]) {
+                                             int group, int dim, float *slot, float2 (&acc)[VPT][4], int m = 0,
+                                             const uint32_t *own = nullptr) {
   float2 s = both(0.f);
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -39,15 +40,15 @@ __device__ __forceinline__ void row_backward(const NormBwdArgs &a, const DropNow
       d[i] = fma2(mul2(hy[j].pair(i), u[i]), both(rstd), d[i]);
       if (a.dh != nullptr) d[i] = add2(d[i], hd[j].pair(i));
     }
-    if (a.dres != nullptr) put<AL>(dres, d, t, group, j, dim);
+    if (a.dres != nullptr) put<AL>(dres, d, t, group, j, dim, m, AL == kShifted ? own[j] : 255u);
     if (drop) drop_vector<AL>(a.drop, now, row, t, group, j, d);
-    put<AL>(dx, d, t, group, j, dim);
+    put<AL>(dx, d, t, group, j, dim, m, AL == kShifted ? own[j] : 255u);
   }
 }
 
 // Straight into registers: blocks stay and take NR rows a group at a time; each
 // thread adds up dy h r of its columns over the rows that it took.
-template <class T, int VPT, bool AL, int NR, int MAX>
+template <class T, int VPT, int AL, int NR, int MAX>
 __global__ void __launch_bounds__(MAX) k_norm_bwd(const __grid_constant__ NormBwdArgs a) {
   __shared__ __align__(16) float slots[64];
   __shared__ float cols[kSmallBlock * VPT * 8];  // dw of the groups of a small block
@@ -116,7 +117,7 @@ __global__ void __launch_bounds__(MAX) k_norm_bwd(const __grid_constant__ NormBw
 }
 
 // Over the ring.
-template <class T, bool AL, bool DROP, int MAX, int BLOCKS>
+template <class T, int AL, bool DROP, int MAX, int BLOCKS>
 __global__ void __launch_bounds__(MAX, BLOCKS)
     k_norm_bwd_ring(const __grid_constant__ NormBwdArgs a, int stages, uint32_t buffer, unsigned *status) {
   constexpr int VPT = kRingVectors;
@@ -140,9 +141,22 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   auto copy_d = [&](const Where &at) {
     return row_copy<AL>(static_cast<const T *>(a.dh) + at.at(a.sdh), a.dim, a.span_d);
   };
+  ShiftCopy shift = {};
+  if constexpr (AL == kShifted)
+    shift = ShiftCopy::of(static_cast<const T *>(a.dy) + int64_t(blockIdx.x) * a.sdy.outer, a.dim, a.rows);
   auto start = [&](int64_t row, int s) {
     const Where at = where(row, a.inner);
     const uint32_t bar = smem_u32(&head->full[s]), buf = smem_u32(ring + s * tensors * buffer);
+    if constexpr (AL == kShifted) {
+      const T *y = static_cast<const T *>(a.dy) + at.at(a.sdy), *h = static_cast<const T *>(a.h) + at.at(a.sh);
+      const T *d = static_cast<const T *>(a.dh) + at.at(a.sdh);
+      mbar_expect_tx(bar, copy_bytes(shift, y, row, a.dim, a.span_y) + copy_bytes(shift, h, row, a.dim, a.span_h) +
+                              (tensors == 3 ? copy_bytes(shift, d, row, a.dim, a.span_d) : 0u));
+      copy_start(shift, y, row, a.dim, a.span_y, buf, bar);
+      copy_start(shift, h, row, a.dim, a.span_h, buf + buffer, bar);
+      if (tensors == 3) copy_start(shift, d, row, a.dim, a.span_d, buf + 2 * buffer, bar);
+      return;
+    }
     const auto cy = copy_y(at), ch = copy_h(at);
     if (tensors == 3) {
       const auto cd = copy_d(at);
@@ -155,7 +169,9 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     copy_start(ch, buf + buffer, bar);
   };
   const int64_t step = gridDim.x;
-  if (t == 0)
+  // (the thread that starts the copies: of a warp without a shifted row's ends)
+  const int starter = AL == kShifted ? group / 64 * 32 : 0;
+  if (t == starter)
     for (int i = 0; i < stages; ++i)
       if (blockIdx.x + i * step < a.rows) start(blockIdx.x + i * step, i);
   float2 acc[VPT][4];
@@ -163,7 +179,9 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
-  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim);
+  uint32_t own[VPT] = {};
+  if constexpr (AL == kShifted) own_bits(own, t, group, a.dim, shift.m);
+  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim, shift.m);
   int s = 0, parity = 0;
   uint32_t phase = 0;
   float rstd = blockIdx.x < a.rows ? a.rstd[blockIdx.x] : 0.f;
@@ -174,10 +192,22 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     ring_wait(head, s, phase, status);
     const uint8_t *buf = ring + s * tensors * buffer;
     Raw8<T> hy[VPT], hh[VPT], hd[VPT];
-    take<AL>(hy, copy_y(at), buf, t, group, a.dim);
-    take<AL>(hh, copy_h(at), buf + buffer, t, group, a.dim);
-    if (tensors == 3) take<AL>(hd, copy_d(at), buf + 2 * buffer, t, group, a.dim);
-    row_backward<AL, true>(a, now, hy, hh, hd, w, rstd, DROP, row, at, t, group, a.dim, slots + 32 * parity, acc);
+    if constexpr (AL == kShifted) {
+      take(hy, shift, static_cast<const T *>(a.dy) + at.at(a.sdy), row, a.span_y, buf, t, group, a.dim);
+      take(hh, shift, static_cast<const T *>(a.h) + at.at(a.sh), row, a.span_h, buf + buffer, t, group, a.dim);
+      if (tensors == 3)
+        take(hd, shift, static_cast<const T *>(a.dh) + at.at(a.sdh), row, a.span_d, buf + 2 * buffer, t, group, a.dim);
+      if (!all_own(own)) {
+        only_own(hy, own);
+        only_own(hh, own);
+      }
+    } else {
+      take<AL>(hy, copy_y(at), buf, t, group, a.dim);
+      take<AL>(hh, copy_h(at), buf + buffer, t, group, a.dim);
+      if (tensors == 3) take<AL>(hd, copy_d(at), buf + 2 * buffer, t, group, a.dim);
+    }
+    row_backward<AL, true>(a, now, hy, hh, hd, w, rstd, DROP, row, at, t, group, a.dim, slots + 32 * parity, acc, shift.m,
+                           own);
     parity ^= 1;
     rstd = next;
     // (its barrier came after every thread had read the stage)
@@ -186,7 +216,7 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
       if (t == 0) ring_drain(head, s, phase, static_cast<int>(left < stages ? left : stages), stages);
       return;
     }
-    if (t == 0 && row + stages * step < a.rows) start(row + stages * step, s);
+    if (t == starter && row + stages * step < a.rows) start(row + stages * step, s);
     if (++s == stages) s = 0, phase ^= 1u;
   }
   if (a.partial == nullptr) return;
@@ -195,8 +225,8 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const int c = element<AL>(t, group, j, k);
-      if (c < a.dim) out[c] = k & 1 ? acc[j][k / 2].y : acc[j][k / 2].x;
+      const int c = element<AL>(t, group, j, k) - shift.m;
+      if (c >= 0 && c < a.dim) out[c] = k & 1 ? acc[j][k / 2].y : acc[j][k / 2].x;
     }
 }
 
@@ -305,12 +335,12 @@ __global__ void __launch_bounds__(256) k_norm_dw(const float *__restrict__ parti
   }
 }
 
-template <class T, bool AL, bool DROP>
+template <class T, int AL, bool DROP>
 cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
-  constexpr int MID = AL ? 384 : 320;
-  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, ring_blocks(256, AL)>
-           : s.block <= MID ? k_norm_bwd_ring<T, AL, DROP, MID, ring_blocks(MID, AL)>
+  constexpr int ES = sizeof(T), MID = AL == kAligned || (AL == kShifted && ES == 2) ? 384 : 320;
+  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, ring_blocks(256, AL, ES)>
+           : s.block <= MID ? k_norm_bwd_ring<T, AL, DROP, MID, ring_blocks(MID, AL, ES)>
                             : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
 }
@@ -320,15 +350,18 @@ cudaError_t launch_bwd_heads(const NormBwdArgs &a, const NormSplit &s, int tenso
   auto k = k_norm_bwd_heads<T, DROP, 384, 2>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows / a.inner.n), s, tensors, a, status, st);
 }
-template <class T, bool AL>
+template <class T, int AL>
 cudaError_t launch_any(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status, cudaStream_t st) {
   if (s.heads)
     return a.dropped ? launch_bwd_heads<T, true>(a, s, tensors, status, st)
                      : launch_bwd_heads<T, false>(a, s, tensors, status, st);
+  if (s.shifted) {
+    if constexpr (AL == kLoose) return launch_bwd_ring<T, kShifted, false>(a, s, tensors, status, st);
+  }
   if (s.ring)
     return a.dropped ? launch_bwd_ring<T, AL, true>(a, s, tensors, status, st)
                      : launch_bwd_ring<T, AL, false>(a, s, tensors, status, st);
-  constexpr int NR = narrow_rows(AL);
+  constexpr int NR = narrow_rows(AL != kLoose);
   auto k = s.nr == NR   ? k_norm_bwd<T, 1, AL, NR, kSmallBlock>
            : s.vpt == 1 ? k_norm_bwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_bwd<T, 4, AL, 1, kSmallBlock>

@@ -35,10 +35,11 @@ __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], float inv_dim,
 
 // x becomes drop(x) + residual, as the stream holds it (rounded once to the
 // dtype: the norm is of that), written to h.
-template <bool AL, class T, int VPT>
+template <int AL, class T, int VPT>
 __device__ __forceinline__ void to_stream(const NormFwdArgs &a, const DropNow &now, Raw8<T> (&x)[VPT],
                                           const Raw8<T> (&res)[VPT], bool drop, int64_t row, T *h,
-                                          int t, int group, int dim) {
+                                          int t, int group, int dim, int m = 0,
+                                          const uint32_t *own = nullptr) {
   if (!drop && a.res == nullptr) return;
 #pragma unroll
   for (int j = 0; j < VPT; ++j) {
@@ -52,8 +53,8 @@ __device__ __forceinline__ void to_stream(const NormFwdArgs &a, const DropNow &n
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) x[j].set(i, v[i]);
-    if (a.h != nullptr) put<AL>(h, x[j], t, group, j, dim);
-    if (AL && (t + j * group) * 8 >= dim) {  // (a mask of zeros may have set a sign)
+    if (a.h != nullptr) put<AL>(h, x[j], t, group, j, dim, m, AL == kShifted ? own[j] : 255u);
+    if (AL == kAligned && (t + j * group) * 8 >= dim) {  // (a mask of zeros may have set a sign)
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[j].set(i, both(0.f));
     }
@@ -61,10 +62,11 @@ __device__ __forceinline__ void to_stream(const NormFwdArgs &a, const DropNow &n
 }
 
 // y = h r w to memory, and the codes and the scale.
-template <bool AL, bool FP8, class T, int VPT>
+template <int AL, bool FP8, class T, int VPT>
 __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (&h)[VPT],
                                            const Weight<AL, true, T, VPT> &w, float rstd, int64_t row, T *y,
-                                           int t, int group, int dim, float *slot) {
+                                           int t, int group, int dim, float *slot, int m = 0,
+                                           const uint32_t *own = nullptr) {
   float2 v[FP8 ? VPT : 1][4];
   float top = 0.f;
 #pragma unroll
@@ -79,7 +81,7 @@ __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(o[i].x), fabsf(o[i].y)));
     }
-    if (a.y != nullptr) put<AL>(y, o, t, group, j, dim);
+    if (a.y != nullptr) put<AL>(y, o, t, group, j, dim, m, AL == kShifted ? own[j] : 255u);
   }
   if (FP8 && a.codes != nullptr) {
     top = over_group<true>(top, group, slot);
@@ -90,12 +92,18 @@ __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (
     uint8_t *q = a.codes + row * a.dim;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      if constexpr (AL) {
-        const int c = (t + j * group) * 8;
+      if constexpr (AL != kLoose) {
+        const int c = (t + j * group) * 8 - m;
         uint32_t p[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) p[i] = to_e4m3x2(mul2(v[j][i], both(inv)));
-        if (c < dim) *reinterpret_cast<uint2 *>(q + c) = make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
+        if (AL == kAligned ? c < dim : own[j] == 255u) {
+          *reinterpret_cast<uint2 *>(q + c) = make_uint2(p[0] | p[1] << 16, p[2] | p[3] << 16);
+        } else if (AL == kShifted) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (own[j] >> k & 1u) q[c + k] = static_cast<uint8_t>(p[k / 2] >> 8 * (k % 2));
+        }
       } else {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
@@ -109,7 +117,7 @@ __device__ __forceinline__ void to_outputs(const NormFwdArgs &a, const Raw8<T> (
 
 // Forward, straight into registers: blocks stay and take NR rows a group of threads
 // at a time, all of them on their way at once.
-template <class T, int VPT, bool AL, int NR, int MAX>
+template <class T, int VPT, int AL, int NR, int MAX>
 __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFwdArgs a) {
   __shared__ __align__(16) float slots[192];  // of a round, and of the next
   clear_slots(slots, 192);
@@ -151,7 +159,7 @@ __global__ void __launch_bounds__(MAX) k_norm_fwd(const __grid_constant__ NormFw
 }
 
 // Forward over the ring: block b takes rows b, b + grid, ...
-template <class T, bool AL, bool DROP, bool FP8, int MAX, int BLOCKS>
+template <class T, int AL, bool DROP, bool FP8, int MAX, int BLOCKS>
 __global__ void __launch_bounds__(MAX, BLOCKS)
     k_norm_fwd_ring(const __grid_constant__ NormFwdArgs a, int stages, uint32_t buffer, unsigned *status) {
   constexpr int VPT = kRingVectors;
@@ -172,9 +180,20 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   auto copy_r = [&](const Where &at) {
     return row_copy<AL>(static_cast<const T *>(a.res) + at.at(a.sr), a.dim, a.span_r);
   };
+  ShiftCopy shift = {};
+  if constexpr (AL == kShifted)
+    shift = ShiftCopy::of(static_cast<const T *>(a.x) + int64_t(blockIdx.x) * a.sx.outer, a.dim, a.rows);
   auto start = [&](int64_t row, int s) {
     const Where at = where(row, a.inner);
     const uint32_t bar = smem_u32(&head->full[s]), buf = smem_u32(ring + s * tensors * buffer);
+    if constexpr (AL == kShifted) {
+      const T *x = static_cast<const T *>(a.x) + at.at(a.sx), *r = static_cast<const T *>(a.res) + at.at(a.sr);
+      mbar_expect_tx(bar, copy_bytes(shift, x, row, a.dim, a.span_x) +
+                              (tensors == 2 ? copy_bytes(shift, r, row, a.dim, a.span_r) : 0u));
+      copy_start(shift, x, row, a.dim, a.span_x, buf, bar);
+      if (tensors == 2) copy_start(shift, r, row, a.dim, a.span_r, buf + buffer, bar);
+      return;
+    }
     const auto cx = copy_x(at);
     if (tensors == 2) {
       const auto cr = copy_r(at);
@@ -186,10 +205,14 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     copy_start(cx, buf, bar);
   };
   const int64_t step = gridDim.x;
-  if (t == 0)
+  // (the thread that starts the copies: of a warp without a shifted row's ends)
+  const int starter = AL == kShifted ? group / 64 * 32 : 0;
+  if (t == starter)
     for (int i = 0; i < stages; ++i)
       if (blockIdx.x + i * step < a.rows) start(blockIdx.x + i * step, i);
-  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim);
+  uint32_t own[VPT] = {};
+  if constexpr (AL == kShifted) own_bits(own, t, group, a.dim, shift.m);
+  const Weight<AL, true, T, VPT> w(a.w, a.w32, t, group, a.dim, shift.m);
   int s = 0, parity = 0;
   uint32_t phase = 0;
   for (int64_t row = blockIdx.x; row < a.rows; row += step) {
@@ -200,9 +223,20 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     {
       const uint8_t *buf = ring + s * tensors * buffer;
       Raw8<T> r[VPT];
-      take<AL>(x, copy_x(at), buf, t, group, a.dim);
-      if (tensors == 2) take<AL>(r, copy_r(at), buf + buffer, t, group, a.dim);
-      to_stream<AL>(a, now, x, r, DROP, row, static_cast<T *>(a.h) + at.at(a.sh), t, group, a.dim);
+      if constexpr (AL == kShifted) {
+        take(x, shift, static_cast<const T *>(a.x) + at.at(a.sx), row, a.span_x, buf, t, group, a.dim);
+        if (tensors == 2)
+          take(r, shift, static_cast<const T *>(a.res) + at.at(a.sr), row, a.span_r, buf + buffer, t, group, a.dim);
+        if (!all_own(own)) {
+          only_own(x, own);
+          if (tensors == 2) only_own(r, own);
+        }
+      } else {
+        take<AL>(x, copy_x(at), buf, t, group, a.dim);
+        if (tensors == 2) take<AL>(r, copy_r(at), buf + buffer, t, group, a.dim);
+      }
+      to_stream<AL>(a, now, x, r, DROP, row, static_cast<T *>(a.h) + at.at(a.sh), t, group, a.dim, shift.m,
+                    own);
     }
     // its barrier: every thread has read the stage
     const float rstd = rstd_of(x, a.inv_dim, a.eps, group, slots + 32 * parity, slots + 64);
@@ -212,13 +246,13 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
       if (t == 0) ring_drain(head, s, phase, static_cast<int>(left < stages ? left : stages), stages);
       return;
     }
-    if (t == 0) {
+    if (t == starter) {
       if (row + stages * step < a.rows) start(row + stages * step, s);
       if (a.rstd != nullptr) a.rstd[row] = rstd;
     }
     if (++s == stages) s = 0, phase ^= 1u;
     to_outputs<AL, FP8>(a, x, w, rstd, row, static_cast<T *>(a.y) + at.at(a.sy), t, group, a.dim,
-                        slots + 96);
+                        slots + 96, shift.m, own);
   }
 }
 
@@ -284,14 +318,14 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   }
 }
 
-template <class T, bool AL, bool DROP, bool FP8>
+template <class T, int AL, bool DROP, bool FP8>
 cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
   const int64_t most = int64_t(kSms) * s.blocks_sm;
   const int blocks = static_cast<int>(a.rows < most ? a.rows : most);
-  constexpr int MID = AL ? 384 : 320;
-  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, ring_blocks(256, AL)>
-           : s.block <= MID ? k_norm_fwd_ring<T, AL, DROP, FP8, MID, ring_blocks(MID, AL)>
+  constexpr int ES = sizeof(T), MID = AL == kAligned || (AL == kShifted && ES == 2) ? 384 : 320;
+  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, ring_blocks(256, AL, ES)>
+           : s.block <= MID ? k_norm_fwd_ring<T, AL, DROP, FP8, MID, ring_blocks(MID, AL, ES)>
                             : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
   return launch_ring(k, blocks, s, tensors, a, status, st);
 }
@@ -302,11 +336,18 @@ cudaError_t launch_fwd_heads(const NormFwdArgs &a, const NormSplit &s, int tenso
   auto k = k_norm_fwd_heads<T, DROP, true, 384, 2>;
   return launch_ring(k, static_cast<int>(entries < most ? entries : most), s, tensors, a, status, st);
 }
-template <class T, bool AL>
+template <class T, int AL>
 cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, unsigned *status, cudaStream_t st) {
   if (s.heads)
     return a.dropped ? launch_fwd_heads<T, true>(a, s, tensors, status, st)
                      : launch_fwd_heads<T, false>(a, s, tensors, status, st);
+  if (s.shifted) {
+    if constexpr (AL == kLoose) {
+      if constexpr (sizeof(T) == 2)
+        if (a.codes != nullptr) return launch_fwd_ring<T, kShifted, false, true>(a, s, tensors, status, st);
+      return launch_fwd_ring<T, kShifted, false, false>(a, s, tensors, status, st);
+    }
+  }
   if (s.ring) {
     if constexpr (sizeof(T) == 2) {
       if (a.codes != nullptr)
@@ -316,7 +357,7 @@ cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, un
     return a.dropped ? launch_fwd_ring<T, AL, true, false>(a, s, tensors, status, st)
                      : launch_fwd_ring<T, AL, false, false>(a, s, tensors, status, st);
   }
-  constexpr int NR = narrow_rows(AL);
+  constexpr int NR = narrow_rows(AL != kLoose);
   auto k = s.nr == NR   ? k_norm_fwd<T, 1, AL, NR, kSmallBlock>
            : s.vpt == 1 ? k_norm_fwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_fwd<T, 4, AL, 1, kSmallBlock>

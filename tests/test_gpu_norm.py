@@ -326,3 +326,51 @@ def test_graph_replay_and_streams():
     got = rl.rms_norm_backward(dy, h3, w, rstd3, dh=dh, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(y3, y2) and torch.equal(got[2], want[2])
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [513, 1001, 1030, 2001, 2046, 4095, 4097, 5121, 8178, 8185])
+@pytest.mark.parametrize("lead,pad", [(0, 0), (3, 1), (1, 7)])
+def test_rows_off_the_16_byte_boundaries(dim, lead, pad, dtype):
+    """More rows than blocks, which begin anywhere: every tensor alike, then one otherwise."""
+    rows = 1000 if dim < 3000 else 500
+    g = torch.Generator(device=DEV).manual_seed(dim + lead)
+    step = dim + pad
+
+    def room(off):
+        t = torch.full((rows * step + off + 1,), 7.0, dtype=dtype, device=DEV)
+        return t, t[off:].as_strided((rows, dim), (step, 1))
+    rand = lambda off: room(off)[1].copy_(torch.randn(rows, dim, generator=g, device=DEV))
+    x, res, dy, dh = (rand(lead) for _ in range(4))
+    w = (1 + 0.3 * torch.randn(dim, generator=g, device=DEV)).to(dtype)
+    for off in (lead, lead + 1):
+        (ty, y), (th, h), (td, d) = (room(o) for o in (off, lead, lead))
+        out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, out=y, h_out=h, fp8=pad == 0)
+        check_forward(x, res, w, 1e-5, out)
+        got = rl.rms_norm_backward(dy, h, w, out[2], dh=dh, dx=d)
+        check_backward(dy, h, w, out[2], dh, got)
+        again = rl.rms_norm_backward(dy, h, w, out[2], dh=dh, dx=d)
+        assert torch.equal(got[2], again[2])
+        for flat, part in ((ty, y), (th, h), (td, d)):
+            part.fill_(7.0)
+            assert torch.all(flat == 7.0)  # nothing beside the rows was written
+    out = rl.rms_norm_forward(x, w, eps=1e-5)
+    check_forward(x, None, w, 1e-5, out)
+    check_backward(dy, x, w, out[2], None, rl.rms_norm_backward(dy, x, w, out[2]))
+    # in place the bits of the same layout elsewhere (another has its sums in another order)
+    want = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, out=room(lead)[1], h_out=room(lead)[1])
+    y, h, rstd = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, out=x, h_out=res)
+    assert torch.equal(y, want[0]) and torch.equal(h, want[1]) and torch.equal(rstd, want[2])
+    rl.device_status()
+
+
+def test_not_finite_neighbours_of_rows_off_the_boundaries():
+    for dtype in (torch.bfloat16, torch.float32):
+        x = torch.randn(901, 1003, device=DEV).to(dtype)
+        w = torch.ones(1003, device=DEV, dtype=dtype)
+        want = rl.rms_norm_forward(x, w)
+        x[1::2] = float("nan")
+        got = rl.rms_norm_forward(x, w)
+        assert torch.equal(got[0][::2], want[0][::2]) and torch.equal(got[2][::2], want[2][::2])
+        dx, _, _ = rl.rms_norm_backward(x, x, w, got[2])
+        assert torch.isfinite(dx[::2]).all() and torch.isnan(dx[1::2]).all()
