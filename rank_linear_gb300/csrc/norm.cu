@@ -7,11 +7,11 @@
 // memory, and it is written once.  Bound by memory: what counts is how many bytes
 // an SM has on their way.
 //
-// Two forms.  NormRows wider than 1024 elements, and more than the SMs take at once:
-// blocks stay, and bulk copies bring the next rows into a ring in shared memory
-// while one is worked on (k_norm_fwd_ring, k_norm_bwd_ring).  Narrow rows, several
-// a warp, and few rows, where latency counts: straight into registers (k_norm_fwd,
-// k_norm_bwd).
+// Two forms.  Wide rows, more than the SMs take at once: blocks stay, and bulk copies
+// bring the next rows into a ring in shared memory while one is worked on
+// (k_norm_fwd_ring, k_norm_bwd_ring; the backward's narrow rows too where they lie side
+// by side, k_norm_bwd_heads).  Narrow rows, several a warp, and few rows, where latency
+// counts: straight into registers (k_norm_fwd, k_norm_bwd).
 #include <climits>
 #include <initializer_list>
 
@@ -81,7 +81,7 @@ lora_status_t check_weight(const void *w, int es, const char *name, bool &vec) {
   return LORA_OK;
 }
 
-// Takes narrow rows side by side over the ring where they stand so: the shape's inner
+// Takes the backward's narrow rows side by side over the ring where they stand so: the shape's inner
 // rows, if each tensor has them `dim` apart; or, of plain contiguous rows, as many as
 // make some 4096 elements and divide their number.
 void use_heads(const lora_norm_t *sh, bool vec, int es, int tensors, NormRows *const *of,
@@ -160,9 +160,6 @@ lora_status_t lora_norm_fwd(const lora_norm_t *sh, const void *x, const void *re
   a.w32 = dtype == LORA_FP32 ? 0 : sh->weight_fp32;
   const int tensors = residual != nullptr ? 2 : 1;
   NormSplit s = norm_split(sh->dim, rows, ts.es, tensors, ts.vec, false, codes != nullptr);
-  NormRows *of[4] = {&a.sx, &a.sr, &a.sh, &a.sy};
-  const bool given[4] = {true, residual != nullptr, h != nullptr, y != nullptr};
-  use_heads(sh, ts.vec, ts.es, tensors, of, given, 4, a.inner, s);
   if (s.ring && !ts.vec && !a.dropped && sh->inner == 1 && a.w32 == 0) {
     NormShift shift;
     shift.add(x, a.sx.outer, ts.es);

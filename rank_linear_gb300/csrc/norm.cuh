@@ -103,6 +103,22 @@ __host__ __device__ constexpr int ring_blocks(int threads, int lay, int es) {
 // whose elements come one by one take all of them).
 __host__ __device__ constexpr int narrow_rows(bool vec) { return vec ? 4 : 2; }
 
+// Vectors a thread of a narrow aligned row: the sums over its threads, which cost as
+// much as the vectors, are over few (131072 rows of 128, forward: one vector a thread
+// and four rows 21.7 us, two and two 15.5, four 13.9; of 96, 20.5, 16.2, and three
+// 14.7).  Three or `most`, whichever leaves fewer places idle.
+inline int narrow_vectors(int vectors, int most) {
+  auto places = [&](int n) {
+    int lanes = 1;
+    while (lanes * n < vectors) lanes *= 2;
+    return lanes * n;
+  };
+  return places(3) < places(most) ? 3 : most;
+}
+// The ring's threads of narrow rows on an SM, whose registers hold two vectors each, or
+// three (four spill, and two at 768 threads).
+__host__ __device__ constexpr int heads_threads(int vpt) { return vpt == 2 ? 640 : 512; }
+
 // Few rows (two an SM at most): as many threads as there are vectors.
 inline bool norm_few_rows(int64_t rows) { return rows <= 2 * kSms; }
 
@@ -134,7 +150,7 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec
     if (s.ring) return s;
     s.vpt = 4;
   } else {
-    s.vpt = vectors > 32 ? 4 : 1;
+    s.vpt = vec && vectors >= 6 ? narrow_vectors(vectors, 4) : vectors > 32 ? 4 : 1;
     if (s.vpt == 1) s.nr = narrow_rows(vec);
   }
   const int threads = (vectors + s.vpt - 1) / s.vpt;
@@ -149,19 +165,30 @@ inline NormSplit norm_split(int dim, int64_t rows, int es, int tensors, bool vec
   return s;
 }
 
-// Narrow rows of which `inner` lie side by side in every tensor, as the ring's rows:
-// each of whole vectors, and of 1, 2, 4 ... 32 threads.  False: not so.
+// The backward's narrow rows of which `inner` lie side by side in every tensor, as the
+// ring's rows: each of whole vectors, on 1, 2, 4 ... 32 threads.  False: not so.
 inline bool norm_heads(int dim, int64_t outer, int64_t inner, int es, int tensors, NormSplit &s) {
-  const int lanes = dim / 8;
+  const int vectors = dim / 8;
   const int64_t wide = inner * dim;
-  if (dim % 8 != 0 || lanes > 32 || (lanes & (lanes - 1)) != 0 || inner < 2 || wide <= 1024 || wide > 6144)
-    return false;
-  const NormSplit t = norm_split(static_cast<int>(wide), outer, es, tensors, true, true);
-  if (!t.ring || t.block > 384) return false;
+  if (dim % 8 != 0 || vectors < 6 || inner < 2 || wide <= 1024 || wide > 8192 || norm_few_rows(outer)) return false;
+  NormSplit t = {};
+  t.heads = true;
+  t.vpt = narrow_vectors(vectors, 2);
+  t.group = 1;
+  while (t.group * t.vpt < vectors) t.group *= 2;
+  t.block = static_cast<int>((inner * t.group + 31) / 32 * 32);
+  if (t.group > 32 || t.block > 256) return false;
+  t.nr = t.per_block = 1;
+  t.buffer = static_cast<uint32_t>(wide * es);
+  t.blocks_sm = heads_threads(t.vpt) / t.block;
+  if (t.blocks_sm > 12) t.blocks_sm = 12;
+  for (; t.blocks_sm > 0; --t.blocks_sm) {
+    t.stages = (kRingSmem / t.blocks_sm - 1024 - kRingHead) / (static_cast<int>(t.buffer) * tensors);
+    if (t.stages >= 2) break;
+  }
+  if (t.blocks_sm == 0) return false;
+  if (t.stages > 4) t.stages = 4;
   s = t;
-  s.ring = false;
-  s.heads = true;
-  s.group = lanes;
   return true;
 }
 

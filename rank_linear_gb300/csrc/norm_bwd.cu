@@ -230,12 +230,12 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
     }
 }
 
-// Narrow rows that lie side by side, over the ring (k_norm_fwd_heads).
-template <class T, bool DROP, int MAX, int BLOCKS>
-__global__ void __launch_bounds__(MAX, BLOCKS)
+// Narrow rows that lie side by side (the heads of a token), over the ring: its row is
+// `inner` of them, each of which belongs to `lanes` neighbouring threads of a warp.
+template <class T, int VPT, bool DROP>
+__global__ void __launch_bounds__(heads_threads(VPT) / 2, 2)
     k_norm_bwd_heads(const __grid_constant__ NormBwdArgs a, int stages, uint32_t buffer,
                      unsigned *status) {
-  constexpr int VPT = kRingVectors;
   extern __shared__ __align__(128) uint8_t smem[];
   auto *head = reinterpret_cast<RingHead *>(smem);
   uint8_t *ring = smem + kRingHead;
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   fence_proxy_async_global();  // what the kernels before wrote, for this thread's copies
   griddep_launch_dependents();
   const DropNow now = DROP ? drop_now(a.drop) : DropNow{};
-  const int lanes = a.group, tl = threadIdx.x % lanes, tensors = a.dh != nullptr ? 3 : 2;
+  const int lanes = a.group, tl = threadIdx.x % lanes, sub = threadIdx.x / lanes;
+  const int tensors = a.dh != nullptr ? 3 : 2;
   const int inner = static_cast<int>(a.inner.n), wide = inner * a.dim;
   const int64_t entries = a.rows / inner, step = gridDim.x;
   auto start = [&](int64_t o, int s) {
@@ -258,50 +259,51 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   if (threadIdx.x == 0)
     for (int i = 0; i < stages; ++i)
       if (blockIdx.x + i * step < entries) start(blockIdx.x + i * step, i);
-  float2 acc[1][4];
+  float2 acc[VPT][4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[0][i] = both(0.f);
-  const Weight<true, true, T, 1> w(a.w, a.w32, tl, lanes, a.dim);
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[j][i] = both(0.f);
+  const Weight<kAligned, true, T, VPT> w(a.w, a.w32, tl, lanes, a.dim);
+  const int dim = sub < inner ? a.dim : 0;
   int s = 0;
   uint32_t phase = 0;
+  float rstd = sub < inner && blockIdx.x < entries ? a.rstd[int64_t(blockIdx.x) * inner + sub] : 0.f;
   for (int64_t o = blockIdx.x; o < entries; o += step) {
-    const int t = each_time(int(threadIdx.x));
-    float rstd[VPT];  // (on their way while the rows are)
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int sub = (t + j * int(blockDim.x)) / lanes;
-      rstd[j] = sub < inner ? a.rstd[o * inner + sub] : 0.f;
-    }
+    const int t = each_time(tl);
+    const float next = sub < inner && o + step < entries ? a.rstd[(o + step) * inner + sub] : 0.f;
     Raw8<T> hy[VPT], hh[VPT], hd[VPT];
     ring_wait(head, s, phase, status);
-    const uint8_t *buf = ring + s * tensors * buffer;
-    fetch<true>(hy, reinterpret_cast<const T *>(buf), t, blockDim.x, wide);
-    fetch<true>(hh, reinterpret_cast<const T *>(buf + buffer), t, blockDim.x, wide);
-    if (tensors == 3) fetch<true>(hd, reinterpret_cast<const T *>(buf + 2 * buffer), t, blockDim.x, wide);
+    const T *buf = reinterpret_cast<const T *>(ring + s * tensors * buffer) + sub * a.dim;
+    const T *buf_h = reinterpret_cast<const T *>(ring + (s * tensors + 1) * buffer) + sub * a.dim;
+    fetch<kAligned>(hy, buf, t, lanes, dim);
+    fetch<kAligned>(hh, buf_h, t, lanes, dim);
+    if (tensors == 3)
+      fetch<kAligned>(hd, reinterpret_cast<const T *>(ring + (s * tensors + 2) * buffer) + sub * a.dim, t, lanes, dim);
     __syncthreads();  // every thread has read the stage
     if (*static_cast<volatile int *>(&head->abort_flag)) {
       const int64_t left = (entries - o + step - 1) / step;
-      if (t == 0) ring_drain(head, s, phase, static_cast<int>(left < stages ? left : stages), stages);
+      if (threadIdx.x == 0) ring_drain(head, s, phase, static_cast<int>(left < stages ? left : stages), stages);
       return;
     }
-    if (t == 0 && o + stages * step < entries) start(o + stages * step, s);
+    if (threadIdx.x == 0 && o + stages * step < entries) start(o + stages * step, s);
     if (++s == stages) s = 0, phase ^= 1u;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int sub = (t + j * int(blockDim.x)) / lanes;
-      const Raw8<T> y1[1] = {hy[j]}, h1[1] = {hh[j]}, d1[1] = {hd[j]};
-      row_backward<true, true>(a, now, y1, h1, d1, w, rstd[j], DROP, o * inner + sub, Where{o, sub}, tl,
-                               lanes, sub < inner ? a.dim : 0, nullptr, acc);
-    }
+    row_backward<kAligned, true>(a, now, hy, hh, hd, w, rstd, DROP, o * inner + sub, Where{o, sub}, t, lanes, dim,
+                                 nullptr, acc);
+    rstd = next;
   }
   if (a.partial == nullptr) return;
   // the sums of the threads with the same columns, in their order; the ring is free
   float *cols = reinterpret_cast<float *>(ring);
-  const int groups = blockDim.x / lanes, of = threadIdx.x / lanes;
+  const int groups = blockDim.x / lanes;
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < 8; ++k)
-    cols[of * a.dim + tl * 8 + k] = k & 1 ? acc[0][k / 2].y : acc[0][k / 2].x;
+  for (int j = 0; j < VPT; ++j)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int c = element<kAligned>(tl, lanes, j, k);
+      if (c < a.dim) cols[sub * a.dim + c] = k & 1 ? acc[j][k / 2].y : acc[j][k / 2].x;
+    }
   __syncthreads();
   for (int c = threadIdx.x; c < a.dim; c += blockDim.x) {
     float sum = 0.f;
@@ -347,7 +349,7 @@ cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensor
 template <class T, bool DROP>
 cudaError_t launch_bwd_heads(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                              cudaStream_t st) {
-  auto k = k_norm_bwd_heads<T, DROP, 384, 2>;
+  auto k = s.vpt == 3 ? k_norm_bwd_heads<T, 3, DROP> : k_norm_bwd_heads<T, 2, DROP>;
   return launch_ring(k, norm_bwd_blocks(s, a.rows / a.inner.n), s, tensors, a, status, st);
 }
 template <class T, int AL>
@@ -366,6 +368,8 @@ cudaError_t launch_any(const NormBwdArgs &a, const NormSplit &s, int tensors, un
            : s.vpt == 1 ? k_norm_bwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_bwd<T, 4, AL, 1, kSmallBlock>
                                     : k_norm_bwd<T, 4, AL, 1, 1024>;
+  if constexpr (AL == kAligned)
+    if (s.vpt == 3) k = s.block <= kSmallBlock ? k_norm_bwd<T, 3, AL, 1, kSmallBlock> : k_norm_bwd<T, 3, AL, 1, 1024>;
   return launch_pdl(k, dim3(norm_bwd_blocks(s, a.rows)), dim3(s.block), 0, st, a);
 }
 }  // namespace

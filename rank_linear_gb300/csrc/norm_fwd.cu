@@ -256,68 +256,6 @@ __global__ void __launch_bounds__(MAX, BLOCKS)
   }
 }
 
-// Narrow rows that lie side by side (the heads of a token): the ring's row is `inner`
-// of them, each of which belongs to `lanes` neighbouring threads of a warp.  (Straight
-// into registers, 131072 rows of 128 took 25 us.)
-template <class T, bool DROP, bool FP8, int MAX, int BLOCKS>
-__global__ void __launch_bounds__(MAX, BLOCKS)
-    k_norm_fwd_heads(const __grid_constant__ NormFwdArgs a, int stages, uint32_t buffer,
-                     unsigned *status) {
-  constexpr int VPT = kRingVectors;
-  extern __shared__ __align__(128) uint8_t smem[];
-  auto *head = reinterpret_cast<RingHead *>(smem);
-  uint8_t *ring = smem + kRingHead;
-  ring_init(head, stages);
-  griddep_wait();
-  fence_proxy_async_global();  // what the kernels before wrote, for this thread's copies
-  griddep_launch_dependents();
-  const DropNow now = DROP ? drop_now(a.drop) : DropNow{};
-  const int lanes = a.group, tl = threadIdx.x % lanes, tensors = a.res != nullptr ? 2 : 1;
-  const int inner = static_cast<int>(a.inner.n), wide = inner * a.dim;
-  const int64_t entries = a.rows / inner, step = gridDim.x;
-  auto start = [&](int64_t o, int s) {
-    const uint32_t bar = smem_u32(&head->full[s]), buf = smem_u32(ring + s * tensors * buffer);
-    const uint32_t n = static_cast<uint32_t>(wide) * static_cast<uint32_t>(sizeof(T));
-    mbar_expect_tx(bar, n * tensors);
-    bulk_load(buf, static_cast<const T *>(a.x) + o * a.sx.outer, n, bar);
-    if (tensors == 2) bulk_load(buf + buffer, static_cast<const T *>(a.res) + o * a.sr.outer, n, bar);
-  };
-  if (threadIdx.x == 0)
-    for (int i = 0; i < stages; ++i)
-      if (blockIdx.x + i * step < entries) start(blockIdx.x + i * step, i);
-  const Weight<true, true, T, 1> w(a.w, a.w32, tl, lanes, a.dim);
-  int s = 0;
-  uint32_t phase = 0;
-  for (int64_t o = blockIdx.x; o < entries; o += step) {
-    const int t = each_time(int(threadIdx.x));
-    Raw8<T> x[VPT], r[VPT];
-    ring_wait(head, s, phase, status);
-    const uint8_t *buf = ring + s * tensors * buffer;
-    fetch<true>(x, reinterpret_cast<const T *>(buf), t, blockDim.x, wide);
-    if (tensors == 2) fetch<true>(r, reinterpret_cast<const T *>(buf + buffer), t, blockDim.x, wide);
-    __syncthreads();  // every thread has read the stage
-    if (*static_cast<volatile int *>(&head->abort_flag)) {
-      const int64_t left = (entries - o + step - 1) / step;
-      if (t == 0) ring_drain(head, s, phase, static_cast<int>(left < stages ? left : stages), stages);
-      return;
-    }
-    if (t == 0 && o + stages * step < entries) start(o + stages * step, s);
-    if (++s == stages) s = 0, phase ^= 1u;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int sub = (t + j * int(blockDim.x)) / lanes;  // of the entry's rows
-      const int dim = sub < inner ? a.dim : 0;
-      const int64_t row = o * inner + sub;
-      const Where at = {o, sub};
-      Raw8<T> h[1] = {x[j]}, res[1] = {r[j]};
-      to_stream<true>(a, now, h, res, DROP, row, static_cast<T *>(a.h) + at.at(a.sh), tl, lanes, dim);
-      const float rstd = rstd_of(h, a.inv_dim, a.eps, lanes, nullptr, nullptr);
-      if (dim > 0 && tl == 0 && a.rstd != nullptr) a.rstd[row] = rstd;
-      to_outputs<true, FP8>(a, h, w, rstd, row, static_cast<T *>(a.y) + at.at(a.sy), tl, lanes, dim, nullptr);
-    }
-  }
-}
-
 template <class T, int AL, bool DROP, bool FP8>
 cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
@@ -329,18 +267,8 @@ cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensor
                             : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
   return launch_ring(k, blocks, s, tensors, a, status, st);
 }
-template <class T, bool DROP>
-cudaError_t launch_fwd_heads(const NormFwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
-                             cudaStream_t st) {
-  const int64_t most = int64_t(kSms) * s.blocks_sm, entries = a.rows / a.inner.n;
-  auto k = k_norm_fwd_heads<T, DROP, true, 384, 2>;
-  return launch_ring(k, static_cast<int>(entries < most ? entries : most), s, tensors, a, status, st);
-}
 template <class T, int AL>
 cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, unsigned *status, cudaStream_t st) {
-  if (s.heads)
-    return a.dropped ? launch_fwd_heads<T, true>(a, s, tensors, status, st)
-                     : launch_fwd_heads<T, false>(a, s, tensors, status, st);
   if (s.shifted) {
     if constexpr (AL == kLoose) {
       if constexpr (sizeof(T) == 2)
@@ -362,6 +290,8 @@ cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, un
            : s.vpt == 1 ? k_norm_fwd<T, 1, AL, 1, 1024>
            : s.block <= kSmallBlock ? k_norm_fwd<T, 4, AL, 1, kSmallBlock>
                                     : k_norm_fwd<T, 4, AL, 1, 1024>;
+  if constexpr (AL == kAligned)
+    if (s.vpt == 3) k = s.block <= kSmallBlock ? k_norm_fwd<T, 3, AL, 1, kSmallBlock> : k_norm_fwd<T, 3, AL, 1, 1024>;
   // (a round of blocks that fills the SMs' threads: 16 of 128, or what fits)
   const int64_t want = (a.rows + s.per_block - 1) / s.per_block;
   const int64_t most = int64_t(kSms) * (s.block <= kSmallBlock ? 12 : 2);
