@@ -369,7 +369,7 @@ cudaError_t launch_any(const NormBwdArgs &a, const NormSplit &s, int tensors, un
            : s.block <= kSmallBlock ? k_norm_bwd<T, 4, AL, 1, kSmallBlock>
                                     : k_norm_bwd<T, 4, AL, 1, 1024>;
   if constexpr (AL == kAligned)
-    if (s.vpt == 3) k = s.block <= kSmallBlock ? k_norm_bwd<T, 3, AL, 1, kSmallBlock> : k_norm_bwd<T, 3, AL, 1, 1024>;
+    if (s.vpt == 3) k = k_norm_bwd<T, 3, AL, 1, kSmallBlock>;  // (96 vectors at most)
   return launch_pdl(k, dim3(norm_bwd_blocks(s, a.rows)), dim3(s.block), 0, st, a);
 }
 }  // namespace
