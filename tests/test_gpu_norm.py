@@ -374,3 +374,34 @@ def test_not_finite_neighbours_of_rows_off_the_boundaries():
         assert torch.equal(got[0][::2], want[0][::2]) and torch.equal(got[2][::2], want[2][::2])
         dx, _, _ = rl.rms_norm_backward(x, x, w, got[2])
         assert torch.isfinite(dx[::2]).all() and torch.isnan(dx[1::2]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim,lead,w_lead", [(2048, 3, 0), (2048, 0, 1), (1056, 1, 3), (4096, 5, 5)])
+def test_whole_vectors_at_odd_addresses(dim, lead, w_lead, dtype):
+    """Widths of whole vectors whose rows, or whose weight alone, begin off 16 bytes."""
+    g = torch.Generator(device=DEV).manual_seed(dim + lead)
+    make_rows = lambda: torch.randn(600 * dim + lead, generator=g, device=DEV).to(dtype)[lead:].view(600, dim)
+    x, res, dy, dh, y, h, dx = (make_rows() for _ in range(7))
+    w = torch.randn(dim + w_lead, generator=g, device=DEV).to(dtype)[w_lead:]
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, out=y, h_out=h)
+    check_forward(x, res, w, 1e-5, out)
+    got = rl.rms_norm_backward(dy, h, w, out[2], dh=dh, dx=dx)
+    check_backward(dy, h, w, out[2], dh, got)
+    rl.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("dim", [8, 40, 48, 56, 72, 80, 96, 104, 160, 168, 192, 232, 248, 520, 640, 768, 776])
+def test_narrow_rows_of_whole_vectors(dim, dtype):
+    """Widths whose vectors fill the threads' three or four, and do not; plain rows and heads."""
+    for shape in ((3001,), (400, 24), (512, 9)):
+        g = torch.Generator(device=DEV).manual_seed(dim)
+        r = lambda: torch.randn(*shape, dim, generator=g, device=DEV).to(dtype)
+        x, res, dy, dh = r(), r(), r(), r()
+        w = (1 + 0.3 * torch.randn(dim, generator=g, device=DEV)).to(dtype)
+        out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5)
+        check_forward(x, res, w, 1e-5, out)
+        got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh)
+        check_backward(dy, out[1], w, out[2], dh, got)
+    rl.device_status()
