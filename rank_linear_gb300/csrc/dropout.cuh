@@ -129,6 +129,10 @@ __device__ __forceinline__ int each_time(int v) {
   asm volatile("" : "+r"(v));
   return v;
 }
+__device__ __forceinline__ float each_time(float v) {
+  asm volatile("" : "+f"(v));
+  return v;
+}
 
 // Eight elements as they lie in memory: aligned and side by side, or one by one.
 template <class T>

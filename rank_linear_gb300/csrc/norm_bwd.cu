@@ -27,7 +27,9 @@ __device__ __forceinline__ void row_backward(const NormBwdArgs &a, const DropNow
     }
   }
   const float along = over_group<false>(s.x + s.y, group, slot) * a.inv_dim;
-  const float2 back = both(-along * rstd * rstd);  // d = r g - h (r^2 mean) + dh
+  // d = r (g - h r mean) + dh: the square of r alone would leave fp32 where h r does not
+  const float2 back = both(-along);
+  rstd = each_time(rstd);  // (h r is made again: held since the sum, it spilled)
   T *dx = static_cast<T *>(a.dx) + at.at(a.sdx);
   T *dres = static_cast<T *>(a.dres) + at.at(a.sdr);
 #pragma unroll
@@ -36,9 +38,9 @@ __device__ __forceinline__ void row_backward(const NormBwdArgs &a, const DropNow
     w.get(j, t, group, a.dim, u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      d[i] = mul2(hh[j].pair(i), back);
-      d[i] = fma2(mul2(hy[j].pair(i), u[i]), both(rstd), d[i]);
-      if (a.dh != nullptr) d[i] = add2(d[i], hd[j].pair(i));
+      const float2 hat = mul2(hh[j].pair(i), both(rstd));
+      d[i] = fma2(hat, back, mul2(hy[j].pair(i), u[i]));
+      d[i] = a.dh != nullptr ? fma2(d[i], both(rstd), hd[j].pair(i)) : mul2(d[i], both(rstd));
     }
     if (a.dres != nullptr) put<AL>(dres, d, t, group, j, dim, m, AL == kShifted ? own[j] : 255u);
     if (drop) drop_vector<AL>(a.drop, now, row, t, group, j, d);

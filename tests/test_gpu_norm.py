@@ -405,3 +405,33 @@ def test_narrow_rows_of_whole_vectors(dim, dtype):
         got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh)
         check_backward(dy, out[1], w, out[2], dh, got)
     rl.device_status()
+
+
+# One shape a kernel: few rows, narrow rows, heads, the ring on and off the boundaries, element by
+# element, and rows too wide for the ring.
+FORMS = [(7, 512), (3001, 96), (12800, 128), (900, 4096), (1000, 1001), (700, 300), (8, 20001), (310, 8200)]
+
+
+def scaled_rows(rows, dim, dtype, scales, seed):
+    """(x, dy, w, factor of each row): rows on the scales in turn, and dy partly along them, of size 1e6
+    (no gradient is as small as the checks' 1e-38)."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    unit = r(rows, dim)
+    s = torch.tensor(scales, device=DEV).repeat(rows // len(scales) + 1)[:rows, None]
+    return ((unit * s).to(dtype), ((r(rows, dim) + unit) * 1e6).to(dtype), (1 + 0.3 * r(dim)).to(dtype), s)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", FORMS)
+def test_gradients_of_large_rows(rows, dim, dtype):
+    """Rows whose squares, or the square of whose rstd, leave fp32, beside ordinary ones: every
+    gradient, within the bounds of ordinary rows."""
+    x, dy, w, s = scaled_rows(rows, dim, dtype, [1.0, 1e18, 1e21, 1e22, 1e25, 1e30, 1e36], dim)
+    out = rl.rms_norm_forward(x, w, eps=1e-6)
+    check_forward(x, None, w, 1e-6, out)
+    check_backward(dy, x, w, out[2], None, rl.rms_norm_backward(dy, x, w, out[2]))
+    # what reaches h otherwise, as small as the rest
+    dh = (dy.float() / s).to(dtype)
+    check_backward(dy, x, w, out[2], dh, rl.rms_norm_backward(dy, x, w, out[2], dh=dh))
+    rl.device_status()
