@@ -6,8 +6,8 @@ namespace lora {
 namespace {
 
 // r = (ss / dim + eps)^(-1/2) of the row in v.  Where the squares leave the
-// range of fp32 the sum is taken again of values scaled down by 2^-70 (exact),
-// which the result is scaled by as well.
+// range of fp32 the sum is taken again of values scaled down by 2^-100 (exact; 32768
+// squares of 2^128 stay below 2^71), which the result is scaled by as well.
 template <class T, int VPT>
 __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], float inv_dim, float eps, int group,
                                          float *slot, float *slot2) {
@@ -26,11 +26,11 @@ __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], float inv_dim,
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 u = mul2(v[j].pair(i), both(0x1p-70f));
+      const float2 u = mul2(v[j].pair(i), both(0x1p-100f));
       s2 = fmaf(u.x, u.x, fmaf(u.y, u.y, s2));
     }
   s2 = over_group<false>(s2, group, slot2);
-  return far ? 0x1p-70f * rsqrtf(fmaf(s2, inv_dim, eps * 0x1p-140f)) : rsqrtf(fmaf(ss, inv_dim, eps));
+  return far ? 0x1p-100f * rsqrtf(fmaf(s2, inv_dim, eps * 0x1p-100f * 0x1p-100f)) : rsqrtf(fmaf(ss, inv_dim, eps));
 }
 
 // x becomes drop(x) + residual, as the stream holds it (rounded once to the

@@ -435,3 +435,19 @@ def test_gradients_of_large_rows(rows, dim, dtype):
     dh = (dy.float() / s).to(dtype)
     check_backward(dy, x, w, out[2], dh, rl.rms_norm_backward(dy, x, w, out[2], dh=dh))
     rl.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", [(3, 8192), (400, 8192), (700, 6001), (2, 32768), (310, 16384)])
+def test_wide_rows_of_the_largest_numbers(rows, dim, dtype):
+    """Rows whose squares leave fp32 although each is scaled down by 2^-70.  rstd is below 2^-126 and
+    so a multiple of 2^-149: 2^-22 of it at most, which y has as well."""
+    g = torch.Generator(device=DEV).manual_seed(dim)
+    sign = torch.randint(0, 2, (rows, dim), generator=g, device=DEV) * 2 - 1
+    x = (sign * 3e38).to(dtype)
+    x[1:, ::2] = sign[1:, ::2].to(dtype)  # (beside it a row of which half the elements count)
+    w = (1 + 0.3 * torch.randn(dim, generator=g, device=DEV)).to(dtype)
+    y, _, rstd = rl.rms_norm_forward(x, w, eps=1e-6)
+    want, r = on.forward(host(x), host(w[None])[0], 1e-6)
+    assert np.all(np.abs(rstd.double().cpu().numpy() - r) <= (24 * F + 2.0 ** -22) * r)
+    assert np.all(np.abs(host(y) - want) <= (U[dtype] + 28 * F + 2.0 ** -22) * np.abs(want) + 2.0 ** -133)
