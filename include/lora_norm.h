@@ -18,10 +18,12 @@
  *     g = dy w,  dresidual = r (g - h r mean(g h r)) + dh,  dx = drop(dresidual)
  *     dw = sum over rows of dy h r
  *
- * Sums are fp32 (rows whose squares leave its range are summed again scaled
- * down); dw adds blocks of rows in a fixed order: the same call gives the same
- * bits.  Errors, streams and the timing hook are those of lora_linear.h.
- * Nothing is allocated; no host synchronisation.
+ * Sums are fp32 (rows whose squares leave its range, or lose bits below it where
+ * eps is as small, are summed again scaled; r itself is an fp32 number: infinite
+ * where h is 0 or its root mean square is below 2^-128 and eps is 0); dw adds
+ * blocks of rows in a fixed order: the same call gives the same bits.  Errors,
+ * streams and the timing hook are those of lora_linear.h.  Nothing is allocated;
+ * no host synchronisation.
  */
 #ifndef LORA_NORM_H
 #define LORA_NORM_H

@@ -6,8 +6,11 @@ namespace lora {
 namespace {
 
 // r = (ss / dim + eps)^(-1/2) of the row in v.  Where the squares leave the
-// range of fp32 the sum is taken again of values scaled down by 2^-100 (exact; 32768
-// squares of 2^128 stay below 2^71), which the result is scaled by as well.
+// range of fp32, or are so small that they lose bits and eps does not cover it (a
+// square rounds by 2^-150 at most), the sum is taken again of values scaled by 2^-100
+// or 2^100 (exact; 32768 squares of 2^128 2^-100 stay below 2^71, and the scaled
+// sum of a row whose mean square is below 2^-100 below 2^115), which the result is
+// scaled by as well.
 template <class T, int VPT>
 __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], float inv_dim, float eps, int group,
                                          float *slot, float *slot2) {
@@ -16,21 +19,22 @@ __device__ __forceinline__ float rstd_of(const Raw8<T> (&v)[VPT], float inv_dim,
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s = fma2(v[j].pair(i), v[j].pair(i), s);
-  const float ss = over_group<false>(s.x + s.y, group, slot);
+  const float ss = over_group<false>(s.x + s.y, group, slot), mean = fmaf(ss, inv_dim, eps);
   // the same in every thread of a block-wide group; the smaller groups of a
   // warp shuffle together
-  const bool far = !(ss <= 1e38f);
-  if (!(group > 32 ? far : __any_sync(0xffffffffu, far))) return rsqrtf(fmaf(ss, inv_dim, eps));
+  const bool near = mean < 0x1p-100f, far = near || !(ss <= 1e38f);
+  if (!(group > 32 ? far : __any_sync(0xffffffffu, far))) return rsqrtf(mean);
+  const float by = near ? 0x1p100f : 0x1p-100f;
   float s2 = 0.f;
 #pragma unroll
   for (int j = 0; j < VPT; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float2 u = mul2(v[j].pair(i), both(0x1p-100f));
+      const float2 u = mul2(v[j].pair(i), both(by));
       s2 = fmaf(u.x, u.x, fmaf(u.y, u.y, s2));
     }
   s2 = over_group<false>(s2, group, slot2);
-  return far ? 0x1p-100f * rsqrtf(fmaf(s2, inv_dim, eps * 0x1p-100f * 0x1p-100f)) : rsqrtf(fmaf(ss, inv_dim, eps));
+  return far ? by * rsqrtf(fmaf(s2, inv_dim, eps * by * by)) : rsqrtf(mean);
 }
 
 // x becomes drop(x) + residual, as the stream holds it (rounded once to the

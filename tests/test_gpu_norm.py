@@ -451,3 +451,19 @@ def test_wide_rows_of_the_largest_numbers(rows, dim, dtype):
     want, r = on.forward(host(x), host(w[None])[0], 1e-6)
     assert np.all(np.abs(rstd.double().cpu().numpy() - r) <= (24 * F + 2.0 ** -22) * r)
     assert np.all(np.abs(host(y) - want) <= (U[dtype] + 28 * F + 2.0 ** -22) * np.abs(want) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", FORMS)
+@pytest.mark.parametrize("eps", [0.0, 2.0 ** -116])
+def test_small_rows_where_eps_is_small(rows, dim, eps, dtype):
+    """Rows whose squares have lost their bits, or are 0, beside ordinary ones, with an eps that does
+    not hide it: outputs and every gradient, within the bounds of ordinary rows."""
+    x, dy, w, s = scaled_rows(rows, dim, dtype, [1.0, 1e-14, 1e-18, 1e-20, 1e-23, 1e-30, 1e-36], dim)
+    dy = dy * 1e-6  # (gradients are as large as rstd: 1e36)
+    out = rl.rms_norm_forward(x, w, eps=eps)
+    check_forward(x, None, w, eps, out)
+    check_backward(dy, x, w, out[2], None, rl.rms_norm_backward(dy, x, w, out[2]))
+    dh = (dy.float() / s).to(dtype)
+    check_backward(dy, x, w, out[2], dh, rl.rms_norm_backward(dy, x, w, out[2], dh=dh))
+    rl.device_status()
