@@ -3,6 +3,8 @@
 // norm_bwd.cu; norm.cu has the C entry points).
 #pragma once
 
+#include <atomic>
+
 #include "dropout.cuh"
 #include "host.h"
 #include "ptx.cuh"
@@ -585,13 +587,14 @@ __device__ __forceinline__ void ring_init(RingHead *head, int stages) {
   __syncthreads();
 }
 
+// `allowed`: of this kernel.  (Its limit is said once, for every call's size: host threads
+// whose calls differ in it would lower it under one another's launches.)
 template <class... P, class A>
-cudaError_t launch_ring(void (*kern)(P...), int blocks, const NormSplit &s, int tensors, const A &a,
-                        unsigned *status, cudaStream_t st) {
+cudaError_t launch_ring(void (*kern)(P...), std::atomic<uint64_t> &allowed, int blocks, const NormSplit &s,
+                        int tensors, const A &a, unsigned *status, cudaStream_t st) {
   // (threads past the end of a shifted row read on, by 2 KB at most; the SM has it left)
   const size_t smem = kRingHead + size_t(s.stages) * tensors * s.buffer + (s.shifted ? kRingRoom : 0);
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(smem));
+  const cudaError_t e = allow_smem(kern, kRingSmem, allowed);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(blocks), dim3(s.block), smem, st, a, s.stages, s.buffer, status);
 }

@@ -343,16 +343,20 @@ template <class T, int AL, bool DROP>
 cudaError_t launch_bwd_ring(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                             cudaStream_t st) {
   constexpr int ES = sizeof(T), MID = AL == kAligned || (AL == kShifted && ES == 2) ? 384 : 320;
-  auto k = s.block <= 256   ? k_norm_bwd_ring<T, AL, DROP, 256, ring_blocks(256, AL, ES)>
-           : s.block <= MID ? k_norm_bwd_ring<T, AL, DROP, MID, ring_blocks(MID, AL, ES)>
-                            : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
-  return launch_ring(k, norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
+  static std::atomic<uint64_t> allowed[3];
+  const int which = s.block <= 256 ? 0 : s.block <= MID ? 1 : 2;
+  auto k = which == 0   ? k_norm_bwd_ring<T, AL, DROP, 256, ring_blocks(256, AL, ES)>
+           : which == 1 ? k_norm_bwd_ring<T, AL, DROP, MID, ring_blocks(MID, AL, ES)>
+                        : k_norm_bwd_ring<T, AL, DROP, 512, 1>;
+  return launch_ring(k, allowed[which], norm_bwd_blocks(s, a.rows), s, tensors, a, status, st);
 }
 template <class T, bool DROP>
 cudaError_t launch_bwd_heads(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status,
                              cudaStream_t st) {
-  auto k = s.vpt == 3 ? k_norm_bwd_heads<T, 3, DROP> : k_norm_bwd_heads<T, 2, DROP>;
-  return launch_ring(k, norm_bwd_blocks(s, a.rows / a.inner.n), s, tensors, a, status, st);
+  static std::atomic<uint64_t> allowed[2];
+  const int which = s.vpt == 3;
+  auto k = which ? k_norm_bwd_heads<T, 3, DROP> : k_norm_bwd_heads<T, 2, DROP>;
+  return launch_ring(k, allowed[which], norm_bwd_blocks(s, a.rows / a.inner.n), s, tensors, a, status, st);
 }
 template <class T, int AL>
 cudaError_t launch_any(const NormBwdArgs &a, const NormSplit &s, int tensors, unsigned *status, cudaStream_t st) {

@@ -266,10 +266,12 @@ cudaError_t launch_fwd_ring(const NormFwdArgs &a, const NormSplit &s, int tensor
   const int64_t most = int64_t(kSms) * s.blocks_sm;
   const int blocks = static_cast<int>(a.rows < most ? a.rows : most);
   constexpr int ES = sizeof(T), MID = AL == kAligned || (AL == kShifted && ES == 2) ? 384 : 320;
-  auto k = s.block <= 256   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, ring_blocks(256, AL, ES)>
-           : s.block <= MID ? k_norm_fwd_ring<T, AL, DROP, FP8, MID, ring_blocks(MID, AL, ES)>
-                            : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
-  return launch_ring(k, blocks, s, tensors, a, status, st);
+  static std::atomic<uint64_t> allowed[3];
+  const int which = s.block <= 256 ? 0 : s.block <= MID ? 1 : 2;
+  auto k = which == 0   ? k_norm_fwd_ring<T, AL, DROP, FP8, 256, ring_blocks(256, AL, ES)>
+           : which == 1 ? k_norm_fwd_ring<T, AL, DROP, FP8, MID, ring_blocks(MID, AL, ES)>
+                        : k_norm_fwd_ring<T, AL, DROP, FP8, 512, 1>;
+  return launch_ring(k, allowed[which], blocks, s, tensors, a, status, st);
 }
 template <class T, int AL>
 cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, unsigned *status, cudaStream_t st) {
