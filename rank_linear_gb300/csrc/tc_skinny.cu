@@ -23,6 +23,9 @@
 // the first CTAs of the grid work on problem 0, the rest on problem 1.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
+#include "host.h"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -498,8 +501,10 @@ cudaError_t launch_skinny(const SkinnyArgs *probs, int nprob, int num_sms, cudaS
       P.zero_words = probs[i].zero_words;
     }
   }
-  cudaError_t e = cudaFuncSetAttribute(k_skinny, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
+  // (said once, for every rank's size: host threads of different ranks would lower it
+  // under one another's launches)
+  static std::atomic<uint64_t> allowed{0};
+  const cudaError_t e = allow_smem(k_skinny, size_t(227) * 1024, allowed);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid, 1, 1);

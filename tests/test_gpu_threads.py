@@ -76,3 +76,15 @@ def test_norms_of_two_widths(backward, dtype):
         return _lib.lib().lora_norm_fwd, (ctypes.byref(sh), at[0], at[1], at[2], None, code, at[3], at[4], at[5],
                                           None, None), (y, h, rstd), keep
     at_once(make, 4096, 2048)
+
+
+def test_layers_of_two_ranks():
+    """The low-rank passes of rank 8 and 256 take 104 KB of shared memory and 134 or more."""
+    def make(rank):
+        X, W, A, B, Y = rand(256, 512), rand(512, 512), rand(rank, 512), rand(512, rank), rand(256, 512)
+        saved = torch.empty(_lib.lib().lora_linear_saved_bytes(256, rank, 0), dtype=torch.uint8, device=DEV)
+        n = _lib.lib().lora_linear_workspace_bytes(256, 512, 512, rank, 0)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        return _lib.lib().lora_linear_fwd, (*(address(t) for t in (X, W, A, B)), 16.0, rank, 256, 512, 512, 0,
+                                            *(address(t) for t in (Y, saved, ws)), n), (Y,), (X, W, A, B, saved, ws)
+    at_once(make, 8, 256)
