@@ -71,9 +71,10 @@ __device__ __forceinline__ void stage64(const float *v, uint8_t *stage, int lane
 }
 
 // The first product's drain of 128 columns of a row (in v): sums, and
-// exponentials in their place.  u = log2(e) c(z) - ref.
+// exponentials in their place.  u = log2(e) c(z) - ref.  real: the row is a token's
+// (else it is what the workspace held, which decides nothing for the others).
 template <bool CAP>
-__device__ __forceinline__ LossPart exponentials(float (&v)[kLossPiece], float ref, int target,
+__device__ __forceinline__ LossPart exponentials(float (&v)[kLossPiece], float ref, int target, bool real,
                                                  int col0, int n, float cap, float inv_cap) {
   constexpr float kLog2e = 1.4426950408889634f;
   // columns past the vocabulary, and the target's, whose 1 is added later: both
@@ -120,7 +121,7 @@ __device__ __forceinline__ LossPart exponentials(float (&v)[kLossPiece], float r
     // polynomial, two scores an instruction.  (With the exponential form for all,
     // 2048 x 32000 x 4096 took 355 us where 294 without a cap: a half of the
     // accumulator waits for the other's exponentials.)
-    if (__all_sync(0xffffffffu, big <= cap && fmaf(big, kLog2e, -ref) <= kLossFar)) {
+    if (__all_sync(0xffffffffu, !real || (big <= cap && fmaf(big, kLog2e, -ref) <= kLossFar))) {
       float2 s2 = make_float2(0.f, 0.f);
       const float2 inv2 = make_float2(inv_cap, inv_cap);
 #pragma unroll
@@ -435,7 +436,7 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_u32(&tail->tempty[h]), 0));
         const int col0 = nb * TN + c0;
         if constexpr (!GRAD) {
-          const LossPart p = exponentials<CAP>(v, ref, target, col0, g.n, g.cap, inv_cap);
+          const LossPart p = exponentials<CAP>(v, ref, target, row < M, col0, g.n, g.cap, inv_cap);
           g.parts[int64_t((nb * TN + c0) / kLossPiece) * g.strip + row] = p;
           if constexpr (KIND == 1) {
 #pragma unroll

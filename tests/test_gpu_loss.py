@@ -223,3 +223,17 @@ def test_graph_and_stream():
     got = rl.cross_entropy_forward(x, w, t, gradient=True, stream=side)
     torch.cuda.current_stream().wait_stream(side)
     assert torch.equal(got[2], dx)
+
+
+@pytest.mark.parametrize("rows", [5, 40, 293])
+def test_what_the_workspace_held_before(rows):
+    """Capped scores: rows behind the last token hold what was there before (here numbers whose scores
+    are beyond the cap, NaN, or nothing); the tokens beside them have the same bits."""
+    x, w, t, weights = make(rows, 64, 1300, scale=0.5, ignored=0.0)
+    got = []
+    for fill in (0x0000, 0x4348, 0x7FC0):  # bf16: 0, 200, NaN
+        room = torch.full((64 << 19,), fill, dtype=torch.int16, device=DEV)
+        got.append(rl.cross_entropy_forward(x, w, t, weights=weights, softcap=30.0, gradient=True, workspace=room))
+    check(got[0], x, w, t, weights, 30.0)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
