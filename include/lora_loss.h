@@ -44,7 +44,9 @@ typedef struct {
 } lora_loss_t;
 
 /* Bytes of device workspace lora_loss needs, with dX or without (0 for bad
- * arguments).  It holds a strip of tokens: at most some 0.7 GB with dX. */
+ * arguments).  It holds a strip of tokens, and four bytes a token: at most 716 MB
+ * (of 2^20 bytes) and these where 256 tokens fit (with dX, vocabularies up to a
+ * million words), else what 256 tokens take. */
 size_t lora_loss_workspace_bytes(const lora_loss_t *shape, int with_dx);
 
 /*

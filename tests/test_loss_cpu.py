@@ -118,3 +118,16 @@ def test_python_refusals():
         rl.cross_entropy_forward(x, w, t)
     with pytest.raises(ValueError):
         rl.cross_entropy_forward(x, w, t, reduction="none")
+
+
+@pytest.mark.parametrize("grad", [0, 1])
+@pytest.mark.parametrize("rows", [1, 300, 8192, 65536, 1 << 20])
+@pytest.mark.parametrize("vocab,dim", [(1, 8), (100, 64), (1000, 65536), (4096, 5120), (8192, 8192), (32000, 4096),
+                                       (128000, 4096), (128000, 65536), (2_000_003, 64), (2 ** 31 - 512, 8)])
+def test_workspace_bound_of_any_shape(vocab, dim, rows, grad):
+    """716 MB (of 2^20) and four bytes a token; or where 256 tokens take more than 640 of them, what
+    these take: two bytes a word and element of X, eight a piece of 128 words (of whole tiles of 512), and
+    numbers of their own; and 76 MB of partial tiles."""
+    need = L.lora_loss_workspace_bytes(ctypes.byref(shape(rows=rows, vocab=vocab, dim=dim)), grad)
+    least = 256 * (2 * (vocab + 7) + 2 * dim + 8 * ((vocab + 511) // 512 * 4) + 16)
+    assert 0 < need <= max(640 << 20, least) + (76 << 20) + 4 * rows + 4096
