@@ -237,3 +237,34 @@ def test_what_the_workspace_held_before(rows):
     check(got[0], x, w, t, weights, 30.0)
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("rows,dim,vocab", [(37, 64, 1000), (300, 1000, 3001), (150, 4096, 2000)])
+@pytest.mark.parametrize("weighted", [False, True])
+def test_losses_of_exact_scores(rows, dim, vocab, weighted):
+    """Scores whose products and sums are exact in fp32 (small whole numbers, scaled by 2^-4), so that
+    what a loss may be off by is the exponentials' and the sums' alone.  With F = 2^-24 and Z the largest
+    score of a row: u = z log2(e) - ref rounds twice and ref once (3 F (2 Z) / ln 2 in u, 6 F Z relative),
+    log2(e) itself is off by F (2 F Z); ex2.approx is off by 4 F; a sum has at most 32 + 2 terms a path in a
+    piece of 128, then vocab / 128 pieces and 5 steps of shuffles in whatever order: F each; log1p 4 F
+    and the loss's own rounding F."""
+    g = torch.Generator(device=DEV).manual_seed(dim)
+    few = lambda *s: torch.randint(-1, 2, s, generator=g, device=DEV) * (torch.rand(s, generator=g, device=DEV) < 0.3)
+    x, w = (few(rows, dim) / 4).bfloat16(), (few(vocab, dim) / 4).bfloat16()
+    t = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    weights = torch.rand(rows, generator=g, device=DEV) if weighted else None
+    loss, losses, _ = rl.cross_entropy_forward(x, w, t, weights=weights, gradient=True)
+    z = x.double() @ w.double().T
+    Z = z.abs().max(-1).values
+    at = torch.arange(rows, device=DEV)
+    rest = z - z[at, t][:, None]
+    rest[at, t] = -float("inf")
+    want = torch.log1p(torch.exp(rest).sum(-1))
+    F = 2.0 ** -24
+    bound = F * (8 * Z + 4 + 34 + vocab / 128 + 5) + 5 * F * want
+    assert torch.all((losses.double() - want).abs() <= bound)
+    share = torch.ones(rows, device=DEV).double() if weights is None else weights.double()
+    total, divisor = (share * want).sum(), share.sum()
+    assert abs(float(loss) - float(total / divisor)) <= float((share * (bound + 2 * F * want)).sum() / divisor) + 2 * F * float(loss)
+    again = rl.cross_entropy_forward(x, w, t, weights=weights)
+    assert torch.equal(again[0], loss) and torch.equal(again[1], losses)

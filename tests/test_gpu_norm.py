@@ -467,3 +467,60 @@ def test_small_rows_where_eps_is_small(rows, dim, eps, dtype):
     dh = (dy.float() / s).to(dtype)
     check_backward(dy, x, w, out[2], dh, rl.rms_norm_backward(dy, x, w, out[2], dh=dh))
     rl.device_status()
+
+
+def dw_of_many(dy, h, rstd, dw):
+    """dw against 64 bits: a block adds its rows one after the other, at most as many as come on one of
+    an SM's blocks each, then its groups of threads, and the join an eighth of at most 12 blocks' lines an
+    SM, and eight."""
+    rows = h.shape[0]
+    terms = dy.double() * h.double() * rstd.double()[..., None]
+    lead = tuple(range(h.dim() - 1))
+    steps = rows / 152 + 12 * 152 / 8 + 64
+    bound = U[dw.dtype] * terms.sum(lead).abs() + steps * F * terms.abs().sum(lead)
+    assert torch.all((dw.double() - terms.sum(lead)).abs() <= bound)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("shape,lead", [
+    ((4500, 4096), 0), ((3000, 4097), 1), ((17000, 1001), 3), ((17000, 513), 0), ((1500, 8185), 0), ((1500, 8192), 0),
+    ((3000, 32, 128), 0), ((4500, 40, 96), 0), ((9000, 24, 96), 0), ((11000, 1030), 1)])
+def test_every_stage_of_the_ring_many_times(shape, lead, dtype):
+    """So many rows (of heads side by side: tokens) that each block fills every stage of its ring more
+    than twice.  Parts of them, which fill none twice, have the same bits: the rows lie alike in both."""
+    g = torch.Generator(device=DEV).manual_seed(shape[0])
+    n, heads, dim = shape[0], shape[1:-1], shape[-1]
+    room = (n, *(k + 2 for k in heads), dim)  # (two heads more, so that tokens are apart)
+    size = torch.Size(room).numel()
+
+    def rand():
+        t = torch.randn(size + lead, generator=g, device=DEV).to(dtype)[lead:].view(room)
+        return t[:, :heads[0]] if heads else t
+    x, res, dy, dh, y, h, dx = (rand() for _ in range(7))
+    w = (1 + 0.3 * torch.randn(shape[-1], generator=g, device=DEV)).to(dtype)
+    _, _, rstd = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, out=y, h_out=h)
+    _, _, dw = rl.rms_norm_backward(dy, h, w, rstd, dh=dh, dx=dx)
+    for at in range(0, n, 8 * (n // 72)):
+        part = slice(at, min(at + 400, n))
+        if part.stop - at < 310:
+            part = slice(n - 8 * (310 // 8 + 1) - n % 8, n)  # (the last rows, from a multiple of eight on)
+        out = rl.rms_norm_forward(x[part], w, residual=res[part], eps=1e-5, out=rand()[part], h_out=rand()[part])
+        got = rl.rms_norm_backward(dy[part], h[part], w, rstd[part], dh=dh[part], dx=rand()[part], need_dweight=False)
+        assert torch.equal(out[0], y[part]) and torch.equal(out[1], h[part]) and torch.equal(out[2], rstd[part])
+        assert torch.equal(got[0], dx[part])
+    dw_of_many(dy, h, rstd, dw)
+    rl.device_status()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,dim", [(12000, 1001), (3000, 4097), (4500, 4096), (1500, 8191)])
+def test_dropped_out_rows_through_every_stage(rows, dim, dtype):
+    """The same with dropout, whose masks go by the row, on the boundaries and element by element."""
+    x, res, w, dy, dh = make(rows, dim, dtype, seed=rows)
+    drop = dict(dropout=0.25, seed=12, offset=3)
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, **drop)
+    check_forward(x, res, w, 1e-5, out, 0.25, 12, 3)
+    got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh, **drop)
+    check_backward(dy, out[1], w, out[2], dh, got, 0.25, 12, 3)
+    dw_of_many(dy, out[1], out[2], got[2])
+    rl.device_status()
