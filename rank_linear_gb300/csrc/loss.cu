@@ -12,7 +12,11 @@
 // With every exponential relative to the target's own, a row's sum without the
 // target is S = 1 / p_t - 1, the loss log1p(S) and the target's element of
 // p - [v = t] is -S / (1 + S): no difference of near numbers, whether the target
-// is nearly certain or hopeless.
+// is nearly certain or hopeless.  The reference is the target's score in fp32
+// arithmetic, known beforehand; the target's own exponential is that of its score in the
+// product, as all others': the tensor cores cut off a little of a score at each 16
+// products (5e-6 of it at a dim of 4096), which a difference of two scores hardly shows
+// (with 1 for it, losses at scores of 30 were 1e-4 off).
 #include <algorithm>
 #include <climits>
 #include <cmath>
@@ -134,7 +138,8 @@ struct Strip {
   const LossHead *head;
   const int *live;  // this strip's first
   int first, rows;  // place of the strip among the tokens that count; its room
-  float *ref, *slope, *scale;
+  float *ref, *slope;
+  float *scale;  // from the first product to k_loss_rows: the target's u
   int *target;
 };
 
@@ -264,6 +269,7 @@ __global__ void __launch_bounds__(256) k_loss_gather(Tokens tk, int mean, LossHe
     // (a target beyond the vocabulary makes its row NaN)
     st.ref[i] = known ? s * 1.4426950408889634f : NAN;
     st.slope[i] = slope;
+    st.scale[i] = 0.f;  // (of a target beyond the vocabulary)
     st.target[i] = known ? static_cast<int>(t) : -1;
   }
 }
@@ -311,8 +317,12 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
   }
   __syncthreads();
   const int i = i0 + warp;  // of the first warps: their token
-  float s = 0.f, top = 0.f;
+  float s = 0.f, top = 0.f, u = 0.f;
   if (warp < kRowTokens) {
+    // (where scores are so large that the target's two differ by more, a bound on it keeps
+    // all finite)
+    if (i < rows) u = st.scale[i];
+    u = u < -60.f ? -60.f : u > 60.f ? 60.f : u;
 #pragma unroll
     for (int k = 0; k < PER / 32; ++k) top = fmaxf(top, ups[warp][lane + 32 * k]);
 #pragma unroll
@@ -325,12 +335,12 @@ __global__ void __launch_bounds__(1024) k_loss_rows(Tokens tk, Strip st,
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   }
-  const float own = exp2f(-top), all = s + own;  // the target's, and with it
+  const float own = exp2f(u - top), all = s + own;  // the target's, and with it
   if (lane == 0 && warp < kRowTokens) {
     far[warp] = i < rows ? top : 0.f;
     if (i < rows) {
       const int n = st.live[i];
-      losses[n] = top == 0.f ? log1pf(s) : fmaf(top, 0.69314718055994531f, logf(all));
+      losses[n] = top == 0.f ? log1pf(s / own) : fmaf(top - u, 0.69314718055994531f, logf(all));
       if (e != nullptr) {
         const float g = (tk.weights != nullptr ? tk.weights[n] : 1.f) / st.head->divisor;
         st.scale[i] = g / all;
@@ -643,6 +653,7 @@ lora_status_t lora_loss(const lora_loss_t *sh, const void *X, const void *W, con
     g.ref = s.ref;
     g.target = s.target;
     g.parts = parts;
+    g.own = s.scale;
     g.dev_status = di.status;
     LORA_TRY(run(LORA_K_LOSS_LOGITS, st, "loss logits",
                  [&] { return launch_loss_gemm(grad ? 1 : 0, g, pairs, st); }));

@@ -134,6 +134,7 @@ struct LossGemm {
   const float *ref = nullptr;  // reference of each row, in units of log2
   const int *target = nullptr;
   LossPart *parts = nullptr;   // [piece][strip]
+  float *own = nullptr;        // the target's u of each row
   // second product
   const float *scale = nullptr;  // of each row
   const int *place = nullptr;    // where each row of the strip goes

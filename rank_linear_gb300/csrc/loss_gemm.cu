@@ -3,9 +3,9 @@
 // fused LoRA", §5.7).
 //
 // First:   Z = X W^T by tiles of 256 tokens x 512 words of the vocabulary, which
-//          leave TMEM as E = exp2(log2(e) c(z) - ref) (ref: the target's, so
-//          that a row's largest is at least 1) in bf16, or not at all, and as
-//          fp32 sums over 128 columns.
+//          leave TMEM as E = exp2(u), u = log2(e) c(z) - ref (ref: the target's, so
+//          that a row's largest is some 1 at least) in bf16, or not at all, and as
+//          fp32 sums over 128 columns; and the target's own u.
 // Second:  dX = scale (E W) by tiles of 256 tokens x 512 of the hidden size, the
 //          vocabulary being the length of the products.
 //
@@ -72,14 +72,16 @@ __device__ __forceinline__ void stage64(const float *v, uint8_t *stage, int lane
 
 // The first product's drain of 128 columns of a row (in v): sums, and
 // exponentials in their place.  u = log2(e) c(z) - ref.  real: the row is a token's
-// (else it is what the workspace held, which decides nothing for the others).
-template <bool CAP>
+// (else it is what the workspace held, which decides nothing for the others).  keep:
+// takes the target's u where it is one of the columns.
+template <bool CAP, class Keep>
 __device__ __forceinline__ LossPart exponentials(float (&v)[kLossPiece], float ref, int target, bool real,
-                                                 int col0, int n, float cap, float inv_cap) {
+                                                 int col0, int n, float cap, float inv_cap, const Keep &keep) {
   constexpr float kLog2e = 1.4426950408889634f;
-  // columns past the vocabulary, and the target's, whose 1 is added later: both
-  // are rare, so that the whole warp looks once
-  const bool odd = col0 + kLossPiece > n || static_cast<unsigned>(target - col0) < unsigned(kLossPiece);
+  // columns past the vocabulary, and the target's, which is added later: both are rare,
+  // so that the whole warp looks once
+  const bool mine = static_cast<unsigned>(target - col0) < unsigned(kLossPiece);
+  const bool odd = col0 + kLossPiece > n || mine;
   const bool any_odd = __any_sync(0xffffffffu, odd);
   auto out = [&](int i) { return col0 + i >= n || col0 + i == target; };
   if constexpr (!CAP) {
@@ -91,11 +93,14 @@ __device__ __forceinline__ LossPart exponentials(float (&v)[kLossPiece], float r
     }
     if (any_odd) {
       top = -INFINITY;
+      float u = 0.f;
 #pragma unroll
       for (int i = 0; i < kLossPiece; ++i) {
+        if (col0 + i == target) u = v[i];
         if (out(i)) v[i] = -INFINITY;
         top = fmaxf(top, v[i]);
       }
+      if (mine) keep(u);
     }
     LossPart p = {0.f, 0.f};
     if (top > kLossFar) {
@@ -113,6 +118,13 @@ __device__ __forceinline__ LossPart exponentials(float (&v)[kLossPiece], float r
     return p;
   } else {
     // what is kept is exp2(u) c'(z)
+    if (any_odd) {
+      float z = 0.f, slope;
+#pragma unroll
+      for (int i = 0; i < kLossPiece; ++i)
+        if (col0 + i == target) z = v[i];
+      if (mine) keep(fmaf(loss_cap(z, cap, inv_cap, slope), kLog2e, -ref));
+    }
     float big = 0.f;
 #pragma unroll
     for (int i = 0; i < kLossPiece; ++i) big = fmaxf(big, fabsf(v[i]));
@@ -436,7 +448,8 @@ __global__ void __launch_bounds__(THREADS, 1)
         if (lane == 0) mbar_arrive_cluster(dsmem_map(smem_u32(&tail->tempty[h]), 0));
         const int col0 = nb * TN + c0;
         if constexpr (!GRAD) {
-          const LossPart p = exponentials<CAP>(v, ref, target, row < M, col0, g.n, g.cap, inv_cap);
+          const LossPart p = exponentials<CAP>(v, ref, target, row < M, col0, g.n, g.cap, inv_cap,
+                                               [&](float u) { g.own[row] = u; });
           g.parts[int64_t((nb * TN + c0) / kLossPiece) * g.strip + row] = p;
           if constexpr (KIND == 1) {
 #pragma unroll

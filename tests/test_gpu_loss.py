@@ -268,3 +268,57 @@ def test_losses_of_exact_scores(rows, dim, vocab, weighted):
     assert abs(float(loss) - float(total / divisor)) <= float((share * (bound + 2 * F * want)).sum() / divisor) + 2 * F * float(loss)
     again = rl.cross_entropy_forward(x, w, t, weights=weights)
     assert torch.equal(again[0], loss) and torch.equal(again[1], losses)
+
+
+@pytest.mark.parametrize("cap", [0.0, 200.0])
+@pytest.mark.parametrize("dim", [1024, 4096, 8192])
+@pytest.mark.parametrize("rows,vocab", [(40, 1000), (300, 5003)])
+def test_losses_where_all_scores_are_large(rows, vocab, dim, cap):
+    """Words whose rows are the same but for the last 16 elements, at scores of some 30: what the tensor
+    cores' accumulation cuts off along the way is the same for all of them and for the target, and must
+    not show.  The last step of 16 products may cut 2^-22 of the largest score Z off each, twice in a
+    difference; the cap's formula is off by 8 F Z, twice (F = 2^-24); the rest as for exact scores."""
+    g = torch.Generator(device=DEV).manual_seed(dim + vocab)
+    r = lambda *s: torch.randn(*s, generator=g, device=DEV)
+    common = r(dim) * dim ** -0.5
+    w = common.repeat(vocab, 1)
+    w[:, -16:] = r(vocab, 16) * 0.5
+    x = common * 30 + r(rows, dim) * 0.3
+    x[:, -16:] = r(rows, 16)
+    x, w = x.bfloat16(), w.bfloat16()
+    t = torch.randint(0, vocab, (rows,), generator=g, device=DEV)
+    loss, losses, dx = rl.cross_entropy_forward(x, w, t, softcap=cap, gradient=True)
+    z = x.double() @ w.double().T
+    Z = z.abs().max(-1).values
+    if cap:
+        z = cap * torch.tanh(z / cap)
+    at = torch.arange(rows, device=DEV)
+    rest = z - z[at, t][:, None]
+    rest[at, t] = -float("inf")
+    want = torch.log1p(torch.exp(rest).sum(-1))
+    F = 2.0 ** -24
+    bound = 2 * 2.0 ** -22 * Z + F * ((24 if cap else 8) * Z + 4 + 34 + vocab / 128 + 5) + 5 * F * want
+    assert torch.all((losses.double() - want).abs() <= bound)
+    assert abs(float(loss) - float(want.mean())) <= float(bound.mean()) + 2 * F * float(loss)
+    check((loss, losses, dx), x, w, t, cap=cap)
+
+
+def test_scores_beyond_all_measure():
+    """Scores of 1e8 and 1e30, whose last bits are more than the exponentials' range: certain targets
+    lose nothing, hopeless ones the difference of the scores; nothing is NaN.  Infinite ones are."""
+    w = torch.zeros(300, 64, device=DEV)
+    w[7], w[8] = 1.0, -1.0
+    x = torch.ones(4, 64, device=DEV) * torch.tensor([1.7e6, 1.7e28, 1.7e6, 1.7e28], device=DEV)[:, None]
+    x, w = x.bfloat16(), w.bfloat16()
+    t = torch.tensor([7, 7, 8, 8], device=DEV)
+    loss, losses, dx = rl.cross_entropy_forward(x, w, t, gradient=True)
+    gap = 128 * x[2:, 0].double()
+    assert torch.all(losses[:2] == 0) and torch.all(dx[:2] == 0)
+    assert torch.all((losses[2:].double() - gap).abs() <= 2.0 ** -22 * gap)
+    want = (w[7] - w[8]).float() / 4
+    assert torch.all((dx[2:].float() - want).abs() <= 2.0 ** -7 * want.abs())
+    x[1, 3] = float("inf")
+    loss, losses, dx = rl.cross_entropy_forward(x, w, t, gradient=True)
+    assert torch.isnan(losses[1]) and torch.isfinite(losses[[0, 2, 3]]).all()
+    one = rl.cross_entropy_forward(x[1:2], w[:1], torch.zeros(1, dtype=torch.int64, device=DEV))
+    assert torch.isnan(one[1]).all()
