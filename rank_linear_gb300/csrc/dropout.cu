@@ -6,8 +6,9 @@
 // of the generator's ten rounds: 1.73e12 words a second is all that an otherwise
 // empty loop of them makes on the 152 SMs (the 32 x 32 -> 64 products bound it),
 // and 1.70e12 elements of bf16 a second is what memory moves.  So what is not the
-// generator is kept small: a block's rows and addresses are worked out once, and
-// where the block has one row, the row's share of the first two rounds as well.
+// generator is kept small: a block's rows and addresses are worked out once; in rows of
+// many units a block is at one row at a time, so that the row's share of the first two
+// rounds is the same in all its threads.
 #include <cmath>
 
 #include "dropout.cuh"

@@ -298,7 +298,7 @@ cudaError_t launch_any(const NormFwdArgs &a, const NormSplit &s, int tensors, un
                                     : k_norm_fwd<T, 4, AL, 1, 1024>;
   if constexpr (AL == kAligned)
     if (s.vpt == 3) k = k_norm_fwd<T, 3, AL, 1, kSmallBlock>;  // (96 vectors at most)
-  // (a round of blocks that fills the SMs' threads: 16 of 128, or what fits)
+  // (blocks stay: 12 of 128 threads an SM, or two wider ones, at most)
   const int64_t want = (a.rows + s.per_block - 1) / s.per_block;
   const int64_t most = int64_t(kSms) * (s.block <= kSmallBlock ? 12 : 2);
   return launch_pdl(k, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(s.block), 0, st, a);

@@ -83,7 +83,8 @@ def rms_norm_forward(x, weight, *, residual=None, eps=1e-6, dropout=0.0, seed=0,
     dropout   probability; seed and offset as dropout_forward's.
     fp8       also returns (codes [..., dim] uint8, scale [...] float32): y in e4m3
               with a power of two for each row, as fp8_forward takes them (rows=).
-    out       may be x; h_out may be residual (the stream updated in place) or x.
+    out       may be x (without residual and dropout the h returned is then y, and the input
+              is gone); h_out may be residual (the stream updated in place) or x.
     """
     drop = _drop_block(dropout, seed, offset, x.device)
     eps, summed = float(eps), residual is not None or drop is not None
