@@ -524,3 +524,18 @@ def test_dropped_out_rows_through_every_stage(rows, dim, dtype):
     check_backward(dy, out[1], w, out[2], dh, got, 0.25, 12, 3)
     dw_of_many(dy, out[1], out[2], got[2])
     rl.device_status()
+
+
+@pytest.mark.parametrize("rows,dim", FORMS + [(4500, 4096), (2000, 4097), (400, 8192)])
+@pytest.mark.parametrize("p", [0.0, 0.25])
+def test_fp32_weights_in_every_form(rows, dim, p):
+    """bf16 rows under weights that bf16 does not hold, with everything else that a call may have."""
+    x, res, w, dy, dh = make(rows, dim, torch.bfloat16, seed=rows + dim)
+    w = w.float() * (1 + 2.0 ** -12)
+    drop = dict(dropout=p, seed=21, offset=6) if p else {}
+    out = rl.rms_norm_forward(x, w, residual=res, eps=1e-5, fp8=True, **drop)
+    check_forward(x, res, w, 1e-5, out, p, 21, 6)
+    got = rl.rms_norm_backward(dy, out[1], w, out[2], dh=dh, **drop)
+    assert got[2].dtype == torch.float32
+    check_backward(dy, out[1], w, out[2], dh, got, p, 21, 6)
+    rl.device_status()
